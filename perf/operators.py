@@ -197,8 +197,8 @@ def _prepare_score(case, g, s):
     s["targets"] = torch.where(torch.rand((T,), device="cuda", generator=g) < 0.6, peak[:, 0],
                                torch.randint(0, V, (T,), device="cuda", generator=g)).to(torch.int32)
     s["ids"] = [(7919 * (i + 1)) % V for i in range(case["suppress"])]
-    s["targets"][s["targets"] == (s["ids"][0] if s["ids"] else -5)] = -1   # positions that are not scored
     s["sup"] = torch.tensor(s["ids"], dtype=torch.long, device="cuda")
+    s["targets"] = torch.where((s["targets"][:, None] == s["sup"]).any(1), -1, s["targets"])  # positions not scored
     if case["op"] == "grad":
         with torch.no_grad():
             lp, ent, lse, top, _ = _plain_score(z, s["targets"], case["top"], s["sup"])
