@@ -37,7 +37,8 @@ EXPORTS = (
     "dllm_workspace_fault", "dllm_token_stats_noalloc", "dllm_token_stats_ex", "dllm_linear_temperature",
     "dllm_uniform_canvas", "dllm_renoise", "dllm_stable_confident_stop", "dllm_block_causal_mask",
     "dllm_lm_head_stats_workspace_size", "dllm_lm_head_stats", "dllm_uniform_update", "dllm_commit_step_host",
-    "dllm_noalloc_fault",
+    "dllm_noalloc_fault", "dllm_cache_append", "dllm_cache_attention_workspace_size", "dllm_cache_attention",
+    "dllm_cache_evict", "dllm_token_logprobs", "dllm_token_logprobs_backward",
 )
 
 
@@ -101,8 +102,16 @@ def _load() -> C.CDLL:
     lib.dllm_lm_head_stats_workspace_size.argtypes = [i64, i64, i64]
     lib.dllm_lm_head_stats_workspace_size.restype = sz
     lib.dllm_lm_head_stats.argtypes = [P, i64, i64, i64, P, i64, i64, f32, u64, P, i32, P, P, P, P, i64, P, sz, P]
+    lib.dllm_cache_append.argtypes = [P, P, P, P, P, i64, i64, P, i64, P, P, P]
+    lib.dllm_cache_attention_workspace_size.argtypes = [i64] * 5
+    lib.dllm_cache_attention_workspace_size.restype = sz
+    lib.dllm_cache_attention.argtypes = [P, P, P, i64, i64, i64, P, i64, P, P, i64, f32, P, P, P, f32, P, sz, P]
+    lib.dllm_cache_evict.argtypes = [P, P, i64, P, i64, P, i64, i64, i64, P, i64, P, P, P, P]
+    lib.dllm_token_logprobs.argtypes = [P, C.c_int, i64, i64, i64, P, P, i32, i32, P, P, P, P, P, P]
+    lib.dllm_token_logprobs_backward.argtypes = [P, C.c_int, i64, i64, i64, P, P, i32, P, P, P, P, i32, P, P, P, i64,
+                                                 P]
     for name in EXPORTS[3:]:
-        if name not in ("dllm_token_stats_workspace_size", "dllm_lm_head_stats_workspace_size"):
+        if not name.endswith("_workspace_size"):
             getattr(lib, name).restype = C.c_int
     return lib
 
@@ -778,3 +787,8 @@ def uniform_update(sample: torch.Tensor, accepted: torch.Tensor, step_argmax: to
                                     int(noise_key) & (2**64 - 1), stop.stability_threshold,
                                     stop.confidence_threshold, _ptr(canvas), _ptr(argmax), _ptr(stop.prev),
                                     _ptr(stop.count), _ptr(done), _stream(stream)), "dllm_uniform_update")
+
+
+# The paged 8-bit cache and the scoring of given tokens (modules of their own).
+from .cache import KVCache, cache_append, cache_attention, cache_evict  # noqa: E402
+from .score import MAX_TOP, score_tokens, token_logprobs, token_logprobs_backward  # noqa: E402

@@ -1,0 +1,204 @@
+"""The paged 8-bit key/value cache of a block decoder: appending tokens,
+attending over them, and evicting the least attended (``dllm_cache_append``,
+``dllm_cache_attention``, ``dllm_cache_evict``)."""
+from __future__ import annotations
+
+import ctypes as C
+import math
+from typing import Optional
+
+import torch
+
+from . import _F32, _I32, _MASK, _arg, _check, _lib, _need_cuda, _ptr, _stream
+
+_I64x3 = C.c_int64 * 3
+
+
+class _CacheStruct(C.Structure):
+    """Mirror of ``dllm_kv_cache``."""
+
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("num_pages", C.c_int64), ("page_size", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32)]
+
+
+class KVCache:
+    """A pool of pages of e4m3 keys and values with one scale per page and head.
+
+    ``k`` and ``v``: (num_pages, heads, page_size, head_dim) float8_e4m3fn;
+    ``k_scale`` and ``v_scale``: (num_pages, heads) float32.  A cached value
+    is its code times its page's scale.  The caller deals the pages out in
+    page tables, (B, width) int32 tensors.
+    """
+
+    def __init__(self, num_pages: int, page_size: int, heads: int, head_dim: int, device=None):
+        dev = device or "cuda"
+        shape = (num_pages, heads, page_size, head_dim)
+        k = torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+        v = torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+        self._hold(k, v, torch.ones((num_pages, heads), device=dev), torch.ones((num_pages, heads), device=dev))
+
+    @classmethod
+    def from_tensors(cls, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor) -> "KVCache":
+        """A cache over existing pools (float8_e4m3fn, or uint8 holding the codes)."""
+        self = cls.__new__(cls)
+        self._hold(k, v, k_scale, v_scale)
+        return self
+
+    def _hold(self, k, v, k_scale, v_scale) -> None:
+        _need_cuda(k, v, k_scale, v_scale)
+        if k.dim() != 4:
+            raise ValueError("k must be (num_pages, heads, page_size, head_dim)")
+        pages, heads, page_size, head_dim = k.shape
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        _arg(k, "k", k.numel(), codes, k.device)
+        _arg(v, "v", k.numel(), codes, k.device)
+        if v.shape != k.shape:
+            raise ValueError("k and v must have one shape")
+        _arg(k_scale, "k_scale", pages * heads, _F32, k.device)
+        _arg(v_scale, "v_scale", pages * heads, _F32, k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, head_dim
+        self.device = k.device
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
+                                    page_size, heads, head_dim)
+        self._ref = C.byref(self._struct)
+
+
+def _table(cache: KVCache, table: torch.Tensor, name: str = "page_table"):
+    """(B, width) of a page table."""
+    if not torch.is_tensor(table) or table.dim() != 2:
+        raise ValueError(f"{name} must be a (B, width) int32 tensor")
+    _arg(table, name, table.numel(), _I32, cache.device)
+    return table.shape
+
+
+def _strided(t, name: str, shape, device):
+    """The three outer strides of a bf16 (B, L, heads, head_dim) tensor."""
+    if not torch.is_tensor(t) or t.dtype != torch.bfloat16 or t.dim() != 4:
+        raise TypeError(f"{name} must be a 4-D bfloat16 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}; the cache is on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name} needs unit stride over its last dimension")
+    # (a dimension of one element has no stride that matters)
+    return _I64x3(*[s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])])
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
+                 count: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Writes the keys and values of L new tokens per sequence, (B, L, heads,
+    head_dim) bf16 of any outer strides, at positions start[b] .. start[b] +
+    L - 1 (the first count[b] of them when ``count`` is given)."""
+    B, width = _table(cache, page_table)
+    if not torch.is_tensor(k) or k.dim() != 4:
+        raise TypeError("k must be a 4-D bfloat16 tensor")
+    shape = (B, k.shape[1], cache.heads, cache.head_dim)
+    ks, vs = _strided(k, "k", shape, cache.device), _strided(v, "v", shape, cache.device)
+    _arg(start, "start", B, _I32, cache.device)
+    _arg(count, "count", B, _I32, cache.device)
+    if start is None:
+        raise ValueError("start is needed")
+    _check(_lib.dllm_cache_append(cache._ref, _ptr(k), _ptr(v), ks, vs, B, k.shape[1], _ptr(page_table), width,
+                                  _ptr(start), _ptr(count), _stream(stream)), "dllm_cache_append")
+
+
+_WS_AT = {}
+
+
+def _attention_ws(B, L, Hq, cache: KVCache, stream) -> torch.Tensor:
+    need = int(_lib.dllm_cache_attention_workspace_size(B, L, Hq, cache.heads, cache.head_dim))
+    s = torch.cuda.current_stream(cache.device) if stream is None else stream
+    key = (cache.device.index, s.cuda_stream)
+    ws = _WS_AT.get(key)
+    if ws is None or ws.numel() < need:
+        ws = _empty((need,), torch.uint8, cache.device, stream)
+        if not torch.cuda.is_current_stream_capturing():   # (a capture's memory belongs to its graph)
+            _WS_AT[key] = ws
+    return ws
+
+
+def cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor,
+                    scale: Optional[float] = None, key_mask: Optional[torch.Tensor] = None,
+                    weights: Optional[torch.Tensor] = None, decay: float = 1.0, out=None,
+                    ws: Optional[torch.Tensor] = None, stream=None):
+    """Attention of q (B, L, Hq, head_dim) bf16 over each sequence's first
+    lens[b] cached tokens.  Returns (out bf16 like q, contiguous; lse (B, L,
+    Hq) float32).
+
+    ``scale`` defaults to 1 / sqrt(head_dim).  ``key_mask``: (B, width *
+    page_size) uint8 / bool, 0 for tokens that are not attended.  ``weights``:
+    (B, heads, width * page_size) float32, updated in place to decay * weights
+    + the probability each token drew.  ``out``: preallocated (out, lse).
+    """
+    B, width = _table(cache, page_table)
+    if not torch.is_tensor(q) or q.dim() != 4:
+        raise TypeError("q must be a 4-D bfloat16 tensor")
+    L, Hq = q.shape[1], q.shape[2]
+    dev = cache.device
+    strides = _strided(q, "q", (B, L, Hq, cache.head_dim), dev)
+    cap = width * cache.page_size
+    if lens is None:
+        raise ValueError("lens is needed")
+    _arg(lens, "lens", B, _I32, dev)
+    mask_stride = 0
+    if key_mask is not None:
+        _arg(key_mask, "key_mask", B * cap, _MASK, dev)
+        mask_stride = cap
+    _arg(weights, "weights", B * cache.heads * cap, _F32, dev)
+    if out is None:
+        o, lse = _empty((B, L, Hq, cache.head_dim), torch.bfloat16, dev, stream), \
+            _empty((B, L, Hq), torch.float32, dev, stream)
+    else:
+        o, lse = out
+        _arg(o, "out", B * L * Hq * cache.head_dim, (torch.bfloat16,), dev)
+        _arg(lse, "lse", B * L * Hq, _F32, dev)
+    if ws is None:
+        ws = _attention_ws(B, L, Hq, cache, stream)
+    _check(_lib.dllm_cache_attention(cache._ref, _ptr(q), strides, B, L, Hq, _ptr(page_table), width, _ptr(lens),
+                                     _ptr(key_mask), mask_stride,
+                                     1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), _ptr(o),
+                                     _ptr(lse), _ptr(weights), float(decay), _ptr(ws), ws.numel(), _stream(stream)),
+           "dllm_cache_attention")
+    return o, lse
+
+
+def cache_evict(cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, budget: int,
+                dst_table: torch.Tensor, keep_first: int = 0, keep_last: int = 0, out=None, stream=None):
+    """Copies, per sequence and head, the ``budget`` tokens to keep (the first
+    keep_first, the last keep_last, and the largest ``weights`` of the rest)
+    into the pages of ``dst_table`` (other pages than ``page_table``'s).
+    Returns (keep (B, heads, budget) int32: the old positions in order, -1
+    behind the last; lens (B) int32; weights like ``weights``, moved along).
+    ``out``: those three, preallocated."""
+    B, width = _table(cache, page_table)
+    B2, dst_width = _table(cache, dst_table, "dst_table")
+    if B2 != B:
+        raise ValueError("page_table and dst_table must have one row per sequence")
+    budget, dev = int(budget), cache.device
+    cap = width * cache.page_size
+    if lens is None or weights is None:
+        raise ValueError("lens and weights are needed")
+    _arg(lens, "lens", B, _I32, dev)
+    _arg(weights, "weights", B * cache.heads * cap, _F32, dev)
+    if out is None:
+        out = (_empty((B, cache.heads, max(budget, 0)), torch.int32, dev, stream),
+               _empty((B,), torch.int32, dev, stream),
+               _empty((B, cache.heads, cap), torch.float32, dev, stream))
+    keep, lens_out, weights_out = out
+    _arg(keep, "keep", B * cache.heads * max(budget, 0), _I32, dev)
+    _arg(lens_out, "lens_out", B, _I32, dev)
+    _arg(weights_out, "weights_out", B * cache.heads * cap, _F32, dev)
+    _check(_lib.dllm_cache_evict(cache._ref, _ptr(page_table), width, _ptr(lens), B, _ptr(weights), budget,
+                                 int(keep_first), int(keep_last), _ptr(dst_table), dst_width, _ptr(keep),
+                                 _ptr(lens_out), _ptr(weights_out), _stream(stream)), "dllm_cache_evict")
+    return keep, lens_out, weights_out

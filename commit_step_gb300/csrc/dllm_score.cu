@@ -1,0 +1,657 @@
+// dllm_score.cu -- log probabilities of given tokens with the entropy and the
+// top alternatives, and the gradient of all three with respect to the logits.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <vector>
+
+#include "dllm_device.cuh"
+#include "dllm_launch.cuh"
+
+namespace dllm {
+
+constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreVec = 4;      // 16-byte vectors a thread has in flight
+constexpr int kTopCap = 128;      // candidates a warp keeps before it cuts them to the best k
+constexpr float kInfF = __builtin_huge_valf();
+constexpr float kLow = -0x1p+100f;  // stands for a difference or exponent that carries no mass: 2^kLow = 0, 0 * kLow = 0
+
+struct ScoreParams {
+  const uint8_t* logits;
+  int64_t T, V, row_bytes;
+  const int32_t* targets;
+  float* logprob;
+  float* entropy;
+  float* lse;
+  int32_t* top_ids;
+  float* top_logprob;
+  int32_t top;
+  float ln_veff;              // ln of the number of ids that are not suppressed
+  int32_t n_sup;
+  int32_t sup[DLLM_MAX_SUPPRESS];  // ascending, distinct
+};
+
+// A candidate: value order in the high word, lower ids first in the low word.
+// 0 is no candidate (every value's key is above 0).
+__device__ __forceinline__ uint64_t candidate(float z, uint32_t id) {
+  return static_cast<uint64_t>(float_key(z)) << 32 | (0xFFFFFFFFu - id);
+}
+__device__ __forceinline__ float candidate_value(uint64_t c) { return key_to_float(static_cast<uint32_t>(c >> 32)); }
+__device__ __forceinline__ uint32_t candidate_id(uint64_t c) { return 0xFFFFFFFFu - static_cast<uint32_t>(c); }
+
+__device__ __forceinline__ float no_nan(float z) { return fmaxf(z, -kInfF); }  // NaN -> -inf
+
+// The state of a softmax over some ids: the largest logit m, Z = sum
+// 2^((z - m) log2 e), S = sum 2^y y of the same exponents.
+struct Soft {
+  float m, Z, S;
+};
+
+// log2 e (from - to) for from <= to, finite (kLow where the mass vanishes).
+__device__ __forceinline__ float shift2(float from, float to) { return fmaxf(from - to, kLow) * kLog2e; }
+
+__device__ __forceinline__ void soft_raise(Soft& a, float m) {
+  const float d = shift2(a.m, m), f = ex2_approx(d);
+  a.S = f * fmaf(d, a.Z, a.S);
+  a.Z *= f;
+  a.m = m;
+}
+
+__device__ __forceinline__ void soft_join(Soft& a, Soft b) {
+  const float m = fmaxf(a.m, b.m);
+  soft_raise(a, m);
+  soft_raise(b, m);
+  a.Z += b.Z;
+  a.S += b.S;
+}
+
+// Ranks the n candidates in `in` (distinct, in shared memory) against each
+// other and stores those with rank < k at out[rank]; `step` threads share the
+// work.  in and out do not overlap.
+__device__ __forceinline__ void rank_candidates(const uint64_t* in, int n, int k, uint64_t* out, int first, int step) {
+  for (int i = first; i < n; i += step) {
+    const uint64_t c = in[i];
+    int r = 0;
+    for (int j = 0; j < n; ++j) r += in[j] > c ? 1 : 0;
+    if (r < k) out[r] = c;
+  }
+}
+
+template <int BYTES>  // of an element
+__device__ __forceinline__ float element(const uint4& v, int e) {
+  const uint32_t w = (&v.x)[BYTES == 2 ? e >> 1 : e];
+  if (BYTES == 4) return __uint_as_float(w);
+  return (e & 1) ? bf16hi(w) : bf16lo(w);
+}
+
+// One cluster of CTAs per row, each CTA an equal range of the row's 16-byte
+// vectors (few rows: up to 8 CTAs a row, so that the whole GPU reads; many
+// rows: one CTA a row, several rows to an SM).  One pass over the logits: each
+// warp holds a running maximum and every lane its sums Z and S of 2^y and 2^y y,
+// y = (z - m) log2 e, rescaled only when the warp's maximum grows; a value that
+// reaches the CTA's k-th best so far (shared by its warps) is kept as a
+// candidate, and a full list is cut to the best k.  The CTAs' parts are joined
+// in rank order through distributed shared memory.
+// Bound: the one read of the logits.
+template <int BYTES>
+__global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_constant__ ScoreParams p) {
+  constexpr int EPV = 16 / BYTES;
+  constexpr int N = kScoreVec * EPV;                       // elements a thread holds
+  __shared__ uint64_t list[kScoreWarps][kTopCap];
+  __shared__ uint64_t scratch[kScoreWarps][DLLM_MAX_TOP];
+  __shared__ uint64_t best[DLLM_MAX_TOP];                  // this CTA's best k, descending
+  __shared__ unsigned long long floor_s;                   // no value below this candidate can be among the best k
+  __shared__ Soft warp_soft[kScoreWarps];
+  __shared__ Soft cta_soft;
+  __shared__ int32_t count_s[kScoreWarps];
+  __shared__ uint64_t joined[8 * DLLM_MAX_TOP];
+  __shared__ uint32_t inf_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t rank, size;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(size));
+  const int64_t row = blockIdx.x / size;
+  const int k = p.top;
+  if (threadIdx.x == 0) {
+    floor_s = 0;
+    inf_s = 0;
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const uint8_t* base = p.logits + row * p.row_bytes;
+  // The row as whole aligned vectors, with up to EPV - 1 elements before and after them.
+  const int64_t lead = std::min<int64_t>(p.V, ((16 - (reinterpret_cast<uintptr_t>(base) & 15u)) & 15u) / BYTES);
+  const int64_t nvec = (p.V - lead) / EPV;
+  const int64_t tail0 = lead + nvec * EPV;
+  const uint4* vecs = reinterpret_cast<const uint4*>(base + lead * BYTES);
+  const int64_t v0 = nvec * rank / size, v1 = nvec * (rank + 1) / size;
+  Soft a{-kInfF, 0.0f, 0.0f};
+  int have = 0;                                            // candidates in this warp's list
+  float floor_z = -kInfF;                                  // the value of the floor this warp last saw
+  uint64_t floor_c = 0;
+  auto cut = [&]() {                                       // keep the best k of the warp's list, raise the floor
+    __syncwarp();
+    rank_candidates(list[warp], have, k, scratch[warp], lane, 32);
+    __syncwarp();
+    if (have > k) have = k;
+    if (lane < have) list[warp][lane] = scratch[warp][lane];
+    __syncwarp();
+    if (have == k && lane == 0) atomicMax(&floor_s, static_cast<unsigned long long>(scratch[warp][k - 1]));
+    __syncwarp();
+  };
+  // Folds N values of each lane (NaN and absent ones as -inf) into the state.
+  // Value e has the id first + (e / EPV) 32 EPV + e % EPV; absent: bits of values that are no candidates.
+  float z[N];
+  auto fold = [&](uint32_t first, uint32_t absent) {
+    float c = z[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) c = fmaxf(c, z[e]);
+    const float cm = warp_max_f32(c);
+    if (cm > a.m) soft_raise(a, cm);                       // warp-uniform
+    float Z = 0.0f, S = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float y = fmaxf(z[e] - a.m, kLow) * kLog2e;
+      const float x = ex2_approx(y);
+      Z += x;
+      S = fmaf(x, y, S);
+    }
+    a.Z += Z;
+    a.S += S;
+    if (k == 0 || cm < floor_z) return;
+    const uint64_t f = *const_cast<volatile unsigned long long*>(&floor_s);
+    if (f > floor_c) {
+      floor_c = f;
+      floor_z = candidate_value(f);
+      if (cm < floor_z) return;
+    }
+    if (floor_c == 0 && have == 0) {
+      // The first values: the k-th largest of the lanes' maxima is below k values, so it is a floor.
+      uint64_t mine = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (!((absent >> e) & 1u)) {
+          const uint64_t q = candidate(z[e], first + e / EPV * 32 * EPV + e % EPV);
+          mine = q > mine ? q : mine;
+        }
+      list[warp][lane] = mine;
+      __syncwarp();
+      int r = 0;
+      for (int j = 0; j < 32; ++j) r += list[warp][j] > mine ? 1 : 0;
+      const uint32_t at = __ballot_sync(0xFFFFFFFFu, r == k - 1 && mine != 0);
+      if (at != 0u) {
+        floor_c = __shfl_sync(0xFFFFFFFFu, mine, __ffs(at) - 1);
+        floor_z = candidate_value(floor_c);
+        if (lane == 0) atomicMax(&floor_s, static_cast<unsigned long long>(floor_c));
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const bool near = z[e] >= floor_z && !((absent >> e) & 1u);
+      uint32_t hit = __ballot_sync(0xFFFFFFFFu, near);
+      if (hit == 0u) continue;
+      if (have + 32 > kTopCap) {
+        cut();
+        const uint64_t g = *const_cast<volatile unsigned long long*>(&floor_s);
+        if (g > floor_c) {
+          floor_c = g;
+          floor_z = candidate_value(g);
+        }
+      }
+      const uint64_t q = candidate(z[e], first + e / EPV * 32 * EPV + e % EPV);
+      hit = __ballot_sync(0xFFFFFFFFu, near && q >= floor_c);
+      if (near && q >= floor_c) list[warp][have + __popc(hit & ((1u << lane) - 1u))] = q;
+      have += __popc(hit);
+    }
+  };
+
+  // The elements outside the whole vectors: the first CTA's first warp takes those before, the last CTA's those after.
+  if (warp == 0 && ((rank == 0 && lead > 0) || (rank == size - 1 && tail0 < p.V))) {
+    uint32_t absent = 0xFFFFFFFFu;
+    // lanes 0 .. EPV - 1 before the vectors, lanes 16 .. 16 + EPV - 1 after them
+    const int64_t v = lane < 16 ? lane : tail0 + lane - 16;
+    const bool in = lane < 16 ? rank == 0 && v < lead : rank == size - 1 && v < p.V;
+    z[0] = -kInfF;
+    if (in) {
+      if (BYTES == 2)
+        z[0] = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[v]) << 16);
+      else
+        z[0] = reinterpret_cast<const float*>(base)[v];
+      z[0] = no_nan(z[0]);
+      absent &= ~1u;
+      for (int q = 0; q < p.n_sup; ++q)
+        if (p.sup[q] == v) {
+          z[0] = -kInfF;
+          absent |= 1u;
+        }
+    }
+#pragma unroll
+    for (int e = 1; e < N; ++e) z[e] = -kInfF;
+    fold(static_cast<uint32_t>(v), absent);
+  }
+
+  int sup_at = 0;                                          // suppressed ids before this warp's position
+  for (int64_t b0 = v0 + warp * (kScoreVec * 32); b0 < v1; b0 += kScoreThreads * kScoreVec) {
+    uint4 x[kScoreVec];
+#pragma unroll
+    for (int u = 0; u < kScoreVec; ++u) {
+      const int64_t v = b0 + u * 32 + lane;
+      if (v < v1) x[u] = __ldcs(vecs + v);
+    }
+    uint32_t absent = 0;
+#pragma unroll
+    for (int u = 0; u < kScoreVec; ++u) {
+      if (b0 + u * 32 + lane < v1) {
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) z[u * EPV + e] = no_nan(element<BYTES>(x[u], e));
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) z[u * EPV + e] = -kInfF;
+        absent |= ((1u << EPV) - 1u) << (u * EPV);
+      }
+    }
+    const int64_t id0 = lead + b0 * EPV, id1 = id0 + kScoreVec * 32 * EPV;
+    while (sup_at < p.n_sup && p.sup[sup_at] < id0) ++sup_at;
+    for (int q = sup_at; q < p.n_sup && p.sup[q] < id1; ++q) {   // rare: a suppressed id among this warp's values
+      const int off = static_cast<int>(p.sup[q] - id0);
+      const int at = off / EPV % 32 == lane ? off / (32 * EPV) * EPV + off % EPV : -1;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e == at) {
+          z[e] = -kInfF;
+          absent |= 1u << e;
+        }
+    }
+    fold(static_cast<uint32_t>(id0) + lane * EPV, absent);
+  }
+
+  // The warp's state, the CTA's, the row's.
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {                       // one maximum per warp: the sums add up
+    a.Z += __shfl_xor_sync(0xFFFFFFFFu, a.Z, o);
+    a.S += __shfl_xor_sync(0xFFFFFFFFu, a.S, o);
+  }
+  if (k > 0) {
+    cut();
+    if (lane == 0) count_s[warp] = have;
+  }
+  if (lane == 0) warp_soft[warp] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    Soft t = warp_soft[0];
+    for (int w = 1; w < kScoreWarps; ++w) soft_join(t, warp_soft[w]);
+    cta_soft = t;
+  }
+  int total = 0;
+  if (k > 0) {
+    // the warps' lists side by side, then the best k of them
+    int at = 0;
+    for (int w = 0; w < kScoreWarps; ++w) {
+      if (w < warp) at += count_s[w];
+      total += count_s[w];
+    }
+    if (lane < have) joined[at + lane] = list[warp][lane];
+    if (threadIdx.x < k) best[threadIdx.x] = 0;
+    __syncthreads();
+    rank_candidates(joined, total, k, best, threadIdx.x, kScoreThreads);
+  }
+  if (size > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0) {
+      auto remote = [&](const void* local, uint32_t r) {
+        uint32_t addr;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(local)), "r"(r));
+        return addr;
+      };
+      if (threadIdx.x == 0) {
+        Soft t = cta_soft;
+        for (uint32_t r = 1; r < size; ++r) {
+          const uint32_t addr = remote(&cta_soft, r);
+          Soft o;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.m) : "r"(addr) : "memory");
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.Z) : "r"(addr + 4) : "memory");
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.S) : "r"(addr + 8) : "memory");
+          soft_join(t, o);
+        }
+        warp_soft[0] = t;
+      }
+      if (k > 0) {
+        const int n = static_cast<int>(size) * k;
+        for (int i = threadIdx.x; i < n; i += kScoreThreads) {
+          const uint32_t addr = remote(&best[i % k], static_cast<uint32_t>(i / k));
+          uint64_t c;
+          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(c) : "r"(addr) : "memory");
+          joined[i] = c;
+        }
+        __syncthreads();
+        if (threadIdx.x < k) best[threadIdx.x] = 0;
+        __syncthreads();
+        rank_candidates(joined, n, k, best, threadIdx.x, kScoreThreads);   // (zeros rank last: at least k are real)
+      }
+      __syncthreads();
+    }
+    // the other CTAs' shared memory has been read
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+  } else {
+    if (threadIdx.x == 0) warp_soft[0] = cta_soft;
+    __syncthreads();
+  }
+
+  const Soft t = warp_soft[0];
+  float ln_z = logf(t.Z);
+  if (t.m == kInfF) {                                      // +inf logits share the mass equally: count them
+    uint32_t mine = 0;
+    for (int64_t v = threadIdx.x; v < p.V; v += kScoreThreads) {
+      bool inf = BYTES == 2 ? reinterpret_cast<const uint16_t*>(base)[v] == 0x7F80u
+                            : reinterpret_cast<const float*>(base)[v] == kInfF;
+      for (int q = 0; q < p.n_sup; ++q) inf = inf && p.sup[q] != v;
+      mine += inf ? 1u : 0u;
+    }
+    if (mine) atomicAdd(&inf_s, mine);
+    __syncthreads();
+    ln_z = logf(static_cast<float>(inf_s));
+  }
+  // log p of a logit z (NaN as -inf) under the row's softmax.
+  auto log_p = [&](float z) {
+    if (t.m == kInfF) return z == kInfF ? -ln_z : -kInfF;
+    if (t.m == -kInfF) return -p.ln_veff;                  // no mass anywhere: the uniform limit
+    return (z - t.m) - ln_z;
+  };
+  if (threadIdx.x == 0) {
+    float ent = t.m == kInfF ? ln_z : (t.m == -kInfF ? p.ln_veff : ln_z - kLn2 * (t.S / t.Z));
+    p.entropy[row] = fminf(fmaxf(ent, 0.0f), p.ln_veff);
+    p.lse[row] = fabsf(t.m) == kInfF ? t.m : t.m + ln_z;
+    const int32_t id = p.targets[row];
+    float lp = 0.0f;                                       // no target
+    if (id >= 0 && id < p.V) {
+      float z;
+      if (BYTES == 2)
+        z = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[id]) << 16);
+      else
+        z = reinterpret_cast<const float*>(base)[id];
+      lp = log_p(no_nan(z));
+      for (int q = 0; q < p.n_sup; ++q)
+        if (p.sup[q] == id) lp = -kInfF;
+    }
+    p.logprob[row] = lp;
+  }
+  if (threadIdx.x < k) {
+    const uint64_t c = best[threadIdx.x];
+    p.top_ids[row * k + threadIdx.x] = static_cast<int32_t>(candidate_id(c));
+    p.top_logprob[row * k + threadIdx.x] = log_p(candidate_value(c));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------
+struct ScoreGradParams {
+  const uint8_t* logits;
+  uint8_t* grad;
+  int64_t T, V, row_bytes, grad_row_bytes;
+  const int32_t* targets;
+  const float* lse;
+  const float* entropy;
+  const float* g_logprob;     // nullable, as the next
+  const float* g_entropy;
+  const int32_t* top_ids;     // (T, top), nullable with g_top
+  const float* g_top;
+  int32_t top;
+  int32_t chunks;             // blocks per row
+  int32_t n_sup;
+  int32_t sup[DLLM_MAX_SUPPRESS];
+};
+
+constexpr int kGradThreads = 256;
+constexpr int kGradVec = 4;
+
+template <int BYTES>
+__device__ __forceinline__ void store_element(uint8_t* row, int64_t v, float f) {
+  if (BYTES == 4) {
+    reinterpret_cast<float*>(row)[v] = f;
+  } else {
+    uint16_t h;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(f));
+    reinterpret_cast<uint16_t*>(row)[v] = h;
+  }
+}
+
+template <int BYTES>
+__device__ __forceinline__ float load_element(const uint8_t* row, int64_t v) {
+  if (BYTES == 4) return reinterpret_cast<const float*>(row)[v];
+  return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[v]) << 16);
+}
+
+// With G = g + sum g_top and y = z - lse, p = e^y:
+//   dz = -p (G + g_entropy (y + H)) + [v = target] g + sum_j [v = top_j] g_top_j,
+// 0 for suppressed ids.  One block per row and chunk of it; every thread
+// transforms whole vectors, and the few named ids (target, alternatives,
+// suppressed ids), read before anything is written, are stored again after the
+// block's vectors, so grad may be the logits' own buffer.
+// Bound: one read of the logits and one write of the gradient.
+template <int BYTES>
+__global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const __grid_constant__ ScoreGradParams p) {
+  constexpr int EPV = 16 / BYTES;
+  __shared__ int32_t top_s[DLLM_MAX_TOP];
+  __shared__ float gt_s[DLLM_MAX_TOP];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t row = blockIdx.x / p.chunks;
+  const int chunk = static_cast<int>(blockIdx.x % p.chunks);
+  const uint8_t* in = p.logits + row * p.row_bytes;
+  uint8_t* out = p.grad + row * p.grad_row_bytes;
+  const float lse = p.lse[row], H = p.entropy[row];
+  const float ge = p.g_entropy ? p.g_entropy[row] : 0.0f;
+  const int32_t target = p.targets[row];
+  if (threadIdx.x < p.top) {
+    const int32_t id = p.top_ids[row * p.top + threadIdx.x];
+    bool counts = id >= 0 && id < p.V;
+    for (int q = 0; q < p.n_sup; ++q) counts = counts && p.sup[q] != id;
+    top_s[threadIdx.x] = id;
+    gt_s[threadIdx.x] = counts ? p.g_top[row * p.top + threadIdx.x] : 0.0f;
+  }
+  float g = p.g_logprob ? p.g_logprob[row] : 0.0f;
+  if (target < 0 || target >= p.V) g = 0.0f;
+  for (int q = 0; q < p.n_sup; ++q)
+    if (p.sup[q] == target) g = 0.0f;                      // its log probability is -inf whatever the logits are
+  const bool dead = !(fabsf(lse) < kInfF);                 // a row without an ordinary softmax: no gradient
+  __syncthreads();
+  float G = g;
+  for (int j = 0; j < p.top; ++j) G += gt_s[j];
+  const float base = dead ? 0.0f : G + ge * H, slope = dead ? 0.0f : ge;
+  const float ref = dead ? kInfF : lse;
+  auto bulk = [&](float z) {
+    const float y = fmaxf(z - ref, kLow);                  // (NaN and -inf: no mass)
+    const float x = ex2_approx(y * kLog2e);
+    return -x * fmaf(slope, y, base);
+  };
+  const int64_t lead = std::min<int64_t>(p.V, ((16 - (reinterpret_cast<uintptr_t>(in) & 15u)) & 15u) / BYTES);
+  const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+  const int64_t nvec = (p.V - lead) / EPV;
+  const int64_t c0 = nvec * chunk / p.chunks, c1 = nvec * (chunk + 1) / p.chunks;
+  // this block's ids are [e0, e1)
+  const int64_t e0 = chunk == 0 ? 0 : lead + c0 * EPV, e1 = chunk == p.chunks - 1 ? p.V : lead + c1 * EPV;
+
+  // The named id of this thread, if it lies here: its gradient, from the logit as it still is.
+  int64_t named = -1;
+  if (threadIdx.x == 0) named = target;
+  else if (threadIdx.x <= p.top) named = top_s[threadIdx.x - 1];
+  else if (threadIdx.x >= 128 && threadIdx.x < 128 + p.n_sup) named = p.sup[threadIdx.x - 128];
+  float named_grad = 0.0f;
+  if (named >= e0 && named < e1) {
+    bool sup = false;
+    for (int q = 0; q < p.n_sup; ++q) sup = sup || p.sup[q] == named;
+    if (!sup && !dead) {
+      float hot = named == target ? g : 0.0f;
+      for (int j = 0; j < p.top; ++j) hot += top_s[j] == named ? gt_s[j] : 0.0f;
+      named_grad = bulk(load_element<BYTES>(in, named)) + hot;
+    }
+  } else {
+    named = -1;
+  }
+  __syncthreads();
+
+  if (same) {
+    const uint4* src = reinterpret_cast<const uint4*>(in + lead * BYTES);
+    uint4* dst = reinterpret_cast<uint4*>(out + lead * BYTES);
+    for (int64_t v0 = c0; v0 < c1; v0 += kGradThreads * kGradVec) {
+      uint4 x[kGradVec];
+#pragma unroll
+      for (int u = 0; u < kGradVec; ++u) {
+        const int64_t v = v0 + u * kGradThreads + threadIdx.x;
+        if (v < c1) x[u] = __ldcs(src + v);
+      }
+#pragma unroll
+      for (int u = 0; u < kGradVec; ++u) {
+        const int64_t v = v0 + u * kGradThreads + threadIdx.x;
+        if (v >= c1) continue;
+        uint4 o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (BYTES == 4) {
+            (&o.x)[q] = __float_as_uint(bulk(__uint_as_float((&x[u].x)[q])));
+          } else {
+            const uint32_t w = (&x[u].x)[q];
+            uint32_t d;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(bulk(bf16hi(w))), "f"(bulk(bf16lo(w))));
+            (&o.x)[q] = d;
+          }
+        }
+        __stcs(dst + v, o);
+      }
+    }
+    const int64_t tail0 = lead + nvec * EPV;
+    if (chunk == 0 && threadIdx.x < lead)
+      store_element<BYTES>(out, threadIdx.x, bulk(load_element<BYTES>(in, threadIdx.x)));
+    if (chunk == p.chunks - 1 && tail0 + threadIdx.x < p.V)
+      store_element<BYTES>(out, tail0 + threadIdx.x, bulk(load_element<BYTES>(in, tail0 + threadIdx.x)));
+  } else {                                                 // rows whose vectors do not line up: one by one
+    for (int64_t v = e0 + threadIdx.x; v < e1; v += kGradThreads)
+      store_element<BYTES>(out, v, bulk(load_element<BYTES>(in, v)));
+  }
+  __syncthreads();
+  if (named >= 0) store_element<BYTES>(out, named, named_grad);
+}
+
+// Checks shared by both directions; the ascending distinct suppressed ids in `sup`.
+static dllm_status check_score(const void* logits, dllm_dtype dt, int64_t T, int64_t V, int64_t row_stride,
+                               const int32_t* suppress_ids, int32_t n_suppress, int32_t top,
+                               std::vector<int32_t>& sup) {
+  if (dt != DLLM_F32 && dt != DLLM_BF16) return DLLM_ERR_INVALID_ARGUMENT;
+  if (T < 0 || V < 1 || V > INT32_MAX - 1 || row_stride < V || top < 0) return DLLM_ERR_INVALID_ARGUMENT;
+  if (mul_or_neg(T, mul_or_neg(row_stride, 4)) < 0 || mul_or_neg(T, 4 * (top + 1)) < 0)
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (n_suppress < 0 || (n_suppress > 0 && !suppress_ids)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (n_suppress > DLLM_MAX_SUPPRESS || top > DLLM_MAX_TOP) return DLLM_ERR_UNSUPPORTED;
+  sup.assign(suppress_ids, suppress_ids + n_suppress);
+  for (int32_t id : sup)
+    if (id < 0 || id >= V) return DLLM_ERR_INVALID_ARGUMENT;
+  std::sort(sup.begin(), sup.end());
+  sup.erase(std::unique(sup.begin(), sup.end()), sup.end());
+  if (static_cast<int64_t>(sup.size()) >= V || top > V - static_cast<int64_t>(sup.size()))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (T > 0 && !logits) return DLLM_ERR_INVALID_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(logits) & (dt == DLLM_BF16 ? 1u : 3u)) != 0) return DLLM_ERR_INVALID_ARGUMENT;
+  return DLLM_OK;
+}
+
+}  // namespace dllm
+
+extern "C" {
+
+dllm_status dllm_token_logprobs(const void* logits, dllm_dtype dt, int64_t T, int64_t V, int64_t row_stride,
+                                const int32_t* targets, const int32_t* suppress_ids, int32_t n_suppress, int32_t top,
+                                float* logprob, float* entropy, float* lse, int32_t* top_ids, float* top_logprob,
+                                dllm_stream_t stream) {
+  using namespace dllm;
+  std::vector<int32_t> sup;
+  const dllm_status st = check_score(logits, dt, T, V, row_stride, suppress_ids, n_suppress, top, sup);
+  if (st != DLLM_OK) return st;
+  if (T == 0) return DLLM_OK;
+  if (!targets || !logprob || !entropy || !lse || (top > 0 && (!top_ids || !top_logprob)))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (!aligned4(targets) || !aligned4(logprob) || !aligned4(entropy) || !aligned4(lse) || !aligned4(top_ids) ||
+      !aligned4(top_logprob))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  const int64_t bytes = dt == DLLM_BF16 ? 2 : 4;
+  // CTAs per row: doubled while the grid would leave SMs without work (304 =
+  // two CTAs for each of 152 SMs) and every CTA still gets two passes of its
+  // threads' vectors.
+  int cluster = 1;
+  while (cluster < 8 && T * cluster < 304 && V * bytes >= 2 * cluster * 2 * 16 * kScoreThreads * kScoreVec) cluster *= 2;
+  if (T > INT32_MAX / cluster) return DLLM_ERR_UNSUPPORTED;
+  ScoreParams p{};
+  p.logits = static_cast<const uint8_t*>(logits);
+  p.T = T;
+  p.V = V;
+  p.row_bytes = row_stride * bytes;
+  p.targets = targets;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.lse = lse;
+  p.top_ids = top_ids;
+  p.top_logprob = top_logprob;
+  p.top = top;
+  p.ln_veff = static_cast<float>(std::log(static_cast<double>(V - static_cast<int64_t>(sup.size()))));
+  p.n_sup = static_cast<int32_t>(sup.size());
+  for (size_t i = 0; i < sup.size(); ++i) p.sup[i] = sup[i];
+  void* args[] = {&p};
+  const void* kernel = dt == DLLM_BF16 ? reinterpret_cast<const void*>(&score_kernel<2>)
+                                       : reinterpret_cast<const void*>(&score_kernel<4>);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(T * cluster)), dim3(kScoreThreads), 0, stream, args, cluster);
+}
+
+dllm_status dllm_token_logprobs_backward(const void* logits, dllm_dtype dt, int64_t T, int64_t V, int64_t row_stride,
+                                         const int32_t* targets, const int32_t* suppress_ids, int32_t n_suppress,
+                                         const float* lse, const float* entropy, const float* grad_logprob,
+                                         const float* grad_entropy, int32_t top, const int32_t* top_ids,
+                                         const float* grad_top, void* grad, int64_t grad_row_stride,
+                                         dllm_stream_t stream) {
+  using namespace dllm;
+  std::vector<int32_t> sup;
+  const dllm_status st = check_score(logits, dt, T, V, row_stride, suppress_ids, n_suppress, top, sup);
+  if (st != DLLM_OK) return st;
+  if (grad_row_stride < V || mul_or_neg(T, mul_or_neg(grad_row_stride, 4)) < 0) return DLLM_ERR_INVALID_ARGUMENT;
+  if (T == 0) return DLLM_OK;
+  if (!targets || !lse || !entropy || !grad || (top > 0 && (!top_ids || !grad_top))) return DLLM_ERR_INVALID_ARGUMENT;
+  if (!aligned4(targets) || !aligned4(lse) || !aligned4(entropy) || !aligned4(grad_logprob) ||
+      !aligned4(grad_entropy) || !aligned4(top_ids) || !aligned4(grad_top))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(grad) & (dt == DLLM_BF16 ? 1u : 3u)) != 0) return DLLM_ERR_INVALID_ARGUMENT;
+  const int64_t bytes = dt == DLLM_BF16 ? 2 : 4;
+  // A block per 32 KB of a row: two passes of its threads' vectors, so the
+  // row's scalars are read once for eight vectors a thread.
+  const int64_t chunks = std::max<int64_t>(1, (V * bytes + 32767) / 32768);
+  if (mul_or_neg(T, chunks) < 0 || T * chunks > INT32_MAX) return DLLM_ERR_UNSUPPORTED;
+  ScoreGradParams p{};
+  p.logits = static_cast<const uint8_t*>(logits);
+  p.grad = static_cast<uint8_t*>(grad);
+  p.T = T;
+  p.V = V;
+  p.row_bytes = row_stride * bytes;
+  p.grad_row_bytes = grad_row_stride * bytes;
+  p.targets = targets;
+  p.lse = lse;
+  p.entropy = entropy;
+  p.g_logprob = grad_logprob;
+  p.g_entropy = grad_entropy;
+  p.top_ids = top_ids;
+  p.g_top = grad_top;
+  p.top = top;
+  p.chunks = static_cast<int32_t>(chunks);
+  p.n_sup = static_cast<int32_t>(sup.size());
+  for (size_t i = 0; i < sup.size(); ++i) p.sup[i] = sup[i];
+  void* args[] = {&p};
+  const void* kernel = dt == DLLM_BF16 ? reinterpret_cast<const void*>(&score_grad_kernel<2>)
+                                       : reinterpret_cast<const void*>(&score_grad_kernel<4>);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(T * chunks)), dim3(kGradThreads), 0, stream, args);
+}
+
+}  // extern "C"

@@ -1,0 +1,130 @@
+"""Log probabilities of given tokens, with the entropy and the top
+alternatives, and their gradient (``dllm_token_logprobs``,
+``dllm_token_logprobs_backward``)."""
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional, Sequence
+
+import torch
+
+from . import _F32, _I32, _arg, _check, _dtype_code, _lib, _need_cuda, _ptr, _stream
+from .cache import _empty
+
+MAX_TOP = 32
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(T, V, row stride) of (T, V) or (B, L, V) logits, unit stride over V."""
+    if not torch.is_tensor(t) or t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be (T, V) or (B, L, V)")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride over V")
+    V = t.shape[-1]
+    if t.dim() == 2:
+        return t.shape[0], V, (t.stride(0) if t.shape[0] > 1 else V)
+    B, L, _ = t.shape
+    stride = t.stride(1) if L > 1 else (t.stride(0) if B > 1 else V)
+    if B > 1 and L > 0 and t.stride(0) != L * stride:
+        raise ValueError(f"{name} must have evenly spaced rows")
+    return B * L, V, stride
+
+
+def _sup(suppress_ids: Sequence[int]):
+    n = len(suppress_ids)
+    return ((C.c_int32 * n)(*[int(v) for v in suppress_ids]) if n else None), n
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, suppress_ids: Sequence[int] = (),
+                   out=None, stream=None):
+    """Scores given tokens under logits (T, V) or (B, L, V), bf16 or fp32.
+
+    Returns (logprob, entropy, lse, top_ids, top_logprob): float32 shaped like
+    ``targets`` (int32, the logits' shape without V; an id outside [0, V) is
+    no target and scores 0), and the ids (int32) and log probabilities of the
+    ``top`` largest logits, shaped (..., top); the last two are None when top
+    is 0.  ``out``: the same five, preallocated."""
+    _need_cuda(logits, targets)
+    T, V, stride = _rows(logits, "logits")
+    dt, dev, shape, top = _dtype_code(logits), logits.device, logits.shape[:-1], int(top)
+    _arg(targets, "targets", T, _I32, dev)
+    if targets is None:
+        raise ValueError("targets is needed")
+    if out is None:
+        lp, ent, lse = [_empty(shape, torch.float32, dev, stream) for _ in range(3)]
+        ids = _empty((*shape, top), torch.int32, dev, stream) if top > 0 else None
+        tlp = _empty((*shape, top), torch.float32, dev, stream) if top > 0 else None
+    else:
+        lp, ent, lse, ids, tlp = out
+        for t, name in ((lp, "logprob"), (ent, "entropy"), (lse, "lse")):
+            _arg(t, name, T, _F32, dev)
+        _arg(ids, "top_ids", T * top, _I32, dev)
+        _arg(tlp, "top_logprob", T * top, _F32, dev)
+    sup, n_sup = _sup(suppress_ids)
+    _check(_lib.dllm_token_logprobs(_ptr(logits), dt, T, V, stride, _ptr(targets), sup, n_sup, top, _ptr(lp),
+                                    _ptr(ent), _ptr(lse), _ptr(ids), _ptr(tlp), _stream(stream)),
+           "dllm_token_logprobs")
+    return lp, ent, lse, ids, tlp
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, entropy: torch.Tensor,
+                            grad_logprob: Optional[torch.Tensor], grad_entropy: Optional[torch.Tensor] = None,
+                            top_ids: Optional[torch.Tensor] = None, grad_top: Optional[torch.Tensor] = None,
+                            suppress_ids: Sequence[int] = (), out: Optional[torch.Tensor] = None, stream=None):
+    """The gradient of token_logprobs with respect to the logits, in their
+    dtype: from the saved ``lse`` and ``entropy`` and the gradients of
+    logprob, entropy and top_logprob (None: zero; ``grad_top`` comes with the
+    ``top_ids`` it belongs to).  ``out`` may be ``logits`` itself."""
+    _need_cuda(logits, targets)
+    T, V, stride = _rows(logits, "logits")
+    dt, dev = _dtype_code(logits), logits.device
+    if targets is None or lse is None or entropy is None:
+        raise ValueError("targets, lse and entropy are needed")
+    _arg(targets, "targets", T, _I32, dev)
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob"),
+                    (grad_entropy, "grad_entropy")):
+        _arg(t, name, T, _F32, dev)
+    top = 0
+    if grad_top is not None:
+        if top_ids is None or not torch.is_tensor(grad_top) or grad_top.dim() < 1:
+            raise ValueError("grad_top comes with the top_ids it belongs to")
+        top = grad_top.shape[-1]
+        _arg(grad_top, "grad_top", T * top, _F32, dev)
+        _arg(top_ids, "top_ids", T * top, _I32, dev)
+    if out is None:
+        out = _empty(logits.shape, logits.dtype, dev, stream)
+    elif not torch.is_tensor(out) or out.dtype != logits.dtype or out.device != dev or out.shape != logits.shape:
+        raise ValueError("out must be shaped and typed like logits, on the same device")
+    _, _, out_stride = _rows(out, "out")
+    sup, n_sup = _sup(suppress_ids)
+    _check(_lib.dllm_token_logprobs_backward(_ptr(logits), dt, T, V, stride, _ptr(targets), sup, n_sup, _ptr(lse),
+                                             _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), top,
+                                             _ptr(top_ids) if top else None, _ptr(grad_top) if top else None,
+                                             _ptr(out), out_stride, _stream(stream)), "dllm_token_logprobs_backward")
+    return out
+
+
+class _ScoreTokens(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, top, suppress_ids):
+        lp, ent, lse, ids, tlp = token_logprobs(logits, targets, top=top, suppress_ids=suppress_ids)
+        ctx.suppress_ids = suppress_ids
+        ctx.save_for_backward(logits, targets, lse, ent, ids)
+        if ids is not None:
+            ctx.mark_non_differentiable(ids)
+        return lp, ent, ids, tlp
+
+    @staticmethod
+    def backward(ctx, g_lp, g_ent, _g_ids, g_top):
+        logits, targets, lse, ent, ids = ctx.saved_tensors
+        # (gradients that reach here expanded from a scalar are not contiguous)
+        g_lp, g_ent, g_top = [None if g is None else g.float().contiguous() for g in (g_lp, g_ent, g_top)]
+        grad = token_logprobs_backward(logits, targets, lse, ent, g_lp, g_ent, ids if g_top is not None else None,
+                                       g_top, suppress_ids=ctx.suppress_ids)
+        return grad, None, None, None
+
+
+def score_tokens(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, suppress_ids: Sequence[int] = ()):
+    """token_logprobs for training: (logprob, entropy, top_ids, top_logprob),
+    differentiable with respect to ``logits`` through autograd."""
+    return _ScoreTokens.apply(logits, targets, int(top), tuple(suppress_ids))

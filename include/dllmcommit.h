@@ -470,6 +470,154 @@ dllm_status dllm_commit_step_host(const void* host_logits, void* dev_logits, dll
                                   int32_t n_suppress, const dllm_commit_params* params, void* dev_out,
                                   void* host_out, void* workspace, size_t workspace_bytes, dllm_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Paged 8-bit key/value cache.
+ *
+ * A block decoder attends from the block it is working on over the keys and
+ * values of the tokens already placed.  Here they are held as e4m3 codes in
+ * pages of page_size tokens, each page with one fp32 scale per head for its
+ * keys and one for its values; a token's key is code * scale.  The page is
+ * the "block of tokens" that shares a scale.
+ *   k, v              device, 16-byte aligned: codes [page][head][slot][dim]
+ *   k_scale, v_scale  device: [page][head], finite and positive
+ * head_dim 64 or 128; page_size 16, 32, 64 or 128 (else DLLM_ERR_UNSUPPORTED).
+ *
+ * A sequence's pages are its row of a page table (device int32 (B, width),
+ * row-major): token j of batch row b lies in slot j % page_size of page
+ * table[b * width + j / page_size].  An entry outside [0, num_pages) names
+ * no page: what is appended there is dropped, its tokens are not attended,
+ * and an eviction that keeps one stores zeros for it.  Lengths are device
+ * int32 (B), clamped to [0, width * page_size].
+ *
+ * Two calls that may run at the same time must not write the same page, nor
+ * one write a page the other reads.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_pages;
+  int32_t page_size, heads, head_dim;
+} dllm_kv_cache;
+
+/* Writes L new tokens per batch row at positions start[b] .. start[b] + L - 1
+ * (only the first count[b], clamped to [0, L], when count is not NULL).
+ * Positions below 0 or past the table are dropped.
+ *   k, v       device bf16, element (b, l, h, d) at b s[0] + l s[1] + h s[2] +
+ *              d with s = k_strides / v_strides (HOST, 3 elements each,
+ *              non-negative); bases 16-byte aligned and strides multiples of
+ *              8 (else DLLM_ERR_UNSUPPORTED)
+ *   start, count   device int32 (B); count may be NULL
+ * The scale of a page whose first slot is written is the smallest power of
+ * two s >= 2^-100 with max |x| <= 448 s over the new tokens of that page and
+ * head (finite values only); a page that is entered in the middle keeps its
+ * old scale where that is larger, and the tokens in front of the new ones are
+ * re-expressed when the scale grows (exact for power-of-two scales, but for
+ * values that fall below the smallest e4m3 magnitude).  Codes are x / s
+ * rounded to nearest even, infinities as +-448, NaN as NaN.  An append ends
+ * the sequence: slots behind the new tokens no longer hold anything, so a
+ * block that is denoised in steps is appended again at the same place. */
+dllm_status dllm_cache_append(const dllm_kv_cache* cache, const void* k, const void* v, const int64_t* k_strides,
+                              const int64_t* v_strides, int64_t B, int64_t L, const int32_t* table, int64_t width,
+                              const int32_t* start, const int32_t* count, dllm_stream_t stream);
+
+/* Attention of L queries per batch row over the first lens[b] cached tokens
+ * (all of them visible to every query: a block attends to itself and to what
+ * lies before it, so append the block first).
+ *   q          device bf16 (B, L, Hq, head_dim) with strides q_strides (HOST,
+ *              3 elements, as in dllm_cache_append); query head i reads key
+ *              head i / (Hq / heads); Hq a multiple of heads
+ *   key_mask   device uint8 (B rows mask_stride bytes apart, mask_stride >=
+ *              width * page_size) or NULL: tokens with 0 are not attended,
+ *              whatever their keys and values hold
+ *   scale      multiplies q . k (0 < scale <= 2^20)
+ *   out        device bf16 (B, L, Hq, head_dim) contiguous, 16-byte aligned
+ *   lse        device fp32 (B, L, Hq): ln sum exp(scale q . k)
+ * A query with no visible token gives out 0 and lse -inf.
+ *   weights    device fp32 (B, heads, width * page_size) or NULL:
+ *              weights = decay * weights + the sum over the queries of the
+ *              key head's group of each token's probability (0 for tokens
+ *              that are not attended; queries whose lse is not finite add
+ *              nothing).  decay in [0, 1]; with 0 the old weights are not read.
+ *   workspace  device, 16-byte aligned, >=
+ *              dllm_cache_attention_workspace_size(...) bytes, any contents
+ * Sums and statistics are fp32. */
+size_t dllm_cache_attention_workspace_size(int64_t B, int64_t L, int64_t Hq, int64_t heads, int64_t head_dim);
+
+dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, const int64_t* q_strides, int64_t B,
+                                 int64_t L, int64_t Hq, const int32_t* table, int64_t width, const int32_t* lens,
+                                 const uint8_t* key_mask, int64_t mask_stride, float scale, void* out, float* lse,
+                                 float* weights, float decay, void* workspace, size_t workspace_bytes,
+                                 dllm_stream_t stream);
+
+/* Cuts every sequence to its budget by the weights its tokens have drawn.
+ * Per batch row and head, of the n = lens[b] tokens min(n, budget) stay: the
+ * first keep_first, the last keep_last (keep_first + keep_last <= budget),
+ * and of the others those with the largest weights (NaN lowest, ties to the
+ * lower position).  They are copied in order to positions 0, 1, ... of
+ * dst_table's pages (device int32 (B, dst_width), dst_width * page_size >=
+ * budget; pages other than the sequence's own: a page that is read and
+ * written in the same call holds undefined codes), with the scale rule of
+ * dllm_cache_append over the tokens of each new page.
+ *   weights      device fp32 (B, heads, width * page_size)
+ *   keep         device int32 (B, heads, budget) output: the old positions in
+ *                order, -1 behind the last
+ *   lens_out     device int32 (B) output: min(n, budget)
+ *   weights_out  device fp32 like weights, output, not overlapping it: the
+ *                kept weights in order, 0 behind them */
+dllm_status dllm_cache_evict(const dllm_kv_cache* cache, const int32_t* table, int64_t width, const int32_t* lens,
+                             int64_t B, const float* weights, int64_t budget, int64_t keep_first, int64_t keep_last,
+                             const int32_t* dst_table, int64_t dst_width, int32_t* keep, int32_t* lens_out,
+                             float* weights_out, dllm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens.
+ *
+ * dllm_token_stats describes the model's own proposal; scoring a given canvas
+ * (rollouts under a policy, a client's log probabilities) needs the log
+ * probability of given ids under the same softmax.  For each of T rows over
+ * the ids A = {0..V-1} minus suppress_ids (NaN as -inf):
+ *   lse          ln sum_A exp(z)
+ *   logprob      z[target] - lse; 0 for a target outside [0, V) (no target),
+ *                -inf for a suppressed one
+ *   entropy      of softmax_A(z), clamped to [0, ln |A|]
+ *   top_ids, top_logprob  (T, top): the ids of the `top` largest logits,
+ *                largest first, equal logits lower id first, and their log
+ *                probabilities; 0 <= top <= min(DLLM_MAX_TOP, |A|); pass NULL
+ *                for both when top is 0
+ * +inf logits share all the mass equally (lse = +inf); a row without mass
+ * (every logit NaN or -inf) reads as uniform over A (lse = -inf).
+ * logits: device, rows row_stride elements apart, aligned to their element;
+ * targets device int32 (T); suppress_ids HOST as in dllm_token_stats; outputs
+ * device.  Any V and any stride: rows need not be 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+#define DLLM_MAX_TOP 32
+
+dllm_status dllm_token_logprobs(const void* logits, dllm_dtype dt, int64_t T, int64_t V, int64_t row_stride,
+                                const int32_t* targets, const int32_t* suppress_ids, int32_t n_suppress, int32_t top,
+                                float* logprob, float* entropy, float* lse, int32_t* top_ids, float* top_logprob,
+                                dllm_stream_t stream);
+
+/* The gradient with respect to the logits, given lse and entropy as
+ * dllm_token_logprobs returned them and the gradients of logprob (T), entropy
+ * (T) and top_logprob (T, top); each gradient may be NULL (zero; top 0
+ * without top_ids and grad_top).  With p = exp(z - lse):
+ *   grad = -p (G + grad_entropy (z - lse + entropy)) + one-hot terms,
+ *   G = grad_logprob + sum_j grad_top_j,
+ * the one-hot terms being grad_logprob at the target and grad_top_j at top_j
+ * (ids outside [0, V) and suppressed ids take no part).  Suppressed ids and
+ * rows whose lse is not finite get 0.  grad: device, the logits' dtype, rows
+ * grad_row_stride elements apart; it may be the logits' own buffer with the
+ * same stride (each value is read before it is replaced), else they must not
+ * overlap. */
+dllm_status dllm_token_logprobs_backward(const void* logits, dllm_dtype dt, int64_t T, int64_t V, int64_t row_stride,
+                                         const int32_t* targets, const int32_t* suppress_ids, int32_t n_suppress,
+                                         const float* lse, const float* entropy, const float* grad_logprob,
+                                         const float* grad_entropy, int32_t top, const int32_t* top_ids,
+                                         const float* grad_top, void* grad, int64_t grad_row_stride,
+                                         dllm_stream_t stream);
+
 /* Reads and clears the device fault word of a workspace (synchronises the
  * stream).  *fault = 0 when no kernel reported a fault; otherwise a code
  * naming the wait that gave up (the kernel stopped early; outputs of that
