@@ -8,21 +8,26 @@
 // The transposed products.  A tile is 128 tokens of one head.  S^T = K Q^T and
 // O^T += V^T P^T put the tokens (then the head dimension) on the tensor core's
 // 128 rows and the queries on its N columns, so a block of 32 queries, or a
-// single one, costs N = 32 or 16 columns and not a padded tile of 128 rows;
-// and a softmax thread holds one token, so masks, page scales and the weights'
-// sums are per-thread values.
-//   * K stays in 8 bits: kind::f8f6f4 on the codes as TMA brought them.  The
-//     queries are split into two e4m3 parts of one power-of-two scale per row,
-//     hi = e4m3(q / s), lo = e4m3(q / s - hi): a bf16 value has 8 significant
-//     bits, e4m3 holds 4 of either sign, so hi + lo is exact for elements above
-//     2^-9 of the row's largest and off by at most 2^-18 of it below.
-//   * V is widened to fp16, which holds e4m3 exactly; P is rounded to fp16 (11
-//     bits against bf16's 8) with the tokens' value scales folded in relative
-//     to a running reference, so nothing is rescaled per page.  Probabilities
-//     are kept at 64 p s_v / v_ref: full precision down to 2^-20 of the row's
-//     largest, absolute error 2^-31 of it below.
-//   * The reference m_r moves only when a score exceeds it by more than 4 (log2
-//     units), so the accumulator in TMEM is rarely rescaled; sums are fp32.
+// single one, costs N = 32 columns and not a padded tile of 128 rows; and a
+// softmax thread holds one token, so masks, page scales and the weights' sums
+// are per-thread values.
+//
+// K and V stay in 8 bits from HBM to the tensor core (kind::f8f6f4 on the codes
+// as TMA brought them): what bounds few rows is the bytes of the cache, and
+// then shared memory, which a widened copy of V crosses five times instead of
+// two.  The other operand is split into e4m3 parts instead:
+//   * a query row into hi = e4m3(q / s) and lo = e4m3(q / s - hi), s a power of
+//     two per row: a bf16 value has 8 significant bits and e4m3 holds 4 of
+//     either sign, so hi + lo is exact for elements above 2^-9 of the row's
+//     largest and off by at most 2^-18 of it below;
+//   * P, held at 64 p s_v / v_ref <= 256 with fp16's 11 bits (bf16 has 8), into
+//     three parts of 4 bits, the second and third of 16 and 256 times the
+//     remainder, with accumulators of their own: exact but for the rounding to
+//     fp16, which is 2^-12 of the value and no finer than 2^-23 of the row's
+//     reference (which lies up to 2 above the row's largest score).
+// The references m_r and v_ref move only when a score exceeds its reference by
+// more than 2 (log2 units) or a page's value scale its own, so the accumulators
+// in TMEM are rarely rescaled; statistics and sums are fp32.
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
 #include <cuda_runtime.h>
 
@@ -59,9 +64,10 @@ struct AttendParams {
   int32_t rows;                // L G: the rows of a key head
   int32_t row_tiles;           // tiles of at most N rows
   int32_t tile_rows;           // rows per row tile (the last may hold fewer)
+  int32_t half;                // rows of a softmax group: tile_rows, or half of them when the groups are paired
   int32_t ctas;
-  float* part_o;               // (2 ctas, N, D): a CTA's unfinished first and last segment
-  float* part_ml;              // (2 ctas, N, 2)
+  float* part_o;               // (2 ctas, columns, D): a CTA's unfinished first and last segment
+  float* part_ml;              // (2 ctas, columns, 2)
   int32_t* fault;
 };
 
@@ -146,24 +152,32 @@ __device__ __forceinline__ void at_tma_load(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void at_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Issued by the one thread of the warp whose `lead` is set; the whole warp
+// executes the code around it, so that addresses and descriptors stay in
+// uniform registers (computed by a single thread, they cost several times the
+// product's own issue time).  Descriptors share their high words.
+__device__ __forceinline__ void at_mma_f8(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                          uint32_t b_hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
 
-__device__ __forceinline__ void at_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void at_commit(uint32_t lead, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
       : "memory");
 }
 
-__device__ __forceinline__ void at_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void at_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void at_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -202,35 +216,33 @@ __device__ __forceinline__ void at_ld(uint32_t t, uint32_t (&r)[C]) {
   }
 }
 
-// The same columns back; complete when the call returns.
-__device__ __forceinline__ void at_st8(uint32_t t, const uint32_t* r) {
+// 16 columns back (complete after tcgen05.wait::st).
+__device__ __forceinline__ void at_st16(uint32_t t, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
 // Shared-memory matrix descriptors: start address / 16 (bits 0-13), leading
 // and stride byte offsets / 16 (bits 16-29, 32-45), version 1 (bit 46), swizzle
 // (bits 61-63: 2 = 128 bytes, 4 = 64 bytes, 6 = 32 bytes).
-//   K-major (K tile and queries, rows of head_dim bytes): the stride offset is
-//   the distance of 8-row groups, the leading offset is not used.
-//   MN-major (V and P, one row of 64 elements per token, P's of N when that is
-//   less): a row is one swizzle span; the leading offset is the distance of
-//   groups of 64 elements, the stride offset that of 8-token groups.
-__device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t leading, uint32_t stride, uint32_t swizzle) {
-  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(leading >> 4) << 16;
-  d |= static_cast<uint64_t>(stride >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(swizzle) << 61;
-  return d;
+//   K-major (K and queries, a row of head_dim bytes per token or query): the
+//   stride offset is the distance of 8-row groups, the leading one is not used.
+//   MN-major (V and P, a row per token that is one swizzle span of head_dim or
+//   N bytes): the leading offset is the distance of such spans along M or N, the
+//   stride offset that of 8-token groups.
+__device__ __forceinline__ uint32_t at_desc_lo(uint32_t saddr, uint32_t leading) {
+  return ((saddr & 0x3FFFFu) >> 4) | (leading >> 4) << 16;
+}
+__device__ __forceinline__ constexpr uint32_t at_desc_hi(uint32_t stride, uint32_t swizzle) {
+  return (stride >> 4) | 1u << 14 | swizzle << 29;
 }
 
-// Instruction descriptor: fp32 accumulator (bits 4-5 = 1), operand types 0
-// (e4m3 for kind::f8f6f4, fp16 for kind::f16), A and B MN-major where set (bits
-// 15, 16), N / 8 in bits 17-22, M / 16 in bits 24-28.
+// Instruction descriptor: fp32 accumulator (bits 4-5 = 1), both operands e4m3
+// (0), A and B MN-major where set (bits 15, 16), N / 8 in bits 17-22, M / 16 in
+// bits 24-28.
 constexpr uint32_t at_idesc(int n, bool mn_major) {
   return (1u << 4) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kTile >> 4) << 24);
@@ -252,6 +264,21 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
+
+// One part of P.  Two values of h = 2^-8 P <= 1 in fp16: the fp16 bits 14 .. 7
+// (5 bits of exponent, the top one 0, and 3 of mantissa, subnormals alike) are
+// the e4m3 code of P rounded toward zero; what is left, exact in fp16, times 16
+// is the next part's h.  (Conversions to e4m3 run at a quarter of the rate of
+// these integer and half-precision instructions.)
+__device__ __forceinline__ uint32_t part_rest16(uint32_t h) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
+      : "=r"(r)
+      : "r"(h), "r"(h & 0xFF80FF80u), "r"(0x4C004C00u));  // 16, 16
+  return r;
+}
+// The codes of four values: bits 14 .. 7 of the halves of a, then of b.
+__device__ __forceinline__ uint32_t part_codes(uint32_t a, uint32_t b) { return __byte_perm(a << 1, b << 1, 0x7531); }
 
 // Whether any of the 128 threads of named barrier `id` has p set.
 __device__ __forceinline__ bool group_any(uint32_t id, bool p) {
@@ -277,16 +304,27 @@ __device__ __forceinline__ int tiles_of(const AttendParams& p, int64_t b) {
   return n > 0 ? (n + kTile - 1) / kTile : 1;  // (an empty sequence still has its zeros written)
 }
 
-__device__ __forceinline__ int64_t cta_begin(int64_t total, int64_t cta, int64_t ctas) { return total * cta / ctas; }
+// CTA c's range begins at tile c q + min(c, r), q = total / ctas, r = total mod
+// ctas (the host keeps totals below 2^31).
+struct Split {
+  uint32_t q, r;
+  __device__ __forceinline__ Split(uint32_t total, uint32_t ctas) : q(total / ctas), r(total % ctas) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * q + min(c, r); }
+  // The CTA that holds a tile.
+  __device__ __forceinline__ uint32_t owner(uint32_t w) const {
+    const uint32_t wide = r * (q + 1);
+    return w < wide ? w / (q + 1) : r + (w - wide) / max(q, 1u);
+  }
+};
 
 struct Cursor {
-  int64_t w, w1;   // position and end of the CTA's range
-  int64_t b;       // batch row at w
-  int64_t off;     // position within the batch row's tiles
+  uint32_t w, w1;  // position and end of the CTA's range
+  int32_t b;       // batch row at w
+  uint32_t off;    // position within the batch row's tiles
 };
 
 struct Segment {
-  int64_t b;
+  int32_t b;
   int32_t h, rt;   // key head, row tile
   int32_t t0, t1;  // tiles [t0, t1) of the sequence
   int32_t T;       // tiles of the sequence
@@ -294,122 +332,139 @@ struct Segment {
   bool starts_range;
 };
 
-__device__ __forceinline__ bool next_segment(const AttendParams& p, Cursor& c, int64_t w0, Segment& s) {
+__device__ __forceinline__ bool next_segment(const AttendParams& p, Cursor& c, uint32_t w0, Segment& s) {
   if (c.w >= c.w1) return false;
   s.b = c.b;
   s.len = attend_len(p, c.b);
   s.T = s.len > 0 ? (s.len + kTile - 1) / kTile : 1;
-  const int64_t hr = c.off / s.T;
-  s.h = static_cast<int32_t>(hr / p.row_tiles);
-  s.rt = static_cast<int32_t>(hr % p.row_tiles);
-  s.t0 = static_cast<int32_t>(c.off % s.T);
-  const int64_t left = c.w1 - c.w;
-  s.t1 = s.t0 + left < s.T ? static_cast<int32_t>(s.t0 + left) : s.T;
+  const uint32_t hr = c.off / static_cast<uint32_t>(s.T);
+  s.h = static_cast<int32_t>(hr / static_cast<uint32_t>(p.row_tiles));
+  s.rt = static_cast<int32_t>(hr % static_cast<uint32_t>(p.row_tiles));
+  s.t0 = static_cast<int32_t>(c.off % static_cast<uint32_t>(s.T));
+  s.t1 = static_cast<int32_t>(min(static_cast<uint32_t>(s.T), s.t0 + (c.w1 - c.w)));
   s.starts_range = c.w == w0;
   c.w += s.t1 - s.t0;
   c.off += s.t1 - s.t0;
-  if (c.off == static_cast<int64_t>(p.c.heads) * p.row_tiles * s.T) {
+  if (c.off == static_cast<uint32_t>(p.c.heads * p.row_tiles) * s.T) {
     ++c.b;
     c.off = 0;
   }
   return true;
 }
 
-// One warp: the tiles of batch rows before `upto`, in every lane.
-__device__ __forceinline__ int64_t tiles_before(const AttendParams& p, int64_t upto) {
-  int64_t sum = 0;
-  for (int64_t b = threadIdx.x & 31; b < upto; b += 32) sum += tiles_of(p, b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  return sum;
+// One warp: the tiles of one head and row tile of the batch rows before `upto`,
+// and of all of them, in every lane.
+__device__ __forceinline__ uint2 tiles_before(const AttendParams& p, int64_t upto) {
+  uint32_t sum = 0, all = 0;
+  for (int64_t b = threadIdx.x & 31; b < p.B; b += 32) {
+    const uint32_t t = static_cast<uint32_t>(tiles_of(p, b));
+    all += t;
+    if (b < upto) sum += t;
+  }
+  return make_uint2(__reduce_add_sync(0xFFFFFFFFu, sum), __reduce_add_sync(0xFFFFFFFFu, all));
 }
 
 // ---------------------------------------------------------------------------
 // the attention kernel
 // ---------------------------------------------------------------------------
-constexpr int kSoftWarps = 8;                          // two groups of 4 warps; a group owns half the columns
-constexpr int kWideWarps = 4;                          // widen V
-constexpr int kTmaWarp = kSoftWarps + kWideWarps;
-constexpr int kMmaWarp = kTmaWarp + 1;
-constexpr int kAttendThreads = (kMmaWarp + 1) * 32;
+// Warps: two groups of 4 softmax warps, one warp for the copies, one for the
+// products.  A group owns a score buffer, a P buffer and an accumulator, and
+// works with N columns.  A "job" is one tile for one group:
+//   taking turns (at most N rows): the groups take the tiles alternately, each
+//   with references and sums of its own, joined at the segment's end (a job is a
+//   chain of waits, TMEM reads and barriers longer than the time of a tile, so
+//   two are in flight);
+//   paired (up to 2 N rows): both groups take every tile, each for its half of
+//   the rows, so K and V are read once for up to 128 rows.
+// Job J belongs to group J & 1 and is that group's (J >> 1)-th.
+template <int N, bool PAIR>
+struct AttendShape {
+  static constexpr int kRows = PAIR ? 2 * N : N;             // columns of both groups
+  static constexpr bool kConcat = N == 32;                   // hi and lo parts as 2 N columns of one product
+  static constexpr int kScoreCols = kConcat ? 2 * N : N;     // (with N = 64 TMEM has no room: two products, one sum)
+  static constexpr int kStages = N == 32 ? 5 : 4;            // of the K and V rings
+  static constexpr int kPBytes = 3 * kTile * N;
+  static constexpr int kScore = 0, kAcc = 2 * kScoreCols;    // TMEM columns: scores, then accumulators of 3 N
+};
+constexpr int kSoftWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
+// 384 threads are launched with 168 registers each; the softmax warps (N
+// exponents and N sums a thread) take what the last group leaves: 256 x 216 +
+// 128 x 72 = 384 x 168.
+constexpr int kAttendThreads = 384;
+constexpr uint32_t kTmemCols = 512;
 constexpr int kMetaSlots = 8;
-constexpr float kSlack = 4.0f;                         // log2: how far a score may exceed the reference
+constexpr float kSlack = 2.0f;                         // log2: how far a score may exceed the reference
+constexpr float kHead = 1.0f;                          // log2: how far a new reference lies above its score
 constexpr float kUnset = -1e30f;                       // the reference before the first score
-constexpr float kPUnit = 64.0f;                        // P is held at 64 p s_v / v_ref: at most 2^(6 + 4 + 4) in fp16
-
-template <int N>
-constexpr int k_stages() { return 3; }
-template <int N>
-constexpr int v_stages() { return N == 128 ? 2 : 3; }
-template <int N>
-constexpr int p_buffers() { return N == 128 ? 1 : 2; }  // (a second buffer would cost a ring stage)
-template <int N>
-constexpr int p_bytes() { return kTile * N * 2; }
-constexpr int kWideBytes = 32768;                      // a tile of V in fp16: 2 groups of 64 dims x 128 tokens
-template <int D, int N>
+constexpr float kPUnit = 64.0f;                        // P is held at 64 p s_v / v_ref: at most 2^(6 + 2) (e4m3 ends at 448)
+template <int D, int N, bool PAIR>
 constexpr int attend_smem() {
-  return 1024 + 2 * kWideBytes + p_buffers<N>() * p_bytes<N>() + 2 * N * D +
-         (k_stages<N>() + v_stages<N>()) * kTile * D;
+  using S = AttendShape<N, PAIR>;
+  return 1024 + 2 * S::kPBytes + 2 * S::kRows * D + 2 * S::kStages * kTile * D + (D == 64 ? kTile * D : 0);
 }
 
 struct TileMeta {
-  float ks[8], vs[8];   // per page of the tile: scale log2 e s_k, and s_v
-  uint32_t valid[4];    // visible tokens
+  alignas(16) uint8_t mask[kTile];  // the tile's part of the key mask, when there is one
+  float ks[8], vs[8];               // per page of the tile: scale log2 e s_k, and s_v
+  uint32_t pages;                   // bits of the pages that exist
+  int32_t left;                     // tokens of the sequence in the tile
 };
 
-// What the MMA and softmax roles share about a tile is in its meta slot; a
-// slot is reused after kMetaSlots tiles, which no role lags behind the
-// producer (K stages + 2 score buffers + 1).
-template <int N>
+__device__ __forceinline__ bool tile_visible(const TileMeta& m, int key, int page, bool masked) {
+  return key < m.left && ((m.pages >> page) & 1u) && (!masked || m.mask[key] != 0);
+}
+
+// What the roles share about a tile is in its meta slot; a slot is reused
+// after kMetaSlots tiles, and the producer is never that far ahead of a role
+// that reads it (kStages tiles ahead of the products, those two jobs ahead of
+// the softmax).
+template <int N, bool PAIR>
 struct AttendShared {
-  uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
+  uint64_t kfull[5], kempty[5], vfull[5], vempty[5];
   uint64_t mfull[kMetaSlots];
-  uint64_t sfull[2], sempty[2], pfull[2], wfull[2], pvdone[2];
+  uint64_t sfull[2], sempty[2], pfull[2], pvdone[2];
   uint64_t qfull;
   TileMeta meta[kMetaSlots];
-  alignas(16) float f[N];    // query scales
-  alignas(16) float nm[N];   // minus the references
-  alignas(16) float fac_o[N];
-  alignas(16) float fac_l[N];
-  float red[2][4][N / 2];
-  int32_t row[N];        // output rows, -1 past the tile's rows
-  int64_t w0, w1, b0, off0;
+  alignas(16) float f[AttendShape<N, PAIR>::kRows];    // query scales
+  alignas(16) float nm[2][N];                          // per group: minus the references,
+  alignas(16) float fac_o[2][N];                       // the factors of a rise,
+  alignas(16) float fac_l[2][N];
+  float red[2][4][N];                                  // maxima or sums per warp
+  float vref[2];
+  float fin[2][N];                                     // what an accumulator's column is multiplied with at the end
+  int32_t row[AttendShape<N, PAIR>::kRows];            // output rows, -1 where a column has none
+  uint32_t w0, w1, off0;
+  int32_t b0;
   uint32_t tmem;
   int32_t abort;
 };
 
-template <int D, int N>
+template <int D, int N, bool PAIR>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int HALF = N / 2;                          // columns of a softmax group
-  constexpr int C = HALF < 32 ? HALF : 32;             // columns read from TMEM at a time
-  constexpr int KST = k_stages<N>(), VST = v_stages<N>(), PB = p_buffers<N>();
+  using S = AttendShape<N, PAIR>;
+  constexpr int ST = S::kStages;
   constexpr int kTileBytes = kTile * D;
-  constexpr uint32_t kPRow = N >= 64 ? 128 : 2 * N;    // bytes of a token's row of P (of a group of 64 columns)
-  constexpr uint32_t kPSwz = N >= 64 ? 2 : (N == 32 ? 4 : 6);
-  constexpr uint32_t kCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
+  constexpr uint32_t kSwz = D == 128 ? 2u : 4u;        // K, V and queries: rows of D bytes, swizzled over D bytes
   extern __shared__ __align__(1024) uint8_t at_smem[];
-  __shared__ AttendShared<N> sh;
+  __shared__ AttendShared<N, PAIR> sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(at_smem) + 1023u) & ~1023u;
-  const uint32_t wide_s = base, p_s = wide_s + 2 * kWideBytes, q_s = p_s + PB * p_bytes<N>();
-  const uint32_t k_s = q_s + 2 * N * D, v_s = k_s + KST * kTileBytes;
+  const uint32_t p_s = base, q_s = p_s + 2 * S::kPBytes, k_s = q_s + 2 * S::kRows * D;
+  const uint32_t v_s = k_s + ST * kTileBytes, zero_s = v_s + ST * kTileBytes;
   volatile int32_t* abort_flag = &sh.abort;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < KST; ++i) {
+    for (int i = 0; i < ST; ++i) {
       mbar_init(smem_addr(&sh.kfull[i]), 1);
       mbar_init(smem_addr(&sh.kempty[i]), 1);
-    }
-    for (int i = 0; i < VST; ++i) {
       mbar_init(smem_addr(&sh.vfull[i]), 1);
-      mbar_init(smem_addr(&sh.vempty[i]), kWideWarps);
+      mbar_init(smem_addr(&sh.vempty[i]), 1);
     }
     for (int i = 0; i < kMetaSlots; ++i) mbar_init(smem_addr(&sh.mfull[i]), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.sfull[i]), 1);
-      mbar_init(smem_addr(&sh.sempty[i]), kSoftWarps);
-      mbar_init(smem_addr(&sh.pfull[i]), kSoftWarps);
-      mbar_init(smem_addr(&sh.wfull[i]), kWideWarps);
+      mbar_init(smem_addr(&sh.sempty[i]), 4);
+      mbar_init(smem_addr(&sh.pfull[i]), 4);
       mbar_init(smem_addr(&sh.pvdone[i]), 1);
     }
     mbar_init(smem_addr(&sh.qfull), kSoftWarps);
@@ -418,23 +473,24 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
-                 "r"(kCols)
+                 "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   if (warp == 0) {   // this CTA's range and the batch row it begins in
-    const int64_t hr = static_cast<int64_t>(p.c.heads) * p.row_tiles;
-    const int64_t total = tiles_before(p, p.B) * hr;
-    const int64_t w0 = cta_begin(total, blockIdx.x, p.ctas), w1 = cta_begin(total, blockIdx.x + 1, p.ctas);
-    int64_t before = 0, b = 0;
+    const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
+    const Split split(tiles_before(p, 0).y * hr, gridDim.x);
+    const uint32_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
+    uint32_t before = 0;
+    int32_t b = 0;
     while (b < p.B) {                                  // 32 batch rows at a time
-      const int64_t t = b + lane < p.B ? tiles_of(p, b + lane) * hr : 0;
-      int64_t inc = t;
+      const uint32_t t = b + lane < p.B ? tiles_of(p, b + lane) * hr : 0;
+      uint32_t inc = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += u;
       }
       const unsigned in = __ballot_sync(0xFFFFFFFFu, b + lane < p.B && before + inc > w0);
@@ -454,10 +510,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       sh.off0 = w0 - before;
     }
   }
-  if (D == 64)       // the upper 64 rows of V^T: zeros, once
-    for (int i = threadIdx.x; i < 2 * 16384 / 16; i += kAttendThreads)
-      sts128(wide_s + static_cast<uint32_t>(i / 1024) * kWideBytes + 16384u + static_cast<uint32_t>(i % 1024) * 16u, 0u,
-             0u, 0u, 0u);
+  if (D == 64)       // the upper 64 rows of V^T: zeros
+    for (int i = threadIdx.x; i < kTileBytes / 16; i += kAttendThreads)
+      sts128(zero_s + static_cast<uint32_t>(i) * 16u, 0u, 0u, 0u, 0u);
   at_fence_async();
   at_fence_before();
   __syncthreads();
@@ -488,216 +543,235 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   const int ps = p.c.page_size;
   const int ppt = kTile / ps;                          // pages per tile
 
-  if (warp == kTmaWarp) {
-    // Lane i < ppt follows page i of the tiles.  A page's id is fetched two
-    // tiles ahead and its scales one tile ahead of the copies that use them.
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kCopyWarp) {
+    // A batch is up to 32 pages of one segment, one to a lane: ids are fetched
+    // two batches ahead and scales one batch ahead of the copies that use
+    // them, since each can cost a DRAM latency (tile by tile, that latency was
+    // the time per tile).
+    const int batch_tiles = 32 / ppt;
+    struct Batch {
+      int32_t b, h, len, t0, n, id;   // batch row, head, length, first tile, tiles; this lane's page id, or -1
+    };
+    struct Page {
+      int32_t at;                     // page heads + head, or -1
+      float ks, vs;
+    };
     Cursor look = cur;
     Segment ahead;
-    int lt = 0;
     bool more = next_segment(p, look, sh.w0, ahead);
-    if (more) lt = ahead.t0;
-    struct Item {
-      int64_t at;      // page heads + head, or -1
-      float ks, vs;
-      uint32_t nib;    // visible tokens among this lane's four
-    };
-    struct Raw {
-      int32_t id;
-      uint32_t nib;
-      int32_t h;
-      bool on;
-    };
-    auto fetch = [&](Raw& r) {                         // the next tile's page id and mask bits
-      r.on = more;
-      r.id = -1;
-      r.nib = 0;
-      r.h = 0;
+    int at_tile = more ? ahead.t0 : 0;
+    auto fetch = [&](Batch& t) {                       // the next batch's page ids
+      t.n = 0;
+      t.id = -1;
       if (!more) return;
-      const int64_t col = static_cast<int64_t>(lt) * ppt + lane;
-      r.h = ahead.h;
-      const int left = ahead.len - lt * kTile;         // tokens from this tile on
-      if (lane < ppt && lane * ps < left) r.id = p.table[ahead.b * p.width + col];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = lane * 4 + i;
-        bool v = j < left;
-        if (v && p.mask) v = p.mask[ahead.b * p.mask_stride + static_cast<int64_t>(lt) * kTile + j] != 0;
-        r.nib |= (v ? 1u : 0u) << i;
-      }
-      if (++lt == ahead.t1) {
+      t.b = ahead.b;
+      t.h = ahead.h;
+      t.len = ahead.len;
+      t.t0 = at_tile;
+      t.n = min(batch_tiles, ahead.t1 - at_tile);
+      const int64_t col = static_cast<int64_t>(at_tile) * ppt + lane;
+      if (lane < t.n * ppt && col * ps < t.len) t.id = p.table[static_cast<int64_t>(ahead.b) * p.width + col];
+      at_tile += t.n;
+      if (at_tile == ahead.t1) {
         more = next_segment(p, look, sh.w0, ahead);
-        if (more) lt = ahead.t0;
+        if (more) at_tile = ahead.t0;
       }
     };
-    auto scales = [&](const Raw& r, Item& it) {
-      it.at = r.id >= 0 && r.id < p.c.pages ? static_cast<int64_t>(r.id) * p.c.heads + r.h : -1;
-      it.ks = it.vs = 0.0f;
-      if (it.at >= 0) {
-        it.ks = p.c.k_scale[it.at];
-        it.vs = p.c.v_scale[it.at];
+    auto scales = [&](const Batch& t) {
+      Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f};
+      if (pg.at >= 0) {
+        pg.ks = p.c.k_scale[pg.at];
+        pg.vs = p.c.v_scale[pg.at];
       }
-      it.nib = r.nib;
+      return pg;
     };
-    Raw r0, r1;
-    Item now, then;
-    fetch(r0);
-    fetch(r1);
-    scales(r0, now);
-    bool have = r0.on;
-    while (have) {
-      const bool next_have = r1.on;
-      scales(r1, then);
-      fetch(r1);
-      const uint32_t ks = g % KST, vs = g % VST, ms = g % kMetaSlots;
-      wait(sh.kempty[ks], ((g / KST) & 1u) ^ 1u, kFaultEmptyWait);
-      wait(sh.vempty[vs], ((g / VST) & 1u) ^ 1u, kFaultEmptyWait);
-      const bool ok = now.at >= 0;
-      const unsigned pages = __ballot_sync(0xFFFFFFFFu, ok);
-      TileMeta& m = sh.meta[ms];
-      if (lane < 8) {
-        m.ks[lane] = now.ks * p.scale2;
-        m.vs[lane] = now.vs;
-      }
-      uint32_t bits = (pages >> (lane * 4 / ps)) & 1u ? now.nib << ((lane & 7) * 4) : 0u;
-      bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 1);
-      bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 2);
-      bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 4);
-      if ((lane & 7) == 0) m.valid[lane >> 3] = bits;
-      __syncwarp();
-      if (!*abort_flag) {
+    Batch now, next;
+    fetch(now);
+    fetch(next);
+    Page page = scales(now);
+    while (now.n > 0) {
+      Batch later;
+      const Page next_page = scales(next);
+      fetch(later);
+      const unsigned named = __ballot_sync(0xFFFFFFFFu, page.at >= 0);
+      for (int i = 0; i < now.n; ++i, ++g) {
+        const uint32_t st = g % ST, ms = g % kMetaSlots;
+        wait(sh.kempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
+        wait(sh.vempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
+        const int slot = lane - i * ppt;               // of this lane's page in the tile
+        const bool mine = slot >= 0 && slot < ppt;
+        const unsigned pages = (named >> (i * ppt)) & (0xFFFFFFFFu >> (32 - ppt));
+        if (*abort_flag) continue;
         if (lane == 0) {
           const uint32_t bytes = static_cast<uint32_t>(__popc(pages) * ps * D);
-          mbar_arrive(smem_addr(&sh.mfull[ms]));
-          mbar_arrive_expect_tx(smem_addr(&sh.kfull[ks]), bytes);
-          mbar_arrive_expect_tx(smem_addr(&sh.vfull[vs]), bytes);
+          mbar_arrive_expect_tx(smem_addr(&sh.kfull[st]), bytes);
+          mbar_arrive_expect_tx(smem_addr(&sh.vfull[st]), bytes);
         }
         __syncwarp();
-        if (ok) {
-          const int y = static_cast<int>(now.at * ps);
-          const uint32_t to = static_cast<uint32_t>(lane * ps * D);
-          at_tma_load(k_s + ks * kTileBytes + to, &p.tm_k, 0, y, smem_addr(&sh.kfull[ks]));
-          at_tma_load(v_s + vs * kTileBytes + to, &p.tm_v, 0, y, smem_addr(&sh.vfull[vs]));
+        if (mine && page.at >= 0) {
+          const int y = page.at * ps;
+          const uint32_t to = static_cast<uint32_t>(slot * ps * D);
+          at_tma_load(k_s + st * kTileBytes + to, &p.tm_k, 0, y, smem_addr(&sh.kfull[st]));
+          at_tma_load(v_s + st * kTileBytes + to, &p.tm_v, 0, y, smem_addr(&sh.vfull[st]));
         }
+        TileMeta& m = sh.meta[ms];
+        const int64_t j0 = static_cast<int64_t>(now.t0 + i) * kTile;
+        if (mine) {
+          m.ks[slot] = page.ks * p.scale2;
+          m.vs[slot] = page.vs;
+        }
+        if (lane == 0) {
+          m.pages = pages;
+          m.left = min(kTile, now.len - static_cast<int32_t>(j0));
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (p.mask) {
+            const uint32_t mb = static_cast<uint32_t>(min(static_cast<int64_t>(kTile), p.cap - j0));
+            mbar_arrive_expect_tx(smem_addr(&sh.mfull[ms]), mb);
+            bulk_copy_g2s(smem_addr(m.mask), p.mask + static_cast<int64_t>(now.b) * p.mask_stride + j0, mb,
+                          smem_addr(&sh.mfull[ms]));
+          } else {
+            mbar_arrive(smem_addr(&sh.mfull[ms]));
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      now = then;
-      have = next_have;
-      ++g;
+      now = next;
+      next = later;
+      page = next_page;
     }
     // On an abort the copies in flight are waited for (bounded) before the CTA ends.
     if (*abort_flag && lane == 0) {
-      for (uint32_t i = g > 4 ? g - 4 : 0; i < g; ++i) {
-        (void)mbar_wait_bounded(smem_addr(&sh.kfull[i % KST]), (i / KST) & 1u);
-        (void)mbar_wait_bounded(smem_addr(&sh.vfull[i % VST]), (i / VST) & 1u);
+      for (uint32_t i = g > ST ? g - ST : 0; i < g; ++i) {
+        (void)mbar_wait_bounded(smem_addr(&sh.kfull[i % ST]), (i / ST) & 1u);
+        (void)mbar_wait_bounded(smem_addr(&sh.vfull[i % ST]), (i / ST) & 1u);
+        (void)mbar_wait_bounded(smem_addr(&sh.mfull[i % kMetaSlots]), (i / kMetaSlots) & 1u);
       }
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t kSwz = D == 128 ? 2u : 4u;    // K tile and queries: rows of D bytes, swizzled over D bytes
-      auto scores = [&](uint32_t t) {                  // S^T of tile t: K (codes) x (hi + lo)
-        wait(sh.kfull[t % KST], (t / KST) & 1u, kFaultFullWait);
-        wait(sh.sempty[t & 1u], ((t >> 1) & 1u) ^ 1u, kFaultEmptyWait);
-        if (*abort_flag) return;
+    } else if (warp == kMmaWarp) {
+    constexpr uint32_t kPerTile = PAIR ? 2 : 1;        // jobs of a tile
+    constexpr uint32_t kHiK = at_desc_hi(8 * D, kSwz), kHiP = at_desc_hi(8 * N, N == 64 ? 4u : 6u);
+    const uint32_t lead = elect_one();
+    const uint32_t kd = at_desc_lo(k_s, 16), qd = at_desc_lo(q_s, 16), pd = at_desc_lo(p_s, kTile * N);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    // Stage and phase of the next tile whose scores, and whose output product, are issued.
+    uint32_t ss = 0, sp = 0, vs = 0, vp = 0;
+    uint32_t js = 0, jv = 0;                           // jobs issued of either
+    auto scores = [&]() {                              // S^T of job js: K (codes) x (hi, lo)
+      const uint32_t grp = js & 1u;
+      wait(sh.kfull[ss], sp, kFaultFullWait);
+      wait(sh.sempty[grp], ((js >> 1) & 1u) ^ 1u, kFaultEmptyWait);
+      __syncwarp();
+      const bool last = kPerTile == 1 || grp == 1;
+      if (!*abort_flag) {
         at_fence_after();
-        const uint32_t k = k_s + (t % KST) * kTileBytes, d = tmem + (t & 1u) * N;
+        const uint32_t k = kd + ss * (kTileBytes >> 4), q = qd + (PAIR ? grp * (2 * N * D >> 4) : 0u);
+        const uint32_t d = tm + S::kScore + grp * S::kScoreCols;
+        constexpr int kParts = S::kConcat ? 1 : 2;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            at_mma_f8(d, at_desc(k + kk * 32, 16, 8 * D, kSwz),
-                      at_desc(q_s + part * N * D + kk * 32, 16, 8 * D, kSwz), at_idesc(N, false),
-                      part != 0 || kk != 0 ? 1u : 0u);
-        at_commit(smem_addr(&sh.kempty[t % KST]));
-        at_commit(smem_addr(&sh.sfull[t & 1u]));
-      };
-      uint32_t seg = 0;
-      while (next_segment(p, cur, sh.w0, sg)) {
-        const uint32_t n = static_cast<uint32_t>(sg.t1 - sg.t0);
-        wait(sh.qfull, seg & 1u, kFaultFullWait);
-        scores(g);
-        for (uint32_t i = 0; i < n; ++i) {
-          if (i + 1 < n) scores(g + i + 1);
-          const uint32_t t = g + i;
-          wait(sh.wfull[t & 1u], (t >> 1) & 1u, kFaultFullWait);
-          wait(sh.pfull[t & 1u], (t >> 1) & 1u, kFaultFullWait);
-          if (*abort_flag) continue;
-          at_fence_after();
-          const uint32_t v = wide_s + (t & 1u) * kWideBytes, pp = p_s + (t % PB) * p_bytes<N>();
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            at_mma_f16(tmem + 2 * N, at_desc(v + kk * 2048, 16384, 1024, 2), at_desc(pp + kk * 16 * kPRow, 16384, 8 * kPRow, kPSwz),
-                       at_idesc(N, true), i != 0 || kk != 0 ? 1u : 0u);
-          at_commit(smem_addr(&sh.pvdone[t & 1u]));
+        for (int i = 0; i < kParts * (D / 32); ++i) {
+          const int part = i / (D / 32), kk = i % (D / 32);
+          at_mma_f8(lead, d, k + kk * 2, kHiK, q + part * (N * D / 16) + kk * 2, kHiK,
+                    at_idesc(S::kScoreCols, false), i != 0 ? 1u : 0u);
         }
-        g += n;
-        ++seg;
+        if (last) at_commit(lead, smem_addr(&sh.kempty[ss]));
+        at_commit(lead, smem_addr(&sh.sfull[grp]));
       }
-    }
-  } else if (warp >= kSoftWarps) {
-    // Widen V: 16 codes (one 16-byte piece of a token) at a time, tokens that are not visible as zeros.
-    const int tid = threadIdx.x - kSoftWarps * 32;
-    constexpr int kPieces = D / 16;                    // of a token
+      __syncwarp();
+      ++js;
+      if (last && ++ss == ST) {
+        ss = 0;
+        sp ^= 1u;
+      }
+    };
+    uint32_t seg = 0;
     while (next_segment(p, cur, sh.w0, sg)) {
-      for (int i = sg.t0; i < sg.t1; ++i, ++g) {
-        wait(sh.mfull[g % kMetaSlots], (g / kMetaSlots) & 1u, kFaultFullWait);
-        wait(sh.vfull[g % VST], (g / VST) & 1u, kFaultFullWait);
-        if (g >= 2) wait(sh.pvdone[g & 1u], ((g >> 1) & 1u) ^ 1u, kFaultEmptyWait);   // the product that read this buffer
-        const TileMeta& m = sh.meta[g % kMetaSlots];
-        const uint32_t src = v_s + (g % VST) * kTileBytes, dst = wide_s + (g & 1u) * kWideBytes;
-#pragma unroll
-        for (int it = 0; it < kPieces; ++it) {
-          const int piece = it * 128 + tid, key = piece / kPieces, c = piece % kPieces;
-          uint4 x = lds128(src + static_cast<uint32_t>(piece) * 16u);
-          if (!((m.valid[key >> 5] >> (key & 31)) & 1u)) x = make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t row = dst + (c >= 4 ? 16384u : 0u) + static_cast<uint32_t>(key) * 128u;
-          const uint32_t lo = static_cast<uint32_t>(((c & 3) * 2) ^ (key & 7)) * 16u;
-          const uint32_t hi = static_cast<uint32_t>(((c & 3) * 2 + 1) ^ (key & 7)) * 16u;
-          const uint32_t a0 = e4m3x2_to_f16x2(x.x & 0xFFFFu), a1 = e4m3x2_to_f16x2(x.x >> 16);
-          const uint32_t a2 = e4m3x2_to_f16x2(x.y & 0xFFFFu), a3 = e4m3x2_to_f16x2(x.y >> 16);
-          const uint32_t b0 = e4m3x2_to_f16x2(x.z & 0xFFFFu), b1 = e4m3x2_to_f16x2(x.z >> 16);
-          const uint32_t b2 = e4m3x2_to_f16x2(x.w & 0xFFFFu), b3 = e4m3x2_to_f16x2(x.w >> 16);
-          if (c < 4) {                                 // (the order spreads a quarter warp over all banks)
-            sts128(row + lo, a0, a1, a2, a3);
-            sts128(row + hi, b0, b1, b2, b3);
-          } else {
-            sts128(row + hi, b0, b1, b2, b3);
-            sts128(row + lo, a0, a1, a2, a3);
-          }
-        }
-        at_fence_async();
+      const uint32_t n = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(sg.t1 - sg.t0) * kPerTile, 0);   // its jobs
+      wait(sh.qfull, seg & 1u, kFaultFullWait);
+      __syncwarp();
+      scores();
+      if (n > 1) scores();
+      for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t grp = jv & 1u;
+        if (i + 2 < n) scores();                       // (job i + 2's, as soon as job i's scores have been read)
+        wait(sh.vfull[vs], vp, kFaultFullWait);
+        wait(sh.pfull[grp], (jv >> 1) & 1u, kFaultFullWait);
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_addr(&sh.vempty[g % VST]));
-          mbar_arrive(smem_addr(&sh.wfull[g & 1u]));
+        const bool last = kPerTile == 1 || grp == 1;
+        if (!*abort_flag) {
+          at_fence_after();
+          const uint32_t vst = v_s + vs * kTileBytes;
+          const uint32_t v = at_desc_lo(vst, zero_s - vst), pp = pd + grp * (S::kPBytes >> 4);
+          const uint32_t d = tm + S::kAcc + grp * 3 * N;
+#pragma unroll
+          for (int kk = 0; kk < kTile / 32; ++kk)
+            at_mma_f8(lead, d, v + kk * (32 * D >> 4), kHiK, pp + kk * (32 * N >> 4), kHiP, at_idesc(3 * N, true),
+                      kk != 0 || i >= 2 ? 1u : 0u);
+          if (last) at_commit(lead, smem_addr(&sh.vempty[vs]));
+          at_commit(lead, smem_addr(&sh.pvdone[grp]));
+        }
+        __syncwarp();
+        ++jv;
+        if (last && ++vs == ST) {
+          vs = 0;
+          vp ^= 1u;
         }
       }
+      ++seg;
+    }
     }
   } else {
-    // Softmax: thread (warp % 4, lane) holds token 32 (warp % 4) + lane of the
-    // tile; group wg = warp / 4 owns columns [wg HALF, (wg + 1) HALF).
-    const int wg = warp >> 2, wq = warp & 3, key = wq * 32 + lane, tid = threadIdx.x & 127;
-    const uint32_t bar_id = 1u + static_cast<uint32_t>(wg);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // Softmax: thread (warp % 4, lane) holds token 32 (warp % 4) + lane of a tile.
+    const int grp = warp >> 2, wq = warp & 3, key = wq * 32 + lane, tid = threadIdx.x & 127;
+    const uint32_t bar_id = 1u + static_cast<uint32_t>(grp);
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const int page_of = key / ps;
-    const int c0 = wg * HALF;
+    const int c0 = PAIR ? grp * N : 0;                 // the group's first column
+    const float* fq = sh.f + c0;
+    float* nm = sh.nm[grp];
+    const uint32_t p_row = p_s + static_cast<uint32_t>(grp) * S::kPBytes + static_cast<uint32_t>(key) * N;
+    const int swz = N == 64 ? (key >> 1) & 3 : (key >> 2) & 1;
+    const uint32_t s_t = tmem + lanes + S::kScore + static_cast<uint32_t>(grp) * S::kScoreCols;
+    const uint32_t o_t = tmem + lanes + S::kAcc + static_cast<uint32_t>(grp) * 3 * N;
+    constexpr int kPer = D / 8;                        // threads that load one row of the queries
+    constexpr int kStep = kSoftWarps * 32 / kPer;      // rows loaded at a time
+    constexpr int kLoads = S::kRows / kStep;
+    static_assert(S::kRows % kStep == 0, "");
     while (next_segment(p, cur, sh.w0, sg)) {
       // The queries: one power-of-two scale per row and two e4m3 parts.
       const int row0 = sg.rt * p.tile_rows;
       const int nrows = min(p.tile_rows, p.rows - row0);
-      constexpr int kPer = D / 8;                      // threads per row, 8 elements each
+      // columns of this group that hold rows, in 16s
+      const int mine = PAIR ? min(p.half, nrows - grp * p.half) : nrows;
+      const int ncols = (mine + 15) & ~15;
+      const int r0 = threadIdx.x / kPer, e = threadIdx.x % kPer;
+      uint4 xq[kLoads];
+      int32_t at_row[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = r0 + i * kStep;                  // column; its row:
+        const int in = PAIR && r >= N ? r - N : r, rr = PAIR && r >= N ? p.half + in : in;
+        xq[i] = make_uint4(0u, 0u, 0u, 0u);
+        at_row[i] = -1;
+        if (rr < nrows && (!PAIR || in < p.half)) {
+          const int l = (row0 + rr) / p.G, hq = sg.h * p.G + (row0 + rr) % p.G;
+          xq[i] = *reinterpret_cast<const uint4*>(p.q + sg.b * p.qb + l * p.ql + hq * p.qh + e * 16);
+          at_row[i] = static_cast<int32_t>((sg.b * p.L + l) * p.Hq + hq);
+        }
+      }
       named_sync(3, kSoftWarps * 32);                  // the previous segment's rows and references are no longer read
-      for (int r = threadIdx.x / kPer; r < N; r += kSoftWarps * 32 / kPer) {
-        const int e = threadIdx.x % kPer;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        const int rr = row0 + r;
-        if (r < nrows)
-          x = *reinterpret_cast<const uint4*>(p.q + sg.b * p.qb + (rr / p.G) * p.ql +
-                                              (static_cast<int64_t>(sg.h) * p.G + rr % p.G) * p.qh + e * 16);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = r0 + i * kStep;
+        const uint32_t w[4] = {xq[i].x, xq[i].y, xq[i].z, xq[i].w};
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t u0 = w[i] & 0x7FFFu, u1 = (w[i] >> 16) & 0x7FFFu;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t u0 = w[j] & 0x7FFFu, u1 = (w[j] >> 16) & 0x7FFFu;
           top = max(top, u0 < 0x7F80u ? u0 : 0u);
           top = max(top, u1 < 0x7F80u ? u1 : 0u);
         }
@@ -708,169 +782,207 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const float inv = __uint_as_float(0x7F000000u - __float_as_uint(s));
         uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float a = bf16lo(w[i]) * inv, b = bf16hi(w[i]) * inv;
+        for (int j = 0; j < 4; ++j) {
+          float a = bf16lo(w[j]) * inv, b = bf16hi(w[j]) * inv;
           if (!(fabsf(a) <= 448.0f)) a = __int_as_float(0x7FFFFFFF);   // infinities and NaN: the row's results are NaN
           if (!(fabsf(b) <= 448.0f)) b = __int_as_float(0x7FFFFFFF);
           const uint32_t h = e4m3x2(a, b);
           float ha, hb;
           f16x2_to_f32(e4m3x2_to_f16x2(h), ha, hb);
           const uint32_t l = e4m3x2(a - ha, b - hb);
-          hi[i >> 1] |= h << (16 * (i & 1));
-          lo[i >> 1] |= l << (16 * (i & 1));
+          hi[j >> 1] |= h << (16 * (j & 1));
+          lo[j >> 1] |= l << (16 * (j & 1));
         }
-        const int chunk = e >> 1;
-        const uint32_t at = static_cast<uint32_t>(r * D + ((D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) << 4) +
-                                                  (e & 1) * 8);
-        sts64(q_s + at, hi[0], hi[1]);
-        sts64(q_s + N * D + at, lo[0], lo[1]);
+        const int chunk = e >> 1, in = PAIR ? r % N : r;
+        const uint32_t at = q_s + static_cast<uint32_t>((PAIR ? r / N : 0) * 2 * N * D + in * D +
+                                                        ((D == 128 ? chunk ^ (in & 7) : chunk ^ ((in >> 1) & 3)) << 4) +
+                                                        (e & 1) * 8);
+        sts64(at, hi[0], hi[1]);
+        sts64(at + N * D, lo[0], lo[1]);
         if (e == 0) {
           sh.f[r] = s;
-          sh.nm[r] = -kUnset;
-          sh.row[r] = r < nrows ? static_cast<int32_t>((sg.b * p.L + rr / p.G) * p.Hq + static_cast<int64_t>(sg.h) * p.G +
-                                                       rr % p.G)
-                                : -1;
+          sh.row[r] = at_row[i];
         }
       }
+      if (tid < N) nm[tid] = -kUnset;
       at_fence_async();
       named_sync(3, kSoftWarps * 32);
       if (lane == 0) mbar_arrive(smem_addr(&sh.qfull));
 
-      uint64_t l2[HALF / 2];                           // this token's share of the sums
+      uint64_t l2[N / 2];                              // this token's share of the sums
 #pragma unroll
-      for (int i = 0; i < HALF / 2; ++i) l2[i] = 0;
-      float vref = 0x1p-120f;
+      for (int i = 0; i < N / 2; ++i) l2[i] = 0;
+      float vref = 0x1p-120f, vscale = kPUnit / 256 / vref;
+      bool begun = false;                              // the accumulator holds earlier tiles
       for (int ti = sg.t0; ti < sg.t1; ++ti, ++g) {
+        if (!PAIR && (g & 1u) != static_cast<uint32_t>(grp)) continue;
+        const uint32_t nth = PAIR ? g : g >> 1;        // this group's job number
         wait(sh.mfull[g % kMetaSlots], (g / kMetaSlots) & 1u, kFaultFullWait);
         const TileMeta& m = sh.meta[g % kMetaSlots];
-        const bool valid = (m.valid[wq] >> lane) & 1u;
+        const bool valid = tile_visible(m, key, page_of, p.mask != nullptr);
         const float ck = m.ks[page_of], vs = m.vs[page_of];
         const uint64_t ck2 = pack2(ck, ck);
-        wait(sh.sfull[g & 1u], (g >> 1) & 1u, kFaultFullWait);
+        if (!valid) {
+          // Codes of tokens that are not visible (any bytes, NaN among them)
+          // would meet probabilities of 0: they become zeros.
+          wait(sh.vfull[g % ST], (g / ST) & 1u, kFaultFullWait);
+          const uint32_t vrow = v_s + (g % ST) * kTileBytes + static_cast<uint32_t>(key) * D;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) sts128(vrow + i * 16, 0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+        wait(sh.sfull[grp], nth & 1u, kFaultFullWait);
+        __syncwarp();
         at_fence_after();
-        const uint32_t s_t = tmem + lanes + (g & 1u) * N + c0;
-        // Does any score exceed its reference by more than the slack?
+        // Exponents x = score - reference, and the largest of them.
+        uint64_t x[N / 2];
+        auto exponents = [&]() {
+#pragma unroll
+          for (int c = 0; c < N; c += 16) {
+            if (c >= ncols) break;                     // (uniform)
+            uint32_t r[16];
+            at_ld<16>(s_t + c, r);
+            if constexpr (S::kConcat) {
+              uint32_t q[16];
+              at_ld<16>(s_t + N + c, q);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fq + c + i);
+              const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(nm + c + i);
+              x[(c + i) / 2] = fma2(at_mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ck2), f.x, n.x);
+              x[(c + i) / 2 + 1] =
+                  fma2(at_mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), ck2), f.y, n.y);
+            }
+          }
+        };
+        exponents();
         float over = -kInf;
 #pragma unroll
-        for (int c = 0; c < HALF; c += C) {
-          uint32_t r[C];
-          at_ld<C>(s_t + c, r);
-#pragma unroll
-          for (int i = 0; i < C; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&sh.f[c0 + c + i]);
-            const float4 n = *reinterpret_cast<const float4*>(&sh.nm[c0 + c + i]);
-            float x0, x1, x2, x3;
-            unpack2(fma2(at_mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ck2), pack2(f.x, f.y),
-                         pack2(n.x, n.y)), x0, x1);
-            unpack2(fma2(at_mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), ck2), pack2(f.z, f.w),
-                         pack2(n.z, n.w)), x2, x3);
-            over = fmaxf(fmaxf(over, fmaxf(x0, x1)), fmaxf(x2, x3));
-          }
+        for (int i = 0; i < N / 2; ++i) {
+          if (i % 8 == 0 && 2 * i >= ncols) break;
+          float a, b;
+          unpack2(x[i], a, b);
+          over = fmaxf(fmaxf(over, a), b);
         }
-        const bool raise = valid && (over > kSlack || vs > 16.0f * vref);
+        const bool raise = valid && (over > kSlack || vs > vref);
         if (group_any(bar_id, raise)) {                // uniform over the group
-          // New references: the largest score of each column so far.
+          // New references: the largest score of each column so far, and a bit
+          // more (a score then has to exceed it eightfold to move it again).
+#pragma unroll 1
+          for (int c = 0; c < ncols; c += 16) {
+            uint32_t r[16];
+            at_ld<16>(s_t + c, r);
+            if constexpr (S::kConcat) {
+              uint32_t q[16];
+              at_ld<16>(s_t + N + c, q);
 #pragma unroll
-          for (int c = 0; c < HALF; c += C) {
-            uint32_t r[C];
-            at_ld<C>(s_t + c, r);
-            float mine = -kInf;
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-              const float x = valid ? __uint_as_float(r[i]) * ck * sh.f[c0 + c + i] : -kInf;
-              const float mx = warp_max_f32(x == x ? x : -kInf);
-              if (lane == i) mine = mx;
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
             }
-            if (lane < C) sh.red[wg][wq][c + lane] = mine;
+            float top = -kInf;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float y = valid ? __uint_as_float(r[i]) * ck * fq[c + i] : -kInf;
+              const float mx = warp_max_f32(y == y ? y : -kInf);
+              if (lane == i) top = mx;
+            }
+            if (lane < 16) sh.red[grp][wq][c + lane] = top;
           }
           float vmax = warp_max_f32(valid ? vs : 0.0f);
-          if (lane == 0) sh.fac_o[c0 + wq] = vmax;
+          if (lane == 0) sh.fac_o[grp][wq] = vmax;
           named_sync(bar_id, 128);
-          vmax = fmaxf(fmaxf(sh.fac_o[c0], sh.fac_o[c0 + 1]), fmaxf(sh.fac_o[c0 + 2], sh.fac_o[c0 + 3]));
+          vmax = fmaxf(fmaxf(sh.fac_o[grp][0], sh.fac_o[grp][1]), fmaxf(sh.fac_o[grp][2], sh.fac_o[grp][3]));
           const float vnew = fmaxf(vref, vmax);
           named_sync(bar_id, 128);
-          if (tid < HALF) {
-            const float old = -sh.nm[c0 + tid];
-            const float mx = fmaxf(fmaxf(sh.red[wg][0][tid], sh.red[wg][1][tid]),
-                                   fmaxf(sh.red[wg][2][tid], sh.red[wg][3][tid]));
-            const float now = fmaxf(old, mx);
+          if (tid < ncols) {
+            const float old = -nm[tid];
+            const float mx = fmaxf(fmaxf(sh.red[grp][0][tid], sh.red[grp][1][tid]),
+                                   fmaxf(sh.red[grp][2][tid], sh.red[grp][3][tid]));
+            const float now = mx > old ? mx + kHead : old;
             const float d = ex2_approx(old - now);
-            sh.nm[c0 + tid] = -now;
-            sh.fac_l[c0 + tid] = d;
-            sh.fac_o[c0 + tid] = d * (vref / vnew);
+            nm[tid] = -now;
+            sh.fac_l[grp][tid] = d;
+            sh.fac_o[grp][tid] = d * (vref / vnew);
           }
           vref = vnew;
+          vscale = kPUnit / 256 / vref;
           named_sync(bar_id, 128);
 #pragma unroll
-          for (int i = 0; i < HALF / 2; ++i)
-            l2[i] = at_mul2(l2[i], *reinterpret_cast<const uint64_t*>(&sh.fac_l[c0 + 2 * i]));
-          if (ti > sg.t0) {                            // the accumulator holds earlier tiles
-            wait(sh.pvdone[(g - 1) & 1u], ((g - 1) >> 1) & 1u, kFaultFullWait);
+          for (int i = 0; i < N / 2; ++i) {
+            if (i % 8 == 0 && 2 * i >= ncols) break;
+            l2[i] = at_mul2(l2[i], *reinterpret_cast<const uint64_t*>(&sh.fac_l[grp][2 * i]));
+          }
+          if (begun) {
+            wait(sh.pvdone[grp], (nth - 1) & 1u, kFaultFullWait);
+            __syncwarp();
             at_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < ncols; c += 16) {
 #pragma unroll
-            for (int c = 0; c < HALF; c += 8) {
-              uint32_t r[8];
-              const uint32_t o_t = tmem + lanes + 2 * N + c0 + c;
-              at_ld<8>(o_t, r);
+              for (int part = 0; part < 3; ++part) {
+                uint32_t r[16];
+                at_ld<16>(o_t + part * N + c, r);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * sh.fac_o[c0 + c + i]);
-              at_st8(o_t, r);
+                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * sh.fac_o[grp][c + i]);
+                at_st16(o_t + part * N + c, r);
+              }
             }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             at_fence_before();
           }
           named_sync(bar_id, 128);                     // (fac_o and red are free again)
+          exponents();
         }
-        // P of this token, in fp16 for the product and summed in fp32.
-        const float vr = valid ? vs * (kPUnit / vref) : 0.0f;
+        at_fence_before();                             // the scores have been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.sempty[grp]));
+        // P of this token: summed in fp32, in three e4m3 parts for the product.
+        if (!valid) {
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) x[i] = pack2(-kInf, -kInf);
+        }
+        const float vr = valid ? vs * vscale : 0.0f;   // 2^-8 64 s_v / v_ref
         const uint64_t vr2 = pack2(vr, vr);
-        // the product that read this buffer last
-        if (g >= PB) wait(sh.pvdone[(g - PB) & 1u], ((g - PB) >> 1) & 1u, kFaultEmptyWait);
-        const uint32_t p_row = p_s + (g % PB) * p_bytes<N>() + static_cast<uint32_t>(key) * kPRow;
-        const int swz = kPRow == 128 ? key & 7 : (kPRow == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
+        if (nth >= 1) wait(sh.pvdone[grp], (nth - 1) & 1u, kFaultEmptyWait);   // the product that read this buffer last
+        __syncwarp();
 #pragma unroll
-        for (int c = 0; c < HALF; c += C) {
-          uint32_t r[C];
-          at_ld<C>(s_t + c, r);
-          if (c + C == HALF) {                         // the scores have been read
-            at_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.sempty[g & 1u]));
-          }
+        for (int i = 0; i < N; i += 16) {
+          if (i >= ncols) break;
+          uint32_t o[3][4];
 #pragma unroll
-          for (int i = 0; i < C; i += 8) {
-            uint32_t o[4];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t h[2];
 #pragma unroll
-            for (int q = 0; q < 8; q += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&sh.f[c0 + c + i + q]);
-              const float4 n = *reinterpret_cast<const float4*>(&sh.nm[c0 + c + i + q]);
-              float x0, x1, x2, x3;
-              unpack2(fma2(at_mul2(pack2(__uint_as_float(r[i + q]), __uint_as_float(r[i + q + 1])), ck2),
-                           pack2(f.x, f.y), pack2(n.x, n.y)), x0, x1);
-              unpack2(fma2(at_mul2(pack2(__uint_as_float(r[i + q + 2]), __uint_as_float(r[i + q + 3])), ck2),
-                           pack2(f.z, f.w), pack2(n.z, n.w)), x2, x3);
-              uint64_t e0 = pack2(ex2_approx(x0), ex2_approx(x1)), e1 = pack2(ex2_approx(x2), ex2_approx(x3));
-              if (!valid) e0 = e1 = 0;
-              l2[(c + i + q) / 2] = add2(l2[(c + i + q) / 2], e0);
-              l2[(c + i + q) / 2 + 1] = add2(l2[(c + i + q) / 2 + 1], e1);
-              float y0, y1, y2, y3;
-              unpack2(at_mul2(e0, vr2), y0, y1);
-              unpack2(at_mul2(e1, vr2), y2, y3);
-              o[q / 2] = f16x2(y0, y1);
-              o[q / 2 + 1] = f16x2(y2, y3);
+            for (int u = 0; u < 2; ++u) {
+              float a, b;
+              unpack2(x[i / 2 + 2 * q + u], a, b);
+              const uint64_t y = pack2(ex2_approx(a), ex2_approx(b));
+              l2[i / 2 + 2 * q + u] = add2(l2[i / 2 + 2 * q + u], y);
+              unpack2(at_mul2(y, vr2), a, b);
+              h[u] = f16x2(a, b);
             }
-            const int col = c0 + c + i;
-            sts128(p_row + static_cast<uint32_t>(col >> 6) * 16384u +
-                       static_cast<uint32_t>(((col & 63) >> 3) ^ swz) * 16u, o[0], o[1], o[2], o[3]);
+            o[0][q] = part_codes(h[0], h[1]);
+            h[0] = part_rest16(h[0]);
+            h[1] = part_rest16(h[1]);
+            o[1][q] = part_codes(h[0], h[1]);
+            o[2][q] = part_codes(part_rest16(h[0]), part_rest16(h[1]));
           }
+          const uint32_t at = p_row + static_cast<uint32_t>((i >> 4) ^ swz) * 16u;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) sts128(at + k * (kTile * N), o[k][0], o[k][1], o[k][2], o[k][3]);
         }
+        begun = true;
         at_fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.pfull[g & 1u]));
+        if (lane == 0) mbar_arrive(smem_addr(&sh.pfull[grp]));
       }
 
       // The segment's sums over its tokens, then its rows.
 #pragma unroll
-      for (int i = 0; i < HALF / 2; ++i) {
+      for (int i = 0; i < N / 2; ++i) {
+        if (2 * i >= ncols) break;
         float a, b;
         unpack2(l2[i], a, b);
 #pragma unroll
@@ -879,41 +991,95 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
         }
         if (lane == 0) {
-          sh.red[wg][wq][2 * i] = a;
-          sh.red[wg][wq][2 * i + 1] = b;
+          sh.red[grp][wq][2 * i] = a;
+          sh.red[grp][wq][2 * i + 1] = b;
         }
       }
-      named_sync(bar_id, 128);
-      wait(sh.pvdone[(g - 1) & 1u], ((g - 1) >> 1) & 1u, kFaultFullWait);
-      at_fence_after();
+      if (tid == 0) sh.vref[grp] = vref;
+      named_sync(3, kSoftWarps * 32);
       const bool whole = sg.t0 == 0 && sg.t1 == sg.T;
-      const int slot = 2 * blockIdx.x + (sg.starts_range ? 0 : 1);
-      const int d = key;                               // the accumulator's lane is a dimension
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (sg.starts_range ? 0 : 1);
+      // Taking turns: the group of the segment's first tile has a part of every
+      // row, the other one too when there are two tiles (else its accumulator
+      // holds nothing).
+      const bool both = !PAIR && sg.t1 - sg.t0 >= 2;
+      const int first = PAIR ? 0 : static_cast<int>((g - static_cast<uint32_t>(sg.t1 - sg.t0)) & 1u);
+      for (int n = threadIdx.x; n < S::kRows; n += kSoftWarps * 32) {
+        const int32_t row = sh.row[n];
+        if (row < 0) continue;
+        const int a = PAIR ? n / N : first, c = PAIR ? n % N : n;
+        float m = -sh.nm[a][c];
+        float l = (sh.red[a][0][c] + sh.red[a][1][c]) + (sh.red[a][2][c] + sh.red[a][3][c]);
+        float fa = sh.vref[a] * (1.0f / kPUnit), fb = 0.0f;
+        if (both) {
+          const int o = first ^ 1;
+          const float mo = -sh.nm[o][c], top = fmaxf(m, mo);
+          const float ea = ex2_approx(m - top), eb = ex2_approx(mo - top);
+          const float lo = (sh.red[o][0][c] + sh.red[o][1][c]) + (sh.red[o][2][c] + sh.red[o][3][c]);
+          l = l * ea + lo * eb;
+          fa *= ea;
+          fb = sh.vref[o] * (1.0f / kPUnit) * eb;
+          m = top;
+        }
+        if (whole) {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // (a NaN sum gives NaN)
+          fa *= inv;
+          fb *= inv;
+          p.lse[row] = l == 0.0f ? -kInf : m * kLn2 + logf(l);
+        } else {
+          p.part_ml[(slot * S::kRows + n) * 2] = m;
+          p.part_ml[(slot * S::kRows + n) * 2 + 1] = l;
+        }
+        sh.fin[a][c] = fa;
+        if (both) sh.fin[first ^ 1][c] = fb;
+      }
+      // The last product of either group.
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t back = PAIR ? 1u : 1u + static_cast<uint32_t>(k);
+        if (!PAIR && k == 1 && !both) break;
+        const uint32_t j = PAIR ? 2 * (g - 1) + static_cast<uint32_t>(k) : g - back;
+        wait(sh.pvdone[j & 1u], (j >> 1) & 1u, kFaultFullWait);
+      }
+      __syncwarp();
+      at_fence_after();
+      named_sync(3, kSoftWarps * 32);
+      const int d = key;                               // an accumulator's lane is a dimension
+      // Taking turns, each group writes half of the columns from both accumulators.
+      const int per = PAIR ? N : N / 2;
+      const int ca = PAIR ? 0 : grp * per;
 #pragma unroll 1
-      for (int c = 0; c < HALF; c += 8) {
-        uint32_t r[8];
-        at_ld<8>(tmem + lanes + 2 * N + c0 + c, r);
+      for (int c = ca; c < ca + per && c < ncols; c += 8) {
+        float o[8];
+        const int a0 = PAIR ? grp : first;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (k == 1 && !both) break;
+          const int a = k == 0 ? a0 : a0 ^ 1;
+          uint32_t r1[8], r2[8], r3[8];
+          const uint32_t t = tmem + lanes + S::kAcc + static_cast<uint32_t>(a) * 3 * N + c;
+          at_ld<8>(t, r1);
+          at_ld<8>(t + N, r2);
+          at_ld<8>(t + 2 * N, r3);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float y = fmaf(fmaf(__uint_as_float(r3[i]), 1.0f / 16, __uint_as_float(r2[i])), 1.0f / 16,
+                                 __uint_as_float(r1[i]));
+            o[i] = k == 0 ? y * sh.fin[a][c + i] : fmaf(y, sh.fin[a][c + i], o[i]);
+          }
+        }
+        if (d >= D) continue;                          // (whole warps)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int n = c0 + c + i;
           const int32_t row = sh.row[n];
           if (row < 0) continue;
-          const float l = (sh.red[wg][0][c + i] + sh.red[wg][1][c + i]) + (sh.red[wg][2][c + i] + sh.red[wg][3][c + i]);
-          const float o = __uint_as_float(r[i]) * (vref * (1.0f / kPUnit));
           if (whole) {
-            if (d < D) {
-              uint16_t u;
-              const float y = l == 0.0f ? 0.0f : o / l;
-              asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(y));
-              p.out[static_cast<int64_t>(row) * D + d] = u;
-            }
-            if (d == 0) p.lse[row] = l == 0.0f ? -kInf : -sh.nm[n] * kLn2 + logf(l);
+            uint16_t u;
+            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(o[i]));
+            p.out[static_cast<int64_t>(row) * D + d] = u;
           } else {
-            if (d < D) p.part_o[(static_cast<int64_t>(slot) * N + n) * D + d] = o;
-            if (d == 0) {
-              p.part_ml[(static_cast<int64_t>(slot) * N + n) * 2] = -sh.nm[n];
-              p.part_ml[(static_cast<int64_t>(slot) * N + n) * 2 + 1] = l;
-            }
+            p.part_o[(slot * S::kRows + n) * D + d] = o[i];
           }
         }
       }
@@ -924,50 +1090,61 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   __syncthreads();
   if (warp == kMmaWarp) {
     at_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 
 // One warp per output row: joins the parts of the items that several CTAs
 // share, in CTA order (a part's reference may differ from the others').
 template <int D>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int N) {
-  pdl_wait();
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int N, int columns) {
   pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= p.B * p.L * p.Hq) return;
-  const int64_t hq = row % p.Hq, l = row / p.Hq % p.L, b = row / (p.Hq * p.L);
-  const int64_t h = hq / p.G, rr = l * p.G + hq % p.G;
-  const int64_t rt = rr / p.tile_rows;
-  const int n = static_cast<int>(rr % p.tile_rows);
-  const int64_t hr = static_cast<int64_t>(p.c.heads) * p.row_tiles;
-  const int64_t total = tiles_before(p, p.B) * hr;
-  const int64_t T = tiles_of(p, b);
-  const int64_t i0 = tiles_before(p, b) * hr + (h * p.row_tiles + rt) * T, i1 = i0 + T;   // the item's tiles
-  // the CTA that holds tile w: the largest c with total c / ctas <= w
-  auto owner = [&](int64_t w) {
-    int64_t c = w * p.ctas / total;
-    while (c + 1 < p.ctas && cta_begin(total, c + 1, p.ctas) <= w) ++c;
-    while (cta_begin(total, c, p.ctas) > w) --c;
-    return c;
-  };
-  const int64_t ca = owner(i0), cb = owner(i1 - 1);
+  const int32_t row = static_cast<int32_t>(blockIdx.x * 4 + (threadIdx.x >> 5));
+  if (row >= static_cast<int32_t>(p.B) * p.rows * p.c.heads) return;
+  const int32_t Hq = static_cast<int32_t>(p.Hq), L = static_cast<int32_t>(p.L);
+  const int32_t hq = row % Hq, bl = row / Hq, l = bl % L, b = bl / L;
+  const int32_t h = hq / p.G, rr = l * p.G + hq % p.G;
+  const int32_t rt = rr / p.tile_rows, in = rr % p.tile_rows;
+  const int n = in / p.half * columns + in % p.half;   // the row's column (columns: of a softmax group)
+  const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
+  const uint2 tiles = tiles_before(p, b);
+  const Split split(tiles.y * hr, static_cast<uint32_t>(p.ctas));
+  const uint32_t T = static_cast<uint32_t>(tiles_of(p, b));
+  const uint32_t i0 = tiles.x * hr + static_cast<uint32_t>(h * p.row_tiles + rt) * T;   // the item's tiles: [i0, i0 + T)
+  const uint32_t ca = split.owner(i0), cb = split.owner(i0 + T - 1);
   if (ca == cb) return;                                // written whole
+  // CTA ca's part is its last segment unless the item begins its range; the
+  // others' is their first.  The statistics of 32 parts are read at a time.
+  const bool late = split.begin(ca) < i0;
+  auto slot_of = [&](uint32_t c) { return static_cast<int64_t>(2 * c + (c == ca && late ? 1 : 0)); };
   float m = kUnset, sum = 0.0f;
   float o[D / 32] = {};
-  for (int64_t c = ca; c <= cb; ++c) {
-    const int64_t begin = cta_begin(total, c, p.ctas);
-    if (begin == cta_begin(total, c + 1, p.ctas)) continue;
-    const int64_t slot = 2 * c + (begin >= i0 ? 0 : 1);
-    const float* ml = p.part_ml + (slot * N + n) * 2;
-    const float mc = __ldcg(ml), lc = __ldcg(ml + 1);
-    const float now = fmaxf(m, mc);
+  for (uint32_t c0 = ca; c0 <= cb; c0 += 32) {
+    const uint32_t c = c0 + lane;
+    float mc = -kInf, lc = 0.0f;
+    if (c <= cb) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(c) * N + n);
+      mc = ml.x;
+      lc = ml.y;
+    }
+    const float now = fmaxf(m, warp_max_f32(mc));
     const float fa = ex2_approx(m - now), fb = ex2_approx(mc - now);
-    sum = sum * fa + lc * fb;
+    float add = lc * fb;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      o[i] = o[i] * fa + __ldcg(p.part_o + (slot * N + n) * D + i * 32 + lane) * fb;
+    for (int k = 16; k > 0; k >>= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, k);
+    sum = sum * fa + add;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] *= fa;
+    const int parts = static_cast<int>(cb - c0 + 1 < 32 ? cb - c0 + 1 : 32);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float f = __shfl_sync(0xFFFFFFFFu, fb, k);
+      const float* src = p.part_o + (slot_of(c0 + k) * N + n) * D + lane;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(__ldcg(src + i * 32), f, o[i]);
+    }
     m = now;
   }
 #pragma unroll
@@ -975,7 +1152,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     uint16_t u;
     const float y = sum == 0.0f ? 0.0f : o[i] / sum;
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(y));
-    p.out[row * D + i * 32 + lane] = u;
+    p.out[static_cast<int64_t>(row) * D + i * 32 + lane] = u;
   }
   if (lane == 0) p.lse[row] = sum == 0.0f ? -kInf : m * kLn2 + logf(sum);
 }
@@ -1020,19 +1197,17 @@ struct AttendVariant {
   int smem;
 };
 
-template <int N>
+template <int N, bool PAIR>
 AttendVariant attend_variant_n(int dim) {
-  if (dim == 64) return {reinterpret_cast<const void*>(&attend_kernel<64, N>), attend_smem<64, N>()};
-  return {reinterpret_cast<const void*>(&attend_kernel<128, N>), attend_smem<128, N>()};
+  if (dim == 64) return {reinterpret_cast<const void*>(&attend_kernel<64, N, PAIR>), attend_smem<64, N, PAIR>()};
+  return {reinterpret_cast<const void*>(&attend_kernel<128, N, PAIR>), attend_smem<128, N, PAIR>()};
 }
 
-AttendVariant attend_variant(int dim, int n) {
-  switch (n) {
-    case 16: return attend_variant_n<16>(dim);
-    case 32: return attend_variant_n<32>(dim);
-    case 64: return attend_variant_n<64>(dim);
-    default: return attend_variant_n<128>(dim);
-  }
+// By the columns of both groups: 32 and 64 taking turns, 128 paired.
+AttendVariant attend_variant(int dim, int columns) {
+  if (columns == 32) return attend_variant_n<32, false>(dim);
+  if (columns == 64) return attend_variant_n<64, false>(dim);
+  return attend_variant_n<64, true>(dim);
 }
 
 struct AttendDevice {
@@ -1049,7 +1224,7 @@ const AttendDevice* attend_device() {
     AttendDevice& d = g_at[dev];
     d.err = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     for (int dim = 64; dim <= 128; dim += 64)
-      for (int n = 16; n <= 128 && d.err == cudaSuccess; n *= 2) {
+      for (int n = 32; n <= 128 && d.err == cudaSuccess; n *= 2) {
         const AttendVariant v = attend_variant(dim, n);
         d.err = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
       }
@@ -1059,17 +1234,18 @@ const AttendDevice* attend_device() {
 }
 
 // The row tiles of a key head and the columns of a tile: as few tiles as 128
-// columns allow, equally filled, then the narrowest built width that holds
-// one (a width is the tensor core's N and the softmax's work per token).
+// columns allow, equally filled, then the narrowest built width that holds one
+// (a width is the tensor core's N and the softmax's registers per token).
 struct RowTiles {
-  int64_t tiles, rows;
-  int n;
+  int64_t tiles, rows, half;
+  int columns;
 };
 RowTiles row_tiles(int64_t rows) {
   RowTiles t;
   t.tiles = (rows + 127) / 128;
   t.rows = (rows + t.tiles - 1) / t.tiles;
-  t.n = t.rows <= 16 ? 16 : (t.rows <= 32 ? 32 : (t.rows <= 64 ? 64 : 128));
+  t.columns = t.rows <= 32 ? 32 : (t.rows <= 64 ? 64 : 128);
+  t.half = t.columns == 128 ? (t.rows + 1) / 2 : t.rows;
   return t;
 }
 
@@ -1089,7 +1265,7 @@ size_t dllm_cache_attention_workspace_size(int64_t B, int64_t L, int64_t Hq, int
       mul_or_neg(L, Hq) < 0)
     return kAttendHeader;
   const AttendDevice* dev = attend_device();
-  return attend_workspace(dev ? dev->sms : 1024, row_tiles(L * (Hq / heads)).n, static_cast<int>(head_dim));
+  return attend_workspace(dev ? dev->sms : 1024, row_tiles(L * (Hq / heads)).columns, static_cast<int>(head_dim));
 }
 
 dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, const int64_t* q_strides, int64_t B,
@@ -1116,25 +1292,26 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
     if (q_strides[i] % 8 != 0) return DLLM_ERR_UNSUPPORTED;
   }
   if (!aligned16(q) || !aligned16(out)) return DLLM_ERR_UNSUPPORTED;
+  if (key_mask && (!aligned16(key_mask) || mask_stride % 16 != 0)) return DLLM_ERR_UNSUPPORTED;   // (bulk copies)
   // (a TMA coordinate is an int32: the pool's rows of one token and head)
   if (rows > INT32_MAX || cache->num_pages * cache->heads * cache->page_size > INT32_MAX) return DLLM_ERR_UNSUPPORTED;
   if (!workspace) return DLLM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return DLLM_ERR_INVALID_ARGUMENT;
   const RowTiles rt = row_tiles(L * (Hq / cache->heads));
-  if (workspace_bytes < attend_workspace(1, rt.n, cache->head_dim)) return DLLM_ERR_WORKSPACE;
+  if (workspace_bytes < attend_workspace(1, rt.columns, cache->head_dim)) return DLLM_ERR_WORKSPACE;
   const AttendDevice* dev = attend_device();
   if (!dev) return DLLM_ERR_CUDA;
   // One CTA per SM, fewer when there are fewer tiles than that.
   const int64_t most = mul_or_neg(mul_or_neg(B, cache->heads), rt.tiles * ((cap + kTile - 1) / kTile));
-  if (most < 0 || most > (static_cast<int64_t>(1) << 52)) return DLLM_ERR_UNSUPPORTED;
+  if (most < 0 || most > INT32_MAX) return DLLM_ERR_UNSUPPORTED;
   const int64_t ctas = std::min<int64_t>(dev->sms, most);
-  if (workspace_bytes < attend_workspace(ctas, rt.n, cache->head_dim)) return DLLM_ERR_WORKSPACE;
+  if (workspace_bytes < attend_workspace(ctas, rt.columns, cache->head_dim)) return DLLM_ERR_WORKSPACE;
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
   p.c = cache_view(*cache);
   const bool d64 = cache->head_dim == 64;
   if (!pool_map(&p.tm_k, cache->k, p.c, d64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !pool_map(&p.tm_v, cache->v, p.c, CU_TENSOR_MAP_SWIZZLE_NONE))
+      !pool_map(&p.tm_v, cache->v, p.c, d64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
     return DLLM_ERR_CUDA;
   p.q = static_cast<const uint8_t*>(q);
   p.qb = q_strides[0] * 2;
@@ -1158,18 +1335,19 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
   p.rows = static_cast<int32_t>(L * p.G);
   p.row_tiles = static_cast<int32_t>(rt.tiles);
   p.tile_rows = static_cast<int32_t>(rt.rows);
+  p.half = static_cast<int32_t>(rt.half);
   p.ctas = static_cast<int32_t>(ctas);
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.fault = reinterpret_cast<int32_t*>(w);
   p.part_o = reinterpret_cast<float*>(w + kAttendHeader);
-  p.part_ml = p.part_o + 2 * ctas * rt.n * cache->head_dim;
+  p.part_ml = p.part_o + 2 * ctas * rt.columns * cache->head_dim;
   void* args[] = {&p};
-  const AttendVariant v = attend_variant(cache->head_dim, rt.n);
-  st = launch_pdl(v.kernel, dim3(static_cast<unsigned>(ctas)), dim3(kAttendThreads), static_cast<size_t>(v.smem), stream,
-                  args);
+  const AttendVariant v = attend_variant(cache->head_dim, rt.columns);
+  st = launch_pdl(v.kernel, dim3(static_cast<unsigned>(ctas)), dim3(kAttendThreads), static_cast<size_t>(v.smem),
+                  stream, args);
   if (st != DLLM_OK) return st;
-  int n = rt.n;
-  void* jargs[] = {&p, &n};
+  int columns = rt.columns, per_group = rt.columns == 128 ? 64 : rt.columns;
+  void* jargs[] = {&p, &columns, &per_group};
   st = launch_pdl(d64 ? reinterpret_cast<const void*>(&attend_join_kernel<64>)
                       : reinterpret_cast<const void*>(&attend_join_kernel<128>),
                   dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, jargs);

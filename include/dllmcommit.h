@@ -530,7 +530,8 @@ dllm_status dllm_cache_append(const dllm_kv_cache* cache, const void* k, const v
  *              head i / (Hq / heads); Hq a multiple of heads
  *   key_mask   device uint8 (B rows mask_stride bytes apart, mask_stride >=
  *              width * page_size) or NULL: tokens with 0 are not attended,
- *              whatever their keys and values hold
+ *              whatever their keys and values hold; 16-byte aligned, the
+ *              stride a multiple of 16 (else DLLM_ERR_UNSUPPORTED)
  *   scale      multiplies q . k (0 < scale <= 2^20)
  *   out        device bf16 (B, L, Hq, head_dim) contiguous, 16-byte aligned
  *   lse        device fp32 (B, L, Hq): ln sum exp(scale q . k)
