@@ -85,62 +85,6 @@ __device__ __forceinline__ int attend_len(const AttendParams& p, int64_t b) {
   return static_cast<int>(n < 0 ? 0 : (n > p.cap ? p.cap : n));
 }
 
-// q . k of one token's codes (D bytes) with a row in shared memory.
-template <int D>
-__device__ __forceinline__ float dot_codes(const uint8_t* codes, const float* q) {
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(codes) + i);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float f0, f1, f2, f3;
-      f16x2_to_f32(e4m3x2_to_f16x2(w[e] & 0xFFFFu), f0, f1);
-      f16x2_to_f32(e4m3x2_to_f16x2(w[e] >> 16), f2, f3);
-      const float* r = q + 16 * i + 4 * e;
-      s = fmaf(f0, r[0], s);
-      s = fmaf(f1, r[1], s);
-      s = fmaf(f2, r[2], s);
-      s = fmaf(f3, r[3], s);
-    }
-  }
-  return s;
-}
-
-// One thread per cached token and key head: the sum over the rows of the head
-// group of exp(s - lse).
-template <int D>
-__global__ void __launch_bounds__(128) attend_weights_kernel(const __grid_constant__ AttendParams p) {
-  __shared__ float q_s[D];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t b = blockIdx.z, h = blockIdx.y;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-  const int n = attend_len(p, b), ps = p.c.page_size;
-  int64_t page;
-  const bool ok = visible(p, b, j, n, page);
-  const int64_t G = p.Hq / p.c.heads;
-  const int64_t at = page * p.c.heads + h;
-  const float ks = ok ? p.c.k_scale[at] : 0.0f;
-  float sum = 0.0f;
-  for (int64_t r = 0; r < p.L * G; ++r) {
-    const int64_t l = r / G, hq = h * G + r % G;
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q + b * p.qb + l * p.ql + hq * p.qh);
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += 128) q_s[d] = __uint_as_float(static_cast<uint32_t>(q[d]) << 16);
-    __syncthreads();
-    const float lse = p.lse[(b * p.L + l) * p.Hq + hq];
-    if (!ok || !(fabsf(lse) < __builtin_huge_valf())) continue;   // a row that attends to nothing gives no weight
-    const float s = dot_codes<D>(p.c.k + (at * ps + j % ps) * D, q_s) * ks * p.scale2;
-    sum += ex2_approx(s - lse * kLog2e);
-  }
-  if (j < p.cap) {
-    float* w = p.weights + (b * p.c.heads + h) * p.cap + j;
-    *w = p.decay == 0.0f ? sum : fmaf(p.decay, *w, sum);
-  }
-}
-
 // ---------------------------------------------------------------------------
 // tensor core and TMEM wrappers
 // ---------------------------------------------------------------------------
@@ -216,6 +160,20 @@ __device__ __forceinline__ void at_ld(uint32_t t, uint32_t (&r)[C]) {
   }
 }
 
+// 8 columns of each of an accumulator's three parts.
+__device__ __forceinline__ void at_ld3(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t (&r)[24]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23])
+      : "r"(t0), "r"(t1), "r"(t2)
+      : "memory");
+}
+
 // 16 columns back (complete after tcgen05.wait::st).
 __device__ __forceinline__ void at_st16(uint32_t t, const uint32_t (&r)[16]) {
   asm volatile(
@@ -279,6 +237,24 @@ __device__ __forceinline__ uint32_t part_rest16(uint32_t h) {
 }
 // The codes of four values: bits 14 .. 7 of the halves of a, then of b.
 __device__ __forceinline__ uint32_t part_codes(uint32_t a, uint32_t b) { return __byte_perm(a << 1, b << 1, 0x7531); }
+
+// Reduces 32 columns over the warp's lanes: lane i returns column i of all
+// lanes (31 exchanges instead of 160 shuffles).
+template <bool MAX>
+__device__ __forceinline__ float column_reduce(float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, send, o);
+      v[i] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  return v[0];
+}
 
 // Whether any of the 128 threads of named barrier `id` has p set.
 __device__ __forceinline__ bool group_any(uint32_t id, bool p) {
@@ -388,14 +364,14 @@ struct AttendShape {
 };
 constexpr int kSoftWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
 // 384 threads are launched with 168 registers each; the softmax warps (N
-// exponents and N sums a thread) take what the last group leaves: 256 x 216 +
-// 128 x 72 = 384 x 168.
+// exponents and N sums a thread) take what the last group leaves: 256 x 208 +
+// 128 x 88 = 384 x 168.
 constexpr int kAttendThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMetaSlots = 8;
 constexpr float kSlack = 2.0f;                         // log2: how far a score may exceed the reference
 constexpr float kHead = 1.0f;                          // log2: how far a new reference lies above its score
-constexpr float kUnset = -1e30f;                       // the reference before the first score
+constexpr float kUnset = -1e30f;                       // stands for the reference of a part without tokens
 constexpr float kPUnit = 64.0f;                        // P is held at 64 p s_v / v_ref: at most 2^(6 + 2) (e4m3 ends at 448)
 template <int D, int N, bool PAIR>
 constexpr int attend_smem() {
@@ -429,6 +405,8 @@ struct AttendShared {
   alignas(16) float nm[2][N];                          // per group: minus the references,
   alignas(16) float fac_o[2][N];                       // the factors of a rise,
   alignas(16) float fac_l[2][N];
+  alignas(16) float delta[2][N];
+  float vmax[2][4];
   float red[2][4][N];                                  // maxima or sums per warp
   float vref[2];
   float fin[2][N];                                     // what an accumulator's column is multiplied with at the end
@@ -438,6 +416,199 @@ struct AttendShared {
   uint32_t tmem;
   int32_t abort;
 };
+
+// The copy warp of a CTA: the tiles of its range, K (and V) through the rings
+// and what is known of each tile into its meta slot.
+template <int D, int ST, bool WITH_V, class SH, class WAIT>
+__device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const Cursor& cur, uint32_t k_s, uint32_t v_s,
+                                          const WAIT& wait) {
+  constexpr int kTileBytes = kTile * D, MS = static_cast<int>(sizeof(sh.meta) / sizeof(TileMeta));
+  const int lane = threadIdx.x & 31;
+  const int ps = p.c.page_size, ppt = kTile / ps;      // pages per tile
+  const uint32_t w0 = sh.w0;
+  volatile int32_t* abort_flag = &sh.abort;
+  uint32_t g = 0;                                      // tiles passed
+  // A batch is up to 32 pages of one segment, one to a lane: ids are fetched
+  // two batches ahead and scales one batch ahead of the copies that use
+  // them, since each can cost a DRAM latency (tile by tile, that latency was
+  // the time per tile).
+  const int batch_tiles = 32 / ppt;
+  struct Batch {
+    int32_t b, h, len, t0, n, id;   // batch row, head, length, first tile, tiles; this lane's page id, or -1
+  };
+  struct Page {
+    int32_t at;                     // page heads + head, or -1
+    float ks, vs;
+  };
+  Cursor look = cur;
+  Segment ahead;
+  bool more = next_segment(p, look, w0, ahead);
+  int at_tile = more ? ahead.t0 : 0;
+  auto fetch = [&](Batch& t) {                       // the next batch's page ids
+    t.n = 0;
+    t.id = -1;
+    if (!more) return;
+    t.b = ahead.b;
+    t.h = ahead.h;
+    t.len = ahead.len;
+    t.t0 = at_tile;
+    t.n = min(batch_tiles, ahead.t1 - at_tile);
+    const int64_t col = static_cast<int64_t>(at_tile) * ppt + lane;
+    if (lane < t.n * ppt && col * ps < t.len) t.id = p.table[static_cast<int64_t>(ahead.b) * p.width + col];
+    at_tile += t.n;
+    if (at_tile == ahead.t1) {
+      more = next_segment(p, look, w0, ahead);
+      if (more) at_tile = ahead.t0;
+    }
+  };
+  auto scales = [&](const Batch& t) {
+    Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f};
+    if (pg.at >= 0) {
+      pg.ks = p.c.k_scale[pg.at];
+      pg.vs = p.c.v_scale[pg.at];
+    }
+    return pg;
+  };
+  Batch now, next;
+  fetch(now);
+  fetch(next);
+  Page page = scales(now);
+  while (now.n > 0) {
+    Batch later;
+    const Page next_page = scales(next);
+    fetch(later);
+    const unsigned named = __ballot_sync(0xFFFFFFFFu, page.at >= 0);
+    for (int i = 0; i < now.n; ++i, ++g) {
+      const uint32_t st = g % ST, ms = g % MS;
+      wait(sh.kempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
+      if (WITH_V) wait(sh.vempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
+      const int slot = lane - i * ppt;               // of this lane's page in the tile
+      const bool mine = slot >= 0 && slot < ppt;
+      const unsigned pages = (named >> (i * ppt)) & (0xFFFFFFFFu >> (32 - ppt));
+      if (*abort_flag) continue;
+      if (lane == 0) {
+        const uint32_t bytes = static_cast<uint32_t>(__popc(pages) * ps * D);
+        mbar_arrive_expect_tx(smem_addr(&sh.kfull[st]), bytes);
+        if (WITH_V) mbar_arrive_expect_tx(smem_addr(&sh.vfull[st]), bytes);
+      }
+      __syncwarp();
+      if (mine && page.at >= 0) {
+        const int y = page.at * ps;
+        const uint32_t to = static_cast<uint32_t>(slot * ps * D);
+        at_tma_load(k_s + st * kTileBytes + to, &p.tm_k, 0, y, smem_addr(&sh.kfull[st]));
+        if (WITH_V) at_tma_load(v_s + st * kTileBytes + to, &p.tm_v, 0, y, smem_addr(&sh.vfull[st]));
+      }
+      TileMeta& m = sh.meta[ms];
+      const int64_t j0 = static_cast<int64_t>(now.t0 + i) * kTile;
+      if (mine) {
+        m.ks[slot] = page.ks * p.scale2;
+        m.vs[slot] = page.vs;
+      }
+      if (lane == 0) {
+        m.pages = pages;
+        m.left = min(kTile, now.len - static_cast<int32_t>(j0));
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (p.mask) {
+          const uint32_t mb = static_cast<uint32_t>(min(static_cast<int64_t>(kTile), p.cap - j0));
+          mbar_arrive_expect_tx(smem_addr(&sh.mfull[ms]), mb);
+          bulk_copy_g2s(smem_addr(m.mask), p.mask + static_cast<int64_t>(now.b) * p.mask_stride + j0, mb,
+                        smem_addr(&sh.mfull[ms]));
+        } else {
+          mbar_arrive(smem_addr(&sh.mfull[ms]));
+        }
+      }
+      __syncwarp();
+    }
+    now = next;
+    next = later;
+    page = next_page;
+  }
+  // On an abort the copies in flight are waited for (bounded) before the CTA ends.
+  if (*abort_flag && lane == 0) {
+    for (uint32_t i = g > ST ? g - ST : 0; i < g; ++i) {
+      (void)mbar_wait_bounded(smem_addr(&sh.kfull[i % ST]), (i / ST) & 1u);
+      if (WITH_V) (void)mbar_wait_bounded(smem_addr(&sh.vfull[i % ST]), (i / ST) & 1u);
+      (void)mbar_wait_bounded(smem_addr(&sh.mfull[i % MS]), (i / MS) & 1u);
+    }
+  }
+}
+
+// One row's 8 elements (of the row's D, spread over the D / 8 consecutive
+// lanes): the row's power-of-two scale and the elements' two e4m3 parts.
+template <int D>
+__device__ __forceinline__ float split_query(const uint4& x, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u0 = w[j] & 0x7FFFu, u1 = (w[j] >> 16) & 0x7FFFu;
+    top = max(top, u0 < 0x7F80u ? u0 : 0u);
+    top = max(top, u1 < 0x7F80u ? u1 : 0u);
+  }
+#pragma unroll
+  for (int o = D / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const float s = block_scale(__uint_as_float(top << 16));
+  // (the largest bf16 needs 2^120: its inverse is still normal)
+  const float inv = __uint_as_float(0x7F000000u - __float_as_uint(s));
+  hi[0] = hi[1] = lo[0] = lo[1] = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a = bf16lo(w[j]) * inv, b = bf16hi(w[j]) * inv;
+    if (!(fabsf(a) <= 448.0f)) a = __int_as_float(0x7FFFFFFF);   // infinities and NaN: the row's results are NaN
+    if (!(fabsf(b) <= 448.0f)) b = __int_as_float(0x7FFFFFFF);
+    const uint32_t h = e4m3x2(a, b);
+    float ha, hb;
+    f16x2_to_f32(e4m3x2_to_f16x2(h), ha, hb);
+    const uint32_t l = e4m3x2(a - ha, b - hb);
+    hi[j >> 1] |= h << (16 * (j & 1));
+    lo[j >> 1] |= l << (16 * (j & 1));
+  }
+  return s;
+}
+
+// Where elements 8 e .. 8 e + 7 of row r lie in a swizzled K-major tile of D-byte rows.
+template <int D>
+__device__ __forceinline__ uint32_t query_offset(int r, int e) {
+  const int chunk = e >> 1;
+  return static_cast<uint32_t>(r * D + ((D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) << 4) + (e & 1) * 8);
+}
+
+// One warp: the CTA's range of tiles and where it begins, into sh.
+template <class SH>
+__device__ __forceinline__ void plan_range(const AttendParams& p, SH& sh) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
+  const Split split(tiles_before(p, 0).y * hr, gridDim.x);
+  const uint32_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
+  uint32_t before = 0;
+  int32_t b = 0;
+  while (b < p.B) {                                  // 32 batch rows at a time
+    const uint32_t t = b + lane < p.B ? tiles_of(p, b + lane) * hr : 0;
+    uint32_t inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    const unsigned in = __ballot_sync(0xFFFFFFFFu, b + lane < p.B && before + inc > w0);
+    if (in != 0u) {
+      const int l = __ffs(in) - 1;
+      before += __shfl_sync(0xFFFFFFFFu, inc - t, l);
+      b += l;
+      break;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    b += 32;
+  }
+  if (lane == 0) {
+    sh.w0 = w0;
+    sh.w1 = w1;
+    sh.b0 = b;
+    sh.off0 = w0 - before;
+  }
+}
 
 template <int D, int N, bool PAIR>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
@@ -479,37 +650,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   }
   pdl_launch_dependents();
   pdl_wait();
-  if (warp == 0) {   // this CTA's range and the batch row it begins in
-    const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
-    const Split split(tiles_before(p, 0).y * hr, gridDim.x);
-    const uint32_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
-    uint32_t before = 0;
-    int32_t b = 0;
-    while (b < p.B) {                                  // 32 batch rows at a time
-      const uint32_t t = b + lane < p.B ? tiles_of(p, b + lane) * hr : 0;
-      uint32_t inc = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      const unsigned in = __ballot_sync(0xFFFFFFFFu, b + lane < p.B && before + inc > w0);
-      if (in != 0u) {
-        const int l = __ffs(in) - 1;
-        before += __shfl_sync(0xFFFFFFFFu, inc - t, l);
-        b += l;
-        break;
-      }
-      before += __shfl_sync(0xFFFFFFFFu, inc, 31);
-      b += 32;
-    }
-    if (lane == 0) {
-      sh.w0 = w0;
-      sh.w1 = w1;
-      sh.b0 = b;
-      sh.off0 = w0 - before;
-    }
-  }
+  if (warp == 0) plan_range(p, sh);
   if (D == 64)       // the upper 64 rows of V^T: zeros
     for (int i = threadIdx.x; i < kTileBytes / 16; i += kAttendThreads)
       sts128(zero_s + static_cast<uint32_t>(i) * 16u, 0u, 0u, 0u, 0u);
@@ -541,116 +682,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   Segment sg;
   uint32_t g = 0;                                      // tiles this CTA has passed
   const int ps = p.c.page_size;
-  const int ppt = kTile / ps;                          // pages per tile
 
   if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kCopyWarp) {
-    // A batch is up to 32 pages of one segment, one to a lane: ids are fetched
-    // two batches ahead and scales one batch ahead of the copies that use
-    // them, since each can cost a DRAM latency (tile by tile, that latency was
-    // the time per tile).
-    const int batch_tiles = 32 / ppt;
-    struct Batch {
-      int32_t b, h, len, t0, n, id;   // batch row, head, length, first tile, tiles; this lane's page id, or -1
-    };
-    struct Page {
-      int32_t at;                     // page heads + head, or -1
-      float ks, vs;
-    };
-    Cursor look = cur;
-    Segment ahead;
-    bool more = next_segment(p, look, sh.w0, ahead);
-    int at_tile = more ? ahead.t0 : 0;
-    auto fetch = [&](Batch& t) {                       // the next batch's page ids
-      t.n = 0;
-      t.id = -1;
-      if (!more) return;
-      t.b = ahead.b;
-      t.h = ahead.h;
-      t.len = ahead.len;
-      t.t0 = at_tile;
-      t.n = min(batch_tiles, ahead.t1 - at_tile);
-      const int64_t col = static_cast<int64_t>(at_tile) * ppt + lane;
-      if (lane < t.n * ppt && col * ps < t.len) t.id = p.table[static_cast<int64_t>(ahead.b) * p.width + col];
-      at_tile += t.n;
-      if (at_tile == ahead.t1) {
-        more = next_segment(p, look, sh.w0, ahead);
-        if (more) at_tile = ahead.t0;
-      }
-    };
-    auto scales = [&](const Batch& t) {
-      Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f};
-      if (pg.at >= 0) {
-        pg.ks = p.c.k_scale[pg.at];
-        pg.vs = p.c.v_scale[pg.at];
-      }
-      return pg;
-    };
-    Batch now, next;
-    fetch(now);
-    fetch(next);
-    Page page = scales(now);
-    while (now.n > 0) {
-      Batch later;
-      const Page next_page = scales(next);
-      fetch(later);
-      const unsigned named = __ballot_sync(0xFFFFFFFFu, page.at >= 0);
-      for (int i = 0; i < now.n; ++i, ++g) {
-        const uint32_t st = g % ST, ms = g % kMetaSlots;
-        wait(sh.kempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
-        wait(sh.vempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
-        const int slot = lane - i * ppt;               // of this lane's page in the tile
-        const bool mine = slot >= 0 && slot < ppt;
-        const unsigned pages = (named >> (i * ppt)) & (0xFFFFFFFFu >> (32 - ppt));
-        if (*abort_flag) continue;
-        if (lane == 0) {
-          const uint32_t bytes = static_cast<uint32_t>(__popc(pages) * ps * D);
-          mbar_arrive_expect_tx(smem_addr(&sh.kfull[st]), bytes);
-          mbar_arrive_expect_tx(smem_addr(&sh.vfull[st]), bytes);
-        }
-        __syncwarp();
-        if (mine && page.at >= 0) {
-          const int y = page.at * ps;
-          const uint32_t to = static_cast<uint32_t>(slot * ps * D);
-          at_tma_load(k_s + st * kTileBytes + to, &p.tm_k, 0, y, smem_addr(&sh.kfull[st]));
-          at_tma_load(v_s + st * kTileBytes + to, &p.tm_v, 0, y, smem_addr(&sh.vfull[st]));
-        }
-        TileMeta& m = sh.meta[ms];
-        const int64_t j0 = static_cast<int64_t>(now.t0 + i) * kTile;
-        if (mine) {
-          m.ks[slot] = page.ks * p.scale2;
-          m.vs[slot] = page.vs;
-        }
-        if (lane == 0) {
-          m.pages = pages;
-          m.left = min(kTile, now.len - static_cast<int32_t>(j0));
-        }
-        __syncwarp();
-        if (lane == 0) {
-          if (p.mask) {
-            const uint32_t mb = static_cast<uint32_t>(min(static_cast<int64_t>(kTile), p.cap - j0));
-            mbar_arrive_expect_tx(smem_addr(&sh.mfull[ms]), mb);
-            bulk_copy_g2s(smem_addr(m.mask), p.mask + static_cast<int64_t>(now.b) * p.mask_stride + j0, mb,
-                          smem_addr(&sh.mfull[ms]));
-          } else {
-            mbar_arrive(smem_addr(&sh.mfull[ms]));
-          }
-        }
-        __syncwarp();
-      }
-      now = next;
-      next = later;
-      page = next_page;
-    }
-    // On an abort the copies in flight are waited for (bounded) before the CTA ends.
-    if (*abort_flag && lane == 0) {
-      for (uint32_t i = g > ST ? g - ST : 0; i < g; ++i) {
-        (void)mbar_wait_bounded(smem_addr(&sh.kfull[i % ST]), (i / ST) & 1u);
-        (void)mbar_wait_bounded(smem_addr(&sh.vfull[i % ST]), (i / ST) & 1u);
-        (void)mbar_wait_bounded(smem_addr(&sh.mfull[i % kMetaSlots]), (i / kMetaSlots) & 1u);
-      }
-    }
+    copy_role<D, ST, true>(p, sh, cur, k_s, v_s, wait);
     } else if (warp == kMmaWarp) {
     constexpr uint32_t kPerTile = PAIR ? 2 : 1;        // jobs of a tile
     constexpr uint32_t kHiK = at_desc_hi(8 * D, kSwz), kHiP = at_desc_hi(8 * N, N == 64 ? 4u : 6u);
@@ -724,7 +760,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // Softmax: thread (warp % 4, lane) holds token 32 (warp % 4) + lane of a tile.
     const int grp = warp >> 2, wq = warp & 3, key = wq * 32 + lane, tid = threadIdx.x & 127;
     const uint32_t bar_id = 1u + static_cast<uint32_t>(grp);
@@ -740,7 +776,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     constexpr int kPer = D / 8;                        // threads that load one row of the queries
     constexpr int kStep = kSoftWarps * 32 / kPer;      // rows loaded at a time
     constexpr int kLoads = S::kRows / kStep;
-    static_assert(S::kRows % kStep == 0, "");
+    static_assert(S::kRows % kStep == 0 && N % kStep == 0, "");
+    const int step_l = kStep / p.G, step_g = kStep % p.G;
     while (next_segment(p, cur, sh.w0, sg)) {
       // The queries: one power-of-two scale per row and two e4m3 parts.
       const int row0 = sg.rt * p.tile_rows;
@@ -751,52 +788,39 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       const int r0 = threadIdx.x / kPer, e = threadIdx.x % kPer;
       uint4 xq[kLoads];
       int32_t at_row[kLoads];
+      // row -> (query l, head of the group), stepped by kStep columns at a time
+      int l = (row0 + r0) / p.G, gq = (row0 + r0) % p.G;
+      int lw = PAIR ? (row0 + p.half + r0) / p.G : 0, gw = PAIR ? (row0 + p.half + r0) % p.G : 0;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = r0 + i * kStep;                  // column; its row:
         const int in = PAIR && r >= N ? r - N : r, rr = PAIR && r >= N ? p.half + in : in;
         xq[i] = make_uint4(0u, 0u, 0u, 0u);
         at_row[i] = -1;
+        if (PAIR && i == N / kStep) {
+          l = lw;
+          gq = gw;
+        }
         if (rr < nrows && (!PAIR || in < p.half)) {
-          const int l = (row0 + rr) / p.G, hq = sg.h * p.G + (row0 + rr) % p.G;
+          const int hq = sg.h * p.G + gq;
           xq[i] = *reinterpret_cast<const uint4*>(p.q + sg.b * p.qb + l * p.ql + hq * p.qh + e * 16);
           at_row[i] = static_cast<int32_t>((sg.b * p.L + l) * p.Hq + hq);
+        }
+        l += step_l;
+        gq += step_g;
+        if (gq >= p.G) {
+          gq -= p.G;
+          ++l;
         }
       }
       named_sync(3, kSoftWarps * 32);                  // the previous segment's rows and references are no longer read
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = r0 + i * kStep;
-        const uint32_t w[4] = {xq[i].x, xq[i].y, xq[i].z, xq[i].w};
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t u0 = w[j] & 0x7FFFu, u1 = (w[j] >> 16) & 0x7FFFu;
-          top = max(top, u0 < 0x7F80u ? u0 : 0u);
-          top = max(top, u1 < 0x7F80u ? u1 : 0u);
-        }
-#pragma unroll
-        for (int o = kPer / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const float s = block_scale(__uint_as_float(top << 16));
-        // (the largest bf16 needs 2^120: its inverse is still normal)
-        const float inv = __uint_as_float(0x7F000000u - __float_as_uint(s));
-        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float a = bf16lo(w[j]) * inv, b = bf16hi(w[j]) * inv;
-          if (!(fabsf(a) <= 448.0f)) a = __int_as_float(0x7FFFFFFF);   // infinities and NaN: the row's results are NaN
-          if (!(fabsf(b) <= 448.0f)) b = __int_as_float(0x7FFFFFFF);
-          const uint32_t h = e4m3x2(a, b);
-          float ha, hb;
-          f16x2_to_f32(e4m3x2_to_f16x2(h), ha, hb);
-          const uint32_t l = e4m3x2(a - ha, b - hb);
-          hi[j >> 1] |= h << (16 * (j & 1));
-          lo[j >> 1] |= l << (16 * (j & 1));
-        }
-        const int chunk = e >> 1, in = PAIR ? r % N : r;
-        const uint32_t at = q_s + static_cast<uint32_t>((PAIR ? r / N : 0) * 2 * N * D + in * D +
-                                                        ((D == 128 ? chunk ^ (in & 7) : chunk ^ ((in >> 1) & 3)) << 4) +
-                                                        (e & 1) * 8);
+        uint32_t hi[2], lo[2];
+        const float s = split_query<D>(xq[i], hi, lo);
+        const int in = PAIR ? r % N : r;
+        const uint32_t at = q_s + static_cast<uint32_t>((PAIR ? r / N : 0) * 2 * N * D) + query_offset<D>(in, e);
         sts64(at, hi[0], hi[1]);
         sts64(at + N * D, lo[0], lo[1]);
         if (e == 0) {
@@ -804,7 +828,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           sh.row[r] = at_row[i];
         }
       }
-      if (tid < N) nm[tid] = -kUnset;
+      if (tid < N) nm[tid] = 0.0f;
       at_fence_async();
       named_sync(3, kSoftWarps * 32);
       if (lane == 0) mbar_arrive(smem_addr(&sh.qfull));
@@ -813,7 +837,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) l2[i] = 0;
       float vref = 0x1p-120f, vscale = kPUnit / 256 / vref;
-      bool begun = false;                              // the accumulator holds earlier tiles
+      bool begun = false, seen = false;                // the accumulator holds earlier tiles; the references a score
       for (int ti = sg.t0; ti < sg.t1; ++ti, ++g) {
         if (!PAIR && (g & 1u) != static_cast<uint32_t>(grp)) continue;
         const uint32_t nth = PAIR ? g : g >> 1;        // this group's job number
@@ -867,42 +891,37 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           unpack2(x[i], a, b);
           over = fmaxf(fmaxf(over, a), b);
         }
-        const bool raise = valid && (over > kSlack || vs > vref);
+        const bool raise = valid && (!seen || over > kSlack || vs > vref);
         if (group_any(bar_id, raise)) {                // uniform over the group
           // New references: the largest score of each column so far, and a bit
           // more (a score then has to exceed it eightfold to move it again).
-#pragma unroll 1
-          for (int c = 0; c < ncols; c += 16) {
-            uint32_t r[16];
-            at_ld<16>(s_t + c, r);
-            if constexpr (S::kConcat) {
-              uint32_t q[16];
-              at_ld<16>(s_t + N + c, q);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
-            }
-            float top = -kInf;
+          for (int c = 0; c < N; c += 32) {
+            float v[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float y = valid ? __uint_as_float(r[i]) * ck * fq[c + i] : -kInf;
-              const float mx = warp_max_f32(y == y ? y : -kInf);
-              if (lane == i) top = mx;
+            for (int i = 0; i < 32; i += 2) {
+              v[i] = v[i + 1] = -kInf;
+              if (c + (i & ~15) < ncols && valid) {
+                unpack2(x[(c + i) / 2], v[i], v[i + 1]);
+                v[i] = fmaxf(v[i], -kInf);             // (NaN does not set a reference)
+                v[i + 1] = fmaxf(v[i + 1], -kInf);
+              }
             }
-            if (lane < 16) sh.red[grp][wq][c + lane] = top;
+            const float top = column_reduce<true>(v);
+            sh.red[grp][wq][c + lane] = top;
           }
-          float vmax = warp_max_f32(valid ? vs : 0.0f);
-          if (lane == 0) sh.fac_o[grp][wq] = vmax;
+          const float vmax = warp_max_f32(valid ? vs : 0.0f);
+          if (lane == 0) sh.vmax[grp][wq] = vmax;
           named_sync(bar_id, 128);
-          vmax = fmaxf(fmaxf(sh.fac_o[grp][0], sh.fac_o[grp][1]), fmaxf(sh.fac_o[grp][2], sh.fac_o[grp][3]));
-          const float vnew = fmaxf(vref, vmax);
-          named_sync(bar_id, 128);
+          const float vnew = fmaxf(vref, fmaxf(fmaxf(sh.vmax[grp][0], sh.vmax[grp][1]),
+                                               fmaxf(sh.vmax[grp][2], sh.vmax[grp][3])));
           if (tid < ncols) {
-            const float old = -nm[tid];
-            const float mx = fmaxf(fmaxf(sh.red[grp][0][tid], sh.red[grp][1][tid]),
-                                   fmaxf(sh.red[grp][2][tid], sh.red[grp][3][tid]));
-            const float now = mx > old ? mx + kHead : old;
-            const float d = ex2_approx(old - now);
-            nm[tid] = -now;
+            const float top = fmaxf(fmaxf(sh.red[grp][0][tid], sh.red[grp][1][tid]),
+                                    fmaxf(sh.red[grp][2][tid], sh.red[grp][3][tid]));   // relative to the old reference
+            const float up = top > 0.0f || (!seen && top > -kInf) ? top + kHead : 0.0f;
+            nm[tid] -= up;
+            sh.delta[grp][tid] = -up;
+            const float d = ex2_approx(-up);
             sh.fac_l[grp][tid] = d;
             sh.fac_o[grp][tid] = d * (vref / vnew);
           }
@@ -912,8 +931,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
           for (int i = 0; i < N / 2; ++i) {
             if (i % 8 == 0 && 2 * i >= ncols) break;
-            l2[i] = at_mul2(l2[i], *reinterpret_cast<const uint64_t*>(&sh.fac_l[grp][2 * i]));
+            x[i] = add2(x[i], *reinterpret_cast<const uint64_t*>(&sh.delta[grp][2 * i]));
+            if (seen) l2[i] = at_mul2(l2[i], *reinterpret_cast<const uint64_t*>(&sh.fac_l[grp][2 * i]));
           }
+          seen = true;
           if (begun) {
             wait(sh.pvdone[grp], (nth - 1) & 1u, kFaultFullWait);
             __syncwarp();
@@ -932,8 +953,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             at_fence_before();
           }
-          named_sync(bar_id, 128);                     // (fac_o and red are free again)
-          exponents();
+          // (the next rise writes what is read here only after every warp's vote for it)
         }
         at_fence_before();                             // the scores have been read
         __syncwarp();
@@ -981,19 +1001,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
       // The segment's sums over its tokens, then its rows.
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        if (2 * i >= ncols) break;
-        float a, b;
-        unpack2(l2[i], a, b);
+      for (int c = 0; c < N; c += 32) {
+        float v[32];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-          b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-        }
-        if (lane == 0) {
-          sh.red[grp][wq][2 * i] = a;
-          sh.red[grp][wq][2 * i + 1] = b;
-        }
+        for (int i = 0; i < 32; i += 2) unpack2(l2[(c + i) / 2], v[i], v[i + 1]);
+        sh.red[grp][wq][c + lane] = column_reduce<false>(v);
       }
       if (tid == 0) sh.vref[grp] = vref;
       named_sync(3, kSoftWarps * 32);
@@ -1010,12 +1022,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int a = PAIR ? n / N : first, c = PAIR ? n % N : n;
         float m = -sh.nm[a][c];
         float l = (sh.red[a][0][c] + sh.red[a][1][c]) + (sh.red[a][2][c] + sh.red[a][3][c]);
+        if (l == 0.0f) m = kUnset;                     // (no token: its reference says nothing)
         float fa = sh.vref[a] * (1.0f / kPUnit), fb = 0.0f;
         if (both) {
           const int o = first ^ 1;
-          const float mo = -sh.nm[o][c], top = fmaxf(m, mo);
-          const float ea = ex2_approx(m - top), eb = ex2_approx(mo - top);
           const float lo = (sh.red[o][0][c] + sh.red[o][1][c]) + (sh.red[o][2][c] + sh.red[o][3][c]);
+          const float mo = lo == 0.0f ? kUnset : -sh.nm[o][c], top = fmaxf(m, mo);
+          const float ea = ex2_approx(m - top), eb = ex2_approx(mo - top);
           l = l * ea + lo * eb;
           fa *= ea;
           fb = sh.vref[o] * (1.0f / kPUnit) * eb;
@@ -1056,15 +1069,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         for (int k = 0; k < 2; ++k) {
           if (k == 1 && !both) break;
           const int a = k == 0 ? a0 : a0 ^ 1;
-          uint32_t r1[8], r2[8], r3[8];
+          uint32_t r[24];
           const uint32_t t = tmem + lanes + S::kAcc + static_cast<uint32_t>(a) * 3 * N + c;
-          at_ld<8>(t, r1);
-          at_ld<8>(t + N, r2);
-          at_ld<8>(t + 2 * N, r3);
+          at_ld3(t, t + N, t + 2 * N, r);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float y = fmaf(fmaf(__uint_as_float(r3[i]), 1.0f / 16, __uint_as_float(r2[i])), 1.0f / 16,
-                                 __uint_as_float(r1[i]));
+            const float y = fmaf(fmaf(__uint_as_float(r[16 + i]), 1.0f / 16, __uint_as_float(r[8 + i])), 1.0f / 16,
+                                 __uint_as_float(r[i]));
             o[i] = k == 0 ? y * sh.fin[a][c + i] : fmaf(y, sh.fin[a][c + i], o[i]);
           }
         }
@@ -1084,6 +1095,245 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
       }
       at_fence_before();
+    }
+  }
+  at_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    at_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the weights
+// ---------------------------------------------------------------------------
+constexpr int kWeightCols = 64;        // rows (columns of a product) of a job
+constexpr int kWeightRows = 512;       // rows of a launch: what the queries' shared memory holds
+constexpr int kWeightStages = 5;       // of the K ring
+constexpr int kWeightBufs = 4;         // score buffers of a group
+// The products run up to 2 x 4 tiles ahead of the softmax and the copies 5
+// ahead of the products: a tile's meta slot is free again after 16.
+constexpr int kWeightMeta = 16;
+
+constexpr int weights_smem(int dim, int chunks) {
+  return 1024 + 2 * chunks * kWeightCols * dim + kWeightStages * kTile * dim;
+}
+
+struct WeightShared {
+  uint64_t kfull[kWeightStages], kempty[kWeightStages];
+  uint64_t mfull[kWeightMeta];
+  uint64_t sfull[2 * kWeightBufs], sempty[2 * kWeightBufs];
+  uint64_t qfull;
+  TileMeta meta[kWeightMeta];
+  alignas(16) float f[kWeightRows], nm[kWeightRows];   // query scales, minus the rows' lse (log2 units)
+  uint32_t w0, w1, off0;
+  int32_t b0;
+  uint32_t tmem;
+  int32_t abort;
+  uint64_t vfull[1], vempty[1];                        // (not used: there is no V)
+};
+
+// w[j] = decay w[j] + sum over the rows of exp(s - lse): S^T as in the
+// attention, a thread per token, so a token's sum stays in its thread and
+// nothing is shared or added atomically.  The two groups take the tiles
+// alternately; a job is one tile and up to 64 rows, with 4 score buffers a
+// group, so the products run ahead.
+// Bound: the products (8 of M 128, N 64, K 32 for a job), since each row's
+// scores are computed twice over the attention's; K's bytes when rows are few.
+template <int D>
+__global__ void __launch_bounds__(kAttendThreads, 1) attend_weights_kernel(const __grid_constant__ AttendParams p,
+                                                                           int32_t first_row, int32_t rows) {
+  constexpr int ST = kWeightStages, NC = kWeightCols;
+  constexpr int kTileBytes = kTile * D;
+  constexpr uint32_t kSwz = D == 128 ? 2u : 4u;
+  extern __shared__ __align__(1024) uint8_t at_smem[];
+  __shared__ WeightShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (rows + NC - 1) / NC;
+  const uint32_t base = (smem_addr(at_smem) + 1023u) & ~1023u;
+  const uint32_t k_s = base, q_s = k_s + ST * kTileBytes;
+  volatile int32_t* abort_flag = &sh.abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(smem_addr(&sh.kfull[i]), 1);
+      mbar_init(smem_addr(&sh.kempty[i]), 1);
+    }
+    for (int i = 0; i < kWeightMeta; ++i) mbar_init(smem_addr(&sh.mfull[i]), 1);
+    for (int i = 0; i < 2 * kWeightBufs; ++i) {
+      mbar_init(smem_addr(&sh.sfull[i]), 1);
+      mbar_init(smem_addr(&sh.sempty[i]), 4);
+    }
+    mbar_init(smem_addr(&sh.qfull), kSoftWarps);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp == 0) plan_range(p, sh);
+  at_fence_before();
+  __syncthreads();
+  at_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  auto wait = [&](uint64_t& bar, uint32_t parity, int32_t code) {   // as in the attention kernel
+    const uint32_t a = smem_addr(&bar);
+    if (mbar_try_wait(a, parity)) return;
+    const long long t0 = clock64();
+    for (;;) {
+      if (*abort_flag) return;
+      if (mbar_try_wait_sleep(a, parity, kSleepHintNs)) return;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        atomicExch(p.fault, code);
+        *abort_flag = 1;
+        return;
+      }
+    }
+  };
+
+  Cursor cur{sh.w0, sh.w1, sh.b0, sh.off0};
+  Segment sg;
+  uint32_t g = 0;                                      // tiles this CTA has passed
+  if (warp == kCopyWarp) {
+    copy_role<D, ST, false>(p, sh, cur, k_s, 0, wait);
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t kHiK = at_desc_hi(8 * D, kSwz);
+    const uint32_t lead = elect_one();
+    const uint32_t kd = at_desc_lo(k_s, 16), qd = at_desc_lo(q_s, 16);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    uint32_t ks = 0, kp = 0;
+    uint32_t jobs[2] = {0, 0};                         // of either group
+    uint32_t seg = 0;
+    while (next_segment(p, cur, sh.w0, sg)) {
+      const uint32_t n = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(sg.t1 - sg.t0), 0);
+      wait(sh.qfull, seg & 1u, kFaultFullWait);
+      __syncwarp();
+      for (uint32_t i = 0; i < n; ++i, ++g) {
+        const uint32_t grp = g & 1u;
+        wait(sh.kfull[ks], kp, kFaultFullWait);
+        __syncwarp();
+        for (int c = 0; c < chunks; ++c) {
+          const uint32_t j = grp ? jobs[1]++ : jobs[0]++;
+          const uint32_t buf = grp * kWeightBufs + j % kWeightBufs;
+          wait(sh.sempty[buf], ((j / kWeightBufs) & 1u) ^ 1u, kFaultEmptyWait);
+          __syncwarp();
+          if (*abort_flag) continue;
+          at_fence_after();
+          const int cols = min(NC, (rows - c * NC + 15) & ~15);
+          const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(cols >> 3) << 17) |
+                                 (static_cast<uint32_t>(kTile >> 4) << 24);
+          const uint32_t k = kd + ks * (kTileBytes >> 4), q = qd + static_cast<uint32_t>(c) * (2 * NC * D >> 4);
+#pragma unroll
+          for (int m = 0; m < 2 * (D / 32); ++m) {
+            const int part = m / (D / 32), kk = m % (D / 32);
+            at_mma_f8(lead, tm + buf * NC, k + kk * 2, kHiK, q + part * (NC * D >> 4) + kk * 2, kHiK, idesc,
+                      m != 0 ? 1u : 0u);
+          }
+          at_commit(lead, smem_addr(&sh.sfull[buf]));
+        }
+        if (!*abort_flag) at_commit(lead, smem_addr(&sh.kempty[ks]));
+        __syncwarp();
+        if (++ks == ST) {
+          ks = 0;
+          kp ^= 1u;
+        }
+      }
+      ++seg;
+    }
+  } else if (warp < kSoftWarps) {
+    const int grp = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const int page_of = key / p.c.page_size;
+    constexpr int kPer = D / 8, kStep = kSoftWarps * 32 / kPer;
+    uint32_t jobs = 0;                                 // this group's
+    while (next_segment(p, cur, sh.w0, sg)) {
+      named_sync(3, kSoftWarps * 32);                  // (the previous segment's rows are no longer read)
+      const int e = threadIdx.x % kPer;
+#pragma unroll 4
+      for (int r = threadIdx.x / kPer; r < chunks * NC; r += kStep) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        float nm = -kInf;
+        if (r < rows) {
+          const int l = (first_row + r) / p.G, hq = sg.h * p.G + (first_row + r) % p.G;
+          x = *reinterpret_cast<const uint4*>(p.q + sg.b * p.qb + l * p.ql + hq * p.qh + e * 16);
+          const float lse = p.lse[(sg.b * p.L + l) * p.Hq + hq];
+          if (fabsf(lse) < kInf) nm = -lse * kLog2e;   // (other rows add nothing)
+        }
+        uint32_t hi[2], lo[2];
+        const float s = split_query<D>(x, hi, lo);
+        const uint32_t at = q_s + static_cast<uint32_t>(r / NC * 2 * NC * D) + query_offset<D>(r % NC, e);
+        sts64(at, hi[0], hi[1]);
+        sts64(at + NC * D, lo[0], lo[1]);
+        if (e == 0) {
+          sh.f[r] = s;
+          sh.nm[r] = nm;
+        }
+      }
+      at_fence_async();
+      named_sync(3, kSoftWarps * 32);
+      if (lane == 0) mbar_arrive(smem_addr(&sh.qfull));
+      for (int ti = sg.t0; ti < sg.t1; ++ti, ++g) {
+        if ((g & 1u) != static_cast<uint32_t>(grp)) continue;
+        float* wj = p.weights + (static_cast<int64_t>(sg.b) * p.c.heads + sg.h) * p.cap +
+                    static_cast<int64_t>(ti) * kTile + key;
+        const bool in = static_cast<int64_t>(ti) * kTile + key < p.cap;
+        const float old = in && p.decay != 0.0f ? *wj : 0.0f;
+        wait(sh.mfull[g % kWeightMeta], (g / kWeightMeta) & 1u, kFaultFullWait);
+        const TileMeta& m = sh.meta[g % kWeightMeta];
+        const bool valid = tile_visible(m, key, page_of, p.mask != nullptr);
+        const float ck = m.ks[page_of];
+        const uint64_t ck2 = pack2(ck, ck);
+        uint64_t sum2[2] = {0, 0};
+        for (int c = 0; c < chunks; ++c, ++jobs) {
+          const uint32_t buf = static_cast<uint32_t>(grp) * kWeightBufs + jobs % kWeightBufs;
+          wait(sh.sfull[buf], (jobs / kWeightBufs) & 1u, kFaultFullWait);
+          __syncwarp();
+          at_fence_after();
+          const int cols = min(NC, (rows - c * NC + 15) & ~15);
+#pragma unroll
+          for (int i0 = 0; i0 < NC; i0 += 16) {
+            if (i0 >= cols) break;
+            uint32_t r[16];
+            at_ld<16>(tmem + lanes + buf * NC + i0, r);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sh.f + c * NC + i0 + i);
+              const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(sh.nm + c * NC + i0 + i);
+              const uint64_t x0 =
+                  fma2(at_mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ck2), f.x, n.x);
+              const uint64_t x1 =
+                  fma2(at_mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), ck2), f.y, n.y);
+              float a0, a1, b0, b1;
+              unpack2(x0, a0, a1);
+              unpack2(x1, b0, b1);
+              // (a row that adds nothing has -inf or NaN here)
+              sum2[0] = add2(sum2[0], pack2(ex2_approx(fmaxf(a0, -1e30f)), ex2_approx(fmaxf(a1, -1e30f))));
+              sum2[1] = add2(sum2[1], pack2(ex2_approx(fmaxf(b0, -1e30f)), ex2_approx(fmaxf(b1, -1e30f))));
+            }
+          }
+          at_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.sempty[buf]));
+        }
+        float a, b;
+        unpack2(add2(sum2[0], sum2[1]), a, b);
+        if (in) *wj = fmaf(p.decay, old, valid ? a + b : 0.0f);
+      }
+    }
+    // Slots past the sequences' last tiles: decayed, or set to 0.
+    const int64_t bh = p.B * p.c.heads;
+    for (int64_t i = blockIdx.x; i < bh; i += gridDim.x) {
+      float* w = p.weights + i * p.cap;
+      for (int64_t j = static_cast<int64_t>(tiles_of(p, i / p.c.heads)) * kTile + threadIdx.x; j < p.cap;
+           j += kSoftWarps * 32)
+        w[j] = p.decay == 0.0f ? 0.0f : p.decay * w[j];
     }
   }
   at_fence_before();
@@ -1228,6 +1478,11 @@ const AttendDevice* attend_device() {
         const AttendVariant v = attend_variant(dim, n);
         d.err = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
       }
+    for (const void* k : {reinterpret_cast<const void*>(&attend_weights_kernel<64>),
+                          reinterpret_cast<const void*>(&attend_weights_kernel<128>)})
+      if (d.err == cudaSuccess)
+        d.err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     weights_smem(128, kWeightRows / kWeightCols));
     if (d.err != cudaSuccess) (void)cudaGetLastError();  // reported through the status; no sticky error
   });
   return g_at[dev].err == cudaSuccess ? &g_at[dev] : nullptr;
@@ -1352,11 +1607,20 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
                       : reinterpret_cast<const void*>(&attend_join_kernel<128>),
                   dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, jargs);
   if (st != DLLM_OK || !weights) return st;
-  return launch_pdl(d64 ? reinterpret_cast<const void*>(&attend_weights_kernel<64>)
+  // The weights: kWeightRows rows of a key head at a time, K read once for each.
+  p.row_tiles = 1;
+  for (int64_t r = 0; r < L * p.G && st == DLLM_OK; r += kWeightRows) {
+    int32_t first = static_cast<int32_t>(r), count = static_cast<int32_t>(std::min<int64_t>(kWeightRows, L * p.G - r));
+    void* wargs[] = {&p, &first, &count};
+    const int chunks = (count + kWeightCols - 1) / kWeightCols;
+    st = launch_pdl(d64 ? reinterpret_cast<const void*>(&attend_weights_kernel<64>)
                         : reinterpret_cast<const void*>(&attend_weights_kernel<128>),
-                    dim3(static_cast<unsigned>((cap + 127) / 128), static_cast<unsigned>(cache->heads),
-                         static_cast<unsigned>(B)),
-                    dim3(128), 0, stream, args);
+                    dim3(static_cast<unsigned>(std::min<int64_t>(
+                        dev->sms, B * cache->heads * ((cap + kTile - 1) / kTile)))),
+                    dim3(kAttendThreads), static_cast<size_t>(weights_smem(cache->head_dim, chunks)), stream, wargs);
+    p.decay = 1.0f;
+  }
+  return st;
 }
 
 }  // extern "C"
