@@ -18,6 +18,7 @@ constexpr int kScoreVec = 4;      // 16-byte vectors a thread has in flight
 constexpr int kTopCap = 128;      // candidates a warp keeps before it cuts them to the best k
 constexpr float kInfF = __builtin_huge_valf();
 constexpr float kLow = -0x1p+100f;  // stands for a difference or exponent that carries no mass: 2^kLow = 0, 0 * kLow = 0
+constexpr int kEntries = 2048;    // block maxima a CTA keeps
 
 struct ScoreParams {
   const uint8_t* logits;
@@ -89,25 +90,35 @@ __device__ __forceinline__ float element(const uint4& v, int e) {
 
 // One cluster of CTAs per row, each CTA an equal range of the row's 16-byte
 // vectors (few rows: up to 8 CTAs a row, so that the whole GPU reads; many
-// rows: one CTA a row, several rows to an SM).  One pass over the logits: each
-// warp holds a running maximum and every lane its sums Z and S of 2^y and 2^y y,
-// y = (z - m) log2 e, rescaled only when the warp's maximum grows; a value that
-// reaches the CTA's k-th best so far (shared by its warps) is kept as a
-// candidate, and a full list is cut to the best k.  The CTAs' parts are joined
-// in rank order through distributed shared memory.
+// rows: one CTA a row, several rows to an SM).
+//
+// One pass over the logits: a warp holds a running maximum and its lanes sums Z
+// and S of 2^y and 2^y y, y = (z - m) log2 e, rescaled only when the maximum
+// grows.  For the alternatives the pass keeps only the maximum of each block of
+// 32 vectors.  The best k elements lie in the best k blocks (by maximum, then
+// position: k better blocks would hold k better elements), so afterwards the
+// blocks that can be among those are read again, a percent or so of the row,
+// and their elements compared one by one.  (Comparing every element with the
+// k-th best so far during the pass was six times slower: almost every 1024
+// elements of a warp hold one that reaches it.)
+// Logits below -2^100 count as -2^100 in the pass; a row whose maximum is not
+// within 2^100 of zero is computed from its logits as they are by one CTA.
 // Bound: the one read of the logits.
 template <int BYTES>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_constant__ ScoreParams p) {
+__global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_constant__ ScoreParams p) {
   constexpr int EPV = 16 / BYTES;
-  constexpr int N = kScoreVec * EPV;                       // elements a thread holds
   __shared__ uint64_t list[kScoreWarps][kTopCap];
   __shared__ uint64_t scratch[kScoreWarps][DLLM_MAX_TOP];
   __shared__ uint64_t best[DLLM_MAX_TOP];                  // this CTA's best k, descending
+  __shared__ uint32_t entry[kEntries];                     // float_key of the blocks' maxima (0: none)
+  __shared__ uint16_t chosen[kEntries];
+  __shared__ uint64_t floor_entry_s;
+  __shared__ int32_t n_chosen;
   __shared__ unsigned long long floor_s;                   // no value below this candidate can be among the best k
   __shared__ Soft warp_soft[kScoreWarps];
   __shared__ Soft cta_soft;
   __shared__ int32_t count_s[kScoreWarps];
-  __shared__ uint64_t joined[8 * DLLM_MAX_TOP];
+  __shared__ alignas(16) uint64_t joined[8 * DLLM_MAX_TOP];
   __shared__ uint32_t inf_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t rank, size;
@@ -117,11 +128,15 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
   const int k = p.top;
   if (threadIdx.x == 0) {
     floor_s = 0;
+    floor_entry_s = 0;
+    n_chosen = 0;
     inf_s = 0;
   }
-  __syncthreads();
-  pdl_wait();
+  if (k > 0)
+    for (int i = threadIdx.x; i < kEntries; i += kScoreThreads) entry[i] = 0;
   pdl_launch_dependents();
+  pdl_wait();
+  __syncthreads();
 
   const uint8_t* base = p.logits + row * p.row_bytes;
   // The row as whole aligned vectors, with up to EPV - 1 elements before and after them.
@@ -130,72 +145,136 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
   const int64_t tail0 = lead + nvec * EPV;
   const uint4* vecs = reinterpret_cast<const uint4*>(base + lead * BYTES);
   const int64_t v0 = nvec * rank / size, v1 = nvec * (rank + 1) / size;
-  Soft a{-kInfF, 0.0f, 0.0f};
-  int have = 0;                                            // candidates in this warp's list
-  float floor_z = -kInfF;                                  // the value of the floor this warp last saw
-  uint64_t floor_c = 0;
-  auto cut = [&]() {                                       // keep the best k of the warp's list, raise the floor
-    __syncwarp();
-    rank_candidates(list[warp], have, k, scratch[warp], lane, 32);
-    __syncwarp();
-    if (have > k) have = k;
-    if (lane < have) list[warp][lane] = scratch[warp][lane];
-    __syncwarp();
-    if (have == k && lane == 0) atomicMax(&floor_s, static_cast<unsigned long long>(scratch[warp][k - 1]));
-    __syncwarp();
-  };
-  // Folds N values of each lane (NaN and absent ones as -inf) into the state.
-  // Value e has the id first + (e / EPV) 32 EPV + e % EPV; absent: bits of values that are no candidates.
-  float z[N];
-  auto fold = [&](uint32_t first, uint32_t absent) {
-    float c = z[0];
+  const int64_t blocks = (v1 - v0 + 31) / 32;
+  int shift = 0;                                           // 2^shift blocks share an entry
+  while (((blocks + (1 << shift) - 1) >> shift) > kEntries) ++shift;
+  Soft a{kLow, 0.0f, 0.0f};
+
+  int sup_at = 0;                                          // suppressed ids before this warp's position
+  for (int64_t b0 = v0 + warp * (kScoreVec * 32); b0 < v1; b0 += kScoreThreads * kScoreVec) {
+    uint4 x[kScoreVec];
 #pragma unroll
-    for (int e = 1; e < N; ++e) c = fmaxf(c, z[e]);
-    const float cm = warp_max_f32(c);
-    if (cm > a.m) soft_raise(a, cm);                       // warp-uniform
-    float Z = 0.0f, S = 0.0f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float y = fmaxf(z[e] - a.m, kLow) * kLog2e;
-      const float x = ex2_approx(y);
-      Z += x;
-      S = fmaf(x, y, S);
+    for (int u = 0; u < kScoreVec; ++u) {
+      const int64_t v = b0 + u * 32 + lane;
+      const uint32_t none = BYTES == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+      x[u] = make_uint4(none, none, none, none);
+      if (v < v1) x[u] = __ldcs(vecs + v);
     }
-    a.Z += Z;
-    a.S += S;
-    if (k == 0 || cm < floor_z) return;
-    const uint64_t f = *const_cast<volatile unsigned long long*>(&floor_s);
-    if (f > floor_c) {
-      floor_c = f;
-      floor_z = candidate_value(f);
-      if (cm < floor_z) return;
-    }
-    if (floor_c == 0 && have == 0) {
-      // The first values: the k-th largest of the lanes' maxima is below k values, so it is a floor.
-      uint64_t mine = 0;
+    const int64_t id0 = lead + b0 * EPV, id1 = id0 + kScoreVec * 32 * EPV;
+    while (sup_at < p.n_sup && p.sup[sup_at] < id0) ++sup_at;
+    for (int q = sup_at; q < p.n_sup && p.sup[q] < id1; ++q) {   // rare: a suppressed id among this warp's values
+      const int off = static_cast<int>(p.sup[q] - id0);
+      const int at = off / EPV % 32 == lane ? off / (32 * EPV) * EPV + off % EPV : -1;
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (!((absent >> e) & 1u)) {
-          const uint64_t q = candidate(z[e], first + e / EPV * 32 * EPV + e % EPV);
-          mine = q > mine ? q : mine;
-        }
-      list[warp][lane] = mine;
-      __syncwarp();
-      int r = 0;
-      for (int j = 0; j < 32; ++j) r += list[warp][j] > mine ? 1 : 0;
-      const uint32_t at = __ballot_sync(0xFFFFFFFFu, r == k - 1 && mine != 0);
-      if (at != 0u) {
-        floor_c = __shfl_sync(0xFFFFFFFFu, mine, __ffs(at) - 1);
-        floor_z = candidate_value(floor_c);
-        if (lane == 0) atomicMax(&floor_s, static_cast<unsigned long long>(floor_c));
+      for (int u = 0; u < kScoreVec; ++u)
+#pragma unroll
+        for (int e = 0; e < EPV; ++e)
+          if (u * EPV + e == at) {
+            uint32_t& w = (&x[u].x)[BYTES == 2 ? e >> 1 : e];
+            w = BYTES == 4 ? 0xFF800000u : ((e & 1) ? (w & 0xFFFFu) | 0xFF800000u : (w & 0xFFFF0000u) | 0xFF80u);
+          }
+    }
+    // NaN and everything below -2^100 as -2^100; the blocks' maxima.
+    float top[kScoreVec];
+#pragma unroll
+    for (int u = 0; u < kScoreVec; ++u) {
+      uint32_t* w = &x[u].x;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        w[q] = BYTES == 2 ? bmax2(w[q], kSentinelBf16x2)
+                          : __float_as_uint(fmaxf(__uint_as_float(w[q]), kLow));
+      if (BYTES == 2) {
+        const uint32_t m2 = bmax2(bmax2(w[0], w[1]), bmax2(w[2], w[3]));
+        top[u] = fmaxf(bf16lo(m2), bf16hi(m2));
+      } else {
+        top[u] = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                       fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
       }
-      __syncwarp();
     }
+    float cm;
+    if (k > 0) {
+      cm = kLow;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const bool near = z[e] >= floor_z && !((absent >> e) & 1u);
-      uint32_t hit = __ballot_sync(0xFFFFFFFFu, near);
-      if (hit == 0u) continue;
+      for (int u = 0; u < kScoreVec; ++u) {
+        const float m = warp_max_f32(top[u]);
+        cm = fmaxf(cm, m);
+        const int64_t block = (b0 - v0) / 32 + u;
+        if (lane == u && block < blocks) {
+          if (shift == 0) entry[block] = float_key(m);
+          else atomicMax(&entry[block >> shift], float_key(m));
+        }
+      }
+    } else {
+      cm = warp_max_f32(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+    }
+    if (cm > a.m) soft_raise(a, cm);                       // warp-uniform
+    const uint64_t nm2 = pack2(-a.m, -a.m), l2e2 = pack2(kLog2e, kLog2e);
+    uint64_t Z2 = 0, S2 = 0;
+#pragma unroll
+    for (int u = 0; u < kScoreVec; ++u) {
+      const uint32_t* w = &x[u].x;
+#pragma unroll
+      for (int q = 0; q < EPV / 2; ++q) {
+        const uint64_t z = BYTES == 2 ? pack2(bf16lo(w[q]), bf16hi(w[q]))
+                                      : pack2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
+        uint64_t y = add2(z, nm2);
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(l2e2));
+        float y0, y1;
+        unpack2(y, y0, y1);
+        const uint64_t e = pack2(ex2_approx(y0), ex2_approx(y1));
+        Z2 = add2(Z2, e);
+        S2 = fma2(e, y, S2);
+      }
+    }
+    float z0, z1, s0, s1;
+    unpack2(Z2, z0, z1);
+    unpack2(S2, s0, s1);
+    a.Z += z0 + z1;
+    a.S += s0 + s1;
+  }
+
+  // The elements outside the whole vectors: the first CTA's first warp holds
+  // those before (lanes 0 .. EPV - 1), the last CTA's those after (lanes 16 ..).
+  const bool edges = warp == 0 && ((rank == 0 && lead > 0) || (rank == size - 1 && tail0 < p.V));
+  const int64_t edge_id = lane < 16 ? lane : tail0 + lane - 16;
+  float edge_z = -kInfF;
+  bool edge_in = false;
+  if (edges) {
+    edge_in = lane < 16 ? rank == 0 && edge_id < lead : rank == size - 1 && edge_id < p.V;
+    if (edge_in) {
+      if (BYTES == 2)
+        edge_z = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[edge_id]) << 16);
+      else
+        edge_z = reinterpret_cast<const float*>(base)[edge_id];
+      edge_z = no_nan(edge_z);
+      for (int q = 0; q < p.n_sup; ++q)
+        if (p.sup[q] == edge_id) edge_in = false;
+    }
+    const float z = edge_in ? fmaxf(edge_z, kLow) : kLow;
+    const float cm = warp_max_f32(z);
+    if (cm > a.m) soft_raise(a, cm);
+    const float y = (z - a.m) * kLog2e, e = edge_in ? ex2_approx(y) : 0.0f;
+    a.Z += e;
+    if (edge_in) a.S = fmaf(e, y, a.S);
+  }
+
+  int have = 0;                                            // candidates in this warp's list
+  if (k > 0) {
+    float floor_z = -kInfF;
+    uint64_t floor_c = 0;                                  // a candidate below it is not among the best k
+    auto cut = [&]() {                                     // keep the best k of the warp's list, raise the floor
+      __syncwarp();
+      rank_candidates(list[warp], have, k, scratch[warp], lane, 32);
+      __syncwarp();
+      if (have > k) have = k;
+      if (lane < have) list[warp][lane] = scratch[warp][lane];
+      __syncwarp();
+      if (have == k && lane == 0) atomicMax(&floor_s, static_cast<unsigned long long>(scratch[warp][k - 1]));
+      __syncwarp();
+    };
+    auto offer = [&](float z, uint32_t id, bool in) {      // one value per lane
+      const bool near = in && z >= floor_z;
+      if (__ballot_sync(0xFFFFFFFFu, near) == 0u) return;
       if (have + 32 > kTopCap) {
         cut();
         const uint64_t g = *const_cast<volatile unsigned long long*>(&floor_s);
@@ -204,71 +283,65 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
           floor_z = candidate_value(g);
         }
       }
-      const uint64_t q = candidate(z[e], first + e / EPV * 32 * EPV + e % EPV);
-      hit = __ballot_sync(0xFFFFFFFFu, near && q >= floor_c);
-      if (near && q >= floor_c) list[warp][have + __popc(hit & ((1u << lane) - 1u))] = q;
+      const uint64_t q = candidate(z, id);
+      const bool keep = near && q >= floor_c;
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, keep);
+      if (keep) list[warp][have + __popc(hit & ((1u << lane) - 1u))] = q;
       have += __popc(hit);
+    };
+    if (edges) offer(edge_z, static_cast<uint32_t>(edge_id), edge_in);
+    // A floor for the entries: each thread's best entry; at least k entries are
+    // no worse than the k-th of those.
+    const int n = static_cast<int>((blocks + (1 << shift) - 1) >> shift);
+    __syncthreads();
+    uint64_t* mine_s = joined;
+    uint64_t mine = 0;
+    for (int e = threadIdx.x; e < n; e += kScoreThreads) {
+      const uint64_t c = static_cast<uint64_t>(entry[e]) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(e));
+      mine = c > mine ? c : mine;
     }
-  };
-
-  // The elements outside the whole vectors: the first CTA's first warp takes those before, the last CTA's those after.
-  if (warp == 0 && ((rank == 0 && lead > 0) || (rank == size - 1 && tail0 < p.V))) {
-    uint32_t absent = 0xFFFFFFFFu;
-    // lanes 0 .. EPV - 1 before the vectors, lanes 16 .. 16 + EPV - 1 after them
-    const int64_t v = lane < 16 ? lane : tail0 + lane - 16;
-    const bool in = lane < 16 ? rank == 0 && v < lead : rank == size - 1 && v < p.V;
-    z[0] = -kInfF;
-    if (in) {
-      if (BYTES == 2)
-        z[0] = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[v]) << 16);
-      else
-        z[0] = reinterpret_cast<const float*>(base)[v];
-      z[0] = no_nan(z[0]);
-      absent &= ~1u;
-      for (int q = 0; q < p.n_sup; ++q)
-        if (p.sup[q] == v) {
-          z[0] = -kInfF;
-          absent |= 1u;
+    mine_s[threadIdx.x] = mine;
+    __syncthreads();
+    if (mine != 0) {
+      int r = 0;
+#pragma unroll 4
+      for (int j = 0; j < kScoreThreads; j += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&mine_s[j]);
+        r += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
+      }
+      // (among values that only stand for "-2^100 or less" the entries say nothing: then all are taken)
+      if (r == k - 1 && candidate_value(mine) > kLow) floor_entry_s = mine;
+    }
+    __syncthreads();
+    const uint64_t fe = floor_entry_s;
+    for (int e = threadIdx.x; e < n; e += kScoreThreads)
+      if ((static_cast<uint64_t>(entry[e]) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(e))) >= fe)
+        chosen[atomicAdd(&n_chosen, 1)] = static_cast<uint16_t>(e);
+    __syncthreads();
+    if (fe != 0) {
+      floor_z = candidate_value(fe);
+      floor_c = fe & 0xFFFFFFFF00000000ull;                // its value with any id
+    }
+    const int nc = n_chosen;
+    for (int c = warp; c < nc; c += kScoreWarps) {
+      const int64_t first = static_cast<int64_t>(chosen[c]) << shift;
+      const int64_t last = std::min<int64_t>(first + (1 << shift), blocks);
+      for (int64_t blk = first; blk < last; ++blk) {
+        const int64_t v = v0 + blk * 32 + lane;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (v < v1) x = vecs[v];
+        const int64_t id = lead + v * EPV;
+        uint32_t absent = v < v1 ? 0u : 0xFFu;
+        for (int q = 0; q < p.n_sup; ++q) {
+          const int64_t off = p.sup[q] - id;
+          if (off >= 0 && off < EPV) absent |= 1u << off;
         }
-    }
 #pragma unroll
-    for (int e = 1; e < N; ++e) z[e] = -kInfF;
-    fold(static_cast<uint32_t>(v), absent);
-  }
-
-  int sup_at = 0;                                          // suppressed ids before this warp's position
-  for (int64_t b0 = v0 + warp * (kScoreVec * 32); b0 < v1; b0 += kScoreThreads * kScoreVec) {
-    uint4 x[kScoreVec];
-#pragma unroll
-    for (int u = 0; u < kScoreVec; ++u) {
-      const int64_t v = b0 + u * 32 + lane;
-      if (v < v1) x[u] = __ldcs(vecs + v);
-    }
-    uint32_t absent = 0;
-#pragma unroll
-    for (int u = 0; u < kScoreVec; ++u) {
-      if (b0 + u * 32 + lane < v1) {
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) z[u * EPV + e] = no_nan(element<BYTES>(x[u], e));
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) z[u * EPV + e] = -kInfF;
-        absent |= ((1u << EPV) - 1u) << (u * EPV);
+        for (int e = 0; e < EPV; ++e)
+          offer(no_nan(element<BYTES>(x, e)), static_cast<uint32_t>(id) + e, !((absent >> e) & 1u));
       }
     }
-    const int64_t id0 = lead + b0 * EPV, id1 = id0 + kScoreVec * 32 * EPV;
-    while (sup_at < p.n_sup && p.sup[sup_at] < id0) ++sup_at;
-    for (int q = sup_at; q < p.n_sup && p.sup[q] < id1; ++q) {   // rare: a suppressed id among this warp's values
-      const int off = static_cast<int>(p.sup[q] - id0);
-      const int at = off / EPV % 32 == lane ? off / (32 * EPV) * EPV + off % EPV : -1;
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (e == at) {
-          z[e] = -kInfF;
-          absent |= 1u << e;
-        }
-    }
-    fold(static_cast<uint32_t>(id0) + lane * EPV, absent);
+    cut();
   }
 
   // The warp's state, the CTA's, the row's.
@@ -277,10 +350,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
     a.Z += __shfl_xor_sync(0xFFFFFFFFu, a.Z, o);
     a.S += __shfl_xor_sync(0xFFFFFFFFu, a.S, o);
   }
-  if (k > 0) {
-    cut();
-    if (lane == 0) count_s[warp] = have;
-  }
+  if (k > 0 && lane == 0) count_s[warp] = have;
   if (lane == 0) warp_soft[warp] = a;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -344,20 +414,46 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
     __syncthreads();
   }
 
-  const Soft t = warp_soft[0];
-  float ln_z = logf(t.Z);
-  if (t.m == kInfF) {                                      // +inf logits share the mass equally: count them
-    uint32_t mine = 0;
-    for (int64_t v = threadIdx.x; v < p.V; v += kScoreThreads) {
-      bool inf = BYTES == 2 ? reinterpret_cast<const uint16_t*>(base)[v] == 0x7F80u
-                            : reinterpret_cast<const float*>(base)[v] == kInfF;
-      for (int q = 0; q < p.n_sup; ++q) inf = inf && p.sup[q] != v;
-      mine += inf ? 1u : 0u;
-    }
-    if (mine) atomicAdd(&inf_s, mine);
+  Soft t = warp_soft[0];
+  if (!(t.m > kLow && t.m < -kLow)) {                      // CTA-uniform, rare: from the logits as they are
+    auto logit = [&](int64_t v) {
+      for (int q = 0; q < p.n_sup; ++q)
+        if (p.sup[q] == v) return -kInfF;
+      if (BYTES == 4) return no_nan(reinterpret_cast<const float*>(base)[v]);
+      return no_nan(__uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[v]) << 16));
+    };
+    float m = -kInfF;
+    for (int64_t v = threadIdx.x; v < p.V; v += kScoreThreads) m = fmaxf(m, logit(v));
+    m = warp_max_f32(m);
     __syncthreads();
-    ln_z = logf(static_cast<float>(inf_s));
+    if (lane == 0) warp_soft[warp].m = m;
+    __syncthreads();
+    for (int w = 0; w < kScoreWarps; ++w) m = fmaxf(m, warp_soft[w].m);
+    t = Soft{m, 0.0f, 0.0f};
+    uint32_t infs = 0;                                     // +inf logits share the mass equally
+    for (int64_t v = threadIdx.x; v < p.V; v += kScoreThreads) {
+      const float z = logit(v);
+      infs += z == kInfF ? 1u : 0u;
+      const float y = fmaxf(z - m, kLow) * kLog2e, e = ex2_approx(y);
+      t.Z += e;
+      t.S = fmaf(e, y, t.S);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      t.Z += __shfl_xor_sync(0xFFFFFFFFu, t.Z, o);
+      t.S += __shfl_xor_sync(0xFFFFFFFFu, t.S, o);
+    }
+    if (infs) atomicAdd(&inf_s, infs);
+    __syncthreads();
+    if (lane == 0) warp_soft[warp] = t;
+    __syncthreads();
+    t.Z = t.S = 0.0f;
+    for (int w = 0; w < kScoreWarps; ++w) {
+      t.Z += warp_soft[w].Z;
+      t.S += warp_soft[w].S;
+    }
   }
+  const float ln_z = t.m == kInfF ? logf(static_cast<float>(inf_s)) : logf(t.Z);
   // log p of a logit z (NaN as -inf) under the row's softmax.
   auto log_p = [&](float z) {
     if (t.m == kInfF) return z == kInfF ? -ln_z : -kInfF;
