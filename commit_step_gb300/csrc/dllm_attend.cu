@@ -485,7 +485,7 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
       const int slot = lane - i * ppt;               // of this lane's page in the tile
       const bool mine = slot >= 0 && slot < ppt;
       const unsigned pages = (named >> (i * ppt)) & (0xFFFFFFFFu >> (32 - ppt));
-      if (*abort_flag) continue;
+      if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) continue;   // (the whole warp or none)
       if (lane == 0) {
         const uint32_t bytes = static_cast<uint32_t>(__popc(pages) * ps * D);
         mbar_arrive_expect_tx(smem_addr(&sh.kfull[st]), bytes);

@@ -30,14 +30,15 @@ constexpr int kAppendVec = 8;  // 16-byte vectors (8 dims of one token) a thread
 // magnitude, fixes the page's scale and writes the codes; tokens the page
 // already held are re-expressed when the scale grows.
 // Bound: the bf16 read and the e4m3 write, 3 bytes an element.
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
+template <int D>
+__global__ void __launch_bounds__(256, 4) append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ float red[8];
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   const int64_t b = blockIdx.z >> 1;
   const int kv = blockIdx.z & 1;
   const int h = blockIdx.y;
-  const int ps = p.c.page_size, D = p.c.dim;
+  const int ps = p.c.page_size;
   const int64_t start = p.start[b];
   int64_t n = p.count ? p.count[b] : p.L;
   n = n < 0 ? 0 : (n > p.L ? p.L : n);
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
   uint8_t* codes = (kv ? p.c.v : p.c.k) + (page * p.c.heads + h) * ps * D;
   float* scale_at = (kv ? p.c.v_scale : p.c.k_scale) + page * p.c.heads + h;
   const uint8_t* src = p.src[kv] + b * p.sb[kv] + h * p.sh[kv];
-  const int per_token = D / 8;
+  constexpr int per_token = D / 8;
   const int from = static_cast<int>(a - lo), to = static_cast<int>(e - lo);  // new slots [from, to)
   uint4 x[kAppendVec];
   uint32_t top = 0;                                              // largest finite |bf16| bits (they order as values)
@@ -131,6 +132,7 @@ struct EvictParams {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectBins = 2048;
 constexpr int kSelectItems = 4;  // consecutive tokens a thread places at a time
+constexpr int kSelectRow = 48 * 1024;  // tokens whose keys a block keeps in shared memory over the passes
 
 __device__ __forceinline__ int seq_len(const int32_t* lens, int64_t b, int64_t cap) {
   const int64_t n = lens[b];
@@ -173,13 +175,15 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sums, 
 // keep_first, the last keep_last, and among the rest the largest weights (ties
 // to the lower slot), by a radix selection of the smallest kept key (11, 11
 // and 10 bits) and one ordered pass that numbers the kept tokens.
-// Bound: latency of the passes over a row that stays in L1 and L2.
+// Bound: latency of the passes over a row that stays in shared memory (longer
+// ones in L2).
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
   __shared__ uint32_t hist[kSelectBins];
   __shared__ uint64_t sums[32];
   __shared__ uint32_t pick_bin, pick_rest;
-  pdl_wait();
+  extern __shared__ uint32_t row_keys[];                     // the row's keys, when they fit
   pdl_launch_dependents();
+  pdl_wait();
   const int h = blockIdx.x;
   const int64_t b = blockIdx.y;
   const int tid = threadIdx.x;
@@ -193,15 +197,30 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   uint32_t prefix = 0, mask = 0;
   const bool all = need >= static_cast<uint32_t>(l - f);
   const bool none = need == 0;
+  const bool held = n <= kSelectRow;
   if (!all && !none) {
+    if (held)
+      for (int j = f + tid; j < l; j += kSelectThreads) row_keys[j] = weight_key(w[j]);
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
       const uint32_t bins = pass == 2 ? 1024u : 2048u;
       for (uint32_t i = tid; i < bins; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
-      for (int j = f + tid; j < l; j += kSelectThreads) {
-        const uint32_t k = weight_key(w[j]);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+      for (int j0 = f; j0 < l; j0 += kSelectThreads) {
+        const int j = j0 + tid;
+        const uint32_t k = j < l ? (held ? row_keys[j] : weight_key(w[j])) : 0u;
+        const bool in = j < l && (k & mask) == prefix;
+        const uint32_t bin = (k >> shift) & (bins - 1);
+        // Weights crowd in a few bins (most tokens draw next to nothing): the
+        // bin of the warp's first lane is added once for all its lanes.
+        const uint32_t some = __ballot_sync(0xFFFFFFFFu, in);
+        if (some == 0u) continue;
+        const int lead = __ffs(some) - 1;
+        const uint32_t common = __shfl_sync(0xFFFFFFFFu, bin, lead);   // (every lane takes part)
+        const bool same = in && bin == common;
+        const uint32_t crowd = __ballot_sync(0xFFFFFFFFu, same);
+        if ((tid & 31) == lead) atomicAdd(&hist[bin], static_cast<uint32_t>(__popc(crowd)));
+        if (in && !same) atomicAdd(&hist[bin], 1u);
       }
       __syncthreads();
       // counts from the top bin down: thread t owns bins 2t and 2t + 1 counted from the top
@@ -228,10 +247,17 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   for (int j0 = 0; j0 < n; j0 += kSelectThreads * kSelectItems) {
     float wj[kSelectItems];
     uint32_t gt = 0, eq = 0;                                 // bits per item
+    const int j1 = j0 + tid * kSelectItems;
+    if (j1 + kSelectItems <= n) {                            // (rows of cap, a multiple of 16, floats)
+#pragma unroll
+      for (int i = 0; i < kSelectItems; ++i) wj[i] = w[j1 + i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSelectItems; ++i) wj[i] = j1 + i < n ? w[j1 + i] : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < kSelectItems; ++i) {
-      const int j = j0 + tid * kSelectItems + i;
-      wj[i] = j < n ? w[j] : 0.0f;
+      const int j = j1 + i;
       const uint32_t k = weight_key(wj[i]);
       const bool middle = j >= f && j < l;
       if (j < n && (!middle || all || (!none && k > prefix))) gt |= 1u << i;
@@ -267,14 +293,15 @@ constexpr int kMoveVec = 4;  // 16-byte vectors (16 codes of one token) a thread
 // gathers the kept tokens of the page (one read), finds their largest value,
 // writes them under the page's new scale.
 // Bound: one byte read and one written for each element that stays.
-__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
+template <int D>
+__global__ void __launch_bounds__(256, 4) evict_move_kernel(const __grid_constant__ EvictParams p) {
   __shared__ float red[8];
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   const int64_t b = blockIdx.z >> 1;
   const int kv = blockIdx.z & 1;
   const int h = blockIdx.y;
-  const int ps = p.c.page_size, D = p.c.dim;
+  const int ps = p.c.page_size;
   const int n = seq_len(p.lens, b, p.cap);
   const int m = n < p.budget ? n : p.budget;
   const int lo = blockIdx.x * ps;
@@ -285,7 +312,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
   const uint8_t* pool = kv ? p.c.v : p.c.k;
   const float* scales = kv ? p.c.v_scale : p.c.k_scale;
   const int32_t* keep = p.keep + (b * p.c.heads + h) * static_cast<int64_t>(p.budget) + lo;
-  const int per_token = D / 16;
+  constexpr int per_token = D / 16;
   uint4 x[kMoveVec];
   float sc[kMoveVec];
   float amax = 0.0f;
@@ -391,7 +418,8 @@ dllm_status dllm_cache_append(const dllm_kv_cache* cache, const void* k, const v
   const unsigned threads = static_cast<unsigned>(std::max<int64_t>(32, ps * cache->head_dim / (8 * kAppendVec)));
   void* args[] = {&p};
   if (2 * B > 65535) return DLLM_ERR_UNSUPPORTED;
-  return launch_pdl(reinterpret_cast<const void*>(&append_kernel),
+  return launch_pdl(cache->head_dim == 64 ? reinterpret_cast<const void*>(&append_kernel<64>)
+                                          : reinterpret_cast<const void*>(&append_kernel<128>),
                     dim3(static_cast<unsigned>(p.cols), static_cast<unsigned>(cache->heads),
                          static_cast<unsigned>(2 * B)),
                     dim3(threads), 0, stream, args);
@@ -433,14 +461,20 @@ dllm_status dllm_cache_evict(const dllm_kv_cache* cache, const int32_t* table, i
   p.keep_first = static_cast<int32_t>(keep_first);
   p.keep_last = static_cast<int32_t>(keep_last);
   void* args[] = {&p};
+  // (set on every call: the current device may be another one)
+  if (cap * 4 > 32 * 1024 &&
+      cudaFuncSetAttribute(reinterpret_cast<const void*>(&evict_select_kernel),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectRow * 4) != cudaSuccess)
+    return DLLM_ERR_CUDA;
   st = launch_pdl(reinterpret_cast<const void*>(&evict_select_kernel),
-                  dim3(static_cast<unsigned>(cache->heads), static_cast<unsigned>(B)), dim3(kSelectThreads), 0, stream,
-                  args);
+                  dim3(static_cast<unsigned>(cache->heads), static_cast<unsigned>(B)), dim3(kSelectThreads),
+                  static_cast<size_t>(std::min<int64_t>(cap, kSelectRow)) * 4, stream, args);
   if (st != DLLM_OK) return st;
   const int64_t ps = cache->page_size;
   const unsigned threads = static_cast<unsigned>(std::max<int64_t>(32, ps * cache->head_dim / (16 * kMoveVec)));
   const int64_t cols = (std::min(budget, cap) + ps - 1) / ps;
-  return launch_pdl(reinterpret_cast<const void*>(&evict_move_kernel),
+  return launch_pdl(cache->head_dim == 64 ? reinterpret_cast<const void*>(&evict_move_kernel<64>)
+                                          : reinterpret_cast<const void*>(&evict_move_kernel<128>),
                     dim3(static_cast<unsigned>(cols), static_cast<unsigned>(cache->heads),
                          static_cast<unsigned>(2 * B)),
                     dim3(threads), 0, stream, args);

@@ -145,34 +145,51 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
   const int64_t tail0 = lead + nvec * EPV;
   const uint4* vecs = reinterpret_cast<const uint4*>(base + lead * BYTES);
   const int64_t v0 = nvec * rank / size, v1 = nvec * (rank + 1) / size;
-  const int64_t blocks = (v1 - v0 + 31) / 32;
+  const int nv = static_cast<int>(v1 - v0);                // this CTA's vectors (V < 2^31)
+  const int blocks = (nv + 31) / 32;
   int shift = 0;                                           // 2^shift blocks share an entry
   while (((blocks + (1 << shift) - 1) >> shift) > kEntries) ++shift;
   Soft a{kLow, 0.0f, 0.0f};
 
-  int sup_at = 0;                                          // suppressed ids before this warp's position
-  for (int64_t b0 = v0 + warp * (kScoreVec * 32); b0 < v1; b0 += kScoreThreads * kScoreVec) {
+  // The next suppressed id, as an element offset from this CTA's first.
+  const int64_t id_base = lead + v0 * EPV;
+  int sup_at = 0;
+  int64_t next_sup = INT64_MAX;
+  auto skip_sup = [&](int64_t upto) {                      // to the first one at or past `upto`
+    while (sup_at < p.n_sup && p.sup[sup_at] - id_base < upto) ++sup_at;
+    next_sup = sup_at < p.n_sup ? p.sup[sup_at] - id_base : INT64_MAX;
+  };
+  skip_sup(0);
+  const uint4* src = vecs + v0 + lane;
+  for (int b0 = warp * (kScoreVec * 32); b0 < nv; b0 += kScoreThreads * kScoreVec) {
     uint4 x[kScoreVec];
+    if (b0 + kScoreVec * 32 <= nv) {
 #pragma unroll
-    for (int u = 0; u < kScoreVec; ++u) {
-      const int64_t v = b0 + u * 32 + lane;
-      const uint32_t none = BYTES == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
-      x[u] = make_uint4(none, none, none, none);
-      if (v < v1) x[u] = __ldcs(vecs + v);
+      for (int u = 0; u < kScoreVec; ++u) x[u] = __ldcs(src + b0 + u * 32);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kScoreVec; ++u) {
+        const uint32_t none = BYTES == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+        x[u] = make_uint4(none, none, none, none);
+        if (b0 + u * 32 + lane < nv) x[u] = __ldcs(src + b0 + u * 32);
+      }
     }
-    const int64_t id0 = lead + b0 * EPV, id1 = id0 + kScoreVec * 32 * EPV;
-    while (sup_at < p.n_sup && p.sup[sup_at] < id0) ++sup_at;
-    for (int q = sup_at; q < p.n_sup && p.sup[q] < id1; ++q) {   // rare: a suppressed id among this warp's values
-      const int off = static_cast<int>(p.sup[q] - id0);
-      const int at = off / EPV % 32 == lane ? off / (32 * EPV) * EPV + off % EPV : -1;
+    const int64_t end = static_cast<int64_t>(b0 + kScoreVec * 32) * EPV;
+    if (next_sup < end) {                                  // rare: a suppressed id among this warp's values
+      skip_sup(static_cast<int64_t>(b0) * EPV);
+      for (int i = sup_at; i < p.n_sup && p.sup[i] - id_base < end; ++i) {
+        const int off = static_cast<int>(p.sup[i] - id_base - static_cast<int64_t>(b0) * EPV);
+        const int at = off / EPV % 32 == lane ? off / (32 * EPV) * EPV + off % EPV : -1;
 #pragma unroll
-      for (int u = 0; u < kScoreVec; ++u)
+        for (int u = 0; u < kScoreVec; ++u)
 #pragma unroll
-        for (int e = 0; e < EPV; ++e)
-          if (u * EPV + e == at) {
-            uint32_t& w = (&x[u].x)[BYTES == 2 ? e >> 1 : e];
-            w = BYTES == 4 ? 0xFF800000u : ((e & 1) ? (w & 0xFFFFu) | 0xFF800000u : (w & 0xFFFF0000u) | 0xFF80u);
-          }
+          for (int e = 0; e < EPV; ++e)
+            if (u * EPV + e == at) {
+              uint32_t& w = (&x[u].x)[BYTES == 2 ? e >> 1 : e];
+              w = BYTES == 4 ? 0xFF800000u : ((e & 1) ? (w & 0xFFFFu) | 0xFF800000u : (w & 0xFFFF0000u) | 0xFF80u);
+            }
+      }
+      skip_sup(end);
     }
     // NaN and everything below -2^100 as -2^100; the blocks' maxima.
     float top[kScoreVec];
@@ -193,16 +210,15 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
     }
     float cm;
     if (k > 0) {
-      cm = kLow;
+      static_assert(kScoreVec == 4, "");
 #pragma unroll
-      for (int u = 0; u < kScoreVec; ++u) {
-        const float m = warp_max_f32(top[u]);
-        cm = fmaxf(cm, m);
-        const int64_t block = (b0 - v0) / 32 + u;
-        if (lane == u && block < blocks) {
-          if (shift == 0) entry[block] = float_key(m);
-          else atomicMax(&entry[block >> shift], float_key(m));
-        }
+      for (int u = 0; u < kScoreVec; ++u) top[u] = warp_max_f32(top[u]);
+      cm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      const float mine = lane & 2 ? (lane & 1 ? top[3] : top[2]) : (lane & 1 ? top[1] : top[0]);
+      const int block = (b0 >> 5) + lane;
+      if (lane < kScoreVec && block < blocks) {
+        if (shift == 0) entry[block] = float_key(mine);
+        else atomicMax(&entry[block >> shift], float_key(mine));
       }
     } else {
       cm = warp_max_f32(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
@@ -292,7 +308,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
     if (edges) offer(edge_z, static_cast<uint32_t>(edge_id), edge_in);
     // A floor for the entries: each thread's best entry; at least k entries are
     // no worse than the k-th of those.
-    const int n = static_cast<int>((blocks + (1 << shift) - 1) >> shift);
+    const int n = (blocks + (1 << shift) - 1) >> shift;
     __syncthreads();
     uint64_t* mine_s = joined;
     uint64_t mine = 0;
@@ -322,24 +338,22 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
       floor_z = candidate_value(fe);
       floor_c = fe & 0xFFFFFFFF00000000ull;                // its value with any id
     }
-    const int nc = n_chosen;
-    for (int c = warp; c < nc; c += kScoreWarps) {
-      const int64_t first = static_cast<int64_t>(chosen[c]) << shift;
-      const int64_t last = std::min<int64_t>(first + (1 << shift), blocks);
-      for (int64_t blk = first; blk < last; ++blk) {
-        const int64_t v = v0 + blk * 32 + lane;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (v < v1) x = vecs[v];
-        const int64_t id = lead + v * EPV;
-        uint32_t absent = v < v1 ? 0u : 0xFFu;
-        for (int q = 0; q < p.n_sup; ++q) {
-          const int64_t off = p.sup[q] - id;
-          if (off >= 0 && off < EPV) absent |= 1u << off;
-        }
-#pragma unroll
-        for (int e = 0; e < EPV; ++e)
-          offer(no_nan(element<BYTES>(x, e)), static_cast<uint32_t>(id) + e, !((absent >> e) & 1u));
+    const int nb = n_chosen << shift;
+    for (int c = warp; c < nb; c += kScoreWarps) {
+      const int blk = (static_cast<int>(chosen[c >> shift]) << shift) + (c & ((1 << shift) - 1));
+      if (blk >= blocks) continue;
+      const int v = blk * 32 + lane;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (v < nv) x = vecs[v0 + v];
+      const int64_t id = id_base + static_cast<int64_t>(v) * EPV;
+      uint32_t absent = v < nv ? 0u : 0xFFu;
+      for (int q = 0; q < p.n_sup; ++q) {
+        const int64_t off = p.sup[q] - id;
+        if (off >= 0 && off < EPV) absent |= 1u << off;
       }
+#pragma unroll
+      for (int e = 0; e < EPV; ++e)
+        offer(no_nan(element<BYTES>(x, e)), static_cast<uint32_t>(id) + e, !((absent >> e) & 1u));
     }
     cut();
   }
