@@ -328,16 +328,11 @@ __device__ __forceinline__ bool next_segment(const AttendParams& p, Cursor& c, u
   return true;
 }
 
-// One warp: the tiles of one head and row tile of the batch rows before `upto`,
-// and of all of them, in every lane.
-__device__ __forceinline__ uint2 tiles_before(const AttendParams& p, int64_t upto) {
-  uint32_t sum = 0, all = 0;
-  for (int64_t b = threadIdx.x & 31; b < p.B; b += 32) {
-    const uint32_t t = static_cast<uint32_t>(tiles_of(p, b));
-    all += t;
-    if (b < upto) sum += t;
-  }
-  return make_uint2(__reduce_add_sync(0xFFFFFFFFu, sum), __reduce_add_sync(0xFFFFFFFFu, all));
+// One warp: the tiles of one head and row tile of all batch rows, in every lane.
+__device__ __forceinline__ uint32_t all_tiles(const AttendParams& p) {
+  uint32_t all = 0;
+  for (int64_t b = threadIdx.x & 31; b < p.B; b += 32) all += static_cast<uint32_t>(tiles_of(p, b));
+  return __reduce_add_sync(0xFFFFFFFFu, all);
 }
 
 // ---------------------------------------------------------------------------
@@ -575,16 +570,13 @@ __device__ __forceinline__ uint32_t query_offset(int r, int e) {
   return static_cast<uint32_t>(r * D + ((D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) << 4) + (e & 1) * 8);
 }
 
-// One warp: the CTA's range of tiles and where it begins, into sh.
-template <class SH>
-__device__ __forceinline__ void plan_range(const AttendParams& p, SH& sh) {
+// One warp: the batch row that holds tile w (p.B when there is none), and the
+// tiles before that row; hr = heads times row tiles.
+__device__ __forceinline__ void find_row(const AttendParams& p, uint32_t hr, uint32_t w, int32_t& b, uint32_t& before) {
   const int lane = threadIdx.x & 31;
-  const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
-  const Split split(tiles_before(p, 0).y * hr, gridDim.x);
-  const uint32_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
-  uint32_t before = 0;
-  int32_t b = 0;
-  while (b < p.B) {                                  // 32 batch rows at a time
+  before = 0;
+  b = 0;
+  while (b < p.B) {                                    // 32 batch rows at a time
     const uint32_t t = b + lane < p.B ? tiles_of(p, b + lane) * hr : 0;
     uint32_t inc = t;
 #pragma unroll
@@ -592,17 +584,28 @@ __device__ __forceinline__ void plan_range(const AttendParams& p, SH& sh) {
       const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= o) inc += u;
     }
-    const unsigned in = __ballot_sync(0xFFFFFFFFu, b + lane < p.B && before + inc > w0);
+    const unsigned in = __ballot_sync(0xFFFFFFFFu, b + lane < p.B && before + inc > w);
     if (in != 0u) {
       const int l = __ffs(in) - 1;
       before += __shfl_sync(0xFFFFFFFFu, inc - t, l);
       b += l;
-      break;
+      return;
     }
     before += __shfl_sync(0xFFFFFFFFu, inc, 31);
     b += 32;
   }
-  if (lane == 0) {
+}
+
+// One warp: the CTA's range of tiles and where it begins, into sh.
+template <class SH>
+__device__ __forceinline__ void plan_range(const AttendParams& p, SH& sh) {
+  const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
+  const Split split(all_tiles(p) * hr, gridDim.x);
+  const uint32_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
+  uint32_t before;
+  int32_t b;
+  find_row(p, hr, w0, b, before);
+  if ((threadIdx.x & 31) == 0) {
     sh.w0 = w0;
     sh.w1 = w1;
     sh.b0 = b;
@@ -1111,8 +1114,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 constexpr int kWeightCols = 64;        // rows (columns of a product) of a job
 constexpr int kWeightRows = 512;       // rows of a launch: what the queries' shared memory holds
 constexpr int kWeightStages = 5;       // of the K ring
-constexpr int kWeightBufs = 4;         // score buffers of a group
-// The products run up to 2 x 4 tiles ahead of the softmax and the copies 5
+constexpr int kWeightGroups = 4;
+constexpr int kWeightSoft = 4 * kWeightGroups, kWeightCopyWarp = kWeightSoft, kWeightMmaWarp = kWeightSoft + 1;
+constexpr int kWeightThreads = (kWeightSoft + 2) * 32;
+constexpr int kWeightBufs = 2;         // score buffers of a group
+// The products run up to 4 x 2 tiles ahead of the softmax and the copies 5
 // ahead of the products: a tile's meta slot is free again after 16.
 constexpr int kWeightMeta = 16;
 
@@ -1123,7 +1129,7 @@ constexpr int weights_smem(int dim, int chunks) {
 struct WeightShared {
   uint64_t kfull[kWeightStages], kempty[kWeightStages];
   uint64_t mfull[kWeightMeta];
-  uint64_t sfull[2 * kWeightBufs], sempty[2 * kWeightBufs];
+  uint64_t sfull[kWeightGroups * kWeightBufs], sempty[kWeightGroups * kWeightBufs];
   uint64_t qfull;
   TileMeta meta[kWeightMeta];
   alignas(16) float f[kWeightRows], nm[kWeightRows];   // query scales, minus the rows' lse (log2 units)
@@ -1136,13 +1142,13 @@ struct WeightShared {
 
 // w[j] = decay w[j] + sum over the rows of exp(s - lse): S^T as in the
 // attention, a thread per token, so a token's sum stays in its thread and
-// nothing is shared or added atomically.  The two groups take the tiles
-// alternately; a job is one tile and up to 64 rows, with 4 score buffers a
-// group, so the products run ahead.
+// nothing is shared or added atomically.  Four groups of 4 warps take the tiles
+// in turn; a job is one tile and up to 64 rows, with 2 score buffers a group, so
+// the products run ahead.
 // Bound: the products (8 of M 128, N 64, K 32 for a job), since each row's
 // scores are computed twice over the attention's; K's bytes when rows are few.
 template <int D>
-__global__ void __launch_bounds__(kAttendThreads, 1) attend_weights_kernel(const __grid_constant__ AttendParams p,
+__global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const __grid_constant__ AttendParams p,
                                                                            int32_t first_row, int32_t rows) {
   constexpr int ST = kWeightStages, NC = kWeightCols;
   constexpr int kTileBytes = kTile * D;
@@ -1161,15 +1167,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_weights_kernel(const
       mbar_init(smem_addr(&sh.kempty[i]), 1);
     }
     for (int i = 0; i < kWeightMeta; ++i) mbar_init(smem_addr(&sh.mfull[i]), 1);
-    for (int i = 0; i < 2 * kWeightBufs; ++i) {
+    for (int i = 0; i < kWeightGroups * kWeightBufs; ++i) {
       mbar_init(smem_addr(&sh.sfull[i]), 1);
       mbar_init(smem_addr(&sh.sempty[i]), 4);
     }
-    mbar_init(smem_addr(&sh.qfull), kSoftWarps);
+    mbar_init(smem_addr(&sh.qfull), kWeightSoft);
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kWeightMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
                  "r"(kTmemCols)
                  : "memory");
@@ -1201,26 +1207,27 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_weights_kernel(const
   Cursor cur{sh.w0, sh.w1, sh.b0, sh.off0};
   Segment sg;
   uint32_t g = 0;                                      // tiles this CTA has passed
-  if (warp == kCopyWarp) {
+  if (warp == kWeightCopyWarp) {
     copy_role<D, ST, false>(p, sh, cur, k_s, 0, wait);
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kWeightMmaWarp) {
     constexpr uint32_t kHiK = at_desc_hi(8 * D, kSwz);
     const uint32_t lead = elect_one();
     const uint32_t kd = at_desc_lo(k_s, 16), qd = at_desc_lo(q_s, 16);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     uint32_t ks = 0, kp = 0;
-    uint32_t jobs[2] = {0, 0};                         // of either group
+    uint32_t jobs = 0;                                 // of a group, when all have passed as many tiles
     uint32_t seg = 0;
     while (next_segment(p, cur, sh.w0, sg)) {
       const uint32_t n = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(sg.t1 - sg.t0), 0);
       wait(sh.qfull, seg & 1u, kFaultFullWait);
       __syncwarp();
       for (uint32_t i = 0; i < n; ++i, ++g) {
-        const uint32_t grp = g & 1u;
+        const uint32_t grp = g % kWeightGroups;
+        jobs = g / kWeightGroups * static_cast<uint32_t>(chunks);
         wait(sh.kfull[ks], kp, kFaultFullWait);
         __syncwarp();
         for (int c = 0; c < chunks; ++c) {
-          const uint32_t j = grp ? jobs[1]++ : jobs[0]++;
+          const uint32_t j = jobs + static_cast<uint32_t>(c);
           const uint32_t buf = grp * kWeightBufs + j % kWeightBufs;
           wait(sh.sempty[buf], ((j / kWeightBufs) & 1u) ^ 1u, kFaultEmptyWait);
           __syncwarp();
@@ -1247,40 +1254,49 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_weights_kernel(const
       }
       ++seg;
     }
-  } else if (warp < kSoftWarps) {
+  } else if (warp < kWeightSoft) {
     const int grp = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const int page_of = key / p.c.page_size;
-    constexpr int kPer = D / 8, kStep = kSoftWarps * 32 / kPer;
+    constexpr int kPer = D / 8, kStep = kWeightSoft * 32 / kPer;
     uint32_t jobs = 0;                                 // this group's
     while (next_segment(p, cur, sh.w0, sg)) {
-      named_sync(3, kSoftWarps * 32);                  // (the previous segment's rows are no longer read)
+      named_sync(5, kWeightSoft * 32);                  // (the previous segment's rows are no longer read)
       const int e = threadIdx.x % kPer;
-#pragma unroll 4
-      for (int r = threadIdx.x / kPer; r < chunks * NC; r += kStep) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        float nm = -kInf;
-        if (r < rows) {
-          const int l = (first_row + r) / p.G, hq = sg.h * p.G + (first_row + r) % p.G;
-          x = *reinterpret_cast<const uint4*>(p.q + sg.b * p.qb + l * p.ql + hq * p.qh + e * 16);
-          const float lse = p.lse[(sg.b * p.L + l) * p.Hq + hq];
-          if (fabsf(lse) < kInf) nm = -lse * kLog2e;   // (other rows add nothing)
+      for (int rb = threadIdx.x / kPer; rb < chunks * NC; rb += 4 * kStep) {   // (whole warps)
+        uint4 x[4];
+        float nm[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = rb + i * kStep;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          nm[i] = -kInf;
+          if (r < rows) {
+            const int l = (first_row + r) / p.G, hq = sg.h * p.G + (first_row + r) - l * p.G;
+            x[i] = *reinterpret_cast<const uint4*>(p.q + sg.b * p.qb + l * p.ql + hq * p.qh + e * 16);
+            nm[i] = -p.lse[(sg.b * p.L + l) * p.Hq + hq] * kLog2e;
+          }
         }
-        uint32_t hi[2], lo[2];
-        const float s = split_query<D>(x, hi, lo);
-        const uint32_t at = q_s + static_cast<uint32_t>(r / NC * 2 * NC * D) + query_offset<D>(r % NC, e);
-        sts64(at, hi[0], hi[1]);
-        sts64(at + NC * D, lo[0], lo[1]);
-        if (e == 0) {
-          sh.f[r] = s;
-          sh.nm[r] = nm;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = rb + i * kStep;
+          if (r >= chunks * NC) break;
+          uint32_t hi[2], lo[2];
+          const float s = split_query<D>(x[i], hi, lo);
+          const uint32_t at = q_s + static_cast<uint32_t>(r / NC * 2 * NC * D) + query_offset<D>(r % NC, e);
+          sts64(at, hi[0], hi[1]);
+          sts64(at + NC * D, lo[0], lo[1]);
+          if (e == 0) {
+            sh.f[r] = s;
+            sh.nm[r] = fabsf(nm[i]) < kInf ? nm[i] : -kInf;   // (a row whose lse is not finite adds nothing)
+          }
         }
       }
       at_fence_async();
-      named_sync(3, kSoftWarps * 32);
+      named_sync(5, kWeightSoft * 32);
       if (lane == 0) mbar_arrive(smem_addr(&sh.qfull));
       for (int ti = sg.t0; ti < sg.t1; ++ti, ++g) {
-        if ((g & 1u) != static_cast<uint32_t>(grp)) continue;
+        if (g % kWeightGroups != static_cast<uint32_t>(grp)) continue;
         float* wj = p.weights + (static_cast<int64_t>(sg.b) * p.c.heads + sg.h) * p.cap +
                     static_cast<int64_t>(ti) * kTile + key;
         const bool in = static_cast<int64_t>(ti) * kTile + key < p.cap;
@@ -1332,79 +1348,88 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_weights_kernel(const
     for (int64_t i = blockIdx.x; i < bh; i += gridDim.x) {
       float* w = p.weights + i * p.cap;
       for (int64_t j = static_cast<int64_t>(tiles_of(p, i / p.c.heads)) * kTile + threadIdx.x; j < p.cap;
-           j += kSoftWarps * 32)
+           j += kWeightSoft * 32)
         w[j] = p.decay == 0.0f ? 0.0f : p.decay * w[j];
     }
   }
   at_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kWeightMmaWarp) {
     at_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 
-// One warp per output row: joins the parts of the items that several CTAs
-// share, in CTA order (a part's reference may differ from the others').
+// Joins the parts of the items that several CTAs share, in CTA order (a part's
+// reference may differ from the others').  Block (x, y) looks at the boundary
+// between CTAs x and x + 1: if an item is cut there for the first time, its
+// warps join rows 8 y .. 8 y + 7 of it, one each.
+constexpr int kJoinRows = 8;
 template <int D>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int N, int columns) {
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p, int N, int columns) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int32_t row = static_cast<int32_t>(blockIdx.x * 4 + (threadIdx.x >> 5));
-  if (row >= static_cast<int32_t>(p.B) * p.rows * p.c.heads) return;
-  const int32_t Hq = static_cast<int32_t>(p.Hq), L = static_cast<int32_t>(p.L);
-  const int32_t hq = row % Hq, bl = row / Hq, l = bl % L, b = bl / L;
-  const int32_t h = hq / p.G, rr = l * p.G + hq % p.G;
-  const int32_t rt = rr / p.tile_rows, in = rr % p.tile_rows;
-  const int n = in / p.half * columns + in % p.half;   // the row's column (columns: of a softmax group)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
-  const uint2 tiles = tiles_before(p, b);
-  const Split split(tiles.y * hr, static_cast<uint32_t>(p.ctas));
+  const uint32_t total = all_tiles(p) * hr;
+  const Split split(total, static_cast<uint32_t>(p.ctas));
+  const uint32_t w = split.begin(blockIdx.x + 1);
+  if (w >= total) return;
+  int32_t b;
+  uint32_t before;
+  find_row(p, hr, w, b, before);
   const uint32_t T = static_cast<uint32_t>(tiles_of(p, b));
-  const uint32_t i0 = tiles.x * hr + static_cast<uint32_t>(h * p.row_tiles + rt) * T;   // the item's tiles: [i0, i0 + T)
+  const uint32_t item = (w - before) / T, i0 = before + item * T;   // the item's tiles: [i0, i0 + T)
+  if (i0 == w) return;                                 // the boundary lies between two items
   const uint32_t ca = split.owner(i0), cb = split.owner(i0 + T - 1);
-  if (ca == cb) return;                                // written whole
-  // CTA ca's part is its last segment unless the item begins its range; the
-  // others' is their first.  The statistics of 32 parts are read at a time.
-  const bool late = split.begin(ca) < i0;
-  auto slot_of = [&](uint32_t c) { return static_cast<int64_t>(2 * c + (c == ca && late ? 1 : 0)); };
-  float m = kUnset, sum = 0.0f;
-  float o[D / 32] = {};
-  for (uint32_t c0 = ca; c0 <= cb; c0 += 32) {
-    const uint32_t c = c0 + lane;
-    float mc = -kInf, lc = 0.0f;
-    if (c <= cb) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(c) * N + n);
-      mc = ml.x;
-      lc = ml.y;
-    }
-    const float now = fmaxf(m, warp_max_f32(mc));
-    const float fa = ex2_approx(m - now), fb = ex2_approx(mc - now);
-    float add = lc * fb;
+  if (ca != blockIdx.x) return;                        // cut before already
+  const int h = static_cast<int>(item) / p.row_tiles, row0 = static_cast<int>(item) % p.row_tiles * p.tile_rows;
+  const int nrows = min(p.tile_rows, p.rows - row0);
+  for (int in = blockIdx.y * kJoinRows + warp; in < min(nrows, static_cast<int>(blockIdx.y + 1) * kJoinRows); in += 8) {
+    const int rr = row0 + in, l = rr / p.G;
+    const int64_t row = (b * p.L + l) * p.Hq + h * p.G + rr % p.G;
+    const int n = in / p.half * columns + in % p.half;   // the row's column (columns: of a softmax group)
+    // CTA ca's part is its last segment unless the item begins its range; the
+    // others' is their first.  The statistics of 32 parts are read at a time.
+    const bool late = split.begin(ca) < i0;
+    auto slot_of = [&](uint32_t c) { return static_cast<int64_t>(2 * c + (c == ca && late ? 1 : 0)); };
+    float m = kUnset, sum = 0.0f;
+    float o[D / 32] = {};
+    for (uint32_t c0 = ca; c0 <= cb; c0 += 32) {
+      const uint32_t c = c0 + lane;
+      float mc = -kInf, lc = 0.0f;
+      if (c <= cb) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(c) * N + n);
+        mc = ml.x;
+        lc = ml.y;
+      }
+      const float now = fmaxf(m, warp_max_f32(mc));
+      const float fa = ex2_approx(m - now), fb = ex2_approx(mc - now);
+      float add = lc * fb;
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, k);
-    sum = sum * fa + add;
+      for (int k = 16; k > 0; k >>= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, k);
+      sum = sum * fa + add;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] *= fa;
-    const int parts = static_cast<int>(cb - c0 + 1 < 32 ? cb - c0 + 1 : 32);
+      for (int i = 0; i < D / 32; ++i) o[i] *= fa;
+      const int parts = static_cast<int>(cb - c0 + 1 < 32 ? cb - c0 + 1 : 32);
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float f = __shfl_sync(0xFFFFFFFFu, fb, k);
-      const float* src = p.part_o + (slot_of(c0 + k) * N + n) * D + lane;
+      for (int k = 0; k < parts; ++k) {
+        const float f = __shfl_sync(0xFFFFFFFFu, fb, k);
+        const float* src = p.part_o + (slot_of(c0 + k) * N + n) * D + lane;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(__ldcg(src + i * 32), f, o[i]);
+        for (int i = 0; i < D / 32; ++i) o[i] = fmaf(__ldcg(src + i * 32), f, o[i]);
+      }
+      m = now;
     }
-    m = now;
-  }
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    uint16_t u;
-    const float y = sum == 0.0f ? 0.0f : o[i] / sum;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(y));
-    p.out[static_cast<int64_t>(row) * D + i * 32 + lane] = u;
+    for (int i = 0; i < D / 32; ++i) {
+      uint16_t u;
+      const float y = sum == 0.0f ? 0.0f : o[i] / sum;
+      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(y));
+      p.out[row * D + i * 32 + lane] = u;
+    }
+    if (lane == 0) p.lse[row] = sum == 0.0f ? -kInf : m * kLn2 + logf(sum);
   }
-  if (lane == 0) p.lse[row] = sum == 0.0f ? -kInf : m * kLn2 + logf(sum);
 }
 
 }  // namespace dllm
@@ -1603,9 +1628,11 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
   if (st != DLLM_OK) return st;
   int columns = rt.columns, per_group = rt.columns == 128 ? 64 : rt.columns;
   void* jargs[] = {&p, &columns, &per_group};
-  st = launch_pdl(d64 ? reinterpret_cast<const void*>(&attend_join_kernel<64>)
-                      : reinterpret_cast<const void*>(&attend_join_kernel<128>),
-                  dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, jargs);
+  if (ctas > 1)
+    st = launch_pdl(d64 ? reinterpret_cast<const void*>(&attend_join_kernel<64>)
+                        : reinterpret_cast<const void*>(&attend_join_kernel<128>),
+                    dim3(static_cast<unsigned>(ctas - 1), static_cast<unsigned>((rt.rows + kJoinRows - 1) / kJoinRows)),
+                    dim3(256), 0, stream, jargs);
   if (st != DLLM_OK || !weights) return st;
   // The weights: kWeightRows rows of a key head at a time, K read once for each.
   p.row_tiles = 1;
@@ -1617,7 +1644,7 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
                         : reinterpret_cast<const void*>(&attend_weights_kernel<128>),
                     dim3(static_cast<unsigned>(std::min<int64_t>(
                         dev->sms, B * cache->heads * ((cap + kTile - 1) / kTile)))),
-                    dim3(kAttendThreads), static_cast<size_t>(weights_smem(cache->head_dim, chunks)), stream, wargs);
+                    dim3(kWeightThreads), static_cast<size_t>(weights_smem(cache->head_dim, chunks)), stream, wargs);
     p.decay = 1.0f;
   }
   return st;

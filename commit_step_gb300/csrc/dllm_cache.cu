@@ -289,17 +289,17 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
 
 constexpr int kMoveVec = 4;  // 16-byte vectors (16 codes of one token) a thread holds
 
-// One block per (destination page column, head, batch row x {keys, values}):
-// gathers the kept tokens of the page (one read), finds their largest value,
-// writes them under the page's new scale.
+// One block per (destination page column, head, batch row): gathers the kept
+// tokens' keys and values of the page (one read; the chain position -> page ->
+// codes is walked once for both, and their bytes are in flight together), finds
+// either's largest value, writes them under the page's new scales.
 // Bound: one byte read and one written for each element that stays.
 template <int D>
-__global__ void __launch_bounds__(256, 4) evict_move_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ float red[8];
+__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ float red[2][8];
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t b = blockIdx.z >> 1;
-  const int kv = blockIdx.z & 1;
+  const int64_t b = blockIdx.z;
   const int h = blockIdx.y;
   const int ps = p.c.page_size;
   const int n = seq_len(p.lens, b, p.cap);
@@ -309,71 +309,93 @@ __global__ void __launch_bounds__(256, 4) evict_move_kernel(const __grid_constan
   if (here <= 0) return;
   const int64_t to = page_at(p.dst_table, p.dst_width, b, blockIdx.x, p.c.pages);
   if (to < 0) return;
-  const uint8_t* pool = kv ? p.c.v : p.c.k;
-  const float* scales = kv ? p.c.v_scale : p.c.k_scale;
   const int32_t* keep = p.keep + (b * p.c.heads + h) * static_cast<int64_t>(p.budget) + lo;
   constexpr int per_token = D / 16;
-  uint4 x[kMoveVec];
-  float sc[kMoveVec];
-  float amax = 0.0f;
+  int64_t at[kMoveVec];                                          // (page, head) and slot of the token, or -1
+  int j[kMoveVec];
 #pragma unroll
   for (int i = 0; i < kMoveVec; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
-    const int slot = v / per_token, d = (v % per_token) * 16;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    sc[i] = 0.0f;
-    if (slot < here) {
-      const int j = keep[slot];
-      const int64_t page = page_at(p.table, p.width, b, j / ps, p.c.pages);
-      if (page >= 0) {                                           // a token on no page reads as zeros
-        const int64_t at = page * p.c.heads + h;
-        x[i] = __ldg(reinterpret_cast<const uint4*>(pool + (at * ps + j % ps) * D + d));
-        sc[i] = scales[at];
-      }
-    }
+    const int slot = (i * blockDim.x + threadIdx.x) / per_token;
+    j[i] = slot < here ? keep[slot] : -1;
   }
 #pragma unroll
   for (int i = 0; i < kMoveVec; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t top = 0;                                            // largest magnitude code: codes order as values
+    at[i] = -1;
+    if (j[i] >= 0) {
+      const int64_t page = page_at(p.table, p.width, b, j[i] / ps, p.c.pages);
+      if (page >= 0) at[i] = page * p.c.heads + h;               // (a token on no page reads as zeros)
+    }
+  }
+  uint4 x[2][kMoveVec];
+  float sc[2][kMoveVec];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+  for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t c = (w[q] >> (8 * e)) & 0x7Fu;
-        top = max(top, c < 0x7Fu ? c : 0u);                      // NaN does not set the scale
+    for (int i = 0; i < kMoveVec; ++i) {
+      x[kv][i] = make_uint4(0u, 0u, 0u, 0u);
+      sc[kv][i] = 0.0f;
+      if (at[i] >= 0) {
+        const int d = ((i * blockDim.x + threadIdx.x) % per_token) * 16;
+        x[kv][i] = __ldg(reinterpret_cast<const uint4*>((kv ? p.c.v : p.c.k) + (at[i] * ps + j[i] % ps) * D + d));
+        sc[kv][i] = (kv ? p.c.v_scale : p.c.k_scale)[at[i]];
       }
     }
-    float v, unused;
-    f16x2_to_f32(e4m3x2_to_f16x2(top), v, unused);
-    const float y = __fmul_rn(v, sc[i]);
-    if (y < __int_as_float(0x7F800000)) amax = fmaxf(amax, y);
-  }
-  const float s = block_scale(block_max(amax, red));
-  if (threadIdx.x == 0) (kv ? p.c.v_scale : p.c.k_scale)[to * p.c.heads + h] = s;
-  uint8_t* out = const_cast<uint8_t*>(pool) + (to * p.c.heads + h) * ps * D;
+  float s[2];
 #pragma unroll
-  for (int i = 0; i < kMoveVec; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
-    const int slot = v / per_token, d = (v % per_token) * 16;
-    if (slot >= here) continue;
-    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    if (sc[i] != s) {
-      const float inv = power_of_two(s) ? 1.0f / s : 0.0f;
+  for (int kv = 0; kv < 2; ++kv) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMoveVec; ++i) {
+      const uint32_t w[4] = {x[kv][i].x, x[kv][i].y, x[kv][i].z, x[kv][i].w};
+      uint32_t top = 0;                                          // largest magnitude code: codes order as values
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float f[4];
-        f16x2_to_f32(e4m3x2_to_f16x2(w[q] & 0xFFFFu), f[0], f[1]);
-        f16x2_to_f32(e4m3x2_to_f16x2(w[q] >> 16), f[2], f[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y = __fmul_rn(f[e], sc[i]);
-          f[e] = inv != 0.0f ? y * inv : __fdiv_rn(y, s);
+          const uint32_t c = (w[q] >> (8 * e)) & 0x7Fu;
+          top = max(top, c < 0x7Fu ? c : 0u);                    // NaN does not set the scale
         }
-        w[q] = e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16;
       }
+      float v, unused;
+      f16x2_to_f32(e4m3x2_to_f16x2(top), v, unused);
+      const float y = __fmul_rn(v, sc[kv][i]);
+      if (y < __int_as_float(0x7F800000)) amax = fmaxf(amax, y);
     }
-    *reinterpret_cast<uint4*>(out + slot * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
+    s[kv] = warp_max_f32(amax);
+    if ((threadIdx.x & 31) == 0) red[kv][threadIdx.x >> 5] = s[kv];
+  }
+  __syncthreads();
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
+    s[0] = fmaxf(s[0], red[0][w]);
+    s[1] = fmaxf(s[1], red[1][w]);
+  }
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const float scale = block_scale(s[kv]);
+    if (threadIdx.x == 0) (kv ? p.c.v_scale : p.c.k_scale)[to * p.c.heads + h] = scale;
+    uint8_t* out = (kv ? p.c.v : p.c.k) + (to * p.c.heads + h) * ps * D;
+#pragma unroll
+    for (int i = 0; i < kMoveVec; ++i) {
+      if (j[i] < 0) continue;
+      const int v = i * blockDim.x + threadIdx.x;
+      uint32_t w[4] = {x[kv][i].x, x[kv][i].y, x[kv][i].z, x[kv][i].w};
+      if (sc[kv][i] != scale) {
+        const float inv = power_of_two(scale) ? 1.0f / scale : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float f[4];
+          f16x2_to_f32(e4m3x2_to_f16x2(w[q] & 0xFFFFu), f[0], f[1]);
+          f16x2_to_f32(e4m3x2_to_f16x2(w[q] >> 16), f[2], f[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = __fmul_rn(f[e], sc[kv][i]);
+            f[e] = inv != 0.0f ? y * inv : __fdiv_rn(y, scale);
+          }
+          w[q] = e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16;
+        }
+      }
+      *reinterpret_cast<uint4*>(out + static_cast<int64_t>(v) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -475,8 +497,7 @@ dllm_status dllm_cache_evict(const dllm_kv_cache* cache, const int32_t* table, i
   const int64_t cols = (std::min(budget, cap) + ps - 1) / ps;
   return launch_pdl(cache->head_dim == 64 ? reinterpret_cast<const void*>(&evict_move_kernel<64>)
                                           : reinterpret_cast<const void*>(&evict_move_kernel<128>),
-                    dim3(static_cast<unsigned>(cols), static_cast<unsigned>(cache->heads),
-                         static_cast<unsigned>(2 * B)),
+                    dim3(static_cast<unsigned>(cols), static_cast<unsigned>(cache->heads), static_cast<unsigned>(B)),
                     dim3(threads), 0, stream, args);
 }
 
