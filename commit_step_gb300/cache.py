@@ -4,14 +4,14 @@ attending over them, and evicting the least attended (``dllm_cache_append``,
 from __future__ import annotations
 
 import ctypes as C
-import math
 from typing import Optional
 
 import torch
 
-from . import _F32, _I32, _MASK, _arg, _check, _lib, _need_cuda, _ptr, _stream
+from . import _F32, _I32, _MASK, _arg, _check, _lib, _need_cuda
 
 _I64x3 = C.c_int64 * 3
+_BF16 = (torch.bfloat16,)
 
 
 class _CacheStruct(C.Structure):
@@ -58,18 +58,36 @@ class KVCache:
         _arg(v_scale, "v_scale", pages * heads, _F32, k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, head_dim
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
                                     page_size, heads, head_dim)
         self._ref = C.byref(self._struct)
 
 
+def _at(t, name: str, numel: int, dtypes, index: int, device) -> int:
+    """The address of a tensor that passes ``_arg``'s checks (a call's cost on
+    the host is mostly these checks, so the usual case is decided here)."""
+    try:
+        if t.get_device() == index and t.dtype in dtypes and t.numel() == numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if t is None:
+        raise ValueError(f"{name} is needed")
+    _arg(t, name, numel, dtypes, device)
+    raise ValueError(f"{name} is not a tensor this call can use")
+
+
+def _at_or_none(t, name: str, numel: int, dtypes, index: int, device):
+    return None if t is None else _at(t, name, numel, dtypes, index, device)
+
+
 def _table(cache: KVCache, table: torch.Tensor, name: str = "page_table"):
-    """(B, width) of a page table."""
+    """(B, width, address) of a page table."""
     if not torch.is_tensor(table) or table.dim() != 2:
         raise ValueError(f"{name} must be a (B, width) int32 tensor")
-    _arg(table, name, table.numel(), _I32, cache.device)
-    return table.shape
+    B, width = table.shape
+    return B, width, _at(table, name, B * width, _I32, cache.index, cache.device)
 
 
 def _strided(t, name: str, shape, device):
@@ -78,12 +96,13 @@ def _strided(t, name: str, shape, device):
         raise TypeError(f"{name} must be a 4-D bfloat16 tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}; the cache is on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    sb, sl, sh, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
         raise ValueError(f"{name} needs unit stride over its last dimension")
     # (a dimension of one element has no stride that matters)
-    return _I64x3(*[s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])])
+    return _I64x3(sb if shape[0] > 1 else 0, sl if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
 
 
 def _empty(shape, dtype, device, stream):
@@ -94,36 +113,46 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _raw_stream(stream, index: int) -> int:
+    """The stream a call runs on: the given one, or the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
 def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
                  count: Optional[torch.Tensor] = None, stream=None) -> None:
     """Writes the keys and values of L new tokens per sequence, (B, L, heads,
     head_dim) bf16 of any outer strides, at positions start[b] .. start[b] +
     L - 1 (the first count[b] of them when ``count`` is given)."""
-    B, width = _table(cache, page_table)
+    B, width, table = _table(cache, page_table)
     if not torch.is_tensor(k) or k.dim() != 4:
         raise TypeError("k must be a 4-D bfloat16 tensor")
-    shape = (B, k.shape[1], cache.heads, cache.head_dim)
-    ks, vs = _strided(k, "k", shape, cache.device), _strided(v, "v", shape, cache.device)
-    _arg(start, "start", B, _I32, cache.device)
-    _arg(count, "count", B, _I32, cache.device)
-    if start is None:
-        raise ValueError("start is needed")
-    _check(_lib.dllm_cache_append(cache._ref, _ptr(k), _ptr(v), ks, vs, B, k.shape[1], _ptr(page_table), width,
-                                  _ptr(start), _ptr(count), _stream(stream)), "dllm_cache_append")
+    L, dev, idx = k.shape[1], cache.device, cache.index
+    shape = (B, L, cache.heads, cache.head_dim)
+    ks, vs = _strided(k, "k", shape, dev), _strided(v, "v", shape, dev)
+    _check(_lib.dllm_cache_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, B, L, table, width,
+                                  _at(start, "start", B, _I32, idx, dev),
+                                  _at_or_none(count, "count", B, _I32, idx, dev), _raw_stream(stream, idx)),
+           "dllm_cache_append")
 
 
 _WS_AT = {}
 
 
-def _attention_ws(B, L, Hq, cache: KVCache, stream) -> torch.Tensor:
-    need = int(_lib.dllm_cache_attention_workspace_size(B, L, Hq, cache.heads, cache.head_dim))
-    s = torch.cuda.current_stream(cache.device) if stream is None else stream
-    key = (cache.device.index, s.cuda_stream)
-    ws = _WS_AT.get(key)
+_NEED = {}
+
+
+def _attention_ws(B, L, Hq, cache: KVCache, raw: int, stream) -> torch.Tensor:
+    """A workspace for the call, cached per device and stream.  What it has to
+    hold goes by the rows of a key head and the head size alone."""
+    size = (cache.index, L * Hq // cache.heads, cache.head_dim)
+    need = _NEED.get(size)
+    if need is None:
+        need = _NEED[size] = int(_lib.dllm_cache_attention_workspace_size(B, L, Hq, cache.heads, cache.head_dim))
+    ws = _WS_AT.get((cache.index, raw))
     if ws is None or ws.numel() < need:
-        ws = _empty((need,), torch.uint8, cache.device, stream)
+        ws = _empty((max(need, 1 << 16),), torch.uint8, cache.device, stream)
         if not torch.cuda.is_current_stream_capturing():   # (a capture's memory belongs to its graph)
-            _WS_AT[key] = ws
+            _WS_AT[(cache.index, raw)] = ws
     return ws
 
 
@@ -140,35 +169,29 @@ def cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, l
     (B, heads, width * page_size) float32, updated in place to decay * weights
     + the probability each token drew.  ``out``: preallocated (out, lse).
     """
-    B, width = _table(cache, page_table)
+    B, width, table = _table(cache, page_table)
     if not torch.is_tensor(q) or q.dim() != 4:
         raise TypeError("q must be a 4-D bfloat16 tensor")
     L, Hq = q.shape[1], q.shape[2]
-    dev = cache.device
-    strides = _strided(q, "q", (B, L, Hq, cache.head_dim), dev)
+    dev, idx, heads, D = cache.device, cache.index, cache.heads, cache.head_dim
+    strides = _strided(q, "q", (B, L, Hq, D), dev)
     cap = width * cache.page_size
-    if lens is None:
-        raise ValueError("lens is needed")
-    _arg(lens, "lens", B, _I32, dev)
-    mask_stride = 0
-    if key_mask is not None:
-        _arg(key_mask, "key_mask", B * cap, _MASK, dev)
-        mask_stride = cap
-    _arg(weights, "weights", B * cache.heads * cap, _F32, dev)
     if out is None:
-        o, lse = _empty((B, L, Hq, cache.head_dim), torch.bfloat16, dev, stream), \
-            _empty((B, L, Hq), torch.float32, dev, stream)
+        o, lse = _empty((B, L, Hq, D), torch.bfloat16, dev, stream), _empty((B, L, Hq), torch.float32, dev, stream)
+        out_at, lse_at = o.data_ptr(), lse.data_ptr()
     else:
         o, lse = out
-        _arg(o, "out", B * L * Hq * cache.head_dim, (torch.bfloat16,), dev)
-        _arg(lse, "lse", B * L * Hq, _F32, dev)
+        out_at = _at(o, "out", B * L * Hq * D, _BF16, idx, dev)
+        lse_at = _at(lse, "lse", B * L * Hq, _F32, idx, dev)
+    raw = _raw_stream(stream, idx)
     if ws is None:
-        ws = _attention_ws(B, L, Hq, cache, stream)
-    _check(_lib.dllm_cache_attention(cache._ref, _ptr(q), strides, B, L, Hq, _ptr(page_table), width, _ptr(lens),
-                                     _ptr(key_mask), mask_stride,
-                                     1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), _ptr(o),
-                                     _ptr(lse), _ptr(weights), float(decay), _ptr(ws), ws.numel(), _stream(stream)),
-           "dllm_cache_attention")
+        ws = _attention_ws(B, L, Hq, cache, raw, stream)
+    _check(_lib.dllm_cache_attention(cache._ref, q.data_ptr(), strides, B, L, Hq, table, width,
+                                     _at(lens, "lens", B, _I32, idx, dev),
+                                     _at_or_none(key_mask, "key_mask", B * cap, _MASK, idx, dev),
+                                     0 if key_mask is None else cap, D ** -0.5 if scale is None else scale, out_at,
+                                     lse_at, _at_or_none(weights, "weights", B * heads * cap, _F32, idx, dev), decay,
+                                     ws.data_ptr(), ws.numel(), raw), "dllm_cache_attention")
     return o, lse
 
 
@@ -180,25 +203,20 @@ def cache_evict(cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor, we
     Returns (keep (B, heads, budget) int32: the old positions in order, -1
     behind the last; lens (B) int32; weights like ``weights``, moved along).
     ``out``: those three, preallocated."""
-    B, width = _table(cache, page_table)
-    B2, dst_width = _table(cache, dst_table, "dst_table")
+    B, width, table = _table(cache, page_table)
+    B2, dst_width, dst = _table(cache, dst_table, "dst_table")
     if B2 != B:
         raise ValueError("page_table and dst_table must have one row per sequence")
-    budget, dev = int(budget), cache.device
-    cap = width * cache.page_size
-    if lens is None or weights is None:
-        raise ValueError("lens and weights are needed")
-    _arg(lens, "lens", B, _I32, dev)
-    _arg(weights, "weights", B * cache.heads * cap, _F32, dev)
+    budget, dev, idx, heads = int(budget), cache.device, cache.index, cache.heads
+    cap, kept = width * cache.page_size, max(budget, 0)
     if out is None:
-        out = (_empty((B, cache.heads, max(budget, 0)), torch.int32, dev, stream),
-               _empty((B,), torch.int32, dev, stream),
-               _empty((B, cache.heads, cap), torch.float32, dev, stream))
+        out = (_empty((B, heads, kept), torch.int32, dev, stream), _empty((B,), torch.int32, dev, stream),
+               _empty((B, heads, cap), torch.float32, dev, stream))
     keep, lens_out, weights_out = out
-    _arg(keep, "keep", B * cache.heads * max(budget, 0), _I32, dev)
-    _arg(lens_out, "lens_out", B, _I32, dev)
-    _arg(weights_out, "weights_out", B * cache.heads * cap, _F32, dev)
-    _check(_lib.dllm_cache_evict(cache._ref, _ptr(page_table), width, _ptr(lens), B, _ptr(weights), budget,
-                                 int(keep_first), int(keep_last), _ptr(dst_table), dst_width, _ptr(keep),
-                                 _ptr(lens_out), _ptr(weights_out), _stream(stream)), "dllm_cache_evict")
+    _check(_lib.dllm_cache_evict(cache._ref, table, width, _at(lens, "lens", B, _I32, idx, dev), B,
+                                 _at(weights, "weights", B * heads * cap, _F32, idx, dev), budget, int(keep_first),
+                                 int(keep_last), dst, dst_width, _at(keep, "keep", B * heads * kept, _I32, idx, dev),
+                                 _at(lens_out, "lens_out", B, _I32, idx, dev),
+                                 _at(weights_out, "weights_out", B * heads * cap, _F32, idx, dev),
+                                 _raw_stream(stream, idx)), "dllm_cache_evict")
     return keep, lens_out, weights_out

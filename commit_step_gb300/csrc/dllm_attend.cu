@@ -66,6 +66,7 @@ struct AttendParams {
   int32_t tile_rows;           // rows per row tile (the last may hold fewer)
   int32_t half;                // rows of a softmax group: tile_rows, or half of them when the groups are paired
   int32_t ctas;
+  int32_t seg_cost;            // what an item costs besides its tiles, in tiles
   float* part_o;               // (2 ctas, columns, D): a CTA's unfinished first and last segment
   float* part_ml;              // (2 ctas, columns, 2)
   int32_t* fault;
@@ -271,22 +272,28 @@ __device__ __forceinline__ bool group_any(uint32_t id, bool p) {
 // ---------------------------------------------------------------------------
 // the partition of the work
 // ---------------------------------------------------------------------------
-// The tiles of all (batch row, key head, row tile) items, in that order, are
-// dealt to the CTAs in equal contiguous ranges, so ragged batches and few long
-// sequences load every SM alike.  A CTA's range cuts at most its first and its
-// last item short; those parts are joined afterwards in CTA order.
+// The work of all (batch row, key head, row tile) items, in that order, is dealt
+// to the CTAs in equal contiguous ranges, so ragged batches and few long
+// sequences load every SM alike.  It is counted in units: an item is as many
+// units as it has tiles, preceded by seg_cost units for what an item costs
+// whatever its length (loading its queries, writing its rows).  A CTA's range
+// cuts at most its first and its last item short; those parts are joined
+// afterwards in CTA order.
 __device__ __forceinline__ int tiles_of(const AttendParams& p, int64_t b) {
   const int n = attend_len(p, b);
   return n > 0 ? (n + kTile - 1) / kTile : 1;  // (an empty sequence still has its zeros written)
 }
+__device__ __forceinline__ uint32_t units_of(const AttendParams& p, int64_t b) {
+  return static_cast<uint32_t>(tiles_of(p, b) + p.seg_cost);
+}
 
-// CTA c's range begins at tile c q + min(c, r), q = total / ctas, r = total mod
+// CTA c's range begins at unit c q + min(c, r), q = total / ctas, r = total mod
 // ctas (the host keeps totals below 2^31).
 struct Split {
   uint32_t q, r;
   __device__ __forceinline__ Split(uint32_t total, uint32_t ctas) : q(total / ctas), r(total % ctas) {}
   __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * q + min(c, r); }
-  // The CTA that holds a tile.
+  // The CTA that holds a unit.
   __device__ __forceinline__ uint32_t owner(uint32_t w) const {
     const uint32_t wide = r * (q + 1);
     return w < wide ? w / (q + 1) : r + (w - wide) / max(q, 1u);
@@ -294,9 +301,9 @@ struct Split {
 };
 
 struct Cursor {
-  uint32_t w, w1;  // position and end of the CTA's range
+  uint32_t w, w1;  // position and end of the CTA's range, in units
   int32_t b;       // batch row at w
-  uint32_t off;    // position within the batch row's tiles
+  uint32_t off;    // position within the batch row's units
 };
 
 struct Segment {
@@ -308,30 +315,35 @@ struct Segment {
   bool starts_range;
 };
 
+// The next part of an item that has tiles in the CTA's range.
 __device__ __forceinline__ bool next_segment(const AttendParams& p, Cursor& c, uint32_t w0, Segment& s) {
-  if (c.w >= c.w1) return false;
-  s.b = c.b;
-  s.len = attend_len(p, c.b);
-  s.T = s.len > 0 ? (s.len + kTile - 1) / kTile : 1;
-  const uint32_t hr = c.off / static_cast<uint32_t>(s.T);
-  s.h = static_cast<int32_t>(hr / static_cast<uint32_t>(p.row_tiles));
-  s.rt = static_cast<int32_t>(hr % static_cast<uint32_t>(p.row_tiles));
-  s.t0 = static_cast<int32_t>(c.off % static_cast<uint32_t>(s.T));
-  s.t1 = static_cast<int32_t>(min(static_cast<uint32_t>(s.T), s.t0 + (c.w1 - c.w)));
-  s.starts_range = c.w == w0;
-  c.w += s.t1 - s.t0;
-  c.off += s.t1 - s.t0;
-  if (c.off == static_cast<uint32_t>(p.c.heads * p.row_tiles) * s.T) {
-    ++c.b;
-    c.off = 0;
+  while (c.w < c.w1) {
+    s.b = c.b;
+    s.len = attend_len(p, c.b);
+    s.T = s.len > 0 ? (s.len + kTile - 1) / kTile : 1;
+    const uint32_t units = static_cast<uint32_t>(s.T + p.seg_cost);
+    const uint32_t hr = c.off / units, at = c.off % units;
+    s.h = static_cast<int32_t>(hr / static_cast<uint32_t>(p.row_tiles));
+    s.rt = static_cast<int32_t>(hr % static_cast<uint32_t>(p.row_tiles));
+    const uint32_t end = min(units, at + (c.w1 - c.w));
+    s.t0 = max(static_cast<int32_t>(at) - p.seg_cost, 0);
+    s.t1 = max(static_cast<int32_t>(end) - p.seg_cost, 0);
+    s.starts_range = c.w == w0;
+    c.w += end - at;
+    c.off += end - at;
+    if (c.off == static_cast<uint32_t>(p.c.heads * p.row_tiles) * units) {
+      ++c.b;
+      c.off = 0;
+    }
+    if (s.t1 > s.t0) return true;
   }
-  return true;
+  return false;
 }
 
-// One warp: the tiles of one head and row tile of all batch rows, in every lane.
-__device__ __forceinline__ uint32_t all_tiles(const AttendParams& p) {
+// One warp: the units of one head and row tile of all batch rows, in every lane.
+__device__ __forceinline__ uint32_t all_units(const AttendParams& p) {
   uint32_t all = 0;
-  for (int64_t b = threadIdx.x & 31; b < p.B; b += 32) all += static_cast<uint32_t>(tiles_of(p, b));
+  for (int64_t b = threadIdx.x & 31; b < p.B; b += 32) all += units_of(p, b);
   return __reduce_add_sync(0xFFFFFFFFu, all);
 }
 
@@ -570,14 +582,14 @@ __device__ __forceinline__ uint32_t query_offset(int r, int e) {
   return static_cast<uint32_t>(r * D + ((D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) << 4) + (e & 1) * 8);
 }
 
-// One warp: the batch row that holds tile w (p.B when there is none), and the
-// tiles before that row; hr = heads times row tiles.
+// One warp: the batch row that holds unit w (p.B when there is none), and the
+// units before that row; hr = heads times row tiles.
 __device__ __forceinline__ void find_row(const AttendParams& p, uint32_t hr, uint32_t w, int32_t& b, uint32_t& before) {
   const int lane = threadIdx.x & 31;
   before = 0;
   b = 0;
   while (b < p.B) {                                    // 32 batch rows at a time
-    const uint32_t t = b + lane < p.B ? tiles_of(p, b + lane) * hr : 0;
+    const uint32_t t = b + lane < p.B ? units_of(p, b + lane) * hr : 0;
     uint32_t inc = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -596,11 +608,11 @@ __device__ __forceinline__ void find_row(const AttendParams& p, uint32_t hr, uin
   }
 }
 
-// One warp: the CTA's range of tiles and where it begins, into sh.
+// One warp: the CTA's range and where it begins, into sh.
 template <class SH>
 __device__ __forceinline__ void plan_range(const AttendParams& p, SH& sh) {
   const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
-  const Split split(all_tiles(p) * hr, gridDim.x);
+  const Split split(all_units(p) * hr, gridDim.x);
   const uint32_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
   uint32_t before;
   int32_t b;
@@ -1371,18 +1383,18 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
-  const uint32_t total = all_tiles(p) * hr;
+  const uint32_t total = all_units(p) * hr;
   const Split split(total, static_cast<uint32_t>(p.ctas));
   const uint32_t w = split.begin(blockIdx.x + 1);
   if (w >= total) return;
   int32_t b;
   uint32_t before;
   find_row(p, hr, w, b, before);
-  const uint32_t T = static_cast<uint32_t>(tiles_of(p, b));
-  const uint32_t item = (w - before) / T, i0 = before + item * T;   // the item's tiles: [i0, i0 + T)
-  if (i0 == w) return;                                 // the boundary lies between two items
-  const uint32_t ca = split.owner(i0), cb = split.owner(i0 + T - 1);
-  if (ca != blockIdx.x) return;                        // cut before already
+  const uint32_t units = units_of(p, b);
+  const uint32_t item = (w - before) / units, i0 = before + item * units;   // the item's units: [i0, i0 + units)
+  // its first tile and its last one
+  const uint32_t ca = split.owner(i0 + p.seg_cost), cb = split.owner(i0 + units - 1);
+  if (ca != blockIdx.x || ca == cb) return;            // no part before this boundary, or cut before already
   const int h = static_cast<int>(item) / p.row_tiles, row0 = static_cast<int>(item) % p.row_tiles * p.tile_rows;
   const int nrows = min(p.tile_rows, p.rows - row0);
   for (int in = blockIdx.y * kJoinRows + warp; in < min(nrows, static_cast<int>(blockIdx.y + 1) * kJoinRows); in += 8) {
@@ -1529,6 +1541,11 @@ RowTiles row_tiles(int64_t rows) {
   return t;
 }
 
+// What an item costs besides its tiles, in tiles (about 7000 cycles against
+// 1500, 2500 and 4800 a tile).  With fewer tiles than SMs there is nothing to
+// balance, and each tile is a CTA's.
+constexpr int32_t kSegCost32 = 4, kSegCost64 = 3, kSegCost128 = 2;
+
 constexpr size_t kAttendHeader = 256;  // the fault word
 
 size_t attend_workspace(int64_t ctas, int n, int dim) {
@@ -1583,7 +1600,7 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
   if (!dev) return DLLM_ERR_CUDA;
   // One CTA per SM, fewer when there are fewer tiles than that.
   const int64_t most = mul_or_neg(mul_or_neg(B, cache->heads), rt.tiles * ((cap + kTile - 1) / kTile));
-  if (most < 0 || most > INT32_MAX) return DLLM_ERR_UNSUPPORTED;
+  if (mul_or_neg(most, 8) < 0 || most * 8 > INT32_MAX) return DLLM_ERR_UNSUPPORTED;   // (units are 32-bit)
   const int64_t ctas = std::min<int64_t>(dev->sms, most);
   if (workspace_bytes < attend_workspace(ctas, rt.columns, cache->head_dim)) return DLLM_ERR_WORKSPACE;
   AttendParams p;
@@ -1617,6 +1634,7 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
   p.tile_rows = static_cast<int32_t>(rt.rows);
   p.half = static_cast<int32_t>(rt.half);
   p.ctas = static_cast<int32_t>(ctas);
+  p.seg_cost = ctas < dev->sms ? 0 : (rt.columns == 32 ? kSegCost32 : (rt.columns == 64 ? kSegCost64 : kSegCost128));
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.fault = reinterpret_cast<int32_t*>(w);
   p.part_o = reinterpret_cast<float*>(w + kAttendHeader);
@@ -1636,6 +1654,7 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
   if (st != DLLM_OK || !weights) return st;
   // The weights: kWeightRows rows of a key head at a time, K read once for each.
   p.row_tiles = 1;
+  p.seg_cost = p.seg_cost > 0 ? 2 : 0;
   for (int64_t r = 0; r < L * p.G && st == DLLM_OK; r += kWeightRows) {
     int32_t first = static_cast<int32_t>(r), count = static_cast<int32_t>(std::min<int64_t>(kWeightRows, L * p.G - r));
     void* wargs[] = {&p, &first, &count};

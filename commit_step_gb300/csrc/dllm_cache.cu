@@ -347,17 +347,16 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < kMoveVec; ++i) {
       const uint32_t w[4] = {x[kv][i].x, x[kv][i].y, x[kv][i].z, x[kv][i].w};
-      uint32_t top = 0;                                          // largest magnitude code: codes order as values
+      uint32_t top = 0;                                          // largest magnitudes in fp16 (NaN does not set the scale)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t c = (w[q] >> (8 * e)) & 0x7Fu;
-          top = max(top, c < 0x7Fu ? c : 0u);                    // NaN does not set the scale
-        }
+        const uint32_t lo = e4m3x2_to_f16x2(w[q] & 0xFFFFu) & 0x7FFF7FFFu, hi = e4m3x2_to_f16x2(w[q] >> 16) & 0x7FFF7FFFu;
+        asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(lo));
+        asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(hi));
       }
-      float v, unused;
-      f16x2_to_f32(e4m3x2_to_f16x2(top), v, unused);
+      float v, v1;
+      f16x2_to_f32(top, v, v1);
+      v = fmaxf(v, v1);
       const float y = __fmul_rn(v, sc[kv][i]);
       if (y < __int_as_float(0x7F800000)) amax = fmaxf(amax, y);
     }
@@ -380,18 +379,31 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
       const int v = i * blockDim.x + threadIdx.x;
       uint32_t w[4] = {x[kv][i].x, x[kv][i].y, x[kv][i].z, x[kv][i].w};
       if (sc[kv][i] != scale) {
-        const float inv = power_of_two(scale) ? 1.0f / scale : 0.0f;
+        const float ratio = sc[kv][i] / scale;
+        if (power_of_two(sc[kv][i]) && power_of_two(scale) && ratio >= 0x1p-14f && ratio <= 0x1p+15f) {
+          // Between powers of two the value in units of the new scale is exact
+          // in fp16 (a code has 4 bits and is at least 2^-9; fp16 goes to 2^-24).
+          const uint32_t r16 = ((__float_as_uint(ratio) >> 23) - 127u + 15u) << 10, r2 = r16 | r16 << 16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float f[4];
-          f16x2_to_f32(e4m3x2_to_f16x2(w[q] & 0xFFFFu), f[0], f[1]);
-          f16x2_to_f32(e4m3x2_to_f16x2(w[q] >> 16), f[2], f[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = __fmul_rn(f[e], sc[kv][i]);
-            f[e] = inv != 0.0f ? y * inv : __fdiv_rn(y, scale);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t lo = e4m3x2_to_f16x2(w[q] & 0xFFFFu), hi = e4m3x2_to_f16x2(w[q] >> 16);
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(r2));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(r2));
+            uint16_t c0, c1;
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c0) : "r"(lo));
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c1) : "r"(hi));
+            w[q] = c0 | static_cast<uint32_t>(c1) << 16;
           }
-          w[q] = e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16;
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float f[4];
+            f16x2_to_f32(e4m3x2_to_f16x2(w[q] & 0xFFFFu), f[0], f[1]);
+            f16x2_to_f32(e4m3x2_to_f16x2(w[q] >> 16), f[2], f[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = __fdiv_rn(__fmul_rn(f[e], sc[kv][i]), scale);
+            w[q] = e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16;
+          }
         }
       }
       *reinterpret_cast<uint4*>(out + static_cast<int64_t>(v) * 16) = make_uint4(w[0], w[1], w[2], w[3]);

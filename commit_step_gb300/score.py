@@ -8,8 +8,8 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import _F32, _I32, _arg, _check, _dtype_code, _lib, _need_cuda, _ptr, _stream
-from .cache import _empty
+from . import _F32, _I32, _check, _dtype_code, _lib, _need_cuda
+from .cache import _at, _at_or_none, _empty, _raw_stream
 
 MAX_TOP = 32
 
@@ -46,24 +46,24 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, su
     is 0.  ``out``: the same five, preallocated."""
     _need_cuda(logits, targets)
     T, V, stride = _rows(logits, "logits")
-    dt, dev, shape, top = _dtype_code(logits), logits.device, logits.shape[:-1], int(top)
-    _arg(targets, "targets", T, _I32, dev)
-    if targets is None:
-        raise ValueError("targets is needed")
+    dt, dev, idx, shape, top = _dtype_code(logits), logits.device, logits.get_device(), logits.shape[:-1], int(top)
     if out is None:
-        lp, ent, lse = [_empty(shape, torch.float32, dev, stream) for _ in range(3)]
+        lp = _empty(shape, torch.float32, dev, stream)
+        ent = _empty(shape, torch.float32, dev, stream)
+        lse = _empty(shape, torch.float32, dev, stream)
+        lp_at, ent_at, lse_at = lp.data_ptr(), ent.data_ptr(), lse.data_ptr()
         ids = _empty((*shape, top), torch.int32, dev, stream) if top > 0 else None
         tlp = _empty((*shape, top), torch.float32, dev, stream) if top > 0 else None
     else:
         lp, ent, lse, ids, tlp = out
-        for t, name in ((lp, "logprob"), (ent, "entropy"), (lse, "lse")):
-            _arg(t, name, T, _F32, dev)
-        _arg(ids, "top_ids", T * top, _I32, dev)
-        _arg(tlp, "top_logprob", T * top, _F32, dev)
+        lp_at, ent_at, lse_at = [_at(t, name, T, _F32, idx, dev)
+                                 for t, name in ((lp, "logprob"), (ent, "entropy"), (lse, "lse"))]
     sup, n_sup = _sup(suppress_ids)
-    _check(_lib.dllm_token_logprobs(_ptr(logits), dt, T, V, stride, _ptr(targets), sup, n_sup, top, _ptr(lp),
-                                    _ptr(ent), _ptr(lse), _ptr(ids), _ptr(tlp), _stream(stream)),
-           "dllm_token_logprobs")
+    _check(_lib.dllm_token_logprobs(logits.data_ptr(), dt, T, V, stride, _at(targets, "targets", T, _I32, idx, dev), sup,
+                                    n_sup, top, lp_at, ent_at, lse_at,
+                                    _at_or_none(ids, "top_ids", T * top, _I32, idx, dev),
+                                    _at_or_none(tlp, "top_logprob", T * top, _F32, idx, dev),
+                                    _raw_stream(stream, idx)), "dllm_token_logprobs")
     return lp, ent, lse, ids, tlp
 
 
@@ -77,30 +77,28 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: to
     ``top_ids`` it belongs to).  ``out`` may be ``logits`` itself."""
     _need_cuda(logits, targets)
     T, V, stride = _rows(logits, "logits")
-    dt, dev = _dtype_code(logits), logits.device
-    if targets is None or lse is None or entropy is None:
-        raise ValueError("targets, lse and entropy are needed")
-    _arg(targets, "targets", T, _I32, dev)
-    for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob"),
-                    (grad_entropy, "grad_entropy")):
-        _arg(t, name, T, _F32, dev)
-    top = 0
+    dt, dev, idx = _dtype_code(logits), logits.device, logits.get_device()
+    top, ids_at, top_at = 0, None, None
     if grad_top is not None:
         if top_ids is None or not torch.is_tensor(grad_top) or grad_top.dim() < 1:
             raise ValueError("grad_top comes with the top_ids it belongs to")
         top = grad_top.shape[-1]
-        _arg(grad_top, "grad_top", T * top, _F32, dev)
-        _arg(top_ids, "top_ids", T * top, _I32, dev)
+        top_at = _at(grad_top, "grad_top", T * top, _F32, idx, dev)
+        ids_at = _at(top_ids, "top_ids", T * top, _I32, idx, dev)
     if out is None:
         out = _empty(logits.shape, logits.dtype, dev, stream)
     elif not torch.is_tensor(out) or out.dtype != logits.dtype or out.device != dev or out.shape != logits.shape:
         raise ValueError("out must be shaped and typed like logits, on the same device")
     _, _, out_stride = _rows(out, "out")
     sup, n_sup = _sup(suppress_ids)
-    _check(_lib.dllm_token_logprobs_backward(_ptr(logits), dt, T, V, stride, _ptr(targets), sup, n_sup, _ptr(lse),
-                                             _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), top,
-                                             _ptr(top_ids) if top else None, _ptr(grad_top) if top else None,
-                                             _ptr(out), out_stride, _stream(stream)), "dllm_token_logprobs_backward")
+    _check(_lib.dllm_token_logprobs_backward(logits.data_ptr(), dt, T, V, stride,
+                                             _at(targets, "targets", T, _I32, idx, dev), sup, n_sup,
+                                             _at(lse, "lse", T, _F32, idx, dev),
+                                             _at(entropy, "entropy", T, _F32, idx, dev),
+                                             _at_or_none(grad_logprob, "grad_logprob", T, _F32, idx, dev),
+                                             _at_or_none(grad_entropy, "grad_entropy", T, _F32, idx, dev), top, ids_at,
+                                             top_at, out.data_ptr(), out_stride, _raw_stream(stream, idx)),
+           "dllm_token_logprobs_backward")
     return out
 
 
