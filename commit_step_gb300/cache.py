@@ -151,6 +151,8 @@ def _attention_ws(B, L, Hq, cache: KVCache, raw: int, stream) -> torch.Tensor:
     ws = _WS_AT.get((cache.index, raw))
     if ws is None or ws.numel() < need:
         ws = _empty((max(need, 1 << 16),), torch.uint8, cache.device, stream)
+        with torch.cuda.stream(torch.cuda.current_stream(cache.device) if stream is None else stream):
+            ws[:256].zero_()                               # (the fault word, for workspace_fault)
         if not torch.cuda.is_current_stream_capturing():   # (a capture's memory belongs to its graph)
             _WS_AT[(cache.index, raw)] = ws
     return ws

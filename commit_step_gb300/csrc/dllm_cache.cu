@@ -295,7 +295,7 @@ constexpr int kMoveVec = 4;  // 16-byte vectors (16 codes of one token) a thread
 // either's largest value, writes them under the page's new scales.
 // Bound: one byte read and one written for each element that stays.
 template <int D>
-__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(256, 3) evict_move_kernel(const __grid_constant__ EvictParams p) {
   __shared__ float red[2][8];
   pdl_launch_dependents();
   pdl_wait();
@@ -347,16 +347,24 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < kMoveVec; ++i) {
       const uint32_t w[4] = {x[kv][i].x, x[kv][i].y, x[kv][i].z, x[kv][i].w};
-      uint32_t top = 0;                                          // largest magnitudes in fp16 (NaN does not set the scale)
+      // largest magnitude code (codes order as values), two bytes at a time
+      uint32_t top2 = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint32_t lo = e4m3x2_to_f16x2(w[q] & 0xFFFFu) & 0x7FFF7FFFu, hi = e4m3x2_to_f16x2(w[q] >> 16) & 0x7FFF7FFFu;
-        asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(lo));
-        asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(hi));
+        asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(w[q] & 0x007F007Fu));
+        asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"((w[q] >> 8) & 0x007F007Fu));
       }
-      float v, v1;
-      f16x2_to_f32(top, v, v1);
-      v = fmaxf(v, v1);
+      uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+      if (top == 0x7Fu) {                                        // NaN does not set the scale
+        top = 0;
+#pragma unroll 1
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t c = (w[e >> 2] >> (8 * (e & 3))) & 0x7Fu;
+          top = max(top, c < 0x7Fu ? c : 0u);
+        }
+      }
+      float v, unused;
+      f16x2_to_f32(e4m3x2_to_f16x2(top), v, unused);
       const float y = __fmul_rn(v, sc[kv][i]);
       if (y < __int_as_float(0x7F800000)) amax = fmaxf(amax, y);
     }

@@ -542,8 +542,16 @@ dllm_status dllm_cache_append(const dllm_kv_cache* cache, const void* k, const v
  *              that are not attended; queries whose lse is not finite add
  *              nothing).  decay in [0, 1]; with 0 the old weights are not read.
  *   workspace  device, 16-byte aligned, >=
- *              dllm_cache_attention_workspace_size(...) bytes, any contents
- * Sums and statistics are fp32. */
+ *              dllm_cache_attention_workspace_size(...) bytes, any contents.
+ *              Its first word takes a fault code when a bounded wait runs out
+ *              (outputs are then undefined): zero it to read it later with
+ *              dllm_workspace_fault.
+ * Sums and statistics are fp32.  Products are exact in the codes and in the
+ * queries' 8 bits (a query's elements below 2^-9 of its largest are rounded at
+ * 2^-18 of that); probabilities times value scales are rounded to fp16, no
+ * finer than 2^-23 of a row's largest.  Results repeat bit for bit.
+ * DLLM_ERR_UNSUPPORTED also for pools of 2^31 or more token rows (pages heads
+ * page_size). */
 size_t dllm_cache_attention_workspace_size(int64_t B, int64_t L, int64_t Hq, int64_t heads, int64_t head_dim);
 
 dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, const int64_t* q_strides, int64_t B,
