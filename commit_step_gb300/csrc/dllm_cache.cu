@@ -56,23 +56,36 @@ __global__ void __launch_bounds__(256, 4) append_kernel(const __grid_constant__ 
   constexpr int per_token = D / 8;
   const int from = static_cast<int>(a - lo), to = static_cast<int>(e - lo);  // new slots [from, to)
   uint4 x[kAppendVec];
-  uint32_t top = 0;                                              // largest finite |bf16| bits (they order as values)
+  // Vector i of this thread: 8 dims of slot slot0 + i step.
+  const int slot0 = threadIdx.x / per_token, step = blockDim.x / per_token, d = threadIdx.x % per_token * 8;
+  const uint8_t* row = src + (lo + slot0 - start) * p.sl[kv] + d * 2;
+  const int64_t row_step = step * p.sl[kv];
 #pragma unroll
   for (int i = 0; i < kAppendVec; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
-    const int slot = v / per_token, d = (v % per_token) * 8;
+    const int slot = slot0 + i * step;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (slot >= from && slot < to)
-      x[i] = __ldg(reinterpret_cast<const uint4*>(src + (lo + slot - start) * p.sl[kv] + d * 2));
+    if (slot >= from && slot < to) x[i] = __ldcs(reinterpret_cast<const uint4*>(row + i * row_step));
   }
+  // Largest |bf16| bits (they order as values), two at a time.
+  uint32_t top2 = 0;
 #pragma unroll
   for (int i = 0; i < kAppendVec; ++i) {
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t u0 = w[q] & 0x7FFFu, u1 = (w[q] >> 16) & 0x7FFFu;
-      top = max(top, u0 < 0x7F80u ? u0 : 0u);                    // infinities and NaN do not set the scale
-      top = max(top, u1 < 0x7F80u ? u1 : 0u);
+    for (int q = 0; q < 4; ++q) asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(w[q] & 0x7FFF7FFFu));
+  }
+  uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+  if (top >= 0x7F80u) {                                          // infinities and NaN do not set the scale
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < kAppendVec; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t u0 = w[q] & 0x7FFFu, u1 = (w[q] >> 16) & 0x7FFFu;
+        top = max(top, u0 < 0x7F80u ? u0 : 0u);
+        top = max(top, u1 < 0x7F80u ? u1 : 0u);
+      }
     }
   }
   const float amax = block_max(__uint_as_float(top << 16), red);
@@ -98,8 +111,7 @@ __global__ void __launch_bounds__(256, 4) append_kernel(const __grid_constant__ 
   const float inv = 1.0f / s;
 #pragma unroll
   for (int i = 0; i < kAppendVec; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
-    const int slot = v / per_token, d = (v % per_token) * 8;
+    const int slot = slot0 + i * step;
     if (slot < from || slot >= to) continue;
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t o[4];
