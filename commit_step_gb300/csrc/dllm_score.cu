@@ -132,11 +132,8 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
     n_chosen = 0;
     inf_s = 0;
   }
-  if (k > 0)
-    for (int i = threadIdx.x; i < kEntries; i += kScoreThreads) entry[i] = 0;
   pdl_launch_dependents();
   pdl_wait();
-  __syncthreads();
 
   const uint8_t* base = p.logits + row * p.row_bytes;
   // The row as whole aligned vectors, with up to EPV - 1 elements before and after them.
@@ -149,6 +146,9 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
   const int blocks = (nv + 31) / 32;
   int shift = 0;                                           // 2^shift blocks share an entry
   while (((blocks + (1 << shift) - 1) >> shift) > kEntries) ++shift;
+  if (k > 0 && shift > 0)                                  // (else every entry is written once)
+    for (int i = threadIdx.x; i < kEntries; i += kScoreThreads) entry[i] = 0;
+  __syncthreads();
   Soft a{kLow, 0.0f, 0.0f};
 
   // The next suppressed id, as an element offset from this CTA's first.
@@ -306,27 +306,35 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
       have += __popc(hit);
     };
     if (edges) offer(edge_z, static_cast<uint32_t>(edge_id), edge_in);
-    // A floor for the entries: each thread's best entry; at least k entries are
-    // no worse than the k-th of those.
+    // A floor for the entries: the best entry of each four threads; at least k
+    // entries are no worse than the k-th of those 64.
+    constexpr int kGroups = kScoreThreads / 4;
+    static_assert(kGroups >= DLLM_MAX_TOP, "");
     const int n = (blocks + (1 << shift) - 1) >> shift;
     __syncthreads();
-    uint64_t* mine_s = joined;
+    uint64_t* group_s = joined;
     uint64_t mine = 0;
     for (int e = threadIdx.x; e < n; e += kScoreThreads) {
       const uint64_t c = static_cast<uint64_t>(entry[e]) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(e));
       mine = c > mine ? c : mine;
     }
-    mine_s[threadIdx.x] = mine;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const uint64_t c = __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+      mine = c > mine ? c : mine;
+    }
+    if ((threadIdx.x & 3) == 0) group_s[threadIdx.x >> 2] = mine;
     __syncthreads();
-    if (mine != 0) {
+    if (threadIdx.x < kGroups) {
+      mine = group_s[threadIdx.x];
       int r = 0;
 #pragma unroll 4
-      for (int j = 0; j < kScoreThreads; j += 2) {
-        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&mine_s[j]);
+      for (int j = 0; j < kGroups; j += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&group_s[j]);
         r += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
       }
       // (among values that only stand for "-2^100 or less" the entries say nothing: then all are taken)
-      if (r == k - 1 && candidate_value(mine) > kLow) floor_entry_s = mine;
+      if (mine != 0 && r == k - 1 && candidate_value(mine) > kLow) floor_entry_s = mine;
     }
     __syncthreads();
     const uint64_t fe = floor_entry_s;
@@ -339,12 +347,20 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
       floor_c = fe & 0xFFFFFFFF00000000ull;                // its value with any id
     }
     const int nb = n_chosen << shift;
-    for (int c = warp; c < nb; c += kScoreWarps) {
-      const int blk = (static_cast<int>(chosen[c >> shift]) << shift) + (c & ((1 << shift) - 1));
-      if (blk >= blocks) continue;
-      const int v = blk * 32 + lane;
+    auto load = [&](int c, int& v) {                       // this lane's vector of chosen block c (v: its index, or nv)
+      v = nv;
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (v < nv) x = vecs[v0 + v];
+      if (c < nb) {
+        const int blk = (static_cast<int>(chosen[c >> shift]) << shift) + (c & ((1 << shift) - 1));
+        v = min(blk * 32 + lane, nv);
+        if (v < nv) x = vecs[v0 + v];
+      }
+      return x;
+    };
+    int v, vn;
+    uint4 x = load(warp, v);
+    for (int c = warp; c < nb; c += kScoreWarps) {
+      const uint4 next = load(c + kScoreWarps, vn);        // (its latency passes behind this block's comparisons)
       const int64_t id = id_base + static_cast<int64_t>(v) * EPV;
       uint32_t absent = v < nv ? 0u : 0xFFu;
       for (int q = 0; q < p.n_sup; ++q) {
@@ -354,6 +370,8 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
 #pragma unroll
       for (int e = 0; e < EPV; ++e)
         offer(no_nan(element<BYTES>(x, e)), static_cast<uint32_t>(id) + e, !((absent >> e) & 1u));
+      x = next;
+      v = vn;
     }
     cut();
   }
