@@ -1124,14 +1124,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 // the weights
 // ---------------------------------------------------------------------------
 constexpr int kWeightCols = 64;        // rows (columns of a product) of a job
-constexpr int kWeightRows = 512;       // rows of a launch: what the queries' shared memory holds
-constexpr int kWeightStages = 5;       // of the K ring
+constexpr int kWeightRows = 256;       // rows of a launch: what the queries' shared memory holds
+constexpr int kWeightStages = 8;       // of the K ring
 constexpr int kWeightGroups = 4;
 constexpr int kWeightSoft = 4 * kWeightGroups, kWeightCopyWarp = kWeightSoft, kWeightMmaWarp = kWeightSoft + 1;
 constexpr int kWeightThreads = (kWeightSoft + 2) * 32;
 constexpr int kWeightBufs = 2;         // score buffers of a group
-// The products run up to 4 x 2 tiles ahead of the softmax and the copies 5
-// ahead of the products: a tile's meta slot is free again after 16.
+// The products run up to 7 tiles ahead of the softmax and the copies 8 ahead of
+// the products: a tile's meta slot is free again after 16.
 constexpr int kWeightMeta = 16;
 
 constexpr int weights_smem(int dim, int chunks) {
@@ -1226,43 +1226,43 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
     const uint32_t lead = elect_one();
     const uint32_t kd = at_desc_lo(k_s, 16), qd = at_desc_lo(q_s, 16);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    uint32_t ks = 0, kp = 0;
-    uint32_t jobs = 0;                                 // of a group, when all have passed as many tiles
     uint32_t seg = 0;
     while (next_segment(p, cur, sh.w0, sg)) {
       const uint32_t n = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(sg.t1 - sg.t0), 0);
       wait(sh.qfull, seg & 1u, kFaultFullWait);
       __syncwarp();
-      for (uint32_t i = 0; i < n; ++i, ++g) {
-        const uint32_t grp = g % kWeightGroups;
-        jobs = g / kWeightGroups * static_cast<uint32_t>(chunks);
-        wait(sh.kfull[ks], kp, kFaultFullWait);
-        __syncwarp();
+      // Four tiles, one to a group, chunk by chunk: so that all groups have work
+      // (tile by tile, a group's two buffers held the others up).
+      for (uint32_t i = 0; i < n; i += kWeightGroups) {
+        const uint32_t tiles = min(static_cast<uint32_t>(kWeightGroups), n - i);
         for (int c = 0; c < chunks; ++c) {
-          const uint32_t j = jobs + static_cast<uint32_t>(c);
-          const uint32_t buf = grp * kWeightBufs + j % kWeightBufs;
-          wait(sh.sempty[buf], ((j / kWeightBufs) & 1u) ^ 1u, kFaultEmptyWait);
-          __syncwarp();
-          if (*abort_flag) continue;
-          at_fence_after();
           const int cols = min(NC, (rows - c * NC + 15) & ~15);
           const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(cols >> 3) << 17) |
                                  (static_cast<uint32_t>(kTile >> 4) << 24);
-          const uint32_t k = kd + ks * (kTileBytes >> 4), q = qd + static_cast<uint32_t>(c) * (2 * NC * D >> 4);
+          const uint32_t q = qd + static_cast<uint32_t>(c) * (2 * NC * D >> 4);
+          for (uint32_t u = 0; u < tiles; ++u) {
+            const uint32_t t = g + u, grp = t % kWeightGroups, st = t % ST;
+            const uint32_t j = t / kWeightGroups * static_cast<uint32_t>(chunks) + static_cast<uint32_t>(c);
+            const uint32_t buf = grp * kWeightBufs + j % kWeightBufs;
+            if (c == 0) wait(sh.kfull[st], (t / ST) & 1u, kFaultFullWait);
+            wait(sh.sempty[buf], ((j / kWeightBufs) & 1u) ^ 1u, kFaultEmptyWait);
+            __syncwarp();
+            if (!*abort_flag) {
+              at_fence_after();
+              const uint32_t k = kd + st * (kTileBytes >> 4);
 #pragma unroll
-          for (int m = 0; m < 2 * (D / 32); ++m) {
-            const int part = m / (D / 32), kk = m % (D / 32);
-            at_mma_f8(lead, tm + buf * NC, k + kk * 2, kHiK, q + part * (NC * D >> 4) + kk * 2, kHiK, idesc,
-                      m != 0 ? 1u : 0u);
+              for (int m = 0; m < 2 * (D / 32); ++m) {
+                const int part = m / (D / 32), kk = m % (D / 32);
+                at_mma_f8(lead, tm + buf * NC, k + kk * 2, kHiK, q + part * (NC * D >> 4) + kk * 2, kHiK, idesc,
+                          m != 0 ? 1u : 0u);
+              }
+              if (c == chunks - 1) at_commit(lead, smem_addr(&sh.kempty[st]));
+              at_commit(lead, smem_addr(&sh.sfull[buf]));
+            }
+            __syncwarp();
           }
-          at_commit(lead, smem_addr(&sh.sfull[buf]));
         }
-        if (!*abort_flag) at_commit(lead, smem_addr(&sh.kempty[ks]));
-        __syncwarp();
-        if (++ks == ST) {
-          ks = 0;
-          kp ^= 1u;
-        }
+        g += tiles;
       }
       ++seg;
     }
