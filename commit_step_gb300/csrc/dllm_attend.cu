@@ -416,8 +416,8 @@ struct AttendShared {
   float vmax[2][4];
   float red[2][4][N];                                  // maxima or sums per warp
   float vref[2];
-  float fin[2][N];                                     // what an accumulator's column is multiplied with at the end
-  int32_t row[AttendShape<N, PAIR>::kRows];            // output rows, -1 where a column has none
+  alignas(16) float fin[2][N];                         // what an accumulator's column is multiplied with at the end
+  alignas(16) int32_t row[AttendShape<N, PAIR>::kRows];            // output rows, -1 where a column has none
   uint32_t w0, w1, off0;
   int32_t b0;
   uint32_t tmem;
@@ -1087,26 +1087,32 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           uint32_t r[24];
           const uint32_t t = tmem + lanes + S::kAcc + static_cast<uint32_t>(a) * 3 * N + c;
           at_ld3(t, t + N, t + 2 * N, r);
+          const float4 f0 = *reinterpret_cast<const float4*>(&sh.fin[a][c]);
+          const float4 f1 = *reinterpret_cast<const float4*>(&sh.fin[a][c + 4]);
+          const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float y = fmaf(fmaf(__uint_as_float(r[16 + i]), 1.0f / 16, __uint_as_float(r[8 + i])), 1.0f / 16,
                                  __uint_as_float(r[i]));
-            o[i] = k == 0 ? y * sh.fin[a][c + i] : fmaf(y, sh.fin[a][c + i], o[i]);
+            o[i] = k == 0 ? y * f[i] : fmaf(y, f[i], o[i]);
           }
         }
         if (d >= D) continue;                          // (whole warps)
+        const int n = c0 + c;
+        const int4 r0 = *reinterpret_cast<const int4*>(&sh.row[n]), r1 = *reinterpret_cast<const int4*>(&sh.row[n + 4]);
+        const int32_t rows8[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int n = c0 + c + i;
-          const int32_t row = sh.row[n];
-          if (row < 0) continue;
-          if (whole) {
+          for (int i = 0; i < 8; ++i) {
             uint16_t u;
             asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(o[i]));
-            p.out[static_cast<int64_t>(row) * D + d] = u;
-          } else {
-            p.part_o[(slot * S::kRows + n) * D + d] = o[i];
+            if (rows8[i] >= 0) p.out[static_cast<int64_t>(rows8[i]) * D + d] = u;
           }
+        } else {
+          float* part = p.part_o + (slot * S::kRows + n) * D + d;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (rows8[i] >= 0) part[i * D] = o[i];
         }
       }
       at_fence_before();
