@@ -1135,8 +1135,8 @@ constexpr int kWeightStages = 8;       // of the K ring
 constexpr int kWeightGroups = 4;
 constexpr int kWeightSoft = 4 * kWeightGroups, kWeightCopyWarp = kWeightSoft, kWeightMmaWarp = kWeightSoft + 1;
 constexpr int kWeightThreads = (kWeightSoft + 2) * 32;
-constexpr int kWeightBufs = 2;         // score buffers of a group
-// The products run up to 7 tiles ahead of the softmax and the copies 8 ahead of
+constexpr int kWeightBufs = 1;         // score buffers of a group: the queries' hi and lo parts as 2 x 64 columns
+// The products run up to 4 tiles ahead of the softmax and the copies 8 ahead of
 // the products: a tile's meta slot is free again after 16.
 constexpr int kWeightMeta = 16;
 
@@ -1161,10 +1161,10 @@ struct WeightShared {
 // w[j] = decay w[j] + sum over the rows of exp(s - lse): S^T as in the
 // attention, a thread per token, so a token's sum stays in its thread and
 // nothing is shared or added atomically.  Four groups of 4 warps take the tiles
-// in turn; a job is one tile and up to 64 rows, with 2 score buffers a group, so
-// the products run ahead.
-// Bound: the products (8 of M 128, N 64, K 32 for a job), since each row's
-// scores are computed twice over the attention's; K's bytes when rows are few.
+// in turn; a job is one tile and up to 64 rows.
+// Bound: the products (4 of M 128, N 128, K 32 for a job) and the softmax's
+// issue, since each row's scores are computed once more; K's bytes when rows
+// are few.
 template <int D>
 __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const __grid_constant__ AttendParams p,
                                                                            int32_t first_row, int32_t rows) {
@@ -1238,13 +1238,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
       wait(sh.qfull, seg & 1u, kFaultFullWait);
       __syncwarp();
       // Four tiles, one to a group, chunk by chunk: so that all groups have work
-      // (tile by tile, a group's two buffers held the others up).
+      // (tile by tile, a group's buffer held the others up).
       for (uint32_t i = 0; i < n; i += kWeightGroups) {
         const uint32_t tiles = min(static_cast<uint32_t>(kWeightGroups), n - i);
         for (int c = 0; c < chunks; ++c) {
-          const int cols = min(NC, (rows - c * NC + 15) & ~15);
-          const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(cols >> 3) << 17) |
-                                 (static_cast<uint32_t>(kTile >> 4) << 24);
           const uint32_t q = qd + static_cast<uint32_t>(c) * (2 * NC * D >> 4);
           for (uint32_t u = 0; u < tiles; ++u) {
             const uint32_t t = g + u, grp = t % kWeightGroups, st = t % ST;
@@ -1257,11 +1254,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
               at_fence_after();
               const uint32_t k = kd + st * (kTileBytes >> 4);
 #pragma unroll
-              for (int m = 0; m < 2 * (D / 32); ++m) {
-                const int part = m / (D / 32), kk = m % (D / 32);
-                at_mma_f8(lead, tm + buf * NC, k + kk * 2, kHiK, q + part * (NC * D >> 4) + kk * 2, kHiK, idesc,
-                          m != 0 ? 1u : 0u);
-              }
+              for (int kk = 0; kk < D / 32; ++kk)
+                at_mma_f8(lead, tm + buf * 2 * NC, k + kk * 2, kHiK, q + kk * 2, kHiK, at_idesc(2 * NC, false),
+                          kk != 0 ? 1u : 0u);
               if (c == chunks - 1) at_commit(lead, smem_addr(&sh.kempty[st]));
               at_commit(lead, smem_addr(&sh.sfull[buf]));
             }
@@ -1281,11 +1276,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
     while (next_segment(p, cur, sh.w0, sg)) {
       named_sync(5, kWeightSoft * 32);                  // (the previous segment's rows are no longer read)
       const int e = threadIdx.x % kPer;
-      for (int rb = threadIdx.x / kPer; rb < chunks * NC; rb += 4 * kStep) {   // (whole warps)
-        uint4 x[4];
-        float nm[4];
+      constexpr int kBatch = kWeightRows / kStep;      // all rows at once
+      {
+        const int rb = threadIdx.x / kPer;
+        uint4 x[kBatch];
+        float nm[kBatch];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kBatch; ++i) {
           const int r = rb + i * kStep;
           x[i] = make_uint4(0u, 0u, 0u, 0u);
           nm[i] = -kInf;
@@ -1296,9 +1293,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kBatch; ++i) {
           const int r = rb + i * kStep;
-          if (r >= chunks * NC) break;
+          if (r >= chunks * NC) break;                 // (whole warps)
           uint32_t hi[2], lo[2];
           const float s = split_query<D>(x[i], hi, lo);
           const uint32_t at = q_s + static_cast<uint32_t>(r / NC * 2 * NC * D) + query_offset<D>(r % NC, e);
@@ -1334,8 +1331,11 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
 #pragma unroll
           for (int i0 = 0; i0 < NC; i0 += 16) {
             if (i0 >= cols) break;
-            uint32_t r[16];
-            at_ld<16>(tmem + lanes + buf * NC + i0, r);
+            uint32_t r[16], lo[16];
+            at_ld<16>(tmem + lanes + buf * 2 * NC + i0, r);
+            at_ld<16>(tmem + lanes + buf * 2 * NC + NC + i0, lo);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(lo[i]));
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
               const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sh.f + c * NC + i0 + i);
