@@ -161,6 +161,27 @@ __device__ __forceinline__ void at_ld(uint32_t t, uint32_t (&r)[C]) {
   }
 }
 
+// 32 columns at each of two places, one wait for both (a load's latency is
+// most of what it costs).
+__device__ __forceinline__ void at_ld32x2(uint32_t t0, uint32_t t1, uint32_t (&a)[32], uint32_t (&b)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,"
+      "%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
+        "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
+        "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]),
+        "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
+        "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]),
+        "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]),
+        "=r"(b[24]), "=r"(b[25]), "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
+      : "r"(t0), "r"(t1)
+      : "memory");
+}
+
 // 8 columns of each of an accumulator's three parts.
 __device__ __forceinline__ void at_ld3(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t (&r)[24]) {
   asm volatile(
@@ -876,25 +897,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         // Exponents x = score - reference, and the largest of them.
         uint64_t x[N / 2];
         auto exponents = [&]() {
+          uint32_t r[2][32];                           // the columns, or their hi and lo sums
+          at_ld32x2(s_t, s_t + 32, r[0], r[1]);
+          if constexpr (S::kConcat) {
 #pragma unroll
-          for (int c = 0; c < N; c += 16) {
-            if (c >= ncols) break;                     // (uniform)
-            uint32_t r[16];
-            at_ld<16>(s_t + c, r);
-            if constexpr (S::kConcat) {
-              uint32_t q[16];
-              at_ld<16>(s_t + N + c, q);
+            for (int i = 0; i < 32; ++i) r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) + __uint_as_float(r[1][i]));
+          }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
-            }
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fq + c + i);
-              const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(nm + c + i);
-              x[(c + i) / 2] = fma2(at_mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ck2), f.x, n.x);
-              x[(c + i) / 2 + 1] =
-                  fma2(at_mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), ck2), f.y, n.y);
-            }
+          for (int i = 0; i < N; i += 4) {
+            if (i % 16 == 0 && i >= ncols) break;      // (uniform)
+            const uint32_t* q = &r[i / 32][i % 32];
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fq + i);
+            const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(nm + i);
+            x[i / 2] = fma2(at_mul2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), ck2), f.x, n.x);
+            x[i / 2 + 1] = fma2(at_mul2(pack2(__uint_as_float(q[2]), __uint_as_float(q[3])), ck2), f.y, n.y);
           }
         };
         exponents();
@@ -1329,24 +1345,21 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
           at_fence_after();
           const int cols = min(NC, (rows - c * NC + 15) & ~15);
 #pragma unroll
-          for (int i0 = 0; i0 < NC; i0 += 16) {
+          for (int i0 = 0; i0 < NC; i0 += 32) {
             if (i0 >= cols) break;
-            uint32_t r[16], lo[16];
-            at_ld<16>(tmem + lanes + buf * 2 * NC + i0, r);
-            at_ld<16>(tmem + lanes + buf * 2 * NC + NC + i0, lo);
+            uint32_t r[32], lo[32];
+            at_ld32x2(tmem + lanes + buf * 2 * NC + i0, tmem + lanes + buf * 2 * NC + NC + i0, r, lo);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(lo[i]));
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = 0; i < 32; i += 4) {
               const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sh.f + c * NC + i0 + i);
               const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(sh.nm + c * NC + i0 + i);
-              const uint64_t x0 =
-                  fma2(at_mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ck2), f.x, n.x);
-              const uint64_t x1 =
-                  fma2(at_mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), ck2), f.y, n.y);
+              uint64_t s0 = add2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                 pack2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+              uint64_t s1 = add2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
+                                 pack2(__uint_as_float(lo[i + 2]), __uint_as_float(lo[i + 3])));
               float a0, a1, b0, b1;
-              unpack2(x0, a0, a1);
-              unpack2(x1, b0, b1);
+              unpack2(fma2(at_mul2(s0, ck2), f.x, n.x), a0, a1);
+              unpack2(fma2(at_mul2(s1, ck2), f.y, n.y), b0, b1);
               // (a row that adds nothing has -inf or NaN here)
               sum2[0] = add2(sum2[0], pack2(ex2_approx(fmaxf(a0, -1e30f)), ex2_approx(fmaxf(a1, -1e30f))));
               sum2[1] = add2(sum2[1], pack2(ex2_approx(fmaxf(b0, -1e30f)), ex2_approx(fmaxf(b1, -1e30f))));
