@@ -103,7 +103,8 @@ __device__ __forceinline__ float element(const uint4& v, int e) {
 // elements of a warp hold one that reaches it.)
 // Logits below -2^100 count as -2^100 in the pass; a row whose maximum is not
 // within 2^100 of zero is computed from its logits as they are by one CTA.
-// Bound: the one read of the logits.
+// Bound: the one read of the logits.  Measured, 4096 x 152064 bf16: 192 us (6.5
+// TB/s) without alternatives, 236 us with the top 20; 32 x 126464, top 8: 11 us.
 template <int BYTES>
 __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_constant__ ScoreParams p) {
   constexpr int EPV = 16 / BYTES;
@@ -563,7 +564,8 @@ __device__ __forceinline__ float load_element(const uint8_t* row, int64_t v) {
 // transforms whole vectors, and the few named ids (target, alternatives,
 // suppressed ids), read before anything is written, are stored again after the
 // block's vectors, so grad may be the logits' own buffer.
-// Bound: one read of the logits and one write of the gradient.
+// Bound: one read of the logits and one write of the gradient.  Measured, 4096 x
+// 152064 bf16: 354 us (7.0 TB/s).
 template <int BYTES>
 __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const __grid_constant__ ScoreGradParams p) {
   constexpr int EPV = 16 / BYTES;
@@ -711,7 +713,9 @@ dllm_status dllm_token_logprobs(const void* logits, dllm_dtype dt, int64_t T, in
   const int64_t bytes = dt == DLLM_BF16 ? 2 : 4;
   // CTAs per row: doubled while the grid would leave SMs without work (304 =
   // two CTAs for each of 152 SMs) and every CTA still gets two passes of its
-  // threads' vectors.
+  // threads' vectors.  Measured, 126464 bf16, top 8, us with 1 / 2 / 4 / 8 CTAs:
+  // 32 rows 18.0 / 13.5 / 11.0 / 11.4, 128 rows 21.1 / 19.0 / 15.7 / 23.5, 256
+  // rows 27.7 / 21.3 / 28.2 / 43.4, 512 rows 31.3 / 38.0 / 51.5 / 81.0.
   int cluster = 1;
   while (cluster < 8 && T * cluster < 304 && V * bytes >= 2 * cluster * 2 * 16 * kScoreThreads * kScoreVec) cluster *= 2;
   if (T > INT32_MAX / cluster) return DLLM_ERR_UNSUPPORTED;
