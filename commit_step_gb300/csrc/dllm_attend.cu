@@ -960,7 +960,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             sh.delta[grp][tid] = -up;
             const float d = ex2_approx(-up);
             sh.fac_l[grp][tid] = d;
-            sh.fac_o[grp][tid] = d * (vref / vnew);
+            // (before any score the accumulator is all zeros, and d may be infinite)
+            sh.fac_o[grp][tid] = seen ? d * (vref / vnew) : 0.0f;
           }
           vref = vnew;
           vscale = kPUnit / 256 / vref;

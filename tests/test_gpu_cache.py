@@ -215,6 +215,21 @@ def test_attention_mask_holes_and_garbage(cs, L):
     check_attention(cs, arrays, queries(rng, B, L, H * G, dim), table, lens, mask=mask)
 
 
+@pytest.mark.parametrize("L", [4, 20])
+def test_attention_very_negative_scores_behind_masked_tiles(cs, L):
+    """Tiles without a visible key, then scores far below zero: a first reference
+    near -180 meets an accumulator that holds products of nothing."""
+    rng = np.random.default_rng(5 + L)
+    ps, H, G, dim, B, width = 16, 2, 4, 128, 64, 32
+    arrays = list(random_pool(rng, B * width, H, ps, dim, spread=1))
+    arrays[0] = arrays[0] & 0x7F                                            # keys above zero, queries below
+    q = -(queries(rng, B, L, H * G, dim).abs() + 12)
+    mask = np.ones((B, width * ps), dtype=np.uint8)
+    mask[:, :256] = 0
+    lens = np.full(B, width * ps, dtype=np.int32)
+    check_attention(cs, arrays, q, tables(rng, B * width, B, width), lens, mask=mask)
+
+
 def test_attention_nan_and_inf_queries_stay_in_their_row(cs):
     rng = np.random.default_rng(3)
     ps, H, G, dim, B, width = 64, 1, 4, 128, 2, 4
