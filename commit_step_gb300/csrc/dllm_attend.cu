@@ -167,14 +167,21 @@ __device__ __forceinline__ void at_ld(uint32_t t, uint32_t (&r)[C]) {
   }
 }
 
-// 32 columns at each of two places, one wait for both (a load's latency is
-// most of what it costs).
-__device__ __forceinline__ void at_ld32x2(uint32_t t0, uint32_t t1, uint32_t (&a)[32], uint32_t (&b)[32]) {
+// Fragments: of 16 TMEM lanes (tokens) by 8 j columns, thread t gets the tokens
+// t / 4 and t / 4 + 8 and of each 8 columns the two at 2 (t mod 4): register 4 j +
+// 2 s + e is token t / 4 + 8 s, column 8 j + 2 (t mod 4) + e.  A thread then
+// meets a quarter of the columns, whose scales and references it can keep in
+// registers (read per column from shared memory by every token's thread, they
+// cost 512 bytes a warp instruction, more than all else in shared memory).
+// 64 columns at each of two places, one wait for both.
+__device__ __forceinline__ void at_frag64x2(uint32_t t0, uint32_t t1, uint32_t (&a)[32], uint32_t (&b)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,"
-      "%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
         "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
@@ -185,6 +192,30 @@ __device__ __forceinline__ void at_ld32x2(uint32_t t0, uint32_t t1, uint32_t (&a
         "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]),
         "=r"(b[24]), "=r"(b[25]), "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
       : "r"(t0), "r"(t1)
+      : "memory");
+}
+
+// 32 columns at each of four places.
+__device__ __forceinline__ void at_frag32x4(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3, uint32_t (&a)[16], uint32_t (&b)[16], uint32_t (&c)[16], uint32_t (&d)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%65];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%66];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%67];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
+        "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
+        "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]),
+        "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]), "=r"(c[4]), "=r"(c[5]), "=r"(c[6]), "=r"(c[7]),
+        "=r"(c[8]), "=r"(c[9]), "=r"(c[10]), "=r"(c[11]), "=r"(c[12]), "=r"(c[13]), "=r"(c[14]), "=r"(c[15]),
+        "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7]),
+        "=r"(d[8]), "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]), "=r"(d[13]), "=r"(d[14]), "=r"(d[15])
+      : "r"(t0), "r"(t1), "r"(t2), "r"(t3)
       : "memory");
 }
 
@@ -266,23 +297,46 @@ __device__ __forceinline__ uint32_t part_rest16(uint32_t h) {
 // The codes of four values: bits 14 .. 7 of the halves of a, then of b.
 __device__ __forceinline__ uint32_t part_codes(uint32_t a, uint32_t b) { return __byte_perm(a << 1, b << 1, 0x7531); }
 
-// Reduces 32 columns over the warp's lanes: lane i returns column i of all
-// lanes (31 exchanges instead of 160 shuffles).
-template <bool MAX>
-__device__ __forceinline__ float column_reduce(float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const bool up = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-      const float got = __shfl_xor_sync(0xFFFFFFFFu, send, o);
-      v[i] = MAX ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  return v[0];
+// 32 columns at each of two places.
+__device__ __forceinline__ void at_frag32x2(uint32_t t0, uint32_t t1, uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
+        "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
+        "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+      : "r"(t0), "r"(t1)
+      : "memory");
 }
+
+// Combines a value over the 8 lanes that hold the same columns.
+template <bool MAX>
+__device__ __forceinline__ float over_tokens(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    const float w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = MAX ? fmaxf(v, w) : v + w;
+  }
+  return v;
+}
+
+// Four 8 x 8 matrices of 16-bit elements, register i's from thread t's row t / 4,
+// elements 2 (t mod 4) and the next; thread t gives the address of row t mod 8 of
+// matrix t / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
+               : "memory");
+}
+
+// P's codes are stored as 16-bit pairs, two groups of 8 columns interleaved, so
+// column n of the scores becomes column place(n) of P and of the accumulator:
+// within 16, bit 3 of n moves below its bits 2 and 1.
+__host__ __device__ constexpr int place(int n) { return (n & ~15) | ((n & 6) << 1) | ((n & 8) >> 2) | (n & 1); }
 
 // Whether any of the 128 threads of named barrier `id` has p set.
 __device__ __forceinline__ bool group_any(uint32_t id, bool p) {
@@ -441,7 +495,7 @@ struct AttendShared {
   alignas(16) float fac_l[2][N];
   alignas(16) float delta[2][N];
   float vmax[2][4];
-  float red[2][4][N];                                  // maxima or sums per warp
+  alignas(16) float red[2][4][N];                                  // maxima or sums per warp
   float vref[2];
   alignas(16) float fin[2][N];                         // what an accumulator's column is multiplied with at the end
   alignas(16) int32_t row[AttendShape<N, PAIR>::kRows];            // output rows, -1 where a column has none
@@ -803,13 +857,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    // Softmax: thread (warp % 4, lane) holds token 32 (warp % 4) + lane of a tile.
+    // Softmax: warp w (mod 4) of a group has tokens 32 w .. 32 w + 31 of a tile,
+    // a thread tokens 32 w + lane / 4 + 8 q, q = 0 .. 3, and the columns 8 j + 2
+    // (lane mod 4) + {0, 1}.  What is stored or cleared by token (P's rows, V's)
+    // goes by key = 32 w + lane.
+    constexpr int J = N / 8;                           // column pairs of a thread
     const int grp = warp >> 2, wq = warp & 3, key = wq * 32 + lane, tid = threadIdx.x & 127;
+    const int col = 2 * (lane & 3);
     const uint32_t bar_id = 1u + static_cast<uint32_t>(grp);
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const int page_of = key / ps;
     const int c0 = PAIR ? grp * N : 0;                 // the group's first column
-    const float* fq = sh.f + c0;
     float* nm = sh.nm[grp];
     const uint32_t p_row = p_s + static_cast<uint32_t>(grp) * S::kPBytes + static_cast<uint32_t>(key) * N;
     const int swz = N == 64 ? (key >> 1) & 3 : (key >> 2) & 1;
@@ -867,7 +925,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         sts64(at + N * D, lo[0], lo[1]);
         if (e == 0) {
           sh.f[r] = s;
-          sh.row[r] = at_row[i];
+          sh.row[place(r)] = at_row[i];
         }
       }
       if (tid < N) nm[tid] = 0.0f;
@@ -875,20 +933,35 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       named_sync(3, kSoftWarps * 32);
       if (lane == 0) mbar_arrive(smem_addr(&sh.qfull));
 
-      uint64_t l2[N / 2];                              // this token's share of the sums
+      // Per column pair: the queries' scales, minus the references, and this
+      // thread's share of the sums.
+      uint64_t f2[J], nm2[J], l2[J];
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) l2[i] = 0;
+      for (int j = 0; j < J; ++j) {
+        f2[j] = *reinterpret_cast<const uint64_t*>(&sh.f[c0 + 8 * j + col]);
+        nm2[j] = l2[j] = 0;
+      }
       float vref = 0x1p-120f, vscale = kPUnit / 256 / vref;
       bool begun = false, seen = false;                // the accumulator holds earlier tiles; the references a score
       for (int ti = sg.t0; ti < sg.t1; ++ti, ++g) {
         if (!PAIR && (g & 1u) != static_cast<uint32_t>(grp)) continue;
         const uint32_t nth = PAIR ? g : g >> 1;        // this group's job number
         wait(sh.mfull[g % kMetaSlots], (g / kMetaSlots) & 1u, kFaultFullWait);
+        __syncwarp();
         const TileMeta& m = sh.meta[g % kMetaSlots];
-        const bool valid = tile_visible(m, key, page_of, p.mask != nullptr);
-        const float ck = m.ks[page_of], vs = m.vs[page_of];
-        const uint64_t ck2 = pack2(ck, ck);
-        if (!valid) {
+        const bool visible = tile_visible(m, key, page_of, p.mask != nullptr);
+        const unsigned seen_keys = __ballot_sync(0xFFFFFFFFu, visible);
+        // The four tokens' scales (8 consecutive tokens share a page).
+        float ck[4], vs[4];
+        float vtop = -1.0f;                            // largest value scale of this thread's visible tokens
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int page = (wq * 32 + 8 * q) / ps;
+          ck[q] = m.ks[page];
+          vs[q] = (seen_keys >> (8 * q + (lane >> 2))) & 1u ? m.vs[page] : 0.0f;
+          if ((seen_keys >> (8 * q + (lane >> 2))) & 1u) vtop = fmaxf(vtop, vs[q]);
+        }
+        if (!visible) {
           // Codes of tokens that are not visible (any bytes, NaN among them)
           // would meet probabilities of 0: they become zeros.
           wait(sh.vfull[g % ST], (g / ST) & 1u, kFaultFullWait);
@@ -900,54 +973,71 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         wait(sh.sfull[grp], nth & 1u, kFaultFullWait);
         __syncwarp();
         at_fence_after();
-        // Exponents x = score - reference, and the largest of them.
-        uint64_t x[N / 2];
-        auto exponents = [&]() {
-          uint32_t r[2][32];                           // the columns, or their hi and lo sums
-          at_ld32x2(s_t, s_t + 32, r[0], r[1]);
+        // Exponents x[q][j] = score - reference of token q, column pair j; columns
+        // past the rows are not looked at (J is cut to what the rows need).
+        uint64_t x[4][J];
+        {
+          uint32_t r[2][N / 2];                        // of tokens 0 .. 15 and 16 .. 31
           if constexpr (S::kConcat) {
+            uint32_t lo[2][N / 2];
+            at_frag32x4(s_t, s_t + (16u << 16), s_t + N, s_t + N + (16u << 16), r[0], r[1], lo[0], lo[1]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) + __uint_as_float(r[1][i]));
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < N / 2; ++i)
+                r[h][i] = __float_as_uint(__uint_as_float(r[h][i]) + __uint_as_float(lo[h][i]));
+          } else {
+            at_frag64x2(s_t, s_t + (16u << 16), r[0], r[1]);
           }
 #pragma unroll
-          for (int i = 0; i < N; i += 4) {
-            if (i % 16 == 0 && i >= ncols) break;      // (uniform)
-            const uint32_t* q = &r[i / 32][i % 32];
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fq + i);
-            const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(nm + i);
-            x[i / 2] = fma2(at_mul2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), ck2), f.x, n.x);
-            x[i / 2 + 1] = fma2(at_mul2(pack2(__uint_as_float(q[2]), __uint_as_float(q[3])), ck2), f.y, n.y);
+          for (int j = 0; j < J; ++j) {
+            if (j % 2 == 0 && 8 * j >= ncols) break;   // (uniform; ncols is a multiple of 16)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t* v = &r[q >> 1][4 * j + 2 * (q & 1)];
+              x[q][j] = fma2(at_mul2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(ck[q], ck[q])), f2[j],
+                             nm2[j]);
+            }
           }
-        };
-        exponents();
+        }
+        if (seen_keys != 0xFFFFFFFFu) {                // (uniform)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (!((seen_keys >> (8 * q + (lane >> 2))) & 1u))
+#pragma unroll
+              for (int j = 0; j < J; ++j) x[q][j] = pack2(-kInf, -kInf);
+        }
         float over = -kInf;
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          if (i % 8 == 0 && 2 * i >= ncols) break;
-          float a, b;
-          unpack2(x[i], a, b);
-          over = fmaxf(fmaxf(over, a), b);
+        for (int j = 0; j < J; ++j) {
+          if (j % 2 == 0 && 8 * j >= ncols) break;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float a, b;
+            unpack2(x[q][j], a, b);
+            over = fmaxf(fmaxf(over, a), b);
+          }
         }
-        const bool raise = valid && (!seen || over > kSlack || vs > vref);
+        const bool raise = over > kSlack || vtop > vref || (!seen && seen_keys != 0u);
         if (group_any(bar_id, raise)) {                // uniform over the group
           // New references: the largest score of each column so far, and a bit
           // more (a score then has to exceed it eightfold to move it again).
 #pragma unroll
-          for (int c = 0; c < N; c += 32) {
-            float v[32];
+          for (int j = 0; j < J; ++j) {
+            if (j % 2 == 0 && 8 * j >= ncols) break;
+            float ta = -kInf, tb = -kInf;              // (NaN does not set a reference)
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              v[i] = v[i + 1] = -kInf;
-              if (c + (i & ~15) < ncols && valid) {
-                unpack2(x[(c + i) / 2], v[i], v[i + 1]);
-                v[i] = fmaxf(v[i], -kInf);             // (NaN does not set a reference)
-                v[i + 1] = fmaxf(v[i + 1], -kInf);
-              }
+            for (int q = 0; q < 4; ++q) {
+              float a, b;
+              unpack2(x[q][j], a, b);
+              ta = fmaxf(ta, a);
+              tb = fmaxf(tb, b);
             }
-            const float top = column_reduce<true>(v);
-            sh.red[grp][wq][c + lane] = top;
+            ta = over_tokens<true>(ta);
+            tb = over_tokens<true>(tb);
+            if (lane < 4) *reinterpret_cast<uint64_t*>(&sh.red[grp][wq][8 * j + col]) = pack2(ta, tb);
           }
-          const float vmax = warp_max_f32(valid ? vs : 0.0f);
+          const float vmax = warp_max_f32(vtop);
           if (lane == 0) sh.vmax[grp][wq] = vmax;
           named_sync(bar_id, 128);
           const float vnew = fmaxf(vref, fmaxf(fmaxf(sh.vmax[grp][0], sh.vmax[grp][1]),
@@ -961,16 +1051,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             const float d = ex2_approx(-up);
             sh.fac_l[grp][tid] = d;
             // (before any score the accumulator is all zeros, and d may be infinite)
-            sh.fac_o[grp][tid] = seen ? d * (vref / vnew) : 0.0f;
+            sh.fac_o[grp][place(tid)] = seen ? d * (vref / vnew) : 0.0f;
           }
           vref = vnew;
           vscale = kPUnit / 256 / vref;
           named_sync(bar_id, 128);
 #pragma unroll
-          for (int i = 0; i < N / 2; ++i) {
-            if (i % 8 == 0 && 2 * i >= ncols) break;
-            x[i] = add2(x[i], *reinterpret_cast<const uint64_t*>(&sh.delta[grp][2 * i]));
-            if (seen) l2[i] = at_mul2(l2[i], *reinterpret_cast<const uint64_t*>(&sh.fac_l[grp][2 * i]));
+          for (int j = 0; j < J; ++j) {
+            if (j % 2 == 0 && 8 * j >= ncols) break;
+            const uint64_t delta = *reinterpret_cast<const uint64_t*>(&sh.delta[grp][8 * j + col]);
+            nm2[j] = *reinterpret_cast<const uint64_t*>(&nm[8 * j + col]);
+            if (seen) l2[j] = at_mul2(l2[j], *reinterpret_cast<const uint64_t*>(&sh.fac_l[grp][8 * j + col]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q][j] = add2(x[q][j], delta);
           }
           seen = true;
           if (begun) {
@@ -996,29 +1089,27 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         at_fence_before();                             // the scores have been read
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.sempty[grp]));
-        // P of this token: summed in fp32, in three e4m3 parts for the product.
-        if (!valid) {
+        // P: summed in fp32, in three e4m3 parts for the product.
+        uint64_t vr2[4];
 #pragma unroll
-          for (int i = 0; i < N / 2; ++i) x[i] = pack2(-kInf, -kInf);
-        }
-        const float vr = valid ? vs * vscale : 0.0f;   // 2^-8 64 s_v / v_ref
-        const uint64_t vr2 = pack2(vr, vr);
+        for (int q = 0; q < 4; ++q) vr2[q] = pack2(vs[q] * vscale, vs[q] * vscale);   // 2^-8 64 s_v / v_ref
         if (nth >= 1) wait(sh.pvdone[grp], (nth - 1) & 1u, kFaultEmptyWait);   // the product that read this buffer last
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < N; i += 16) {
-          if (i >= ncols) break;
+        for (int jj = 0; jj < J / 2; ++jj) {           // 16 columns
+          if (16 * jj >= ncols) break;
           uint32_t o[3][4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t h[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
+              const int j = 2 * jj + u;
               float a, b;
-              unpack2(x[i / 2 + 2 * q + u], a, b);
+              unpack2(x[q][j], a, b);
               const uint64_t y = pack2(ex2_approx(a), ex2_approx(b));
-              l2[i / 2 + 2 * q + u] = add2(l2[i / 2 + 2 * q + u], y);
-              unpack2(at_mul2(y, vr2), a, b);
+              l2[j] = add2(l2[j], y);
+              unpack2(at_mul2(y, vr2[q]), a, b);
               h[u] = f16x2(a, b);
             }
             o[0][q] = part_codes(h[0], h[1]);
@@ -1027,9 +1118,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             o[1][q] = part_codes(h[0], h[1]);
             o[2][q] = part_codes(part_rest16(h[0]), part_rest16(h[1]));
           }
-          const uint32_t at = p_row + static_cast<uint32_t>((i >> 4) ^ swz) * 16u;
+          const uint32_t at = p_row + static_cast<uint32_t>(jj ^ swz) * 16u;
 #pragma unroll
-          for (int k = 0; k < 3; ++k) sts128(at + k * (kTile * N), o[k][0], o[k][1], o[k][2], o[k][3]);
+          for (int k = 0; k < 3; ++k) stmatrix4(at + k * (kTile * N), o[k][0], o[k][1], o[k][2], o[k][3]);
         }
         begun = true;
         at_fence_async();
@@ -1039,11 +1130,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
       // The segment's sums over its tokens, then its rows.
 #pragma unroll
-      for (int c = 0; c < N; c += 32) {
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) unpack2(l2[(c + i) / 2], v[i], v[i + 1]);
-        sh.red[grp][wq][c + lane] = column_reduce<false>(v);
+      for (int j = 0; j < J; ++j) {
+        float a, b;
+        unpack2(l2[j], a, b);
+        a = over_tokens<false>(a);
+        b = over_tokens<false>(b);
+        if (lane < 4) *reinterpret_cast<uint64_t*>(&sh.red[grp][wq][8 * j + col]) = pack2(a, b);
       }
       if (tid == 0) sh.vref[grp] = vref;
       named_sync(3, kSoftWarps * 32);
@@ -1055,7 +1147,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       const bool both = !PAIR && sg.t1 - sg.t0 >= 2;
       const int first = PAIR ? 0 : static_cast<int>((g - static_cast<uint32_t>(sg.t1 - sg.t0)) & 1u);
       for (int n = threadIdx.x; n < S::kRows; n += kSoftWarps * 32) {
-        const int32_t row = sh.row[n];
+        const int at = place(n);
+        const int32_t row = sh.row[at];
         if (row < 0) continue;
         const int a = PAIR ? n / N : first, c = PAIR ? n % N : n;
         float m = -sh.nm[a][c];
@@ -1078,11 +1171,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           fb *= inv;
           p.lse[row] = l == 0.0f ? -kInf : m * kLn2 + logf(l);
         } else {
-          p.part_ml[(slot * S::kRows + n) * 2] = m;
-          p.part_ml[(slot * S::kRows + n) * 2 + 1] = l;
+          p.part_ml[(slot * S::kRows + at) * 2] = m;
+          p.part_ml[(slot * S::kRows + at) * 2 + 1] = l;
         }
-        sh.fin[a][c] = fa;
-        if (both) sh.fin[first ^ 1][c] = fb;
+        sh.fin[a][place(c)] = fa;
+        if (both) sh.fin[first ^ 1][place(c)] = fb;
       }
       // The last product of either group.
 #pragma unroll
@@ -1182,8 +1275,8 @@ struct WeightShared {
 };
 
 // w[j] = decay w[j] + sum over the rows of exp(s - lse): S^T as in the
-// attention, a thread per token, so a token's sum stays in its thread and
-// nothing is shared or added atomically.  Four groups of 4 warps take the tiles
+// attention; a token's columns lie with four lanes of one warp, so its sum stays
+// there and nothing is added atomically.  Four groups of 4 warps take the tiles
 // in turn; a job is one tile and up to 64 rows.
 // Bound: the products (4 of M 128, N 128, K 32 for a job) and the softmax's
 // issue, since each row's scores are computed once more; K's bytes when rows
@@ -1291,9 +1384,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
       ++seg;
     }
   } else if (warp < kWeightSoft) {
-    const int grp = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
+    const int grp = warp >> 2, wq = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const int page_of = key / p.c.page_size;
     constexpr int kPer = D / 8, kStep = kWeightSoft * 32 / kPer;
     uint32_t jobs = 0;                                 // this group's
     while (next_segment(p, cur, sh.w0, sg)) {
@@ -1335,16 +1427,20 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
       if (lane == 0) mbar_arrive(smem_addr(&sh.qfull));
       for (int ti = sg.t0; ti < sg.t1; ++ti, ++g) {
         if (g % kWeightGroups != static_cast<uint32_t>(grp)) continue;
-        float* wj = p.weights + (static_cast<int64_t>(sg.b) * p.c.heads + sg.h) * p.cap +
-                    static_cast<int64_t>(ti) * kTile + key;
-        const bool in = static_cast<int64_t>(ti) * kTile + key < p.cap;
+        // This thread's tokens are 32 wq + lane / 4 + 8 q; it writes the weight of
+        // the one with q = lane mod 4.
+        const int mine = wq * 32 + 8 * (lane & 3) + (lane >> 2);
+        const int64_t at = static_cast<int64_t>(ti) * kTile + mine;
+        float* wj = p.weights + (static_cast<int64_t>(sg.b) * p.c.heads + sg.h) * p.cap + at;
+        const bool in = at < p.cap;
         const float old = in && p.decay != 0.0f ? *wj : 0.0f;
         wait(sh.mfull[g % kWeightMeta], (g / kWeightMeta) & 1u, kFaultFullWait);
         const TileMeta& m = sh.meta[g % kWeightMeta];
-        const bool valid = tile_visible(m, key, page_of, p.mask != nullptr);
-        const float ck = m.ks[page_of];
-        const uint64_t ck2 = pack2(ck, ck);
-        uint64_t sum2[2] = {0, 0};
+        const bool valid = tile_visible(m, mine, mine / p.c.page_size, p.mask != nullptr);
+        float ck[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ck[q] = m.ks[(wq * 32 + 8 * q) / p.c.page_size];
+        uint64_t sum2[4] = {0, 0, 0, 0};
         for (int c = 0; c < chunks; ++c, ++jobs) {
           const uint32_t buf = static_cast<uint32_t>(grp) * kWeightBufs + jobs % kWeightBufs;
           wait(sh.sfull[buf], (jobs / kWeightBufs) & 1u, kFaultFullWait);
@@ -1352,33 +1448,51 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
           at_fence_after();
           const int cols = min(NC, (rows - c * NC + 15) & ~15);
 #pragma unroll
-          for (int i0 = 0; i0 < NC; i0 += 32) {
-            if (i0 >= cols) break;
-            uint32_t r[32], lo[32];
-            at_ld32x2(tmem + lanes + buf * 2 * NC + i0, tmem + lanes + buf * 2 * NC + NC + i0, r, lo);
+          for (int n = 0; n < NC; n += 32) {
+            if (n >= cols) break;                      // (uniform)
+            uint64_t f2[4], nm2[4];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sh.f + c * NC + i0 + i);
-              const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(sh.nm + c * NC + i0 + i);
-              uint64_t s0 = add2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                                 pack2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
-              uint64_t s1 = add2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
-                                 pack2(__uint_as_float(lo[i + 2]), __uint_as_float(lo[i + 3])));
-              float a0, a1, b0, b1;
-              unpack2(fma2(at_mul2(s0, ck2), f.x, n.x), a0, a1);
-              unpack2(fma2(at_mul2(s1, ck2), f.y, n.y), b0, b1);
-              // (a row that adds nothing has -inf or NaN here)
-              sum2[0] = add2(sum2[0], pack2(ex2_approx(fmaxf(a0, -1e30f)), ex2_approx(fmaxf(a1, -1e30f))));
-              sum2[1] = add2(sum2[1], pack2(ex2_approx(fmaxf(b0, -1e30f)), ex2_approx(fmaxf(b1, -1e30f))));
+            for (int j = 0; j < 4; ++j) {
+              f2[j] = *reinterpret_cast<const uint64_t*>(&sh.f[c * NC + n + 8 * j + 2 * (lane & 3)]);
+              nm2[j] = *reinterpret_cast<const uint64_t*>(&sh.nm[c * NC + n + 8 * j + 2 * (lane & 3)]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {              // tokens 16 h .. 16 h + 15
+              uint32_t r[16], lo[16];
+              const uint32_t s_t = tmem + lanes + (static_cast<uint32_t>(16 * h) << 16) + buf * 2 * NC + n;
+              at_frag32x2(s_t, s_t + NC, r, lo);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (j == 2 && n + 16 >= cols) break;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int q = 2 * h + k, i = 4 * j + 2 * k;
+                  const uint64_t y = add2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                          pack2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+                  float a, b;
+                  unpack2(fma2(at_mul2(y, pack2(ck[q], ck[q])), f2[j], nm2[j]), a, b);
+                  // (a row that adds nothing has -inf or NaN here)
+                  sum2[q] = add2(sum2[q], pack2(ex2_approx(fmaxf(a, -1e30f)), ex2_approx(fmaxf(b, -1e30f))));
+                }
+              }
             }
           }
           at_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh.sempty[buf]));
         }
-        float a, b;
-        unpack2(add2(sum2[0], sum2[1]), a, b);
-        if (in) *wj = fmaf(p.decay, old, valid ? a + b : 0.0f);
+        // A token's columns lie with four lanes.
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float a, b;
+          unpack2(sum2[q], a, b);
+          a += b;
+          a += __shfl_xor_sync(0xFFFFFFFFu, a, 1);
+          a += __shfl_xor_sync(0xFFFFFFFFu, a, 2);
+          if ((lane & 3) == q) sum = a;
+        }
+        if (in) *wj = fmaf(p.decay, old, valid ? sum : 0.0f);
       }
     }
     // Slots past the sequences' last tiles: decayed, or set to 0.
@@ -1426,7 +1540,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   for (int in = blockIdx.y * kJoinRows + warp; in < min(nrows, static_cast<int>(blockIdx.y + 1) * kJoinRows); in += 8) {
     const int rr = row0 + in, l = rr / p.G;
     const int64_t row = (b * p.L + l) * p.Hq + h * p.G + rr % p.G;
-    const int n = in / p.half * columns + in % p.half;   // the row's column (columns: of a softmax group)
+    const int n = place(in / p.half * columns + in % p.half);   // the row's column (columns: of a softmax group)
     // CTA ca's part is its last segment unless the item begins its range; the
     // others' is their first.  The statistics of 32 parts are read at a time.
     const bool late = split.begin(ca) < i0;
