@@ -8,9 +8,7 @@
 // The transposed products.  A tile is 128 tokens of one head.  S^T = K Q^T and
 // O^T += V^T P^T put the tokens (then the head dimension) on the tensor core's
 // 128 rows and the queries on its N columns, so a block of 32 queries, or a
-// single one, costs N = 32 columns and not a padded tile of 128 rows; and a
-// softmax thread holds one token, so masks, page scales and the weights' sums
-// are per-thread values.
+// single one, costs N = 32 columns and not a padded tile of 128 rows.
 //
 // K and V stay in 8 bits from HBM to the tensor core (kind::f8f6f4 on the codes
 // as TMA brought them): what bounds few rows is the bytes of the cache, and
@@ -30,10 +28,11 @@
 // in TMEM are rarely rescaled; statistics and sums are fp32.
 //
 // Measured (head_dim 128, pages of 64 to 128, one GB300, replayed in a graph):
-// single tokens, 32 over 8 heads, 4 sequences of 95000: 131 us, 5.9 TB/s of
-// cache (89 % of a copy); blocks of 32 queries, 32 heads, 8 x 2306 tokens: 46
-// us, 210 TFLOP/s; 112 rows a head, 16 x 5096 tokens, 4 heads: 61 us, 306
-// TFLOP/s, bound by the softmax's issue.
+// single tokens, 32 over 8 heads, 4 sequences of 95000: 130 us, 6.0 TB/s of
+// cache (89 % of a copy); blocks of 32 queries, 32 heads, 8 x 2306 tokens: 45
+// us, 216 TFLOP/s; 224 rows a head, 16 x 5096 tokens, 4 heads: 99 us, 378
+// TFLOP/s, bound by the softmax (a tile's 128 x 112 scores take 4800 clocks of
+// 8 warps, a third of them the three parts of P; products 1500).
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
 #include <cuda_runtime.h>
 
@@ -77,15 +76,6 @@ struct AttendParams {
   float* part_ml;              // (2 ctas, columns, 2)
   int32_t* fault;
 };
-
-// Whether the sequence's token j is attended; its page.
-__device__ __forceinline__ bool visible(const AttendParams& p, int64_t b, int64_t j, int n, int64_t& page) {
-  page = -1;
-  if (j >= n) return false;
-  if (p.mask && p.mask[b * p.mask_stride + j] == 0) return false;
-  page = page_at(p.table, p.width, b, j / p.c.page_size, p.c.pages);
-  return page >= 0;
-}
 
 __device__ __forceinline__ int attend_len(const AttendParams& p, int64_t b) {
   const int64_t n = p.lens[b];
@@ -135,36 +125,15 @@ __device__ __forceinline__ void at_fence_after() { asm volatile("tcgen05.fence::
 // Shared-memory writes of this thread become visible to the tensor core.
 __device__ __forceinline__ void at_fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// C consecutive fp32 columns of this warp's 32 TMEM lanes, one lane a thread.
-template <int C>
-__device__ __forceinline__ void at_ld(uint32_t t, uint32_t (&r)[C]) {
-  static_assert(C == 8 || C == 16 || C == 32, "");
-  if constexpr (C == 8) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(t)
-                 : "memory");
-  } else if constexpr (C == 16) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(t)
-        : "memory");
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(t)
-        : "memory");
-  }
+// 16 consecutive fp32 columns of this warp's 32 TMEM lanes, one lane a thread.
+__device__ __forceinline__ void at_ld16(uint32_t t, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
+      : "memory");
 }
 
 // Fragments: of 16 TMEM lanes (tokens) by 8 j columns, thread t gets the tokens
@@ -195,8 +164,25 @@ __device__ __forceinline__ void at_frag64x2(uint32_t t0, uint32_t t1, uint32_t (
       : "memory");
 }
 
+// 32 columns at each of two places.
+__device__ __forceinline__ void at_frag32x2(uint32_t t0, uint32_t t1, uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
+        "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
+        "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+      : "r"(t0), "r"(t1)
+      : "memory");
+}
+
 // 32 columns at each of four places.
-__device__ __forceinline__ void at_frag32x4(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3, uint32_t (&a)[16], uint32_t (&b)[16], uint32_t (&c)[16], uint32_t (&d)[16]) {
+__device__ __forceinline__ void at_frag32x4(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3, uint32_t (&a)[16],
+                                            uint32_t (&b)[16], uint32_t (&c)[16], uint32_t (&d)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
       "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%64];\n\t"
@@ -296,22 +282,6 @@ __device__ __forceinline__ uint32_t part_rest16(uint32_t h) {
 }
 // The codes of four values: bits 14 .. 7 of the halves of a, then of b.
 __device__ __forceinline__ uint32_t part_codes(uint32_t a, uint32_t b) { return __byte_perm(a << 1, b << 1, 0x7531); }
-
-// 32 columns at each of two places.
-__device__ __forceinline__ void at_frag32x2(uint32_t t0, uint32_t t1, uint32_t (&a)[16], uint32_t (&b)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
-        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
-        "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
-        "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
-      : "r"(t0), "r"(t1)
-      : "memory");
-}
 
 // Combines a value over the 8 lanes that hold the same columns.
 template <bool MAX>
@@ -460,7 +430,7 @@ constexpr int kMetaSlots = 8;
 constexpr float kSlack = 2.0f;                         // log2: how far a score may exceed the reference
 constexpr float kHead = 1.0f;                          // log2: how far a new reference lies above its score
 constexpr float kUnset = -1e30f;                       // stands for the reference of a part without tokens
-constexpr float kPUnit = 64.0f;                        // P is held at 64 p s_v / v_ref: at most 2^(6 + 2) (e4m3 ends at 448)
+constexpr float kPUnit = 64.0f;                        // P is held at 64 p s_v / v_ref <= 2^(6 + 2) (e4m3 ends at 448)
 template <int D, int N, bool PAIR>
 constexpr int attend_smem() {
   using S = AttendShape<N, PAIR>;
@@ -495,10 +465,10 @@ struct AttendShared {
   alignas(16) float fac_l[2][N];
   alignas(16) float delta[2][N];
   float vmax[2][4];
-  alignas(16) float red[2][4][N];                                  // maxima or sums per warp
+  alignas(16) float red[2][4][N];                      // maxima or sums per warp
   float vref[2];
   alignas(16) float fin[2][N];                         // what an accumulator's column is multiplied with at the end
-  alignas(16) int32_t row[AttendShape<N, PAIR>::kRows];            // output rows, -1 where a column has none
+  alignas(16) int32_t row[AttendShape<N, PAIR>::kRows];    // output rows, -1 where a column has none
   uint32_t w0, w1, off0;
   int32_t b0;
   uint32_t tmem;
@@ -782,78 +752,78 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kCopyWarp) {
-    copy_role<D, ST, true>(p, sh, cur, k_s, v_s, wait);
+      copy_role<D, ST, true>(p, sh, cur, k_s, v_s, wait);
     } else if (warp == kMmaWarp) {
-    constexpr uint32_t kPerTile = PAIR ? 2 : 1;        // jobs of a tile
-    constexpr uint32_t kHiK = at_desc_hi(8 * D, kSwz), kHiP = at_desc_hi(8 * N, N == 64 ? 4u : 6u);
-    const uint32_t lead = elect_one();
-    const uint32_t kd = at_desc_lo(k_s, 16), qd = at_desc_lo(q_s, 16), pd = at_desc_lo(p_s, kTile * N);
-    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    // Stage and phase of the next tile whose scores, and whose output product, are issued.
-    uint32_t ss = 0, sp = 0, vs = 0, vp = 0;
-    uint32_t js = 0, jv = 0;                           // jobs issued of either
-    auto scores = [&]() {                              // S^T of job js: K (codes) x (hi, lo)
-      const uint32_t grp = js & 1u;
-      wait(sh.kfull[ss], sp, kFaultFullWait);
-      wait(sh.sempty[grp], ((js >> 1) & 1u) ^ 1u, kFaultEmptyWait);
-      __syncwarp();
-      const bool last = kPerTile == 1 || grp == 1;
-      if (!*abort_flag) {
-        at_fence_after();
-        const uint32_t k = kd + ss * (kTileBytes >> 4), q = qd + (PAIR ? grp * (2 * N * D >> 4) : 0u);
-        const uint32_t d = tm + S::kScore + grp * S::kScoreCols;
-        constexpr int kParts = S::kConcat ? 1 : 2;
-#pragma unroll
-        for (int i = 0; i < kParts * (D / 32); ++i) {
-          const int part = i / (D / 32), kk = i % (D / 32);
-          at_mma_f8(lead, d, k + kk * 2, kHiK, q + part * (N * D / 16) + kk * 2, kHiK,
-                    at_idesc(S::kScoreCols, false), i != 0 ? 1u : 0u);
-        }
-        if (last) at_commit(lead, smem_addr(&sh.kempty[ss]));
-        at_commit(lead, smem_addr(&sh.sfull[grp]));
-      }
-      __syncwarp();
-      ++js;
-      if (last && ++ss == ST) {
-        ss = 0;
-        sp ^= 1u;
-      }
-    };
-    uint32_t seg = 0;
-    while (next_segment(p, cur, sh.w0, sg)) {
-      const uint32_t n = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(sg.t1 - sg.t0) * kPerTile, 0);   // its jobs
-      wait(sh.qfull, seg & 1u, kFaultFullWait);
-      __syncwarp();
-      scores();
-      if (n > 1) scores();
-      for (uint32_t i = 0; i < n; ++i) {
-        const uint32_t grp = jv & 1u;
-        if (i + 2 < n) scores();                       // (job i + 2's, as soon as job i's scores have been read)
-        wait(sh.vfull[vs], vp, kFaultFullWait);
-        wait(sh.pfull[grp], (jv >> 1) & 1u, kFaultFullWait);
+      constexpr uint32_t kPerTile = PAIR ? 2 : 1;        // jobs of a tile
+      constexpr uint32_t kHiK = at_desc_hi(8 * D, kSwz), kHiP = at_desc_hi(8 * N, N == 64 ? 4u : 6u);
+      const uint32_t lead = elect_one();
+      const uint32_t kd = at_desc_lo(k_s, 16), qd = at_desc_lo(q_s, 16), pd = at_desc_lo(p_s, kTile * N);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      // Stage and phase of the next tile whose scores, and whose output product, are issued.
+      uint32_t ss = 0, sp = 0, vs = 0, vp = 0;
+      uint32_t js = 0, jv = 0;                           // jobs issued of either
+      auto scores = [&]() {                              // S^T of job js: K (codes) x (hi, lo)
+        const uint32_t grp = js & 1u;
+        wait(sh.kfull[ss], sp, kFaultFullWait);
+        wait(sh.sempty[grp], ((js >> 1) & 1u) ^ 1u, kFaultEmptyWait);
         __syncwarp();
         const bool last = kPerTile == 1 || grp == 1;
         if (!*abort_flag) {
           at_fence_after();
-          const uint32_t vst = v_s + vs * kTileBytes;
-          const uint32_t v = at_desc_lo(vst, zero_s - vst), pp = pd + grp * (S::kPBytes >> 4);
-          const uint32_t d = tm + S::kAcc + grp * 3 * N;
-#pragma unroll
-          for (int kk = 0; kk < kTile / 32; ++kk)
-            at_mma_f8(lead, d, v + kk * (32 * D >> 4), kHiK, pp + kk * (32 * N >> 4), kHiP, at_idesc(3 * N, true),
-                      kk != 0 || i >= 2 ? 1u : 0u);
-          if (last) at_commit(lead, smem_addr(&sh.vempty[vs]));
-          at_commit(lead, smem_addr(&sh.pvdone[grp]));
+          const uint32_t k = kd + ss * (kTileBytes >> 4), q = qd + (PAIR ? grp * (2 * N * D >> 4) : 0u);
+          const uint32_t d = tm + S::kScore + grp * S::kScoreCols;
+          constexpr int kParts = S::kConcat ? 1 : 2;
+  #pragma unroll
+          for (int i = 0; i < kParts * (D / 32); ++i) {
+            const int part = i / (D / 32), kk = i % (D / 32);
+            at_mma_f8(lead, d, k + kk * 2, kHiK, q + part * (N * D / 16) + kk * 2, kHiK,
+                      at_idesc(S::kScoreCols, false), i != 0 ? 1u : 0u);
+          }
+          if (last) at_commit(lead, smem_addr(&sh.kempty[ss]));
+          at_commit(lead, smem_addr(&sh.sfull[grp]));
         }
         __syncwarp();
-        ++jv;
-        if (last && ++vs == ST) {
-          vs = 0;
-          vp ^= 1u;
+        ++js;
+        if (last && ++ss == ST) {
+          ss = 0;
+          sp ^= 1u;
         }
+      };
+      uint32_t seg = 0;
+      while (next_segment(p, cur, sh.w0, sg)) {
+        const uint32_t n = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(sg.t1 - sg.t0) * kPerTile, 0);   // its jobs
+        wait(sh.qfull, seg & 1u, kFaultFullWait);
+        __syncwarp();
+        scores();
+        if (n > 1) scores();
+        for (uint32_t i = 0; i < n; ++i) {
+          const uint32_t grp = jv & 1u;
+          if (i + 2 < n) scores();                       // (job i + 2's, as soon as job i's scores have been read)
+          wait(sh.vfull[vs], vp, kFaultFullWait);
+          wait(sh.pfull[grp], (jv >> 1) & 1u, kFaultFullWait);
+          __syncwarp();
+          const bool last = kPerTile == 1 || grp == 1;
+          if (!*abort_flag) {
+            at_fence_after();
+            const uint32_t vst = v_s + vs * kTileBytes;
+            const uint32_t v = at_desc_lo(vst, zero_s - vst), pp = pd + grp * (S::kPBytes >> 4);
+            const uint32_t d = tm + S::kAcc + grp * 3 * N;
+  #pragma unroll
+            for (int kk = 0; kk < kTile / 32; ++kk)
+              at_mma_f8(lead, d, v + kk * (32 * D >> 4), kHiK, pp + kk * (32 * N >> 4), kHiP, at_idesc(3 * N, true),
+                        kk != 0 || i >= 2 ? 1u : 0u);
+            if (last) at_commit(lead, smem_addr(&sh.vempty[vs]));
+            at_commit(lead, smem_addr(&sh.pvdone[grp]));
+          }
+          __syncwarp();
+          ++jv;
+          if (last && ++vs == ST) {
+            vs = 0;
+            vp ^= 1u;
+          }
+        }
+        ++seg;
       }
-      ++seg;
-    }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -1075,7 +1045,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
               for (int part = 0; part < 3; ++part) {
                 uint32_t r[16];
-                at_ld<16>(o_t + part * N + c, r);
+                at_ld16(o_t + part * N + c, r);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * sh.fac_o[grp][c + i]);
                 at_st16(o_t + part * N + c, r);
@@ -1668,9 +1638,11 @@ const AttendDevice* attend_device() {
 // The row tiles of a key head and the columns of a tile: as few tiles as 128
 // columns allow, equally filled, then the narrowest built width that holds one
 // (a width is the tensor core's N and the softmax's registers per token).
-// Measured: 32 rows 46.1 us with 32 columns, 57.4 with 64 (8 x 2306 tokens, 32
-// heads); 64 rows 63.3 us taking turns with 64 columns, 76.1 paired (16 x 5096
-// tokens, 8 heads); 112 rows 61.0 us paired, 62.4 as two tiles of 56.
+// Measured: 32 rows 44.7 us with 32 columns, 56.7 with 64 (8 x 2306 tokens, 32
+// heads); 64 rows 62.1 us taking turns with 64 columns, 75.7 paired, 70.0 as two
+// tiles of 32 (16 x 5096 tokens, 8 heads); 112 rows 59.9 us paired, 60.8 as two
+// tiles of 56, 67.7 as four of 28; 224 rows of 2000 to 8192 tokens 99.5 and
+// 105.3 as two of 112 and four of 56.
 struct RowTiles {
   int64_t tiles, rows, half;
   int columns;
