@@ -27,12 +27,13 @@
 // more than 2 (log2 units) or a page's value scale its own, so the accumulators
 // in TMEM are rarely rescaled; statistics and sums are fp32.
 //
-// Measured (head_dim 128, pages of 64 to 128, one GB300, replayed in a graph):
-// single tokens, 32 over 8 heads, 4 sequences of 95000: 130 us, 6.0 TB/s of
-// cache (89 % of a copy); blocks of 32 queries, 32 heads, 8 x 2306 tokens: 45
-// us, 216 TFLOP/s; 224 rows a head, 16 x 5096 tokens, 4 heads: 99 us, 378
-// TFLOP/s, bound by the softmax (a tile's 128 x 112 scores take 4800 clocks of
-// 8 warps, a third of them the three parts of P; products 1500).
+// Measured (head_dim 128, pages of 64 and 128, one GB300, replayed in a graph):
+// single tokens, 32 over 8 heads, 4 sequences of 60001 to 131072: 129 us, 6.06
+// TB/s of cache (91 % of a copy); blocks of 32 queries, 32 heads, 8 x 2306
+// tokens: 43 us, 226 TFLOP/s; 224 rows a head, 16 x 5096 tokens, 4 heads: 95 us,
+// 393 TFLOP/s, bound by the softmax groups' chain of waits and instructions (a
+// tile's 128 x 112 scores take 8 warps 4600 clocks, a third of them the three
+// parts of P; the products 1500).
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
 #include <cuda_runtime.h>
 
@@ -355,6 +356,7 @@ struct Cursor {
   uint32_t w, w1;  // position and end of the CTA's range, in units
   int32_t b;       // batch row at w
   uint32_t off;    // position within the batch row's units
+  int32_t len_of = -1, len = 0;   // a batch row and its length, read once for its items
 };
 
 struct Segment {
@@ -370,7 +372,11 @@ struct Segment {
 __device__ __forceinline__ bool next_segment(const AttendParams& p, Cursor& c, uint32_t w0, Segment& s) {
   while (c.w < c.w1) {
     s.b = c.b;
-    s.len = attend_len(p, c.b);
+    if (c.len_of != c.b) {
+      c.len = attend_len(p, c.b);
+      c.len_of = c.b;
+    }
+    s.len = c.len;
     s.T = s.len > 0 ? (s.len + kTile - 1) / kTile : 1;
     const uint32_t units = static_cast<uint32_t>(s.T + p.seg_cost);
     const uint32_t hr = c.off / units, at = c.off % units;
@@ -836,7 +842,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     const int col = 2 * (lane & 3);
     const uint32_t bar_id = 1u + static_cast<uint32_t>(grp);
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const int page_of = key / ps;
+    const int ps_log = __ffs(ps) - 1, page_of = key >> ps_log;   // (page sizes are powers of two)
     const int c0 = PAIR ? grp * N : 0;                 // the group's first column
     float* nm = sh.nm[grp];
     const uint32_t p_row = p_s + static_cast<uint32_t>(grp) * S::kPBytes + static_cast<uint32_t>(key) * N;
@@ -848,16 +854,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     constexpr int kLoads = S::kRows / kStep;
     static_assert(S::kRows % kStep == 0 && N % kStep == 0, "");
     const int step_l = kStep / p.G, step_g = kStep % p.G;
-    while (next_segment(p, cur, sh.w0, sg)) {
-      // The queries: one power-of-two scale per row and two e4m3 parts.
-      const int row0 = sg.rt * p.tile_rows;
-      const int nrows = min(p.tile_rows, p.rows - row0);
-      // columns of this group that hold rows, in 16s
-      const int mine = PAIR ? min(p.half, nrows - grp * p.half) : nrows;
-      const int ncols = (mine + 15) & ~15;
-      const int r0 = threadIdx.x / kPer, e = threadIdx.x % kPer;
-      uint4 xq[kLoads];
-      int32_t at_row[kLoads];
+    const int r0 = threadIdx.x / kPer, e = threadIdx.x % kPer;
+    uint4 xq[kLoads];
+    int32_t at_row[kLoads];
+    // This thread's part of a segment's rows.  With 32 columns the next segment's
+    // are fetched before this one's sums and epilogue (8 x 2306 tokens, 32 rows of
+    // 32 heads: 43.5 us, 44.4 without); with 64 the registers do not reach (114
+    // us, 98.9 without, for 224 rows).
+    constexpr bool kAhead = N == 32;
+    auto fetch_rows = [&](const Segment& s) {
+      const int row0 = s.rt * p.tile_rows, nrows = min(p.tile_rows, p.rows - row0);
       // row -> (query l, head of the group), stepped by kStep columns at a time
       int l = (row0 + r0) / p.G, gq = (row0 + r0) % p.G;
       int lw = PAIR ? (row0 + p.half + r0) / p.G : 0, gw = PAIR ? (row0 + p.half + r0) % p.G : 0;
@@ -872,9 +878,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           gq = gw;
         }
         if (rr < nrows && (!PAIR || in < p.half)) {
-          const int hq = sg.h * p.G + gq;
-          xq[i] = *reinterpret_cast<const uint4*>(p.q + sg.b * p.qb + l * p.ql + hq * p.qh + e * 16);
-          at_row[i] = static_cast<int32_t>((sg.b * p.L + l) * p.Hq + hq);
+          const int hq = s.h * p.G + gq;
+          xq[i] = *reinterpret_cast<const uint4*>(p.q + s.b * p.qb + l * p.ql + hq * p.qh + e * 16);
+          at_row[i] = static_cast<int32_t>((s.b * p.L + l) * p.Hq + hq);
         }
         l += step_l;
         gq += step_g;
@@ -883,6 +889,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           ++l;
         }
       }
+    };
+    Segment ahead;
+    bool more = next_segment(p, cur, sh.w0, ahead);
+    if (kAhead && more) fetch_rows(ahead);
+    while (more) {
+      sg = ahead;
+      if (!kAhead) fetch_rows(sg);
+      // The queries: one power-of-two scale per row and two e4m3 parts.
+      // Columns of this group that hold rows, in 16s:
+      const int nrows = min(p.tile_rows, p.rows - sg.rt * p.tile_rows);
+      const int mine = PAIR ? min(p.half, nrows - grp * p.half) : nrows;
+      const int ncols = (mine + 15) & ~15;
       named_sync(3, kSoftWarps * 32);                  // the previous segment's rows and references are no longer read
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -926,7 +944,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         float vtop = -1.0f;                            // largest value scale of this thread's visible tokens
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int page = (wq * 32 + 8 * q) / ps;
+          const int page = (wq * 32 + 8 * q) >> ps_log;
           ck[q] = m.ks[page];
           vs[q] = (seen_keys >> (8 * q + (lane >> 2))) & 1u ? m.vs[page] : 0.0f;
           if ((seen_keys >> (8 * q + (lane >> 2))) & 1u) vtop = fmaxf(vtop, vs[q]);
@@ -1098,6 +1116,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (lane == 0) mbar_arrive(smem_addr(&sh.pfull[grp]));
       }
 
+      if (kAhead) {
+        more = next_segment(p, cur, sh.w0, ahead);
+        if (more) fetch_rows(ahead);
+      }
+
       // The segment's sums over its tokens, then its rows.
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -1202,6 +1225,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
       }
       at_fence_before();
+      if (!kAhead) more = next_segment(p, cur, sh.w0, ahead);
     }
   }
   at_fence_before();
@@ -1354,7 +1378,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
       ++seg;
     }
   } else if (warp < kWeightSoft) {
-    const int grp = warp >> 2, wq = warp & 3;
+    const int grp = warp >> 2, wq = warp & 3, ps_log = __ffs(p.c.page_size) - 1;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     constexpr int kPer = D / 8, kStep = kWeightSoft * 32 / kPer;
     uint32_t jobs = 0;                                 // this group's
@@ -1406,10 +1430,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
         const float old = in && p.decay != 0.0f ? *wj : 0.0f;
         wait(sh.mfull[g % kWeightMeta], (g / kWeightMeta) & 1u, kFaultFullWait);
         const TileMeta& m = sh.meta[g % kWeightMeta];
-        const bool valid = tile_visible(m, mine, mine / p.c.page_size, p.mask != nullptr);
+        const bool valid = tile_visible(m, mine, mine >> ps_log, p.mask != nullptr);
         float ck[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) ck[q] = m.ks[(wq * 32 + 8 * q) / p.c.page_size];
+        for (int q = 0; q < 4; ++q) ck[q] = m.ks[(wq * 32 + 8 * q) >> ps_log];
         uint64_t sum2[4] = {0, 0, 0, 0};
         for (int c = 0; c < chunks; ++c, ++jobs) {
           const uint32_t buf = static_cast<uint32_t>(grp) * kWeightBufs + jobs % kWeightBufs;
@@ -1638,11 +1662,12 @@ const AttendDevice* attend_device() {
 // The row tiles of a key head and the columns of a tile: as few tiles as 128
 // columns allow, equally filled, then the narrowest built width that holds one
 // (a width is the tensor core's N and the softmax's registers per token).
-// Measured: 32 rows 44.7 us with 32 columns, 56.7 with 64 (8 x 2306 tokens, 32
-// heads); 64 rows 62.1 us taking turns with 64 columns, 75.7 paired, 70.0 as two
-// tiles of 32 (16 x 5096 tokens, 8 heads); 112 rows 59.9 us paired, 60.8 as two
-// tiles of 56, 67.7 as four of 28; 224 rows of 2000 to 8192 tokens 99.5 and
-// 105.3 as two of 112 and four of 56.
+// Measured (in a build whose tiles took 4 % longer throughout): 32 rows 44.7 us
+// with 32 columns, 56.7 with 64 (8 x 2306 tokens, 32 heads); 64 rows 62.1 us
+// taking turns with 64 columns, 75.7 paired, 70.0 as two tiles of 32 (16 x 5096
+// tokens, 8 heads); 112 rows 59.9 us paired, 60.8 as two tiles of 56, 67.7 as
+// four of 28; 224 rows of 2000 to 8192 tokens 99.5 us as two of 112, 105.3 as
+// four of 56.
 struct RowTiles {
   int64_t tiles, rows, half;
   int columns;
