@@ -1509,38 +1509,60 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
 // Joins the parts of the items that several CTAs share, in CTA order (a part's
 // reference may differ from the others').  Block (x, y) looks at the boundary
 // between CTAs x and x + 1: if an item is cut there for the first time, its
-// warps join rows 8 y .. 8 y + 7 of it, one each.
+// warps join rows 8 y .. 8 y + 7 of it, one each.  Where the item lies takes some
+// 500 instructions, which one warp runs for the block (224 rows a head, 16 x 5096
+// tokens, attention included: 92.8 us, 94.9 when every warp ran them; 8 x 2306
+// tokens, 32 rows of 32 heads: 41.8 us, 44.1 and 47.9 with 16 and 32 rows a
+// block).
 constexpr int kJoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p, int N, int columns) {
+  constexpr int V = D / 32;                            // dimensions of a lane
+  __shared__ uint32_t s_ca, s_cb;
+  __shared__ int32_t s_b, s_item, s_late;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
-  const uint32_t total = all_units(p) * hr;
-  const Split split(total, static_cast<uint32_t>(p.ctas));
-  const uint32_t w = split.begin(blockIdx.x + 1);
-  if (w >= total) return;
-  int32_t b;
-  uint32_t before;
-  find_row(p, hr, w, b, before);
-  const uint32_t units = units_of(p, b);
-  const uint32_t item = (w - before) / units, i0 = before + item * units;   // the item's units: [i0, i0 + units)
-  // its first tile and its last one
-  const uint32_t ca = split.owner(i0 + p.seg_cost), cb = split.owner(i0 + units - 1);
-  if (ca != blockIdx.x || ca == cb) return;            // no part before this boundary, or cut before already
-  const int h = static_cast<int>(item) / p.row_tiles, row0 = static_cast<int>(item) % p.row_tiles * p.tile_rows;
+  if (warp == 0) {
+    const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
+    const uint32_t total = all_units(p) * hr;
+    const Split split(total, static_cast<uint32_t>(p.ctas));
+    const uint32_t w = split.begin(blockIdx.x + 1);
+    uint32_t ca = 0, cb = 0, before, item = 0, i0 = 0;
+    int32_t b = 0;
+    if (w < total) {
+      find_row(p, hr, w, b, before);
+      const uint32_t units = units_of(p, b);
+      item = (w - before) / units;
+      i0 = before + item * units;                      // the item's units: [i0, i0 + units)
+      ca = split.owner(i0 + p.seg_cost);               // its first tile's CTA and its last one's
+      cb = split.owner(i0 + units - 1);
+      if (ca != blockIdx.x) cb = ca;                   // no part before this boundary, or cut before already
+    }
+    if (lane == 0) {
+      s_ca = ca;
+      s_cb = cb;
+      s_b = b;
+      s_item = static_cast<int32_t>(item);
+      s_late = split.begin(ca) < i0;
+    }
+  }
+  __syncthreads();
+  const uint32_t ca = s_ca, cb = s_cb;
+  if (ca == cb) return;
+  // CTA ca's part is its last segment unless the item begins its range; the
+  // others' is their first.  The statistics of 32 parts are read at a time.
+  const int64_t b = s_b;
+  const int h = s_item / p.row_tiles, row0 = s_item % p.row_tiles * p.tile_rows;
   const int nrows = min(p.tile_rows, p.rows - row0);
+  const uint32_t first = 2 * ca + static_cast<uint32_t>(s_late);
   for (int in = blockIdx.y * kJoinRows + warp; in < min(nrows, static_cast<int>(blockIdx.y + 1) * kJoinRows); in += 8) {
     const int rr = row0 + in, l = rr / p.G;
-    const int64_t row = (b * p.L + l) * p.Hq + h * p.G + rr % p.G;
-    const int n = place(in / p.half * columns + in % p.half);   // the row's column (columns: of a softmax group)
-    // CTA ca's part is its last segment unless the item begins its range; the
-    // others' is their first.  The statistics of 32 parts are read at a time.
-    const bool late = split.begin(ca) < i0;
-    auto slot_of = [&](uint32_t c) { return static_cast<int64_t>(2 * c + (c == ca && late ? 1 : 0)); };
+    const int64_t row = (b * p.L + l) * p.Hq + h * p.G + (rr - l * p.G);
+    const int n = place(in >= p.half ? in - p.half + columns : in);   // the row's column (columns: of a softmax group)
+    auto slot_of = [&](uint32_t c) { return static_cast<int64_t>(c == ca ? first : 2 * c); };
     float m = kUnset, sum = 0.0f;
-    float o[D / 32] = {};
+    float o[V] = {};
     for (uint32_t c0 = ca; c0 <= cb; c0 += 32) {
       const uint32_t c = c0 + lane;
       float mc = -kInf, lc = 0.0f;
@@ -1556,24 +1578,35 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
       for (int k = 16; k > 0; k >>= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, k);
       sum = sum * fa + add;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] *= fa;
+      for (int i = 0; i < V; ++i) o[i] *= fa;
       const int parts = static_cast<int>(cb - c0 + 1 < 32 ? cb - c0 + 1 : 32);
 #pragma unroll 4
       for (int k = 0; k < parts; ++k) {
         const float f = __shfl_sync(0xFFFFFFFFu, fb, k);
-        const float* src = p.part_o + (slot_of(c0 + k) * N + n) * D + lane;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = fmaf(__ldcg(src + i * 32), f, o[i]);
+        const float* src = p.part_o + (slot_of(c0 + k) * N + n) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          o[0] = fmaf(x.x, f, o[0]);
+          o[1] = fmaf(x.y, f, o[1]);
+          o[2] = fmaf(x.z, f, o[2]);
+          o[3] = fmaf(x.w, f, o[3]);
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          o[0] = fmaf(x.x, f, o[0]);
+          o[1] = fmaf(x.y, f, o[1]);
+        }
       }
       m = now;
     }
+    uint32_t u[V / 2];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint16_t u;
-      const float y = sum == 0.0f ? 0.0f : o[i] / sum;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(y));
-      p.out[row * D + i * 32 + lane] = u;
+    for (int i = 0; i < V / 2; ++i) {
+      const float lo = sum == 0.0f ? 0.0f : o[2 * i] / sum, hi = sum == 0.0f ? 0.0f : o[2 * i + 1] / sum;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(hi), "f"(lo));
     }
+    uint16_t* to = p.out + row * D + lane * V;
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
+    else *reinterpret_cast<uint32_t*>(to) = u[0];
     if (lane == 0) p.lse[row] = sum == 0.0f ? -kInf : m * kLn2 + logf(sum);
   }
 }
