@@ -28,10 +28,10 @@
 // in TMEM are rarely rescaled; statistics and sums are fp32.
 //
 // Measured (head_dim 128, pages of 64 and 128, one GB300, replayed in a graph):
-// single tokens, 32 over 8 heads, 4 sequences of 60001 to 131072: 129 us, 6.06
-// TB/s of cache (91 % of a copy); blocks of 32 queries, 32 heads, 8 x 2306
-// tokens: 43 us, 226 TFLOP/s; 224 rows a head, 16 x 5096 tokens, 4 heads: 95 us,
-// 393 TFLOP/s, bound by the softmax groups' chain of waits and instructions (a
+// single tokens, 32 over 8 heads, 4 sequences of 60001 to 131072: 123 us, 6.3
+// TB/s of cache (95 % of a copy); blocks of 32 queries, 32 heads, 8 x 2306
+// tokens: 40 us, 243 TFLOP/s; 224 rows a head, 16 x 5096 tokens, 4 heads: 92 us,
+// 408 TFLOP/s, bound by the softmax groups' chain of waits and instructions (a
 // tile's 128 x 112 scores take 8 warps 4600 clocks, a third of them the three
 // parts of P; the products 1500).
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
@@ -79,7 +79,7 @@ struct AttendParams {
 };
 
 __device__ __forceinline__ int attend_len(const AttendParams& p, int64_t b) {
-  const int64_t n = p.lens[b];
+  const int64_t n = __ldcg(p.lens + b);
   return static_cast<int>(n < 0 ? 0 : (n > p.cap ? p.cap : n));
 }
 
@@ -720,8 +720,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  pdl_launch_dependents();
+  // In this order: what the launches behind this one (the join and the weights)
+  // read before their own wait, the call's inputs, is then complete.
   pdl_wait();
+  pdl_launch_dependents();
   if (warp == 0) plan_range(p, sh);
   if (D == 64)       // the upper 64 rows of V^T: zeros
     for (int i = threadIdx.x; i < kTileBytes / 16; i += kAttendThreads)
@@ -1310,7 +1312,6 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_launch_dependents();
-  pdl_wait();
   if (warp == 0) plan_range(p, sh);
   at_fence_before();
   __syncthreads();
@@ -1382,6 +1383,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     constexpr int kPer = D / 8, kStep = kWeightSoft * 32 / kPer;
     uint32_t jobs = 0;                                 // this group's
+    pdl_wait();   // the rows' lse (the copies and the plan, which need the call's inputs only, do not wait: 2 us less)
     while (next_segment(p, cur, sh.w0, sg)) {
       named_sync(5, kWeightSoft * 32);                  // (the previous segment's rows are no longer read)
       const int e = threadIdx.x % kPer;
@@ -1513,7 +1515,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
 // 500 instructions, which one warp runs for the block (224 rows a head, 16 x 5096
 // tokens, attention included: 92.8 us, 94.9 when every warp ran them; 8 x 2306
 // tokens, 32 rows of 32 heads: 41.8 us, 44.1 and 47.9 with 16 and 32 rows a
-// block).
+// block).  It does so before the attention ends: one microsecond less (12.4 us,
+// 11.3 so, for a single token over 1999).
 constexpr int kJoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p, int N, int columns) {
@@ -1522,7 +1525,6 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   __shared__ int32_t s_b, s_item, s_late;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
-  pdl_wait();
   if (warp == 0) {
     const uint32_t hr = static_cast<uint32_t>(p.c.heads * p.row_tiles);
     const uint32_t total = all_units(p) * hr;
@@ -1547,6 +1549,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
       s_late = split.begin(ca) < i0;
     }
   }
+  pdl_wait();                                          // (until here only the lengths were read)
   __syncthreads();
   const uint32_t ca = s_ca, cb = s_cb;
   if (ca == cb) return;
@@ -1695,7 +1698,7 @@ const AttendDevice* attend_device() {
 // The row tiles of a key head and the columns of a tile: as few tiles as 128
 // columns allow, equally filled, then the narrowest built width that holds one
 // (a width is the tensor core's N and the softmax's registers per token).
-// Measured (in a build whose tiles took 4 % longer throughout): 32 rows 44.7 us
+// Measured (in a build that took 2 to 5 us longer throughout): 32 rows 44.7 us
 // with 32 columns, 56.7 with 64 (8 x 2306 tokens, 32 heads); 64 rows 62.1 us
 // taking turns with 64 columns, 75.7 paired, 70.0 as two tiles of 32 (16 x 5096
 // tokens, 8 heads); 112 rows 59.9 us paired, 60.8 as two tiles of 56, 67.7 as
