@@ -1247,9 +1247,10 @@ constexpr int kWeightStages = 8;       // of the K ring
 constexpr int kWeightGroups = 4;
 constexpr int kWeightSoft = 4 * kWeightGroups, kWeightCopyWarp = kWeightSoft, kWeightMmaWarp = kWeightSoft + 1;
 constexpr int kWeightThreads = (kWeightSoft + 2) * 32;
-constexpr int kWeightBufs = 1;         // score buffers of a group: the queries' hi and lo parts as 2 x 64 columns
-// The products run up to 4 tiles ahead of the softmax and the copies 8 ahead of
-// the products: a tile's meta slot is free again after 16.
+constexpr int kWeightBufs = 2;         // score buffers of a group
+// While a group works on tile t the products get to tile t + 7 at most (t + 8
+// needs its buffer) and the copies 8 tiles further: a tile's meta slot is free
+// again after 16.
 constexpr int kWeightMeta = 16;
 
 constexpr int weights_smem(int dim, int chunks) {
@@ -1274,9 +1275,11 @@ struct WeightShared {
 // attention; a token's columns lie with four lanes of one warp, so its sum stays
 // there and nothing is added atomically.  Four groups of 4 warps take the tiles
 // in turn; a job is one tile and up to 64 rows.
-// Bound: the products (4 of M 128, N 128, K 32 for a job) and the softmax's
-// issue, since each row's scores are computed once more; K's bytes when rows
-// are few.  Measured, 224 rows a head, 16 x 5096 tokens, 4 heads: 48 us.
+// Bound: the softmax's chain of waits and instructions (50 % of the issue slots),
+// since each row's scores are computed once more; K's bytes when rows are few.
+// The hi and lo parts add up in one buffer of 64 columns, so a group has two (one
+// of 128, both parts in one product: 2.7 us more).  Measured, 224 rows a head, 16
+// x 5096 tokens, 4 heads: 42 us.
 template <int D>
 __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const __grid_constant__ AttendParams p,
                                                                            int32_t first_row, int32_t rows) {
@@ -1365,9 +1368,11 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
               at_fence_after();
               const uint32_t k = kd + st * (kTileBytes >> 4);
 #pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                at_mma_f8(lead, tm + buf * 2 * NC, k + kk * 2, kHiK, q + kk * 2, kHiK, at_idesc(2 * NC, false),
-                          kk != 0 ? 1u : 0u);
+              for (int i = 0; i < 2 * (D / 32); ++i) {   // hi parts, then lo parts
+                const int part = i / (D / 32), kk = i % (D / 32);
+                at_mma_f8(lead, tm + buf * NC, k + kk * 2, kHiK, q + part * (NC * D / 16) + kk * 2, kHiK,
+                          at_idesc(NC, false), i != 0 ? 1u : 0u);
+              }
               if (c == chunks - 1) at_commit(lead, smem_addr(&sh.kempty[st]));
               at_commit(lead, smem_addr(&sh.sfull[buf]));
             }
@@ -1452,24 +1457,20 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
               f2[j] = *reinterpret_cast<const uint64_t*>(&sh.f[c * NC + n + 8 * j + 2 * (lane & 3)]);
               nm2[j] = *reinterpret_cast<const uint64_t*>(&sh.nm[c * NC + n + 8 * j + 2 * (lane & 3)]);
             }
+            uint32_t r[2][16];                         // tokens 0 .. 15 and 16 .. 31
+            const uint32_t s_t = tmem + lanes + buf * NC + n;
+            at_frag32x2(s_t, s_t + (16u << 16), r[0], r[1]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {              // tokens 16 h .. 16 h + 15
-              uint32_t r[16], lo[16];
-              const uint32_t s_t = tmem + lanes + (static_cast<uint32_t>(16 * h) << 16) + buf * 2 * NC + n;
-              at_frag32x2(s_t, s_t + NC, r, lo);
+            for (int j = 0; j < 4; ++j) {
+              if (j == 2 && n + 16 >= cols) break;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (j == 2 && n + 16 >= cols) break;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int q = 2 * h + k, i = 4 * j + 2 * k;
-                  const uint64_t y = add2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                                          pack2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
-                  float a, b;
-                  unpack2(fma2(at_mul2(y, pack2(ck[q], ck[q])), f2[j], nm2[j]), a, b);
-                  // (a row that adds nothing has -inf or NaN here)
-                  sum2[q] = add2(sum2[q], pack2(ex2_approx(fmaxf(a, -1e30f)), ex2_approx(fmaxf(b, -1e30f))));
-                }
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t* y = &r[q >> 1][4 * j + 2 * (q & 1)];
+                float a, b;
+                unpack2(fma2(at_mul2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(ck[q], ck[q])), f2[j],
+                             nm2[j]), a, b);
+                // (a row that adds nothing has -inf or NaN here)
+                sum2[q] = add2(sum2[q], pack2(ex2_approx(fmaxf(a, -1e30f)), ex2_approx(fmaxf(b, -1e30f))));
               }
             }
           }
