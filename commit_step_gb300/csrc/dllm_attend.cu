@@ -1516,12 +1516,16 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
 // 500 instructions, which one warp runs for the block (224 rows a head, 16 x 5096
 // tokens, attention included: 92.8 us, 94.9 when every warp ran them; 8 x 2306
 // tokens, 32 rows of 32 heads: 41.8 us, 44.1 and 47.9 with 16 and 32 rows a
-// block).  It does so before the attention ends: one microsecond less (12.4 us,
-// 11.3 so, for a single token over 1999).
+// block).  It does so before the attention ends (12.4 us, 11.3 so, for a single
+// token over 1999), and asks for two parts' rows before their factors are known
+// (11.3 us, 9.9 so).
 constexpr int kJoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p, int N, int columns) {
   constexpr int V = D / 32;                            // dimensions of a lane
+  struct PartV {
+    float v[V];
+  };
   __shared__ uint32_t s_ca, s_cb;
   __shared__ int32_t s_b, s_item, s_late;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1567,6 +1571,19 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     auto slot_of = [&](uint32_t c) { return static_cast<int64_t>(c == ca ? first : 2 * c); };
     float m = kUnset, sum = 0.0f;
     float o[V] = {};
+    auto part = [&](uint32_t c) {
+      PartV x;
+      const float* src = p.part_o + (slot_of(c) * N + n) * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+        x.v[0] = y.x, x.v[1] = y.y, x.v[2] = y.z, x.v[3] = y.w;
+      } else {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+        x.v[0] = y.x, x.v[1] = y.y;
+      }
+      return x;
+    };
+    const PartV x0 = part(ca), x1 = part(ca + 1);      // (at least two: asked for before their factors are known)
     for (uint32_t c0 = ca; c0 <= cb; c0 += 32) {
       const uint32_t c = c0 + lane;
       float mc = -kInf, lc = 0.0f;
@@ -1584,22 +1601,17 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 #pragma unroll
       for (int i = 0; i < V; ++i) o[i] *= fa;
       const int parts = static_cast<int>(cb - c0 + 1 < 32 ? cb - c0 + 1 : 32);
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) {
+      auto add_part = [&](const PartV& x, int k) {
         const float f = __shfl_sync(0xFFFFFFFFu, fb, k);
-        const float* src = p.part_o + (slot_of(c0 + k) * N + n) * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-          o[0] = fmaf(x.x, f, o[0]);
-          o[1] = fmaf(x.y, f, o[1]);
-          o[2] = fmaf(x.z, f, o[2]);
-          o[3] = fmaf(x.w, f, o[3]);
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-          o[0] = fmaf(x.x, f, o[0]);
-          o[1] = fmaf(x.y, f, o[1]);
-        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf(x.v[i], f, o[i]);
+      };
+      if (c0 == ca) {
+        add_part(x0, 0);
+        add_part(x1, 1);
       }
+#pragma unroll 4
+      for (int k = c0 == ca ? 2 : 0; k < parts; ++k) add_part(part(c0 + k), k);
       m = now;
     }
     uint32_t u[V / 2];
