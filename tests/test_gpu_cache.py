@@ -191,6 +191,18 @@ def test_attention_many_sequences(cs):
     check_attention(cs, arrays, queries(rng, B, 2, 2, dim), tables(rng, B * width, B, width), lens)
 
 
+@pytest.mark.parametrize("dim,L", [(64, 12), (128, 12), (64, 25), (128, 25)])
+def test_attention_many_items_a_cta(cs, dim, L):
+    """48 and 100 rows of ragged sequences, several to a CTA, cut anywhere."""
+    rng = np.random.default_rng(dim + L)
+    ps, H, G, B, width = 32, 2, 4, 110, 16
+    lens = rng.integers(0, width * ps + 1, B).astype(np.int32)
+    arrays = random_pool(rng, B * width, H, ps, dim)
+    mask = (rng.random((B, width * ps)) < 0.9).astype(np.uint8)
+    mask[::7] = 0
+    check_attention(cs, arrays, queries(rng, B, L, H * G, dim), tables(rng, B * width, B, width), lens, mask=mask)
+
+
 @pytest.mark.parametrize("L", [1, 40])
 def test_attention_mask_holes_and_garbage(cs, L):
     """Masked tokens, slots past the length and pages that do not exist hold NaN
