@@ -1732,9 +1732,10 @@ RowTiles row_tiles(int64_t rows) {
 
 // What an item costs besides its tiles, in tiles (about 7000 cycles against
 // 1500, 2500 and 4800 a tile).  With fewer tiles than SMs there is nothing to
-// balance, and each tile is a CTA's.  Measured: 32 sequences of 100 to 4096
-// tokens, 4 rows of 8 heads, 89 us without and 42 with; 8 of 517 to 4096, 32
-// rows of 32 heads, 68 and 54.
+// balance, and each tile is a CTA's.  Measured in an earlier build: 32 sequences
+// of 100 to 4096 tokens, 4 rows of 8 heads, 89 us without and 42 with; 8 of 517
+// to 4096, 32 rows of 32 heads, 68 and 54.  One tile more or less: within 2 %, and
+// 37 us against 40 where one less is worst (the 32 sequences).
 constexpr int32_t kSegCost32 = 4, kSegCost64 = 3, kSegCost128 = 2;
 
 constexpr size_t kAttendHeader = 256;  // the fault word
