@@ -27,7 +27,8 @@
 // more than 2 (log2 units) or a page's value scale its own, so the accumulators
 // in TMEM are rarely rescaled; statistics and sums are fp32.
 //
-// Measured (head_dim 128, pages of 64 and 128, one GB300, replayed in a graph):
+// Measured (head_dim 128, pages of 64 and 128 with one scale, where references
+// rise in few tiles, one GB300, replayed in a graph):
 // single tokens, 32 over 8 heads, 4 sequences of 60001 to 131072: 123 us, 6.3
 // TB/s of cache (95 % of a copy); blocks of 32 queries, 32 heads, 8 x 2306
 // tokens: 40 us, 243 TFLOP/s; 224 rows a head, 16 x 5096 tokens, 4 heads: 92 us,
