@@ -141,13 +141,20 @@ _WS_AT = {}
 _NEED = {}
 
 
-def _attention_ws(B, L, Hq, cache: KVCache, raw: int, stream) -> torch.Tensor:
-    """A workspace for the call, cached per device and stream.  What it has to
-    hold goes by the rows of a key head and the head size alone."""
-    size = (cache.index, L * Hq // cache.heads, cache.head_dim)
+def _attention_need(L: int, Hq: int, cache: KVCache) -> int:
+    """The bytes of workspace that L queries of Hq heads per sequence need, however
+    many sequences there are.  Kept by all that the library's answer depends on:
+    a size asked for by a call that is empty or refused must answer no other."""
+    size = (cache.index, L, Hq, cache.heads, cache.head_dim)
     need = _NEED.get(size)
     if need is None:
-        need = _NEED[size] = int(_lib.dllm_cache_attention_workspace_size(B, L, Hq, cache.heads, cache.head_dim))
+        need = _NEED[size] = int(_lib.dllm_cache_attention_workspace_size(1, L, Hq, cache.heads, cache.head_dim))
+    return need
+
+
+def _attention_ws(L, Hq, cache: KVCache, raw: int, stream) -> torch.Tensor:
+    """A workspace for the call, cached per device and stream."""
+    need = _attention_need(L, Hq, cache)
     ws = _WS_AT.get((cache.index, raw))
     if ws is None or ws.numel() < need:
         ws = _empty((max(need, 1 << 16),), torch.uint8, cache.device, stream)
@@ -187,7 +194,7 @@ def cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, l
         lse_at = _at(lse, "lse", B * L * Hq, _F32, idx, dev)
     raw = _raw_stream(stream, idx)
     if ws is None:
-        ws = _attention_ws(B, L, Hq, cache, raw, stream)
+        ws = _attention_ws(L, Hq, cache, raw, stream)
     _check(_lib.dllm_cache_attention(cache._ref, q.data_ptr(), strides, B, L, Hq, table, width,
                                      _at(lens, "lens", B, _I32, idx, dev),
                                      _at_or_none(key_mask, "key_mask", B * cap, _MASK, idx, dev),
