@@ -4,6 +4,7 @@ attending over them, and evicting the least attended (``dllm_cache_append``,
 from __future__ import annotations
 
 import ctypes as C
+import threading
 from typing import Optional
 
 import torch
@@ -135,9 +136,6 @@ def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: t
            "dllm_cache_append")
 
 
-_WS_AT = {}
-
-
 _NEED = {}
 
 
@@ -152,16 +150,26 @@ def _attention_need(L: int, Hq: int, cache: KVCache) -> int:
     return need
 
 
-def _attention_ws(L, Hq, cache: KVCache, raw: int, stream) -> torch.Tensor:
-    """A workspace for the call, cached per device and stream."""
+_KEPT = threading.local()
+
+
+def _attention_ws(L: int, Hq: int, cache: KVCache, raw: int) -> torch.Tensor:
+    """A workspace for a call on the current stream.  A call's launches pass its
+    parts on through it, so it is kept for later calls of the same host thread on
+    the same stream only: those of another thread may be enqueued in between.  A
+    call that is captured gets memory of its graph's, which is not kept, and no
+    kept one, which a later call may replace.  (Allocated anew for every call,
+    large blocks cost the host 2 to 5 of its 16 us for a single token.)"""
     need = _attention_need(L, Hq, cache)
-    ws = _WS_AT.get((cache.index, raw))
+    if torch.cuda.is_current_stream_capturing():
+        return _empty((need,), torch.uint8, cache.device, None)
+    try:
+        kept = _KEPT.ws
+    except AttributeError:
+        kept = _KEPT.ws = {}
+    ws = kept.get((cache.index, raw))
     if ws is None or ws.numel() < need:
-        ws = _empty((max(need, 1 << 16),), torch.uint8, cache.device, stream)
-        with torch.cuda.stream(torch.cuda.current_stream(cache.device) if stream is None else stream):
-            ws[:256].zero_()                               # (the fault word, for workspace_fault)
-        if not torch.cuda.is_current_stream_capturing():   # (a capture's memory belongs to its graph)
-            _WS_AT[(cache.index, raw)] = ws
+        ws = kept[(cache.index, raw)] = _empty((need,), torch.uint8, cache.device, None)
     return ws
 
 
@@ -177,7 +185,12 @@ def cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, l
     page_size) uint8 / bool, 0 for tokens that are not attended.  ``weights``:
     (B, heads, width * page_size) float32, updated in place to decay * weights
     + the probability each token drew.  ``out``: preallocated (out, lse).
+    ``ws``: a workspace of the caller's, not in use by another call; zeroed, it
+    tells ``workspace_fault`` afterwards whether a wait ran out.
     """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_attention(q, cache, page_table, lens, scale, key_mask, weights, decay, out, ws)
     B, width, table = _table(cache, page_table)
     if not torch.is_tensor(q) or q.dim() != 4:
         raise TypeError("q must be a 4-D bfloat16 tensor")
@@ -186,15 +199,15 @@ def cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, l
     strides = _strided(q, "q", (B, L, Hq, D), dev)
     cap = width * cache.page_size
     if out is None:
-        o, lse = _empty((B, L, Hq, D), torch.bfloat16, dev, stream), _empty((B, L, Hq), torch.float32, dev, stream)
+        o, lse = _empty((B, L, Hq, D), torch.bfloat16, dev, None), _empty((B, L, Hq), torch.float32, dev, None)
         out_at, lse_at = o.data_ptr(), lse.data_ptr()
     else:
         o, lse = out
         out_at = _at(o, "out", B * L * Hq * D, _BF16, idx, dev)
         lse_at = _at(lse, "lse", B * L * Hq, _F32, idx, dev)
-    raw = _raw_stream(stream, idx)
+    raw = _raw_stream(None, idx)
     if ws is None:
-        ws = _attention_ws(L, Hq, cache, raw, stream)
+        ws = _attention_ws(L, Hq, cache, raw)
     _check(_lib.dllm_cache_attention(cache._ref, q.data_ptr(), strides, B, L, Hq, table, width,
                                      _at(lens, "lens", B, _I32, idx, dev),
                                      _at_or_none(key_mask, "key_mask", B * cap, _MASK, idx, dev),

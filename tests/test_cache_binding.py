@@ -3,6 +3,9 @@ workspaces, streams and devices they pass, and the calls they refuse.  CPU only:
 a stand-in for the library records what reaches it, CPU tensors stand for device
 tensors."""
 import contextlib
+import gc
+import threading
+import weakref
 
 import pytest
 import torch
@@ -19,6 +22,7 @@ class FakeLib:
 
     def __init__(self):
         self.calls = []
+        self.attend_hook = lambda: None
 
     def __getattr__(self, name):
         if name.endswith("_workspace_size"):
@@ -26,6 +30,8 @@ class FakeLib:
 
         def call(*args):
             self.calls.append((name, args))
+            if name == "dllm_cache_attention":
+                self.attend_hook()
             return 0
 
         return call
@@ -42,7 +48,7 @@ def lib(monkeypatch):
     monkeypatch.setattr(cache_mod, "_raw_stream", lambda stream, index: STREAM)
     monkeypatch.setattr(cache_mod, "_need_cuda", lambda *ts: None)
     monkeypatch.setattr(cache_mod, "_NEED", {})
-    monkeypatch.setattr(cache_mod, "_WS_AT", {}, raising=False)
+    monkeypatch.setattr(cache_mod, "_KEPT", threading.local(), raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
     monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
@@ -73,3 +79,69 @@ def test_the_workspace_of_a_call_does_not_go_by_an_empty_or_refused_one(lib, bef
     attend(cache, *before)
     attend(cache, *after)
     assert lib.workspaces()[-1][1] >= need(cache, *after)
+
+
+def test_two_threads_on_one_stream_do_not_share_a_workspace(lib):
+    """The calls overlap (ctypes lets go of the interpreter's lock), and a call's
+    later launches read what its first one left in the workspace."""
+    cache, both = host_cache(), threading.Barrier(2, timeout=20)
+    lib.attend_hook = both.wait
+    threads = [threading.Thread(target=attend, args=(cache, 2, 32, 8)) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    a, b = lib.workspaces()
+    assert a[0] + a[1] <= b[0] or b[0] + b[1] <= a[0]
+
+
+class Streams:
+    """Stands for torch.cuda's current stream: which it is, and whether it is being captured."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.captured = 1, set()
+        monkeypatch.setattr(torch.cuda, "stream", self.enter)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.current in self.captured)
+        monkeypatch.setattr(cache_mod, "_raw_stream", lambda stream, index: self.current if stream is None else stream)
+
+    @contextlib.contextmanager
+    def enter(self, stream):
+        before, self.current = self.current, stream
+        yield
+        self.current = before
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_captured_call_has_a_workspace_of_its_own(lib, monkeypatch, given):
+    """A graph keeps addresses: not that of a workspace which a later call may
+    replace; and its own memory is not kept for calls outside of it.  The stream
+    that counts is the one the call runs on."""
+    streams, made, empty = Streams(monkeypatch), [], cache_mod._empty
+
+    def recorded(shape, dtype, device, stream):
+        t = empty(shape, dtype, device, stream)
+        if dtype == torch.uint8:
+            made.append((t.data_ptr(), weakref.ref(t)))
+        return t
+
+    monkeypatch.setattr(cache_mod, "_empty", recorded)
+    cache = host_cache()
+
+    def call(L):
+        if given:
+            attend(cache, 2, L, 8, stream=2)
+        else:
+            with streams.enter(2):
+                attend(cache, 2, L, 8)
+
+    call(32)                                   # the warm-up
+    streams.captured = {2}
+    call(4)
+    call(16)
+    streams.captured = {1}                     # (another stream's capture does not matter)
+    call(4)
+    gc.collect()
+    assert len(made) == 3 and made[0][1]() is not None
+    assert made[1][1]() is None and made[2][1]() is None
+    at = [a for a, _ in lib.workspaces()]
+    assert at[0] == at[3] == made[0][0] and at[0] not in at[1:3]

@@ -335,6 +335,35 @@ def test_attention_in_a_graph(cs):
     assert torch.equal(out[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(out[1], want[1])
 
 
+def test_attention_in_a_graph_on_a_stream_that_goes_on(cs):
+    """Warmed up, captured and followed by larger calls on one stream, with no
+    workspace given: replays touch no memory that was given to someone else."""
+    rng = np.random.default_rng(23)
+    ps, H, dim, B, width = 64, 2, 128, 2, 40
+    cache = device_cache(cs, random_pool(rng, B * width, H, ps, dim))
+    table, lens = dev(tables(rng, B * width, B, width)), dev(np.array([2500, 900], dtype=np.int32))
+    q, more = queries(rng, B, 4, H * 2, dim), queries(rng, B, 60, H * 2, dim)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in cs.cache_attention(q, cache, table, lens)]
+        want_more = [t.clone() for t in cs.cache_attention(more, cache, table, lens)]
+        cs.cache_attention(q, cache, table, lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out, lse = cs.cache_attention(q, cache, table, lens)
+    with torch.cuda.stream(side):
+        got_more = cs.cache_attention(more, cache, table, lens)
+        side.synchronize()
+        others = [torch.full((n << 10,), 5, dtype=torch.uint8, device="cuda") for n in (64, 256, 1024, 4096, 16384, 32768)]
+        graph.replay()
+        side.synchronize()
+        assert all(bool((t == 5).all()) for t in others)
+    assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+    assert torch.equal(got_more[0].view(torch.int16), want_more[0].view(torch.int16))
+    assert torch.equal(got_more[1], want_more[1])
+
+
 def test_pages_past_4_gib(cs):
     """A pool of more than 2^32 bytes: append, attention and eviction in its last pages."""
     rng = np.random.default_rng(12)
