@@ -115,8 +115,18 @@ def _empty(shape, dtype, device, stream):
 
 
 def _raw_stream(stream, index: int) -> int:
-    """The stream a call runs on: the given one, or the device's current one."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    """The stream a call runs on: the given one, or the device's current one.  The
+    library launches on the current device, so that has to be the tensors' device
+    (another one's default stream has the same handle, and no use for their
+    addresses)."""
+    current = torch._C._cuda_getDevice()
+    if current != index:
+        raise ValueError(f"the tensors are on cuda:{index}; the current device is cuda:{current}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"the tensors are on cuda:{index}; the stream is on {stream.device}")
+    return stream.cuda_stream
 
 
 def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,

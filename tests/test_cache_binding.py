@@ -5,6 +5,7 @@ tensors."""
 import contextlib
 import gc
 import threading
+import types
 import weakref
 
 import pytest
@@ -13,6 +14,7 @@ import torch
 from test_binding_checks import cs
 
 from commit_step_gb300 import cache as cache_mod
+from commit_step_gb300 import score as score_mod
 
 STREAM = 77
 
@@ -145,3 +147,38 @@ def test_a_captured_call_has_a_workspace_of_its_own(lib, monkeypatch, given):
     assert made[1][1]() is None and made[2][1]() is None
     at = [a for a, _ in lib.workspaces()]
     assert at[0] == at[3] == made[0][0] and at[0] not in at[1:3]
+
+
+@pytest.mark.parametrize("current,stream_on", [(1, None), (-1, 1)])
+def test_another_device_is_refused(monkeypatch, current, stream_on):
+    """The tensors' device (-1 here) is not the current one, or not the stream's:
+    nothing reaches the library."""
+    fake = FakeLib()
+    for mod in (cache_mod, score_mod):
+        monkeypatch.setattr(mod, "_lib", fake)
+        monkeypatch.setattr(mod, "_need_cuda", lambda *ts: None)
+    monkeypatch.setattr(cache_mod, "_NEED", {})
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+    stream = None if stream_on is None else types.SimpleNamespace(device=torch.device("cuda", stream_on), cuda_stream=5)
+    cache, i32 = host_cache(), torch.int32
+    kv = torch.zeros((2, 3, 4, 64), dtype=torch.bfloat16)
+    table, lens = torch.zeros((2, 2), dtype=i32), torch.zeros(2, dtype=i32)
+    z, t, f = torch.zeros((2, 9)), torch.zeros(2, dtype=i32), torch.zeros(2)
+    calls = [lambda s: cs.cache_append(cache, kv, kv, table, lens, stream=s),
+             lambda s: cs.cache_evict(cache, table, lens, torch.zeros((2, 4, 32)), 4, table.clone(), stream=s),
+             lambda s: cs.token_logprobs(z, t, stream=s),
+             lambda s: cs.token_logprobs_backward(z, t, f, f, f, stream=s)]
+    if stream is None:                          # (the attention enters the given stream, and its device with it)
+        calls.append(lambda s: cs.cache_attention(kv, cache, table, lens, stream=s))
+    for call in calls:
+        with pytest.raises(ValueError, match="device|stream"):
+            call(stream)
+    assert not fake.calls
+    if current != -1:
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
+        for call in calls:
+            call(None)
+        assert len(fake.calls) == 5
