@@ -182,3 +182,13 @@ def test_another_device_is_refused(monkeypatch, current, stream_on):
         for call in calls:
             call(None)
         assert len(fake.calls) == 5
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(1 << 20, dtype=torch.uint8, device="meta"),     # on another device
+                                torch.zeros(1 << 20, dtype=torch.uint8)[::2],               # not contiguous
+                                torch.zeros(1, dtype=torch.uint8).expand(1 << 20),          # one byte of memory
+                                torch.zeros(1 << 18), b"0" * 1024])
+def test_a_workspace_that_the_kernels_cannot_write_is_refused(lib, ws):
+    with pytest.raises((ValueError, TypeError)):
+        attend(host_cache(), 2, 4, 8, ws=ws)
+    assert not lib.calls
