@@ -12,7 +12,7 @@ import torch
 from . import _F32, _I32, _MASK, _arg, _check, _lib, _need_cuda
 
 _I64x3 = C.c_int64 * 3
-_BF16, _U8 = (torch.bfloat16,), (torch.uint8,)
+_BF16 = (torch.bfloat16,)
 
 
 class _CacheStruct(C.Structure):
@@ -221,7 +221,7 @@ def cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, l
     elif not torch.is_tensor(ws):
         raise TypeError("ws must be a tensor")
     else:
-        _arg(ws, "ws", ws.numel(), _U8, dev)
+        _arg(ws, "ws", ws.numel(), (ws.dtype,), dev)
     _check(_lib.dllm_cache_attention(cache._ref, q.data_ptr(), strides, B, L, Hq, table, width,
                                      _at(lens, "lens", B, _I32, idx, dev),
                                      _at_or_none(key_mask, "key_mask", B * cap, _MASK, idx, dev),

@@ -184,11 +184,18 @@ def test_another_device_is_refused(monkeypatch, current, stream_on):
         assert len(fake.calls) == 5
 
 
-@pytest.mark.parametrize("ws", [torch.zeros(1 << 20, dtype=torch.uint8, device="meta"),     # on another device
-                                torch.zeros(1 << 20, dtype=torch.uint8)[::2],               # not contiguous
-                                torch.zeros(1, dtype=torch.uint8).expand(1 << 20),          # one byte of memory
-                                torch.zeros(1 << 18), b"0" * 1024])
+@pytest.mark.parametrize("ws", [torch.zeros(1 << 20, dtype=torch.uint8, device="meta"),
+                                torch.zeros(1 << 20, dtype=torch.uint8)[::2],
+                                torch.zeros(1, dtype=torch.uint8).expand(1 << 20), [0]],
+                         ids=["another device", "not contiguous", "one byte of memory", "no tensor"])
 def test_a_workspace_that_the_kernels_cannot_write_is_refused(lib, ws):
     with pytest.raises((ValueError, TypeError)):
         attend(host_cache(), 2, 4, 8, ws=ws)
     assert not lib.calls
+
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.int8, torch.float32])
+def test_a_workspace_of_any_type_is_used(lib, dtype):
+    ws = torch.zeros(1 << 16, dtype=dtype)
+    attend(host_cache(), 2, 4, 8, ws=ws)
+    assert lib.workspaces() == [(ws.data_ptr(), 1 << 16)]
