@@ -102,6 +102,26 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: to
     return out
 
 
+class _ScoreGrad(torch.autograd.Function):
+    """The gradient as a step of a graph that is to be differentiated again: there
+    is no second derivative, and leaving it out of a sum of losses would go unseen."""
+
+    @staticmethod
+    def forward(ctx, logits, targets, lse, ent, ids, suppress_ids, g_lp, g_ent, g_top):
+        return _score_grad(logits, targets, lse, ent, ids, suppress_ids, g_lp, g_ent, g_top)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the gradient of score_tokens cannot be differentiated again")
+
+
+def _score_grad(logits, targets, lse, ent, ids, suppress_ids, g_lp, g_ent, g_top):
+    # (gradients that reach here expanded from a scalar are not contiguous)
+    g_lp, g_ent, g_top = [None if g is None else g.float().contiguous() for g in (g_lp, g_ent, g_top)]
+    return token_logprobs_backward(logits, targets, lse, ent, g_lp, g_ent, ids if g_top is not None else None, g_top,
+                                   suppress_ids=suppress_ids)
+
+
 class _ScoreTokens(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, targets, top, suppress_ids):
@@ -115,14 +135,11 @@ class _ScoreTokens(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g_lp, g_ent, _g_ids, g_top):
         logits, targets, lse, ent, ids = ctx.saved_tensors
-        # (gradients that reach here expanded from a scalar are not contiguous)
-        g_lp, g_ent, g_top = [None if g is None else g.float().contiguous() for g in (g_lp, g_ent, g_top)]
-        grad = token_logprobs_backward(logits, targets, lse, ent, g_lp, g_ent, ids if g_top is not None else None,
-                                       g_top, suppress_ids=ctx.suppress_ids)
-        return grad, None, None, None
+        grad = _ScoreGrad.apply if torch.is_grad_enabled() else _score_grad      # (enabled under create_graph)
+        return grad(logits, targets, lse, ent, ids, ctx.suppress_ids, g_lp, g_ent, g_top), None, None, None
 
 
 def score_tokens(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, suppress_ids: Sequence[int] = ()):
     """token_logprobs for training: (logprob, entropy, top_ids, top_logprob),
-    differentiable with respect to ``logits`` through autograd."""
+    differentiable once with respect to ``logits`` through autograd."""
     return _ScoreTokens.apply(logits, targets, int(top), tuple(suppress_ids))

@@ -199,3 +199,36 @@ def test_a_workspace_of_any_type_is_used(lib, dtype):
     ws = torch.zeros(1 << 16, dtype=dtype)
     attend(host_cache(), 2, 4, 8, ws=ws)
     assert lib.workspaces() == [(ws.data_ptr(), 1 << 16)]
+
+
+@pytest.fixture
+def host_scores(monkeypatch):
+    """score_tokens over CPU tensors, by torch's own operations without a graph."""
+    def forward(logits, targets, top=0, suppress_ids=()):
+        lse = torch.logsumexp(logits.detach(), -1)
+        lp = logits.detach().gather(1, targets.long()[:, None])[:, 0] - lse
+        return lp, torch.zeros_like(lse), lse, None, None
+
+    def backward(logits, targets, lse, ent, g_lp, *_, **__):
+        hot = torch.nn.functional.one_hot(targets.long(), logits.shape[1])
+        return g_lp[:, None] * (hot - torch.softmax(logits.detach(), -1))
+
+    monkeypatch.setattr(score_mod, "token_logprobs", forward)
+    monkeypatch.setattr(score_mod, "token_logprobs_backward", backward)
+    return torch.randn((3, 7), generator=torch.Generator().manual_seed(2), requires_grad=True)
+
+
+@pytest.mark.parametrize("loss", [lambda lp: lp.sum(), lambda lp: (lp ** 2).sum()])
+def test_the_gradient_of_a_gradient_is_refused(host_scores, loss):
+    """A penalty on the gradient, alone or beside the loss itself, is not dropped in silence."""
+    z, t = host_scores, torch.tensor([1, 0, 6], dtype=torch.int32)
+    lp = cs.score_tokens(z, t)[0]
+    g, = torch.autograd.grad(loss(lp), z, create_graph=True)
+    want, = torch.autograd.grad(loss(torch.log_softmax(z, 1)[[0, 1, 2], t.long()]), z)
+    assert torch.allclose(g, want, atol=1e-6)
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        (loss(lp) + (g ** 2).sum()).backward()
+    lp = cs.score_tokens(z, t)[0]
+    z.grad = None
+    loss(lp).backward()
+    assert torch.allclose(z.grad, want, atol=1e-6) and not z.grad.requires_grad
