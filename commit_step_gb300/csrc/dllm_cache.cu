@@ -298,7 +298,6 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   }
   for (int i = m + tid; i < p.budget; i += kSelectThreads) keep[i] = -1;
   for (int64_t i = m + tid; i < p.cap; i += kSelectThreads) wo[i] = 0.0f;
-  if (h == 0 && tid == 0) p.lens_out[b] = m;
 }
 
 constexpr int kMoveVec = 4;  // 16-byte vectors (16 codes of one token) a thread holds
@@ -321,6 +320,9 @@ __global__ void __launch_bounds__(256, 3) evict_move_kernel(const __grid_constan
   const int m = n < p.budget ? n : p.budget;
   const int lo = blockIdx.x * ps;
   const int here = m - lo < ps ? m - lo : ps;                    // tokens of this page
+  // (lens_out may be lens: the selections have read it, and min(n, budget) comes
+  // out the same for a block that reads the new length)
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) p.lens_out[b] = m;
   if (here <= 0) return;
   const int64_t to = page_at(p.dst_table, p.dst_width, b, blockIdx.x, p.c.pages);
   if (to < 0) return;

@@ -572,7 +572,7 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
  *   weights      device fp32 (B, heads, width * page_size)
  *   keep         device int32 (B, heads, budget) output: the old positions in
  *                order, -1 behind the last
- *   lens_out     device int32 (B) output: min(n, budget)
+ *   lens_out     device int32 (B) output: min(n, budget); may be lens itself
  *   weights_out  device fp32 like weights, output, not overlapping it: the
  *                kept weights in order, 0 behind them */
 dllm_status dllm_cache_evict(const dllm_kv_cache* cache, const int32_t* table, int64_t width, const int32_t* lens,

@@ -446,3 +446,27 @@ def test_evict_bad_pages_and_nan_codes(cs):
     assert np.array_equal(keep.cpu().numpy(), keep_w) and np.array_equal(n.cpu().numpy(), n_w)
     assert np.array_equal(moved.cpu().numpy(), moved_w)
     assert_pool(cache, pool)
+
+
+def test_evict_updates_the_lengths_in_place(cs):
+    """Every head selects by the lengths from before the call, however early another
+    one's block is done."""
+    rng = np.random.default_rng(41)
+    ps, dim, H, B, width, budget = 16, 64, 32, 24, 20, 60
+    dst_width = -(-budget // ps)
+    pages = B * (width + dst_width)
+    arrays = random_pool(rng, pages, H, ps, dim)
+    order = rng.permutation(pages).astype(np.int32)
+    table, dst = order[:B * width].reshape(B, width), order[B * width:].reshape(B, dst_width)
+    lens = rng.integers(0, width * ps + 1, B).astype(np.int32)
+    w = rng.random((B, H, width * ps)).astype(np.float32)
+    pool = Pool(*arrays)
+    keep_w, n_w, moved_w = pool.evict(table, lens, w, budget, 4, 8, dst)
+    cache, n = device_cache(cs, arrays), dev(lens)
+    out = (torch.empty((B, H, budget), dtype=torch.int32, device="cuda"), n, torch.empty_like(dev(w)))
+    keep, n_out, moved = cs.cache_evict(cache, dev(table), n, dev(w), budget, dev(dst), keep_first=4, keep_last=8,
+                                        out=out)
+    assert n_out is n and np.array_equal(n.cpu().numpy(), n_w)
+    assert np.array_equal(keep.cpu().numpy(), keep_w)
+    assert np.array_equal(moved.cpu().numpy(), moved_w)
+    assert_pool(cache, pool)
