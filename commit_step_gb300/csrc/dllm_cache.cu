@@ -500,9 +500,12 @@ dllm_status dllm_cache_evict(const dllm_kv_cache* cache, const int32_t* table, i
     return DLLM_ERR_INVALID_ARGUMENT;
   if (2 * B > 65535) return DLLM_ERR_UNSUPPORTED;
   if (B == 0) return DLLM_OK;
-  if (!lens || !weights || !keep || !lens_out || !weights_out || weights == weights_out)
-    return DLLM_ERR_INVALID_ARGUMENT;
+  if (!lens || !weights || !keep || !lens_out || !weights_out) return DLLM_ERR_INVALID_ARGUMENT;
   if (!aligned4(lens) || !aligned4(weights) || !aligned4(keep) || !aligned4(lens_out) || !aligned4(weights_out))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  // A row's weights are stored while other rows' are still read.
+  const uintptr_t w0 = reinterpret_cast<uintptr_t>(weights), w1 = reinterpret_cast<uintptr_t>(weights_out);
+  if ((w0 < w1 ? w1 - w0 : w0 - w1) < static_cast<uintptr_t>(B) * cache->heads * cap * 4)
     return DLLM_ERR_INVALID_ARGUMENT;
   EvictParams p{};
   p.c = cache_view(*cache);

@@ -12,6 +12,7 @@ import pytest
 import torch
 
 from test_binding_checks import cs
+from test_cache_score_checks import FAKE, INVALID, cache as fake_cache, evict
 
 from commit_step_gb300 import cache as cache_mod
 from commit_step_gb300 import score as score_mod
@@ -232,3 +233,9 @@ def test_the_gradient_of_a_gradient_is_refused(host_scores, loss):
     z.grad = None
     loss(lp).backward()
     assert torch.allclose(z.grad, want, atol=1e-6) and not z.grad.requires_grad
+
+
+def test_evict_refuses_weights_that_overlap_the_moved_ones():
+    """2 rows of 4 heads of 256 tokens: 8192 bytes."""
+    for off in (-8188, -4096, -4, 0, 4, 4096, 8188):
+        assert evict(fake_cache(), lo=FAKE + (1 << 16), wo=FAKE + off) == INVALID, off

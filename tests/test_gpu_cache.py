@@ -470,3 +470,20 @@ def test_evict_updates_the_lengths_in_place(cs):
     assert np.array_equal(keep.cpu().numpy(), keep_w)
     assert np.array_equal(moved.cpu().numpy(), moved_w)
     assert_pool(cache, pool)
+
+
+def test_evict_weights_next_to_the_moved_ones(cs):
+    rng = np.random.default_rng(42)
+    ps, dim, H, width, budget = 16, 64, 2, 5, 30
+    arrays = random_pool(rng, 8, H, ps, dim)
+    table, dst, lens = np.arange(5, dtype=np.int32)[None], np.array([[5, 6]], dtype=np.int32), np.array([77], dtype=np.int32)
+    w = rng.random((1, H, width * ps)).astype(np.float32)
+    for first in (0, 1):
+        cache, pool = device_cache(cs, arrays), Pool(*arrays)
+        both = torch.zeros((2, 1, H, width * ps), device="cuda")
+        both[first] = dev(w)
+        out = (torch.empty((1, H, budget), dtype=torch.int32, device="cuda"), dev(lens), both[1 - first])
+        keep, n, moved = cs.cache_evict(cache, dev(table), dev(lens), both[first], budget, dev(dst), out=out)
+        keep_w, n_w, moved_w = pool.evict(table, lens, w, budget, 0, 0, dst)
+        assert np.array_equal(keep.cpu().numpy(), keep_w) and np.array_equal(n.cpu().numpy(), n_w)
+        assert np.array_equal(moved.cpu().numpy(), moved_w) and np.array_equal(both[first].cpu().numpy(), w)
