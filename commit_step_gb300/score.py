@@ -31,8 +31,16 @@ def _rows(t: torch.Tensor, name: str):
 
 
 def _sup(suppress_ids: Sequence[int]):
-    n = len(suppress_ids)
-    return ((C.c_int32 * n)(*[int(v) for v in suppress_ids]) if n else None), n
+    ids = [_int32(v, "suppress_ids") for v in suppress_ids]
+    return ((C.c_int32 * len(ids))(*ids) if ids else None), len(ids)
+
+
+def _int32(v, name: str) -> int:
+    """v as the library takes it (ctypes would cut it to its low bits)."""
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name}: {v} is out of range")
+    return v
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, suppress_ids: Sequence[int] = (),
@@ -46,7 +54,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, su
     is 0.  ``out``: the same five, preallocated."""
     _need_cuda(logits, targets)
     T, V, stride = _rows(logits, "logits")
-    dt, dev, idx, shape, top = _dtype_code(logits), logits.device, logits.get_device(), logits.shape[:-1], int(top)
+    dt, dev, idx, shape, top = _dtype_code(logits), logits.device, logits.get_device(), logits.shape[:-1], _int32(top, "top")
     if out is None:
         lp = _empty(shape, torch.float32, dev, stream)
         ent = _empty(shape, torch.float32, dev, stream)

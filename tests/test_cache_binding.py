@@ -239,3 +239,21 @@ def test_evict_refuses_weights_that_overlap_the_moved_ones():
     """2 rows of 4 heads of 256 tokens: 8192 bytes."""
     for off in (-8188, -4096, -4, 0, 4, 4096, 8188):
         assert evict(fake_cache(), lo=FAKE + (1 << 16), wo=FAKE + off) == INVALID, off
+
+
+@pytest.mark.parametrize("kw", [dict(suppress_ids=(3, (1 << 32) + 5)), dict(suppress_ids=(-(1 << 32),)),
+                                dict(top=(1 << 32) + 2), dict(top=-(1 << 32))])
+def test_numbers_that_do_not_fit_are_refused(monkeypatch, kw):
+    """They would reach the library as others: 2^32 + 5 as id 5."""
+    fake = FakeLib()
+    monkeypatch.setattr(score_mod, "_lib", fake)
+    monkeypatch.setattr(score_mod, "_need_cuda", lambda *ts: None)
+    monkeypatch.setattr(score_mod, "_raw_stream", lambda stream, index: STREAM)
+    monkeypatch.setattr(score_mod, "_empty", lambda shape, dtype, device, stream: torch.empty(0, dtype=dtype))
+    z, t, f = torch.zeros((2, 9)), torch.zeros(2, dtype=torch.int32), torch.zeros(2)
+    with pytest.raises(ValueError):
+        cs.token_logprobs(z, t, **kw)
+    if "suppress_ids" in kw:
+        with pytest.raises(ValueError):
+            cs.token_logprobs_backward(z, t, f, f, f, out=torch.zeros_like(z), **kw)
+    assert not fake.calls
