@@ -676,7 +676,7 @@ static dllm_status check_score(const void* logits, dllm_dtype dt, int64_t T, int
                                std::vector<int32_t>& sup) {
   if (dt != DLLM_F32 && dt != DLLM_BF16) return DLLM_ERR_INVALID_ARGUMENT;
   if (T < 0 || V < 1 || V > INT32_MAX - 1 || row_stride < V || top < 0) return DLLM_ERR_INVALID_ARGUMENT;
-  if (mul_or_neg(T, mul_or_neg(row_stride, 4)) < 0 || mul_or_neg(T, 4 * (top + 1)) < 0)
+  if (mul_or_neg(T, mul_or_neg(row_stride, 4)) < 0 || mul_or_neg(T, 4 * (static_cast<int64_t>(top) + 1)) < 0)
     return DLLM_ERR_INVALID_ARGUMENT;
   if (n_suppress < 0 || (n_suppress > 0 && !suppress_ids)) return DLLM_ERR_INVALID_ARGUMENT;
   if (n_suppress > DLLM_MAX_SUPPRESS || top > DLLM_MAX_TOP) return DLLM_ERR_UNSUPPORTED;

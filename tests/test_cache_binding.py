@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from test_binding_checks import cs
-from test_cache_score_checks import FAKE, INVALID, cache as fake_cache, evict
+from test_cache_score_checks import FAKE, INVALID, UNSUPPORTED, cache as fake_cache, evict, grad, score
 
 from commit_step_gb300 import cache as cache_mod
 from commit_step_gb300 import score as score_mod
@@ -257,3 +257,9 @@ def test_numbers_that_do_not_fit_are_refused(monkeypatch, kw):
         with pytest.raises(ValueError):
             cs.token_logprobs_backward(z, t, f, f, f, out=torch.zeros_like(z), **kw)
     assert not fake.calls
+
+
+@pytest.mark.parametrize("call", [score, grad])
+def test_a_top_far_past_the_most_is_unsupported(call):
+    for top in (33, 1 << 29, (1 << 30) - 1, (1 << 31) - 1):
+        assert call(V=1 << 30, stride=1 << 30, top=top) == UNSUPPORTED, top
