@@ -2,8 +2,11 @@
 // key/value cache, and the attention weight each cached token draws.
 //
 // Mathematics.  For the rows r of one key head (the queries of its head group)
-// and its tokens j: x = scale log2 e s_k(j) q_r . k_j, p = 2^(x - m_r), l_r =
-// sum p, out_r = sum p s_v(j) v_j / l_r, with a running reference m_r.
+// and its tokens j: x = scale log2 e s_k(j) q_r . k_j, y = 2^(x + log2 s_v(j) -
+// m_r), out_r = sum y v_j / l_r with l_r = sum y / s_v(j), lse_r = ln 2 (m_r +
+// log2 l_r).  The running reference m_r follows a row's largest probability times
+// value scale, so what a token adds to the row is held to that and to nothing
+// that another row, or a page the row does not attend to, has.
 //
 // The transposed products.  A tile is 128 tokens of one head.  S^T = K Q^T and
 // O^T += V^T P^T put the tokens (then the head dimension) on the tensor core's
@@ -18,14 +21,13 @@
 //     two per row: a bf16 value has 8 significant bits and e4m3 holds 4 of
 //     either sign, so hi + lo is exact for elements above 2^-9 of the row's
 //     largest and off by at most 2^-18 of it below;
-//   * P, held at 64 p s_v / v_ref <= 256 with fp16's 11 bits (bf16 has 8), into
-//     three parts of 4 bits, the second and third of 16 and 256 times the
-//     remainder, with accumulators of their own: exact but for the rounding to
-//     fp16, which is 2^-12 of the value and no finer than 2^-23 of the row's
-//     reference (which lies up to 2 above the row's largest score).
-// The references m_r and v_ref move only when a score exceeds its reference by
-// more than 2 (log2 units) or a page's value scale its own, so the accumulators
-// in TMEM are rarely rescaled; statistics and sums are fp32.
+//   * P = 64 y <= 256, with fp16's 11 bits (bf16 has 8), into three parts of 4
+//     bits, the second and third of 16 and 256 times the remainder, with
+//     accumulators of their own: exact but for the rounding to fp16, which is
+//     2^-12 of the value, or 2^-22 of the row's largest y where that is more (a
+//     new reference lies 1 above its y, in log2; 64 y rounds at 2^-17).
+// A reference moves only when a y exceeds it by more than 2 (log2 units), so the
+// accumulators in TMEM are rarely rescaled; statistics and sums are fp32.
 //
 // Measured (head_dim 128, pages of 64 and 128 with one scale, where references
 // rise in few tiles, one GB300, replayed in a graph):
@@ -437,7 +439,9 @@ constexpr int kMetaSlots = 8;
 constexpr float kSlack = 2.0f;                         // log2: how far a score may exceed the reference
 constexpr float kHead = 1.0f;                          // log2: how far a new reference lies above its score
 constexpr float kUnset = -1e30f;                       // stands for the reference of a part without tokens
-constexpr float kPUnit = 64.0f;                        // P is held at 64 p s_v / v_ref <= 2^(6 + 2) (e4m3 ends at 448)
+constexpr float kPUnit = 64.0f;                        // P = 64 y <= 2^(6 + 2) (e4m3 ends at 448)
+constexpr int kPShift = -2;                            // log2 of P / (256 y): exponents are those of P / 256
+constexpr float kTinyUnit = -42.0f;                    // lv below which a token is summed by itself
 template <int D, int N, bool PAIR>
 constexpr int attend_smem() {
   using S = AttendShape<N, PAIR>;
@@ -446,7 +450,8 @@ constexpr int attend_smem() {
 
 struct TileMeta {
   alignas(16) uint8_t mask[kTile];  // the tile's part of the key mask, when there is one
-  float ks[8], vs[8];               // per page of the tile: scale log2 e s_k, and s_v
+  float ks[8];                      // per page of the tile: scale log2 e s_k,
+  float lv[8], iv[8];               // log2(s_v / 4), and 4 / s_v
   uint32_t pages;                   // bits of the pages that exist
   int32_t left;                     // tokens of the sequence in the tile
 };
@@ -471,9 +476,7 @@ struct AttendShared {
   alignas(16) float fac_o[2][N];                       // the factors of a rise,
   alignas(16) float fac_l[2][N];
   alignas(16) float delta[2][N];
-  float vmax[2][4];
   alignas(16) float red[2][4][N];                      // maxima or sums per warp
-  float vref[2];
   alignas(16) float fin[2][N];                         // what an accumulator's column is multiplied with at the end
   alignas(16) int32_t row[AttendShape<N, PAIR>::kRows];    // output rows, -1 where a column has none
   uint32_t w0, w1, off0;
@@ -481,6 +484,17 @@ struct AttendShared {
   uint32_t tmem;
   int32_t abort;
 };
+
+// log2(s / 4) of a value scale s, and 4 / s as the sums use it: exact for powers
+// of two, else a page's tokens count by a factor within 2^-18 of s, which the two
+// agree on.  A scale below 2^-100 (that of an all-zero page) counts as that.
+__device__ __forceinline__ void value_unit(float s, float& lv, float& iv) {
+  const uint32_t b = __float_as_uint(fmaxf(s, 0x1p-100f));
+  const int e = static_cast<int>(b >> 23) - 127;
+  const float whole = static_cast<float>(e + kPShift), f = __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
+  lv = f == 1.0f ? whole : whole + __log2f(f);
+  iv = __uint_as_float(static_cast<uint32_t>(127 - kPShift - e) << 23) * (f == 1.0f ? 1.0f : ex2_approx(whole - lv));
+}
 
 // The copy warp of a CTA: the tiles of its range, K (and V) through the rings
 // and what is known of each tile into its meta slot.
@@ -503,7 +517,7 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
   };
   struct Page {
     int32_t at;                     // page heads + head, or -1
-    float ks, vs;
+    float ks, lv, iv;
   };
   Cursor look = cur;
   Segment ahead;
@@ -527,10 +541,10 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
     }
   };
   auto scales = [&](const Batch& t) {
-    Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f};
+    Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f, 0.0f};
     if (pg.at >= 0) {
       pg.ks = p.c.k_scale[pg.at];
-      pg.vs = p.c.v_scale[pg.at];
+      if (WITH_V) value_unit(p.c.v_scale[pg.at], pg.lv, pg.iv);
     }
     return pg;
   };
@@ -567,7 +581,8 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
       const int64_t j0 = static_cast<int64_t>(now.t0 + i) * kTile;
       if (mine) {
         m.ks[slot] = page.ks * p.scale2;
-        m.vs[slot] = page.vs;
+        m.lv[slot] = page.lv;
+        m.iv[slot] = page.iv;
       }
       if (lane == 0) {
         m.pages = pages;
@@ -932,7 +947,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         f2[j] = *reinterpret_cast<const uint64_t*>(&sh.f[c0 + 8 * j + col]);
         nm2[j] = l2[j] = 0;
       }
-      float vref = 0x1p-120f, vscale = kPUnit / 256 / vref;
       bool begun = false, seen = false;                // the accumulator holds earlier tiles; the references a score
       for (int ti = sg.t0; ti < sg.t1; ++ti, ++g) {
         if (!PAIR && (g & 1u) != static_cast<uint32_t>(grp)) continue;
@@ -943,14 +957,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const bool visible = tile_visible(m, key, page_of, p.mask != nullptr);
         const unsigned seen_keys = __ballot_sync(0xFFFFFFFFu, visible);
         // The four tokens' scales (8 consecutive tokens share a page).
-        float ck[4], vs[4];
-        float vtop = -1.0f;                            // largest value scale of this thread's visible tokens
+        float ck[4], lv[4], iv[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int page = (wq * 32 + 8 * q) >> ps_log;
           ck[q] = m.ks[page];
-          vs[q] = (seen_keys >> (8 * q + (lane >> 2))) & 1u ? m.vs[page] : 0.0f;
-          if ((seen_keys >> (8 * q + (lane >> 2))) & 1u) vtop = fmaxf(vtop, vs[q]);
+          lv[q] = m.lv[page];
+          iv[q] = (seen_keys >> (8 * q + (lane >> 2))) & 1u ? m.iv[page] : 0.0f;   // (a masked page's may be NaN)
         }
         if (!visible) {
           // Codes of tokens that are not visible (any bytes, NaN among them)
@@ -964,8 +977,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         wait(sh.sfull[grp], nth & 1u, kFaultFullWait);
         __syncwarp();
         at_fence_after();
-        // Exponents x[q][j] = score - reference of token q, column pair j; columns
-        // past the rows are not looked at (J is cut to what the rows need).
+        // Exponents x[q][j] = log2(P / 256) of token q, column pair j; columns past
+        // the rows are not looked at (J is cut to what the rows need).
         uint64_t x[4][J];
         {
           uint32_t r[2][N / 2];                        // of tokens 0 .. 15 and 16 .. 31
@@ -986,8 +999,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint32_t* v = &r[q >> 1][4 * j + 2 * (q & 1)];
-              x[q][j] = fma2(at_mul2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(ck[q], ck[q])), f2[j],
-                             nm2[j]);
+              x[q][j] = add2(fma2(at_mul2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(ck[q], ck[q])),
+                                  f2[j], nm2[j]), pack2(lv[q], lv[q]));
             }
           }
         }
@@ -1009,10 +1022,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             over = fmaxf(fmaxf(over, a), b);
           }
         }
-        const bool raise = over > kSlack || vtop > vref || (!seen && seen_keys != 0u);
+        const bool raise = over > kSlack + kPShift || (!seen && seen_keys != 0u);
         if (group_any(bar_id, raise)) {                // uniform over the group
-          // New references: the largest score of each column so far, and a bit
-          // more (a score then has to exceed it eightfold to move it again).
+          // New references: the largest y of each column so far, and a bit more
+          // (one then has to exceed it eightfold to move it again).
 #pragma unroll
           for (int j = 0; j < J; ++j) {
             if (j % 2 == 0 && 8 * j >= ncols) break;
@@ -1028,24 +1041,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             tb = over_tokens<true>(tb);
             if (lane < 4) *reinterpret_cast<uint64_t*>(&sh.red[grp][wq][8 * j + col]) = pack2(ta, tb);
           }
-          const float vmax = warp_max_f32(vtop);
-          if (lane == 0) sh.vmax[grp][wq] = vmax;
           named_sync(bar_id, 128);
-          const float vnew = fmaxf(vref, fmaxf(fmaxf(sh.vmax[grp][0], sh.vmax[grp][1]),
-                                               fmaxf(sh.vmax[grp][2], sh.vmax[grp][3])));
           if (tid < ncols) {
             const float top = fmaxf(fmaxf(sh.red[grp][0][tid], sh.red[grp][1][tid]),
-                                    fmaxf(sh.red[grp][2][tid], sh.red[grp][3][tid]));   // relative to the old reference
+                                    fmaxf(sh.red[grp][2][tid], sh.red[grp][3][tid])) - kPShift;   // above the old reference
             const float up = top > 0.0f || (!seen && top > -kInf) ? top + kHead : 0.0f;
             nm[tid] -= up;
             sh.delta[grp][tid] = -up;
             const float d = ex2_approx(-up);
             sh.fac_l[grp][tid] = d;
             // (before any score the accumulator is all zeros, and d may be infinite)
-            sh.fac_o[grp][place(tid)] = seen ? d * (vref / vnew) : 0.0f;
+            sh.fac_o[grp][place(tid)] = seen ? d : 0.0f;
           }
-          vref = vnew;
-          vscale = kPUnit / 256 / vref;
           named_sync(bar_id, 128);
 #pragma unroll
           for (int j = 0; j < J; ++j) {
@@ -1080,10 +1087,25 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         at_fence_before();                             // the scores have been read
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.sempty[grp]));
-        // P: summed in fp32, in three e4m3 parts for the product.
-        uint64_t vr2[4];
+        // P: summed in fp32, in three e4m3 parts for the product.  Next to pages of
+        // ordinary scales a tiny one's y can fall below what fp32 holds while its
+        // probability counts (all-zero values that draw attention): those tokens are
+        // summed by their scores alone.
+        if (fminf(fminf(lv[0], lv[1]), fminf(lv[2], lv[3])) < kTinyUnit) {   // (the same in all lanes)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) vr2[q] = pack2(vs[q] * vscale, vs[q] * vscale);   // 2^-8 64 s_v / v_ref
+          for (int j = 0; j < J; ++j) {
+            if (j % 2 == 0 && 8 * j >= ncols) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float a, b;
+              unpack2(x[q][j], a, b);
+              if (lv[q] < kTinyUnit) l2[j] = add2(l2[j], pack2(ex2_approx(a - lv[q]), ex2_approx(b - lv[q])));
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (lv[q] < kTinyUnit) iv[q] = 0.0f;
+        }
         if (nth >= 1) wait(sh.pvdone[grp], (nth - 1) & 1u, kFaultEmptyWait);   // the product that read this buffer last
         __syncwarp();
 #pragma unroll
@@ -1098,9 +1120,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
               const int j = 2 * jj + u;
               float a, b;
               unpack2(x[q][j], a, b);
-              const uint64_t y = pack2(ex2_approx(a), ex2_approx(b));
-              l2[j] = add2(l2[j], y);
-              unpack2(at_mul2(y, vr2[q]), a, b);
+              a = ex2_approx(a);
+              b = ex2_approx(b);
+              l2[j] = fma2(pack2(a, b), pack2(iv[q], iv[q]), l2[j]);
               h[u] = f16x2(a, b);
             }
             o[0][q] = part_codes(h[0], h[1]);
@@ -1133,7 +1155,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         b = over_tokens<false>(b);
         if (lane < 4) *reinterpret_cast<uint64_t*>(&sh.red[grp][wq][8 * j + col]) = pack2(a, b);
       }
-      if (tid == 0) sh.vref[grp] = vref;
       named_sync(3, kSoftWarps * 32);
       const bool whole = sg.t0 == 0 && sg.t1 == sg.T;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (sg.starts_range ? 0 : 1);
@@ -1150,7 +1171,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         float m = -sh.nm[a][c];
         float l = (sh.red[a][0][c] + sh.red[a][1][c]) + (sh.red[a][2][c] + sh.red[a][3][c]);
         if (l == 0.0f) m = kUnset;                     // (no token: its reference says nothing)
-        float fa = sh.vref[a] * (1.0f / kPUnit), fb = 0.0f;
+        float fa = 1.0f / kPUnit, fb = 0.0f;
         if (both) {
           const int o = first ^ 1;
           const float lo = (sh.red[o][0][c] + sh.red[o][1][c]) + (sh.red[o][2][c] + sh.red[o][3][c]);
@@ -1158,7 +1179,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           const float ea = ex2_approx(m - top), eb = ex2_approx(mo - top);
           l = l * ea + lo * eb;
           fa *= ea;
-          fb = sh.vref[o] * (1.0f / kPUnit) * eb;
+          fb = 1.0f / kPUnit * eb;
           m = top;
         }
         if (whole) {

@@ -283,6 +283,50 @@ def test_attention_general_scales(cs):
                     np.array([250, 100], dtype=np.int32))
 
 
+def page_that_draws(rng, heads, G, L, ps, dim, width, drawn):
+    """(q, arrays, table, lens) of one sequence whose queries put nearly all mass on the
+    pages `drawn`: keys along the queries' common signs there, against them elsewhere."""
+    sign = np.where(rng.random((heads, dim)) < 0.5, -1.0, 1.0)
+    q = sign.repeat(G, 0)[None, None] * (0.5 + rng.random((1, L, heads * G, dim)))
+    k, v, ks, vs = [np.array(a) for a in random_pool(rng, width, heads, ps, dim)]
+    side = np.where(np.isin(np.arange(width), drawn), 1.0, -1.0)[:, None, None, None] * sign[None, :, None]
+    x = side * (1.0 + rng.random((width, heads, ps, dim)))
+    k[:] = torch.from_numpy(x).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    ks[:] = 1.0
+    table = np.arange(width, dtype=np.int32)[None]
+    return torch.from_numpy(q).to(torch.bfloat16).cuda(), [k, v, ks, vs], table, np.array([width * ps - 3], np.int32)
+
+
+@pytest.mark.parametrize("dim,L,G", [(64, 1, 1), (128, 8, 4), (128, 16, 4), (64, 25, 4), (128, 40, 4)])
+@pytest.mark.parametrize("drawn", [[0], [13], [5, 6]])
+@pytest.mark.parametrize("ratio", [2.0 ** 12, 2.0 ** 18, 2.0 ** 26, 1.7 * 2.0 ** 45])
+def test_attention_of_a_page_of_small_values(cs, dim, L, G, drawn, ratio):
+    """All mass lies on pages whose value scale is `ratio` times smaller than that of
+    pages before, behind and between them, which the queries see and do not attend
+    to: the result is as exact as without those.  (Mass elsewhere: about e^-67.)"""
+    rng = np.random.default_rng(dim + L + drawn[0])
+    q, arrays, table, lens = page_that_draws(rng, 2, G, L, 32, dim, 14, drawn)
+    arrays[3][:] = 2.0 ** -8
+    arrays[3][drawn] = 2.0 ** -8 / ratio
+    check_attention(cs, arrays, q, table, lens, scale=0.5 * 45 / dim)
+
+
+@pytest.mark.parametrize("L,G", [(1, 1), (8, 4), (25, 4)])
+@pytest.mark.parametrize("small", [2.0 ** -100, 2.0 ** -70, 2.0 ** -45, 2.0 ** -30])
+def test_attention_drawn_by_values_of_nothing(cs, L, G, small):
+    """Pages of zero values (scale 2^-100), and of next to none, that draw a part of the
+    mass, most of it or nearly all: it counts in the sums."""
+    rng = np.random.default_rng(L + G)
+    ps, dim, width = 16, 128, 30
+    for scale in (2.0 ** -9, 2.0 ** -6, 2.0 ** -4):
+        q, arrays, table, lens = page_that_draws(rng, 2, G, L, ps, dim, width, [3, 4, 20, 29])
+        arrays[3][:] = 2.0 ** 5
+        arrays[3][[3, 4, 20, 29]] = small
+        if small == 2.0 ** -100:
+            arrays[1][[3, 4, 20, 29]] = 0
+        check_attention(cs, arrays, q, table, lens, scale=scale)
+
+
 def test_attention_strided_queries_and_stream(cs):
     rng = np.random.default_rng(6)
     ps, H, G, dim, B, width, L = 64, 2, 2, 128, 3, 4, 12
