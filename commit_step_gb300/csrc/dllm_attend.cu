@@ -1810,6 +1810,18 @@ dllm_status dllm_cache_attention(const dllm_kv_cache* cache, const void* q, cons
   if (!aligned16(workspace)) return DLLM_ERR_INVALID_ARGUMENT;
   const RowTiles rt = row_tiles(L * (Hq / cache->heads));
   if (workspace_bytes < attend_workspace(1, rt.columns, cache->head_dim)) return DLLM_ERR_WORKSPACE;
+  // Rows are stored while other items' queries are still to be read, and the
+  // weights read all of them once more.
+  const int64_t D = cache->head_dim, in_place[3] = {L * Hq * D, Hq * D, D};
+  int64_t last = D;
+  bool same = out == q && !weights;
+  for (int i = 0; i < 3; ++i) {
+    last += (extent[i] - 1) * q_strides[i];
+    same = same && (extent[i] == 1 || q_strides[i] == in_place[i]);
+  }
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  if (!same && q0 < o0 + static_cast<uintptr_t>(rows * D) * 2 && o0 < q0 + static_cast<uintptr_t>(last) * 2)
+    return DLLM_ERR_INVALID_ARGUMENT;
   const AttendDevice* dev = attend_device();
   if (!dev) return DLLM_ERR_CUDA;
   // One CTA per SM, fewer when there are fewer tiles than that.

@@ -533,7 +533,8 @@ dllm_status dllm_cache_append(const dllm_kv_cache* cache, const void* k, const v
  *              whatever their keys and values hold; 16-byte aligned, the
  *              stride a multiple of 16 (else DLLM_ERR_UNSUPPORTED)
  *   scale      multiplies q . k (0 < scale <= 2^20)
- *   out        device bf16 (B, L, Hq, head_dim) contiguous, 16-byte aligned
+ *   out        device bf16 (B, L, Hq, head_dim) contiguous, 16-byte aligned;
+ *              not overlapping q, but that without weights it may be q itself
  *   lse        device fp32 (B, L, Hq): ln sum exp(scale q . k)
  * A query with no visible token gives out 0 and lse -inf.
  *   weights    device fp32 (B, heads, width * page_size) or NULL:

@@ -12,7 +12,8 @@ import pytest
 import torch
 
 from test_binding_checks import cs
-from test_cache_score_checks import FAKE, INVALID, UNSUPPORTED, cache as fake_cache, evict, grad, score
+from test_cache_score_checks import (FAKE, I3, INVALID, UNSUPPORTED, attend as c_attend, cache as fake_cache, evict,
+                                     grad, score)
 
 from commit_step_gb300 import cache as cache_mod
 from commit_step_gb300 import score as score_mod
@@ -263,3 +264,14 @@ def test_numbers_that_do_not_fit_are_refused(monkeypatch, kw):
 def test_a_top_far_past_the_most_is_unsupported(call):
     for top in (33, 1 << 29, (1 << 30) - 1, (1 << 31) - 1):
         assert call(V=1 << 30, stride=1 << 30, top=top) == UNSUPPORTED, top
+
+
+def test_attention_refuses_an_output_over_the_queries():
+    """2 x 4 queries of 8 heads of 128: 16384 bytes, contiguous at strides 4096, 1024, 128."""
+    whole = I3(4096, 1024, 128)
+    for off in (-16384 + 16, -16, 16, 2048, 16384 - 16):
+        assert c_attend(fake_cache(), s=whole, out=FAKE + off) == INVALID, off
+    assert c_attend(fake_cache(), s=whole, w=FAKE + (1 << 16)) == INVALID           # (the weights read q again)
+    packed = I3(4 * 1536, 1536, 128)
+    for off in (0, 16, 2 * (4 * 1536 + 3 * 1536 + 1024) - 16, -16384 + 16):
+        assert c_attend(fake_cache(), s=packed, out=FAKE + off) == INVALID, off

@@ -357,6 +357,26 @@ def test_attention_repeats_bit_for_bit(cs):
         assert all(torch.equal(a, b) for a, b in zip(got, first))
 
 
+@pytest.mark.parametrize("L", [1, 20, 70])
+def test_attention_over_its_own_queries(cs, L):
+    """The output in the queries' place, and next to them."""
+    rng = np.random.default_rng(L)
+    ps, H, dim, B, width = 16, 2, 128, 9, 40
+    cache = device_cache(cs, random_pool(rng, B * width, H, ps, dim))
+    table, lens = dev(tables(rng, B * width, B, width)), dev(rng.integers(0, width * ps + 1, B).astype(np.int32))
+    q = queries(rng, B, L, H * 3, dim)
+    want, lse = cs.cache_attention(q, cache, table, lens)
+    both = torch.zeros((2, *q.shape), dtype=torch.bfloat16, device="cuda")
+    for at in (0, 1):
+        both[at] = q
+        cs.cache_attention(both[at], cache, table, lens, out=(both[1 - at], torch.empty_like(lse)),
+                           weights=torch.zeros((B, H, width * ps), device="cuda"))
+        assert torch.equal(both[1 - at].view(torch.int16), want.view(torch.int16))
+        assert torch.equal(both[at].view(torch.int16), q.view(torch.int16))
+    out, _ = cs.cache_attention(q, cache, table, lens, out=(q, torch.empty_like(lse)))
+    assert out is q and torch.equal(q.view(torch.int16), want.view(torch.int16))
+
+
 def test_attention_in_a_graph(cs):
     rng = np.random.default_rng(22)
     ps, H, dim, B, width = 64, 2, 128, 2, 6
