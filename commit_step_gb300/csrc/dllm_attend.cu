@@ -312,6 +312,14 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t r0, uint32_t r
 // within 16, bit 3 of n moves below its bits 2 and 1.
 __host__ __device__ constexpr int place(int n) { return (n & ~15) | ((n & 6) << 1) | ((n & 8) >> 2) | (n & 1); }
 
+// ln(2^m l), -inf for l = 0: the exponent of l goes to m, which it may all but
+// cancel (l is in units of the value scales' inverse).
+__device__ __forceinline__ float lse_of(float m, float l) {
+  int k;
+  const float f = frexpf(l, &k);
+  return l == 0.0f ? -kInf : fmaf(m + static_cast<float>(k), kLn2, logf(f));
+}
+
 // Whether any of the 128 threads of named barrier `id` has p set.
 __device__ __forceinline__ bool group_any(uint32_t id, bool p) {
   uint32_t r;
@@ -441,7 +449,6 @@ constexpr float kHead = 1.0f;                          // log2: how far a new re
 constexpr float kUnset = -1e30f;                       // stands for the reference of a part without tokens
 constexpr float kPUnit = 64.0f;                        // P = 64 y <= 2^(6 + 2) (e4m3 ends at 448)
 constexpr int kPShift = -2;                            // log2 of P / (256 y): exponents are those of P / 256
-constexpr float kTinyUnit = -42.0f;                    // lv below which a token is summed by itself
 template <int D, int N, bool PAIR>
 constexpr int attend_smem() {
   using S = AttendShape<N, PAIR>;
@@ -452,7 +459,7 @@ struct TileMeta {
   alignas(16) uint8_t mask[kTile];  // the tile's part of the key mask, when there is one
   float ks[8];                      // per page of the tile: scale log2 e s_k,
   float lv[8], iv[8];               // log2(s_v / 4), and 4 / s_v
-  uint32_t pages;                   // bits of the pages that exist
+  uint32_t pages, nothing;          // bits of the pages that exist, of those without values
   int32_t left;                     // tokens of the sequence in the tile
 };
 
@@ -487,13 +494,17 @@ struct AttendShared {
 
 // log2(s / 4) of a value scale s, and 4 / s as the sums use it: exact for powers
 // of two, else a page's tokens count by a factor within 2^-18 of s, which the two
-// agree on.  A scale below 2^-100 (that of an all-zero page) counts as that.
-__device__ __forceinline__ void value_unit(float s, float& lv, float& iv) {
-  const uint32_t b = __float_as_uint(fmaxf(s, 0x1p-100f));
-  const int e = static_cast<int>(b >> 23) - 127;
-  const float whole = static_cast<float>(e + kPShift), f = __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
+// agree on.  A page of no values (2^-100, the least that an append gives) returns
+// true and counts by 2^-64, with zeros: its tokens' share of the sums, which may be
+// all of them, must stay within fp32's range next to ordinary pages'.
+__device__ __forceinline__ bool value_unit(float s, float& lv, float& iv) {
+  const bool nothing = !(s > 0x1p-100f);
+  const uint32_t b = __float_as_uint(nothing ? 0x1p-64f : fminf(s, 0x1p+120f));
+  const int e = static_cast<int>(b >> 23) - 127 + kPShift;
+  const float whole = static_cast<float>(e), f = __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
   lv = f == 1.0f ? whole : whole + __log2f(f);
-  iv = __uint_as_float(static_cast<uint32_t>(127 - kPShift - e) << 23) * (f == 1.0f ? 1.0f : ex2_approx(whole - lv));
+  iv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (f == 1.0f ? 1.0f : ex2_approx(whole - lv));
+  return nothing;
 }
 
 // The copy warp of a CTA: the tiles of its range, K (and V) through the rings
@@ -518,6 +529,7 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
   struct Page {
     int32_t at;                     // page heads + head, or -1
     float ks, lv, iv;
+    bool nothing;                   // no values
   };
   Cursor look = cur;
   Segment ahead;
@@ -541,10 +553,10 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
     }
   };
   auto scales = [&](const Batch& t) {
-    Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f, 0.0f};
+    Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f, 0.0f, false};
     if (pg.at >= 0) {
       pg.ks = p.c.k_scale[pg.at];
-      if (WITH_V) value_unit(p.c.v_scale[pg.at], pg.lv, pg.iv);
+      if (WITH_V) pg.nothing = value_unit(p.c.v_scale[pg.at], pg.lv, pg.iv);
     }
     return pg;
   };
@@ -557,13 +569,14 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
     const Page next_page = scales(next);
     fetch(later);
     const unsigned named = __ballot_sync(0xFFFFFFFFu, page.at >= 0);
+    const unsigned nothing = __ballot_sync(0xFFFFFFFFu, page.nothing);
     for (int i = 0; i < now.n; ++i, ++g) {
       const uint32_t st = g % ST, ms = g % MS;
       wait(sh.kempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
       if (WITH_V) wait(sh.vempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
       const int slot = lane - i * ppt;               // of this lane's page in the tile
       const bool mine = slot >= 0 && slot < ppt;
-      const unsigned pages = (named >> (i * ppt)) & (0xFFFFFFFFu >> (32 - ppt));
+      const unsigned tile_pages = 0xFFFFFFFFu >> (32 - ppt), pages = (named >> (i * ppt)) & tile_pages;
       if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) continue;   // (the whole warp or none)
       if (lane == 0) {
         const uint32_t bytes = static_cast<uint32_t>(__popc(pages) * ps * D);
@@ -586,6 +599,7 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
       }
       if (lane == 0) {
         m.pages = pages;
+        m.nothing = (nothing >> (i * ppt)) & tile_pages;
         m.left = min(kTile, now.len - static_cast<int32_t>(j0));
       }
       __syncwarp();
@@ -965,15 +979,37 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           lv[q] = m.lv[page];
           iv[q] = (seen_keys >> (8 * q + (lane >> 2))) & 1u ? m.iv[page] : 0.0f;   // (a masked page's may be NaN)
         }
-        if (!visible) {
+        const bool nothing = (m.nothing >> page_of) & 1u;
+        if (!visible || nothing) {
           // Codes of tokens that are not visible (any bytes, NaN among them)
-          // would meet probabilities of 0: they become zeros.
+          // would meet probabilities of 0: they become zeros.  So do those of
+          // pages without values, but NaN.
           wait(sh.vfull[g % ST], (g / ST) & 1u, kFaultFullWait);
           const uint32_t vrow = v_s + (g % ST) * kTileBytes + static_cast<uint32_t>(key) * D;
+          if (!visible) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) sts128(vrow + i * 16, 0u, 0u, 0u, 0u);
+            for (int i = 0; i < D / 16; ++i) sts128(vrow + i * 16, 0u, 0u, 0u, 0u);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < D / 4; ++i) {
+              uint32_t c;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c) : "r"(vrow + i * 4) : "memory");
+              c = __vcmpeq4(c & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & c;
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(vrow + i * 4), "r"(c) : "memory");
+            }
+          }
         }
         __syncwarp();
+        if (!seen) {
+          // Until a row has a reference of its own: the tile's largest value scale, so
+          // that no exponent is rounded for what the reference will take away.
+          float first_ref = -1e4f;
+          for (int page = 0; page < kTile >> ps_log; ++page)
+            if ((m.pages >> page) & 1u) first_ref = fmaxf(first_ref, m.lv[page]);
+#pragma unroll
+          for (int j = 0; j < J; ++j) nm2[j] = pack2(-first_ref, -first_ref);
+          if (tid < N) nm[tid] = -first_ref;
+        }
         wait(sh.sfull[grp], nth & 1u, kFaultFullWait);
         __syncwarp();
         at_fence_after();
@@ -999,8 +1035,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint32_t* v = &r[q >> 1][4 * j + 2 * (q & 1)];
-              x[q][j] = add2(fma2(at_mul2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(ck[q], ck[q])),
-                                  f2[j], nm2[j]), pack2(lv[q], lv[q]));
+              // (reference and scale first: they may both be large and next to equal)
+              x[q][j] = fma2(at_mul2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(ck[q], ck[q])), f2[j],
+                             add2(nm2[j], pack2(lv[q], lv[q])));
             }
           }
         }
@@ -1046,9 +1083,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             const float top = fmaxf(fmaxf(sh.red[grp][0][tid], sh.red[grp][1][tid]),
                                     fmaxf(sh.red[grp][2][tid], sh.red[grp][3][tid])) - kPShift;   // above the old reference
             const float up = top > 0.0f || (!seen && top > -kInf) ? top + kHead : 0.0f;
-            nm[tid] -= up;
-            sh.delta[grp][tid] = -up;
-            const float d = ex2_approx(-up);
+            const float was = nm[tid], now = was - up, delta = now - was;   // (-up, as the reference is rounded)
+            nm[tid] = now;
+            sh.delta[grp][tid] = delta;
+            const float d = ex2_approx(delta);
             sh.fac_l[grp][tid] = d;
             // (before any score the accumulator is all zeros, and d may be infinite)
             sh.fac_o[grp][place(tid)] = seen ? d : 0.0f;
@@ -1087,25 +1125,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         at_fence_before();                             // the scores have been read
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.sempty[grp]));
-        // P: summed in fp32, in three e4m3 parts for the product.  Next to pages of
-        // ordinary scales a tiny one's y can fall below what fp32 holds while its
-        // probability counts (all-zero values that draw attention): those tokens are
-        // summed by their scores alone.
-        if (fminf(fminf(lv[0], lv[1]), fminf(lv[2], lv[3])) < kTinyUnit) {   // (the same in all lanes)
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            if (j % 2 == 0 && 8 * j >= ncols) break;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float a, b;
-              unpack2(x[q][j], a, b);
-              if (lv[q] < kTinyUnit) l2[j] = add2(l2[j], pack2(ex2_approx(a - lv[q]), ex2_approx(b - lv[q])));
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (lv[q] < kTinyUnit) iv[q] = 0.0f;
-        }
+        // P: summed in fp32, in three e4m3 parts for the product.
         if (nth >= 1) wait(sh.pvdone[grp], (nth - 1) & 1u, kFaultEmptyWait);   // the product that read this buffer last
         __syncwarp();
 #pragma unroll
@@ -1186,7 +1206,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // (a NaN sum gives NaN)
           fa *= inv;
           fb *= inv;
-          p.lse[row] = l == 0.0f ? -kInf : m * kLn2 + logf(l);
+          p.lse[row] = lse_of(m, l);
         } else {
           p.part_ml[(slot * S::kRows + at) * 2] = m;
           p.part_ml[(slot * S::kRows + at) * 2 + 1] = l;
@@ -1645,7 +1665,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     uint16_t* to = p.out + row * D + lane * V;
     if constexpr (V == 4) *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
     else *reinterpret_cast<uint32_t*>(to) = u[0];
-    if (lane == 0) p.lse[row] = sum == 0.0f ? -kInf : m * kLn2 + logf(sum);
+    if (lane == 0) p.lse[row] = lse_of(m, sum);
   }
 }
 

@@ -479,7 +479,11 @@ dllm_status dllm_commit_step_host(const void* host_logits, void* dev_logits, dll
  * keys and one for its values; a token's key is code * scale.  The page is
  * the "block of tokens" that shares a scale.
  *   k, v              device, 16-byte aligned: codes [page][head][slot][dim]
- *   k_scale, v_scale  device: [page][head], finite and positive
+ *   k_scale, v_scale  device: [page][head], finite and positive.  A page whose
+ *                     value scale is 2^-100 or less (an append's for values
+ *                     below 2^-91) holds no values: an attention takes them as
+ *                     0, NaN as NaN.  Other value scales that one query meets
+ *                     are to lie within 2^100 of each other, 2^120 at most.
  * head_dim 64 or 128; page_size 16, 32, 64 or 128 (else DLLM_ERR_UNSUPPORTED).
  *
  * A sequence's pages are its row of a page table (device int32 (B, width),
@@ -549,8 +553,10 @@ dllm_status dllm_cache_append(const dllm_kv_cache* cache, const void* k, const v
  *              dllm_workspace_fault.
  * Sums and statistics are fp32.  Products are exact in the codes and in the
  * queries' 8 bits (a query's elements below 2^-9 of its largest are rounded at
- * 2^-18 of that); probabilities times value scales are rounded to fp16, no
- * finer than 2^-23 of a row's largest.  Results repeat bit for bit.
+ * 2^-18 of that); a probability times its value scale is rounded to fp16, by
+ * 2^-12 of itself or 2^-22 of the row's largest such product, whichever is more
+ * (a page without values counting as one of scale 2^-64).  Results repeat bit
+ * for bit.
  * DLLM_ERR_UNSUPPORTED also for pools of 2^31 or more token rows (pages heads
  * page_size). */
 size_t dllm_cache_attention_workspace_size(int64_t B, int64_t L, int64_t Hq, int64_t heads, int64_t head_dim);

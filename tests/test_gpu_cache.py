@@ -327,6 +327,36 @@ def test_attention_drawn_by_values_of_nothing(cs, L, G, small):
         check_attention(cs, arrays, q, table, lens, scale=scale)
 
 
+@pytest.mark.parametrize("L,G", [(1, 1), (8, 4), (25, 4)])
+def test_attention_of_pages_without_values(cs, L, G):
+    """What appends of zeros, of infinities and of NaN leave: the least scale, with codes
+    of 0, 448 and NaN.  Such a page draws its share; NaN stays, all else counts as 0."""
+    rng = np.random.default_rng(L)
+    ps, dim, H, width = 16, 64, 2, 20
+    arrays = [np.array(a) for a in random_pool(rng, width, H, ps, dim)]
+    least = [0, 7, 8, 9, 15]
+    arrays[3][least] = 2.0 ** -100
+    arrays[1][least] = 0
+    arrays[1][8, :, 3, 5:9] = 0x7E
+    arrays[1][9, 1, 4, 17], arrays[1][15, 0, 0, 63] = 0x7F, 0xFF
+    q = queries(rng, 1, L, H * G, dim)
+    table = np.arange(width, dtype=np.int32)[None]
+    check_attention(cs, arrays, q, table, np.array([width * ps - 5], np.int32))
+    check_attention(cs, arrays, q, table[:, :1].copy(), np.array([ps], np.int32))
+
+
+@pytest.mark.parametrize("scale_v", [2.0 ** -99, 2.0 ** -60, 1.3 * 2.0 ** -40, 2.0 ** 40, 1.9 * 2.0 ** 90, 2.0 ** 117])
+@pytest.mark.parametrize("L,G", [(1, 1), (8, 4), (25, 4)])
+def test_attention_of_values_of_any_size(cs, L, G, scale_v):
+    """One scale on all pages, over the range that appends make."""
+    rng = np.random.default_rng(L)
+    ps, dim, H, width = 16, 64, 2, 30
+    arrays = list(random_pool(rng, width, H, ps, dim))
+    arrays[3] = np.full_like(arrays[3], scale_v)
+    q = queries(rng, 1, L, H * G, dim)
+    check_attention(cs, arrays, q, np.arange(width, dtype=np.int32)[None], np.array([width * ps - 5], np.int32))
+
+
 def test_attention_strided_queries_and_stream(cs):
     rng = np.random.default_rng(6)
     ps, H, G, dim, B, width, L = 64, 2, 2, 128, 3, 4, 12
