@@ -11,6 +11,7 @@ error, each of sum p |v|.  A token's weight is a sum of probabilities.
 Codes, scales, kept positions and lengths are compared exactly.
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -456,6 +457,28 @@ def test_attention_in_a_graph_on_a_stream_that_goes_on(cs):
     assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
     assert torch.equal(got_more[0].view(torch.int16), want_more[0].view(torch.int16))
     assert torch.equal(got_more[1], want_more[1])
+
+
+def test_attention_from_two_threads_on_one_stream(cs):
+    """Calls whose items are cut among CTAs, enqueued between one another."""
+    rng = np.random.default_rng(24)
+    ps, H, dim, B, width = 64, 2, 128, 2, 40
+    cache = device_cache(cs, random_pool(rng, B * width, H, ps, dim))
+    table, lens = dev(tables(rng, B * width, B, width)), dev(np.array([2500, 900], dtype=np.int32))
+    qs = [queries(rng, B, 4, H * 2, dim) for _ in range(2)]
+    want = [cs.cache_attention(q, cache, table, lens)[0].view(torch.int16) for q in qs]
+    same = [[], []]
+
+    def work(i):
+        for _ in range(300):
+            same[i].append(torch.equal(cs.cache_attention(qs[i], cache, table, lens)[0].view(torch.int16), want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert [len(x) for x in same] == [300, 300] and all(map(all, same))
 
 
 def test_pages_past_4_gib(cs):
