@@ -457,9 +457,11 @@ constexpr int attend_smem() {
 
 struct TileMeta {
   alignas(16) uint8_t mask[kTile];  // the tile's part of the key mask, when there is one
-  float ks[8];                      // per page of the tile: scale log2 e s_k,
-  float lv[8], iv[8];               // log2(s_v / 4), and 4 / s_v
-  uint32_t pages, nothing;          // bits of the pages that exist, of those without values
+  // Per page of the tile: scale log2 e s_k, log2(s_v / 4), 4 / s_v, and the largest
+  // log2(s_v / 4) of the tile's pages (one store: with pages of 16 tokens the copy
+  // warp's instructions set the pace).
+  float4 page[8];
+  uint32_t pages;                   // bits of the pages that exist, and 16 bits up of those without values
   int32_t left;                     // tokens of the sequence in the tile
 };
 
@@ -528,8 +530,7 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
   };
   struct Page {
     int32_t at;                     // page heads + head, or -1
-    float ks, lv, iv;
-    bool nothing;                   // no values
+    float ks, vs;
   };
   Cursor look = cur;
   Segment ahead;
@@ -553,10 +554,10 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
     }
   };
   auto scales = [&](const Batch& t) {
-    Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f, 0.0f, false};
+    Page pg{t.id >= 0 && t.id < p.c.pages ? t.id * p.c.heads + t.h : -1, 0.0f, 0.0f};
     if (pg.at >= 0) {
       pg.ks = p.c.k_scale[pg.at];
-      if (WITH_V) pg.nothing = value_unit(p.c.v_scale[pg.at], pg.lv, pg.iv);
+      if (WITH_V) pg.vs = p.c.v_scale[pg.at];
     }
     return pg;
   };
@@ -569,7 +570,14 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
     const Page next_page = scales(next);
     fetch(later);
     const unsigned named = __ballot_sync(0xFFFFFFFFu, page.at >= 0);
-    const unsigned nothing = __ballot_sync(0xFFFFFFFFu, page.nothing);
+    float lv = 0.0f, iv = 0.0f, top = kUnset;
+    unsigned nothing = 0;
+    if (WITH_V) {                                      // (here, a batch after the scales were asked for)
+      const bool none = value_unit(page.vs, lv, iv) && page.at >= 0;
+      nothing = __ballot_sync(0xFFFFFFFFu, none);
+      if (page.at >= 0) top = lv;
+      for (int o = 1; o < ppt; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // of the tile
+    }
     for (int i = 0; i < now.n; ++i, ++g) {
       const uint32_t st = g % ST, ms = g % MS;
       wait(sh.kempty[st], ((g / ST) & 1u) ^ 1u, kFaultEmptyWait);
@@ -592,14 +600,9 @@ __device__ __forceinline__ void copy_role(const AttendParams& p, SH& sh, const C
       }
       TileMeta& m = sh.meta[ms];
       const int64_t j0 = static_cast<int64_t>(now.t0 + i) * kTile;
-      if (mine) {
-        m.ks[slot] = page.ks * p.scale2;
-        m.lv[slot] = page.lv;
-        m.iv[slot] = page.iv;
-      }
+      if (mine) m.page[slot] = make_float4(page.ks * p.scale2, lv, iv, top);
       if (lane == 0) {
-        m.pages = pages;
-        m.nothing = (nothing >> (i * ppt)) & tile_pages;
+        m.pages = pages | ((nothing >> (i * ppt)) & tile_pages) << 16;
         m.left = min(kTile, now.len - static_cast<int32_t>(j0));
       }
       __syncwarp();
@@ -971,15 +974,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const bool visible = tile_visible(m, key, page_of, p.mask != nullptr);
         const unsigned seen_keys = __ballot_sync(0xFFFFFFFFu, visible);
         // The four tokens' scales (8 consecutive tokens share a page).
-        float ck[4], lv[4], iv[4];
+        float ck[4], lv[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int page = (wq * 32 + 8 * q) >> ps_log;
-          ck[q] = m.ks[page];
-          lv[q] = m.lv[page];
-          iv[q] = (seen_keys >> (8 * q + (lane >> 2))) & 1u ? m.iv[page] : 0.0f;   // (a masked page's may be NaN)
+          ck[q] = m.page[page].x;
+          lv[q] = m.page[page].y;
         }
-        const bool nothing = (m.nothing >> page_of) & 1u;
+        const bool nothing = (m.pages >> (16 + page_of)) & 1u;
         if (!visible || nothing) {
           // Codes of tokens that are not visible (any bytes, NaN among them)
           // would meet probabilities of 0: they become zeros.  So do those of
@@ -1003,12 +1005,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (!seen) {
           // Until a row has a reference of its own: the tile's largest value scale, so
           // that no exponent is rounded for what the reference will take away.
-          float first_ref = -1e4f;
-          for (int page = 0; page < kTile >> ps_log; ++page)
-            if ((m.pages >> page) & 1u) first_ref = fmaxf(first_ref, m.lv[page]);
+          const float first = -m.page[0].w;
 #pragma unroll
-          for (int j = 0; j < J; ++j) nm2[j] = pack2(-first_ref, -first_ref);
-          if (tid < N) nm[tid] = -first_ref;
+          for (int j = 0; j < J; ++j) nm2[j] = pack2(first, first);
+          if (tid < N) nm[tid] = first;
         }
         wait(sh.sfull[grp], nth & 1u, kFaultFullWait);
         __syncwarp();
@@ -1126,6 +1126,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.sempty[grp]));
         // P: summed in fp32, in three e4m3 parts for the product.
+        float iv[4];                                   // (read here: registers are short above)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) iv[q] = m.page[(wq * 32 + 8 * q) >> ps_log].z;
         if (nth >= 1) wait(sh.pvdone[grp], (nth - 1) & 1u, kFaultEmptyWait);   // the product that read this buffer last
         __syncwarp();
 #pragma unroll
@@ -1482,7 +1485,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
         const bool valid = tile_visible(m, mine, mine >> ps_log, p.mask != nullptr);
         float ck[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) ck[q] = m.ks[(wq * 32 + 8 * q) >> ps_log];
+        for (int q = 0; q < 4; ++q) ck[q] = m.page[(wq * 32 + 8 * q) >> ps_log].x;
         uint64_t sum2[4] = {0, 0, 0, 0};
         for (int c = 0; c < chunks; ++c, ++jobs) {
           const uint32_t buf = static_cast<uint32_t>(grp) * kWeightBufs + jobs % kWeightBufs;
