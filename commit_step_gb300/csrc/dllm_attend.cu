@@ -29,14 +29,15 @@
 // A reference moves only when a y exceeds it by more than 2 (log2 units), so the
 // accumulators in TMEM are rarely rescaled; statistics and sums are fp32.
 //
-// Measured (head_dim 128, pages of 64 and 128 with one scale, where references
-// rise in few tiles, one GB300, replayed in a graph):
-// single tokens, 32 over 8 heads, 4 sequences of 60001 to 131072: 123 us, 6.3
-// TB/s of cache (95 % of a copy); blocks of 32 queries, 32 heads, 8 x 2306
-// tokens: 40 us, 243 TFLOP/s; 224 rows a head, 16 x 5096 tokens, 4 heads: 92 us,
-// 408 TFLOP/s, bound by the softmax groups' chain of waits and instructions (a
-// tile's 128 x 112 scores take 8 warps 4600 clocks, a third of them the three
-// parts of P; the products 1500).
+// Measured (head_dim 128, pages of 64 and 128, one GB300, replayed in a graph; with
+// one scale on all pages, where references rise in few tiles, and with scales of
+// three binades): single tokens, 32 over 8 heads, 4 sequences of 60001 to 131072:
+// 123 us both, 6.35 TB/s of cache (95 % of a copy); blocks of 32 queries, 32 heads,
+// 8 x 2306 tokens: 39.4 and 42.3 us, 245 and 229 TFLOP/s; 224 rows a head, 16 x
+// 5096 tokens, 4 heads: 87.4 and 100.8 us, 428 and 371 TFLOP/s, bound by the softmax
+// groups' chain of waits and instructions (of a tile's 3730 clocks in a group, for
+// 128 x 56 scores, 720 pass waiting for the scores, 530 reading them, 680 with the
+// maxima and the vote, 1270 with three binades, and 1220 with P; tensor pipe 29 %).
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
 #include <cuda_runtime.h>
 
@@ -894,8 +895,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     int32_t at_row[kLoads];
     // This thread's part of a segment's rows.  With 32 columns the next segment's
     // are fetched before this one's sums and epilogue (8 x 2306 tokens, 32 rows of
-    // 32 heads: 43.5 us, 44.4 without); with 64 the registers do not reach (114
-    // us, 98.9 without, for 224 rows).
+    // 32 heads: 39.4 us, 40.7 without); with 64 the registers do not reach (107
+    // us, 87.4 without, for 224 rows).
     constexpr bool kAhead = N == 32;
     auto fetch_rows = [&](const Segment& s) {
       const int row0 = s.rt * p.tile_rows, nrows = min(p.tile_rows, p.rows - row0);
@@ -1558,12 +1559,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1) attend_weights_kernel(const
 // reference may differ from the others').  Block (x, y) looks at the boundary
 // between CTAs x and x + 1: if an item is cut there for the first time, its
 // warps join rows 8 y .. 8 y + 7 of it, one each.  Where the item lies takes some
-// 500 instructions, which one warp runs for the block (224 rows a head, 16 x 5096
-// tokens, attention included: 92.8 us, 94.9 when every warp ran them; 8 x 2306
-// tokens, 32 rows of 32 heads: 41.8 us, 44.1 and 47.9 with 16 and 32 rows a
-// block).  It does so before the attention ends (12.4 us, 11.3 so, for a single
-// token over 1999), and asks for two parts' rows before their factors are known
-// (11.3 us, 9.9 so).
+// 500 instructions, which one warp runs for the block, before the attention ends,
+// and two parts' rows are asked for before their factors are known.  (What each
+// saved when it was built: the one warp 2.1 of 94.9 us at 224 rows a head, the early
+// start 1.1 of 12.4 and the early rows 1.4 of 11.3 at a single token over 1999.)
+// Rows a block: 8 x 2306 tokens, 32 rows of 32 heads, 39.4
+// us, 41.0 and 44.0 with 16 and 32; 224 rows a head, 16 x 5096 tokens, 87.4, 86.0
+// and 84.5; a single token the same.
 constexpr int kJoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p, int N, int columns) {
@@ -1756,12 +1758,11 @@ const AttendDevice* attend_device() {
 // The row tiles of a key head and the columns of a tile: as few tiles as 128
 // columns allow, equally filled, then the narrowest built width that holds one
 // (a width is the tensor core's N and the softmax's registers per token).
-// Measured (in a build that took 2 to 5 us longer throughout): 32 rows 44.7 us
-// with 32 columns, 56.7 with 64 (8 x 2306 tokens, 32 heads); 64 rows 62.1 us
-// taking turns with 64 columns, 75.7 paired, 70.0 as two tiles of 32 (16 x 5096
-// tokens, 8 heads); 112 rows 59.9 us paired, 60.8 as two tiles of 56, 67.7 as
-// four of 28; 224 rows of 2000 to 8192 tokens 99.5 us as two of 112, 105.3 as
-// four of 56.
+// Measured: 32 rows 39.4 us with 32 columns, 51.3 with 64 (8 x 2306 tokens, 32
+// heads); 64 rows 56.6 us taking turns with 64 columns, 66.0 paired, 65.0 as two
+// tiles of 32 (16 x 5096 tokens, 8 heads); 112 rows 54.6 us paired, 54.6 as two
+// tiles of 56, 59.7 as four of 28; 224 rows of 2000 to 8192 tokens 88.9 us as two of
+// 112, 95.6 as four of 56.
 struct RowTiles {
   int64_t tiles, rows, half;
   int columns;
@@ -1776,11 +1777,11 @@ RowTiles row_tiles(int64_t rows) {
 }
 
 // What an item costs besides its tiles, in tiles (about 7000 cycles against
-// 1500, 2500 and 4800 a tile).  With fewer tiles than SMs there is nothing to
-// balance, and each tile is a CTA's.  Measured in an earlier build: 32 sequences
-// of 100 to 4096 tokens, 4 rows of 8 heads, 89 us without and 42 with; 8 of 517
-// to 4096, 32 rows of 32 heads, 68 and 54.  One tile more or less: within 2 %, and
-// 37 us against 40 where one less is worst (the 32 sequences).
+// 1500, 2200 and 3700 a tile).  With fewer tiles than SMs there is nothing to
+// balance, and each tile is a CTA's.  Measured: 32 sequences of 100 to 4096 tokens,
+// 4 rows of 8 heads, 72.7 us without and 33.3 with; 8 of 517 to 4096, 32 rows of 32
+// heads, masked, 56.0 and 48.8; 16 of 2000 to 8192, 224 rows of 4 heads, 93.9 and
+// 88.9.  One tile more: 33.8, 49.3 and 87.8; one less: 35.8, 48.0 and 90.9.
 constexpr int32_t kSegCost32 = 4, kSegCost64 = 3, kSegCost128 = 2;
 
 constexpr size_t kAttendHeader = 256;  // the fault word

@@ -103,8 +103,9 @@ __device__ __forceinline__ float element(const uint4& v, int e) {
 // elements of a warp hold one that reaches it.)
 // Logits below -2^100 count as -2^100 in the pass; a row whose maximum is not
 // within 2^100 of zero is computed from its logits as they are by one CTA.
-// Bound: the one read of the logits.  Measured, 4096 x 152064 bf16: 192 us (6.5
-// TB/s) without alternatives, 236 us with the top 20; 32 x 126464, top 8: 11 us.
+// Bound: the one read of the logits.  Measured, 4096 x 152064 bf16: 191 us (6.5
+// TB/s) without alternatives, 233 us with the top 20; 2048 x 152064 fp32: 186 us
+// (6.7 TB/s) and 207 us; 32 x 126464 bf16, top 8: 11 us.
 template <int BYTES>
 __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_constant__ ScoreParams p) {
   constexpr int EPV = 16 / BYTES;
@@ -714,8 +715,10 @@ dllm_status dllm_token_logprobs(const void* logits, dllm_dtype dt, int64_t T, in
   // CTAs per row: doubled while the grid would leave SMs without work (304 =
   // two CTAs for each of 152 SMs) and every CTA still gets two passes of its
   // threads' vectors.  Measured, 126464 bf16, top 8, us with 1 / 2 / 4 / 8 CTAs:
-  // 32 rows 18.0 / 13.5 / 11.0 / 11.4, 128 rows 21.1 / 19.0 / 15.7 / 23.5, 256
-  // rows 27.7 / 21.3 / 28.2 / 43.4, 512 rows 31.3 / 38.0 / 51.5 / 81.0.
+  // 32 rows 18.4 / 13.4 / 11.4 / 11.2, 128 rows 23.3 / 19.0 / 14.7 / 22.3, 256
+  // rows 28.4 / 20.3 / 26.9 / 41.4, 512 rows 30.3 / 36.7 / 50.0 / 78.9; in fp32 26.7 /
+  // 18.8 / 13.6 / 11.8, 31.4 / 23.3 / 17.9 / 24.6, 36.3 / 27.5 / 33.7 / 46.4, 44.9 /
+  // 52.5 / 65.3 / 88.9.
   int cluster = 1;
   while (cluster < 8 && T * cluster < 304 && V * bytes >= 2 * cluster * 2 * 16 * kScoreThreads * kScoreVec) cluster *= 2;
   if (T > INT32_MAX / cluster) return DLLM_ERR_UNSUPPORTED;
