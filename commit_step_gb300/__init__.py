@@ -39,6 +39,9 @@ EXPORTS = (
     "dllm_lm_head_stats_workspace_size", "dllm_lm_head_stats", "dllm_uniform_update", "dllm_commit_step_host",
     "dllm_noalloc_fault", "dllm_cache_append", "dllm_cache_attention_workspace_size", "dllm_cache_attention",
     "dllm_cache_evict", "dllm_token_logprobs", "dllm_token_logprobs_backward",
+    "dllm_lm_head_logprobs_workspace_size", "dllm_lm_head_logprobs", "dllm_lm_head_logprobs_backward_workspace_size",
+    "dllm_lm_head_logprobs_backward", "dllm_embed_tokens", "dllm_embed_tokens_backward_workspace_size",
+    "dllm_embed_tokens_backward",
 )
 
 
@@ -110,6 +113,17 @@ def _load() -> C.CDLL:
     lib.dllm_token_logprobs.argtypes = [P, C.c_int, i64, i64, i64, P, P, i32, i32, P, P, P, P, P, P]
     lib.dllm_token_logprobs_backward.argtypes = [P, C.c_int, i64, i64, i64, P, P, i32, P, P, P, P, i32, P, P, P, i64,
                                                  P]
+    head = [P, i64, i64, i64, P, i64, i64, P, P, i32]
+    lib.dllm_lm_head_logprobs_workspace_size.argtypes = [i64] * 3
+    lib.dllm_lm_head_logprobs_workspace_size.restype = sz
+    lib.dllm_lm_head_logprobs.argtypes = head + [P, P, P, P, sz, P]
+    lib.dllm_lm_head_logprobs_backward_workspace_size.argtypes = [i64] * 3
+    lib.dllm_lm_head_logprobs_backward_workspace_size.restype = sz
+    lib.dllm_lm_head_logprobs_backward.argtypes = head + [P, P, P, P, P, i64, P, C.c_int, i64, i32, P, sz, P]
+    lib.dllm_embed_tokens.argtypes = [P, i64, i64, i64, P, C.c_int, i64, i64, i64, f32, P, P]
+    lib.dllm_embed_tokens_backward_workspace_size.argtypes = [i64] * 3
+    lib.dllm_embed_tokens_backward_workspace_size.restype = sz
+    lib.dllm_embed_tokens_backward.argtypes = [P, i64, i64, i64, P, C.c_int, i64, i64, f32, P, C.c_int, i64, i32, P, sz, P]
     for name in EXPORTS[3:]:
         if not name.endswith("_workspace_size"):
             getattr(lib, name).restype = C.c_int
@@ -789,6 +803,8 @@ def uniform_update(sample: torch.Tensor, accepted: torch.Tensor, step_argmax: to
                                     _ptr(stop.count), _ptr(done), _stream(stream)), "dllm_uniform_update")
 
 
-# The paged 8-bit cache and the scoring of given tokens (modules of their own).
+# The paged 8-bit cache, the scoring of given tokens, and a model's two ends (modules of their own).
 from .cache import KVCache, cache_append, cache_attention, cache_evict  # noqa: E402
+from .embed import embed_canvas, embed_tokens, embed_tokens_backward  # noqa: E402
+from .head import lm_head_logprobs, lm_head_logprobs_backward, score_hidden  # noqa: E402
 from .score import MAX_TOP, score_tokens, token_logprobs, token_logprobs_backward  # noqa: E402

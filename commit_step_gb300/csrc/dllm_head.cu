@@ -1,0 +1,1103 @@
+// dllm_head.cu -- scores of given tokens straight from the hidden states, and
+// their gradient: logits z = h W^T that are never stored (sm_103a).
+//
+// Only scored rows (a target in [0, V)) take part: a first kernel numbers them,
+// a second gathers their hidden states (unless all rows are scored), and every
+// later kernel reads their count n on the device.
+//
+// Forward: one matrix product whose epilogue folds a tile's logits into a
+// partial softmax (m, sum 2^y, sum 2^y y, y = (z - m) log2 e) per row; a last
+// kernel joins a row's partials.
+//
+// Backward, over pieces of the vocabulary so that only a piece of dz is ever
+// held (bf16, as the product's operands have to be): dz = the product again,
+// with p = exp(z - lse) and dz = -p (g + gH (z - lse + H)) + g [v = target] in its
+// epilogue; dH += dz W over the piece (K: the piece's ids); dW = dz^T H (K: the
+// scored rows).
+//
+// All products run on the 5th-generation tensor cores: TMA brings 64-wide slabs
+// of K into a ring in shared memory (128-byte swizzle), tcgen05.mma (bf16 in,
+// fp32 accumulate) fills one of two accumulators in TMEM while eight epilogue
+// warps empty the other.  K-major operands (hidden and weight in the first
+// product, dz in the second) lie as rows of 64 k; the others (weight in the
+// second, both in the third) are read as they lie in memory, MN-major, as rows
+// of 64 m or n.
+#include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <vector>
+
+#include "../../include/dllmcommit.h"
+#include "dllm_device.cuh"
+#include "dllm_launch.cuh"
+
+namespace dllm {
+
+constexpr int kHdBM = 128;                       // rows of an accumulator tile
+constexpr int kHdBN = 256;                       // its columns at most
+constexpr int kHdBK = 64;                        // K of a stage: one 128-byte swizzle row of bf16
+constexpr int kHdABytes = kHdBM * kHdBK * 2;     // 16 KB
+constexpr int kHdBBytes = kHdBN * kHdBK * 2;     // 32 KB
+constexpr int kHdStages = 4;
+constexpr int kHdEpiWarps = 8;                   // two warpgroups, each reads every other 32-column chunk of a tile
+constexpr int kHdTmaWarp = 10;
+constexpr int kHdMmaWarp = 11;
+constexpr int kHdThreads = 12 * 32;
+constexpr int kHdTmemCols = 512;
+constexpr int kHdSmem = kHdStages * (kHdABytes + kHdBBytes) + 1024;
+constexpr int kHdBand = 32;                      // row tiles that share a pass over the vocabulary (4096 rows: 32 MB of
+                                                 // hidden states of 4096 stay in L2 while the weight streams)
+constexpr float kHdCap = 0x1p+125f;              // logits are read within +-2^125 (NaN as the lowest): differences stay finite
+constexpr float kHdAbsent = -0x1p+126f;          // suppressed ids and columns past the vocabulary
+
+enum HeadOp { kHdScore, kHdDz, kHdDh, kHdDw };
+
+// A scored row's constants of the backward pass.
+struct HeadRow {
+  float lse, entropy, g, gh;
+};
+
+struct HeadParams {
+  CUtensorMap tm_a, tm_b;        // the operands; where one is the hidden states, the caller's tensor,
+  CUtensorMap tm_packed;         // read when every row is scored, and else their gathered copy
+  const int32_t* n_rows;         // device: the scored rows
+  int64_t T, V;
+  int64_t v0;                    // the piece's first id
+  int64_t cols;                  // its ids
+  int64_t d;
+  int32_t bn;                    // columns of a tile
+  int32_t n_n;                   // tiles along N
+  uint32_t idesc;
+  uint32_t a_bytes;              // what one load of A brings
+  const int32_t* target;         // per scored row
+  int32_t n_sup;
+  int32_t sup[DLLM_MAX_SUPPRESS];
+  float4* part;                  // score: (tiles along N, 2, rows): m, Z, S
+  int64_t part_rows;
+  float* z_target;               // score: per scored row
+  const HeadRow* row;            // dz
+  uint16_t* dz;                  // dz: (rows, dz_stride) bf16
+  int64_t dz_stride;
+  float* acc;                    // dh: (splits, row tiles x 128, acc_stride) fp32
+  int64_t acc_stride;
+  int32_t add;                   // dh: the piece is not the first
+  int32_t split_slabs;           // dh: the slabs of a whole piece, which decide the splits
+  void* grad_w;                  // dw
+  int64_t grad_w_stride;
+  int32_t grad_w_f32, accumulate;
+  int32_t* fault;
+};
+
+__host__ __device__ constexpr bool hd_a_mn(int op) { return op == kHdDw; }
+__host__ __device__ constexpr bool hd_b_mn(int op) { return op == kHdDh || op == kHdDw; }
+
+// Instruction descriptor of tcgen05.mma.kind::f16: fp32 accumulator (bits 4-5 =
+// 1), bf16 A and B (bits 7-9, 10-12 = 1), MN-major A, B (bits 15, 16), N / 8 in
+// bits 17-22, M / 16 in bits 24-28.
+constexpr uint32_t hd_idesc(int op, int bn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (hd_a_mn(op) ? 1u << 15 : 0u) | (hd_b_mn(op) ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(kHdBM >> 4) << 24);
+}
+
+// Shared-memory descriptor in the 128-byte swizzle: start / 16 in bits 0-13, the
+// leading offset / 16 in bits 16-29 (MN-major: the distance of spans of 64 along
+// M or N; K-major: unused), the stride offset / 16 in bits 32-45 (1024 bytes, 8
+// rows of 128), version 1 at bit 46, swizzle 2 at bits 61-63.
+__device__ __forceinline__ uint64_t hd_desc(uint32_t addr, uint32_t leading) {
+  const uint32_t lo = ((addr & 0x3FFFFu) >> 4) | (leading >> 4) << 16;
+  const uint32_t hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+__device__ __forceinline__ void hd_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void hd_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void hd_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void hd_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void hd_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 consecutive fp32 columns of this warp's 32 TMEM lanes, one lane a thread.
+__device__ __forceinline__ void hd_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A bounded wait: false after the deadline or once the CTA gave up.
+__device__ __forceinline__ bool hd_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitLimitCycles) return false;
+  }
+}
+
+__device__ __forceinline__ void hd_fail(const HeadParams& p, volatile int32_t* abort_flag, int32_t code) {
+  if (!*abort_flag) {
+    atomicExch(p.fault, code);
+    *abort_flag = 1;
+  }
+}
+
+// bf16 pair, lo in the low half.
+__device__ __forceinline__ uint32_t hd_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// How many ways the second product's K is split, for n scored rows (the same
+// answer in the product and in the kernel that joins the parts).
+__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int ctas, int slabs) {
+  const int64_t tiles = (n + kHdBM - 1) / kHdBM * n_n;
+  if (tiles == 0) return 1;
+  const int64_t s = ctas / tiles;
+  return static_cast<int>(s < 1 ? 1 : (s > slabs ? slabs : s));
+}
+
+// The tiles of a product and the order in which the CTAs take them (tile i to
+// CTA i mod grid).  A split of a short last piece may hold no slab: such a tile
+// is passed over (what it adds to, an earlier piece has written).
+struct HeadTile {
+  int32_t m, n;        // tile coordinates
+  int32_t k0, k1;      // slabs
+  int32_t split;
+};
+
+template <int OP>
+struct HeadWork {
+  int64_t n;           // scored rows
+  int32_t n_m, n_n, slabs, splits;
+  int64_t total;
+
+  __device__ __forceinline__ HeadWork(const HeadParams& p, int64_t rows) : n(rows), n_n(p.n_n), splits(1) {
+    if (OP == kHdScore || OP == kHdDz) {
+      n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
+      slabs = static_cast<int32_t>((p.d + kHdBK - 1) / kHdBK);
+    } else if (OP == kHdDh) {
+      n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
+      slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
+      splits = hd_splits(n, n_n, gridDim.x, p.split_slabs);
+    } else {
+      n_m = static_cast<int32_t>((p.cols + kHdBM - 1) / kHdBM);
+      slabs = static_cast<int32_t>((n + kHdBK - 1) / kHdBK);
+    }
+    total = n == 0 ? 0 : static_cast<int64_t>(n_m) * n_n * splits;
+  }
+
+  __device__ __forceinline__ HeadTile tile(int64_t i) const {
+    HeadTile t;
+    t.split = 0;
+    t.k0 = 0;
+    t.k1 = slabs;
+    if (OP == kHdScore || OP == kHdDz) {
+      // bands of row tiles, each over the whole vocabulary, its row tiles inner
+      const int64_t per_band = static_cast<int64_t>(kHdBand) * n_n;
+      const int32_t band = static_cast<int32_t>(i / per_band);
+      const int32_t in = static_cast<int32_t>(i - band * per_band);
+      const int32_t rows = min(kHdBand, n_m - band * kHdBand);
+      t.m = band * kHdBand + in % rows;
+      t.n = in / rows;
+    } else if (OP == kHdDh) {
+      const int64_t tiles = static_cast<int64_t>(n_m) * n_n;
+      t.split = static_cast<int32_t>(i / tiles);
+      const int32_t in = static_cast<int32_t>(i - t.split * tiles);
+      t.m = in / n_n;
+      t.n = in % n_n;
+      t.k0 = static_cast<int32_t>(static_cast<int64_t>(slabs) * t.split / splits);
+      t.k1 = static_cast<int32_t>(static_cast<int64_t>(slabs) * (t.split + 1) / splits);
+    } else {
+      t.m = static_cast<int32_t>(i / n_n);
+      t.n = static_cast<int32_t>(i % n_n);
+    }
+    return t;
+  }
+};
+
+// A row's running softmax: m, and sums of 2^y and 2^y y with y = (z - m) log2 e.
+struct HeadSoft {
+  float m, Z, S;
+};
+
+__device__ __forceinline__ void hd_raise(HeadSoft& a, float m) {
+  const float d = fmaxf(a.m - m, -1000.0f) * kLog2e, f = ex2_approx(d);
+  a.S = f * fmaf(d, a.Z, a.S);
+  a.Z *= f;
+  a.m = m;
+}
+
+__device__ __forceinline__ void hd_join(HeadSoft& a, HeadSoft b) {
+  const float m = fmaxf(a.m, b.m);
+  hd_raise(a, m);
+  hd_raise(b, m);
+  a.Z += b.Z;
+  a.S += b.S;
+}
+
+// The columns of a 32-column chunk at id v0 that hold no id to be counted.
+__device__ __forceinline__ uint32_t hd_absent(const int32_t* sup, int n_sup, int64_t v0, int lim) {
+  uint32_t absent = lim >= 32 ? 0u : ~((1u << lim) - 1u);
+  for (int q = 0; q < n_sup; ++q) {
+    const int64_t off = sup[q] - v0;
+    if (off >= 0 && off < 32) absent |= 1u << off;
+  }
+  return absent;
+}
+
+// 32 columns of an accumulator row to bf16 or fp32 memory, in 16-byte stores;
+// `lim` columns (a multiple of 8) exist.  With `add` the old values are added.
+__device__ __forceinline__ void hd_store_bf16(uint16_t* out, const float (&x)[32], int lim, bool add) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) {
+    if (j >= lim) break;
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[j + e];
+    uint4* at = reinterpret_cast<uint4*>(out + j);
+    if (add) {
+      const uint4 o = *at;
+      y[0] += bf16lo(o.x), y[1] += bf16hi(o.x), y[2] += bf16lo(o.y), y[3] += bf16hi(o.y);
+      y[4] += bf16lo(o.z), y[5] += bf16hi(o.z), y[6] += bf16lo(o.w), y[7] += bf16hi(o.w);
+    }
+    *at = make_uint4(hd_bf16x2(y[0], y[1]), hd_bf16x2(y[2], y[3]), hd_bf16x2(y[4], y[5]), hd_bf16x2(y[6], y[7]));
+  }
+}
+
+__device__ __forceinline__ void hd_store_f32(float* out, const float (&x)[32], int lim, bool add) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    if (j >= lim) break;
+    float4* at = reinterpret_cast<float4*>(out + j);
+    float4 y = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    if (add) {
+      const float4 o = *at;
+      y.x += o.x, y.y += o.y, y.z += o.z, y.w += o.w;
+    }
+    *at = y;
+  }
+}
+
+template <int OP>
+__global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_constant__ HeadParams p) {
+  extern __shared__ __align__(1024) uint8_t hd_smem[];
+  __shared__ __align__(8) uint64_t full_bar[kHdStages], empty_bar[kHdStages], accf_bar[2], acce_bar[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int32_t abort_flag_s;
+  __shared__ int32_t sup_s[DLLM_MAX_SUPPRESS];
+  volatile int32_t* abort_flag = &abort_flag_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = (smem_addr(hd_smem) + 1023u) & ~1023u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kHdStages; ++s) {
+      mbar_init(smem_addr(&full_bar[s]), 1);
+      mbar_init(smem_addr(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_addr(&accf_bar[b]), 1);
+      mbar_init(smem_addr(&acce_bar[b]), kHdEpiWarps);
+    }
+    abort_flag_s = 0;
+    fence_mbar_init();
+  }
+  for (int q = threadIdx.x; q < p.n_sup; q += blockDim.x) sup_s[q] = p.sup[q];
+  if (warp == kHdMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+                 "r"(kHdTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  hd_fence_before();
+  __syncthreads();
+  hd_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t n = *p.n_rows;
+  const HeadWork<OP> work(p, n);
+  const bool packed = n != p.T;
+
+  if (warp == kHdTmaWarp) {
+    if (lane == 0) {
+      const CUtensorMap* ma = (OP == kHdScore || OP == kHdDz) && packed ? &p.tm_packed : &p.tm_a;
+      const CUtensorMap* mb = OP == kHdDw && packed ? &p.tm_packed : &p.tm_b;
+      const uint32_t tx = p.a_bytes + static_cast<uint32_t>(p.bn) * kHdBK * 2;
+      int s = 0;
+      uint32_t ph = 0;
+      int64_t issued = 0;
+      for (int64_t i = blockIdx.x; i < work.total && !*abort_flag; i += gridDim.x) {
+        const HeadTile t = work.tile(i);
+        const int m0 = t.m * kHdBM, n0 = t.n * p.bn;
+        for (int k = t.k0; k < t.k1; ++k) {
+          if (!hd_wait(smem_addr(&empty_bar[s]), ph ^ 1u, abort_flag)) {
+            hd_fail(p, abort_flag, kFaultEmptyWait);
+            break;
+          }
+          const uint32_t bar = smem_addr(&full_bar[s]);
+          const uint32_t a = ring + static_cast<uint32_t>(s) * (kHdABytes + kHdBBytes), b = a + kHdABytes;
+          mbar_arrive_expect_tx(bar, tx);
+          if (hd_a_mn(OP)) {
+            hd_load(a, ma, m0, k * kHdBK, bar);
+            hd_load(a + 8192, ma, m0 + 64, k * kHdBK, bar);
+          } else {
+            hd_load(a, ma, k * kHdBK, m0, bar);
+          }
+          if (OP == kHdScore || OP == kHdDz) {
+            hd_load(b, mb, k * kHdBK, static_cast<int>(p.v0) + n0, bar);
+          } else {
+            const int y = (OP == kHdDh ? static_cast<int>(p.v0) : 0) + k * kHdBK;
+            for (int x = 0; x < p.bn; x += 64) hd_load(b + x * 128, mb, n0 + x, y, bar);
+          }
+          ++issued;
+          if (++s == kHdStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // Giving up: the copies still in flight land before the CTA ends.
+      if (*abort_flag)
+        for (int64_t q = issued > kHdStages ? issued - kHdStages : 0; q < issued; ++q)
+          mbar_wait_bounded(smem_addr(&full_bar[q % kHdStages]), static_cast<uint32_t>((q / kHdStages) & 1));
+    }
+  } else if (warp == kHdMmaWarp) {
+    if (lane == 0) {
+      int s = 0, j = 0;
+      uint32_t ph = 0;
+      for (int64_t i = blockIdx.x; i < work.total && !*abort_flag; i += gridDim.x) {
+        const HeadTile t = work.tile(i);
+        if (t.k0 == t.k1) continue;
+        const int buf = j & 1;
+        if (!hd_wait(smem_addr(&acce_bar[buf]), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag)) {
+          hd_fail(p, abort_flag, kFaultEmptyWait);
+          break;
+        }
+        hd_fence_after();
+        const uint32_t d_tmem = tmem + static_cast<uint32_t>(buf * kHdBN);
+        for (int k = t.k0; k < t.k1; ++k) {
+          if (!hd_wait(smem_addr(&full_bar[s]), ph, abort_flag)) {
+            hd_fail(p, abort_flag, kFaultFullWait);
+            break;
+          }
+          hd_fence_after();
+          const uint32_t a = ring + static_cast<uint32_t>(s) * (kHdABytes + kHdBBytes), b = a + kHdABytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes of a K-major row, 16 rows of 128 bytes MN-major
+            hd_mma(d_tmem, hd_desc(a + kk * (hd_a_mn(OP) ? 2048 : 32), 8192), hd_desc(b + kk * (hd_b_mn(OP) ? 2048 : 32), 8192),
+                   p.idesc, k != t.k0 || kk != 0 ? 1u : 0u);
+          hd_commit(smem_addr(&empty_bar[s]));
+          if (++s == kHdStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        hd_commit(smem_addr(&accf_bar[buf]));
+        ++j;
+      }
+    }
+  } else if (warp < kHdEpiWarps) {
+    const int ew = warp & 3, half = warp >> 2;
+    int j = 0;
+    for (int64_t i = blockIdx.x; i < work.total; i += gridDim.x) {
+      const HeadTile t = work.tile(i);
+      if (t.k0 == t.k1) continue;
+      const int buf = j & 1;
+      const int64_t row = static_cast<int64_t>(t.m) * kHdBM + ew * 32 + lane;   // scored row, or (dw) id of the piece
+      HeadRow info{};
+      int32_t target = -1;
+      if (OP == kHdScore && row < n) target = p.target[row];
+      if (OP == kHdDz && row < n) {
+        target = p.target[row];
+        info = p.row[row];
+      }
+      // warp-uniform: the TMEM loads below are .sync.aligned
+      const bool ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&accf_bar[buf]), static_cast<uint32_t>((j >> 1) & 1), abort_flag));
+      if (!ok) {
+        if (lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
+        break;
+      }
+      hd_fence_after();
+      ++j;
+      const int64_t col0 = static_cast<int64_t>(t.n) * p.bn;
+      const int64_t width = OP == kHdScore || OP == kHdDz ? p.cols : p.d;
+      const int in_tile = static_cast<int>(min(static_cast<int64_t>(p.bn), width - col0));
+      HeadSoft soft{-kHdCap, 0.0f, 0.0f};
+      // Rows a warp has to visit: those that exist; of dz also the rows up to the
+      // end of the third product's last slab, which read as zero.
+      const int64_t visit = OP == kHdDw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : n);
+      const bool warp_rows = row - lane < visit;
+#pragma unroll 1
+      for (int c = half * 32; c < p.bn; c += 64) {
+        if (!warp_rows || (c >= in_tile && OP != kHdDz)) break;
+        uint32_t r[32];
+        hd_ld32(tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * kHdBN + c), r);
+        const int lim = min(32, in_tile - c);
+        float x[32];
+        if (OP == kHdScore || OP == kHdDz) {
+          const int64_t v = p.v0 + col0 + c;
+          const uint32_t absent = lim <= 0 ? 0xFFFFFFFFu : hd_absent(sup_s, p.n_sup, v, lim);
+          const int64_t hit = target - v;
+          if (OP == kHdScore) {
+            if (hit >= 0 && hit < 32 && row < n) {
+              float zt = 0.0f;
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q == hit) zt = __uint_as_float(r[q]);
+              if (hit < lim) p.z_target[row] = fminf(fmaxf(zt, -kHdCap), kHdCap);
+            }
+#pragma unroll
+            for (int q = 0; q < 32; ++q) x[q] = fminf(fmaxf(__uint_as_float(r[q]), -kHdCap), kHdCap);
+            if (absent != 0u) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if ((absent >> q) & 1u) x[q] = kHdAbsent;
+            }
+            float cm[4] = {-kHdCap, -kHdCap, -kHdCap, -kHdCap};
+#pragma unroll
+            for (int q = 0; q < 32; ++q) cm[q & 3] = fmaxf(cm[q & 3], x[q]);
+            const float m = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
+            if (m > soft.m) hd_raise(soft, m);
+            float Z[4] = {0.0f, 0.0f, 0.0f, 0.0f}, S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float y = (x[q] - soft.m) * kLog2e, e = ex2_approx(y);
+              Z[q & 3] += e;
+              S[q & 3] = fmaf(e, y, S[q & 3]);
+            }
+            soft.Z += (Z[0] + Z[1]) + (Z[2] + Z[3]);
+            soft.S += (S[0] + S[1]) + (S[2] + S[3]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float y = fmaxf(__uint_as_float(r[q]), -kHdCap) - info.lse;
+              const float e = ex2_approx(y * kLog2e);
+              x[q] = -e * fmaf(info.gh, y + info.entropy, info.g);
+            }
+            if (hit >= 0 && hit < 32) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q == hit) x[q] += info.g;
+            }
+            if (absent != 0u || row >= n) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (((absent >> q) & 1u) || row >= n) x[q] = 0.0f;
+            }
+            if (row < visit) hd_store_bf16(p.dz + row * p.dz_stride + col0 + c, x, 32, false);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(r[q]);
+          if (row < visit) {
+            if (OP == kHdDh) {
+              float* out = p.acc + (static_cast<int64_t>(t.split) * work.n_m * kHdBM + row) * p.acc_stride + col0 + c;
+              hd_store_f32(out, x, lim, p.add != 0);
+            } else if (p.grad_w_f32) {
+              hd_store_f32(static_cast<float*>(p.grad_w) + (p.v0 + row) * p.grad_w_stride + col0 + c, x, lim, p.accumulate != 0);
+            } else {
+              hd_store_bf16(static_cast<uint16_t*>(p.grad_w) + (p.v0 + row) * p.grad_w_stride + col0 + c, x, lim,
+                            p.accumulate != 0);
+            }
+          }
+        }
+      }
+      hd_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&acce_bar[buf]));
+      if (OP == kHdScore && row < n)
+        p.part[(static_cast<int64_t>(t.n) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
+    }
+  }
+  // The third product without a scored row: the gradient is zero.
+  if (OP == kHdDw && n == 0 && !p.accumulate) {
+    const int64_t chunks = p.d / 8 * (p.grad_w_f32 ? 2 : 1);
+    const int64_t stride = p.grad_w_stride * (p.grad_w_f32 ? 4 : 2);
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(kHdThreads) + threadIdx.x; i < p.cols * chunks;
+         i += static_cast<int64_t>(gridDim.x) * kHdThreads)
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.grad_w) + (p.v0 + i / chunks) * stride + i % chunks * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+  }
+  // Every product has completed (the epilogue waited for each accumulator) or
+  // the CTA gave up; release the TMEM.
+  hd_fence_before();
+  __syncthreads();
+  if (warp == kHdMmaWarp) {
+    hd_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kHdTmemCols) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Numbering the scored rows
+// ---------------------------------------------------------------------------
+constexpr int kHdListThreads = 1024;
+
+struct HeadListParams {
+  const int32_t* targets;
+  int64_t T, V;
+  int32_t backward;
+  const float *lse, *entropy, *g, *gh;     // backward (g, gh nullable)
+  int32_t n_sup;
+  int32_t sup[DLLM_MAX_SUPPRESS];
+  int32_t* n_rows;
+  int32_t* rows;                           // scored row -> row
+  int32_t* place;                          // backward: row -> scored row, or -1
+  int32_t* target;                         // per scored row
+  HeadRow* row;                            // backward: per scored row
+  float *o_logprob, *o_entropy, *o_lse;    // forward: rows that are not scored get 0
+};
+
+// A row of the forward pass is scored when it has a target; in the backward pass
+// it counts when a gradient reaches it (and its log-sum-exp is finite).  A
+// suppressed target has no gradient.
+__device__ __forceinline__ bool hd_row(const HeadListParams& p, int64_t t, HeadRow* out) {
+  const int32_t v = p.targets[t];
+  if (v < 0 || v >= p.V) return false;
+  if (!p.backward) return true;
+  HeadRow r;
+  r.lse = p.lse[t];
+  r.entropy = p.entropy[t];
+  r.g = p.g ? p.g[t] : 0.0f;
+  r.gh = p.gh ? p.gh[t] : 0.0f;
+  for (int q = 0; q < p.n_sup; ++q)
+    if (p.sup[q] == v) r.g = 0.0f;
+  *out = r;
+  return isfinite(r.lse) && (r.g != 0.0f || r.gh != 0.0f);
+}
+
+__global__ void __launch_bounds__(kHdListThreads) head_list_kernel(const __grid_constant__ HeadListParams p) {
+  __shared__ int32_t sums[32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t per = (p.T + kHdListThreads - 1) / kHdListThreads;
+  const int64_t t0 = min(p.T, tid * per), t1 = min(p.T, t0 + per);
+  HeadRow r{};
+  int32_t count = 0;
+  for (int64_t t = t0; t < t1; ++t) count += hd_row(p, t, &r) ? 1 : 0;
+  int32_t scan = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sums[warp] = scan;
+  __syncthreads();
+  if (warp == 0) {
+    int32_t s = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += v;
+    }
+    sums[lane] = s;
+  }
+  __syncthreads();
+  int32_t at = scan - count + (warp > 0 ? sums[warp - 1] : 0);
+  if (tid == 0) *p.n_rows = sums[31];
+  for (int64_t t = t0; t < t1; ++t) {
+    if (hd_row(p, t, &r)) {
+      p.rows[at] = static_cast<int32_t>(t);
+      p.target[at] = p.targets[t];
+      if (p.backward) {
+        p.row[at] = r;
+        p.place[t] = at;
+      }
+      ++at;
+    } else if (p.backward) {
+      p.place[t] = -1;
+    } else {
+      p.o_logprob[t] = 0.0f;
+      p.o_entropy[t] = 0.0f;
+      p.o_lse[t] = 0.0f;
+    }
+  }
+}
+
+// The scored rows' hidden states one after the other, with rows of zeros up to
+// the next multiple of 64 (the third product's K); nothing when every row is
+// scored.  A warp a row.
+__global__ void __launch_bounds__(256) head_gather_kernel(const uint16_t* hidden, int64_t stride, int64_t T, int64_t d,
+                                                          const int32_t* n_rows, const int32_t* rows, uint16_t* out) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t n = *n_rows;
+  if (n == T) return;
+  const int64_t end = (n + kHdBK - 1) / kHdBK * kHdBK;
+  const int lane = threadIdx.x & 31;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(8) + (threadIdx.x >> 5); i < end; i += static_cast<int64_t>(gridDim.x) * 8) {
+    const uint4* from = i < n ? reinterpret_cast<const uint4*>(hidden + rows[i] * stride) : nullptr;
+    uint4* to = reinterpret_cast<uint4*>(out + i * d);
+    for (int64_t q = lane; q < d / 8; q += 32) to[q] = from ? from[q] : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The last kernels
+// ---------------------------------------------------------------------------
+struct HeadFinishParams {
+  const int32_t *n_rows, *rows, *target;
+  const float4* part;
+  int64_t part_rows;
+  int32_t parts;
+  const float* z_target;
+  int32_t n_sup;
+  int32_t sup[DLLM_MAX_SUPPRESS];
+  float ln_ids;                  // ln |A|
+  float *logprob, *entropy, *lse;
+};
+
+// 32 rows a block: a lane a row, the warps share its partials.
+__global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant__ HeadFinishParams p) {
+  __shared__ HeadSoft s[32][33];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n = *p.n_rows;
+  for (int64_t base = blockIdx.x * static_cast<int64_t>(32); base < n; base += static_cast<int64_t>(gridDim.x) * 32) {
+    const int64_t row = base + lane;
+    HeadSoft a{-kHdCap, 0.0f, 0.0f};
+    if (row < n)
+      for (int q = warp; q < p.parts; q += 32) {
+        const float4 v = p.part[q * p.part_rows + row];
+        hd_join(a, HeadSoft{v.x, v.y, v.z});
+      }
+    s[warp][lane] = a;
+    __syncthreads();
+    if (warp == 0 && row < n) {
+      for (int q = 1; q < 32; ++q) hd_join(a, s[q][lane]);
+      const float lnZ = logf(a.Z);
+      const int32_t t = p.rows[row], v = p.target[row];
+      bool gone = false;
+      for (int q = 0; q < p.n_sup; ++q) gone = gone || p.sup[q] == v;
+      p.logprob[t] = gone ? -INFINITY : (p.z_target[row] - a.m) - lnZ;
+      p.entropy[t] = fminf(fmaxf(fmaf(-kLn2, a.S / a.Z, lnZ), 0.0f), p.ln_ids);
+      p.lse[t] = a.m >= kHdCap ? INFINITY : (a.m <= -kHdCap ? -INFINITY : a.m + lnZ);
+    }
+    __syncthreads();
+  }
+}
+
+// grad_hidden from the second product's parts, added in order: a block a row.
+__global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, const int32_t* place, const float* acc,
+                                                      int64_t acc_stride, int32_t n_n, int32_t ctas, int32_t slabs,
+                                                      int64_t T, int64_t d, uint16_t* out, int64_t out_stride) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t n = *n_rows;
+  const int splits = hd_splits(n, n_n, ctas, slabs);
+  const int64_t step = (n + kHdBM - 1) / kHdBM * kHdBM * acc_stride;
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    const int32_t row = place[t];
+    for (int64_t c = threadIdx.x * 8; c < d; c += 256 * 8) {
+      float y[8] = {};
+      if (row >= 0)
+        for (int s = 0; s < splits; ++s) {
+          const float4* at = reinterpret_cast<const float4*>(acc + s * step + row * acc_stride + c);
+          const float4 a = at[0], b = at[1];
+          y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
+          y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
+        }
+      *reinterpret_cast<uint4*>(out + t * out_stride + c) =
+          make_uint4(hd_bf16x2(y[0], y[1]), hd_bf16x2(y[2], y[3]), hd_bf16x2(y[4], y[5]), hd_bf16x2(y[6], y[7]));
+    }
+  }
+}
+
+}  // namespace dllm
+
+namespace {
+
+using namespace dllm;
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, []() {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// rows x cols of bf16 (cols contiguous), read in boxes of box_rows x 64 columns
+// in the 128-byte swizzle; what lies outside reads as 0.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t stride, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kHdBK), box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct HdDevice {
+  int sms = 0;
+  cudaError_t err = cudaSuccess;
+};
+HdDevice g_hd[64];
+std::once_flag g_hd_once[64];
+
+const HdDevice* hd_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  std::call_once(g_hd_once[dev], [dev]() {
+    HdDevice& d = g_hd[dev];
+    d.err = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    for (const void* k : {reinterpret_cast<const void*>(&head_kernel<kHdScore>), reinterpret_cast<const void*>(&head_kernel<kHdDz>),
+                          reinterpret_cast<const void*>(&head_kernel<kHdDh>), reinterpret_cast<const void*>(&head_kernel<kHdDw>)})
+      if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kHdSmem);
+    if (d.err != cudaSuccess) (void)cudaGetLastError();  // report through the status, leave no sticky error
+  });
+  return g_hd[dev].err == cudaSuccess ? &g_hd[dev] : nullptr;
+}
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// How a call uses its workspace, and its tiles.
+struct HdPlan {
+  int64_t t_pad;        // T to whole tiles
+  int32_t bn_v, n_v;    // tiles along the vocabulary (a piece of it in the backward pass)
+  int32_t bn_d, n_d;    // along d
+  int64_t piece;        // ids of a piece
+  int64_t acc;          // floats of the second product's parts
+  size_t rows, target, place, row, z_target, hidden, part, dz, accs, bytes;   // offsets, size
+};
+
+constexpr int64_t kPieceElements = int64_t{1} << 28;  // of dz: 512 MB
+
+HdPlan hd_plan(int64_t T, int64_t V, int64_t d, int64_t sms, bool backward) {
+  HdPlan h{};
+  h.t_pad = round_up(T, kHdBM);
+  int64_t piece = round_up(V, kHdBN);
+  if (backward) {
+    const int64_t most = std::max<int64_t>(4096, kPieceElements / h.t_pad / kHdBN * kHdBN);
+    const int64_t pieces = (V + most - 1) / most;
+    piece = round_up((V + pieces - 1) / pieces, kHdBN);
+  }
+  h.piece = piece;
+  h.bn_v = kHdBN;
+  h.n_v = static_cast<int32_t>(piece / kHdBN);
+  h.n_d = static_cast<int32_t>((d + kHdBN - 1) / kHdBN);
+  h.bn_d = static_cast<int32_t>(round_up((d + h.n_d - 1) / h.n_d, 64));
+  h.n_d = static_cast<int32_t>((d + h.bn_d - 1) / h.bn_d);
+  h.acc = std::max<int64_t>(h.t_pad * h.n_d * h.bn_d, sms * kHdBM * kHdBN);
+  size_t at = 256;
+  auto take = [&at](int64_t bytes) {
+    const size_t here = at;
+    at += static_cast<size_t>(round_up(bytes, 256));
+    return here;
+  };
+  h.rows = take(4 * T);
+  h.target = take(4 * T);
+  h.hidden = take(2 * d * round_up(T, kHdBK));
+  if (backward) {
+    h.place = take(4 * T);
+    h.row = take(static_cast<int64_t>(sizeof(HeadRow)) * T);
+    h.dz = take(2 * h.t_pad * h.piece);
+    h.accs = take(4 * h.acc);
+  } else {
+    h.z_target = take(4 * T);
+    h.part = take(static_cast<int64_t>(sizeof(float4)) * 2 * h.n_v * h.t_pad);
+  }
+  h.bytes = at;
+  return h;
+}
+
+constexpr int64_t kHdMaxT = int64_t{1} << 24, kHdMaxD = int64_t{1} << 20;
+
+// What forward and backward check alike; `sup` takes the suppressed ids.
+dllm_status hd_check(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride, const void* weight, int64_t V,
+                     int64_t weight_stride, const int32_t* targets, const int32_t* suppress_ids, int32_t n_suppress,
+                     std::vector<int32_t>& sup) {
+  if (T < 0 || V < 1 || V > INT32_MAX || d < 1) return DLLM_ERR_INVALID_ARGUMENT;
+  if (hidden_stride < d || weight_stride < d) return DLLM_ERR_INVALID_ARGUMENT;
+  if (mul_or_neg(mul_or_neg(T, hidden_stride), 2) < 0 || mul_or_neg(mul_or_neg(V, weight_stride), 4) < 0)
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (n_suppress < 0 || (n_suppress > 0 && !suppress_ids)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (n_suppress > DLLM_MAX_SUPPRESS) return DLLM_ERR_UNSUPPORTED;
+  sup.assign(suppress_ids, suppress_ids + n_suppress);
+  for (int32_t id : sup)
+    if (id < 0 || id >= V) return DLLM_ERR_INVALID_ARGUMENT;
+  std::sort(sup.begin(), sup.end());
+  sup.erase(std::unique(sup.begin(), sup.end()), sup.end());
+  if (static_cast<int64_t>(sup.size()) >= V) return DLLM_ERR_INVALID_ARGUMENT;
+  if (T == 0) return DLLM_OK;
+  if (!hidden || !weight || !targets || !aligned4(targets)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (d % 8 != 0 || !aligned16(hidden) || !aligned16(weight) || hidden_stride % 8 != 0 || weight_stride % 8 != 0)
+    return DLLM_ERR_UNSUPPORTED;
+  if (T > kHdMaxT || d > kHdMaxD || hidden_stride > (int64_t{1} << 38) || weight_stride > (int64_t{1} << 38))
+    return DLLM_ERR_UNSUPPORTED;
+  return DLLM_OK;
+}
+
+template <int OP>
+dllm_status hd_launch(HeadParams& p, int sms, dllm_stream_t stream) {
+  void* args[] = {&p};
+  return launch_pdl(reinterpret_cast<const void*>(&head_kernel<OP>), dim3(static_cast<unsigned>(sms)), dim3(kHdThreads), kHdSmem,
+                    stream, args);
+}
+
+dllm_status hd_gather(const void* hidden, int64_t stride, int64_t T, int64_t d, const int32_t* n_rows, const int32_t* rows,
+                      uint8_t* packed, int sms, dllm_stream_t stream) {
+  const uint16_t* from = static_cast<const uint16_t*>(hidden);
+  uint16_t* to = reinterpret_cast<uint16_t*>(packed);
+  void* args[] = {&from, &stride, &T, &d, &n_rows, &rows, &to};
+  const int64_t blocks = std::min<int64_t>((T + 7) / 8 + 8, sms * 8);
+  return launch_pdl(reinterpret_cast<const void*>(&head_gather_kernel), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                    args);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dllm_lm_head_logprobs_workspace_size(int64_t T, int64_t V, int64_t d) {
+  if (T <= 0 || V <= 0 || d <= 0 || T > kHdMaxT || V > INT32_MAX || d > kHdMaxD) return 256;
+  return hd_plan(T, V, d, 0, false).bytes;
+}
+
+size_t dllm_lm_head_logprobs_backward_workspace_size(int64_t T, int64_t V, int64_t d) {
+  if (T <= 0 || V <= 0 || d <= 0 || T > kHdMaxT || V > INT32_MAX || d > kHdMaxD) return 256;
+  const HdDevice* dev = hd_device();
+  return hd_plan(T, V, d, dev ? dev->sms : 1024, true).bytes;
+}
+
+dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride, const void* weight,
+                                  int64_t V, int64_t weight_stride, const int32_t* targets, const int32_t* suppress_ids,
+                                  int32_t n_suppress, float* logprob, float* entropy, float* lse, void* workspace,
+                                  size_t workspace_bytes, dllm_stream_t stream) {
+  std::vector<int32_t> sup;
+  dllm_status st = hd_check(hidden, T, d, hidden_stride, weight, V, weight_stride, targets, suppress_ids, n_suppress, sup);
+  if (st != DLLM_OK || T == 0) return st;
+  if (!logprob || !entropy || !lse || !aligned4(logprob) || !aligned4(entropy) || !aligned4(lse)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (!workspace || workspace_bytes < dllm_lm_head_logprobs_workspace_size(T, V, d)) return DLLM_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return DLLM_ERR_INVALID_ARGUMENT;
+  const HdDevice* dev = hd_device();
+  if (!dev) return DLLM_ERR_CUDA;
+  const HdPlan h = hd_plan(T, V, d, dev->sms, false);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* n_rows = reinterpret_cast<int32_t*>(ws + 128);
+
+  HeadListParams l{};
+  l.targets = targets;
+  l.T = T;
+  l.V = V;
+  l.n_rows = n_rows;
+  l.rows = reinterpret_cast<int32_t*>(ws + h.rows);
+  l.target = reinterpret_cast<int32_t*>(ws + h.target);
+  l.o_logprob = logprob;
+  l.o_entropy = entropy;
+  l.o_lse = lse;
+
+  HeadParams p{};
+  const uint32_t a_rows = static_cast<uint32_t>(std::min<int64_t>(kHdBM, round_up(T, 8)));
+  if (!make_map(&p.tm_a, hidden, T, d, hidden_stride, a_rows) ||
+      !make_map(&p.tm_packed, ws + h.hidden, round_up(T, kHdBK), d, d, a_rows) ||
+      !make_map(&p.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v)))
+    return DLLM_ERR_CUDA;
+  p.n_rows = n_rows;
+  p.T = T;
+  p.V = V;
+  p.cols = V;
+  p.d = d;
+  p.bn = h.bn_v;
+  p.n_n = h.n_v;
+  p.idesc = hd_idesc(kHdScore, h.bn_v);
+  p.a_bytes = a_rows * kHdBK * 2;
+  p.target = l.target;
+  p.n_sup = static_cast<int32_t>(sup.size());
+  std::copy(sup.begin(), sup.end(), p.sup);
+  p.part = reinterpret_cast<float4*>(ws + h.part);
+  p.part_rows = h.t_pad;
+  p.z_target = reinterpret_cast<float*>(ws + h.z_target);
+  p.fault = reinterpret_cast<int32_t*>(ws);
+
+  HeadFinishParams f{};
+  f.n_rows = n_rows;
+  f.rows = l.rows;
+  f.target = l.target;
+  f.part = p.part;
+  f.part_rows = h.t_pad;
+  f.parts = 2 * h.n_v;
+  f.z_target = p.z_target;
+  f.n_sup = p.n_sup;
+  std::copy(sup.begin(), sup.end(), f.sup);
+  f.ln_ids = static_cast<float>(std::log(static_cast<double>(V - static_cast<int64_t>(sup.size()))));
+  f.logprob = logprob;
+  f.entropy = entropy;
+  f.lse = lse;
+
+  void* largs[] = {&l};
+  st = launch_pdl(reinterpret_cast<const void*>(&head_list_kernel), dim3(1), dim3(kHdListThreads), 0, stream, largs);
+  if (st != DLLM_OK) return st;
+  st = hd_gather(hidden, hidden_stride, T, d, n_rows, l.rows, ws + h.hidden, dev->sms, stream);
+  if (st != DLLM_OK) return st;
+  st = hd_launch<kHdScore>(p, dev->sms, stream);
+  if (st != DLLM_OK) return st;
+  void* fargs[] = {&f};
+  return launch_pdl(reinterpret_cast<const void*>(&head_finish_kernel),
+                    dim3(static_cast<unsigned>(std::min<int64_t>((T + 31) / 32, dev->sms * 2))), dim3(1024), 0, stream, fargs);
+}
+
+dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride,
+                                           const void* weight, int64_t V, int64_t weight_stride, const int32_t* targets,
+                                           const int32_t* suppress_ids, int32_t n_suppress, const float* lse,
+                                           const float* entropy, const float* grad_logprob, const float* grad_entropy,
+                                           void* grad_hidden, int64_t grad_hidden_stride, void* grad_weight,
+                                           dllm_dtype grad_weight_dt, int64_t grad_weight_stride, int32_t accumulate,
+                                           void* workspace, size_t workspace_bytes, dllm_stream_t stream) {
+  std::vector<int32_t> sup;
+  dllm_status st = hd_check(hidden, T, d, hidden_stride, weight, V, weight_stride, targets, suppress_ids, n_suppress, sup);
+  if (st != DLLM_OK) return st;
+  if (grad_weight_dt != DLLM_F32 && grad_weight_dt != DLLM_BF16) return DLLM_ERR_INVALID_ARGUMENT;
+  if (grad_hidden && (grad_hidden_stride < d || mul_or_neg(mul_or_neg(T, grad_hidden_stride), 2) < 0)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (grad_weight && (grad_weight_stride < d || mul_or_neg(mul_or_neg(V, grad_weight_stride), 4) < 0)) return DLLM_ERR_INVALID_ARGUMENT;
+  if ((grad_hidden && (!aligned16(grad_hidden) || grad_hidden_stride % 8 != 0)) ||
+      (grad_weight && (!aligned16(grad_weight) || grad_weight_stride % 8 != 0)))
+    return DLLM_ERR_UNSUPPORTED;
+  if (!grad_hidden && !grad_weight) return DLLM_OK;
+  if (T == 0) {  // no row: the weight's gradient is zero
+    const size_t size = grad_weight_dt == DLLM_F32 ? 4 : 2;
+    if (!grad_weight || accumulate) return DLLM_OK;
+    return cudaMemset2DAsync(grad_weight, static_cast<size_t>(grad_weight_stride) * size, 0, static_cast<size_t>(d) * size,
+                             static_cast<size_t>(V), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? DLLM_OK
+               : DLLM_ERR_CUDA;
+  }
+  if (!lse || !entropy || !aligned4(lse) || !aligned4(entropy) || !aligned4(grad_logprob) || !aligned4(grad_entropy))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (!workspace || workspace_bytes < dllm_lm_head_logprobs_backward_workspace_size(T, V, d)) return DLLM_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return DLLM_ERR_INVALID_ARGUMENT;
+  const HdDevice* dev = hd_device();
+  if (!dev) return DLLM_ERR_CUDA;
+  const HdPlan h = hd_plan(T, V, d, dev->sms, true);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* n_rows = reinterpret_cast<int32_t*>(ws + 128);
+
+  HeadListParams l{};
+  l.targets = targets;
+  l.T = T;
+  l.V = V;
+  l.backward = 1;
+  l.lse = lse;
+  l.entropy = entropy;
+  l.g = grad_logprob;
+  l.gh = grad_entropy;
+  l.n_sup = static_cast<int32_t>(sup.size());
+  std::copy(sup.begin(), sup.end(), l.sup);
+  l.n_rows = n_rows;
+  l.rows = reinterpret_cast<int32_t*>(ws + h.rows);
+  l.place = reinterpret_cast<int32_t*>(ws + h.place);
+  l.target = reinterpret_cast<int32_t*>(ws + h.target);
+  l.row = reinterpret_cast<HeadRow*>(ws + h.row);
+
+  HeadParams p{};
+  const uint32_t a_rows = static_cast<uint32_t>(std::min<int64_t>(kHdBM, round_up(T, 8)));
+  p.n_rows = n_rows;
+  p.T = T;
+  p.V = V;
+  p.d = d;
+  p.target = l.target;
+  p.n_sup = l.n_sup;
+  std::copy(sup.begin(), sup.end(), p.sup);
+  p.row = l.row;
+  p.dz = reinterpret_cast<uint16_t*>(ws + h.dz);
+  p.dz_stride = h.piece;
+  p.acc = reinterpret_cast<float*>(ws + h.accs);
+  p.acc_stride = static_cast<int64_t>(h.n_d) * h.bn_d;
+  p.grad_w = grad_weight;
+  p.grad_w_stride = grad_weight_stride;
+  p.grad_w_f32 = grad_weight_dt == DLLM_F32 ? 1 : 0;
+  p.accumulate = accumulate != 0 ? 1 : 0;
+  p.fault = reinterpret_cast<int32_t*>(ws);
+  HeadParams pz = p, ph = p, pw = p;
+  const int64_t packed_rows = round_up(T, kHdBK);
+  if (!make_map(&pz.tm_a, hidden, T, d, hidden_stride, a_rows) ||
+      !make_map(&pz.tm_packed, ws + h.hidden, packed_rows, d, d, a_rows) ||
+      !make_map(&pz.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v)) ||
+      !make_map(&ph.tm_a, p.dz, h.t_pad, h.piece, h.piece, kHdBM) || !make_map(&ph.tm_b, weight, V, d, weight_stride, 64) ||
+      !make_map(&pw.tm_a, p.dz, h.t_pad, h.piece, h.piece, 64) || !make_map(&pw.tm_b, hidden, T, d, hidden_stride, 64) ||
+      !make_map(&pw.tm_packed, ws + h.hidden, packed_rows, d, d, 64))
+    return DLLM_ERR_CUDA;
+  pz.bn = h.bn_v;
+  pz.n_n = h.n_v;
+  pz.idesc = hd_idesc(kHdDz, h.bn_v);
+  pz.a_bytes = a_rows * kHdBK * 2;
+  ph.bn = pw.bn = h.bn_d;
+  ph.n_n = pw.n_n = h.n_d;
+  ph.idesc = hd_idesc(kHdDh, h.bn_d);
+  pw.idesc = hd_idesc(kHdDw, h.bn_d);
+  ph.a_bytes = pw.a_bytes = kHdABytes;
+  ph.split_slabs = static_cast<int32_t>((std::min(h.piece, V) + kHdBK - 1) / kHdBK);
+
+  void* largs[] = {&l};
+  st = launch_pdl(reinterpret_cast<const void*>(&head_list_kernel), dim3(1), dim3(kHdListThreads), 0, stream, largs);
+  if (st != DLLM_OK) return st;
+  st = hd_gather(hidden, hidden_stride, T, d, n_rows, l.rows, ws + h.hidden, dev->sms, stream);
+  if (st != DLLM_OK) return st;
+  for (int64_t v0 = 0; v0 < V; v0 += h.piece) {
+    const int64_t cols = std::min(h.piece, V - v0);
+    for (HeadParams* q : {&pz, &ph, &pw}) {
+      q->v0 = v0;
+      q->cols = cols;
+      q->add = v0 > 0 ? 1 : 0;
+    }
+    pz.n_n = static_cast<int32_t>((cols + kHdBN - 1) / kHdBN);
+    st = hd_launch<kHdDz>(pz, dev->sms, stream);
+    if (st == DLLM_OK && grad_hidden) st = hd_launch<kHdDh>(ph, dev->sms, stream);
+    if (st == DLLM_OK && grad_weight) st = hd_launch<kHdDw>(pw, dev->sms, stream);
+    if (st != DLLM_OK) return st;
+  }
+  if (!grad_hidden) return DLLM_OK;
+  const float* acc = p.acc;
+  uint16_t* out = static_cast<uint16_t*>(grad_hidden);
+  const int32_t* place = l.place;
+  int32_t n_n = h.n_d, ctas = dev->sms, slabs = ph.split_slabs;
+  int64_t stride = p.acc_stride;
+  void* args[] = {&n_rows, &place, &acc, &stride, &n_n, &ctas, &slabs, &T, &d, &out, &grad_hidden_stride};
+  return launch_pdl(reinterpret_cast<const void*>(&head_dh_kernel), dim3(static_cast<unsigned>(std::min<int64_t>(T, dev->sms * 8))),
+                    dim3(256), 0, stream, args);
+}
+
+}  // extern "C"

@@ -1,0 +1,130 @@
+"""The embedding of a canvas and its gradient (``dllm_embed_tokens``,
+``dllm_embed_tokens_backward``)."""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import DLLM_BF16, DLLM_F32, _check, _lib, _need_cuda
+from .cache import _empty, _raw_stream
+from .head import _workspace
+
+
+def _dtype(t, name: str) -> int:
+    if not torch.is_tensor(t) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+    return DLLM_BF16 if t.dtype == torch.bfloat16 else DLLM_F32
+
+
+def _canvas(tokens, device):
+    """(B, L, row stride) of (T,) or (B, L) int32 tokens, unit stride over the last dimension."""
+    if not torch.is_tensor(tokens) or tokens.dtype != torch.int32 or tokens.dim() not in (1, 2):
+        raise TypeError("tokens must be a (T,) or (B, L) int32 tensor")
+    if tokens.device != device:
+        raise ValueError(f"tokens are on {tokens.device}; the call runs on {device}")
+    if tokens.shape[-1] > 1 and tokens.stride(-1) != 1:
+        raise ValueError("tokens need unit stride over their last dimension")
+    if tokens.dim() == 1:
+        return 1, tokens.shape[0], tokens.shape[0]
+    B, L = tokens.shape
+    return B, L, (tokens.stride(0) if B > 1 else L)
+
+
+def _weight(t, name: str, V: int, d: int) -> int:
+    """The row stride of a (V, d) tensor with unit column stride."""
+    if t.dim() != 2 or t.shape != (V, d) or (d > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be (V, d) = ({V}, {d}) with unit column stride")
+    return t.stride(0) if V > 1 else d
+
+
+def embed_tokens(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                 stream=None):
+    """scale * weight[tokens]: (..., d) in weight's dtype, contiguous.
+
+    ``tokens``: (T,) or (B, L) int32, rows at any stride (a window of a longer
+    canvas); an id outside [0, V) gives zeros.  ``weight``: (V, d) bf16 or fp32.
+    ``out``: preallocated."""
+    _need_cuda(tokens, weight)
+    dt = _dtype(weight, "weight")
+    if weight.dim() != 2:
+        raise ValueError("weight must be (V, d)")
+    V, d = weight.shape
+    stride = _weight(weight, "weight", V, d)
+    dev, idx = weight.device, weight.get_device()
+    B, L, t_stride = _canvas(tokens, dev)
+    if out is None:
+        out = _empty((*tokens.shape, d), weight.dtype, dev, stream)
+    elif (not torch.is_tensor(out) or out.dtype != weight.dtype or out.device != dev or out.shape != (*tokens.shape, d)
+          or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous (..., d) tensor of weight's dtype, on the same device")
+    _check(_lib.dllm_embed_tokens(tokens.data_ptr(), B, L, t_stride, weight.data_ptr(), dt, V, d, stride, scale,
+                                  out.data_ptr(), _raw_stream(stream, idx)), "dllm_embed_tokens")
+    return out
+
+
+def embed_tokens_backward(tokens: torch.Tensor, grad: torch.Tensor, V: int, scale: float = 1.0,
+                          out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                          ws: Optional[torch.Tensor] = None, stream=None):
+    """The gradient of embed_tokens with respect to its weight, (V, d): scale
+    times the sum of ``grad`` (..., d), bf16 or fp32, over each id's positions.
+    ``out``: preallocated, bf16 or fp32 (by default of grad's dtype);
+    ``accumulate`` adds to it, e.g. to the gradient of a head that shares the
+    weight.  ``ws``: a workspace of the caller's, not in use by another call."""
+    _need_cuda(tokens, grad)
+    dt = _dtype(grad, "grad")
+    dev, idx, V = grad.device, grad.get_device(), int(V)
+    B, L, t_stride = _canvas(tokens, dev)
+    if grad.shape[:-1] != tokens.shape or not grad.is_contiguous():
+        raise ValueError("grad must be a contiguous tensor of the tokens' shape and d")
+    if not 0 < V < 1 << 31:
+        raise ValueError(f"V: {V} is out of range")
+    d = grad.shape[-1]
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to the gradient given as out")
+        out = _empty((V, d), grad.dtype, dev, stream)
+    out_dt = _dtype(out, "out")
+    if out.device != dev:
+        raise ValueError(f"out is on {out.device}; grad is on {dev}")
+    out_stride = _weight(out, "out", V, d)
+    raw = _raw_stream(stream, idx)
+    ws = _workspace(ws, int(_lib.dllm_embed_tokens_backward_workspace_size(B * L, V, d)), dev, stream)
+    _check(_lib.dllm_embed_tokens_backward(tokens.data_ptr(), B, L, t_stride, grad.data_ptr(), dt, V, d, scale,
+                                           out.data_ptr(), out_dt, out_stride, 1 if accumulate else 0, ws.data_ptr(),
+                                           ws.numel() * ws.element_size(), raw), "dllm_embed_tokens_backward")
+    return out
+
+
+class _EmbedGrad(torch.autograd.Function):
+    """The gradient is linear in its input, but its derivative is not built."""
+
+    @staticmethod
+    def forward(ctx, tokens, grad, V, scale):
+        return embed_tokens_backward(tokens, grad, V, scale)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the gradient of embed_canvas cannot be differentiated again")
+
+
+class _EmbedCanvas(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, weight, scale):
+        ctx.V, ctx.scale = weight.shape[0], scale
+        ctx.save_for_backward(tokens)
+        return embed_tokens(tokens, weight, scale)
+
+    @staticmethod
+    def backward(ctx, g):
+        tokens, = ctx.saved_tensors
+        g = g.contiguous()
+        if torch.is_grad_enabled():                                              # (under create_graph)
+            return None, _EmbedGrad.apply(tokens, g, ctx.V, ctx.scale), None
+        return None, embed_tokens_backward(tokens, g, ctx.V, ctx.scale), None
+
+
+def embed_canvas(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0):
+    """embed_tokens for training: differentiable once with respect to ``weight``
+    through autograd."""
+    return _EmbedCanvas.apply(tokens, weight, float(scale))

@@ -1,0 +1,161 @@
+"""Log probabilities of given tokens straight from the hidden states, and their
+gradient with respect to hidden states and weight, without the logits in memory
+(``dllm_lm_head_logprobs``, ``dllm_lm_head_logprobs_backward``)."""
+from __future__ import annotations
+
+from typing import Optional, Sequence
+
+import torch
+
+from . import DLLM_BF16, DLLM_F32, _F32, _I32, _check, _lib, _need_cuda
+from .cache import _at, _at_or_none, _empty, _raw_stream
+from .score import _rows, _sup
+
+
+def _matrix(t, name: str, cols: int, device):
+    """(rows, row stride) of a 2-D bf16 tensor of `cols` columns."""
+    if not torch.is_tensor(t) or t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D bfloat16 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}; hidden is on {device}")
+    if t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must have {cols} columns at unit stride")
+    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else cols)
+
+
+def _ends(hidden, weight, targets):
+    """Shape and stride of hidden (T, d) or (B, L, d) and weight (V, d)."""
+    _need_cuda(hidden, weight, targets)
+    T, d, stride = _rows(hidden, "hidden")
+    if hidden.dtype != torch.bfloat16:
+        raise TypeError("hidden must be bfloat16")
+    V, w_stride = _matrix(weight, "weight", d, hidden.device)
+    return T, d, stride, V, w_stride
+
+
+def _workspace(ws, need: int, device, stream):
+    """The caller's workspace, or a new one that belongs to the call's stream."""
+    if ws is None:
+        return _empty((need,), torch.uint8, device, stream)
+    if not torch.is_tensor(ws):
+        raise TypeError("ws must be a tensor")
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws
+
+
+def lm_head_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, suppress_ids: Sequence[int] = (),
+                     out=None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Scores given tokens under the logits hidden @ weight^T, which are never
+    stored: (logprob, entropy, lse), float32 shaped like ``targets``.
+
+    hidden (T, d) or (B, L, d) and weight (V, d) bf16; ``targets`` int32, hidden's
+    shape without d.  A row whose target lies outside [0, V) is not scored: it
+    gets 0 for all three, costs nothing, and its hidden state may hold anything.
+    ``out``: the same three, preallocated.  ``ws``: a workspace of the caller's,
+    not in use by another call; zeroed, it tells ``workspace_fault`` afterwards
+    whether a wait ran out."""
+    T, d, stride, V, w_stride = _ends(hidden, weight, targets)
+    dev, idx, shape = hidden.device, hidden.get_device(), hidden.shape[:-1]
+    if out is None:
+        out = [_empty(shape, torch.float32, dev, stream) for _ in range(3)]
+    lp, ent, lse = out
+    at = [_at(t, name, T, _F32, idx, dev) for t, name in ((lp, "logprob"), (ent, "entropy"), (lse, "lse"))]
+    raw = _raw_stream(stream, idx)
+    ws = _workspace(ws, int(_lib.dllm_lm_head_logprobs_workspace_size(T, V, d)), dev, stream)
+    sup, n_sup = _sup(suppress_ids)
+    _check(_lib.dllm_lm_head_logprobs(hidden.data_ptr(), T, d, stride, weight.data_ptr(), V, w_stride,
+                                      _at(targets, "targets", T, _I32, idx, dev), sup, n_sup, *at, ws.data_ptr(),
+                                      ws.numel() * ws.element_size(), raw), "dllm_lm_head_logprobs")
+    return lp, ent, lse
+
+
+def lm_head_logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                              entropy: torch.Tensor, grad_logprob: Optional[torch.Tensor],
+                              grad_entropy: Optional[torch.Tensor] = None, suppress_ids: Sequence[int] = (), out=None,
+                              accumulate: bool = False, hidden_grad: bool = True, weight_grad: bool = True,
+                              ws: Optional[torch.Tensor] = None, stream=None):
+    """The gradient of lm_head_logprobs: (grad_hidden bf16 like hidden,
+    grad_weight bf16 like weight), from the saved ``lse`` and ``entropy`` and the
+    gradients of logprob and entropy (None: zero).  One that is not wanted
+    (``hidden_grad``, ``weight_grad`` false) is None.  ``out``: the two,
+    preallocated (grad_weight bf16 or float32, either None to be made here);
+    ``accumulate`` adds to out's grad_weight.  ``ws`` as in lm_head_logprobs."""
+    T, d, stride, V, w_stride = _ends(hidden, weight, targets)
+    dev, idx = hidden.device, hidden.get_device()
+    gh, gw = (None, None) if out is None else out
+    if (gh is not None and not hidden_grad) or (gw is not None and not weight_grad):
+        raise ValueError("out holds a gradient that is not wanted")
+    if accumulate and gw is None:
+        raise ValueError("accumulate adds to the grad_weight given in out")
+    if hidden_grad and gh is None:
+        gh = _empty(hidden.shape, torch.bfloat16, dev, stream)
+    if weight_grad and gw is None:
+        gw = _empty((V, d), torch.bfloat16, dev, stream)
+    gh_stride, gw_stride, gw_dt = d, d, DLLM_BF16
+    if gh is not None:
+        if not torch.is_tensor(gh) or gh.dtype != torch.bfloat16 or gh.device != dev or gh.shape != hidden.shape:
+            raise ValueError("grad_hidden must be shaped and typed like hidden, on the same device")
+        _, _, gh_stride = _rows(gh, "grad_hidden")
+    if gw is not None:
+        if not torch.is_tensor(gw) or gw.dtype not in (torch.bfloat16, torch.float32) or gw.device != dev:
+            raise ValueError("grad_weight must be a bfloat16 or float32 tensor on hidden's device")
+        if gw.shape != (V, d) or (d > 1 and gw.stride(1) != 1):
+            raise ValueError("grad_weight must be shaped like weight, with unit column stride")
+        gw_stride = gw.stride(0) if V > 1 else d
+        gw_dt = DLLM_F32 if gw.dtype == torch.float32 else DLLM_BF16
+    raw = _raw_stream(stream, idx)
+    ws = _workspace(ws, int(_lib.dllm_lm_head_logprobs_backward_workspace_size(T, V, d)), dev, stream)
+    sup, n_sup = _sup(suppress_ids)
+    _check(_lib.dllm_lm_head_logprobs_backward(
+        hidden.data_ptr(), T, d, stride, weight.data_ptr(), V, w_stride, _at(targets, "targets", T, _I32, idx, dev), sup,
+        n_sup, _at(lse, "lse", T, _F32, idx, dev), _at(entropy, "entropy", T, _F32, idx, dev),
+        _at_or_none(grad_logprob, "grad_logprob", T, _F32, idx, dev),
+        _at_or_none(grad_entropy, "grad_entropy", T, _F32, idx, dev), None if gh is None else gh.data_ptr(), gh_stride,
+        None if gw is None else gw.data_ptr(), gw_dt, gw_stride, 1 if accumulate else 0, ws.data_ptr(),
+        ws.numel() * ws.element_size(), raw), "dllm_lm_head_logprobs_backward")
+    return gh, gw
+
+
+def _head_grad(hidden, weight, targets, lse, ent, suppress_ids, g_lp, g_ent, want):
+    # (gradients that reach here expanded from a scalar are not contiguous)
+    g_lp, g_ent = [None if g is None else g.float().contiguous() for g in (g_lp, g_ent)]
+    return lm_head_logprobs_backward(hidden, weight, targets, lse, ent, g_lp, g_ent, suppress_ids=suppress_ids,
+                                     hidden_grad=want[0], weight_grad=want[1])
+
+
+class _HeadGrad(torch.autograd.Function):
+    """The gradient as a step of a graph that is to be differentiated again: there
+    is no second derivative, and leaving it out of a sum of losses would go unseen."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, lse, ent, suppress_ids, g_lp, g_ent, want):
+        return _head_grad(hidden, weight, targets, lse, ent, suppress_ids, g_lp, g_ent, want)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the gradient of score_hidden cannot be differentiated again")
+
+
+class _ScoreHidden(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, suppress_ids):
+        ctx.set_materialize_grads(False)
+        lp, ent, lse = lm_head_logprobs(hidden, weight, targets, suppress_ids=suppress_ids)
+        ctx.suppress_ids = suppress_ids
+        ctx.save_for_backward(hidden, weight, targets, lse, ent)
+        return lp, ent
+
+    @staticmethod
+    def backward(ctx, g_lp, g_ent):
+        hidden, weight, targets, lse, ent = ctx.saved_tensors
+        want = ctx.needs_input_grad[:2]
+        grad = _HeadGrad.apply if torch.is_grad_enabled() else _head_grad        # (enabled under create_graph)
+        gh, gw = grad(hidden, weight, targets, lse, ent, ctx.suppress_ids, g_lp, g_ent, want)
+        return gh, gw, None, None
+
+
+def score_hidden(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, suppress_ids: Sequence[int] = ()):
+    """lm_head_logprobs for training: (logprob, entropy), differentiable once with
+    respect to ``hidden`` and ``weight`` through autograd."""
+    return _ScoreHidden.apply(hidden, weight, targets, tuple(suppress_ids))

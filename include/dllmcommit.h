@@ -634,6 +634,107 @@ dllm_status dllm_token_logprobs_backward(const void* logits, dllm_dtype dt, int6
                                          const float* grad_top, void* grad, int64_t grad_row_stride,
                                          dllm_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Scores of given tokens straight from the hidden states.
+ *
+ * dllm_token_logprobs reads logits from memory; a trainer that only wants the
+ * scores of the masked positions' tokens need not hold them.  logits z = hidden
+ * weight^T (bf16 in, fp32 tensor-core accumulation) are formed tile by tile and
+ * never stored.  A row is scored when its target lies in [0, V); for each scored
+ * row over the ids A = {0..V-1} minus suppress_ids (NaN products as -inf):
+ *   lse          ln sum_A exp(z)
+ *   logprob      z[target] - lse; -inf for a suppressed target
+ *   entropy      of softmax_A(z), clamped to [0, ln |A|]
+ * Rows that are not scored get 0 for all three; their hidden states are not
+ * read into any result, whatever they hold.  Products are read within +-2^125;
+ * such maxima give lse = +-inf as in dllm_token_logprobs.
+ *   hidden   device bf16 (T, d), rows hidden_stride elements apart
+ *   weight   device bf16 (V, d), rows weight_stride elements apart
+ *   targets  device int32 (T); suppress_ids HOST as in dllm_token_stats
+ *   logprob, entropy, lse   device fp32 (T)
+ *   workspace  device, 16-byte aligned, >= the size that
+ *            dllm_lm_head_logprobs_workspace_size gives, any contents.  Its first
+ *            word takes a fault code when a bounded wait runs out (outputs are
+ *            then undefined): zero it to read it later with dllm_workspace_fault.
+ * d a multiple of 8, bases 16-byte aligned and row strides multiples of 8, T up
+ * to 2^24, d up to 2^20 (else DLLM_ERR_UNSUPPORTED).  The work is that of the
+ * scored rows.  Results repeat bit for bit.
+ * ------------------------------------------------------------------------ */
+size_t dllm_lm_head_logprobs_workspace_size(int64_t T, int64_t V, int64_t d);
+
+dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride, const void* weight,
+                                  int64_t V, int64_t weight_stride, const int32_t* targets, const int32_t* suppress_ids,
+                                  int32_t n_suppress, float* logprob, float* entropy, float* lse, void* workspace,
+                                  size_t workspace_bytes, dllm_stream_t stream);
+
+/* The gradient with respect to hidden and weight, given lse and entropy as
+ * dllm_lm_head_logprobs returned them and the gradients of logprob (T) and
+ * entropy (T), each of which may be NULL (zero).  With p = exp(z - lse):
+ *   dz = -p (grad_logprob + grad_entropy (z - lse + entropy)) + grad_logprob at
+ *        the target (grad_logprob counts as 0 where the target is suppressed)
+ *   grad_hidden = dz weight,  grad_weight = dz^T hidden.
+ * Rows that are not scored, whose lse is not finite or whose gradients are both
+ * zero take no part: their grad_hidden is 0 and their hidden states are not
+ * read into any result.  Suppressed ids get 0.
+ * dz is formed piece by piece of the vocabulary (at most 2^28 elements, or 4096
+ * ids, at a time) and held in bf16, as the products' operands have to be: each
+ * element is rounded by at most 2^-8 of itself; sums are fp32.
+ *   grad_hidden  device bf16 (T, d), rows grad_hidden_stride elements apart, or
+ *                NULL (not wanted)
+ *   grad_weight  device (V, d) fp32 or bf16 (grad_weight_dt), rows
+ *                grad_weight_stride elements apart, or NULL; with accumulate it
+ *                is added to (in fp32, rounded once), else it is replaced
+ *   workspace    as above, of dllm_lm_head_logprobs_backward_workspace_size
+ * Outputs 16-byte aligned, their strides multiples of 8 (else
+ * DLLM_ERR_UNSUPPORTED); they must not overlap an input or each other.  The
+ * weight of every id must be finite where grad_hidden is wanted (a suppressed
+ * id's too: it is multiplied by 0).  Results repeat bit for bit. */
+size_t dllm_lm_head_logprobs_backward_workspace_size(int64_t T, int64_t V, int64_t d);
+
+dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride,
+                                           const void* weight, int64_t V, int64_t weight_stride, const int32_t* targets,
+                                           const int32_t* suppress_ids, int32_t n_suppress, const float* lse,
+                                           const float* entropy, const float* grad_logprob, const float* grad_entropy,
+                                           void* grad_hidden, int64_t grad_hidden_stride, void* grad_weight,
+                                           dllm_dtype grad_weight_dt, int64_t grad_weight_stride, int32_t accumulate,
+                                           void* workspace, size_t workspace_bytes, dllm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The embedding of a canvas: out[b, l] = scale weight[tokens[b, l]], what a model
+ * reads of the canvas that the commit step updates (a head often shares the
+ * weight).  An id outside [0, V) gives zeros.
+ *   tokens  device int32, row b token_stride elements apart (a window of a
+ *           longer canvas)
+ *   weight  device fp32 or bf16 (V, d), rows weight_stride elements apart
+ *   out     device (B, L, d) contiguous, weight's dtype; the product with scale
+ *           (finite) is fp32, rounded once
+ * Rows in whole 16-byte vectors: d and strides multiples of 8 (bf16) or 4 (fp32),
+ * bases 16-byte aligned; at most 2^30 tokens (else DLLM_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+dllm_status dllm_embed_tokens(const int32_t* tokens, int64_t B, int64_t L, int64_t token_stride, const void* weight,
+                              dllm_dtype dt, int64_t V, int64_t d, int64_t weight_stride, float scale, void* out,
+                              dllm_stream_t stream);
+
+/* Its gradient: grad_weight[v] = scale times the sum of grad over the positions
+ * whose token is v (ids outside [0, V) take no part); 0 for ids that no position
+ * names.
+ *   grad         device fp32 or bf16 (B, L, d) contiguous
+ *   grad_weight  device fp32 or bf16 (V, d), rows grad_weight_stride elements
+ *                apart; with accumulate it is added to (in fp32, rounded once;
+ *                rows that no position names are not touched), else it is
+ *                replaced.  Not overlapping grad or tokens.
+ *   workspace    device, 16-byte aligned, of
+ *                dllm_embed_tokens_backward_workspace_size(B L, V, d) bytes
+ * Sums are fp32 in an order that depends on the tokens alone: results repeat bit
+ * for bit.  B L == 0 without accumulate sets grad_weight to zero.  Alignment as
+ * above. */
+size_t dllm_embed_tokens_backward_workspace_size(int64_t T, int64_t V, int64_t d);
+
+dllm_status dllm_embed_tokens_backward(const int32_t* tokens, int64_t B, int64_t L, int64_t token_stride, const void* grad,
+                                       dllm_dtype grad_dt, int64_t V, int64_t d, float scale, void* grad_weight,
+                                       dllm_dtype grad_weight_dt, int64_t grad_weight_stride, int32_t accumulate,
+                                       void* workspace, size_t workspace_bytes, dllm_stream_t stream);
+
 /* Reads and clears the device fault word of a workspace (synchronises the
  * stream).  *fault = 0 when no kernel reported a fault; otherwise a code
  * naming the wait that gave up (the kernel stopped early; outputs of that

@@ -1,0 +1,327 @@
+"""Scores of given tokens from hidden states, and their gradients, on the GPU
+against 64-bit formulas.
+
+Tolerances (derived).  A logit is a sum of d products; added one by one in 32
+bits, truncated, it is off by at most d 2^-23 sum |h w|, called e below (its
+largest over the ids).  lse and log probabilities move by at most 2 e, the
+entropy by at most e sum p |log p + H| <= 2 e (H + 1) <= 2 e (ln V + 1), beside
+2^-15 + 2^-21 |value| (2^-12 for the entropy) of the sums of exponentials.
+
+The gradient's dz is rounded to bf16 (2^-8 of itself at most) after an error of
+2^-12 (exponent and logit); sums of n terms in 32 bits are off by n 2^-23 of the
+sum of magnitudes at most; the result is rounded to its type.  So an element is
+within (2^-8 + 2^-12 + e + n 2^-23) sum |dz| |w| + half a step.  That bound is
+wide for sums whose terms cancel, so the 2-norm of the whole error is held too:
+two roundings of at most 2^-8, spread evenly, have a root mean square of
+2^-8 / sqrt 3 each, sqrt(2 / 3) 2^-8 together (fp32 results: one), and 2^-8 is
+asked for.
+"""
+import math
+
+import pytest
+import torch
+
+from head_reference import grads, scores
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def inputs(T, V, d, seed, scored=1.0, n_sup=0, spread=2.5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = (torch.randn((V, d), device="cuda", generator=g) * spread / math.sqrt(d)).to(BF16)
+    t = torch.randint(0, V, (T,), device="cuda", generator=g)
+    h = torch.randn((T, d), device="cuda", generator=g) + torch.rand((T, 1), device="cuda", generator=g) * w[t].float()
+    drop = torch.rand((T,), device="cuda", generator=g) >= scored
+    t = torch.where(drop, torch.where(torch.rand((T,), device="cuda", generator=g) < 0.5, -1, V + 3), t).to(torch.int32)
+    sup = torch.randperm(V, device="cuda", generator=g)[:n_sup].tolist()
+    return h.to(BF16), w, t, sup
+
+
+def logit_error(h, w, scored):
+    """e, per row."""
+    live = torch.where(scored[:, None], h.double(), torch.zeros((), dtype=torch.float64, device=h.device))
+    return h.shape[1] * 2.0 ** -23 * (live.abs() @ w.double().abs().T).amax(1)
+
+
+def near(got, want, tol):
+    got, want = got.double().reshape(want.shape), want.double()
+    odd = ~torch.isfinite(want)
+    assert torch.equal(got[odd], want[odd])
+    err = (got[~odd] - want[~odd]).abs()
+    lim = (tol + 2.0 ** -21 * want.abs())[~odd]
+    assert bool((err <= lim).all()), (float(err.max()), float(lim.min()))
+
+
+def check_scores(cs, h, w, t, sup, **kw):
+    lp, ent, lse = cs.lm_head_logprobs(h, w, t, suppress_ids=sup, **kw)
+    flat, tt, V = h.reshape(-1, h.shape[-1]), t.reshape(-1), w.shape[0]
+    scored = (tt >= 0) & (tt < V)
+    e = logit_error(flat, w, scored)
+    clean = torch.where(scored[:, None], flat, torch.zeros((), dtype=flat.dtype, device=flat.device))
+    want = scores(clean, w, tt, sup)
+    near(lp, want[0], 2 * e + 2.0 ** -15)
+    near(ent, want[1], 2 * e * (math.log(V) + 1) + 2.0 ** -12)
+    near(lse, want[2], 2 * e + 2.0 ** -15)
+    for x in (lp, ent, lse):
+        assert x.shape == t.shape and not bool(x.reshape(-1)[~scored].any())
+    return lp, ent, lse
+
+
+def check_grad(got, exact, size, e, n, old=None):
+    """got against exact, sums of n terms whose magnitudes add up to size."""
+    half = torch.finfo(got.dtype).eps / 2
+    want = exact if old is None else exact + old.double()
+    lim = (2.0 ** -8 + 2.0 ** -12 + e + n * 2.0 ** -23) * size + half * want.abs() + 1e-30
+    err = (got.double() - want).abs()
+    assert bool((err <= lim * (1 + half)).all()), float((err - lim).max())
+    if exact.numel() >= 4096 and old is None and float(exact.norm()) > 0:
+        assert float((got.double() - want).norm()) <= 2.0 ** -8 * float(want.norm())
+
+
+def check_backward(cs, h, w, t, sup, with_entropy=True, with_logprob=True, seed=0, **kw):
+    flat, tt = h.reshape(-1, h.shape[-1]), t.reshape(-1)
+    T, V = flat.shape[0], w.shape[0]
+    _, ent, lse = cs.lm_head_logprobs(h, w, t, suppress_ids=sup)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    gl = torch.randn(t.shape, device="cuda", generator=g) if with_logprob else None
+    ge = torch.randn(t.shape, device="cuda", generator=g) * 0.2 if with_entropy else None
+    gh, gw = cs.lm_head_logprobs_backward(h, w, t, lse, ent, gl, ge, suppress_ids=sup, **kw)
+    dz, clean = grads(flat, w, tt, lse.reshape(-1), ent.reshape(-1), None if gl is None else gl.reshape(-1),
+                      None if ge is None else ge.reshape(-1), sup)
+    scored = (tt >= 0) & (tt < V)
+    e = float(logit_error(flat, w, scored).max()) * 8 if T else 0.0     # of p, and of z - lse beside the entropy
+    # a term p (g + gH (...)) has no part smaller than p |gH| for the error to hide in
+    size = dz.abs()
+    if gh is not None:
+        check_grad(gh.reshape(-1, h.shape[-1]), dz @ w.double(), size @ w.double().abs() + 1e-6, e, V)
+        assert not bool(gh.reshape(-1, h.shape[-1])[~scored].any())
+    if gw is not None and kw.get("accumulate") is None:
+        check_grad(gw, dz.T @ clean, size.T @ clean.abs() + 1e-6, e, T)
+    return gh, gw, dz, clean, (gl, ge, lse, ent)
+
+
+SIZES = [(1, 1, 8, 1.0, 0), (1, 2, 8, 1.0, 1), (3, 7, 16, 1.0, 2), (33, 300, 64, 0.5, 1), (61, 1000, 72, 1.0, 0),
+         (128, 257, 200, 0.9, 5), (129, 513, 320, 1.0, 64), (65, 255, 1288, 1.0, 1), (300, 2049, 768, 0.3, 1),
+         (64, 50257, 768, 1.0, 0), (700, 20001, 136, 0.6, 3), (1025, 1024, 512, 1.0, 0), (40, 126464, 256, 0.02, 1)]
+
+
+@pytest.mark.parametrize("T,V,d,scored,n_sup", SIZES)
+def test_scores(cs, T, V, d, scored, n_sup):
+    check_scores(cs, *inputs(T, V, d, T + V, scored, n_sup))
+
+
+@pytest.mark.parametrize("T,V,d,scored,n_sup", SIZES)
+def test_gradients(cs, T, V, d, scored, n_sup):
+    h, w, t, sup = inputs(T, V, d, T + V + 1, scored, n_sup)
+    check_backward(cs, h, w, t, sup)
+    check_backward(cs, h, w, t, sup, with_entropy=False)
+
+
+def test_several_bands_and_pieces(cs):
+    """More rows than one pass over the vocabulary takes, and a dz of several pieces, the last a short one."""
+    h, w, t, sup = inputs(9000, 33000, 64, 5, 0.9, 1)
+    check_scores(cs, h, w, t, sup)
+    check_backward(cs, h, w, t, sup)
+
+
+def test_few_scored_rows_of_many(cs):
+    """Splits of the second product follow the scored rows, pieces all rows."""
+    h, w, t, sup = inputs(70000, 9000, 64, 6, 0.004, 1)
+    check_scores(cs, h, w, t, sup)
+    check_backward(cs, h, w, t, sup)
+
+
+def test_no_row_is_scored(cs):
+    h, w, t, _ = inputs(70, 500, 64, 7, 0.0)
+    h.fill_(math.nan)
+    lp, ent, lse = cs.lm_head_logprobs(h, w, t)
+    assert not bool(lp.any() or ent.any() or lse.any())
+    one = torch.ones(70, device="cuda")
+    gh, gw = cs.lm_head_logprobs_backward(h, w, t, lse, ent, one, one)
+    assert not bool(gh.any() or gw.any())
+    old = torch.randn_like(w)
+    kept = old.clone()
+    _, same = cs.lm_head_logprobs_backward(h, w, t, lse, ent, one, one, out=(None, old), accumulate=True)
+    assert same is old and torch.equal(old, kept)
+
+
+def test_no_rows(cs):
+    h, w, _, _ = inputs(4, 100, 64, 8)
+    h, t, f = h[:0], torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, device="cuda")
+    assert [x.numel() for x in cs.lm_head_logprobs(h, w, t)] == [0, 0, 0]
+    for dtype in (BF16, torch.float32):
+        wide = torch.full((100, 72), 7.0, dtype=dtype, device="cuda")
+        gh, gw = cs.lm_head_logprobs_backward(h, w, t, f, f, f, out=(None, wide[:, :64]))
+        assert gh.shape == (0, 64) and not bool(wide[:, :64].any()) and bool((wide[:, 64:] == 7).all())
+
+
+def test_nan_and_infinities_where_no_row_is_scored(cs):
+    """Rows without a target, without a gradient or with a lost log-sum-exp are in no result."""
+    h, w, t, sup = inputs(200, 777, 128, 9, 0.5, 1)
+    dead = t < 0
+    h[dead] = math.nan
+    h[t > 776] = math.inf
+    check_scores(cs, h, w, t, sup)
+    _, ent, lse = cs.lm_head_logprobs(h, w, t, suppress_ids=sup)
+    live = torch.nonzero((t >= 0) & (t < 777))[:, 0]
+    gl, ge = torch.ones(200, device="cuda"), torch.zeros(200, device="cuda")
+    gl[live[3]] = 0.0
+    h[live[3]] = math.nan
+    lse[live[5]] = math.inf
+    h[live[5]] = -math.inf
+    gh, gw = cs.lm_head_logprobs_backward(h, w, t, lse, ent, gl, ge, suppress_ids=sup)
+    assert bool(torch.isfinite(gh).all()) and bool(torch.isfinite(gw).all())
+    assert not bool(gh[live[3]].any()) and not bool(gh[live[5]].any())
+    dz, clean = grads(h, w, t, lse, ent, gl, ge, sup)
+    e = 8 * float(logit_error(clean, w, torch.ones_like(dead)).max())
+    check_grad(gh, dz @ w.double(), dz.abs() @ w.double().abs() + 1e-6, e, 777)
+    check_grad(gw, dz.T @ clean, dz.abs().T @ clean.abs() + 1e-6, e, 200)
+
+
+def test_rows_without_mass_and_with_infinite_logits(cs):
+    """NaN and infinite products read as dllm_token_logprobs reads such logits."""
+    V, d = 300, 64
+    h = torch.zeros((6, d), device="cuda")
+    h[:, 0] = 1.0
+    h[1, 0] = math.nan                                   # every product NaN
+    h[3, 0] = 0.0                                        # every product 0
+    h[4, 0] = 2.0 ** 120                                 # products beyond any bound but finite differences
+    h[5, 0] = -2.0 ** 100
+    w = torch.zeros((V, d), device="cuda")
+    w[:, 0] = torch.linspace(-3, 3, V, device="cuda")
+    h, w = h.to(BF16), w.to(BF16)
+    t = torch.tensor([5, 5, 299, 7, 299, 0], dtype=torch.int32, device="cuda")
+    lp, ent, lse = cs.lm_head_logprobs(h, w, t, suppress_ids=[17])
+    want = scores(h, w, t, [17])
+    e = torch.full((6,), 2.0 ** -12, device="cuda", dtype=torch.float64)
+    near(lp, want[0], e)
+    near(ent, want[1], 10 * e)
+    near(lse, want[2], e)
+    assert float(lse[1]) == -math.inf and abs(float(lp[1]) + math.log(299)) < 1e-5
+    w[40, 0], w[41, 0] = math.inf, math.inf              # two ids share all the mass
+    lp, ent, lse = cs.lm_head_logprobs(h[:1], w, torch.tensor([41], dtype=torch.int32, device="cuda"))
+    assert float(lse[0]) == math.inf and abs(float(lp[0]) + math.log(2)) < 1e-5 and abs(float(ent[0]) - math.log(2)) < 1e-5
+
+
+def test_suppressed_target(cs):
+    h, w, t, _ = inputs(9, 333, 64, 10)
+    t[4] = 11
+    lp, ent, lse = check_scores(cs, h, w, t, [11, 12])
+    assert float(lp[4]) == -math.inf
+    one = torch.ones(9, device="cuda")
+    gh, gw = cs.lm_head_logprobs_backward(h, w, t, lse, ent, one, suppress_ids=[11, 12])
+    assert not bool(gh[4].any()) and bool(gh[3].any()) and not bool(gw[11].any() or gw[12].any())
+    check_backward(cs, h, w, t, [11, 12])
+
+
+def test_one_wanted_gradient(cs):
+    h, w, t, sup = inputs(150, 700, 96, 11, 0.7, 1)
+    both = check_backward(cs, h, w, t, sup)
+    only_h = check_backward(cs, h, w, t, sup, weight_grad=False)
+    only_w = check_backward(cs, h, w, t, sup, hidden_grad=False)
+    assert only_h[1] is None and only_w[0] is None
+    assert torch.equal(only_h[0], both[0]) and torch.equal(only_w[1], both[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_given_outputs(cs, dtype, accumulate):
+    """Rows of wider tensors, and adding to what is there (rows no token moves among it)."""
+    T, V, d = 130, 600, 136
+    h, w, t, sup = inputs(T, V, d, 12, 0.8, 2)
+    gw_all = torch.randn((V, d + 24), device="cuda").to(dtype)
+    gh_all = torch.randn((T, d + 8), device="cuda").to(BF16)
+    old = gw_all.clone()
+    before = gh_all.clone()
+    gh, gw, dz, clean, _ = check_backward(cs, h, w, t, sup, out=(gh_all[:, :d], gw_all[:, :d]),
+                                          **({"accumulate": True} if accumulate else {}))
+    assert gw.data_ptr() == gw_all.data_ptr() and torch.equal(gw_all[:, d:], old[:, d:])
+    assert torch.equal(gh_all[:, d:], before[:, d:])
+    check_grad(gw, dz.T @ clean, dz.abs().T @ clean.abs() + 1e-6, 1e-3, T, old[:, :d] if accumulate else None)
+
+
+def test_strided_inputs_and_batches(cs):
+    h, w, t, sup = inputs(150, 700, 96, 13, 0.7, 1)
+    hw = torch.full((150, 200), math.nan, dtype=BF16, device="cuda")
+    ww = torch.full((700, 104), math.nan, dtype=BF16, device="cuda")
+    hw[:, :96], ww[:, :96] = h, w
+    a = check_scores(cs, h.view(3, 50, 96), w, t.view(3, 50), sup)
+    b = cs.lm_head_logprobs(hw[:, :96], ww[:, :96], t, suppress_ids=sup)
+    assert all(torch.equal(x.reshape(-1), y) for x, y in zip(a, b))
+    g = torch.ones(150, device="cuda")
+    c = cs.lm_head_logprobs_backward(h, w, t, b[2], b[1], g, suppress_ids=sup)
+    e = cs.lm_head_logprobs_backward(hw[:, :96], ww[:, :96], t, b[2], b[1], g, suppress_ids=sup)
+    assert torch.equal(c[0], e[0]) and torch.equal(c[1], e[1])
+
+
+def test_results_repeat_and_do_not_depend_on_the_workspace(cs):
+    h, w, t, sup = inputs(900, 30000, 256, 14, 0.5, 1)
+    g = torch.randn(900, device="cuda")
+    runs = []
+    for fill in (0, 255):
+        need = cs.lib_handle().dllm_lm_head_logprobs_workspace_size(900, 30000, 256)
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        s = cs.lm_head_logprobs(h, w, t, suppress_ids=sup, ws=ws)
+        need = cs.lib_handle().dllm_lm_head_logprobs_backward_workspace_size(900, 30000, 256)
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        runs.append([*s, *cs.lm_head_logprobs_backward(h, w, t, s[2], s[1], g, g, suppress_ids=sup, ws=ws)])
+        if fill == 0:
+            assert cs.workspace_fault(ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+def test_autograd(cs):
+    h, w, t, sup = inputs(77, 900, 128, 15, 0.6, 1)
+    ha, wa = h.view(7, 11, 128).clone().requires_grad_(), w.clone().requires_grad_()
+    lp, ent = cs.score_hidden(ha, wa, t.view(7, 11), suppress_ids=sup)
+    (lp.sum() * -0.5 + 0.1 * ent.sum()).backward()
+    l0, e0, s0 = cs.lm_head_logprobs(h, w, t, suppress_ids=sup)
+    one = torch.ones(77, device="cuda")
+    gh, gw = cs.lm_head_logprobs_backward(h, w, t, s0, e0, -0.5 * one, 0.1 * one, suppress_ids=sup)
+    assert torch.equal(lp.reshape(-1), l0) and torch.equal(ent.reshape(-1), e0)
+    assert torch.equal(ha.grad.reshape(77, 128), gh) and torch.equal(wa.grad, gw)
+    lp, _ = cs.score_hidden(h.requires_grad_(), w, t, suppress_ids=sup)      # one output, one input
+    lp.mean().backward()
+    assert h.grad is not None and w.grad is None
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        lp, _ = cs.score_hidden(ha, wa, t.view(7, 11))
+        g, = torch.autograd.grad(lp.sum(), ha, create_graph=True)
+        g.float().sum().backward()
+
+
+def test_matches_the_scores_of_stored_logits(cs):
+    """The same model through logits in memory: one softmax, one loss."""
+    h, w, t, sup = inputs(64, 4000, 256, 16, 1.0, 1)
+    z = h.float() @ w.float().T
+    want = cs.token_logprobs(z, t, suppress_ids=sup)
+    got = cs.lm_head_logprobs(h, w, t, suppress_ids=sup)
+    for a, b in zip(got, want[:3]):
+        assert float((a - b).abs().max()) < 1e-3
+    e = float(logit_error(h, w, torch.ones_like(t, dtype=torch.bool)).max())
+    assert float((got[0] - want[0]).abs().max()) <= 4 * e + 2.0 ** -14
+
+
+def test_side_stream_and_graph(cs):
+    h, w, t, sup = inputs(300, 5000, 192, 17, 0.5, 1)
+    g = torch.randn(300, device="cuda")
+    want = [*cs.lm_head_logprobs(h, w, t, suppress_ids=sup)]
+    want += cs.lm_head_logprobs_backward(h, w, t, want[2], want[1], g, suppress_ids=sup)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [*cs.lm_head_logprobs(h, w, t, suppress_ids=sup, stream=side)]
+    got += cs.lm_head_logprobs_backward(h, w, t, got[2], got[1], g, suppress_ids=sup, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = [*cs.lm_head_logprobs(h, w, t, suppress_ids=sup)]
+        cap += cs.lm_head_logprobs_backward(h, w, t, cap[2], cap[1], g, suppress_ids=sup)
+    t.copy_(t.roll(7))                                   # other rows are scored in the replay
+    h.copy_(h.roll(3, 0))
+    graph.replay()
+    torch.cuda.synchronize()
+    want = [*cs.lm_head_logprobs(h, w, t, suppress_ids=sup)]
+    want += cs.lm_head_logprobs_backward(h, w, t, want[2], want[1], g, suppress_ids=sup)
+    assert all(torch.equal(a, b) for a, b in zip(cap, want))
