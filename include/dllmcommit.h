@@ -709,7 +709,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
  *   out     device (B, L, d) contiguous, weight's dtype; the product with scale
  *           (finite) is fp32, rounded once
  * Rows in whole 16-byte vectors: d and strides multiples of 8 (bf16) or 4 (fp32),
- * bases 16-byte aligned; at most 2^30 tokens (else DLLM_ERR_UNSUPPORTED).
+ * bases 16-byte aligned; at most 2^30 tokens, d up to 2^20 (else
+ * DLLM_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 dllm_status dllm_embed_tokens(const int32_t* tokens, int64_t B, int64_t L, int64_t token_stride, const void* weight,
                               dllm_dtype dt, int64_t V, int64_t d, int64_t weight_stride, float scale, void* out,
