@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
 // away take fewer groups (1.09 GB: 143 us, 167 to 172 in equal shares).  It is
 // launched behind the sort and runs beside it: it waits for the sort at its end
 // only, so that whoever waits for this kernel waits for both.
-constexpr int kZeroThreads = 1024;
+constexpr int kZeroThreads = 512;
 constexpr int kZeroBits = 1 << 20;
 
 struct ZeroParams {
@@ -271,7 +271,7 @@ struct ZeroParams {
   int32_t rows;                 // rows of a group: a power of two
 };
 
-__global__ void __launch_bounds__(kZeroThreads, 1) embed_zero_kernel(const __grid_constant__ ZeroParams p) {
+__global__ void __launch_bounds__(kZeroThreads, 3) embed_zero_kernel(const __grid_constant__ ZeroParams p) {
   extern __shared__ uint32_t em_named[];
   __shared__ __align__(16) uint4 answer;
   __shared__ __align__(8) uint64_t answer_bar;
@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(kRunWarps * 32) embed_sum_kernel(const __grid_
   constexpr int kAhead = 8;
   __shared__ float4 edge[kRunWarps][2][kCols / 4][32];
   __shared__ int32_t edge_key[kRunWarps][2];             // of the first and the last run; no row: V
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t block = blockIdx.x / p.slabs;
   const int64_t vec = (blockIdx.x - block * p.slabs) * 32 + lane;
@@ -529,8 +529,8 @@ template <bool BF16, bool OUT16>
 __global__ void __launch_bounds__(kRunWarps * 32) embed_join_kernel(const __grid_constant__ RunParams p) {
   constexpr int kCols = RunLane<BF16>::kCols;
   __shared__ float4 share[kRunWarps][kCols / 4][32];
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t block = blockIdx.x / p.slabs;
   const int64_t vec = (blockIdx.x - block * p.slabs) * 32 + lane;
@@ -755,26 +755,30 @@ dllm_status dllm_embed_tokens_backward(const int32_t* tokens, int64_t B, int64_t
                                    : reinterpret_cast<const void*>(&embed_join_kernel<true, false>))
                           : (out16 ? reinterpret_cast<const void*>(&embed_join_kernel<false, true>)
                                    : reinterpret_cast<const void*>(&embed_join_kernel<false, false>));
-  void* kargs[] = {&k};
+  ZeroParams z{};
+  z.tok = k.tok;
+  z.out = static_cast<uint8_t*>(grad_weight);
+  z.row_bytes = grad_weight_stride * size;
+  z.vecs = em_div(static_cast<uint32_t>(d * size / 16));
+  z.rows = 1;
+  while (z.rows < 4096 && 2 * z.rows * static_cast<int64_t>(z.vecs.d) <= 4096) z.rows *= 2;   // 64 KB a group
+  const size_t zero_smem = static_cast<size_t>((std::min<int64_t>(V, kZeroBits) + 31) / 32 * 4);
+  const dim3 zero_grid(static_cast<unsigned>((V + z.rows - 1) / z.rows));
+  void *kargs[] = {&k}, *args[] = {&r}, *zargs[] = {&z};
+  auto zero = [&] {
+    return launch_pdl(reinterpret_cast<const void*>(&embed_zero_kernel), zero_grid, dim3(kZeroThreads), zero_smem, stream, zargs);
+  };
+  // The zero rows run beside the sort, and beside the sums as well where these fit
+  // the GPU at once (each kernel lets the next begin before it waits, so that the
+  // sums' blocks only have to have begun).
+  const bool sums_first = !accumulate && r.blocks * r.slabs <= 2 * sms;
   dllm_status ok = launch_pdl(reinterpret_cast<const void*>(&embed_sort_kernel), dim3(kSortCtas), dim3(kSortThreads), kSortSmem,
                               stream, kargs, kSortCtas);
-  if (ok == DLLM_OK && !accumulate) {
-    ZeroParams z{};
-    z.tok = k.tok;
-    z.out = static_cast<uint8_t*>(grad_weight);
-    z.row_bytes = grad_weight_stride * size;
-    z.vecs = em_div(static_cast<uint32_t>(d * size / 16));
-    z.rows = 1;
-    while (z.rows < 4096 && 2 * z.rows * static_cast<int64_t>(z.vecs.d) <= 4096) z.rows *= 2;   // 64 KB a group
-    const size_t smem = static_cast<size_t>((std::min<int64_t>(V, kZeroBits) + 31) / 32 * 4);
-    void* zargs[] = {&z};
-    ok = launch_pdl(reinterpret_cast<const void*>(&embed_zero_kernel), dim3(static_cast<unsigned>((V + z.rows - 1) / z.rows)),
-                    dim3(kZeroThreads), smem, stream, zargs);
-  }
-  void* args[] = {&r};
+  if (ok == DLLM_OK && !accumulate && !sums_first) ok = zero();
   if (ok == DLLM_OK) ok = launch_pdl(sum, grid, block, 0, stream, args);
-  if (ok != DLLM_OK || r.blocks < 2) return ok;
-  return launch_pdl(join, grid, block, 0, stream, args);
+  if (ok == DLLM_OK && r.blocks > 1) ok = launch_pdl(join, grid, block, 0, stream, args);
+  if (ok == DLLM_OK && sums_first) ok = zero();
+  return ok;
 }
 
 }  // extern "C"
