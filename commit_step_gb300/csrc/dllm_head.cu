@@ -15,10 +15,12 @@
 // epilogue; dH += dz W over the piece (K: the piece's ids); dW = dz^T H (K: the
 // scored rows).
 //
-// All products run on the 5th-generation tensor cores: TMA brings 64-wide slabs
-// of K into a ring in shared memory (128-byte swizzle), tcgen05.mma (bf16 in,
-// fp32 accumulate) fills one of two accumulators in TMEM while eight epilogue
-// warps empty the other.  K-major operands (hidden and weight in the first
+// All products run on the 5th-generation tensor cores, a pair of CTAs a tile of
+// 256 x 256 (cta_group::2): each CTA holds 128 rows of A and of the accumulator
+// and half of B's columns, so that a slab of K costs a CTA 32 KB of shared memory.
+// TMA brings 64-wide slabs of K into a ring (128-byte swizzle), tcgen05.mma (bf16
+// in, fp32 accumulate) fills one of two accumulators in TMEM while eight epilogue
+// warps of each CTA empty the other.  K-major operands (hidden and weight in the first
 // product, dz in the second) lie as rows of 64 k; the others (weight in the
 // second, both in the third) are read as they lie in memory, MN-major, as rows
 // of 64 m or n.
@@ -38,19 +40,20 @@
 
 namespace dllm {
 
-constexpr int kHdBM = 128;                       // rows of an accumulator tile
+constexpr int kHdBM = 256;                       // rows of a pair's accumulator tile
+constexpr int kHdRows = kHdBM / 2;               // a CTA's
 constexpr int kHdBN = 256;                       // its columns at most
 constexpr int kHdBK = 64;                        // K of a stage: one 128-byte swizzle row of bf16
-constexpr int kHdABytes = kHdBM * kHdBK * 2;     // 16 KB
-constexpr int kHdBBytes = kHdBN * kHdBK * 2;     // 32 KB
-constexpr int kHdStages = 4;
+constexpr int kHdABytes = kHdRows * kHdBK * 2;   // 16 KB
+constexpr int kHdBBytes = kHdBN / 2 * kHdBK * 2; // 16 KB
+constexpr int kHdStages = 7;
 constexpr int kHdEpiWarps = 8;                   // two warpgroups, each reads every other 32-column chunk of a tile
 constexpr int kHdTmaWarp = 10;
 constexpr int kHdMmaWarp = 11;
 constexpr int kHdThreads = 12 * 32;
 constexpr int kHdTmemCols = 512;
 constexpr int kHdSmem = kHdStages * (kHdABytes + kHdBBytes) + 1024;
-constexpr int kHdBand = 32;                      // row tiles that share a pass over the vocabulary (4096 rows: 32 MB of
+constexpr int kHdBand = 16;                      // row tiles that share a pass over the vocabulary (4096 rows: 32 MB of
                                                  // hidden states of 4096 stay in L2 while the weight streams)
 constexpr float kHdCap = 0x1p+125f;              // logits are read within +-2^125 (NaN as the lowest): differences stay finite
 constexpr float kHdAbsent = -0x1p+126f;          // suppressed ids and columns past the vocabulary
@@ -73,7 +76,7 @@ struct HeadParams {
   int32_t bn;                    // columns of a tile
   int32_t n_n;                   // tiles along N
   uint32_t idesc;
-  uint32_t a_bytes;              // what one load of A brings
+  uint32_t a_bytes;              // what a CTA's load of A brings
   const int32_t* target;         // per scored row
   int32_t n_sup;
   int32_t sup[DLLM_MAX_SUPPRESS];
@@ -114,9 +117,10 @@ __device__ __forceinline__ uint64_t hd_desc(uint32_t addr, uint32_t leading) {
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
+// A load of this CTA's shared memory that counts on the leader's barrier.
 __device__ __forceinline__ void hd_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
@@ -125,13 +129,36 @@ __device__ __forceinline__ void hd_load(uint32_t dst, const CUtensorMap* map, in
 __device__ __forceinline__ void hd_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 
+// Arrives on the barrier at this place of both CTAs when the products issued so far are done.
 __device__ __forceinline__ void hd_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t hd_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The place of addr in the leader's shared memory.
+__device__ __forceinline__ uint32_t hd_leader(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void hd_arrive_leader(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void hd_cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void hd_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -151,12 +178,24 @@ __device__ __forceinline__ void hd_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 
+__device__ __forceinline__ bool hd_try_wait(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+
 // A bounded wait: false after the deadline or once the CTA gave up.
 __device__ __forceinline__ bool hd_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (hd_try_wait(bar, parity, kSleepHintNs)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (hd_try_wait(bar, parity, kSleepHintNs)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > kWaitLimitCycles) return false;
   }
@@ -178,15 +217,15 @@ __device__ __forceinline__ uint32_t hd_bf16x2(float lo, float hi) {
 
 // How many ways the second product's K is split, for n scored rows (the same
 // answer in the product and in the kernel that joins the parts).
-__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int ctas, int slabs) {
+__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int pairs, int slabs) {
   const int64_t tiles = (n + kHdBM - 1) / kHdBM * n_n;
   if (tiles == 0) return 1;
-  const int64_t s = ctas / tiles;
+  const int64_t s = pairs / tiles;
   return static_cast<int>(s < 1 ? 1 : (s > slabs ? slabs : s));
 }
 
-// The tiles of a product and the order in which the CTAs take them (tile i to
-// CTA i mod grid).  A split of a short last piece may hold no slab: such a tile
+// The tiles of a product and the order in which the pairs of CTAs take them (tile i
+// to pair i mod pairs).  A split of a short last piece may hold no slab: such a tile
 // is passed over (what it adds to, an earlier piece has written).
 struct HeadTile {
   int32_t m, n;        // tile coordinates
@@ -207,7 +246,7 @@ struct HeadWork {
     } else if (OP == kHdDh) {
       n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
       slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
-      splits = hd_splits(n, n_n, gridDim.x, p.split_slabs);
+      splits = hd_splits(n, n_n, gridDim.x / 2, p.split_slabs);
     } else {
       n_m = static_cast<int32_t>((p.cols + kHdBM - 1) / kHdBM);
       slabs = static_cast<int32_t>((n + kHdBK - 1) / kHdBK);
@@ -222,11 +261,12 @@ struct HeadWork {
     t.k1 = slabs;
     if (OP == kHdScore || OP == kHdDz) {
       // bands of row tiles, each over the whole vocabulary, its row tiles inner
-      const int64_t per_band = static_cast<int64_t>(kHdBand) * n_n;
+      const int32_t bands = (n_m + kHdBand - 1) / kHdBand, high = (n_m + bands - 1) / bands;
+      const int64_t per_band = static_cast<int64_t>(high) * n_n;
       const int32_t band = static_cast<int32_t>(i / per_band);
       const int32_t in = static_cast<int32_t>(i - band * per_band);
-      const int32_t rows = min(kHdBand, n_m - band * kHdBand);
-      t.m = band * kHdBand + in % rows;
+      const int32_t rows = min(high, n_m - band * high);
+      t.m = band * high + in % rows;
       t.n = in / rows;
     } else if (OP == kHdDh) {
       const int64_t tiles = static_cast<int64_t>(n_m) * n_n;
@@ -316,8 +356,12 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   __shared__ int32_t sup_s[DLLM_MAX_SUPPRESS];
   volatile int32_t* abort_flag = &abort_flag_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = hd_rank();
   const uint32_t ring = (smem_addr(hd_smem) + 1023u) & ~1023u;
 
+  // full (counted in the leader, by the loads of both CTAs) and acce (the epilogue
+  // warps of both) are waited for by the leader's products; empty and accf are
+  // arrived at in both CTAs by the products.
   if (threadIdx.x == 0) {
     for (int s = 0; s < kHdStages; ++s) {
       mbar_init(smem_addr(&full_bar[s]), 1);
@@ -325,20 +369,21 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&accf_bar[b]), 1);
-      mbar_init(smem_addr(&acce_bar[b]), kHdEpiWarps);
+      mbar_init(smem_addr(&acce_bar[b]), 2 * kHdEpiWarps);
     }
     abort_flag_s = 0;
     fence_mbar_init();
   }
   for (int q = threadIdx.x; q < p.n_sup; q += blockDim.x) sup_s[q] = p.sup[q];
   if (warp == kHdMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
                  "r"(kHdTmemCols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   hd_fence_before();
   __syncthreads();
+  hd_cluster_sync();
   hd_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_wait();
@@ -346,37 +391,45 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   const int64_t n = *p.n_rows;
   const HeadWork<OP> work(p, n);
   const bool packed = n != p.T;
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // Rows of A and of the accumulator that exist.
+  const int64_t a_rows = OP == kHdDw ? p.cols : n;
 
   if (warp == kHdTmaWarp) {
     if (lane == 0) {
       const CUtensorMap* ma = (OP == kHdScore || OP == kHdDz) && packed ? &p.tm_packed : &p.tm_a;
       const CUtensorMap* mb = OP == kHdDw && packed ? &p.tm_packed : &p.tm_b;
-      const uint32_t tx = p.a_bytes + static_cast<uint32_t>(p.bn) * kHdBK * 2;
+      const int half = p.bn / 2;
       int s = 0;
       uint32_t ph = 0;
       int64_t issued = 0;
-      for (int64_t i = blockIdx.x; i < work.total && !*abort_flag; i += gridDim.x) {
+      for (int64_t i = pair; i < work.total && !*abort_flag; i += pairs) {
         const HeadTile t = work.tile(i);
-        const int m0 = t.m * kHdBM, n0 = t.n * p.bn;
+        const int m0 = t.m * kHdBM + static_cast<int>(rank) * kHdRows, n0 = t.n * p.bn + static_cast<int>(rank) * half;
+        // The second CTA's rows may all be past the end: then its A is not loaded.
+        const bool second = static_cast<int64_t>(t.m) * kHdBM + kHdRows < a_rows;
+        const uint32_t tx = (second ? 2u : 1u) * p.a_bytes + static_cast<uint32_t>(p.bn) * kHdBK * 2;
         for (int k = t.k0; k < t.k1; ++k) {
           if (!hd_wait(smem_addr(&empty_bar[s]), ph ^ 1u, abort_flag)) {
             hd_fail(p, abort_flag, kFaultEmptyWait);
             break;
           }
-          const uint32_t bar = smem_addr(&full_bar[s]);
+          const uint32_t bar = hd_leader(smem_addr(&full_bar[s]));
           const uint32_t a = ring + static_cast<uint32_t>(s) * (kHdABytes + kHdBBytes), b = a + kHdABytes;
-          mbar_arrive_expect_tx(bar, tx);
-          if (hd_a_mn(OP)) {
-            hd_load(a, ma, m0, k * kHdBK, bar);
-            hd_load(a + 8192, ma, m0 + 64, k * kHdBK, bar);
-          } else {
-            hd_load(a, ma, k * kHdBK, m0, bar);
+          if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full_bar[s]), tx);
+          if (rank == 0 || second) {
+            if (hd_a_mn(OP)) {
+              hd_load(a, ma, m0, k * kHdBK, bar);
+              hd_load(a + 8192, ma, m0 + 64, k * kHdBK, bar);
+            } else {
+              hd_load(a, ma, k * kHdBK, m0, bar);
+            }
           }
           if (OP == kHdScore || OP == kHdDz) {
             hd_load(b, mb, k * kHdBK, static_cast<int>(p.v0) + n0, bar);
           } else {
             const int y = (OP == kHdDh ? static_cast<int>(p.v0) : 0) + k * kHdBK;
-            for (int x = 0; x < p.bn; x += 64) hd_load(b + x * 128, mb, n0 + x, y, bar);
+            for (int x = 0; x < half; x += 64) hd_load(b + x * 128, mb, n0 + x, y, bar);
           }
           ++issued;
           if (++s == kHdStages) {
@@ -386,15 +439,15 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         }
       }
       // Giving up: the copies still in flight land before the CTA ends.
-      if (*abort_flag)
+      if (*abort_flag && rank == 0)
         for (int64_t q = issued > kHdStages ? issued - kHdStages : 0; q < issued; ++q)
           mbar_wait_bounded(smem_addr(&full_bar[q % kHdStages]), static_cast<uint32_t>((q / kHdStages) & 1));
     }
   } else if (warp == kHdMmaWarp) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       int s = 0, j = 0;
       uint32_t ph = 0;
-      for (int64_t i = blockIdx.x; i < work.total && !*abort_flag; i += gridDim.x) {
+      for (int64_t i = pair; i < work.total && !*abort_flag; i += pairs) {
         const HeadTile t = work.tile(i);
         if (t.k0 == t.k1) continue;
         const int buf = j & 1;
@@ -428,11 +481,11 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   } else if (warp < kHdEpiWarps) {
     const int ew = warp & 3, half = warp >> 2;
     int j = 0;
-    for (int64_t i = blockIdx.x; i < work.total; i += gridDim.x) {
+    for (int64_t i = pair; i < work.total; i += pairs) {
       const HeadTile t = work.tile(i);
       if (t.k0 == t.k1) continue;
       const int buf = j & 1;
-      const int64_t row = static_cast<int64_t>(t.m) * kHdBM + ew * 32 + lane;   // scored row, or (dw) id of the piece
+      const int64_t row = static_cast<int64_t>(t.m) * kHdBM + rank * kHdRows + ew * 32 + lane;  // scored row, or (dw) id of the piece
       HeadRow info{};
       int32_t target = -1;
       if (OP == kHdScore && row < n) target = p.target[row];
@@ -533,7 +586,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       }
       hd_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&acce_bar[buf]));
+      if (lane == 0) hd_arrive_leader(hd_leader(smem_addr(&acce_bar[buf])));
       if (OP == kHdScore && row < n)
         p.part[(static_cast<int64_t>(t.n) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
     }
@@ -551,9 +604,10 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   // the CTA gave up; release the TMEM.
   hd_fence_before();
   __syncthreads();
+  hd_cluster_sync();                                     // (neither CTA's memory is used by the other any more)
   if (warp == kHdMmaWarp) {
     hd_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kHdTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kHdTmemCols) : "memory");
   }
 }
 
@@ -710,12 +764,12 @@ __global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant
 
 // grad_hidden from the second product's parts, added in order: a block a row.
 __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, const int32_t* place, const float* acc,
-                                                      int64_t acc_stride, int32_t n_n, int32_t ctas, int32_t slabs,
+                                                      int64_t acc_stride, int32_t n_n, int32_t pairs, int32_t slabs,
                                                       int64_t T, int64_t d, uint16_t* out, int64_t out_stride) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t n = *n_rows;
-  const int splits = hd_splits(n, n_n, ctas, slabs);
+  const int splits = hd_splits(n, n_n, pairs, slabs);
   const int64_t step = (n + kHdBM - 1) / kHdBM * kHdBM * acc_stride;
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     const int32_t row = place[t];
@@ -819,7 +873,7 @@ HdPlan hd_plan(int64_t T, int64_t V, int64_t d, int64_t sms, bool backward) {
   h.bn_v = kHdBN;
   h.n_v = static_cast<int32_t>(piece / kHdBN);
   h.n_d = static_cast<int32_t>((d + kHdBN - 1) / kHdBN);
-  h.bn_d = static_cast<int32_t>(round_up((d + h.n_d - 1) / h.n_d, 64));
+  h.bn_d = static_cast<int32_t>(round_up((d + h.n_d - 1) / h.n_d, 128));
   h.n_d = static_cast<int32_t>((d + h.bn_d - 1) / h.bn_d);
   h.acc = std::max<int64_t>(h.t_pad * h.n_d * h.bn_d, sms * kHdBM * kHdBN);
   size_t at = 256;
@@ -874,8 +928,8 @@ dllm_status hd_check(const void* hidden, int64_t T, int64_t d, int64_t hidden_st
 template <int OP>
 dllm_status hd_launch(HeadParams& p, int sms, dllm_stream_t stream) {
   void* args[] = {&p};
-  return launch_pdl(reinterpret_cast<const void*>(&head_kernel<OP>), dim3(static_cast<unsigned>(sms)), dim3(kHdThreads), kHdSmem,
-                    stream, args);
+  return launch_pdl(reinterpret_cast<const void*>(&head_kernel<OP>), dim3(static_cast<unsigned>(sms / 2 * 2)), dim3(kHdThreads), kHdSmem,
+                    stream, args, 2);
 }
 
 dllm_status hd_gather(const void* hidden, int64_t stride, int64_t T, int64_t d, const int32_t* n_rows, const int32_t* rows,
@@ -931,10 +985,10 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   l.o_lse = lse;
 
   HeadParams p{};
-  const uint32_t a_rows = static_cast<uint32_t>(std::min<int64_t>(kHdBM, round_up(T, 8)));
+  const uint32_t a_rows = static_cast<uint32_t>(std::min<int64_t>(kHdRows, round_up(T, 8)));
   if (!make_map(&p.tm_a, hidden, T, d, hidden_stride, a_rows) ||
       !make_map(&p.tm_packed, ws + h.hidden, round_up(T, kHdBK), d, d, a_rows) ||
-      !make_map(&p.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v)))
+      !make_map(&p.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v / 2)))
     return DLLM_ERR_CUDA;
   p.n_rows = n_rows;
   p.T = T;
@@ -1033,7 +1087,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   l.row = reinterpret_cast<HeadRow*>(ws + h.row);
 
   HeadParams p{};
-  const uint32_t a_rows = static_cast<uint32_t>(std::min<int64_t>(kHdBM, round_up(T, 8)));
+  const uint32_t a_rows = static_cast<uint32_t>(std::min<int64_t>(kHdRows, round_up(T, 8)));
   p.n_rows = n_rows;
   p.T = T;
   p.V = V;
@@ -1055,8 +1109,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   const int64_t packed_rows = round_up(T, kHdBK);
   if (!make_map(&pz.tm_a, hidden, T, d, hidden_stride, a_rows) ||
       !make_map(&pz.tm_packed, ws + h.hidden, packed_rows, d, d, a_rows) ||
-      !make_map(&pz.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v)) ||
-      !make_map(&ph.tm_a, p.dz, h.t_pad, h.piece, h.piece, kHdBM) || !make_map(&ph.tm_b, weight, V, d, weight_stride, 64) ||
+      !make_map(&pz.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v / 2)) ||
+      !make_map(&ph.tm_a, p.dz, h.t_pad, h.piece, h.piece, kHdRows) || !make_map(&ph.tm_b, weight, V, d, weight_stride, 64) ||
       !make_map(&pw.tm_a, p.dz, h.t_pad, h.piece, h.piece, 64) || !make_map(&pw.tm_b, hidden, T, d, hidden_stride, 64) ||
       !make_map(&pw.tm_packed, ws + h.hidden, packed_rows, d, d, 64))
     return DLLM_ERR_CUDA;
@@ -1093,9 +1147,9 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   const float* acc = p.acc;
   uint16_t* out = static_cast<uint16_t*>(grad_hidden);
   const int32_t* place = l.place;
-  int32_t n_n = h.n_d, ctas = dev->sms, slabs = ph.split_slabs;
+  int32_t n_n = h.n_d, pairs = dev->sms / 2, slabs = ph.split_slabs;
   int64_t stride = p.acc_stride;
-  void* args[] = {&n_rows, &place, &acc, &stride, &n_n, &ctas, &slabs, &T, &d, &out, &grad_hidden_stride};
+  void* args[] = {&n_rows, &place, &acc, &stride, &n_n, &pairs, &slabs, &T, &d, &out, &grad_hidden_stride};
   return launch_pdl(reinterpret_cast<const void*>(&head_dh_kernel), dim3(static_cast<unsigned>(std::min<int64_t>(T, dev->sms * 8))),
                     dim3(256), 0, stream, args);
 }
