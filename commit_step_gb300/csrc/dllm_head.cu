@@ -1,9 +1,9 @@
 // dllm_head.cu -- scores of given tokens straight from the hidden states, and
 // their gradient: logits z = h W^T that are never stored (sm_103a).
 //
-// Only scored rows (a target in [0, V)) take part: a first kernel numbers them,
-// a second gathers their hidden states (unless all rows are scored), and every
-// later kernel reads their count n on the device.
+// Only scored rows (a target in [0, V)) take part: a first kernel numbers them and
+// gathers their hidden states (unless all rows are scored), and every later kernel
+// reads their count n on the device.
 //
 // Forward: one matrix product whose epilogue folds a tile's logits into a
 // partial softmax (m, sum 2^y, sum 2^y y, y = (z - m) log2 e) per row; a last
@@ -46,13 +46,14 @@ constexpr int kHdBN = 256;                       // its columns at most
 constexpr int kHdBK = 64;                        // K of a stage: one 128-byte swizzle row of bf16
 constexpr int kHdABytes = kHdRows * kHdBK * 2;   // 16 KB
 constexpr int kHdBBytes = kHdBN / 2 * kHdBK * 2; // 16 KB
-constexpr int kHdStages = 7;
+constexpr int kHdStages = 6;
 constexpr int kHdEpiWarps = 8;                   // two warpgroups, each reads every other 32-column chunk of a tile
 constexpr int kHdTmaWarp = 10;
 constexpr int kHdMmaWarp = 11;
 constexpr int kHdThreads = 12 * 32;
 constexpr int kHdTmemCols = 512;
-constexpr int kHdSmem = kHdStages * (kHdABytes + kHdBBytes) + 1024;
+constexpr int kHdStoreBytes = 32 * 64 * 2;       // a warp's 32 rows of 64 bf16 columns on their way out
+constexpr int kHdSmem = kHdStages * (kHdABytes + kHdBBytes) + kHdEpiWarps * kHdStoreBytes + 1024;
 constexpr int kHdBand = 16;                      // row tiles that share a pass over the vocabulary (4096 rows: 32 MB of
                                                  // hidden states of 4096 stay in L2 while the weight streams)
 constexpr float kHdCap = 0x1p+125f;              // logits are read within +-2^125 (NaN as the lowest): differences stay finite
@@ -68,7 +69,8 @@ struct HeadRow {
 struct HeadParams {
   CUtensorMap tm_a, tm_b;        // the operands; where one is the hidden states, the caller's tensor,
   CUtensorMap tm_packed;         // read when every row is scored, and else their gathered copy
-  const int32_t* n_rows;         // device: the scored rows
+  CUtensorMap tm_out;            // dw in bf16 without accumulate: the weight's gradient
+  const int32_t* n_rows;         // device: the scored rows; then the splits of the second product
   int64_t T, V;
   int64_t v0;                    // the piece's first id
   int64_t cols;                  // its ids
@@ -80,7 +82,7 @@ struct HeadParams {
   const int32_t* target;         // per scored row
   int32_t n_sup;
   int32_t sup[DLLM_MAX_SUPPRESS];
-  float4* part;                  // score: (tiles along N, 2, rows): m, Z, S
+  float4* part;                  // score: (tiles along N, or pairs where there is one row tile; 2; rows): m, Z, S
   int64_t part_rows;
   float* z_target;               // score: per scored row
   const HeadRow* row;            // dz
@@ -89,7 +91,6 @@ struct HeadParams {
   float* acc;                    // dh: (splits, row tiles x 128, acc_stride) fp32
   int64_t acc_stride;
   int32_t add;                   // dh: the piece is not the first
-  int32_t split_slabs;           // dh: the slabs of a whole piece, which decide the splits
   void* grad_w;                  // dw
   int64_t grad_w_stride;
   int32_t grad_w_f32, accumulate;
@@ -215,13 +216,23 @@ __device__ __forceinline__ uint32_t hd_bf16x2(float lo, float hi) {
   return d;
 }
 
-// How many ways the second product's K is split, for n scored rows (the same
-// answer in the product and in the kernel that joins the parts).
-__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int pairs, int slabs) {
-  const int64_t tiles = (n + kHdBM - 1) / kHdBM * n_n;
-  if (tiles == 0) return 1;
-  const int64_t s = pairs / tiles;
-  return static_cast<int>(s < 1 ? 1 : (s > slabs ? slabs : s));
+// How many ways the second product's K is split: the fewest rounds of tiles that the
+// pairs can be kept busy with, against 8 bytes a split of every element written and
+// read again (1.5 MB in the time of a slab of 256 x 256 x 64).  32 tiles of 1976
+// slabs on 76 pairs: 7 splits, 3 full rounds (2 splits leave 12 pairs idle).
+__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int bn, int pairs, int slabs, int64_t room) {
+  const int64_t tiles = (n + kHdBM - 1) / kHdBM * n_n, size = tiles * kHdBM * bn;
+  int best = 1;
+  float least = 3.4e38f;
+  for (int s = 1; s <= 32 && s <= slabs && (s == 1 || s * size <= room); ++s) {
+    const float cost = static_cast<float>((tiles * s + pairs - 1) / pairs) * static_cast<float>((slabs + s - 1) / s) * (bn / 256.0f) +
+                       static_cast<float>(s) * static_cast<float>(size) * (8.0f / 1.5e6f);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 // The tiles of a product and the order in which the pairs of CTAs take them (tile i
@@ -246,7 +257,7 @@ struct HeadWork {
     } else if (OP == kHdDh) {
       n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
       slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
-      splits = hd_splits(n, n_n, gridDim.x / 2, p.split_slabs);
+      splits = p.n_rows[1];
     } else {
       n_m = static_cast<int32_t>((p.cols + kHdBM - 1) / kHdBM);
       slabs = static_cast<int32_t>((n + kHdBK - 1) / kHdBK);
@@ -333,6 +344,49 @@ __device__ __forceinline__ void hd_store_bf16(uint16_t* out, const float (&x)[32
   }
 }
 
+// The same to 32-byte aligned memory, whole sectors a store.
+__device__ __forceinline__ void hd_store_dz(uint16_t* out, const float (&x)[32], int lim) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 16) {
+    if (j >= lim) break;
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j), "r"(hd_bf16x2(x[j], x[j + 1])),
+                 "r"(hd_bf16x2(x[j + 2], x[j + 3])), "r"(hd_bf16x2(x[j + 4], x[j + 5])), "r"(hd_bf16x2(x[j + 6], x[j + 7])),
+                 "r"(hd_bf16x2(x[j + 8], x[j + 9])), "r"(hd_bf16x2(x[j + 10], x[j + 11])),
+                 "r"(hd_bf16x2(x[j + 12], x[j + 13])), "r"(hd_bf16x2(x[j + 14], x[j + 15]))
+                 : "memory");
+  }
+}
+
+// This warp's 32 rows of 64 accumulator columns at taddr, as bf16, to columns x and
+// rows y of the tensor: through shared memory in the 128-byte swizzle and out by
+// TMA, so that memory sees whole lines (stored from registers, a row a thread, the
+// weight's gradient took 504 us where it now takes [DW] at 512 x 126464 x 4096).
+__device__ __forceinline__ void hd_store_tile(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (the last one has left the buffer)
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r[32];
+    hd_ld32(taddr + 32 * h, r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = hd_bf16x2(__uint_as_float(r[8 * j + 2 * e]), __uint_as_float(r[8 * j + 2 * e + 1]));
+      const uint32_t at = buf + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4);
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(buf)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
 __device__ __forceinline__ void hd_store_f32(float* out, const float (&x)[32], int lim, bool add) {
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
@@ -386,6 +440,13 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   hd_cluster_sync();
   hd_fence_after();
   const uint32_t tmem = tmem_slot;
+  // With one row tile the pair's first tile does not depend on the count: while the
+  // rows are numbered, its weight comes to L2.
+  if ((OP == kHdScore || OP == kHdDz) && p.T <= kHdBM && warp == kHdTmaWarp && lane == 0 && (blockIdx.x >> 1) < p.n_n)
+    for (int x = 0; x < p.d && x < 16 * kHdBK; x += kHdBK)
+      asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&p.tm_b)), "r"(x),
+                   "r"(static_cast<int>(p.v0) + static_cast<int>(blockIdx.x >> 1) * p.bn + static_cast<int>(rank) * (p.bn / 2))
+                   : "memory");
   pdl_wait();
   pdl_launch_dependents();
   const int64_t n = *p.n_rows;
@@ -480,6 +541,8 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
     }
   } else if (warp < kHdEpiWarps) {
     const int ew = warp & 3, half = warp >> 2;
+    const uint32_t store_buf = ring + kHdStages * (kHdABytes + kHdBBytes) + warp * kHdStoreBytes;
+    HeadSoft soft{-kHdCap, 0.0f, 0.0f};
     int j = 0;
     for (int64_t i = pair; i < work.total; i += pairs) {
       const HeadTile t = work.tile(i);
@@ -504,11 +567,17 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       const int64_t col0 = static_cast<int64_t>(t.n) * p.bn;
       const int64_t width = OP == kHdScore || OP == kHdDz ? p.cols : p.d;
       const int in_tile = static_cast<int>(min(static_cast<int64_t>(p.bn), width - col0));
-      HeadSoft soft{-kHdCap, 0.0f, 0.0f};
+      if (work.n_m > 1) soft = HeadSoft{-kHdCap, 0.0f, 0.0f};
       // Rows a warp has to visit: those that exist; of dz also the rows up to the
       // end of the third product's last slab, which read as zero.
       const int64_t visit = OP == kHdDw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : n);
       const bool warp_rows = row - lane < visit;
+      if (OP == kHdDw && !p.grad_w_f32 && !p.accumulate) {
+        if (warp_rows)
+          for (int c = half * 64; c < in_tile; c += 128)
+            hd_store_tile(tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * kHdBN + c), store_buf, &p.tm_out,
+                          static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane, lane);
+      } else
 #pragma unroll 1
       for (int c = half * 32; c < p.bn; c += 64) {
         if (!warp_rows || (c >= in_tile && OP != kHdDz)) break;
@@ -566,7 +635,9 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
               for (int q = 0; q < 32; ++q)
                 if (((absent >> q) & 1u) || row >= n) x[q] = 0.0f;
             }
-            if (row < visit) hd_store_bf16(p.dz + row * p.dz_stride + col0 + c, x, 32, false);
+            // (up to the tile's end and the row's; what is there past the piece reads as zero)
+            const int room = static_cast<int>(min(static_cast<int64_t>(p.bn - c), p.dz_stride - col0 - c));
+            if (row < visit) hd_store_dz(p.dz + row * p.dz_stride + col0 + c, x, room);
           }
         } else {
 #pragma unroll
@@ -587,9 +658,11 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       hd_fence_before();
       __syncwarp();
       if (lane == 0) hd_arrive_leader(hd_leader(smem_addr(&acce_bar[buf])));
-      if (OP == kHdScore && row < n)
-        p.part[(static_cast<int64_t>(t.n) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
+      // With one row tile a thread keeps its row's state from tile to tile.
+      if (OP == kHdScore && row < n && (work.n_m > 1 || i + pairs >= work.total))
+        p.part[((work.n_m > 1 ? t.n : pair) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
     }
+    if (OP == kHdDw && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   // The third product without a scored row: the gradient is zero.
   if (OP == kHdDw && n == 0 && !p.accumulate) {
@@ -614,7 +687,8 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 // Numbering the scored rows
 // ---------------------------------------------------------------------------
-constexpr int kHdListThreads = 1024;
+constexpr int kHdListThreads = 512;
+constexpr int64_t kHdListMost = 16384;           // rows that every block counts for itself
 
 struct HeadListParams {
   const int32_t* targets;
@@ -623,21 +697,27 @@ struct HeadListParams {
   const float *lse, *entropy, *g, *gh;     // backward (g, gh nullable)
   int32_t n_sup;
   int32_t sup[DLLM_MAX_SUPPRESS];
-  int32_t* n_rows;
+  int32_t* n_rows;                         // the count, and the splits of the second product
   int32_t* rows;                           // scored row -> row
   int32_t* place;                          // backward: row -> scored row, or -1
   int32_t* target;                         // per scored row
   HeadRow* row;                            // backward: per scored row
   float *o_logprob, *o_entropy, *o_lse;    // forward: rows that are not scored get 0
+  const uint16_t* hidden;
+  int64_t stride, d;
+  uint16_t* packed;
+  int32_t n_d, bn_d, pairs, slabs;         // backward: what decides the splits
+  int64_t room;
+  int32_t* counts;                         // more than kHdListMost rows: the scored rows of each block
 };
 
 // A row of the forward pass is scored when it has a target; in the backward pass
 // it counts when a gradient reaches it (and its log-sum-exp is finite).  A
 // suppressed target has no gradient.
-__device__ __forceinline__ bool hd_row(const HeadListParams& p, int64_t t, HeadRow* out) {
+__device__ __forceinline__ bool hd_row(const HeadListParams& p, int64_t t, HeadRow* out, int32_t* target) {
   const int32_t v = p.targets[t];
-  if (v < 0 || v >= p.V) return false;
-  if (!p.backward) return true;
+  *target = v;
+  if (!p.backward) return v >= 0 && v < p.V;
   HeadRow r;
   r.lse = p.lse[t];
   r.entropy = p.entropy[t];
@@ -646,73 +726,102 @@ __device__ __forceinline__ bool hd_row(const HeadListParams& p, int64_t t, HeadR
   for (int q = 0; q < p.n_sup; ++q)
     if (p.sup[q] == v) r.g = 0.0f;
   *out = r;
-  return isfinite(r.lse) && (r.g != 0.0f || r.gh != 0.0f);
+  return v >= 0 && v < p.V && isfinite(r.lse) && (r.g != 0.0f || r.gh != 0.0f);
 }
 
-__global__ void __launch_bounds__(kHdListThreads) head_list_kernel(const __grid_constant__ HeadListParams p) {
-  __shared__ int32_t sums[32];
+// The rows of a block: at most as many as it has threads.
+__device__ __forceinline__ int64_t hd_first(int64_t T, int64_t b) { return min(T, b * ((T + gridDim.x - 1) / gridDim.x)); }
+
+// More than kHdListMost rows: the scored rows of each block of the next kernel.
+__global__ void __launch_bounds__(kHdListThreads) head_count_kernel(const __grid_constant__ HeadListParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t t = hd_first(p.T, blockIdx.x) + threadIdx.x;
+  HeadRow r{};
+  int32_t v;
+  const bool scored = t < hd_first(p.T, blockIdx.x + 1) && hd_row(p, t, &r, &v);
+  const int total = __syncthreads_count(scored);
+  if (threadIdx.x == 0) p.counts[blockIdx.x] = total;
+}
+
+// Numbers the scored rows in order, block by block, and gathers their hidden
+// states (with rows of zeros up to the next multiple of 64, the third product's K),
+// but for those when every row is scored.  Each block counts the scored rows before
+// its own, and all of them, for itself.
+__global__ void __launch_bounds__(kHdListThreads) head_rows_kernel(const __grid_constant__ HeadListParams p) {
+  __shared__ int32_t warp_sums[kHdListThreads / 32];
+  __shared__ int32_t list[kHdListThreads];
+  __shared__ int32_t before_s, total_s;
+  if (threadIdx.x == 0) before_s = total_s = 0;
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t per = (p.T + kHdListThreads - 1) / kHdListThreads;
-  const int64_t t0 = min(p.T, tid * per), t1 = min(p.T, t0 + per);
+  const int64_t t0 = hd_first(p.T, blockIdx.x), t1 = hd_first(p.T, blockIdx.x + 1);
   HeadRow r{};
-  int32_t count = 0;
-  for (int64_t t = t0; t < t1; ++t) count += hd_row(p, t, &r) ? 1 : 0;
-  int32_t scan = count;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 31) sums[warp] = scan;
-  __syncthreads();
-  if (warp == 0) {
-    int32_t s = sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t v = __shfl_up_sync(0xFFFFFFFFu, s, o);
-      if (lane >= o) s += v;
+  int32_t v, before = 0, total = 0;
+  if (p.counts) {
+    for (int64_t b = tid; b < gridDim.x; b += kHdListThreads) {
+      const int32_t c = p.counts[b];
+      total += c;
+      if (b < blockIdx.x) before += c;
     }
-    sums[lane] = s;
-  }
-  __syncthreads();
-  int32_t at = scan - count + (warp > 0 ? sums[warp - 1] : 0);
-  if (tid == 0) *p.n_rows = sums[31];
-  for (int64_t t = t0; t < t1; ++t) {
-    if (hd_row(p, t, &r)) {
-      p.rows[at] = static_cast<int32_t>(t);
-      p.target[at] = p.targets[t];
-      if (p.backward) {
-        p.row[at] = r;
-        p.place[t] = at;
-      }
-      ++at;
-    } else if (p.backward) {
-      p.place[t] = -1;
-    } else {
-      p.o_logprob[t] = 0.0f;
-      p.o_entropy[t] = 0.0f;
-      p.o_lse[t] = 0.0f;
+  } else {
+#pragma unroll 4
+    for (int64_t t = tid; t < p.T; t += kHdListThreads) {
+      const bool scored = hd_row(p, t, &r, &v);
+      total += scored ? 1 : 0;
+      before += scored && t < t0 ? 1 : 0;
     }
   }
-}
-
-// The scored rows' hidden states one after the other, with rows of zeros up to
-// the next multiple of 64 (the third product's K); nothing when every row is
-// scored.  A warp a row.
-__global__ void __launch_bounds__(256) head_gather_kernel(const uint16_t* hidden, int64_t stride, int64_t T, int64_t d,
-                                                          const int32_t* n_rows, const int32_t* rows, uint16_t* out) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t n = *n_rows;
-  if (n == T) return;
-  const int64_t end = (n + kHdBK - 1) / kHdBK * kHdBK;
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(8) + (threadIdx.x >> 5); i < end; i += static_cast<int64_t>(gridDim.x) * 8) {
-    const uint4* from = i < n ? reinterpret_cast<const uint4*>(hidden + rows[i] * stride) : nullptr;
-    uint4* to = reinterpret_cast<uint4*>(out + i * d);
-    for (int64_t q = lane; q < d / 8; q += 32) to[q] = from ? from[q] : make_uint4(0u, 0u, 0u, 0u);
+  total = __reduce_add_sync(0xFFFFFFFFu, total);
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  if (lane == 0) {
+    atomicAdd(&total_s, total);
+    atomicAdd(&before_s, before);
+  }
+  const int64_t t = t0 + tid;
+  const bool mine = t < t1, scored = mine && hd_row(p, t, &r, &v);
+  const uint32_t vote = __ballot_sync(0xFFFFFFFFu, scored);
+  if (lane == 0) warp_sums[warp] = __popc(vote);
+  __syncthreads();
+  int32_t local = __popc(vote & ((1u << lane) - 1u)), count = 0;
+  for (int w = 0; w < kHdListThreads / 32; ++w) {
+    if (w < warp) local += warp_sums[w];
+    count += warp_sums[w];
+  }
+  const int32_t first = before_s;
+  const int64_t n = total_s;
+  if (scored) {
+    const int32_t at = first + local;
+    list[local] = static_cast<int32_t>(t);
+    p.rows[at] = static_cast<int32_t>(t);
+    p.target[at] = v;
+    if (p.backward) p.row[at] = r;
+  }
+  if (mine && p.backward) p.place[t] = scored ? first + local : -1;
+  if (mine && !p.backward && !scored) {
+    p.o_logprob[t] = 0.0f;
+    p.o_entropy[t] = 0.0f;
+    p.o_lse[t] = 0.0f;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    p.n_rows[0] = static_cast<int32_t>(n);
+    if (p.backward) p.n_rows[1] = hd_splits(n, p.n_d, p.bn_d, p.pairs, p.slabs, p.room);
+  }
+  __syncthreads();
+  if (n == p.T) return;
+  const int64_t vecs = p.d / 8;
+  for (int i = warp; i < count; i += kHdListThreads / 32) {
+    const uint4* from = reinterpret_cast<const uint4*>(p.hidden + list[i] * p.stride);
+    uint4* to = reinterpret_cast<uint4*>(p.packed + (first + i) * p.d);
+#pragma unroll 4
+    for (int64_t q = lane; q < vecs; q += 32) to[q] = __ldcs(from + q);
+  }
+  if (blockIdx.x == 0) {
+    const int64_t end = (n + kHdBK - 1) / kHdBK * kHdBK;
+    for (int64_t i = n + warp; i < end; i += kHdListThreads / 32)
+      for (int64_t q = lane; q < vecs; q += 32) reinterpret_cast<uint4*>(p.packed + i * p.d)[q] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -723,7 +832,7 @@ struct HeadFinishParams {
   const int32_t *n_rows, *rows, *target;
   const float4* part;
   int64_t part_rows;
-  int32_t parts;
+  int32_t parts, pairs;          // of a row: 2 for each tile along N, or for each pair where there is one row tile
   const float* z_target;
   int32_t n_sup;
   int32_t sup[DLLM_MAX_SUPPRESS];
@@ -738,11 +847,13 @@ __global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = *p.n_rows;
+  const int parts = n > kHdBM ? p.parts : min(p.parts, 2 * p.pairs);
   for (int64_t base = blockIdx.x * static_cast<int64_t>(32); base < n; base += static_cast<int64_t>(gridDim.x) * 32) {
     const int64_t row = base + lane;
     HeadSoft a{-kHdCap, 0.0f, 0.0f};
     if (row < n)
-      for (int q = warp; q < p.parts; q += 32) {
+#pragma unroll 4
+      for (int q = warp; q < parts; q += 32) {
         const float4 v = p.part[q * p.part_rows + row];
         hd_join(a, HeadSoft{v.x, v.y, v.z});
       }
@@ -764,27 +875,26 @@ __global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant
 
 // grad_hidden from the second product's parts, added in order: a block a row.
 __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, const int32_t* place, const float* acc,
-                                                      int64_t acc_stride, int32_t n_n, int32_t pairs, int32_t slabs,
-                                                      int64_t T, int64_t d, uint16_t* out, int64_t out_stride) {
+                                                      int64_t acc_stride, int64_t d, uint16_t* out, int64_t out_stride) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t n = *n_rows;
-  const int splits = hd_splits(n, n_n, pairs, slabs);
+  const int64_t n = n_rows[0], t = blockIdx.x;
+  const int splits = n_rows[1];
   const int64_t step = (n + kHdBM - 1) / kHdBM * kHdBM * acc_stride;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const int32_t row = place[t];
-    for (int64_t c = threadIdx.x * 8; c < d; c += 256 * 8) {
-      float y[8] = {};
-      if (row >= 0)
-        for (int s = 0; s < splits; ++s) {
-          const float4* at = reinterpret_cast<const float4*>(acc + s * step + row * acc_stride + c);
-          const float4 a = at[0], b = at[1];
-          y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
-          y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
-        }
-      *reinterpret_cast<uint4*>(out + t * out_stride + c) =
-          make_uint4(hd_bf16x2(y[0], y[1]), hd_bf16x2(y[2], y[3]), hd_bf16x2(y[4], y[5]), hd_bf16x2(y[6], y[7]));
+  const int32_t row = place[t];
+  for (int64_t c = threadIdx.x * 8; c < d; c += 256 * 8) {
+    float y[8] = {};
+    if (row >= 0) {
+      const float* from = acc + row * acc_stride + c;
+#pragma unroll 8
+      for (int s = 0; s < splits; ++s, from += step) {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(from)), b = __ldcs(reinterpret_cast<const float4*>(from) + 1);
+        y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
+        y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
+      }
     }
+    *reinterpret_cast<uint4*>(out + t * out_stride + c) =
+        make_uint4(hd_bf16x2(y[0], y[1]), hd_bf16x2(y[2], y[3]), hd_bf16x2(y[4], y[5]), hd_bf16x2(y[6], y[7]));
   }
 }
 
@@ -855,7 +965,8 @@ struct HdPlan {
   int32_t bn_d, n_d;    // along d
   int64_t piece;        // ids of a piece
   int64_t acc;          // floats of the second product's parts
-  size_t rows, target, place, row, z_target, hidden, part, dz, accs, bytes;   // offsets, size
+  int64_t list_blocks;  // of the kernel that numbers the rows
+  size_t rows, target, place, row, z_target, hidden, part, dz, accs, counts, bytes;   // offsets, size
 };
 
 constexpr int64_t kPieceElements = int64_t{1} << 28;  // of dz: 512 MB
@@ -870,18 +981,35 @@ HdPlan hd_plan(int64_t T, int64_t V, int64_t d, int64_t sms, bool backward) {
     piece = round_up((V + pieces - 1) / pieces, kHdBN);
   }
   h.piece = piece;
+  // One row tile: the width in [128, 256] with which the busiest pair has the fewest
+  // ids (the weight's bytes are what such a call costs); else whole tiles.
   h.bn_v = kHdBN;
-  h.n_v = static_cast<int32_t>(piece / kHdBN);
+  if (h.t_pad == kHdBM) {
+    const int64_t pairs = std::max<int64_t>(1, sms / 2);
+    int64_t least = INT64_MAX;
+    for (int32_t bn = kHdBN; bn >= 128; bn -= 16) {
+      const int64_t cost = ((V + bn - 1) / bn + pairs - 1) / pairs * bn;
+      if (cost < least) {
+        least = cost;
+        h.bn_v = bn;
+      }
+    }
+  }
+  h.n_v = static_cast<int32_t>((std::min(piece, V) + h.bn_v - 1) / h.bn_v);
   h.n_d = static_cast<int32_t>((d + kHdBN - 1) / kHdBN);
   h.bn_d = static_cast<int32_t>(round_up((d + h.n_d - 1) / h.n_d, 128));
   h.n_d = static_cast<int32_t>((d + h.bn_d - 1) / h.bn_d);
-  h.acc = std::max<int64_t>(h.t_pad * h.n_d * h.bn_d, sms * kHdBM * kHdBN);
+  const int64_t one = h.t_pad * h.n_d * h.bn_d;
+  h.acc = std::max<int64_t>({one, std::min<int64_t>(8 * one, int64_t{1} << 25), sms / 2 * kHdBM * kHdBN});
   size_t at = 256;
   auto take = [&at](int64_t bytes) {
     const size_t here = at;
     at += static_cast<size_t>(round_up(bytes, 256));
     return here;
   };
+  h.list_blocks = T <= kHdListMost ? std::min<int64_t>((T + 15) / 16, std::max<int64_t>(304, (T + kHdListThreads - 1) / kHdListThreads))
+                                   : (T + kHdListThreads - 1) / kHdListThreads;
+  h.counts = take(4 * h.list_blocks);
   h.rows = take(4 * T);
   h.target = take(4 * T);
   h.hidden = take(2 * d * round_up(T, kHdBK));
@@ -932,14 +1060,15 @@ dllm_status hd_launch(HeadParams& p, int sms, dllm_stream_t stream) {
                     stream, args, 2);
 }
 
-dllm_status hd_gather(const void* hidden, int64_t stride, int64_t T, int64_t d, const int32_t* n_rows, const int32_t* rows,
-                      uint8_t* packed, int sms, dllm_stream_t stream) {
-  const uint16_t* from = static_cast<const uint16_t*>(hidden);
-  uint16_t* to = reinterpret_cast<uint16_t*>(packed);
-  void* args[] = {&from, &stride, &T, &d, &n_rows, &rows, &to};
-  const int64_t blocks = std::min<int64_t>((T + 7) / 8 + 8, sms * 8);
-  return launch_pdl(reinterpret_cast<const void*>(&head_gather_kernel), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
-                    args);
+dllm_status hd_list(HeadListParams& l, const HdPlan& h, uint8_t* ws, dllm_stream_t stream) {
+  const dim3 grid(static_cast<unsigned>(h.list_blocks)), block(kHdListThreads);
+  void* args[] = {&l};
+  if (l.T > kHdListMost) {
+    l.counts = reinterpret_cast<int32_t*>(ws + h.counts);
+    const dllm_status st = launch_pdl(reinterpret_cast<const void*>(&head_count_kernel), grid, block, 0, stream, args);
+    if (st != DLLM_OK) return st;
+  }
+  return launch_pdl(reinterpret_cast<const void*>(&head_rows_kernel), grid, block, 0, stream, args);
 }
 
 }  // namespace
@@ -948,13 +1077,14 @@ extern "C" {
 
 size_t dllm_lm_head_logprobs_workspace_size(int64_t T, int64_t V, int64_t d) {
   if (T <= 0 || V <= 0 || d <= 0 || T > kHdMaxT || V > INT32_MAX || d > kHdMaxD) return 256;
-  return hd_plan(T, V, d, 0, false).bytes;
+  const HdDevice* dev = hd_device();
+  return hd_plan(T, V, d, dev ? dev->sms : 152, false).bytes;
 }
 
 size_t dllm_lm_head_logprobs_backward_workspace_size(int64_t T, int64_t V, int64_t d) {
   if (T <= 0 || V <= 0 || d <= 0 || T > kHdMaxT || V > INT32_MAX || d > kHdMaxD) return 256;
   const HdDevice* dev = hd_device();
-  return hd_plan(T, V, d, dev ? dev->sms : 1024, true).bytes;
+  return hd_plan(T, V, d, dev ? dev->sms : 152, true).bytes;
 }
 
 dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride, const void* weight,
@@ -1014,6 +1144,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   f.part = p.part;
   f.part_rows = h.t_pad;
   f.parts = 2 * h.n_v;
+  f.pairs = dev->sms / 2;
   f.z_target = p.z_target;
   f.n_sup = p.n_sup;
   std::copy(sup.begin(), sup.end(), f.sup);
@@ -1022,10 +1153,11 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   f.entropy = entropy;
   f.lse = lse;
 
-  void* largs[] = {&l};
-  st = launch_pdl(reinterpret_cast<const void*>(&head_list_kernel), dim3(1), dim3(kHdListThreads), 0, stream, largs);
-  if (st != DLLM_OK) return st;
-  st = hd_gather(hidden, hidden_stride, T, d, n_rows, l.rows, ws + h.hidden, dev->sms, stream);
+  l.hidden = static_cast<const uint16_t*>(hidden);
+  l.stride = hidden_stride;
+  l.d = d;
+  l.packed = reinterpret_cast<uint16_t*>(ws + h.hidden);
+  st = hd_list(l, h, ws, stream);
   if (st != DLLM_OK) return st;
   st = hd_launch<kHdScore>(p, dev->sms, stream);
   if (st != DLLM_OK) return st;
@@ -1112,7 +1244,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
       !make_map(&pz.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v / 2)) ||
       !make_map(&ph.tm_a, p.dz, h.t_pad, h.piece, h.piece, kHdRows) || !make_map(&ph.tm_b, weight, V, d, weight_stride, 64) ||
       !make_map(&pw.tm_a, p.dz, h.t_pad, h.piece, h.piece, 64) || !make_map(&pw.tm_b, hidden, T, d, hidden_stride, 64) ||
-      !make_map(&pw.tm_packed, ws + h.hidden, packed_rows, d, d, 64))
+      !make_map(&pw.tm_packed, ws + h.hidden, packed_rows, d, d, 64) ||
+      (grad_weight && grad_weight_dt == DLLM_BF16 && !make_map(&pw.tm_out, grad_weight, V, d, grad_weight_stride, 32)))
     return DLLM_ERR_CUDA;
   pz.bn = h.bn_v;
   pz.n_n = h.n_v;
@@ -1123,12 +1256,17 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   ph.idesc = hd_idesc(kHdDh, h.bn_d);
   pw.idesc = hd_idesc(kHdDw, h.bn_d);
   ph.a_bytes = pw.a_bytes = kHdABytes;
-  ph.split_slabs = static_cast<int32_t>((std::min(h.piece, V) + kHdBK - 1) / kHdBK);
 
-  void* largs[] = {&l};
-  st = launch_pdl(reinterpret_cast<const void*>(&head_list_kernel), dim3(1), dim3(kHdListThreads), 0, stream, largs);
-  if (st != DLLM_OK) return st;
-  st = hd_gather(hidden, hidden_stride, T, d, n_rows, l.rows, ws + h.hidden, dev->sms, stream);
+  l.hidden = static_cast<const uint16_t*>(hidden);
+  l.stride = hidden_stride;
+  l.d = d;
+  l.packed = reinterpret_cast<uint16_t*>(ws + h.hidden);
+  l.n_d = h.n_d;
+  l.bn_d = h.bn_d;
+  l.pairs = dev->sms / 2;
+  l.slabs = static_cast<int32_t>((std::min(h.piece, V) + kHdBK - 1) / kHdBK);
+  l.room = h.acc;
+  st = hd_list(l, h, ws, stream);
   if (st != DLLM_OK) return st;
   for (int64_t v0 = 0; v0 < V; v0 += h.piece) {
     const int64_t cols = std::min(h.piece, V - v0);
@@ -1137,7 +1275,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
       q->cols = cols;
       q->add = v0 > 0 ? 1 : 0;
     }
-    pz.n_n = static_cast<int32_t>((cols + kHdBN - 1) / kHdBN);
+    // (to the end of the second product's last slab, where dz reads as zero)
+    pz.n_n = static_cast<int32_t>((round_up(cols, kHdBK) + h.bn_v - 1) / h.bn_v);
     st = hd_launch<kHdDz>(pz, dev->sms, stream);
     if (st == DLLM_OK && grad_hidden) st = hd_launch<kHdDh>(ph, dev->sms, stream);
     if (st == DLLM_OK && grad_weight) st = hd_launch<kHdDw>(pw, dev->sms, stream);
@@ -1147,11 +1286,9 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   const float* acc = p.acc;
   uint16_t* out = static_cast<uint16_t*>(grad_hidden);
   const int32_t* place = l.place;
-  int32_t n_n = h.n_d, pairs = dev->sms / 2, slabs = ph.split_slabs;
   int64_t stride = p.acc_stride;
-  void* args[] = {&n_rows, &place, &acc, &stride, &n_n, &pairs, &slabs, &T, &d, &out, &grad_hidden_stride};
-  return launch_pdl(reinterpret_cast<const void*>(&head_dh_kernel), dim3(static_cast<unsigned>(std::min<int64_t>(T, dev->sms * 8))),
-                    dim3(256), 0, stream, args);
+  void* args[] = {&n_rows, &place, &acc, &stride, &d, &out, &grad_hidden_stride};
+  return launch_pdl(reinterpret_cast<const void*>(&head_dh_kernel), dim3(static_cast<unsigned>(T)), dim3(256), 0, stream, args);
 }
 
 }  // extern "C"
