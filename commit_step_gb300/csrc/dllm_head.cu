@@ -44,16 +44,18 @@ constexpr int kHdBM = 256;                       // rows of a pair's accumulator
 constexpr int kHdRows = kHdBM / 2;               // a CTA's
 constexpr int kHdBN = 256;                       // its columns at most
 constexpr int kHdBK = 64;                        // K of a stage: one 128-byte swizzle row of bf16
-constexpr int kHdABytes = kHdRows * kHdBK * 2;   // 16 KB
+constexpr int kHdABytes = kHdRows * kHdBK * 2;   // 16 KB: a CTA's part of a slab of A, whole
 constexpr int kHdBBytes = kHdBN / 2 * kHdBK * 2; // 16 KB
-constexpr int kHdStages = 6;
+constexpr int kHdMaxStages = 16;                 // of the ring; 7 of 32 KB, 6 where tiles are stored by TMA, more where
+                                                 // few rows leave A small (the weight's bytes in flight are what counts then)
 constexpr int kHdEpiWarps = 8;                   // two warpgroups, each reads every other 32-column chunk of a tile
 constexpr int kHdTmaWarp = 10;
 constexpr int kHdMmaWarp = 11;
 constexpr int kHdThreads = 12 * 32;
 constexpr int kHdTmemCols = 512;
 constexpr int kHdStoreBytes = 32 * 64 * 2;       // a warp's 32 rows of 64 bf16 columns on their way out
-constexpr int kHdSmem = kHdStages * (kHdABytes + kHdBBytes) + kHdEpiWarps * kHdStoreBytes + 1024;
+constexpr int kHdRing = 7 * (kHdABytes + kHdBBytes);
+constexpr int kHdSmem = kHdRing + 1024;
 constexpr int kHdBand = 16;                      // row tiles that share a pass over the vocabulary (4096 rows: 32 MB of
                                                  // hidden states of 4096 stay in L2 while the weight streams)
 constexpr float kHdCap = 0x1p+125f;              // logits are read within +-2^125 (NaN as the lowest): differences stay finite
@@ -79,6 +81,8 @@ struct HeadParams {
   int32_t n_n;                   // tiles along N
   uint32_t idesc;
   uint32_t a_bytes;              // what a CTA's load of A brings
+  uint32_t a_room, stage_bytes;  // a stage: A's rows (whole swizzle atoms), then B
+  int32_t stages;
   const int32_t* target;         // per scored row
   int32_t n_sup;
   int32_t sup[DLLM_MAX_SUPPRESS];
@@ -404,7 +408,7 @@ __device__ __forceinline__ void hd_store_f32(float* out, const float (&x)[32], i
 template <int OP>
 __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_constant__ HeadParams p) {
   extern __shared__ __align__(1024) uint8_t hd_smem[];
-  __shared__ __align__(8) uint64_t full_bar[kHdStages], empty_bar[kHdStages], accf_bar[2], acce_bar[2];
+  __shared__ __align__(8) uint64_t full_bar[kHdMaxStages], empty_bar[kHdMaxStages], accf_bar[2], acce_bar[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t abort_flag_s;
   __shared__ int32_t sup_s[DLLM_MAX_SUPPRESS];
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   // warps of both) are waited for by the leader's products; empty and accf are
   // arrived at in both CTAs by the products.
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kHdStages; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(smem_addr(&full_bar[s]), 1);
       mbar_init(smem_addr(&empty_bar[s]), 1);
     }
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
             break;
           }
           const uint32_t bar = hd_leader(smem_addr(&full_bar[s]));
-          const uint32_t a = ring + static_cast<uint32_t>(s) * (kHdABytes + kHdBBytes), b = a + kHdABytes;
+          const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes, b = a + p.a_room;
           if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full_bar[s]), tx);
           if (rank == 0 || second) {
             if (hd_a_mn(OP)) {
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
             for (int x = 0; x < half; x += 64) hd_load(b + x * 128, mb, n0 + x, y, bar);
           }
           ++issued;
-          if (++s == kHdStages) {
+          if (++s == p.stages) {
             s = 0;
             ph ^= 1u;
           }
@@ -501,8 +505,8 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       }
       // Giving up: the copies still in flight land before the CTA ends.
       if (*abort_flag && rank == 0)
-        for (int64_t q = issued > kHdStages ? issued - kHdStages : 0; q < issued; ++q)
-          mbar_wait_bounded(smem_addr(&full_bar[q % kHdStages]), static_cast<uint32_t>((q / kHdStages) & 1));
+        for (int64_t q = issued > p.stages ? issued - p.stages : 0; q < issued; ++q)
+          mbar_wait_bounded(smem_addr(&full_bar[q % p.stages]), static_cast<uint32_t>((q / p.stages) & 1));
     }
   } else if (warp == kHdMmaWarp) {
     if (lane == 0 && rank == 0) {
@@ -524,13 +528,13 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
             break;
           }
           hd_fence_after();
-          const uint32_t a = ring + static_cast<uint32_t>(s) * (kHdABytes + kHdBBytes), b = a + kHdABytes;
+          const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes, b = a + p.a_room;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes of a K-major row, 16 rows of 128 bytes MN-major
             hd_mma(d_tmem, hd_desc(a + kk * (hd_a_mn(OP) ? 2048 : 32), 8192), hd_desc(b + kk * (hd_b_mn(OP) ? 2048 : 32), 8192),
                    p.idesc, k != t.k0 || kk != 0 ? 1u : 0u);
           hd_commit(smem_addr(&empty_bar[s]));
-          if (++s == kHdStages) {
+          if (++s == p.stages) {
             s = 0;
             ph ^= 1u;
           }
@@ -541,7 +545,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
     }
   } else if (warp < kHdEpiWarps) {
     const int ew = warp & 3, half = warp >> 2;
-    const uint32_t store_buf = ring + kHdStages * (kHdABytes + kHdBBytes) + warp * kHdStoreBytes;
+    const uint32_t store_buf = ring + kHdRing - (kHdEpiWarps - warp) * kHdStoreBytes;   // (dw: behind the last stage)
     HeadSoft soft{-kHdCap, 0.0f, 0.0f};
     int j = 0;
     for (int64_t i = pair; i < work.total; i += pairs) {
@@ -812,11 +816,20 @@ __global__ void __launch_bounds__(kHdListThreads) head_rows_kernel(const __grid_
   __syncthreads();
   if (n == p.T) return;
   const int64_t vecs = p.d / 8;
-  for (int i = warp; i < count; i += kHdListThreads / 32) {
+  // A unit is a row's 128 vectors, four a lane.
+  const int per_row = static_cast<int>((vecs + 127) / 128);
+  for (int u = warp; u < count * per_row; u += kHdListThreads / 32) {
+    const int i = u / per_row;
+    const int64_t q = static_cast<int64_t>(u - i * per_row) * 128 + lane;
     const uint4* from = reinterpret_cast<const uint4*>(p.hidden + list[i] * p.stride);
     uint4* to = reinterpret_cast<uint4*>(p.packed + (first + i) * p.d);
-#pragma unroll 4
-    for (int64_t q = lane; q < vecs; q += 32) to[q] = __ldcs(from + q);
+    uint4 x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (q + 32 * e < vecs) x[e] = __ldcs(from + q + 32 * e);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (q + 32 * e < vecs) to[q + 32 * e] = x[e];
   }
   if (blockIdx.x == 0) {
     const int64_t end = (n + kHdBK - 1) / kHdBK * kHdBK;
@@ -873,28 +886,58 @@ __global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant
   }
 }
 
-// grad_hidden from the second product's parts, added in order: a block a row.
+// grad_hidden from the second product's parts, added in a fixed order.  A block
+// makes 2048 columns of a row: with few splits a thread 8 of them; with many the
+// warps share the splits of 256 columns at a time and meet in shared memory.
+constexpr int kHdJoinMany = 4;
+
+__device__ __forceinline__ void hd_add8(float (&y)[8], const float* from) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(from)), b = __ldcs(reinterpret_cast<const float4*>(from) + 1);
+  y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
+  y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
+}
+
+__device__ __forceinline__ void hd_put8(uint16_t* at, const float (&y)[8]) {
+  *reinterpret_cast<uint4*>(at) =
+      make_uint4(hd_bf16x2(y[0], y[1]), hd_bf16x2(y[2], y[3]), hd_bf16x2(y[4], y[5]), hd_bf16x2(y[6], y[7]));
+}
+
 __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, const int32_t* place, const float* acc,
                                                       int64_t acc_stride, int64_t d, uint16_t* out, int64_t out_stride) {
+  __shared__ float part[8][8][33];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t n = n_rows[0], t = blockIdx.x;
-  const int splits = n_rows[1];
+  const int64_t n = n_rows[0], t = blockIdx.x, c0 = blockIdx.y * static_cast<int64_t>(2048);
+  const int splits = n_rows[1], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = (n + kHdBM - 1) / kHdBM * kHdBM * acc_stride;
   const int32_t row = place[t];
-  for (int64_t c = threadIdx.x * 8; c < d; c += 256 * 8) {
+  const float* from = acc + static_cast<int64_t>(row) * acc_stride;
+  uint16_t* to = out + t * out_stride;
+  if (row < 0 || splits < kHdJoinMany) {
+    const int64_t c = c0 + threadIdx.x * 8;
+    if (c >= d) return;
     float y[8] = {};
-    if (row >= 0) {
-      const float* from = acc + row * acc_stride + c;
-#pragma unroll 8
-      for (int s = 0; s < splits; ++s, from += step) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(from)), b = __ldcs(reinterpret_cast<const float4*>(from) + 1);
-        y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
-        y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
-      }
+    if (row >= 0)
+      for (int s = 0; s < splits; ++s) hd_add8(y, from + s * step + c);
+    hd_put8(to + c, y);
+    return;
+  }
+  for (int64_t b = c0; b < d && b < c0 + 2048; b += 256) {
+    const int64_t c = b + lane * 8;
+    float y[8] = {};
+    if (c < d)
+#pragma unroll 4
+      for (int s = warp; s < splits; s += 8) hd_add8(y, from + s * step + c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[warp][e][lane] = y[e];
+    __syncthreads();
+    if (warp == 0 && c < d) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        for (int w = 1; w < 8; ++w) y[e] += part[w][e][lane];
+      hd_put8(to + c, y);
     }
-    *reinterpret_cast<uint4*>(out + t * out_stride + c) =
-        make_uint4(hd_bf16x2(y[0], y[1]), hd_bf16x2(y[2], y[3]), hd_bf16x2(y[4], y[5]), hd_bf16x2(y[6], y[7]));
+    __syncthreads();
   }
 }
 
@@ -1053,6 +1096,16 @@ dllm_status hd_check(const void* hidden, int64_t T, int64_t d, int64_t hidden_st
   return DLLM_OK;
 }
 
+// A stage holds the rows of A that exist and B's share of a tile.  (The products
+// read a whole A: what lies past the last stage's rows has to be in the ring.)
+void hd_ring(HeadParams& p, int op, int32_t a_rows) {
+  p.a_bytes = static_cast<uint32_t>(a_rows) * kHdBK * 2;
+  p.a_room = static_cast<uint32_t>(round_up(p.a_bytes, 1024));
+  p.stage_bytes = p.a_room + static_cast<uint32_t>(round_up(p.bn / 2 * kHdBK * 2, 1024));
+  const int32_t room = kHdRing - (op == kHdDw ? kHdEpiWarps * kHdStoreBytes : kHdABytes - static_cast<int32_t>(p.a_room));
+  p.stages = std::min(kHdMaxStages, room / static_cast<int32_t>(p.stage_bytes));
+}
+
 template <int OP>
 dllm_status hd_launch(HeadParams& p, int sms, dllm_stream_t stream) {
   void* args[] = {&p};
@@ -1128,7 +1181,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   p.bn = h.bn_v;
   p.n_n = h.n_v;
   p.idesc = hd_idesc(kHdScore, h.bn_v);
-  p.a_bytes = a_rows * kHdBK * 2;
+  hd_ring(p, kHdScore, static_cast<int32_t>(a_rows));
   p.target = l.target;
   p.n_sup = static_cast<int32_t>(sup.size());
   std::copy(sup.begin(), sup.end(), p.sup);
@@ -1242,7 +1295,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   if (!make_map(&pz.tm_a, hidden, T, d, hidden_stride, a_rows) ||
       !make_map(&pz.tm_packed, ws + h.hidden, packed_rows, d, d, a_rows) ||
       !make_map(&pz.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v / 2)) ||
-      !make_map(&ph.tm_a, p.dz, h.t_pad, h.piece, h.piece, kHdRows) || !make_map(&ph.tm_b, weight, V, d, weight_stride, 64) ||
+      !make_map(&ph.tm_a, p.dz, h.t_pad, h.piece, h.piece, a_rows) || !make_map(&ph.tm_b, weight, V, d, weight_stride, 64) ||
       !make_map(&pw.tm_a, p.dz, h.t_pad, h.piece, h.piece, 64) || !make_map(&pw.tm_b, hidden, T, d, hidden_stride, 64) ||
       !make_map(&pw.tm_packed, ws + h.hidden, packed_rows, d, d, 64) ||
       (grad_weight && grad_weight_dt == DLLM_BF16 && !make_map(&pw.tm_out, grad_weight, V, d, grad_weight_stride, 32)))
@@ -1250,12 +1303,13 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   pz.bn = h.bn_v;
   pz.n_n = h.n_v;
   pz.idesc = hd_idesc(kHdDz, h.bn_v);
-  pz.a_bytes = a_rows * kHdBK * 2;
+  hd_ring(pz, kHdDz, static_cast<int32_t>(a_rows));
   ph.bn = pw.bn = h.bn_d;
   ph.n_n = pw.n_n = h.n_d;
   ph.idesc = hd_idesc(kHdDh, h.bn_d);
   pw.idesc = hd_idesc(kHdDw, h.bn_d);
-  ph.a_bytes = pw.a_bytes = kHdABytes;
+  hd_ring(ph, kHdDh, static_cast<int32_t>(a_rows));
+  hd_ring(pw, kHdDw, kHdRows);
 
   l.hidden = static_cast<const uint16_t*>(hidden);
   l.stride = hidden_stride;
@@ -1288,7 +1342,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   const int32_t* place = l.place;
   int64_t stride = p.acc_stride;
   void* args[] = {&n_rows, &place, &acc, &stride, &d, &out, &grad_hidden_stride};
-  return launch_pdl(reinterpret_cast<const void*>(&head_dh_kernel), dim3(static_cast<unsigned>(T)), dim3(256), 0, stream, args);
+  return launch_pdl(reinterpret_cast<const void*>(&head_dh_kernel), dim3(static_cast<unsigned>(T), static_cast<unsigned>((d + 2047) / 2048)),
+                    dim3(256), 0, stream, args);
 }
 
 }  // extern "C"
