@@ -113,13 +113,16 @@ constexpr uint32_t hd_idesc(int op, int bn) {
 }
 
 // Shared-memory descriptor in the 128-byte swizzle: start / 16 in bits 0-13, the
-// leading offset / 16 in bits 16-29 (MN-major: the distance of spans of 64 along
-// M or N; K-major: unused), the stride offset / 16 in bits 32-45 (1024 bytes, 8
+// leading offset / 16 in bits 16-29 (MN-major: the distance of spans of 64 along M
+// or N; K-major: unused), the stride offset / 16 in bits 32-45 (1024 bytes, 8
 // rows of 128), version 1 at bit 46, swizzle 2 at bits 61-63.
-__device__ __forceinline__ uint64_t hd_desc(uint32_t addr, uint32_t leading) {
-  const uint32_t lo = ((addr & 0x3FFFFu) >> 4) | (leading >> 4) << 16;
-  const uint32_t hi = (1024u >> 4) | 1u << 14 | 2u << 29;
-  return static_cast<uint64_t>(hi) << 32 | lo;
+__device__ __forceinline__ uint32_t hd_desc(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (8192u >> 4) << 16; }
+constexpr uint32_t kHdDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ uint32_t hd_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
 
 // A load of this CTA's shared memory that counts on the leader's barrier.
@@ -131,19 +134,25 @@ __device__ __forceinline__ void hd_load(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
-__device__ __forceinline__ void hd_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Issued by the one thread of the warp whose `lead` is set; the whole warp executes
+// the code around it, so that addresses and descriptors stay in uniform registers
+// (formed by a single thread, they held a slab up to 335 ns, whatever its width:
+// 32 x 126464 x 4096 took 187 us, and [BLOCK] so).
+__device__ __forceinline__ void hd_mma(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kHdDescHigh), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
 
 // Arrives on the barrier at this place of both CTAs when the products issued so far are done.
-__device__ __forceinline__ void hd_commit(uint32_t bar) {
+__device__ __forceinline__ void hd_commit(uint32_t lead, uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3)), "r"(lead)
       : "memory");
 }
 
@@ -183,24 +192,12 @@ __device__ __forceinline__ void hd_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 
-__device__ __forceinline__ bool hd_try_wait(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(hint_ns)
-      : "memory");
-  return ok != 0;
-}
-
 // A bounded wait: false after the deadline or once the CTA gave up.
 __device__ __forceinline__ bool hd_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag) {
-  if (hd_try_wait(bar, parity, kSleepHintNs)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (hd_try_wait(bar, parity, kSleepHintNs)) return true;
+    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > kWaitLimitCycles) return false;
   }
@@ -509,37 +506,41 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
           mbar_wait_bounded(smem_addr(&full_bar[q % p.stages]), static_cast<uint32_t>((q / p.stages) & 1));
     }
   } else if (warp == kHdMmaWarp) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const uint32_t lead = hd_elect();
       int s = 0, j = 0;
       uint32_t ph = 0;
-      for (int64_t i = pair; i < work.total && !*abort_flag; i += pairs) {
+      bool ok = true;
+      for (int64_t i = pair; i < work.total && ok; i += pairs) {
         const HeadTile t = work.tile(i);
         if (t.k0 == t.k1) continue;
         const int buf = j & 1;
-        if (!hd_wait(smem_addr(&acce_bar[buf]), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag)) {
-          hd_fail(p, abort_flag, kFaultEmptyWait);
+        if (!__all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&acce_bar[buf]), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag))) {
+          if (lane == 0) hd_fail(p, abort_flag, kFaultEmptyWait);
           break;
         }
         hd_fence_after();
         const uint32_t d_tmem = tmem + static_cast<uint32_t>(buf * kHdBN);
         for (int k = t.k0; k < t.k1; ++k) {
-          if (!hd_wait(smem_addr(&full_bar[s]), ph, abort_flag)) {
-            hd_fail(p, abort_flag, kFaultFullWait);
+          ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&full_bar[s]), ph, abort_flag));
+          if (!ok) {
+            if (lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
             break;
           }
           hd_fence_after();
-          const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes, b = a + p.a_room;
+          const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes;
+          const uint32_t da = hd_desc(a), db = hd_desc(a + p.a_room);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes of a K-major row, 16 rows of 128 bytes MN-major
-            hd_mma(d_tmem, hd_desc(a + kk * (hd_a_mn(OP) ? 2048 : 32), 8192), hd_desc(b + kk * (hd_b_mn(OP) ? 2048 : 32), 8192),
-                   p.idesc, k != t.k0 || kk != 0 ? 1u : 0u);
-          hd_commit(smem_addr(&empty_bar[s]));
+            hd_mma(lead, d_tmem, da + kk * ((hd_a_mn(OP) ? 2048 : 32) >> 4), db + kk * ((hd_b_mn(OP) ? 2048 : 32) >> 4), p.idesc,
+                   k != t.k0 || kk != 0 ? 1u : 0u);
+          hd_commit(lead, smem_addr(&empty_bar[s]));
           if (++s == p.stages) {
             s = 0;
             ph ^= 1u;
           }
         }
-        hd_commit(smem_addr(&accf_bar[buf]));
+        hd_commit(lead, smem_addr(&accf_bar[buf]));
         ++j;
       }
     }
