@@ -221,19 +221,16 @@ __device__ __forceinline__ uint32_t hd_bf16x2(float lo, float hi) {
 // pairs can be kept busy with, against 8 bytes a split of every element written and
 // read again (1.5 MB in the time of a slab of 256 x 256 x 64).  32 tiles of 1976
 // slabs on 76 pairs: 7 splits, 3 full rounds (2 splits leave 12 pairs idle).
+// Called by a whole warp, a lane a number of splits.
 __device__ __forceinline__ int hd_splits(int64_t n, int n_n, int bn, int pairs, int slabs, int64_t room) {
-  const int64_t tiles = (n + kHdBM - 1) / kHdBM * n_n, size = tiles * kHdBM * bn;
-  int best = 1;
-  float least = 3.4e38f;
-  for (int s = 1; s <= 32 && s <= slabs && (s == 1 || s * size <= room); ++s) {
-    const float cost = static_cast<float>((tiles * s + pairs - 1) / pairs) * static_cast<float>((slabs + s - 1) / s) * (bn / 256.0f) +
-                       static_cast<float>(s) * static_cast<float>(size) * (8.0f / 1.5e6f);
-    if (cost < least) {
-      least = cost;
-      best = s;
-    }
-  }
-  return best;
+  const int s = (threadIdx.x & 31) + 1;
+  const int tiles = static_cast<int>((n + kHdBM - 1) / kHdBM) * n_n;
+  const float size = static_cast<float>(tiles) * static_cast<float>(kHdBM * bn);
+  const float rounds = ceilf(static_cast<float>(tiles) * s / static_cast<float>(pairs));
+  float cost = rounds * ceilf(static_cast<float>(slabs) / s) * (bn / 256.0f) + s * size * (8.0f / 1.5e6f);
+  if (s > 1 && (s > slabs || static_cast<int64_t>(s) * tiles * kHdBM * bn > room)) cost = 3.0e38f;
+  const float least = -warp_max_f32(-cost);
+  return __ffs(__ballot_sync(0xFFFFFFFFu, cost == least));
 }
 
 // The tiles of a product and the order in which the pairs of CTAs take them (tile i
@@ -810,9 +807,12 @@ __global__ void __launch_bounds__(kHdListThreads) head_rows_kernel(const __grid_
     p.o_entropy[t] = 0.0f;
     p.o_lse[t] = 0.0f;
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    p.n_rows[0] = static_cast<int32_t>(n);
-    if (p.backward) p.n_rows[1] = hd_splits(n, p.n_d, p.bn_d, p.pairs, p.slabs, p.room);
+  if (blockIdx.x == 0 && warp == 0) {
+    const int splits = p.backward ? hd_splits(n, p.n_d, p.bn_d, p.pairs, p.slabs, p.room) : 1;
+    if (lane == 0) {
+      p.n_rows[0] = static_cast<int32_t>(n);
+      p.n_rows[1] = splits;
+    }
   }
   __syncthreads();
   if (n == p.T) return;
@@ -854,27 +854,33 @@ struct HeadFinishParams {
   float *logprob, *entropy, *lse;
 };
 
-// 32 rows a block: a lane a row, the warps share its partials.
+// 32 rows a block: first a lane a row, the warps sharing its partials, then a warp a
+// row, its lanes joining what the warps have.
 __global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant__ HeadFinishParams p) {
-  __shared__ HeadSoft s[32][33];
+  __shared__ float sm[32][33], sz[32][33], ss[32][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = *p.n_rows;
   const int parts = n > kHdBM ? p.parts : min(p.parts, 2 * p.pairs);
   for (int64_t base = blockIdx.x * static_cast<int64_t>(32); base < n; base += static_cast<int64_t>(gridDim.x) * 32) {
-    const int64_t row = base + lane;
     HeadSoft a{-kHdCap, 0.0f, 0.0f};
-    if (row < n)
+    if (base + lane < n)
 #pragma unroll 4
       for (int q = warp; q < parts; q += 32) {
-        const float4 v = p.part[q * p.part_rows + row];
+        const float4 v = p.part[q * p.part_rows + base + lane];
         hd_join(a, HeadSoft{v.x, v.y, v.z});
       }
-    s[warp][lane] = a;
+    sm[warp][lane] = a.m;
+    sz[warp][lane] = a.Z;
+    ss[warp][lane] = a.S;
     __syncthreads();
-    if (warp == 0 && row < n) {
-      for (int q = 1; q < 32; ++q) hd_join(a, s[q][lane]);
+    const int64_t row = base + warp;
+    a = HeadSoft{sm[lane][warp], sz[lane][warp], ss[lane][warp]};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      hd_join(a, HeadSoft{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.Z, o), __shfl_xor_sync(0xFFFFFFFFu, a.S, o)});
+    if (lane == 0 && row < n) {
       const float lnZ = logf(a.Z);
       const int32_t t = p.rows[row], v = p.target[row];
       bool gone = false;

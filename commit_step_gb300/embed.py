@@ -7,8 +7,8 @@ from typing import Optional
 import torch
 
 from . import DLLM_BF16, DLLM_F32, _check, _lib, _need_cuda
-from .cache import _empty, _raw_stream
-from .head import _workspace
+from .cache import _raw_stream
+from .head import _size, _workspace
 
 
 def _dtype(t, name: str) -> int:
@@ -33,9 +33,12 @@ def _canvas(tokens, device):
 
 def _weight(t, name: str, V: int, d: int) -> int:
     """The row stride of a (V, d) tensor with unit column stride."""
-    if t.dim() != 2 or t.shape != (V, d) or (d > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be (V, d) = ({V}, {d}) with unit column stride")
-    return t.stride(0) if V > 1 else d
+    if t.dim() != 2 or t.shape != (V, d):
+        raise ValueError(f"{name} must be (V, d) = ({V}, {d})")
+    stride, unit = t.stride()
+    if d > 1 and unit != 1:
+        raise ValueError(f"{name} needs unit column stride")
+    return stride if V > 1 else d
 
 
 def embed_tokens(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
@@ -45,21 +48,24 @@ def embed_tokens(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
     ``tokens``: (T,) or (B, L) int32, rows at any stride (a window of a longer
     canvas); an id outside [0, V) gives zeros.  ``weight``: (V, d) bf16 or fp32.
     ``out``: preallocated."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embed_tokens(tokens, weight, scale, out)
     _need_cuda(tokens, weight)
     dt = _dtype(weight, "weight")
     if weight.dim() != 2:
         raise ValueError("weight must be (V, d)")
     V, d = weight.shape
     stride = _weight(weight, "weight", V, d)
-    dev, idx = weight.device, weight.get_device()
+    dev = weight.device
     B, L, t_stride = _canvas(tokens, dev)
     if out is None:
-        out = _empty((*tokens.shape, d), weight.dtype, dev, stream)
+        out = torch.empty((*tokens.shape, d), dtype=weight.dtype, device=dev)
     elif (not torch.is_tensor(out) or out.dtype != weight.dtype or out.device != dev or out.shape != (*tokens.shape, d)
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous (..., d) tensor of weight's dtype, on the same device")
     _check(_lib.dllm_embed_tokens(tokens.data_ptr(), B, L, t_stride, weight.data_ptr(), dt, V, d, stride, scale,
-                                  out.data_ptr(), _raw_stream(stream, idx)), "dllm_embed_tokens")
+                                  out.data_ptr(), _raw_stream(None, weight.get_device())), "dllm_embed_tokens")
     return out
 
 
@@ -71,6 +77,9 @@ def embed_tokens_backward(tokens: torch.Tensor, grad: torch.Tensor, V: int, scal
     ``out``: preallocated, bf16 or fp32 (by default of grad's dtype);
     ``accumulate`` adds to it, e.g. to the gradient of a head that shares the
     weight.  ``ws``: a workspace of the caller's, not in use by another call."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embed_tokens_backward(tokens, grad, V, scale, out, accumulate, ws)
     _need_cuda(tokens, grad)
     dt = _dtype(grad, "grad")
     dev, idx, V = grad.device, grad.get_device(), int(V)
@@ -83,13 +92,13 @@ def embed_tokens_backward(tokens: torch.Tensor, grad: torch.Tensor, V: int, scal
     if out is None:
         if accumulate:
             raise ValueError("accumulate adds to the gradient given as out")
-        out = _empty((V, d), grad.dtype, dev, stream)
+        out = torch.empty((V, d), dtype=grad.dtype, device=dev)
     out_dt = _dtype(out, "out")
     if out.device != dev:
         raise ValueError(f"out is on {out.device}; grad is on {dev}")
     out_stride = _weight(out, "out", V, d)
-    raw = _raw_stream(stream, idx)
-    ws = _workspace(ws, int(_lib.dllm_embed_tokens_backward_workspace_size(B * L, V, d)), dev, stream)
+    raw = _raw_stream(None, idx)
+    ws = _workspace(ws, _size("dllm_embed_tokens_backward_workspace_size", B * L, V, d), dev, raw)
     _check(_lib.dllm_embed_tokens_backward(tokens.data_ptr(), B, L, t_stride, grad.data_ptr(), dt, V, d, scale,
                                            out.data_ptr(), out_dt, out_stride, 1 if accumulate else 0, ws.data_ptr(),
                                            ws.numel() * ws.element_size(), raw), "dllm_embed_tokens_backward")

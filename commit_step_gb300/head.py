@@ -3,12 +3,13 @@ gradient with respect to hidden states and weight, without the logits in memory
 (``dllm_lm_head_logprobs``, ``dllm_lm_head_logprobs_backward``)."""
 from __future__ import annotations
 
+import threading
 from typing import Optional, Sequence
 
 import torch
 
 from . import DLLM_BF16, DLLM_F32, _F32, _I32, _check, _lib, _need_cuda
-from .cache import _at, _at_or_none, _empty, _raw_stream
+from .cache import _at, _at_or_none, _raw_stream
 from .score import _rows, _sup
 
 
@@ -18,30 +19,63 @@ def _matrix(t, name: str, cols: int, device):
         raise TypeError(f"{name} must be a 2-D bfloat16 tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}; hidden is on {device}")
-    if t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+    (rows, width), (stride, unit) = t.shape, t.stride()
+    if width != cols or (cols > 1 and unit != 1):
         raise ValueError(f"{name} must have {cols} columns at unit stride")
-    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else cols)
+    return rows, (stride if rows > 1 else cols)
 
 
 def _ends(hidden, weight, targets):
     """Shape and stride of hidden (T, d) or (B, L, d) and weight (V, d)."""
     _need_cuda(hidden, weight, targets)
+    if not torch.is_tensor(hidden) or hidden.dtype != torch.bfloat16 or hidden.dim() not in (2, 3):
+        raise TypeError("hidden must be a (T, d) or (B, L, d) bfloat16 tensor")
     T, d, stride = _rows(hidden, "hidden")
-    if hidden.dtype != torch.bfloat16:
-        raise TypeError("hidden must be bfloat16")
     V, w_stride = _matrix(weight, "weight", d, hidden.device)
     return T, d, stride, V, w_stride
 
 
-def _workspace(ws, need: int, device, stream):
-    """The caller's workspace, or a new one that belongs to the call's stream."""
-    if ws is None:
-        return _empty((need,), torch.uint8, device, stream)
-    if not torch.is_tensor(ws):
-        raise TypeError("ws must be a tensor")
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous tensor on {device}")
+_KEPT = threading.local()
+_KEEP = 32 << 20
+
+
+def _workspace(ws, need: int, device, raw: int):
+    """The caller's workspace, or one for a call on the current stream.  A call's
+    launches pass their parts on through it, so it is kept for later calls of the
+    same host thread on the same stream only, up to 32 MB (a larger one costs
+    little beside the call that needs it), and a call that is captured gets memory
+    of its graph's.  (Allocated anew for every call, 7 MB cost the host 7 of 30 us.)"""
+    if ws is not None:
+        if not torch.is_tensor(ws):
+            raise TypeError("ws must be a tensor")
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on {device}")
+        return ws
+    if need > _KEEP or torch.cuda.is_current_stream_capturing():
+        return torch.empty((need,), dtype=torch.uint8, device=device)
+    try:
+        kept = _KEPT.ws
+    except AttributeError:
+        kept = _KEPT.ws = {}
+    key = (device.index, raw)
+    ws = kept.get(key)
+    if ws is None or ws.numel() < need:
+        ws = kept[key] = torch.empty((need,), dtype=torch.uint8, device=device)
     return ws
+
+
+_SIZES = {}
+
+
+def _size(query, *shape):
+    """What a size query answers on the current device."""
+    key = (query, torch._C._cuda_getDevice(), shape)
+    need = _SIZES.get(key)
+    if need is None:
+        if len(_SIZES) > 4096:                                                  # (ever new lengths)
+            _SIZES.clear()
+        need = _SIZES[key] = int(getattr(_lib, query)(*shape))
+    return need
 
 
 def lm_head_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, suppress_ids: Sequence[int] = (),
@@ -55,14 +89,20 @@ def lm_head_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
     ``out``: the same three, preallocated.  ``ws``: a workspace of the caller's,
     not in use by another call; zeroed, it tells ``workspace_fault`` afterwards
     whether a wait ran out."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lm_head_logprobs(hidden, weight, targets, suppress_ids, out, ws)
     T, d, stride, V, w_stride = _ends(hidden, weight, targets)
-    dev, idx, shape = hidden.device, hidden.get_device(), hidden.shape[:-1]
+    dev, idx = hidden.device, hidden.get_device()
     if out is None:
-        out = [_empty(shape, torch.float32, dev, stream) for _ in range(3)]
-    lp, ent, lse = out
-    at = [_at(t, name, T, _F32, idx, dev) for t, name in ((lp, "logprob"), (ent, "entropy"), (lse, "lse"))]
-    raw = _raw_stream(stream, idx)
-    ws = _workspace(ws, int(_lib.dllm_lm_head_logprobs_workspace_size(T, V, d)), dev, stream)
+        out = [torch.empty(hidden.shape[:-1], dtype=torch.float32, device=dev) for _ in range(3)]
+        lp, ent, lse = out
+        at = [t.data_ptr() for t in out]
+    else:
+        lp, ent, lse = out
+        at = [_at(t, name, T, _F32, idx, dev) for t, name in ((lp, "logprob"), (ent, "entropy"), (lse, "lse"))]
+    raw = _raw_stream(None, idx)
+    ws = _workspace(ws, _size("dllm_lm_head_logprobs_workspace_size", T, V, d), dev, raw)
     sup, n_sup = _sup(suppress_ids)
     _check(_lib.dllm_lm_head_logprobs(hidden.data_ptr(), T, d, stride, weight.data_ptr(), V, w_stride,
                                       _at(targets, "targets", T, _I32, idx, dev), sup, n_sup, *at, ws.data_ptr(),
@@ -81,6 +121,10 @@ def lm_head_logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, target
     (``hidden_grad``, ``weight_grad`` false) is None.  ``out``: the two,
     preallocated (grad_weight bf16 or float32, either None to be made here);
     ``accumulate`` adds to out's grad_weight.  ``ws`` as in lm_head_logprobs."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lm_head_logprobs_backward(hidden, weight, targets, lse, entropy, grad_logprob, grad_entropy, suppress_ids,
+                                             out, accumulate, hidden_grad, weight_grad, ws)
     T, d, stride, V, w_stride = _ends(hidden, weight, targets)
     dev, idx = hidden.device, hidden.get_device()
     gh, gw = (None, None) if out is None else out
@@ -89,9 +133,9 @@ def lm_head_logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, target
     if accumulate and gw is None:
         raise ValueError("accumulate adds to the grad_weight given in out")
     if hidden_grad and gh is None:
-        gh = _empty(hidden.shape, torch.bfloat16, dev, stream)
+        gh = torch.empty(hidden.shape, dtype=torch.bfloat16, device=dev)
     if weight_grad and gw is None:
-        gw = _empty((V, d), torch.bfloat16, dev, stream)
+        gw = torch.empty((V, d), dtype=torch.bfloat16, device=dev)
     gh_stride, gw_stride, gw_dt = d, d, DLLM_BF16
     if gh is not None:
         if not torch.is_tensor(gh) or gh.dtype != torch.bfloat16 or gh.device != dev or gh.shape != hidden.shape:
@@ -104,8 +148,8 @@ def lm_head_logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, target
             raise ValueError("grad_weight must be shaped like weight, with unit column stride")
         gw_stride = gw.stride(0) if V > 1 else d
         gw_dt = DLLM_F32 if gw.dtype == torch.float32 else DLLM_BF16
-    raw = _raw_stream(stream, idx)
-    ws = _workspace(ws, int(_lib.dllm_lm_head_logprobs_backward_workspace_size(T, V, d)), dev, stream)
+    raw = _raw_stream(None, idx)
+    ws = _workspace(ws, _size("dllm_lm_head_logprobs_backward_workspace_size", T, V, d), dev, raw)
     sup, n_sup = _sup(suppress_ids)
     _check(_lib.dllm_lm_head_logprobs_backward(
         hidden.data_ptr(), T, d, stride, weight.data_ptr(), V, w_stride, _at(targets, "targets", T, _I32, idx, dev), sup,
