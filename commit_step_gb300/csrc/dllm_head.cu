@@ -46,8 +46,7 @@ constexpr int kHdBN = 256;                       // its columns at most
 constexpr int kHdBK = 64;                        // K of a stage: one 128-byte swizzle row of bf16
 constexpr int kHdABytes = kHdRows * kHdBK * 2;   // 16 KB: a CTA's part of a slab of A, whole
 constexpr int kHdBBytes = kHdBN / 2 * kHdBK * 2; // 16 KB
-constexpr int kHdMaxStages = 16;                 // of the ring; 7 of 32 KB, 6 where tiles are stored by TMA, more where
-                                                 // few rows leave A small (the weight's bytes in flight are what counts then)
+constexpr int kHdMaxStages = 16;                 // of the ring: 7 of 32 KB, 6 where tiles are stored by TMA, more of narrow ones
 constexpr int kHdEpiWarps = 8;                   // two warpgroups, each reads every other 32-column chunk of a tile
 constexpr int kHdTmaWarp = 10;
 constexpr int kHdMmaWarp = 11;
@@ -81,8 +80,8 @@ struct HeadParams {
   int32_t n_n;                   // tiles along N
   uint32_t idesc;
   uint32_t a_bytes;              // what a CTA's load of A brings
-  uint32_t a_room, stage_bytes;  // a stage: A's rows (whole swizzle atoms), then B
-  int32_t stages;
+  uint32_t stage_bytes;          // of the ring: A, then B's share of a tile
+  int32_t stages, clear_a;
   const int32_t* target;         // per scored row
   int32_t n_sup;
   int32_t sup[DLLM_MAX_SUPPRESS];
@@ -427,6 +426,16 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
     fence_mbar_init();
   }
   for (int q = threadIdx.x; q < p.n_sup; q += blockDim.x) sup_s[q] = p.sup[q];
+  // Few rows: what the loads of A leave out of its place reads as zero (the products
+  // of rows that do not exist then draw little power, which the weight's stream
+  // would pay for in clocks: [ZERO]).
+  if (p.clear_a) {
+    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(p.stages) * (kHdABytes / 16); i += kHdThreads)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i / (kHdABytes / 16) * p.stage_bytes + i % (kHdABytes / 16) * 16),
+                   "r"(0)
+                   : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   if (warp == kHdMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
                  "r"(kHdTmemCols)
@@ -474,7 +483,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
             break;
           }
           const uint32_t bar = hd_leader(smem_addr(&full_bar[s]));
-          const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes, b = a + p.a_room;
+          const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes, b = a + kHdABytes;
           if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full_bar[s]), tx);
           if (rank == 0 || second) {
             if (hd_a_mn(OP)) {
@@ -526,7 +535,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
           }
           hd_fence_after();
           const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes;
-          const uint32_t da = hd_desc(a), db = hd_desc(a + p.a_room);
+          const uint32_t da = hd_desc(a), db = hd_desc(a + kHdABytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes of a K-major row, 16 rows of 128 bytes MN-major
             hd_mma(lead, d_tmem, da + kk * ((hd_a_mn(OP) ? 2048 : 32) >> 4), db + kk * ((hd_b_mn(OP) ? 2048 : 32) >> 4), p.idesc,
@@ -754,10 +763,11 @@ __global__ void __launch_bounds__(kHdListThreads) head_rows_kernel(const __grid_
   __shared__ int32_t warp_sums[kHdListThreads / 32];
   __shared__ int32_t list[kHdListThreads];
   __shared__ int32_t before_s, total_s;
+  // (the products' kernel may begin: before its own wait it only sets itself up)
+  pdl_launch_dependents();
   if (threadIdx.x == 0) before_s = total_s = 0;
   __syncthreads();
   pdl_wait();
-  pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t t0 = hd_first(p.T, blockIdx.x), t1 = hd_first(p.T, blockIdx.x + 1);
   HeadRow r{};
@@ -854,10 +864,13 @@ struct HeadFinishParams {
   float *logprob, *entropy, *lse;
 };
 
-// 32 rows a block: first a lane a row, the warps sharing its partials, then a warp a
-// row, its lanes joining what the warps have.
-__global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant__ HeadFinishParams p) {
-  __shared__ float sm[32][33], sz[32][33], ss[32][33];
+// 32 rows a block: first a lane a row, the warps sharing its partials, then half a
+// warp a row, its lanes joining what the warps have.  (Of a size that fits an SM
+// beside the products' kernel, so that it is there when that ends.)
+constexpr int kHdFinishWarps = 16;
+
+__global__ void __launch_bounds__(kHdFinishWarps * 32, 3) head_finish_kernel(const __grid_constant__ HeadFinishParams p) {
+  __shared__ float sm[kHdFinishWarps][33], sz[kHdFinishWarps][33], ss[kHdFinishWarps][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -867,7 +880,7 @@ __global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant
     HeadSoft a{-kHdCap, 0.0f, 0.0f};
     if (base + lane < n)
 #pragma unroll 4
-      for (int q = warp; q < parts; q += 32) {
+      for (int q = warp; q < parts; q += kHdFinishWarps) {
         const float4 v = p.part[q * p.part_rows + base + lane];
         hd_join(a, HeadSoft{v.x, v.y, v.z});
       }
@@ -875,12 +888,13 @@ __global__ void __launch_bounds__(1024) head_finish_kernel(const __grid_constant
     sz[warp][lane] = a.Z;
     ss[warp][lane] = a.S;
     __syncthreads();
-    const int64_t row = base + warp;
-    a = HeadSoft{sm[lane][warp], sz[lane][warp], ss[lane][warp]};
+    const int at = 2 * warp + (lane >> 4);
+    const int64_t row = base + at;
+    a = HeadSoft{sm[lane & 15][at], sz[lane & 15][at], ss[lane & 15][at]};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 8; o > 0; o >>= 1)
       hd_join(a, HeadSoft{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.Z, o), __shfl_xor_sync(0xFFFFFFFFu, a.S, o)});
-    if (lane == 0 && row < n) {
+    if ((lane & 15) == 0 && row < n) {
       const float lnZ = logf(a.Z);
       const int32_t t = p.rows[row], v = p.target[row];
       bool gone = false;
@@ -1103,14 +1117,11 @@ dllm_status hd_check(const void* hidden, int64_t T, int64_t d, int64_t hidden_st
   return DLLM_OK;
 }
 
-// A stage holds the rows of A that exist and B's share of a tile.  (The products
-// read a whole A: what lies past the last stage's rows has to be in the ring.)
 void hd_ring(HeadParams& p, int op, int32_t a_rows) {
   p.a_bytes = static_cast<uint32_t>(a_rows) * kHdBK * 2;
-  p.a_room = static_cast<uint32_t>(round_up(p.a_bytes, 1024));
-  p.stage_bytes = p.a_room + static_cast<uint32_t>(round_up(p.bn / 2 * kHdBK * 2, 1024));
-  const int32_t room = kHdRing - (op == kHdDw ? kHdEpiWarps * kHdStoreBytes : kHdABytes - static_cast<int32_t>(p.a_room));
-  p.stages = std::min(kHdMaxStages, room / static_cast<int32_t>(p.stage_bytes));
+  p.stage_bytes = kHdABytes + static_cast<uint32_t>(round_up(p.bn / 2 * kHdBK * 2, 1024));
+  p.stages = std::min<int32_t>(kHdMaxStages, (kHdRing - (op == kHdDw ? kHdEpiWarps * kHdStoreBytes : 0)) / static_cast<int32_t>(p.stage_bytes));
+  p.clear_a = op != kHdDw && p.T <= kHdRows ? 1 : 0;
 }
 
 template <int OP>
@@ -1223,7 +1234,8 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   if (st != DLLM_OK) return st;
   void* fargs[] = {&f};
   return launch_pdl(reinterpret_cast<const void*>(&head_finish_kernel),
-                    dim3(static_cast<unsigned>(std::min<int64_t>((T + 31) / 32, dev->sms * 2))), dim3(1024), 0, stream, fargs);
+                    dim3(static_cast<unsigned>(std::min<int64_t>((T + 31) / 32, dev->sms * 2))), dim3(kHdFinishWarps * 32), 0, stream,
+                    fargs);
 }
 
 dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride,
