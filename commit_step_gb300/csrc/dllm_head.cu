@@ -60,7 +60,7 @@ constexpr int kHdBand = 16;                      // row tiles that share a pass 
 constexpr float kHdCap = 0x1p+125f;              // logits are read within +-2^125 (NaN as the lowest): differences stay finite
 constexpr float kHdAbsent = -0x1p+126f;          // suppressed ids and columns past the vocabulary
 
-enum HeadOp { kHdScore, kHdDz, kHdDh, kHdDw };
+enum HeadOp { kHdScore, kHdDz, kHdBack };         // the last: dH and dW, tiles of both in one launch
 
 // A scored row's constants of the backward pass.
 struct HeadRow {
@@ -70,6 +70,7 @@ struct HeadRow {
 struct HeadParams {
   CUtensorMap tm_a, tm_b;        // the operands; where one is the hidden states, the caller's tensor,
   CUtensorMap tm_packed;         // read when every row is scored, and else their gathered copy
+  CUtensorMap tm_aw, tm_bw;      // dw's operands, as rows of 64 m or n (tm_packed then for these)
   CUtensorMap tm_out;            // dw in bf16 without accumulate: the weight's gradient
   const int32_t* n_rows;         // device: the scored rows; then the splits of the second product
   int64_t T, V;
@@ -78,7 +79,8 @@ struct HeadParams {
   int64_t d;
   int32_t bn;                    // columns of a tile
   int32_t n_n;                   // tiles along N
-  uint32_t idesc;
+  uint32_t idesc, idesc_w;       // (of dw)
+  int32_t want_h, want_w;        // dh and dw: wanted
   uint32_t a_bytes;              // what a CTA's load of A brings
   uint32_t stage_bytes;          // of the ring: A, then B's share of a tile
   int32_t stages, clear_a;
@@ -100,14 +102,11 @@ struct HeadParams {
   int32_t* fault;
 };
 
-__host__ __device__ constexpr bool hd_a_mn(int op) { return op == kHdDw; }
-__host__ __device__ constexpr bool hd_b_mn(int op) { return op == kHdDh || op == kHdDw; }
-
 // Instruction descriptor of tcgen05.mma.kind::f16: fp32 accumulator (bits 4-5 =
 // 1), bf16 A and B (bits 7-9, 10-12 = 1), MN-major A, B (bits 15, 16), N / 8 in
 // bits 17-22, M / 16 in bits 24-28.
-constexpr uint32_t hd_idesc(int op, int bn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (hd_a_mn(op) ? 1u << 15 : 0u) | (hd_b_mn(op) ? 1u << 16 : 0u) |
+constexpr uint32_t hd_idesc(bool a_mn, bool b_mn, int bn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(kHdBM >> 4) << 24);
 }
 
@@ -124,19 +123,29 @@ __device__ __forceinline__ uint32_t hd_elect() {
   return r;
 }
 
+// What follows is issued by the one thread of the warp whose `lead` is set; the whole
+// warp executes the code around it, so that addresses and descriptors stay in uniform
+// registers (formed by a single thread, a product and a load held a slab up by some
+// 170 and 190 cycles each: 32 x 126464 x 4096 took 187 us, and [BLOCK] so).
+
 // A load of this CTA's shared memory that counts on the leader's barrier.
-__device__ __forceinline__ void hd_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void hd_load(uint32_t lead, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(lead)
       : "memory");
 }
 
-// Issued by the one thread of the warp whose `lead` is set; the whole warp executes
-// the code around it, so that addresses and descriptors stay in uniform registers
-// (formed by a single thread, they held a slab up to 335 ns, whatever its width:
-// 32 x 126464 x 4096 took 187 us, and [BLOCK] so).
+__device__ __forceinline__ void hd_expect(uint32_t lead, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(lead)
+      : "memory");
+}
+
 __device__ __forceinline__ void hd_mma(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
@@ -216,58 +225,76 @@ __device__ __forceinline__ uint32_t hd_bf16x2(float lo, float hi) {
   return d;
 }
 
-// How many ways the second product's K is split: the fewest rounds of tiles that the
-// pairs can be kept busy with, against 8 bytes a split of every element written and
-// read again (1.5 MB in the time of a slab of 256 x 256 x 64).  32 tiles of 1976
-// slabs on 76 pairs: 7 splits, 3 full rounds (2 splits leave 12 pairs idle).
-// Called by a whole warp, a lane a number of splits.
-__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int bn, int pairs, int slabs, int64_t room) {
+// A tile of dw costs its slabs and, for its output's 128 KB, those of 4 more, 6 at
+// least (512 x 126464 x 4096: 1148, 1129 and 1107 us with 0, 2 and 4 more; 61 x 50257 x
+// 768: 66, 70 and 72 us with 6, 8 and 10 at least).
+__host__ __device__ constexpr int hd_dw_cost(int slabs) { return slabs > 2 ? slabs + 4 : 6; }
+
+// How many ways the second product's K is split: the least of the pairs' time, which
+// is their share of all tiles, or the rounds that dh's take where these are more (the
+// third product's tiles fill what a last round of dh leaves), and 8 bytes a split of
+// every element written and read again (1.5 MB in the time of a slab of 256 x 256 x
+// 64).  Called by a whole warp, a lane a number of splits.
+__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int bn, int pairs, int slabs, int64_t dw_tiles, int64_t room) {
   const int s = (threadIdx.x & 31) + 1;
   const int tiles = static_cast<int>((n + kHdBM - 1) / kHdBM) * n_n;
   const float size = static_cast<float>(tiles) * static_cast<float>(kHdBM * bn);
-  const float rounds = ceilf(static_cast<float>(tiles) * s / static_cast<float>(pairs));
-  float cost = rounds * ceilf(static_cast<float>(slabs) / s) * (bn / 256.0f) + s * size * (8.0f / 1.5e6f);
+  const float share = (static_cast<float>(tiles) * slabs +
+                       static_cast<float>(dw_tiles) * hd_dw_cost(static_cast<int>((n + kHdBK - 1) / kHdBK))) / static_cast<float>(pairs);
+  const float rounds = ceilf(static_cast<float>(tiles) * s / static_cast<float>(pairs)) * ceilf(static_cast<float>(slabs) / s);
+  float cost = fmaxf(share, rounds) * (bn / 256.0f) + s * size * (8.0f / 1.5e6f);
   if (s > 1 && (s > slabs || static_cast<int64_t>(s) * tiles * kHdBM * bn > room)) cost = 3.0e38f;
   const float least = -warp_max_f32(-cost);
   return __ffs(__ballot_sync(0xFFFFFFFFu, cost == least));
 }
 
-// The tiles of a product and the order in which the pairs of CTAs take them (tile i
-// to pair i mod pairs).  A split of a short last piece may hold no slab: such a tile
+// A tile of a product.  A split of a short last piece may hold no slab: such a tile
 // is passed over (what it adds to, an earlier piece has written).
 struct HeadTile {
   int32_t m, n;        // tile coordinates
   int32_t k0, k1;      // slabs
   int32_t split;
+  bool dw;
 };
 
+// The tiles in the order in which this pair of CTAs takes them: tile i goes to pair i
+// mod pairs, dh's before dw's; the pairs that a last round of dh leaves out take as
+// many tiles of dw as fit its time first.
 template <int OP>
 struct HeadWork {
-  int64_t n;           // scored rows
-  int32_t n_m, n_n, slabs, splits;
+  int64_t pair, pairs;
+  int32_t n_n;
+  int32_t n_m, slabs, splits;            // of scores, dz or dh
   int64_t total;
+  int32_t slabs_w, rest;                 // dw; dh's tiles in a last round
+  int64_t total_w, extra;
 
-  __device__ __forceinline__ HeadWork(const HeadParams& p, int64_t rows) : n(rows), n_n(p.n_n), splits(1) {
-    if (OP == kHdScore || OP == kHdDz) {
-      n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
+  __device__ __forceinline__ HeadWork(const HeadParams& p, int64_t n)
+      : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), n_n(p.n_n), splits(1), slabs_w(0), rest(0), total_w(0), extra(0) {
+    n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
+    if (OP != kHdBack) {
       slabs = static_cast<int32_t>((p.d + kHdBK - 1) / kHdBK);
-    } else if (OP == kHdDh) {
-      n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
-      slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
-      splits = p.n_rows[1];
-    } else {
-      n_m = static_cast<int32_t>((p.cols + kHdBM - 1) / kHdBM);
-      slabs = static_cast<int32_t>((n + kHdBK - 1) / kHdBK);
+      total = static_cast<int64_t>(n_m) * n_n;
+      return;
     }
-    total = n == 0 ? 0 : static_cast<int64_t>(n_m) * n_n * splits;
+    slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
+    splits = p.n_rows[1];
+    total = p.want_h ? static_cast<int64_t>(n_m) * n_n * splits : 0;
+    slabs_w = static_cast<int32_t>((n + kHdBK - 1) / kHdBK);
+    total_w = p.want_w && n > 0 ? (p.cols + kHdBM - 1) / kHdBM * n_n : 0;
+    rest = static_cast<int32_t>(total % pairs);
+    if (rest > 0) extra = min(static_cast<int64_t>(slabs / splits / hd_dw_cost(slabs_w)), total_w / (pairs - rest));
   }
 
-  __device__ __forceinline__ HeadTile tile(int64_t i) const {
-    HeadTile t;
+  // Its tile number `it`; false behind the last.
+  __device__ __forceinline__ bool tile(int64_t it, HeadTile& t) const {
     t.split = 0;
     t.k0 = 0;
     t.k1 = slabs;
-    if (OP == kHdScore || OP == kHdDz) {
+    t.dw = false;
+    int64_t i = it * pairs + pair;
+    if (OP != kHdBack) {
+      if (i >= total) return false;
       // bands of row tiles, each over the whole vocabulary, its row tiles inner
       const int32_t bands = (n_m + kHdBand - 1) / kHdBand, high = (n_m + bands - 1) / bands;
       const int64_t per_band = static_cast<int64_t>(high) * n_n;
@@ -276,7 +303,9 @@ struct HeadWork {
       const int32_t rows = min(high, n_m - band * high);
       t.m = band * high + in % rows;
       t.n = in / rows;
-    } else if (OP == kHdDh) {
+      return true;
+    }
+    if (i < total) {
       const int64_t tiles = static_cast<int64_t>(n_m) * n_n;
       t.split = static_cast<int32_t>(i / tiles);
       const int32_t in = static_cast<int32_t>(i - t.split * tiles);
@@ -284,11 +313,22 @@ struct HeadWork {
       t.n = in % n_n;
       t.k0 = static_cast<int32_t>(static_cast<int64_t>(slabs) * t.split / splits);
       t.k1 = static_cast<int32_t>(static_cast<int64_t>(slabs) * (t.split + 1) / splits);
-    } else {
-      t.m = static_cast<int32_t>(i / n_n);
-      t.n = static_cast<int32_t>(i % n_n);
+      return true;
     }
-    return t;
+    const bool left_out = pair >= rest;                  // of the last round of dh
+    int64_t j = it - total / pairs - (left_out ? 0 : 1);
+    if (left_out && j < extra) {
+      i = j * (pairs - rest) + pair - rest;
+    } else {
+      if (left_out) j -= extra;
+      i = extra * (pairs - rest) + j * pairs + pair;
+    }
+    if (i >= total_w) return false;
+    t.dw = true;
+    t.k1 = slabs_w;
+    t.m = static_cast<int32_t>(i / n_n);
+    t.n = static_cast<int32_t>(i % n_n);
+    return true;
   }
 };
 
@@ -358,22 +398,25 @@ __device__ __forceinline__ void hd_store_dz(uint16_t* out, const float (&x)[32],
 // rows y of the tensor: through shared memory in the 128-byte swizzle and out by
 // TMA, so that memory sees whole lines (stored from registers, a row a thread, the
 // weight's gradient took 504 us where it now takes [DW] at 512 x 126464 x 4096).
-__device__ __forceinline__ void hd_store_tile(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane) {
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (the last one has left the buffer)
-  __syncwarp();
+// `done` is called once the accumulator has been read.
+template <class Done>
+__device__ __forceinline__ void hd_store_tile(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane, Done done) {
+  uint32_t w[32];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t r[32];
     hd_ld32(taddr + 32 * h, r);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = hd_bf16x2(__uint_as_float(r[8 * j + 2 * e]), __uint_as_float(r[8 * j + 2 * e + 1]));
-      const uint32_t at = buf + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4);
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-    }
+    for (int j = 0; j < 16; ++j) w[16 * h + j] = hd_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
   }
+  done();
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (the last one has left the buffer)
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((j ^ (lane & 7)) << 4)), "r"(w[4 * j]),
+                 "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                 : "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
   if (lane == 0) {
@@ -459,67 +502,69 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   const int64_t n = *p.n_rows;
   const HeadWork<OP> work(p, n);
   const bool packed = n != p.T;
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  // Rows of A and of the accumulator that exist.
-  const int64_t a_rows = OP == kHdDw ? p.cols : n;
+  HeadTile t;
 
   if (warp == kHdTmaWarp) {
-    if (lane == 0) {
-      const CUtensorMap* ma = (OP == kHdScore || OP == kHdDz) && packed ? &p.tm_packed : &p.tm_a;
-      const CUtensorMap* mb = OP == kHdDw && packed ? &p.tm_packed : &p.tm_b;
-      const int half = p.bn / 2;
-      int s = 0;
-      uint32_t ph = 0;
-      int64_t issued = 0;
-      for (int64_t i = pair; i < work.total && !*abort_flag; i += pairs) {
-        const HeadTile t = work.tile(i);
-        const int m0 = t.m * kHdBM + static_cast<int>(rank) * kHdRows, n0 = t.n * p.bn + static_cast<int>(rank) * half;
-        // The second CTA's rows may all be past the end: then its A is not loaded.
-        const bool second = static_cast<int64_t>(t.m) * kHdBM + kHdRows < a_rows;
-        const uint32_t tx = (second ? 2u : 1u) * p.a_bytes + static_cast<uint32_t>(p.bn) * kHdBK * 2;
-        for (int k = t.k0; k < t.k1; ++k) {
-          if (!hd_wait(smem_addr(&empty_bar[s]), ph ^ 1u, abort_flag)) {
-            hd_fail(p, abort_flag, kFaultEmptyWait);
-            break;
-          }
-          const uint32_t bar = hd_leader(smem_addr(&full_bar[s]));
-          const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes, b = a + kHdABytes;
-          if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full_bar[s]), tx);
-          if (rank == 0 || second) {
-            if (hd_a_mn(OP)) {
-              hd_load(a, ma, m0, k * kHdBK, bar);
-              hd_load(a + 8192, ma, m0 + 64, k * kHdBK, bar);
-            } else {
-              hd_load(a, ma, k * kHdBK, m0, bar);
-            }
-          }
-          if (OP == kHdScore || OP == kHdDz) {
-            hd_load(b, mb, k * kHdBK, static_cast<int>(p.v0) + n0, bar);
+    const uint32_t lead = hd_elect(), lead0 = rank == 0 ? lead : 0u;
+    const CUtensorMap* ma = OP != kHdBack && packed ? &p.tm_packed : &p.tm_a;
+    const CUtensorMap* mw = packed ? &p.tm_packed : &p.tm_bw;
+    const int half = p.bn / 2;
+    const uint32_t leader_full = hd_leader(smem_addr(&full_bar[0]));
+    int s = 0;
+    uint32_t ph = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t it = 0; work.tile(it, t) && ok; ++it) {
+      const bool dw = OP == kHdBack && t.dw;
+      const int m0 = t.m * kHdBM + static_cast<int>(rank) * kHdRows, n0 = t.n * p.bn + static_cast<int>(rank) * half;
+      // The second CTA's rows may all be past the end: then its A is not loaded.
+      const bool second = static_cast<int64_t>(t.m) * kHdBM + kHdRows < (dw ? p.cols : n);
+      const uint32_t tx = (second ? 2u : 1u) * (dw ? kHdABytes : p.a_bytes) + static_cast<uint32_t>(p.bn) * kHdBK * 2;
+      const uint32_t lead_a = rank == 0 || second ? lead : 0u;
+      for (int k = t.k0; k < t.k1; ++k) {
+        ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&empty_bar[s]), ph ^ 1u, abort_flag));
+        if (!ok) {
+          if (lane == 0) hd_fail(p, abort_flag, kFaultEmptyWait);
+          break;
+        }
+        const uint32_t bar = leader_full + s * 8;
+        const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes, b = a + kHdABytes;
+        hd_expect(lead0, smem_addr(&full_bar[s]), tx);
+        if (dw) {
+          hd_load(lead_a, a, &p.tm_aw, m0, k * kHdBK, bar);
+          hd_load(lead_a, a + 8192, &p.tm_aw, m0 + 64, k * kHdBK, bar);
+          hd_load(lead, b, mw, n0, k * kHdBK, bar);
+          if (half > 64) hd_load(lead, b + 8192, mw, n0 + 64, k * kHdBK, bar);
+        } else {
+          hd_load(lead_a, a, ma, k * kHdBK, m0, bar);
+          if (OP == kHdBack) {
+            hd_load(lead, b, &p.tm_b, n0, static_cast<int>(p.v0) + k * kHdBK, bar);
+            if (half > 64) hd_load(lead, b + 8192, &p.tm_b, n0 + 64, static_cast<int>(p.v0) + k * kHdBK, bar);
           } else {
-            const int y = (OP == kHdDh ? static_cast<int>(p.v0) : 0) + k * kHdBK;
-            for (int x = 0; x < half; x += 64) hd_load(b + x * 128, mb, n0 + x, y, bar);
-          }
-          ++issued;
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
+            hd_load(lead, b, &p.tm_b, k * kHdBK, static_cast<int>(p.v0) + n0, bar);
           }
         }
+        ++issued;
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      // Giving up: the copies still in flight land before the CTA ends.
-      if (*abort_flag && rank == 0)
-        for (int64_t q = issued > p.stages ? issued - p.stages : 0; q < issued; ++q)
-          mbar_wait_bounded(smem_addr(&full_bar[q % p.stages]), static_cast<uint32_t>((q / p.stages) & 1));
     }
+    // Giving up: the copies still in flight land before the CTA ends.
+    if (*abort_flag && rank == 0)
+      for (int64_t q = issued > p.stages ? issued - p.stages : 0; q < issued; ++q)
+        mbar_wait_bounded(smem_addr(&full_bar[q % p.stages]), static_cast<uint32_t>((q / p.stages) & 1));
   } else if (warp == kHdMmaWarp) {
     if (rank == 0) {
       const uint32_t lead = hd_elect();
       int s = 0, j = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int64_t i = pair; i < work.total && ok; i += pairs) {
-        const HeadTile t = work.tile(i);
+      for (int64_t it = 0; work.tile(it, t) && ok; ++it) {
         if (t.k0 == t.k1) continue;
+        const bool dw = OP == kHdBack && t.dw;
+        const uint32_t idesc = dw ? p.idesc_w : p.idesc, step_a = (dw ? 2048u : 32u) >> 4;
         const int buf = j & 1;
         if (!__all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&acce_bar[buf]), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag))) {
           if (lane == 0) hd_fail(p, abort_flag, kFaultEmptyWait);
@@ -538,8 +583,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
           const uint32_t da = hd_desc(a), db = hd_desc(a + kHdABytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes of a K-major row, 16 rows of 128 bytes MN-major
-            hd_mma(lead, d_tmem, da + kk * ((hd_a_mn(OP) ? 2048 : 32) >> 4), db + kk * ((hd_b_mn(OP) ? 2048 : 32) >> 4), p.idesc,
-                   k != t.k0 || kk != 0 ? 1u : 0u);
+            hd_mma(lead, d_tmem, da + kk * step_a, db + kk * ((OP == kHdBack ? 2048 : 32) >> 4), idesc, k != t.k0 || kk != 0 ? 1u : 0u);
           hd_commit(lead, smem_addr(&empty_bar[s]));
           if (++s == p.stages) {
             s = 0;
@@ -555,9 +599,9 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
     const uint32_t store_buf = ring + kHdRing - (kHdEpiWarps - warp) * kHdStoreBytes;   // (dw: behind the last stage)
     HeadSoft soft{-kHdCap, 0.0f, 0.0f};
     int j = 0;
-    for (int64_t i = pair; i < work.total; i += pairs) {
-      const HeadTile t = work.tile(i);
+    for (int64_t it = 0; work.tile(it, t); ++it) {
       if (t.k0 == t.k1) continue;
+      const bool dw = OP == kHdBack && t.dw;
       const int buf = j & 1;
       const int64_t row = static_cast<int64_t>(t.m) * kHdBM + rank * kHdRows + ew * 32 + lane;  // scored row, or (dw) id of the piece
       HeadRow info{};
@@ -576,18 +620,29 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       hd_fence_after();
       ++j;
       const int64_t col0 = static_cast<int64_t>(t.n) * p.bn;
-      const int64_t width = OP == kHdScore || OP == kHdDz ? p.cols : p.d;
+      const int64_t width = OP != kHdBack ? p.cols : p.d;
       const int in_tile = static_cast<int>(min(static_cast<int64_t>(p.bn), width - col0));
       if (work.n_m > 1) soft = HeadSoft{-kHdCap, 0.0f, 0.0f};
       // Rows a warp has to visit: those that exist; of dz also the rows up to the
       // end of the third product's last slab, which read as zero.
-      const int64_t visit = OP == kHdDw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : n);
+      const int64_t visit = dw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : n);
       const bool warp_rows = row - lane < visit;
-      if (OP == kHdDw && !p.grad_w_f32 && !p.accumulate) {
+      bool released = false;
+      auto release = [&] {                               // the accumulator has been read
+        hd_fence_before();
+        __syncwarp();
+        if (lane == 0) hd_arrive_leader(hd_leader(smem_addr(&acce_bar[buf])));
+        released = true;
+      };
+      if (dw && !p.grad_w_f32 && !p.accumulate) {
         if (warp_rows)
-          for (int c = half * 64; c < in_tile; c += 128)
-            hd_store_tile(tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * kHdBN + c), store_buf, &p.tm_out,
-                          static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane, lane);
+          for (int c = half * 64; c < in_tile; c += 128) {
+            hd_store_tile(tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * kHdBN + c),
+                          store_buf, &p.tm_out, static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane,
+                          lane, [&] {
+                            if (c + 128 >= in_tile) release();
+                          });
+          }
       } else
 #pragma unroll 1
       for (int c = half * 32; c < p.bn; c += 64) {
@@ -596,7 +651,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         hd_ld32(tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * kHdBN + c), r);
         const int lim = min(32, in_tile - c);
         float x[32];
-        if (OP == kHdScore || OP == kHdDz) {
+        if (OP != kHdBack) {
           const int64_t v = p.v0 + col0 + c;
           const uint32_t absent = lim <= 0 ? 0xFFFFFFFFu : hd_absent(sup_s, p.n_sup, v, lim);
           const int64_t hit = target - v;
@@ -654,7 +709,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
 #pragma unroll
           for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(r[q]);
           if (row < visit) {
-            if (OP == kHdDh) {
+            if (!dw) {
               float* out = p.acc + (static_cast<int64_t>(t.split) * work.n_m * kHdBM + row) * p.acc_stride + col0 + c;
               hd_store_f32(out, x, lim, p.add != 0);
             } else if (p.grad_w_f32) {
@@ -666,17 +721,15 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
           }
         }
       }
-      hd_fence_before();
-      __syncwarp();
-      if (lane == 0) hd_arrive_leader(hd_leader(smem_addr(&acce_bar[buf])));
+      if (!released) release();
       // With one row tile a thread keeps its row's state from tile to tile.
-      if (OP == kHdScore && row < n && (work.n_m > 1 || i + pairs >= work.total))
-        p.part[((work.n_m > 1 ? t.n : pair) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
+      if (OP == kHdScore && row < n && (work.n_m > 1 || (it + 1) * work.pairs + work.pair >= work.total))
+        p.part[((work.n_m > 1 ? t.n : work.pair) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
     }
-    if (OP == kHdDw && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (OP == kHdBack && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   // The third product without a scored row: the gradient is zero.
-  if (OP == kHdDw && n == 0 && !p.accumulate) {
+  if (OP == kHdBack && n == 0 && p.want_w && !p.accumulate) {
     const int64_t chunks = p.d / 8 * (p.grad_w_f32 ? 2 : 1);
     const int64_t stride = p.grad_w_stride * (p.grad_w_f32 ? 4 : 2);
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kHdThreads) + threadIdx.x; i < p.cols * chunks;
@@ -718,6 +771,7 @@ struct HeadListParams {
   int64_t stride, d;
   uint16_t* packed;
   int32_t n_d, bn_d, pairs, slabs;         // backward: what decides the splits
+  int64_t dw_tiles;
   int64_t room;
   int32_t* counts;                         // more than kHdListMost rows: the scored rows of each block
 };
@@ -818,7 +872,7 @@ __global__ void __launch_bounds__(kHdListThreads) head_rows_kernel(const __grid_
     p.o_lse[t] = 0.0f;
   }
   if (blockIdx.x == 0 && warp == 0) {
-    const int splits = p.backward ? hd_splits(n, p.n_d, p.bn_d, p.pairs, p.slabs, p.room) : 1;
+    const int splits = p.backward ? hd_splits(n, p.n_d, p.bn_d, p.pairs, p.slabs, p.dw_tiles, p.room) : 1;
     if (lane == 0) {
       p.n_rows[0] = static_cast<int32_t>(n);
       p.n_rows[1] = splits;
@@ -864,46 +918,50 @@ struct HeadFinishParams {
   float *logprob, *entropy, *lse;
 };
 
-// 32 rows a block: first a lane a row, the warps sharing its partials, then half a
-// warp a row, its lanes joining what the warps have.  (Of a size that fits an SM
-// beside the products' kernel, so that it is there when that ends.)
+// 8 rows a block: four lanes of each warp share a row's partials, then half a warp
+// joins what they have.  (Of a size that fits an SM beside the products' kernel, so
+// that it is there when that ends.)
 constexpr int kHdFinishWarps = 16;
 
+__device__ __forceinline__ HeadSoft hd_join_lane(HeadSoft a, int o) {
+  hd_join(a, HeadSoft{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.Z, o), __shfl_xor_sync(0xFFFFFFFFu, a.S, o)});
+  return a;
+}
+
 __global__ void __launch_bounds__(kHdFinishWarps * 32, 3) head_finish_kernel(const __grid_constant__ HeadFinishParams p) {
-  __shared__ float sm[kHdFinishWarps][33], sz[kHdFinishWarps][33], ss[kHdFinishWarps][33];
+  __shared__ HeadSoft share[8][kHdFinishWarps + 1];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = *p.n_rows;
   const int parts = n > kHdBM ? p.parts : min(p.parts, 2 * p.pairs);
-  for (int64_t base = blockIdx.x * static_cast<int64_t>(32); base < n; base += static_cast<int64_t>(gridDim.x) * 32) {
-    HeadSoft a{-kHdCap, 0.0f, 0.0f};
-    if (base + lane < n)
+  const int64_t base = blockIdx.x * static_cast<int64_t>(8);
+  if (base >= n) return;
+  HeadSoft a{-kHdCap, 0.0f, 0.0f};
+  const int64_t mine = base + (lane & 7);
+  if (mine < n)
 #pragma unroll 4
-      for (int q = warp; q < parts; q += kHdFinishWarps) {
-        const float4 v = p.part[q * p.part_rows + base + lane];
-        hd_join(a, HeadSoft{v.x, v.y, v.z});
-      }
-    sm[warp][lane] = a.m;
-    sz[warp][lane] = a.Z;
-    ss[warp][lane] = a.S;
-    __syncthreads();
-    const int at = 2 * warp + (lane >> 4);
-    const int64_t row = base + at;
-    a = HeadSoft{sm[lane & 15][at], sz[lane & 15][at], ss[lane & 15][at]};
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-      hd_join(a, HeadSoft{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.Z, o), __shfl_xor_sync(0xFFFFFFFFu, a.S, o)});
-    if ((lane & 15) == 0 && row < n) {
-      const float lnZ = logf(a.Z);
-      const int32_t t = p.rows[row], v = p.target[row];
-      bool gone = false;
-      for (int q = 0; q < p.n_sup; ++q) gone = gone || p.sup[q] == v;
-      p.logprob[t] = gone ? -INFINITY : (p.z_target[row] - a.m) - lnZ;
-      p.entropy[t] = fminf(fmaxf(fmaf(-kLn2, a.S / a.Z, lnZ), 0.0f), p.ln_ids);
-      p.lse[t] = a.m >= kHdCap ? INFINITY : (a.m <= -kHdCap ? -INFINITY : a.m + lnZ);
+    for (int q = 4 * warp + (lane >> 3); q < parts; q += 4 * kHdFinishWarps) {
+      const float4 v = __ldcs(p.part + q * p.part_rows + mine);
+      hd_join(a, HeadSoft{v.x, v.y, v.z});
     }
-    __syncthreads();
+  a = hd_join_lane(hd_join_lane(a, 8), 16);
+  if (lane < 8) share[lane][warp] = a;
+  __syncthreads();
+  if (warp >= 4) return;
+  const int at = 2 * warp + (lane >> 4);
+  const int64_t row = base + at;
+  a = share[at][lane & 15];
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) a = hd_join_lane(a, o);
+  if ((lane & 15) == 0 && row < n) {
+    const float lnZ = logf(a.Z);
+    const int32_t t = p.rows[row], v = p.target[row];
+    bool gone = false;
+    for (int q = 0; q < p.n_sup; ++q) gone = gone || p.sup[q] == v;
+    p.logprob[t] = gone ? -INFINITY : (p.z_target[row] - a.m) - lnZ;
+    p.entropy[t] = fminf(fmaxf(fmaf(-kLn2, a.S / a.Z, lnZ), 0.0f), p.ln_ids);
+    p.lse[t] = a.m >= kHdCap ? INFINITY : (a.m <= -kHdCap ? -INFINITY : a.m + lnZ);
   }
 }
 
@@ -1013,7 +1071,7 @@ const HdDevice* hd_device() {
     HdDevice& d = g_hd[dev];
     d.err = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     for (const void* k : {reinterpret_cast<const void*>(&head_kernel<kHdScore>), reinterpret_cast<const void*>(&head_kernel<kHdDz>),
-                          reinterpret_cast<const void*>(&head_kernel<kHdDh>), reinterpret_cast<const void*>(&head_kernel<kHdDw>)})
+                          reinterpret_cast<const void*>(&head_kernel<kHdBack>)})
       if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kHdSmem);
     if (d.err != cudaSuccess) (void)cudaGetLastError();  // report through the status, leave no sticky error
   });
@@ -1120,8 +1178,8 @@ dllm_status hd_check(const void* hidden, int64_t T, int64_t d, int64_t hidden_st
 void hd_ring(HeadParams& p, int op, int32_t a_rows) {
   p.a_bytes = static_cast<uint32_t>(a_rows) * kHdBK * 2;
   p.stage_bytes = kHdABytes + static_cast<uint32_t>(round_up(p.bn / 2 * kHdBK * 2, 1024));
-  p.stages = std::min<int32_t>(kHdMaxStages, (kHdRing - (op == kHdDw ? kHdEpiWarps * kHdStoreBytes : 0)) / static_cast<int32_t>(p.stage_bytes));
-  p.clear_a = op != kHdDw && p.T <= kHdRows ? 1 : 0;
+  p.stages = std::min<int32_t>(kHdMaxStages, (kHdRing - (op == kHdBack ? kHdEpiWarps * kHdStoreBytes : 0)) / static_cast<int32_t>(p.stage_bytes));
+  p.clear_a = p.T <= kHdRows ? 1 : 0;
 }
 
 template <int OP>
@@ -1198,7 +1256,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   p.d = d;
   p.bn = h.bn_v;
   p.n_n = h.n_v;
-  p.idesc = hd_idesc(kHdScore, h.bn_v);
+  p.idesc = hd_idesc(false, false, h.bn_v);
   hd_ring(p, kHdScore, static_cast<int32_t>(a_rows));
   p.target = l.target;
   p.n_sup = static_cast<int32_t>(sup.size());
@@ -1234,8 +1292,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   if (st != DLLM_OK) return st;
   void* fargs[] = {&f};
   return launch_pdl(reinterpret_cast<const void*>(&head_finish_kernel),
-                    dim3(static_cast<unsigned>(std::min<int64_t>((T + 31) / 32, dev->sms * 2))), dim3(kHdFinishWarps * 32), 0, stream,
-                    fargs);
+                    dim3(static_cast<unsigned>((T + 7) / 8)), dim3(kHdFinishWarps * 32), 0, stream, fargs);
 }
 
 dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride,
@@ -1309,26 +1366,26 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   p.grad_w_f32 = grad_weight_dt == DLLM_F32 ? 1 : 0;
   p.accumulate = accumulate != 0 ? 1 : 0;
   p.fault = reinterpret_cast<int32_t*>(ws);
-  HeadParams pz = p, ph = p, pw = p;
+  HeadParams pz = p, pb = p;
   const int64_t packed_rows = round_up(T, kHdBK);
   if (!make_map(&pz.tm_a, hidden, T, d, hidden_stride, a_rows) ||
       !make_map(&pz.tm_packed, ws + h.hidden, packed_rows, d, d, a_rows) ||
       !make_map(&pz.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v / 2)) ||
-      !make_map(&ph.tm_a, p.dz, h.t_pad, h.piece, h.piece, a_rows) || !make_map(&ph.tm_b, weight, V, d, weight_stride, 64) ||
-      !make_map(&pw.tm_a, p.dz, h.t_pad, h.piece, h.piece, 64) || !make_map(&pw.tm_b, hidden, T, d, hidden_stride, 64) ||
-      !make_map(&pw.tm_packed, ws + h.hidden, packed_rows, d, d, 64) ||
-      (grad_weight && grad_weight_dt == DLLM_BF16 && !make_map(&pw.tm_out, grad_weight, V, d, grad_weight_stride, 32)))
+      !make_map(&pb.tm_a, p.dz, h.t_pad, h.piece, h.piece, a_rows) || !make_map(&pb.tm_b, weight, V, d, weight_stride, 64) ||
+      !make_map(&pb.tm_aw, p.dz, h.t_pad, h.piece, h.piece, 64) || !make_map(&pb.tm_bw, hidden, T, d, hidden_stride, 64) ||
+      !make_map(&pb.tm_packed, ws + h.hidden, packed_rows, d, d, 64) ||
+      (grad_weight && grad_weight_dt == DLLM_BF16 && !make_map(&pb.tm_out, grad_weight, V, d, grad_weight_stride, 32)))
     return DLLM_ERR_CUDA;
   pz.bn = h.bn_v;
-  pz.n_n = h.n_v;
-  pz.idesc = hd_idesc(kHdDz, h.bn_v);
+  pz.idesc = hd_idesc(false, false, h.bn_v);
   hd_ring(pz, kHdDz, static_cast<int32_t>(a_rows));
-  ph.bn = pw.bn = h.bn_d;
-  ph.n_n = pw.n_n = h.n_d;
-  ph.idesc = hd_idesc(kHdDh, h.bn_d);
-  pw.idesc = hd_idesc(kHdDw, h.bn_d);
-  hd_ring(ph, kHdDh, static_cast<int32_t>(a_rows));
-  hd_ring(pw, kHdDw, kHdRows);
+  pb.bn = h.bn_d;
+  pb.n_n = h.n_d;
+  pb.idesc = hd_idesc(false, true, h.bn_d);
+  pb.idesc_w = hd_idesc(true, true, h.bn_d);
+  pb.want_h = grad_hidden ? 1 : 0;
+  pb.want_w = grad_weight ? 1 : 0;
+  hd_ring(pb, kHdBack, static_cast<int32_t>(a_rows));
 
   l.hidden = static_cast<const uint16_t*>(hidden);
   l.stride = hidden_stride;
@@ -1338,12 +1395,13 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   l.bn_d = h.bn_d;
   l.pairs = dev->sms / 2;
   l.slabs = static_cast<int32_t>((std::min(h.piece, V) + kHdBK - 1) / kHdBK);
+  l.dw_tiles = grad_weight ? (std::min(h.piece, V) + kHdBM - 1) / kHdBM * h.n_d : 0;
   l.room = h.acc;
   st = hd_list(l, h, ws, stream);
   if (st != DLLM_OK) return st;
   for (int64_t v0 = 0; v0 < V; v0 += h.piece) {
     const int64_t cols = std::min(h.piece, V - v0);
-    for (HeadParams* q : {&pz, &ph, &pw}) {
+    for (HeadParams* q : {&pz, &pb}) {
       q->v0 = v0;
       q->cols = cols;
       q->add = v0 > 0 ? 1 : 0;
@@ -1351,8 +1409,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
     // (to the end of the second product's last slab, where dz reads as zero)
     pz.n_n = static_cast<int32_t>((round_up(cols, kHdBK) + h.bn_v - 1) / h.bn_v);
     st = hd_launch<kHdDz>(pz, dev->sms, stream);
-    if (st == DLLM_OK && grad_hidden) st = hd_launch<kHdDh>(ph, dev->sms, stream);
-    if (st == DLLM_OK && grad_weight) st = hd_launch<kHdDw>(pw, dev->sms, stream);
+    if (st == DLLM_OK) st = hd_launch<kHdBack>(pb, dev->sms, stream);
     if (st != DLLM_OK) return st;
   }
   if (!grad_hidden) return DLLM_OK;
