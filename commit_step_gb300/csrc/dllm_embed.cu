@@ -298,17 +298,32 @@ __global__ void __launch_bounds__(kZeroThreads, 3) embed_zero_kernel(const __gri
       const int64_t v1 = min(V, v0 + kZeroBits);
       for (int i = threadIdx.x; i < (v1 - v0 + 31) / 32; i += kZeroThreads) em_named[i] = 0u;
       __syncthreads();
+      // Token i lies at row i / L, column i mod L; a step of the threads' number adds to both.
+      const uint32_t L = p.tok.L.d, down = p.tok.L(kZeroThreads), along = kZeroThreads - down * L;
+      const uint32_t b0 = p.tok.L(threadIdx.x);
+      uint32_t l = threadIdx.x - b0 * L;
+      const int32_t* at = p.tok.at + b0 * p.tok.stride + l;
+      const int64_t step = down * p.tok.stride + along, wrap = p.tok.stride - L;
+      const uint32_t span = static_cast<uint32_t>(v1 - v0), first = static_cast<uint32_t>(v0);
       for (int64_t i0 = threadIdx.x; i0 < p.tok.T; i0 += 8 * kZeroThreads) {
-        int32_t v[8];
+        uint32_t v[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = i0 + q * kZeroThreads < p.tok.T ? p.tok[i0 + q * kZeroThreads] : static_cast<int32_t>(V);
+        for (int q = 0; q < 8; ++q) {
+          v[q] = i0 + q * kZeroThreads < p.tok.T ? static_cast<uint32_t>(*at) - first : 0xFFFFFFFFu;
+          at += step;
+          l += along;
+          if (l >= L) {
+            l -= L;
+            at += wrap;
+          }
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (v[q] >= v0 && v[q] < v1) {
+          if (v[q] < span) {
             // (a frequent token is marked once: atomics on one word take their turns)
-            volatile uint32_t* word = &em_named[(v[q] - v0) >> 5];
+            volatile uint32_t* word = &em_named[v[q] >> 5];
             const uint32_t bit = 1u << (v[q] & 31);
-            if (!(*word & bit)) atomicOr(&em_named[(v[q] - v0) >> 5], bit);
+            if (!(*word & bit)) atomicOr(&em_named[v[q] >> 5], bit);
           }
       }
       __syncthreads();
@@ -420,7 +435,7 @@ __device__ __forceinline__ void run_write(const RunParams& p, int64_t row, int64
 // meet those of its neighbours in shared memory, where warp 0 walks the chunks in
 // order, and only the runs that reach over the block's ends become parts.
 template <bool BF16, bool OUT16>
-__global__ void __launch_bounds__(kRunWarps * 32) embed_sum_kernel(const __grid_constant__ RunParams p) {
+__global__ void __launch_bounds__(kRunWarps * 32, 4) embed_sum_kernel(const __grid_constant__ RunParams p) {
   constexpr int kCols = RunLane<BF16>::kCols;
   constexpr int kAhead = 8;
   __shared__ float4 edge[kRunWarps][2][kCols / 4][32];

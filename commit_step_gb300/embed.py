@@ -11,24 +11,29 @@ from .cache import _raw_stream
 from .head import _size, _workspace
 
 
+_DTYPES = {torch.bfloat16: DLLM_BF16, torch.float32: DLLM_F32}
+
+
 def _dtype(t, name: str) -> int:
-    if not torch.is_tensor(t) or t.dtype not in (torch.bfloat16, torch.float32):
+    code = _DTYPES.get(t.dtype) if torch.is_tensor(t) else None
+    if code is None:
         raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
-    return DLLM_BF16 if t.dtype == torch.bfloat16 else DLLM_F32
+    return code
 
 
-def _canvas(tokens, device):
+def _canvas(tokens, index: int):
     """(B, L, row stride) of (T,) or (B, L) int32 tokens, unit stride over the last dimension."""
     if not torch.is_tensor(tokens) or tokens.dtype != torch.int32 or tokens.dim() not in (1, 2):
         raise TypeError("tokens must be a (T,) or (B, L) int32 tensor")
-    if tokens.device != device:
-        raise ValueError(f"tokens are on {tokens.device}; the call runs on {device}")
-    if tokens.shape[-1] > 1 and tokens.stride(-1) != 1:
+    if tokens.get_device() != index:
+        raise ValueError(f"tokens are on {tokens.device}; the call runs on cuda:{index}")
+    shape, strides = tokens.shape, tokens.stride()
+    L = shape[-1]
+    if L > 1 and strides[-1] != 1:
         raise ValueError("tokens need unit stride over their last dimension")
-    if tokens.dim() == 1:
-        return 1, tokens.shape[0], tokens.shape[0]
-    B, L = tokens.shape
-    return B, L, (tokens.stride(0) if B > 1 else L)
+    if len(shape) == 1:
+        return 1, L, L
+    return shape[0], L, (strides[0] if shape[0] > 1 else L)
 
 
 def _weight(t, name: str, V: int, d: int) -> int:
@@ -51,21 +56,22 @@ def embed_tokens(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
     if stream is not None:
         with torch.cuda.stream(stream):
             return embed_tokens(tokens, weight, scale, out)
-    _need_cuda(tokens, weight)
-    dt = _dtype(weight, "weight")
+    dt, idx = _dtype(weight, "weight"), weight.get_device()
+    if idx < 0:
+        raise ValueError("device tensors are required")
     if weight.dim() != 2:
         raise ValueError("weight must be (V, d)")
-    V, d = weight.shape
-    stride = _weight(weight, "weight", V, d)
-    dev = weight.device
-    B, L, t_stride = _canvas(tokens, dev)
+    (V, d), (stride, unit) = weight.shape, weight.stride()
+    if d > 1 and unit != 1:
+        raise ValueError("weight needs unit column stride")
+    B, L, t_stride = _canvas(tokens, idx)
     if out is None:
-        out = torch.empty((*tokens.shape, d), dtype=weight.dtype, device=dev)
-    elif (not torch.is_tensor(out) or out.dtype != weight.dtype or out.device != dev or out.shape != (*tokens.shape, d)
-          or not out.is_contiguous()):
+        out = weight.new_empty((*tokens.shape, d))
+    elif (not torch.is_tensor(out) or out.dtype != weight.dtype or out.get_device() != idx
+          or out.shape != (*tokens.shape, d) or not out.is_contiguous()):
         raise ValueError("out must be a contiguous (..., d) tensor of weight's dtype, on the same device")
-    _check(_lib.dllm_embed_tokens(tokens.data_ptr(), B, L, t_stride, weight.data_ptr(), dt, V, d, stride, scale,
-                                  out.data_ptr(), _raw_stream(None, weight.get_device())), "dllm_embed_tokens")
+    _check(_lib.dllm_embed_tokens(tokens.data_ptr(), B, L, t_stride, weight.data_ptr(), dt, V, d, stride if V > 1 else d,
+                                  scale, out.data_ptr(), _raw_stream(None, idx)), "dllm_embed_tokens")
     return out
 
 
@@ -83,7 +89,7 @@ def embed_tokens_backward(tokens: torch.Tensor, grad: torch.Tensor, V: int, scal
     _need_cuda(tokens, grad)
     dt = _dtype(grad, "grad")
     dev, idx, V = grad.device, grad.get_device(), int(V)
-    B, L, t_stride = _canvas(tokens, dev)
+    B, L, t_stride = _canvas(tokens, idx)
     if grad.shape[:-1] != tokens.shape or not grad.is_contiguous():
         raise ValueError("grad must be a contiguous tensor of the tokens' shape and d")
     if not 0 < V < 1 << 31:

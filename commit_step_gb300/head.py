@@ -95,9 +95,9 @@ def lm_head_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
     T, d, stride, V, w_stride = _ends(hidden, weight, targets)
     dev, idx = hidden.device, hidden.get_device()
     if out is None:
-        out = [torch.empty(hidden.shape[:-1], dtype=torch.float32, device=dev) for _ in range(3)]
-        lp, ent, lse = out
-        at = [t.data_ptr() for t in out]
+        lp = hidden.new_empty(hidden.shape[:-1], dtype=torch.float32)
+        ent, lse = torch.empty_like(lp), torch.empty_like(lp)
+        at = lp.data_ptr(), ent.data_ptr(), lse.data_ptr()
     else:
         lp, ent, lse = out
         at = [_at(t, name, T, _F32, idx, dev) for t, name in ((lp, "logprob"), (ent, "entropy"), (lse, "lse"))]
