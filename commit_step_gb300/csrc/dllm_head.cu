@@ -62,6 +62,15 @@ constexpr float kHdAbsent = -0x1p+126f;          // suppressed ids and columns p
 
 enum HeadOp { kHdScore, kHdDz, kHdBack };         // the last: dH and dW, tiles of both in one launch
 
+// The tensor core adds in fp32 and cuts off what does not fit: summed in one
+// accumulator, the logits of d = 4096 were off by 4e-6 of themselves, always toward
+// zero, and a confident row's log probability by 2e-5.  So an accumulator takes some
+// slabs of K, and these parts are added in registers, rounded.  Errors of the scores
+// of 8 rows of d = 4096 and 4096 x 152064 x 3584 rows' time in one part, in parts of
+// 16, 8 and 4 slabs: 5e-6, 1.3e-6, 6e-7, 2e-7 and 2506, 2507, 2605, 2750 us.  dz, which
+// is rounded to bf16, only has to agree with a log-sum-exp so formed.
+__host__ __device__ constexpr int hd_part(int op) { return op == kHdScore ? 8 : 16; }
+
 // A scored row's constants of the backward pass.
 struct HeadRow {
   float lse, entropy, g, gh;
@@ -175,8 +184,9 @@ __device__ __forceinline__ uint32_t hd_leader(uint32_t addr) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
+// (no memory is passed on, and a release over the cluster took a microsecond)
 __device__ __forceinline__ void hd_arrive_leader(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void hd_cluster_sync() {
   __syncwarp();
@@ -196,6 +206,17 @@ __device__ __forceinline__ void hd_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 16 columns.
+__device__ __forceinline__ void hd_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
@@ -565,93 +586,106 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         if (t.k0 == t.k1) continue;
         const bool dw = OP == kHdBack && t.dw;
         const uint32_t idesc = dw ? p.idesc_w : p.idesc, step_a = (dw ? 2048u : 32u) >> 4;
-        const int buf = j & 1;
-        if (!__all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&acce_bar[buf]), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag))) {
-          if (lane == 0) hd_fail(p, abort_flag, kFaultEmptyWait);
-          break;
-        }
-        hd_fence_after();
-        const uint32_t d_tmem = tmem + static_cast<uint32_t>(buf * kHdBN);
-        for (int k = t.k0; k < t.k1; ++k) {
-          ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&full_bar[s]), ph, abort_flag));
+        const int part = OP == kHdBack ? t.k1 - t.k0 : hd_part(OP);
+        for (int k0 = t.k0; k0 < t.k1 && ok; k0 += part, ++j) {
+          const int buf = j & 1;
+          ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&acce_bar[buf]), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag));
           if (!ok) {
-            if (lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
+            if (lane == 0) hd_fail(p, abort_flag, kFaultEmptyWait);
             break;
           }
           hd_fence_after();
-          const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes;
-          const uint32_t da = hd_desc(a), db = hd_desc(a + kHdABytes);
+          const uint32_t d_tmem = tmem + static_cast<uint32_t>(buf * kHdBN);
+          for (int k = k0; k < t.k1 && k < k0 + part; ++k) {
+            ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&full_bar[s]), ph, abort_flag));
+            if (!ok) {
+              if (lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
+              break;
+            }
+            hd_fence_after();
+            const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes;
+            const uint32_t da = hd_desc(a), db = hd_desc(a + kHdABytes);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes of a K-major row, 16 rows of 128 bytes MN-major
-            hd_mma(lead, d_tmem, da + kk * step_a, db + kk * ((OP == kHdBack ? 2048 : 32) >> 4), idesc, k != t.k0 || kk != 0 ? 1u : 0u);
-          hd_commit(lead, smem_addr(&empty_bar[s]));
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
+            for (int kk = 0; kk < 4; ++kk)  // 16 k: 32 bytes of a K-major row, 16 rows of 128 bytes MN-major
+              hd_mma(lead, d_tmem, da + kk * step_a, db + kk * ((OP == kHdBack ? 2048 : 32) >> 4), idesc, k != k0 || kk != 0 ? 1u : 0u);
+            hd_commit(lead, smem_addr(&empty_bar[s]));
+            if (++s == p.stages) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
+          hd_commit(lead, smem_addr(&accf_bar[buf]));
         }
-        hd_commit(lead, smem_addr(&accf_bar[buf]));
-        ++j;
       }
     }
   } else if (warp < kHdEpiWarps) {
     const int ew = warp & 3, half = warp >> 2;
-    const uint32_t store_buf = ring + kHdRing - (kHdEpiWarps - warp) * kHdStoreBytes;   // (dw: behind the last stage)
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(ew * 32) << 16);
+    const uint32_t store_buf = ring + kHdRing - (kHdEpiWarps - warp) * kHdStoreBytes;   // (back: behind the last stage)
     HeadSoft soft{-kHdCap, 0.0f, 0.0f};
     int j = 0;
+    // The next accumulator: warp-uniform, since the TMEM loads are .sync.aligned.
+    auto await = [&] {
+      const bool ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&accf_bar[j & 1]), static_cast<uint32_t>((j >> 1) & 1), abort_flag));
+      if (!ok && lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
+      hd_fence_after();
+      return ok;
+    };
+    // It has been read.
+    auto release = [&] {
+      hd_fence_before();
+      __syncwarp();
+      if (lane == 0) hd_arrive_leader(hd_leader(smem_addr(&acce_bar[j & 1])));
+      ++j;
+    };
     for (int64_t it = 0; work.tile(it, t); ++it) {
       if (t.k0 == t.k1) continue;
       const bool dw = OP == kHdBack && t.dw;
-      const int buf = j & 1;
       const int64_t row = static_cast<int64_t>(t.m) * kHdBM + rank * kHdRows + ew * 32 + lane;  // scored row, or (dw) id of the piece
-      HeadRow info{};
-      int32_t target = -1;
-      if (OP == kHdScore && row < n) target = p.target[row];
-      if (OP == kHdDz && row < n) {
-        target = p.target[row];
-        info = p.row[row];
-      }
-      // warp-uniform: the TMEM loads below are .sync.aligned
-      const bool ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&accf_bar[buf]), static_cast<uint32_t>((j >> 1) & 1), abort_flag));
-      if (!ok) {
-        if (lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
-        break;
-      }
-      hd_fence_after();
-      ++j;
       const int64_t col0 = static_cast<int64_t>(t.n) * p.bn;
       const int64_t width = OP != kHdBack ? p.cols : p.d;
       const int in_tile = static_cast<int>(min(static_cast<int64_t>(p.bn), width - col0));
-      if (work.n_m > 1) soft = HeadSoft{-kHdCap, 0.0f, 0.0f};
       // Rows a warp has to visit: those that exist; of dz also the rows up to the
       // end of the third product's last slab, which read as zero.
       const int64_t visit = dw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : n);
       const bool warp_rows = row - lane < visit;
-      bool released = false;
-      auto release = [&] {                               // the accumulator has been read
-        hd_fence_before();
-        __syncwarp();
-        if (lane == 0) hd_arrive_leader(hd_leader(smem_addr(&acce_bar[buf])));
-        released = true;
-      };
-      if (dw && !p.grad_w_f32 && !p.accumulate) {
-        if (warp_rows)
-          for (int c = half * 64; c < in_tile; c += 128) {
-            hd_store_tile(tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * kHdBN + c),
-                          store_buf, &p.tm_out, static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane,
-                          lane, [&] {
-                            if (c + 128 >= in_tile) release();
-                          });
+      if constexpr (OP != kHdBack) {
+        HeadRow info{};
+        int32_t target = -1;
+        if (row < n) target = p.target[row];
+        if (OP == kHdDz && row < n) info = p.row[row];
+        // The logits of this thread's row in the chunks 32 (2 i + half).
+        float z[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = 0; q < 32; ++q) z[i][q] = 0.0f;
+        bool ok = true;
+        for (int k = 0; k < t.k1 && ok; k += hd_part(OP)) {
+          ok = await();
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 64 * i + 32 * half;
+            if (warp_rows && c < in_tile) {
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                uint32_t r[16];
+                hd_ld16(lanes + static_cast<uint32_t>((j & 1) * kHdBN + c + h), r);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) z[i][h + q] += __uint_as_float(r[q]);
+              }
+            }
           }
-      } else
-#pragma unroll 1
-      for (int c = half * 32; c < p.bn; c += 64) {
-        if (!warp_rows || (c >= in_tile && OP != kHdDz)) break;
-        uint32_t r[32];
-        hd_ld32(tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * kHdBN + c), r);
-        const int lim = min(32, in_tile - c);
-        float x[32];
-        if (OP != kHdBack) {
+          release();
+        }
+        if (!ok) break;
+        if (work.n_m > 1) soft = HeadSoft{-kHdCap, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 64 * i + 32 * half;
+          if (!warp_rows || c >= p.bn || (OP == kHdScore && c >= in_tile)) continue;
+          const int lim = min(32, in_tile - c);
           const int64_t v = p.v0 + col0 + c;
           const uint32_t absent = lim <= 0 ? 0xFFFFFFFFu : hd_absent(sup_s, p.n_sup, v, lim);
           const int64_t hit = target - v;
@@ -660,25 +694,25 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
               float zt = 0.0f;
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if (q == hit) zt = __uint_as_float(r[q]);
+                if (q == hit) zt = z[i][q];
               if (hit < lim) p.z_target[row] = fminf(fmaxf(zt, -kHdCap), kHdCap);
             }
 #pragma unroll
-            for (int q = 0; q < 32; ++q) x[q] = fminf(fmaxf(__uint_as_float(r[q]), -kHdCap), kHdCap);
+            for (int q = 0; q < 32; ++q) z[i][q] = fminf(fmaxf(z[i][q], -kHdCap), kHdCap);
             if (absent != 0u) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if ((absent >> q) & 1u) x[q] = kHdAbsent;
+                if ((absent >> q) & 1u) z[i][q] = kHdAbsent;
             }
             float cm[4] = {-kHdCap, -kHdCap, -kHdCap, -kHdCap};
 #pragma unroll
-            for (int q = 0; q < 32; ++q) cm[q & 3] = fmaxf(cm[q & 3], x[q]);
+            for (int q = 0; q < 32; ++q) cm[q & 3] = fmaxf(cm[q & 3], z[i][q]);
             const float m = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
             if (m > soft.m) hd_raise(soft, m);
             float Z[4] = {0.0f, 0.0f, 0.0f, 0.0f}, S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-              const float y = (x[q] - soft.m) * kLog2e, e = ex2_approx(y);
+              const float y = (z[i][q] - soft.m) * kLog2e, e = ex2_approx(y);
               Z[q & 3] += e;
               S[q & 3] = fmaf(e, y, S[q & 3]);
             }
@@ -687,44 +721,61 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
           } else {
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-              const float y = fmaxf(__uint_as_float(r[q]), -kHdCap) - info.lse;
+              const float y = fmaxf(z[i][q], -kHdCap) - info.lse;
               const float e = ex2_approx(y * kLog2e);
-              x[q] = -e * fmaf(info.gh, y + info.entropy, info.g);
+              z[i][q] = -e * fmaf(info.gh, y + info.entropy, info.g);
             }
             if (hit >= 0 && hit < 32) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if (q == hit) x[q] += info.g;
+                if (q == hit) z[i][q] += info.g;
             }
             if (absent != 0u || row >= n) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if (((absent >> q) & 1u) || row >= n) x[q] = 0.0f;
+                if (((absent >> q) & 1u) || row >= n) z[i][q] = 0.0f;
             }
             // (up to the tile's end and the row's; what is there past the piece reads as zero)
             const int room = static_cast<int>(min(static_cast<int64_t>(p.bn - c), p.dz_stride - col0 - c));
-            if (row < visit) hd_store_dz(p.dz + row * p.dz_stride + col0 + c, x, room);
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(r[q]);
-          if (row < visit) {
-            if (!dw) {
-              float* out = p.acc + (static_cast<int64_t>(t.split) * work.n_m * kHdBM + row) * p.acc_stride + col0 + c;
-              hd_store_f32(out, x, lim, p.add != 0);
-            } else if (p.grad_w_f32) {
-              hd_store_f32(static_cast<float*>(p.grad_w) + (p.v0 + row) * p.grad_w_stride + col0 + c, x, lim, p.accumulate != 0);
-            } else {
-              hd_store_bf16(static_cast<uint16_t*>(p.grad_w) + (p.v0 + row) * p.grad_w_stride + col0 + c, x, lim,
-                            p.accumulate != 0);
-            }
+            if (row < visit) hd_store_dz(p.dz + row * p.dz_stride + col0 + c, z[i], room);
           }
         }
+        // With one row tile a thread keeps its row's state from tile to tile.
+        if (OP == kHdScore && row < n && (work.n_m > 1 || (it + 1) * work.pairs + work.pair >= work.total))
+          p.part[((work.n_m > 1 ? t.n : work.pair) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
+      } else {
+        if (!await()) break;
+        const uint32_t from = lanes + static_cast<uint32_t>((j & 1) * kHdBN);
+        bool released = false;
+        if (dw && !p.grad_w_f32 && !p.accumulate) {
+          if (warp_rows)
+            for (int c = half * 64; c < in_tile; c += 128)
+              hd_store_tile(from + c, store_buf, &p.tm_out, static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane, lane, [&] {
+                if (c + 128 >= in_tile) {
+                  release();
+                  released = true;
+                }
+              });
+        } else {
+#pragma unroll 1
+          for (int c = half * 32; warp_rows && c < in_tile; c += 64) {
+            uint32_t r[32];
+            hd_ld32(from + c, r);
+            const int lim = min(32, in_tile - c);
+            float x[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(r[q]);
+            if (row >= visit) continue;
+            if (!dw)
+              hd_store_f32(p.acc + (static_cast<int64_t>(t.split) * work.n_m * kHdBM + row) * p.acc_stride + col0 + c, x, lim, p.add != 0);
+            else if (p.grad_w_f32)
+              hd_store_f32(static_cast<float*>(p.grad_w) + (p.v0 + row) * p.grad_w_stride + col0 + c, x, lim, p.accumulate != 0);
+            else
+              hd_store_bf16(static_cast<uint16_t*>(p.grad_w) + (p.v0 + row) * p.grad_w_stride + col0 + c, x, lim, p.accumulate != 0);
+          }
+        }
+        if (!released) release();
       }
-      if (!released) release();
-      // With one row tile a thread keeps its row's state from tile to tile.
-      if (OP == kHdScore && row < n && (work.n_m > 1 || (it + 1) * work.pairs + work.pair >= work.total))
-        p.part[((work.n_m > 1 ? t.n : work.pair) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
     }
     if (OP == kHdBack && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
