@@ -269,6 +269,7 @@ struct ZeroParams {
   int64_t row_bytes;
   EmDiv vecs;                   // 16-byte vectors of a row
   int32_t rows;                 // rows of a group: a power of two
+  int32_t* fault;
 };
 
 __global__ void __launch_bounds__(kZeroThreads, 3) embed_zero_kernel(const __grid_constant__ ZeroParams p) {
@@ -335,7 +336,10 @@ __global__ void __launch_bounds__(kZeroThreads, 3) embed_zero_kernel(const __gri
       if (!((em_named[bit >> 5] >> (bit & 31)) & 1u))
         reinterpret_cast<uint4*>(p.out + (r0 + r) * p.row_bytes)[j - r * p.vecs.d] = make_uint4(0u, 0u, 0u, 0u);
     }
-    if (!mbar_wait_bounded(bar, phase)) break;
+    if (!mbar_wait_bounded(bar, phase)) {
+      if (threadIdx.x == 0) atomicExch(p.fault, kFaultFullWait);
+      break;
+    }
     uint32_t more;
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\tld.shared.b128 a, [%2];\n\tmov.u32 %1, 0;\n\t"
@@ -645,7 +649,7 @@ EmPlan em_plan(int64_t T, int64_t V, int64_t d) {
   e.chunk = 8;
   while (e.chunk < kRunMost && T * ((d + 255) / 256) > static_cast<int64_t>(e.chunk) * 152 * 16) e.chunk *= 2;
   e.blocks = (T + kRunWarps * e.chunk - 1) / (kRunWarps * e.chunk);
-  size_t at = 0;
+  size_t at = 256;                                       // the fault word
   auto take = [&at](int64_t bytes) {
     const size_t here = at;
     at += static_cast<size_t>((bytes + 255) / 256 * 256);
@@ -691,9 +695,11 @@ dllm_status dllm_embed_tokens(const int32_t* tokens, int64_t B, int64_t L, int64
   if (T == 0) return DLLM_OK;
   if (!out) return DLLM_ERR_INVALID_ARGUMENT;
   if (!aligned16(out)) return DLLM_ERR_UNSUPPORTED;
+  const int64_t size = dt == DLLM_BF16 ? 2 : 4;
+  if (overlapping({extent(out, T, d, d, size)}, {extent(weight, V, d, weight_stride, size), extent(tokens, B, L, token_stride, 4)}))
+    return DLLM_ERR_INVALID_ARGUMENT;
   const int sms = em_sms();
   if (sms == 0) return DLLM_ERR_CUDA;
-  const int64_t size = dt == DLLM_BF16 ? 2 : 4;
   EmbedTokens tok{tokens, em_div(static_cast<uint32_t>(L)), token_stride, T, V};
   const uint8_t* w = static_cast<const uint8_t*>(weight);
   int64_t row_bytes = weight_stride * size;
@@ -725,6 +731,10 @@ dllm_status dllm_embed_tokens_backward(const int32_t* tokens, int64_t B, int64_t
   if (!aligned16(grad_weight) || d % group != 0 || grad_weight_stride % group != 0) return DLLM_ERR_UNSUPPORTED;
   if (T > 0 && (!workspace || workspace_bytes < dllm_embed_tokens_backward_workspace_size(T, V, d))) return DLLM_ERR_WORKSPACE;
   if (T > 0 && !aligned16(workspace)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (overlapping({extent(grad_weight, V, d, grad_weight_stride, size),
+                   Extent{workspace, static_cast<int64_t>(dllm_embed_tokens_backward_workspace_size(T, V, d))}},
+                  {extent(grad, T, d, d, grad_dt == DLLM_BF16 ? 2 : 4), extent(tokens, B, L, token_stride, 4)}))
+    return DLLM_ERR_INVALID_ARGUMENT;
   const int sms = em_sms();
   if (sms == 0) return DLLM_ERR_CUDA;
   if (T == 0) {  // no token: the gradient is zero
@@ -773,6 +783,7 @@ dllm_status dllm_embed_tokens_backward(const int32_t* tokens, int64_t B, int64_t
   ZeroParams z{};
   z.tok = k.tok;
   z.out = static_cast<uint8_t*>(grad_weight);
+  z.fault = reinterpret_cast<int32_t*>(ws);
   z.row_bytes = grad_weight_stride * size;
   z.vecs = em_div(static_cast<uint32_t>(d * size / 16));
   z.rows = 1;

@@ -135,7 +135,8 @@ __device__ __forceinline__ uint32_t hd_elect() {
 // What follows is issued by the one thread of the warp whose `lead` is set; the whole
 // warp executes the code around it, so that addresses and descriptors stay in uniform
 // registers (formed by a single thread, a product and a load held a slab up by some
-// 170 and 190 cycles each: 32 x 126464 x 4096 took 187 us, and [BLOCK] so).
+// 170 and 190 cycles each: 32 x 126464 x 4096 took 187 us and takes 169 so, 4506 x 126464 x 4096
+// backward 9.0 and 8.4 ms).
 
 // A load of this CTA's shared memory that counts on the leader's barrier.
 __device__ __forceinline__ void hd_load(uint32_t lead, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -418,7 +419,8 @@ __device__ __forceinline__ void hd_store_dz(uint16_t* out, const float (&x)[32],
 // This warp's 32 rows of 64 accumulator columns at taddr, as bf16, to columns x and
 // rows y of the tensor: through shared memory in the 128-byte swizzle and out by
 // TMA, so that memory sees whole lines (stored from registers, a row a thread, the
-// weight's gradient took 504 us where it now takes [DW] at 512 x 126464 x 4096).
+// weight's gradient of 512 x 126464 x 4096 took 504 us in a launch of its own, and 381
+// so).
 // `done` is called once the accumulator has been read.
 template <class Done>
 __device__ __forceinline__ void hd_store_tile(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane, Done done) {
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   for (int q = threadIdx.x; q < p.n_sup; q += blockDim.x) sup_s[q] = p.sup[q];
   // Few rows: what the loads of A leave out of its place reads as zero (the products
   // of rows that do not exist then draw little power, which the weight's stream
-  // would pay for in clocks: [ZERO]).
+  // would pay for in clocks: 32 x 126464 x 4096 183 and 169 us).
   if (p.clear_a) {
     for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(p.stages) * (kHdABytes / 16); i += kHdThreads)
       asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i / (kHdABytes / 16) * p.stage_bytes + i % (kHdABytes / 16) * 16),
@@ -654,37 +656,10 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         int32_t target = -1;
         if (row < n) target = p.target[row];
         if (OP == kHdDz && row < n) info = p.row[row];
-        // The logits of this thread's row in the chunks 32 (2 i + half).
-        float z[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int q = 0; q < 32; ++q) z[i][q] = 0.0f;
-        bool ok = true;
-        for (int k = 0; k < t.k1 && ok; k += hd_part(OP)) {
-          ok = await();
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = 64 * i + 32 * half;
-            if (warp_rows && c < in_tile) {
-#pragma unroll
-              for (int h = 0; h < 32; h += 16) {
-                uint32_t r[16];
-                hd_ld16(lanes + static_cast<uint32_t>((j & 1) * kHdBN + c + h), r);
-#pragma unroll
-                for (int q = 0; q < 16; ++q) z[i][h + q] += __uint_as_float(r[q]);
-              }
-            }
-          }
-          release();
-        }
-        if (!ok) break;
         if (work.n_m > 1) soft = HeadSoft{-kHdCap, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 64 * i + 32 * half;
-          if (!warp_rows || c >= p.bn || (OP == kHdScore && c >= in_tile)) continue;
+        const int end = !warp_rows ? 0 : (OP == kHdScore ? in_tile : p.bn);
+        // What becomes of 32 columns of this thread's row, from column c of the tile.
+        auto chunk = [&](float (&z)[32], int c) {
           const int lim = min(32, in_tile - c);
           const int64_t v = p.v0 + col0 + c;
           const uint32_t absent = lim <= 0 ? 0xFFFFFFFFu : hd_absent(sup_s, p.n_sup, v, lim);
@@ -694,25 +669,25 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
               float zt = 0.0f;
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if (q == hit) zt = z[i][q];
+                if (q == hit) zt = z[q];
               if (hit < lim) p.z_target[row] = fminf(fmaxf(zt, -kHdCap), kHdCap);
             }
 #pragma unroll
-            for (int q = 0; q < 32; ++q) z[i][q] = fminf(fmaxf(z[i][q], -kHdCap), kHdCap);
+            for (int q = 0; q < 32; ++q) z[q] = fminf(fmaxf(z[q], -kHdCap), kHdCap);
             if (absent != 0u) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if ((absent >> q) & 1u) z[i][q] = kHdAbsent;
+                if ((absent >> q) & 1u) z[q] = kHdAbsent;
             }
             float cm[4] = {-kHdCap, -kHdCap, -kHdCap, -kHdCap};
 #pragma unroll
-            for (int q = 0; q < 32; ++q) cm[q & 3] = fmaxf(cm[q & 3], z[i][q]);
+            for (int q = 0; q < 32; ++q) cm[q & 3] = fmaxf(cm[q & 3], z[q]);
             const float m = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
             if (m > soft.m) hd_raise(soft, m);
             float Z[4] = {0.0f, 0.0f, 0.0f, 0.0f}, S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-              const float y = (z[i][q] - soft.m) * kLog2e, e = ex2_approx(y);
+              const float y = (z[q] - soft.m) * kLog2e, e = ex2_approx(y);
               Z[q & 3] += e;
               S[q & 3] = fmaf(e, y, S[q & 3]);
             }
@@ -721,24 +696,67 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
           } else {
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-              const float y = fmaxf(z[i][q], -kHdCap) - info.lse;
+              const float y = fmaxf(z[q], -kHdCap) - info.lse;
               const float e = ex2_approx(y * kLog2e);
-              z[i][q] = -e * fmaf(info.gh, y + info.entropy, info.g);
+              z[q] = -e * fmaf(info.gh, y + info.entropy, info.g);
             }
             if (hit >= 0 && hit < 32) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if (q == hit) z[i][q] += info.g;
+                if (q == hit) z[q] += info.g;
             }
             if (absent != 0u || row >= n) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if (((absent >> q) & 1u) || row >= n) z[i][q] = 0.0f;
+                if (((absent >> q) & 1u) || row >= n) z[q] = 0.0f;
             }
             // (up to the tile's end and the row's; what is there past the piece reads as zero)
             const int room = static_cast<int>(min(static_cast<int64_t>(p.bn - c), p.dz_stride - col0 - c));
-            if (row < visit) hd_store_dz(p.dz + row * p.dz_stride + col0 + c, z[i], room);
+            if (row < visit) hd_store_dz(p.dz + row * p.dz_stride + col0 + c, z, room);
           }
+        };
+        if (t.k1 <= hd_part(OP)) {
+          // One part: chunk by chunk.
+          if (!await()) break;
+#pragma unroll 1
+          for (int c = 32 * half; c < end; c += 64) {
+            uint32_t r[32];
+            float z[32];
+            hd_ld32(lanes + static_cast<uint32_t>((j & 1) * kHdBN + c), r);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) z[q] = __uint_as_float(r[q]);
+            chunk(z, c);
+          }
+          release();
+        } else {
+          float z[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 32; ++q) z[i][q] = 0.0f;
+          bool ok = true;
+          for (int k = 0; k < t.k1 && ok; k += hd_part(OP)) {
+            ok = await();
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = 64 * i + 32 * half;
+              if (warp_rows && c < in_tile) {
+#pragma unroll
+                for (int h = 0; h < 32; h += 16) {
+                  uint32_t r[16];
+                  hd_ld16(lanes + static_cast<uint32_t>((j & 1) * kHdBN + c + h), r);
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) z[i][h + q] += __uint_as_float(r[q]);
+                }
+              }
+            }
+            release();
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (64 * i + 32 * half < end) chunk(z[i], 64 * i + 32 * half);
         }
         // With one row tile a thread keeps its row's state from tile to tile.
         if (OP == kHdScore && row < n && (work.n_m > 1 || (it + 1) * work.pairs + work.pair >= work.total))
@@ -1275,8 +1293,13 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   dllm_status st = hd_check(hidden, T, d, hidden_stride, weight, V, weight_stride, targets, suppress_ids, n_suppress, sup);
   if (st != DLLM_OK || T == 0) return st;
   if (!logprob || !entropy || !lse || !aligned4(logprob) || !aligned4(entropy) || !aligned4(lse)) return DLLM_ERR_INVALID_ARGUMENT;
-  if (!workspace || workspace_bytes < dllm_lm_head_logprobs_workspace_size(T, V, d)) return DLLM_ERR_WORKSPACE;
+  const size_t need = dllm_lm_head_logprobs_workspace_size(T, V, d);
+  if (!workspace || workspace_bytes < need) return DLLM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (overlapping({extent(logprob, 1, T, T, 4), extent(entropy, 1, T, T, 4), extent(lse, 1, T, T, 4),
+                   Extent{workspace, static_cast<int64_t>(need)}},
+                  {extent(hidden, T, d, hidden_stride, 2), extent(weight, V, d, weight_stride, 2), extent(targets, 1, T, T, 4)}))
+    return DLLM_ERR_INVALID_ARGUMENT;
   const HdDevice* dev = hd_device();
   if (!dev) return DLLM_ERR_CUDA;
   const HdPlan h = hd_plan(T, V, d, dev->sms, false);
@@ -1373,8 +1396,16 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   }
   if (!lse || !entropy || !aligned4(lse) || !aligned4(entropy) || !aligned4(grad_logprob) || !aligned4(grad_entropy))
     return DLLM_ERR_INVALID_ARGUMENT;
-  if (!workspace || workspace_bytes < dllm_lm_head_logprobs_backward_workspace_size(T, V, d)) return DLLM_ERR_WORKSPACE;
+  const size_t need = dllm_lm_head_logprobs_backward_workspace_size(T, V, d);
+  if (!workspace || workspace_bytes < need) return DLLM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (overlapping({extent(grad_hidden, T, d, grad_hidden_stride, 2),
+                   extent(grad_weight, V, d, grad_weight_stride, grad_weight_dt == DLLM_F32 ? 4 : 2),
+                   Extent{workspace, static_cast<int64_t>(need)}},
+                  {extent(hidden, T, d, hidden_stride, 2), extent(weight, V, d, weight_stride, 2), extent(targets, 1, T, T, 4),
+                   extent(lse, 1, T, T, 4), extent(entropy, 1, T, T, 4), extent(grad_logprob, 1, T, T, 4),
+                   extent(grad_entropy, 1, T, T, 4)}))
+    return DLLM_ERR_INVALID_ARGUMENT;
   const HdDevice* dev = hd_device();
   if (!dev) return DLLM_ERR_CUDA;
   const HdPlan h = hd_plan(T, V, d, dev->sms, true);

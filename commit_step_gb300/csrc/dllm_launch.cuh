@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 #include "../../include/dllmcommit.h"
@@ -40,6 +41,30 @@ inline int64_t mul_or_neg(int64_t a, int64_t b) {
   if (a < 0 || b < 0) return -1;
   if (a == 0 || b == 0) return 0;
   return a > lim / b ? -1 : a * b;
+}
+
+// The bytes of rows x cols elements of `size` bytes, rows `stride` elements apart.
+struct Extent {
+  const void* at;
+  int64_t bytes;
+};
+inline Extent extent(const void* at, int64_t rows, int64_t cols, int64_t stride, int64_t size) {
+  return {at, at && rows > 0 ? ((rows - 1) * stride + cols) * size : 0};
+}
+inline bool overlap(Extent a, Extent b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+// Whether an output overlaps an input, or another output.
+template <size_t N, size_t M>
+inline bool overlapping(const Extent (&outs)[N], const Extent (&ins)[M]) {
+  for (size_t i = 0; i < N; ++i) {
+    for (const Extent& in : ins)
+      if (overlap(outs[i], in)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+  }
+  return false;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

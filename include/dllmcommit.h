@@ -658,7 +658,9 @@ dllm_status dllm_token_logprobs_backward(const void* logits, dllm_dtype dt, int6
  *            then undefined): zero it to read it later with dllm_workspace_fault.
  * d a multiple of 8, bases 16-byte aligned and row strides multiples of 8, T up
  * to 2^24, d up to 2^20 (else DLLM_ERR_UNSUPPORTED).  The work is that of the
- * scored rows.  Results repeat bit for bit.
+ * scored rows.  Logits are summed in parts of 512 products, each in the tensor
+ * core's fp32, the parts in fp32; the softmax's sums are fp32.  Results repeat bit
+ * for bit.  Outputs must not overlap each other or an input.
  * ------------------------------------------------------------------------ */
 size_t dllm_lm_head_logprobs_workspace_size(int64_t T, int64_t V, int64_t d);
 
@@ -686,7 +688,8 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
  *                is added to (in fp32, rounded once), else it is replaced
  *   workspace    as above, of dllm_lm_head_logprobs_backward_workspace_size
  * Outputs 16-byte aligned, their strides multiples of 8 (else
- * DLLM_ERR_UNSUPPORTED); they must not overlap an input or each other.  The
+ * DLLM_ERR_UNSUPPORTED).  What lies between an output's first and last element must
+ * not overlap an input or another output (DLLM_ERR_INVALID_ARGUMENT).  The
  * weight of every id must be finite where grad_hidden is wanted (a suppressed
  * id's too: it is multiplied by 0).  Results repeat bit for bit. */
 size_t dllm_lm_head_logprobs_backward_workspace_size(int64_t T, int64_t V, int64_t d);
@@ -706,8 +709,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
  *   tokens  device int32, row b token_stride elements apart (a window of a
  *           longer canvas)
  *   weight  device fp32 or bf16 (V, d), rows weight_stride elements apart
- *   out     device (B, L, d) contiguous, weight's dtype; the product with scale
- *           (finite) is fp32, rounded once
+ *   out     device (B, L, d) contiguous, weight's dtype, not overlapping weight or
+ *           tokens; the product with scale (finite) is fp32, rounded once
  * Rows in whole 16-byte vectors: d and strides multiples of 8 (bf16) or 4 (fp32),
  * bases 16-byte aligned; at most 2^30 tokens, d up to 2^20 (else
  * DLLM_ERR_UNSUPPORTED).
@@ -723,9 +726,11 @@ dllm_status dllm_embed_tokens(const int32_t* tokens, int64_t B, int64_t L, int64
  *   grad_weight  device fp32 or bf16 (V, d), rows grad_weight_stride elements
  *                apart; with accumulate it is added to (in fp32, rounded once;
  *                rows that no position names are not touched), else it is
- *                replaced.  Not overlapping grad or tokens.
+ *                replaced.  The bytes from its first to its last row overlap
+ *                neither grad nor tokens (DLLM_ERR_INVALID_ARGUMENT).
  *   workspace    device, 16-byte aligned, of
- *                dllm_embed_tokens_backward_workspace_size(B L, V, d) bytes
+ *                dllm_embed_tokens_backward_workspace_size(B L, V, d) bytes, any
+ *                contents; its first word as in dllm_lm_head_logprobs
  * Sums are fp32 in an order that depends on the tokens alone: results repeat bit
  * for bit.  B L == 0 without accumulate sets grad_weight to zero.  Alignment as
  * above. */

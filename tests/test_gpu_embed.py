@@ -68,7 +68,7 @@ def test_embedding_keeps_nan_and_infinities(cs):
 
 SIZES = [(1, 1, 1, 8, 0.0), (1, 2, 3, 8, 0.0), (1, 64, 7, 16, 0.0), (1, 65, 5000, 72, 0.5), (2, 64, 4, 24, 1.0),
          (3, 333, 1000, 264, 0.5), (1, 2047, 1023, 40, 0.1), (1, 2049, 1024, 40, 0.9), (4, 1025, 70000, 16, 0.4),
-         (2, 9000, 1 << 20, 8, 0.6), (16, 4096, 300, 520, 0.5), (1, 70001, 126464, 32, 0.99)]
+         (2, 9000, 1 << 20, 8, 0.6), (1, 3000, (1 << 21) + 77, 8, 0.1), (3, 40, 9, 40000, 0.5), (16, 4096, 300, 520, 0.5), (1, 70001, 126464, 32, 0.99)]
 
 
 @TYPES
@@ -151,6 +151,79 @@ def test_autograd_and_tied_weight(cs):
     with pytest.raises(RuntimeError, match="cannot be differentiated again"):
         g, = torch.autograd.grad(cs.embed_canvas(t, w).float().square().sum(), w, create_graph=True)
         g.float().sum().backward()
+
+
+def test_the_fault_word_and_the_workspaces_contents(cs):
+    t = canvas(3, 700, 900, 5, 0.5)
+    grad = torch.randn((3, 700, 64), device="cuda").to(BF16)
+    need = cs.lib_handle().dllm_embed_tokens_backward_workspace_size(2100, 900, 64)
+    got = []
+    for fill in (0, 255):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        got.append(cs.embed_tokens_backward(t, grad, 900, ws=ws))
+        if fill == 0:
+            assert cs.workspace_fault(ws) == 0
+    assert torch.equal(got[0], got[1])
+
+
+def test_two_threads_on_one_stream(cs):
+    import threading
+
+    jobs = []
+    for i in range(2):
+        t = canvas(2, 900 + 400 * i, 5000, 10 + i, 0.5)
+        g = torch.randn((*t.shape, 128), device="cuda").to(BF16)
+        jobs.append((t, g, cs.embed_tokens_backward(t, g, 5000)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(t, g, want):
+        for _ in range(40):
+            if not torch.equal(cs.embed_tokens_backward(t, g, 5000), want):
+                bad.append(t.shape)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not bad
+
+
+def test_outputs_written_before_are_complete(cs):
+    """The zero rows run ahead of the sums: what a kernel just before the call writes into the output is replaced."""
+    V, d = 30000, 512
+    t = canvas(1, 100, V, 9, 0.3)
+    g = torch.randn((1, 100, d), device="cuda").to(BF16)
+    want = cs.embed_tokens_backward(t, g, V)
+    out = torch.empty_like(want)
+    for _ in range(20):
+        out.fill_(3.0)
+        cs.embed_tokens_backward(t, g, V, out=out)
+        assert torch.equal(out, want)
+
+
+def test_the_binding_refuses(cs):
+    w = torch.zeros((10, 16), dtype=BF16, device="cuda")
+    t = torch.zeros((2, 4), dtype=torch.int32, device="cuda")
+    g = torch.zeros((2, 4, 16), dtype=BF16, device="cuda")
+    for bad in (lambda: cs.embed_tokens(t.long(), w), lambda: cs.embed_tokens(t, w.half()), lambda: cs.embed_tokens(t[None], w),
+                lambda: cs.embed_tokens_backward(t, g.half(), 10), lambda: cs.embed_tokens_backward(t, g, 10, out=g.half())):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: cs.embed_tokens(t.T, w), lambda: cs.embed_tokens(t, w.T), lambda: cs.embed_tokens(t.cpu(), w),
+                lambda: cs.embed_tokens(t, w, out=g[:1]), lambda: cs.embed_tokens_backward(t, g[:1], 10),
+                lambda: cs.embed_tokens_backward(t, g, 0), lambda: cs.embed_tokens_backward(t, g, 1 << 31),
+                lambda: cs.embed_tokens_backward(t, g, 10, accumulate=True),
+                lambda: cs.embed_tokens_backward(t, g, 10, out=w[:9].clone()),
+                lambda: cs.embed_tokens_backward(t, g.transpose(0, 1), 10)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: cs.embed_tokens(t, w[:, :4].contiguous()), lambda: cs.embed_tokens(t, w, scale=math.inf),
+                lambda: cs.embed_tokens_backward(t, g, 10, ws=torch.zeros(16, dtype=torch.uint8, device="cuda")),
+                lambda: cs.embed_tokens_backward(t, g, 8, out=g.view(8, 16))):
+        with pytest.raises(cs.DllmError):
+            bad()
 
 
 def test_side_stream_and_graph(cs):

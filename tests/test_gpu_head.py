@@ -1,9 +1,9 @@
 """Scores of given tokens from hidden states, and their gradients, on the GPU
 against 64-bit formulas.
 
-Tolerances (derived).  A logit is a sum of d products; added one by one in 32
-bits, truncated, it is off by at most d 2^-23 sum |h w|, called e below (its
-largest over the ids).  lse and log probabilities move by at most 2 e, the
+Tolerances (derived).  A logit is a sum of d products, added in parts of at most
+512 (1024 backward) one by one in 32 bits, truncated, and the parts rounded: off by
+at most (512 + d / 512) 2^-23 sum |h w|, called e below (its largest over the ids).  lse and log probabilities move by at most 2 e, the
 entropy by at most e sum p |log p + H| <= 2 e (H + 1) <= 2 e (ln V + 1), beside
 2^-15 + 2^-21 |value| (2^-12 for the entropy) of the sums of exponentials.
 
@@ -39,10 +39,12 @@ def inputs(T, V, d, seed, scored=1.0, n_sup=0, spread=2.5):
     return h.to(BF16), w, t, sup
 
 
-def logit_error(h, w, scored):
+def logit_error(h, w, scored, part=512):
     """e, per row."""
+    d = h.shape[1]
+    terms = min(d, part) + d // part
     live = torch.where(scored[:, None], h.double(), torch.zeros((), dtype=torch.float64, device=h.device))
-    return h.shape[1] * 2.0 ** -23 * (live.abs() @ w.double().abs().T).amax(1)
+    return terms * 2.0 ** -23 * (live.abs() @ w.double().abs().T).amax(1)
 
 
 def near(got, want, tol):
@@ -91,7 +93,7 @@ def check_backward(cs, h, w, t, sup, with_entropy=True, with_logprob=True, seed=
     dz, clean = grads(flat, w, tt, lse.reshape(-1), ent.reshape(-1), None if gl is None else gl.reshape(-1),
                       None if ge is None else ge.reshape(-1), sup)
     scored = (tt >= 0) & (tt < V)
-    e = float(logit_error(flat, w, scored).max()) * 8 if T else 0.0     # of p, and of z - lse beside the entropy
+    e = float(logit_error(flat, w, scored, 1024).max()) * 8 if T else 0.0     # of p, and of z - lse beside the entropy
     # a term p (g + gH (...)) has no part smaller than p |gH| for the error to hide in
     size = dz.abs()
     if gh is not None:
@@ -175,7 +177,7 @@ def test_nan_and_infinities_where_no_row_is_scored(cs):
     assert bool(torch.isfinite(gh).all()) and bool(torch.isfinite(gw).all())
     assert not bool(gh[live[3]].any()) and not bool(gh[live[5]].any())
     dz, clean = grads(h, w, t, lse, ent, gl, ge, sup)
-    e = 8 * float(logit_error(clean, w, torch.ones_like(dead)).max())
+    e = 8 * float(logit_error(clean, w, torch.ones_like(dead), 1024).max())
     check_grad(gh, dz @ w.double(), dz.abs() @ w.double().abs() + 1e-6, e, 777)
     check_grad(gw, dz.T @ clean, dz.abs().T @ clean.abs() + 1e-6, e, 200)
 
@@ -301,6 +303,116 @@ def test_matches_the_scores_of_stored_logits(cs):
         assert float((a - b).abs().max()) < 1e-3
     e = float(logit_error(h, w, torch.ones_like(t, dtype=torch.bool)).max())
     assert float((got[0] - want[0]).abs().max()) <= 4 * e + 2.0 ** -14
+
+
+def test_confident_rows_of_long_sums(cs):
+    """Log probabilities near 0, -ln(1 + sum over the others of exp(z_v - z_t)): off by the differences' errors, 2 e, times
+    themselves, and 2^-20 of the exponentials."""
+    T, V, d = 8, 300, 4096
+    g = torch.Generator(device="cuda").manual_seed(21)
+    w = (torch.randn((V, d), device="cuda", generator=g) * 2.5 / math.sqrt(d)).to(BF16)
+    t = torch.randint(0, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    h = (torch.randn((T, d), device="cuda", generator=g) + 2.5 * w[t.long()].float()).to(BF16)
+    lp = cs.lm_head_logprobs(h, w, t)[0]
+    want = scores(h, w, t)[0]
+    e = logit_error(h, w, torch.ones_like(t, dtype=torch.bool))
+    assert float(want.max()) > -0.05
+    assert bool(((lp.double() - want).abs() <= (2 * e + 2.0 ** -20) * want.abs() + 2.0 ** -23).all())
+
+
+def test_two_threads_on_one_stream(cs):
+    import threading
+
+    jobs = []
+    for i in range(2):
+        h, w, t, sup = inputs(200 + 77 * i, 3000 + 999 * i, 128, 30 + i, 0.6, 1)
+        g = torch.randn(t.shape, device="cuda")
+        first = [*cs.lm_head_logprobs(h, w, t, suppress_ids=sup)]
+        first += cs.lm_head_logprobs_backward(h, w, t, first[2], first[1], g, g, suppress_ids=sup)
+        jobs.append((h, w, t, sup, g, first))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(h, w, t, sup, g, first):
+        for _ in range(30):
+            got = [*cs.lm_head_logprobs(h, w, t, suppress_ids=sup)]
+            got += cs.lm_head_logprobs_backward(h, w, t, got[2], got[1], g, g, suppress_ids=sup)
+            if not all(torch.equal(a, b) for a, b in zip(got, first)):
+                bad.append(t.shape)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not bad
+
+
+def test_two_graphs_at_once(cs):
+    """Graphs hold memory of their own: replayed on two streams together, neither meets the other's workspace."""
+    cases, graphs, outs = [], [], []
+    for i in range(2):
+        h, w, t, sup = inputs(150 + i, 20000, 256, 40 + i, 0.7, 0)
+        g = torch.randn(t.shape, device="cuda")
+        want = [*cs.lm_head_logprobs(h, w, t)]
+        want += cs.lm_head_logprobs_backward(h, w, t, want[2], want[1], g)
+        cases.append((h, w, t, g, want))
+    torch.cuda.synchronize()
+    for h, w, t, g, _ in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = [*cs.lm_head_logprobs(h, w, t)]
+            got += cs.lm_head_logprobs_backward(h, w, t, got[2], got[1], g)
+        graphs.append(graph)
+        outs.append(got)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for got, (_, _, _, _, want) in zip(outs, cases):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_of_other_sizes_in_between(cs):
+    """A kept workspace serves calls of any size and kind in turn."""
+    h, w, t, sup = inputs(64, 2000, 64, 50, 1.0, 1)
+    big = inputs(300, 9000, 512, 51, 0.5, 1)
+    first = cs.lm_head_logprobs(h, w, t, suppress_ids=sup)
+    for _ in range(3):
+        cs.lm_head_logprobs(*big[:3], suppress_ids=big[3])
+        cs.embed_tokens_backward(t, h, 2000)
+        again = cs.lm_head_logprobs(h, w, t, suppress_ids=sup)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_the_binding_refuses(cs):
+    h, w, t, _ = inputs(8, 100, 64, 60)
+    f = torch.zeros(8, device="cuda")
+    for bad in (lambda: cs.lm_head_logprobs(h.float(), w, t), lambda: cs.lm_head_logprobs(h, w.half(), t),
+                lambda: cs.lm_head_logprobs(h[None, None], w, t), lambda: cs.score_hidden(h, w[0], t),
+                lambda: cs.lm_head_logprobs(h, w, t, ws="no")):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: cs.lm_head_logprobs(h, w[:, :32], t), lambda: cs.lm_head_logprobs(h, w, t.long()),
+                lambda: cs.lm_head_logprobs(h, w, t[:7]), lambda: cs.lm_head_logprobs(h.T, w, t),
+                lambda: cs.lm_head_logprobs(h, w, t, suppress_ids=[1 << 33]),
+                lambda: cs.lm_head_logprobs(h, w, t, ws=torch.zeros(8, dtype=torch.uint8)),
+                lambda: cs.lm_head_logprobs_backward(h, w, t, f, f, f, accumulate=True),
+                lambda: cs.lm_head_logprobs_backward(h, w, t, f, f, f, out=(h.clone(), None), hidden_grad=False),
+                lambda: cs.lm_head_logprobs_backward(h, w, t, f, f, f, out=(None, w.half())),
+                lambda: cs.lm_head_logprobs_backward(h, w, t, f, f, f, out=(None, w[:50].clone())),
+                lambda: cs.lm_head_logprobs_backward(h, w, t, f[:4], f, f)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: cs.lm_head_logprobs(h, w, t, suppress_ids=[100]),
+                lambda: cs.lm_head_logprobs(h, w, t, ws=torch.zeros(256, dtype=torch.uint8, device="cuda")),
+                lambda: cs.lm_head_logprobs(h[:, :60].contiguous(), w[:, :60].contiguous(), t),
+                lambda: cs.lm_head_logprobs_backward(h, w, t, f, f, f, out=(h, None)),
+                lambda: cs.lm_head_logprobs_backward(h, w, t, f, f, f, out=(None, w))):
+        with pytest.raises(cs.DllmError):
+            bad()
 
 
 def test_side_stream_and_graph(cs):

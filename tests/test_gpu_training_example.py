@@ -1,0 +1,49 @@
+"""The training example: it runs, and its gradients are those of the same model in 64-bit torch operations."""
+import importlib.util
+import math
+import os
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def example():
+    spec = importlib.util.spec_from_file_location("masked_training_step",
+                                                  os.path.join(ROOT, "examples", "masked_training_step.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_gradients(cs):
+    m = example()
+    model = m.TinyMaskedModel(seed=4)
+    tokens = torch.randint(0, model.vocab - 1, (4, 64), dtype=torch.int32, generator=torch.Generator().manual_seed(5)).cuda()
+    value = m.loss(model, tokens, torch.Generator().manual_seed(6), entropy_bonus=0.05)
+    value.backward()
+    w, mix, dense = [p.detach().double().requires_grad_() for p in model.parameters()]
+    canvas, targets, weight = m.noised(tokens, model.mask_id, torch.Generator().manual_seed(6))
+    x = w[canvas.long()] * math.sqrt(model.d)
+    y = x + torch.einsum("lm,bmd->bld", mix, x)
+    z = (y + torch.tanh(y @ dense)) @ w.T
+    z = z.index_fill(2, torch.tensor([model.mask_id], device="cuda"), -math.inf)
+    logp = torch.log_softmax(z, -1)
+    on = (targets >= 0).double()
+    lp = logp.gather(2, targets.clamp(min=0).long()[..., None])[..., 0] * on
+    p = logp.exp()
+    ent = -(p * torch.where(p > 0, logp, torch.zeros_like(logp))).sum(-1) * on
+    want = (-(weight.double() * lp).sum() - 0.05 * ent.sum()) / tokens.numel()
+    want.backward()
+    # Activations and gradients pass through a dozen roundings to bf16, each 2^-8 of a value at most and of the same
+    # spread: together about sqrt(12 / 3) 2^-8 of the norm, held to twice that.
+    assert abs(float(value) - float(want)) <= 2.0 ** -6 * abs(float(want))
+    for got, ref in zip(model.parameters(), (w, mix, dense)):
+        assert float((got.grad.double() - ref.grad).norm()) <= 4 * 2.0 ** -8 * float(ref.grad.norm())
+
+
+def test_it_runs(cs):
+    example().main()

@@ -72,6 +72,25 @@ def test_embed_refusals():
     assert embed_grad(ws=FAKE + 8) == INVALID and embed_grad(dt=0, d=60) == UNSUPPORTED
 
 
+FAR = [FAKE << k for k in range(1, 12)]                  # apart by more than the small calls below touch
+
+
+def test_overlapping_outputs_are_refused():
+    """(Only refused calls: the addresses are made up.)"""
+    h, w, t, lp, ent, lse, ws, g, gh, gw = FAR[:10]
+    good = dict(h=h, w=w, t=t, lp=lp, ent=ent, lse=lse, ws=ws)
+    for kw in (dict(lp=h), dict(ent=w + 99 * 128 + 124), dict(lse=t + 12), dict(lp=ent + 12), dict(ws=h - 16), dict(lse=ws + 64)):
+        assert score(**{**good, **kw}) == INVALID, kw
+    good = dict(h=h, w=w, t=t, ent=ent, lse=lse, ws=ws, g=g, gh=gh, gw=gw)
+    for kw in (dict(gh=h), dict(gw=w), dict(gh=gw + 99 * 128), dict(gw=h - 16), dict(ge=gw), dict(gw=lse), dict(ws=gw - 16),
+               dict(gw=t - 256, dt=0)):
+        assert grad(**{**good, **kw}) == INVALID, kw
+    assert embed(t=t, w=w, out=w + 128) == INVALID and embed(t=t, w=w, out=t - 16) == INVALID
+    good = dict(t=t, w=g, out=gw, ws=ws)
+    for kw in (dict(out=g), dict(out=t - 16), dict(ws=g), dict(ws=gw + 99 * 128)):
+        assert embed_grad(**{**good, **kw}) == INVALID, kw
+
+
 def test_the_binding_refuses_host_tensors():
     h, w, t = torch.zeros((2, 8), dtype=torch.bfloat16), torch.zeros((5, 8), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
     f = torch.zeros(2)
