@@ -80,7 +80,7 @@ struct HeadParams {
   CUtensorMap tm_a, tm_b;        // the operands; where one is the hidden states, the caller's tensor,
   CUtensorMap tm_packed;         // read when every row is scored, and else their gathered copy
   CUtensorMap tm_aw, tm_bw;      // dw's operands, as rows of 64 m or n (tm_packed then for these)
-  CUtensorMap tm_out;            // dw in bf16 without accumulate: the weight's gradient
+  CUtensorMap tm_out;            // the weight's gradient
   const int32_t* n_rows;         // device: the scored rows; then the splits of the second product
   int64_t T, V;
   int64_t v0;                    // the piece's first id
@@ -384,26 +384,8 @@ __device__ __forceinline__ uint32_t hd_absent(const int32_t* sup, int n_sup, int
   return absent;
 }
 
-// 32 columns of an accumulator row to bf16 or fp32 memory, in 16-byte stores;
-// `lim` columns (a multiple of 8) exist.  With `add` the old values are added.
-__device__ __forceinline__ void hd_store_bf16(uint16_t* out, const float (&x)[32], int lim, bool add) {
-#pragma unroll
-  for (int j = 0; j < 32; j += 8) {
-    if (j >= lim) break;
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = x[j + e];
-    uint4* at = reinterpret_cast<uint4*>(out + j);
-    if (add) {
-      const uint4 o = *at;
-      y[0] += bf16lo(o.x), y[1] += bf16hi(o.x), y[2] += bf16lo(o.y), y[3] += bf16hi(o.y);
-      y[4] += bf16lo(o.z), y[5] += bf16hi(o.z), y[6] += bf16lo(o.w), y[7] += bf16hi(o.w);
-    }
-    *at = make_uint4(hd_bf16x2(y[0], y[1]), hd_bf16x2(y[2], y[3]), hd_bf16x2(y[4], y[5]), hd_bf16x2(y[6], y[7]));
-  }
-}
-
-// The same to 32-byte aligned memory, whole sectors a store.
+// 32 columns of an accumulator row as bf16 to 32-byte aligned memory, whole sectors a
+// store; `lim` of them exist.
 __device__ __forceinline__ void hd_store_dz(uint16_t* out, const float (&x)[32], int lim) {
 #pragma unroll
   for (int j = 0; j < 32; j += 16) {
@@ -450,6 +432,70 @@ __device__ __forceinline__ void hd_store_tile(uint32_t taddr, uint32_t buf, cons
   }
 }
 
+// The same, added to what is there, whose 32 x 64 the buffer holds (loaded by TMA while
+// the products ran; read from memory a row a thread, 512 x 126464 x 4096 took 9.6 ms
+// where it now takes 1.2).
+__device__ __forceinline__ void hd_load_old(uint32_t buf, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, kHdStoreBytes);
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(buf),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void hd_add_tile(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r[32];
+    hd_ld32(taddr + 32 * h, r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t at = buf + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4);
+      const uint4 o = lds128(at);
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = hd_bf16x2(__uint_as_float(r[8 * j + 2 * e]) + bf16lo((&o.x)[e]), __uint_as_float(r[8 * j + 2 * e + 1]) + bf16hi((&o.x)[e]));
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(buf)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
+// 32 columns in fp32, stored or added to what is there.
+__device__ __forceinline__ void hd_store_tile_f32(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane, bool add) {
+  uint32_t r[32];
+  hd_ld32(taddr, r);
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((j ^ (lane & 7)) << 4)), "r"(r[4 * j]),
+                 "r"(r[4 * j + 1]), "r"(r[4 * j + 2]), "r"(r[4 * j + 3])
+                 : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    if (add)
+      asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(x), "r"(y), "r"(buf)
+                   : "memory");
+    else
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                   "r"(x), "r"(y), "r"(buf)
+                   : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
 __device__ __forceinline__ void hd_store_f32(float* out, const float (&x)[32], int lim, bool add) {
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
@@ -468,6 +514,7 @@ template <int OP>
 __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_constant__ HeadParams p) {
   extern __shared__ __align__(1024) uint8_t hd_smem[];
   __shared__ __align__(8) uint64_t full_bar[kHdMaxStages], empty_bar[kHdMaxStages], accf_bar[2], acce_bar[2];
+  __shared__ __align__(8) uint64_t old_bar[kHdEpiWarps][2];
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t abort_flag_s;
   __shared__ int32_t sup_s[DLLM_MAX_SUPPRESS];
@@ -488,6 +535,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       mbar_init(smem_addr(&accf_bar[b]), 1);
       mbar_init(smem_addr(&acce_bar[b]), 2 * kHdEpiWarps);
     }
+    for (int b = 0; b < 2 * kHdEpiWarps; ++b) mbar_init(smem_addr(&old_bar[b >> 1][b & 1]), 1);
     abort_flag_s = 0;
     fence_mbar_init();
   }
@@ -623,7 +671,9 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   } else if (warp < kHdEpiWarps) {
     const int ew = warp & 3, half = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(ew * 32) << 16);
-    const uint32_t store_buf = ring + kHdRing - (kHdEpiWarps - warp) * kHdStoreBytes;   // (back: behind the last stage)
+    const bool add16 = OP == kHdBack && p.accumulate && !p.grad_w_f32;
+    const uint32_t store_buf = ring + kHdRing - (kHdEpiWarps - warp) * (add16 ? 2 : 1) * kHdStoreBytes;   // (back: behind the last stage)
+    uint32_t old_phase[2] = {0, 0}, old_asked = 0;
     HeadSoft soft{-kHdCap, 0.0f, 0.0f};
     int j = 0;
     // The next accumulator: warp-uniform, since the TMEM loads are .sync.aligned.
@@ -762,10 +812,36 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         if (OP == kHdScore && row < n && (work.n_m > 1 || (it + 1) * work.pairs + work.pair >= work.total))
           p.part[((work.n_m > 1 ? t.n : work.pair) * 2 + half) * p.part_rows + row] = make_float4(soft.m, soft.Z, soft.S, 0.0f);
       } else {
+        if (dw && add16 && warp_rows && lane == 0) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            if (64 * half + 128 * b < in_tile)
+              hd_load_old(store_buf + b * kHdStoreBytes, &p.tm_out, static_cast<int>(col0) + 64 * half + 128 * b,
+                          static_cast<int>(p.v0 + row), smem_addr(&old_bar[warp][b]));
+          old_asked = 3;
+        }
         if (!await()) break;
         const uint32_t from = lanes + static_cast<uint32_t>((j & 1) * kHdBN);
         bool released = false;
-        if (dw && !p.grad_w_f32 && !p.accumulate) {
+        if (dw && add16) {
+          bool ok = true;
+          if (warp_rows)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int c = 64 * half + 128 * b;
+              if (c >= in_tile || !ok) continue;
+              ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&old_bar[warp][b]), old_phase[b], abort_flag));
+              if (!ok) continue;
+              old_phase[b] ^= 1u;
+              hd_add_tile(from + c, store_buf + b * kHdStoreBytes, &p.tm_out, static_cast<int>(col0) + c,
+                          static_cast<int>(p.v0 + row) - lane, lane);
+            }
+          if (!ok) {
+            if (lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
+            break;
+          }
+        } else if (dw && !p.grad_w_f32) {
           if (warp_rows)
             for (int c = half * 64; c < in_tile; c += 128)
               hd_store_tile(from + c, store_buf, &p.tm_out, static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane, lane, [&] {
@@ -774,6 +850,11 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
                   released = true;
                 }
               });
+        } else if (dw && p.grad_w_f32) {
+#pragma unroll 1
+          for (int c = half * 32; warp_rows && c < in_tile; c += 64)
+            hd_store_tile_f32(from + c, store_buf, &p.tm_out, static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane, lane,
+                              p.accumulate != 0);
         } else {
 #pragma unroll 1
           for (int c = half * 32; warp_rows && c < in_tile; c += 64) {
@@ -784,17 +865,16 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
 #pragma unroll
             for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(r[q]);
             if (row >= visit) continue;
-            if (!dw)
-              hd_store_f32(p.acc + (static_cast<int64_t>(t.split) * work.n_m * kHdBM + row) * p.acc_stride + col0 + c, x, lim, p.add != 0);
-            else if (p.grad_w_f32)
-              hd_store_f32(static_cast<float*>(p.grad_w) + (p.v0 + row) * p.grad_w_stride + col0 + c, x, lim, p.accumulate != 0);
-            else
-              hd_store_bf16(static_cast<uint16_t*>(p.grad_w) + (p.v0 + row) * p.grad_w_stride + col0 + c, x, lim, p.accumulate != 0);
+            hd_store_f32(p.acc + (static_cast<int64_t>(t.split) * work.n_m * kHdBM + row) * p.acc_stride + col0 + c, x, lim, p.add != 0);
           }
         }
         if (!released) release();
+        old_asked = 0;
       }
     }
+    // Giving up: the old values still in flight land before the CTA ends.
+    if (old_asked)
+      for (int b = 0; b < 2; ++b) mbar_wait_bounded(smem_addr(&old_bar[warp][b]), old_phase[b]);
     if (OP == kHdBack && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   // The third product without a scored row: the gradient is zero.
@@ -1112,16 +1192,16 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// rows x cols of bf16 (cols contiguous), read in boxes of box_rows x 64 columns
-// in the 128-byte swizzle; what lies outside reads as 0.
-bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t stride, uint32_t box_rows) {
+// rows x cols of bf16 or fp32 (cols contiguous) in boxes of box_rows x 128 bytes in
+// the 128-byte swizzle; what lies outside reads as 0 and is not written.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t stride, uint32_t box_rows, bool f32 = false) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kHdBK), box_rows};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {f32 ? 32u : static_cast<cuuint32_t>(kHdBK), box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1247,7 +1327,7 @@ dllm_status hd_check(const void* hidden, int64_t T, int64_t d, int64_t hidden_st
 void hd_ring(HeadParams& p, int op, int32_t a_rows) {
   p.a_bytes = static_cast<uint32_t>(a_rows) * kHdBK * 2;
   p.stage_bytes = kHdABytes + static_cast<uint32_t>(round_up(p.bn / 2 * kHdBK * 2, 1024));
-  p.stages = std::min<int32_t>(kHdMaxStages, (kHdRing - (op == kHdBack ? kHdEpiWarps * kHdStoreBytes : 0)) / static_cast<int32_t>(p.stage_bytes));
+  p.stages = std::min<int32_t>(kHdMaxStages, (kHdRing - (op == kHdBack ? kHdEpiWarps * kHdStoreBytes * (p.accumulate && !p.grad_w_f32 ? 2 : 1) : 0)) / static_cast<int32_t>(p.stage_bytes));
   p.clear_a = p.T <= kHdRows ? 1 : 0;
 }
 
@@ -1456,7 +1536,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
       !make_map(&pb.tm_a, p.dz, h.t_pad, h.piece, h.piece, a_rows) || !make_map(&pb.tm_b, weight, V, d, weight_stride, 64) ||
       !make_map(&pb.tm_aw, p.dz, h.t_pad, h.piece, h.piece, 64) || !make_map(&pb.tm_bw, hidden, T, d, hidden_stride, 64) ||
       !make_map(&pb.tm_packed, ws + h.hidden, packed_rows, d, d, 64) ||
-      (grad_weight && grad_weight_dt == DLLM_BF16 && !make_map(&pb.tm_out, grad_weight, V, d, grad_weight_stride, 32)))
+      (grad_weight && !make_map(&pb.tm_out, grad_weight, V, d, grad_weight_stride, 32, grad_weight_dt == DLLM_F32)))
     return DLLM_ERR_CUDA;
   pz.bn = h.bn_v;
   pz.idesc = hd_idesc(false, false, h.bn_v);

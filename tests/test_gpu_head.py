@@ -244,6 +244,20 @@ def test_given_outputs(cs, dtype, accumulate):
     check_grad(gw, dz.T @ clean, dz.abs().T @ clean.abs() + 1e-6, 1e-3, T, old[:, :d] if accumulate else None)
 
 
+@pytest.mark.parametrize("dtype", [BF16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,V,d", [(40, 9001, 520), (700, 30011, 264), (300, 2000, 64)])
+def test_adding_over_many_tiles(cs, dtype, T, V, d):
+    """Micro-batches added to one gradient: each call adds its own, rounded once."""
+    h, w, t, sup = inputs(T, V, d, V, 0.9, 1)
+    gw = torch.randn((V, d), device="cuda").to(dtype) * 0.1
+    e = 8 * float(logit_error(h, w, (t >= 0) & (t < V), 1024).max())
+    for seed in range(2):
+        old = gw.clone()
+        gh, got, dz, clean, _ = check_backward(cs, h, w, t, sup, seed=seed, out=(None, gw), accumulate=True)
+        assert got is gw
+        check_grad(gw, dz.T @ clean, dz.abs().T @ clean.abs() + 1e-6, e, T, old)
+
+
 def test_strided_inputs_and_batches(cs):
     h, w, t, sup = inputs(150, 700, 96, 13, 0.7, 1)
     hw = torch.full((150, 200), math.nan, dtype=BF16, device="cuda")
