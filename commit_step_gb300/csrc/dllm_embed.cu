@@ -71,8 +71,9 @@ __device__ __forceinline__ uint4 em_scale(uint4 v, float s) {
   return o;
 }
 
-// A block copies `rows` consecutive rows of the output.  (One block a piece, not a
-// grid that fits the GPU: SMs whose memory is further away then take fewer pieces.)
+// A block copies `rows` consecutive rows of the output, 16 KB where there are blocks
+// enough.  One block a piece, not a grid that fits the GPU: SMs whose memory is further
+// away then take fewer pieces (65536 x 2560 bf16: 107 and 97 us, 6.3 TB/s).
 template <bool BF16>
 __global__ void __launch_bounds__(kEmThreads) embed_kernel(const __grid_constant__ EmbedTokens tok, const uint8_t* weight,
                                                            int64_t row_bytes, EmDiv vecs, int32_t rows, float scale, uint8_t* out) {
@@ -434,6 +435,10 @@ __device__ __forceinline__ void run_write(const RunParams& p, int64_t row, int64
   }
 }
 
+// Bound by memory: 65536 rows of 4096 bf16 with half of them one token's, 126464 ids,
+// in 125 us (0.54 GB read, some 0.2 written: 5.8 TB/s); four blocks an SM (64
+// registers) against three: 134.
+//
 // A block sums the runs of 8 consecutive chunks in a slab of 32 vectors, a chunk
 // a warp.  A run inside a chunk goes to its row; a chunk's first and last runs
 // meet those of its neighbours in shared memory, where warp 0 walks the chunks in

@@ -40,7 +40,7 @@ def test_gradients(cs):
     want.backward()
     # Activations and gradients pass through a dozen roundings to bf16, each 2^-8 of a value at most and of the same
     # spread: together about sqrt(12 / 3) 2^-8 of the norm, held to twice that.
-    assert abs(float(value) - float(want)) <= 2.0 ** -6 * abs(float(want))
+    assert abs(value.item() - want.item()) <= 2.0 ** -6 * abs(want.item())
     for got, ref in zip(model.parameters(), (w, mix, dense)):
         assert float((got.grad.double() - ref.grad).norm()) <= 4 * 2.0 ** -8 * float(ref.grad.norm())
 
