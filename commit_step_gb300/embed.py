@@ -66,7 +66,7 @@ def embed_tokens(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
         raise ValueError("weight needs unit column stride")
     B, L, t_stride = _canvas(tokens, idx)
     if out is None:
-        out = weight.new_empty((*tokens.shape, d))
+        out = torch.empty((*tokens.shape, d), dtype=weight.dtype, device=weight.device)
     elif (not torch.is_tensor(out) or out.dtype != weight.dtype or out.get_device() != idx
           or out.shape != (*tokens.shape, d) or not out.is_contiguous()):
         raise ValueError("out must be a contiguous (..., d) tensor of weight's dtype, on the same device")

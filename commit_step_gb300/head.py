@@ -27,6 +27,15 @@ def _matrix(t, name: str, cols: int, device):
 
 def _ends(hidden, weight, targets):
     """Shape and stride of hidden (T, d) or (B, L, d) and weight (V, d)."""
+    try:                                     # (the usual case; a call's cost on the host is mostly these checks)
+        h, w = hidden.shape, weight.shape
+        if (len(h) == 2 and len(w) == 2 and h[1] == w[1] and hidden.dtype == weight.dtype == torch.bfloat16
+                and hidden.get_device() == weight.get_device() >= 0):
+            (hs, unit), (ws, w_unit) = hidden.stride(), weight.stride()
+            if unit == 1 and w_unit == 1:
+                return h[0], h[1], (hs if h[0] > 1 else h[1]), w[0], (ws if w[0] > 1 else h[1])
+    except AttributeError:
+        pass
     _need_cuda(hidden, weight, targets)
     if not torch.is_tensor(hidden) or hidden.dtype != torch.bfloat16 or hidden.dim() not in (2, 3):
         raise TypeError("hidden must be a (T, d) or (B, L, d) bfloat16 tensor")
@@ -95,8 +104,10 @@ def lm_head_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
     T, d, stride, V, w_stride = _ends(hidden, weight, targets)
     dev, idx = hidden.device, hidden.get_device()
     if out is None:
-        lp = hidden.new_empty(hidden.shape[:-1], dtype=torch.float32)
-        ent, lse = torch.empty_like(lp), torch.empty_like(lp)
+        shape = hidden.shape[:-1]
+        lp = torch.empty(shape, dtype=torch.float32, device=dev)
+        ent = torch.empty(shape, dtype=torch.float32, device=dev)
+        lse = torch.empty(shape, dtype=torch.float32, device=dev)
         at = lp.data_ptr(), ent.data_ptr(), lse.data_ptr()
     else:
         lp, ent, lse = out
