@@ -117,6 +117,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCtas = 8;
 constexpr int kSortAhead = 8;                           // rounds of 32 keys whose loads are in flight together
+constexpr int kSortFew = 128;                           // keys that are ranked by comparing all with all
 constexpr int kSortSmem = (kSortWarps + 1) * kSortBins * 4;
 
 struct SortParams {
@@ -203,7 +204,7 @@ __device__ __forceinline__ void sort_warp(const SortParams& p, int pass, int64_t
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ SortParams p) {
-  extern __shared__ int32_t em_smem[];
+  extern __shared__ __align__(16) int32_t em_smem[];
   __shared__ int32_t sums[kSortWarps];
   int32_t* total = em_smem;                              // per bin, of this CTA
   int32_t* count = em_smem + kSortBins;                  // (warps, bins)
@@ -212,6 +213,27 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
   // kernel before this one still uses.
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5;
+  if (p.tok.T <= kSortFew) {
+    // A thread's place is the count of the keys before its own (a call with 40 keys: 18.5
+    // and 12.3 us, with 333: 22.5 and 24.6).
+    if (blockIdx.x != 0) return;
+    const int n = static_cast<int>(p.tok.T), i = threadIdx.x;
+    const int32_t key = i < n ? p.tok[i] : INT32_MAX;
+    em_smem[i] = key;
+    __syncthreads();
+    int place = 0;
+    for (int j = 0; j < n; j += 4) {
+      const int4 k = *reinterpret_cast<const int4*>(em_smem + j);        // (INT32_MAX behind the last)
+      place += (k.x < key || (k.x == key && j < i) ? 1 : 0) + (k.y < key || (k.y == key && j + 1 < i) ? 1 : 0) +
+               (k.z < key || (k.z == key && j + 2 < i) ? 1 : 0) + (k.w < key || (k.w == key && j + 3 < i) ? 1 : 0);
+    }
+    if (i < n) {
+      const int last = (p.passes - 1) & 1;
+      p.key[last][place] = key;
+      p.pos[last][place] = i;
+    }
+    return;
+  }
   const int bins = 1 << p.bits;
   const uint32_t rank = blockIdx.x;
   const int64_t per = (p.tok.T + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps);

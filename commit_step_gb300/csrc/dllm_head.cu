@@ -628,6 +628,9 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         }
       }
     }
+    // The products' last arrivals on this CTA's barriers come before it ends.
+    for (int64_t q = issued > p.stages ? issued - p.stages : 0; q < issued && ok; ++q)
+      ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&empty_bar[q % p.stages]), static_cast<uint32_t>((q / p.stages) & 1), abort_flag));
     // Giving up: the copies still in flight land before the CTA ends.
     if (*abort_flag && rank == 0)
       for (int64_t q = issued > p.stages ? issued - p.stages : 0; q < issued; ++q)
@@ -1336,10 +1339,13 @@ dllm_status hd_check(const void* hidden, int64_t T, int64_t d, int64_t hidden_st
   return DLLM_OK;
 }
 
-void hd_ring(HeadParams& p, int op, int32_t a_rows) {
+void hd_ring(HeadParams& p, int op, int32_t a_rows, int64_t pairs) {
   p.a_bytes = static_cast<uint32_t>(a_rows) * kHdBK * 2;
   p.stage_bytes = kHdABytes + static_cast<uint32_t>(round_up(p.bn / 2 * kHdBK * 2, 1024));
-  p.stages = std::min<int32_t>(kHdMaxStages, (kHdRing - (op == kHdBack ? kHdEpiWarps * kHdStoreBytes * (p.accumulate && !p.grad_w_f32 ? 2 : 1) : 0)) / static_cast<int32_t>(p.stage_bytes));
+  // No more stages than a pair has slabs (what few rows leave empty of each is cleared).
+  const int64_t slabs = op == kHdBack ? kHdMaxStages
+                                      : (round_up(p.T, kHdBM) / kHdBM * p.n_n + pairs - 1) / pairs * (round_up(p.d, kHdBK) / kHdBK);
+  p.stages = std::min<int32_t>(static_cast<int32_t>(std::min<int64_t>(kHdMaxStages, slabs)), (kHdRing - (op == kHdBack ? kHdEpiWarps * kHdStoreBytes * (p.accumulate && !p.grad_w_f32 ? 2 : 1) : 0)) / static_cast<int32_t>(p.stage_bytes));
   p.clear_a = p.T <= kHdRows ? 1 : 0;
 }
 
@@ -1423,7 +1429,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   p.bn = h.bn_v;
   p.n_n = h.n_v;
   p.idesc = hd_idesc(false, false, h.bn_v);
-  hd_ring(p, kHdScore, static_cast<int32_t>(a_rows));
+  hd_ring(p, kHdScore, static_cast<int32_t>(a_rows), dev->sms / 2);
   p.target = l.target;
   p.n_sup = static_cast<int32_t>(sup.size());
   std::copy(sup.begin(), sup.end(), p.sup);
@@ -1561,14 +1567,15 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
     return DLLM_ERR_CUDA;
   pz.bn = h.bn_v;
   pz.idesc = hd_idesc(false, false, h.bn_v);
-  hd_ring(pz, kHdDz, static_cast<int32_t>(a_rows));
+  pz.n_n = h.n_v;
+  hd_ring(pz, kHdDz, static_cast<int32_t>(a_rows), dev->sms / 2);
   pb.bn = h.bn_d;
   pb.n_n = h.n_d;
   pb.idesc = hd_idesc(false, true, h.bn_d);
   pb.idesc_w = hd_idesc(true, true, h.bn_d);
   pb.want_h = grad_hidden ? 1 : 0;
   pb.want_w = grad_weight ? 1 : 0;
-  hd_ring(pb, kHdBack, static_cast<int32_t>(a_rows));
+  hd_ring(pb, kHdBack, static_cast<int32_t>(a_rows), dev->sms / 2);
 
   l.hidden = static_cast<const uint16_t*>(hidden);
   l.stride = hidden_stride;
