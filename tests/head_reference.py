@@ -32,8 +32,8 @@ def scores(hidden, weight, targets, sup=()):
     return [torch.where(scored, x, zero) for x in (logprob, entropy, lse)]
 
 
-def grads(hidden, weight, targets, lse, entropy, g, gh, sup=()):
-    """dz (T, V), and the rows that take part; the gradients are dz @ weight and dz^T @ hidden."""
+def _taking_part(hidden, weight, targets, lse, g, gh, sup):
+    """(rows that take part, g, gH) in 64 bits."""
     T, V = hidden.shape[0], weight.shape[0]
     t = targets.long()
     zero = torch.zeros(T, dtype=torch.float64, device=hidden.device)
@@ -41,7 +41,15 @@ def grads(hidden, weight, targets, lse, entropy, g, gh, sup=()):
     gh = zero if gh is None else gh.double()
     for v in sup:
         g = torch.where(t == v, zero, g)
-    rows = (t >= 0) & (t < V) & torch.isfinite(lse) & ((g != 0) | (gh != 0))
+    return (t >= 0) & (t < V) & torch.isfinite(lse) & ((g != 0) | (gh != 0)), g, gh
+
+
+def grads(hidden, weight, targets, lse, entropy, g, gh, sup=()):
+    """dz (T, V), and the hidden states of the rows that take part; the gradients are dz @ weight and dz^T @ hidden."""
+    T, V = hidden.shape[0], weight.shape[0]
+    t = targets.long()
+    zero = torch.zeros(T, dtype=torch.float64, device=hidden.device)
+    rows, g, gh = _taking_part(hidden, weight, targets, lse, g, gh, sup)
     clean = torch.where(rows[:, None], hidden.double(), torch.zeros((), dtype=torch.float64, device=hidden.device))
     y = logits(clean, weight, sup) - torch.where(rows, lse.double(), zero)[:, None]
     p = torch.exp(y)
@@ -49,6 +57,19 @@ def grads(hidden, weight, targets, lse, entropy, g, gh, sup=()):
     dz = -p * (g[:, None] + gh[:, None] * (y + entropy.double()[:, None]))
     dz[torch.arange(T, device=dz.device), t.clamp(0, V - 1)] += g
     return torch.where(rows[:, None], dz, torch.zeros_like(dz)), clean
+
+
+def grad_parts(hidden, weight, targets, lse, entropy, g, gh, sup=()):
+    """The magnitude of what the elements of dz are made of, p (|g| + |gH| (|z - lse + H| + 1)): a relative error of p, or an
+    error of z, moves an element by that share of it, however small what is left of the element."""
+    zero = torch.zeros(hidden.shape[0], dtype=torch.float64, device=hidden.device)
+    _, clean = grads(hidden, weight, targets, lse, entropy, g, gh, sup)
+    rows, g, gh = _taking_part(hidden, weight, targets, lse, g, gh, sup)
+    y = logits(clean, weight, sup) - torch.where(rows, lse.double(), zero)[:, None]
+    p = torch.exp(y)
+    y = torch.where(p > 0, y, torch.zeros_like(y))
+    size = p * (g.abs()[:, None] + gh.abs()[:, None] * ((y + entropy.double()[:, None]).abs() + 1))
+    return torch.where(rows[:, None], size, torch.zeros_like(size))
 
 
 def embedding_grad(tokens, grad, V, scale=1.0):

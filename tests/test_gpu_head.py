@@ -7,21 +7,24 @@ at most (512 + d / 512) 2^-23 sum |h w|, called e below (its largest over the id
 entropy by at most e sum p |log p + H| <= 2 e (H + 1) <= 2 e (ln V + 1), beside
 2^-15 + 2^-21 |value| (2^-12 for the entropy) of the sums of exponentials.
 
-The gradient's dz is rounded to bf16 (2^-8 of itself at most) after an error of
-2^-12 (exponent and logit); sums of n terms in 32 bits are off by n 2^-23 of the
-sum of magnitudes at most; the result is rounded to its type.  So an element is
-within (2^-8 + 2^-12 + e + n 2^-23) sum |dz| |w| + half a step.  That bound is
-wide for sums whose terms cancel, so the 2-norm of the whole error is held too:
-two roundings of at most 2^-8, spread evenly, have a root mean square of
+The gradient's dz is rounded to bf16 (2^-8 of itself at most) after the errors of z
+(e) and of p (e, and 2^-18 for the exponent's roundings and the exponential), which
+move it by that share of what it is made of (grad_parts: at a confident target what
+is left of g - g p is far smaller); sums of n terms in 32 bits are off by n 2^-23 of
+the sum of magnitudes at most; the result is rounded to its type.  So an element is
+within (2^-8 + n 2^-23) sum |dz| |w| + (2 e + 2^-18) sum parts |w| + half a step.
+That bound is wide for sums whose terms cancel, so the 2-norm of the whole error is
+held too: two roundings of at most 2^-8, spread evenly, have a root mean square of
 2^-8 / sqrt 3 each, sqrt(2 / 3) 2^-8 together (fp32 results: one), and 2^-8 is
-asked for.
+asked for beside the second term's norm; of few rows a handful of elements decides,
+which may all be off by the most: twice that.
 """
 import math
 
 import pytest
 import torch
 
-from head_reference import grads, scores
+from head_reference import grad_parts, grads, scores
 
 pytestmark = pytest.mark.gpu
 
@@ -71,15 +74,18 @@ def check_scores(cs, h, w, t, sup, **kw):
     return lp, ent, lse
 
 
-def check_grad(got, exact, size, e, n, old=None):
-    """got against exact, sums of n terms whose magnitudes add up to size."""
+def check_grad(got, dz, parts, by, e, old=None):
+    """got against dz @ by (dz and its parts transposed for the weight's)."""
     half = torch.finfo(got.dtype).eps / 2
+    exact, by = dz @ by.double(), by.double().abs()
     want = exact if old is None else exact + old.double()
-    lim = (2.0 ** -8 + 2.0 ** -12 + e + n * 2.0 ** -23) * size + half * want.abs() + 1e-30
+    slack = (2 * e + 2.0 ** -18) * (parts @ by)
+    lim = (2.0 ** -8 + dz.shape[1] * 2.0 ** -23) * (dz.abs() @ by) + slack + half * want.abs() + 1e-30
     err = (got.double() - want).abs()
     assert bool((err <= lim * (1 + half)).all()), float((err - lim).max())
-    if exact.numel() >= 4096 and old is None and float(exact.norm()) > 0:
-        assert float((got.double() - want).norm()) <= 2.0 ** -8 * float(want.norm())
+    if exact.numel() >= 4096 and old is None:
+        few = int((dz != 0).any(0).sum()) < 100 or int((dz != 0).any(1).sum()) < 100
+        assert float(err.norm()) <= (2 if few else 1) * 2.0 ** -8 * float(want.norm()) + float(slack.norm())
 
 
 def check_backward(cs, h, w, t, sup, with_entropy=True, with_logprob=True, seed=0, **kw):
@@ -90,18 +96,17 @@ def check_backward(cs, h, w, t, sup, with_entropy=True, with_logprob=True, seed=
     gl = torch.randn(t.shape, device="cuda", generator=g) if with_logprob else None
     ge = torch.randn(t.shape, device="cuda", generator=g) * 0.2 if with_entropy else None
     gh, gw = cs.lm_head_logprobs_backward(h, w, t, lse, ent, gl, ge, suppress_ids=sup, **kw)
-    dz, clean = grads(flat, w, tt, lse.reshape(-1), ent.reshape(-1), None if gl is None else gl.reshape(-1),
-                      None if ge is None else ge.reshape(-1), sup)
+    what = (flat, w, tt, lse.reshape(-1), ent.reshape(-1), None if gl is None else gl.reshape(-1),
+            None if ge is None else ge.reshape(-1), sup)
+    (dz, clean), parts = grads(*what), grad_parts(*what)
     scored = (tt >= 0) & (tt < V)
-    e = float(logit_error(flat, w, scored, 1024).max()) * 8 if T else 0.0     # of p, and of z - lse beside the entropy
-    # a term p (g + gH (...)) has no part smaller than p |gH| for the error to hide in
-    size = dz.abs()
+    e = float(logit_error(flat, w, scored, 1024).max()) if T else 0.0
     if gh is not None:
-        check_grad(gh.reshape(-1, h.shape[-1]), dz @ w.double(), size @ w.double().abs() + 1e-6, e, V)
+        check_grad(gh.reshape(-1, h.shape[-1]), dz, parts, w, e)
         assert not bool(gh.reshape(-1, h.shape[-1])[~scored].any())
     if gw is not None and kw.get("accumulate") is None:
-        check_grad(gw, dz.T @ clean, size.T @ clean.abs() + 1e-6, e, T)
-    return gh, gw, dz, clean, (gl, ge, lse, ent)
+        check_grad(gw, dz.T, parts.T, clean, e)
+    return gh, gw, dz, clean, parts
 
 
 SIZES = [(1, 1, 8, 1.0, 0), (1, 2, 8, 1.0, 1), (3, 7, 16, 1.0, 2), (33, 300, 64, 0.5, 1), (61, 1000, 72, 1.0, 0),
@@ -176,10 +181,10 @@ def test_nan_and_infinities_where_no_row_is_scored(cs):
     gh, gw = cs.lm_head_logprobs_backward(h, w, t, lse, ent, gl, ge, suppress_ids=sup)
     assert bool(torch.isfinite(gh).all()) and bool(torch.isfinite(gw).all())
     assert not bool(gh[live[3]].any()) and not bool(gh[live[5]].any())
-    dz, clean = grads(h, w, t, lse, ent, gl, ge, sup)
-    e = 8 * float(logit_error(clean, w, torch.ones_like(dead), 1024).max())
-    check_grad(gh, dz @ w.double(), dz.abs() @ w.double().abs() + 1e-6, e, 777)
-    check_grad(gw, dz.T @ clean, dz.abs().T @ clean.abs() + 1e-6, e, 200)
+    (dz, clean), parts = grads(h, w, t, lse, ent, gl, ge, sup), grad_parts(h, w, t, lse, ent, gl, ge, sup)
+    e = float(logit_error(clean, w, torch.ones_like(dead), 1024).max())
+    check_grad(gh, dz, parts, w, e)
+    check_grad(gw, dz.T, parts.T, clean, e)
 
 
 def test_rows_without_mass_and_with_infinite_logits(cs):
@@ -237,11 +242,12 @@ def test_given_outputs(cs, dtype, accumulate):
     gh_all = torch.randn((T, d + 8), device="cuda").to(BF16)
     old = gw_all.clone()
     before = gh_all.clone()
-    gh, gw, dz, clean, _ = check_backward(cs, h, w, t, sup, out=(gh_all[:, :d], gw_all[:, :d]),
+    gh, gw, dz, clean, parts = check_backward(cs, h, w, t, sup, out=(gh_all[:, :d], gw_all[:, :d]),
                                           **({"accumulate": True} if accumulate else {}))
     assert gw.data_ptr() == gw_all.data_ptr() and torch.equal(gw_all[:, d:], old[:, d:])
     assert torch.equal(gh_all[:, d:], before[:, d:])
-    check_grad(gw, dz.T @ clean, dz.abs().T @ clean.abs() + 1e-6, 1e-3, T, old[:, :d] if accumulate else None)
+    e = float(logit_error(h, w, (t >= 0) & (t < V), 1024).max())
+    check_grad(gw, dz.T, parts.T, clean, e, old[:, :d] if accumulate else None)
 
 
 @pytest.mark.parametrize("dtype", [BF16, torch.float32], ids=["bf16", "f32"])
@@ -250,12 +256,12 @@ def test_adding_over_many_tiles(cs, dtype, T, V, d):
     """Micro-batches added to one gradient: each call adds its own, rounded once."""
     h, w, t, sup = inputs(T, V, d, V, 0.9, 1)
     gw = torch.randn((V, d), device="cuda").to(dtype) * 0.1
-    e = 8 * float(logit_error(h, w, (t >= 0) & (t < V), 1024).max())
+    e = float(logit_error(h, w, (t >= 0) & (t < V), 1024).max())
     for seed in range(2):
         old = gw.clone()
-        gh, got, dz, clean, _ = check_backward(cs, h, w, t, sup, seed=seed, out=(None, gw), accumulate=True)
+        gh, got, dz, clean, parts = check_backward(cs, h, w, t, sup, seed=seed, out=(None, gw), accumulate=True)
         assert got is gw
-        check_grad(gw, dz.T @ clean, dz.abs().T @ clean.abs() + 1e-6, e, T, old)
+        check_grad(gw, dz.T, parts.T, clean, e, old)
 
 
 def test_strided_inputs_and_batches(cs):
