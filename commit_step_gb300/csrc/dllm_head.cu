@@ -253,10 +253,10 @@ __device__ __forceinline__ uint32_t hd_bf16x2(float lo, float hi) {
   return d;
 }
 
-// A tile of dw costs its slabs and, for its output's 128 KB, those of 4 more, 6 at
-// least (512 x 126464 x 4096: 1148, 1129 and 1107 us with 0, 2 and 4 more; 61 x 50257 x
-// 768: 66, 70 and 72 us with 6, 8 and 10 at least).
-__host__ __device__ constexpr int hd_dw_cost(int slabs) { return slabs > 2 ? slabs + 4 : 6; }
+// A tile of dw costs its slabs and, for its output's 128 KB, those of 4 more (512 x
+// 126464 x 4096: 1148, 1129 and 1107 us with 0, 2 and 4 more); one of a slab or two
+// costs 4 (61 x 50257 x 768: 72, 64, 62, 63, 66 and 70 us with 2, 3, 4, 5, 6 and 8).
+__host__ __device__ constexpr int hd_dw_cost(int slabs) { return slabs > 2 ? slabs + 4 : 4; }
 
 // How many ways the second product's K is split: the least of the pairs' time, which
 // is their share of all tiles, or the rounds that dh's take where these are more (the

@@ -45,5 +45,39 @@ def test_gradients(cs):
         assert float((got.grad.double() - ref.grad).norm()) <= 4 * 2.0 ** -8 * float(ref.grad.norm())
 
 
+def test_a_captured_step(cs):
+    """Forward and backward as one graph: what it replays is what the eager step computes."""
+    m = example()
+    model = m.TinyMaskedModel(seed=7)
+    tokens = torch.randint(0, model.vocab - 1, (4, 64), dtype=torch.int32, generator=torch.Generator().manual_seed(8)).cuda()
+    canvas, targets, weight = m.noised(tokens, model.mask_id, torch.Generator().manual_seed(9))
+
+    def step():
+        lp, ent = cs.score_hidden(model.hidden(canvas), model.weight, targets, suppress_ids=(model.mask_id,))
+        value = (-(weight * lp).sum() - 0.01 * ent.sum()) / tokens.numel()
+        return value.detach(), torch.autograd.grad(value, model.parameters())
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        value, grads = step()
+    for seed in (10, 11):
+        c, t, w = m.noised(tokens, model.mask_id, torch.Generator().manual_seed(seed))
+        canvas.copy_(c), targets.copy_(t), weight.copy_(w)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [value.clone(), *[g.clone() for g in grads]]
+        want_value, want = step()
+        # (torch's own products may add in another order inside a graph)
+        assert abs(got[0].item() - want_value.item()) <= 2.0 ** -8 * abs(want_value.item())
+        for a, b in zip(got[1:], want):
+            assert float((a.double() - b.double()).norm()) <= 2.0 ** -7 * float(b.double().norm())
+
+
 def test_it_runs(cs):
     example().main()
