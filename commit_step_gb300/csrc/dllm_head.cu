@@ -10,7 +10,8 @@
 // kernel joins a row's partials.
 //
 // Backward, over pieces of the vocabulary so that only a piece of dz is ever
-// held (bf16, as the product's operands have to be): dz = the product again,
+// held (bf16, as the product's operands have to be; up to 128 rows in two parts, whose
+// second takes the half of dH's tiles that is empty then): dz = the product again,
 // with p = exp(z - lse) and dz = -p (g + gH (z - lse + H)) + g [v = target] in its
 // epilogue; dH += dz W over the piece (K: the piece's ids); dW = dz^T H (K: the
 // scored rows).
@@ -31,6 +32,7 @@
 // 4506 x 126464 x 4096 backward in 8.4 to 8.6 ms (1.63 to 1.67; a cuBLAS product of
 // 8192^3 run for seconds: 1.69).
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -107,6 +109,7 @@ struct HeadParams {
   float* z_target;               // score: per scored row
   const HeadRow* row;            // dz
   uint16_t* dz;                  // dz: (rows, dz_stride) bf16
+  int32_t two;                   // at most 128 rows: dz in two parts, the second in the rows from 128 on
   int64_t dz_stride;
   float* acc;                    // dh: (splits, row tiles x 128, acc_stride) fp32
   int64_t acc_stride;
@@ -308,7 +311,7 @@ struct HeadWork {
     slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
     splits = p.n_rows[1];
     total = p.want_h ? static_cast<int64_t>(n_m) * n_n * splits : 0;
-    slabs_w = static_cast<int32_t>((n + kHdBK - 1) / kHdBK);
+    slabs_w = static_cast<int32_t>((n + kHdBK - 1) / kHdBK) * (p.two ? 2 : 1);
     total_w = p.want_w && n > 0 ? (p.cols + kHdBM - 1) / kHdBM * n_n : 0;
     rest = static_cast<int32_t>(total % pairs);
     if (rest > 0) extra = min(static_cast<int64_t>(slabs / splits / hd_dw_cost(slabs_w)), total_w / (pairs - rest));
@@ -595,7 +598,8 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       const bool dw = OP == kHdBack && t.dw;
       const int m0 = t.m * kHdBM + static_cast<int>(rank) * kHdRows, n0 = t.n * p.bn + static_cast<int>(rank) * half;
       // The second CTA's rows may all be past the end: then its A is not loaded.
-      const bool second = static_cast<int64_t>(t.m) * kHdBM + kHdRows < (dw ? p.cols : n);
+      // (Of dz in two parts they are the second part.)
+      const bool second = (OP == kHdBack && !dw && p.two) || static_cast<int64_t>(t.m) * kHdBM + kHdRows < (dw ? p.cols : n);
       const uint32_t tx = (second ? 2u : 1u) * (dw ? kHdABytes : p.a_bytes) + static_cast<uint32_t>(p.bn) * kHdBK * 2;
       const uint32_t lead_a = rank == 0 || second ? lead : 0u;
       for (int k = t.k0; k < t.k1; ++k) {
@@ -608,10 +612,13 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         const uint32_t a = ring + static_cast<uint32_t>(s) * p.stage_bytes, b = a + kHdABytes;
         hd_expect(lead0, smem_addr(&full_bar[s]), tx);
         if (dw) {
-          hd_load(lead_a, a, &p.tm_aw, m0, k * kHdBK, bar);
-          hd_load(lead_a, a + 8192, &p.tm_aw, m0 + 64, k * kHdBK, bar);
-          hd_load(lead, b, mw, n0, k * kHdBK, bar);
-          if (half > 64) hd_load(lead, b + 8192, mw, n0 + 64, k * kHdBK, bar);
+          // (dz's second part meets the same hidden states)
+          const bool low = p.two && 2 * k >= t.k1;
+          const int y = (low ? k - t.k1 / 2 : k) * kHdBK, yz = low ? y + kHdRows : y;
+          hd_load(lead_a, a, &p.tm_aw, m0, yz, bar);
+          hd_load(lead_a, a + 8192, &p.tm_aw, m0 + 64, yz, bar);
+          hd_load(lead, b, mw, n0, y, bar);
+          if (half > 64) hd_load(lead, b + 8192, mw, n0 + 64, y, bar);
         } else {
           hd_load(lead_a, a, ma, k * kHdBK, m0, bar);
           if (OP == kHdBack) {
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       const int in_tile = static_cast<int>(min(static_cast<int64_t>(p.bn), width - col0));
       // Rows a warp has to visit: those that exist; of dz also the rows up to the
       // end of the third product's last slab, which read as zero.
-      const int64_t visit = dw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : n);
+      const int64_t visit = dw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : (p.two ? rank * kHdRows + n : n));
       const bool warp_rows = row - lane < visit;
       if constexpr (OP != kHdBack) {
         HeadRow info{};
@@ -772,6 +779,11 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
             // (up to the tile's end and the row's; what is there past the piece reads as zero)
             const int room = static_cast<int>(min(static_cast<int64_t>(p.bn - c), p.dz_stride - col0 - c));
             if (row < visit) hd_store_dz(p.dz + row * p.dz_stride + col0 + c, z, room);
+            if (row < visit && p.two) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) z[q] -= __bfloat162float(__float2bfloat16_rn(z[q]));
+              hd_store_dz(p.dz + (row + kHdRows) * p.dz_stride + col0 + c, z, room);
+            }
           }
         };
         if (t.k1 <= hd_part(OP)) {
@@ -1146,7 +1158,8 @@ __device__ __forceinline__ void hd_put8(uint16_t* at, const float (&y)[8]) {
 }
 
 __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, const int32_t* place, const float* acc,
-                                                      int64_t acc_stride, int64_t d, uint16_t* out, int64_t out_stride) {
+                                                      int64_t acc_stride, int32_t two, int64_t d, uint16_t* out,
+                                                      int64_t out_stride) {
   __shared__ float part[8][8][33];
   pdl_wait();
   pdl_launch_dependents();
@@ -1161,7 +1174,10 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, con
     if (c >= d) return;
     float y[8] = {};
     if (row >= 0)
-      for (int s = 0; s < splits; ++s) hd_add8(y, from + s * step + c);
+      for (int s = 0; s < splits; ++s) {
+        hd_add8(y, from + s * step + c);
+        if (two) hd_add8(y, from + s * step + kHdRows * acc_stride + c);
+      }
     hd_put8(to + c, y);
     return;
   }
@@ -1170,7 +1186,10 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, con
     float y[8] = {};
     if (c < d)
 #pragma unroll 4
-      for (int s = warp; s < splits; s += 8) hd_add8(y, from + s * step + c);
+      for (int s = warp; s < splits; s += 8) {
+        hd_add8(y, from + s * step + c);
+        if (two) hd_add8(y, from + s * step + kHdRows * acc_stride + c);
+      }
 #pragma unroll
     for (int e = 0; e < 8; ++e) part[warp][e][lane] = y[e];
     __syncthreads();
@@ -1547,6 +1566,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   std::copy(sup.begin(), sup.end(), p.sup);
   p.row = l.row;
   p.dz = reinterpret_cast<uint16_t*>(ws + h.dz);
+  // Few rows leave half of every tile of dh empty: what bf16 cuts off dz takes it.
+  p.two = T <= kHdRows ? 1 : 0;
   p.dz_stride = h.piece;
   p.acc = reinterpret_cast<float*>(ws + h.accs);
   p.acc_stride = static_cast<int64_t>(h.n_d) * h.bn_d;
@@ -1607,7 +1628,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   uint16_t* out = static_cast<uint16_t*>(grad_hidden);
   const int32_t* place = l.place;
   int64_t stride = p.acc_stride;
-  void* args[] = {&n_rows, &place, &acc, &stride, &d, &out, &grad_hidden_stride};
+  int32_t two = p.two;
+  void* args[] = {&n_rows, &place, &acc, &stride, &two, &d, &out, &grad_hidden_stride};
   return launch_pdl(reinterpret_cast<const void*>(&head_dh_kernel), dim3(static_cast<unsigned>(T), static_cast<unsigned>((d + 2047) / 2048)),
                     dim3(256), 0, stream, args);
 }

@@ -74,13 +74,13 @@ def check_scores(cs, h, w, t, sup, **kw):
     return lp, ent, lse
 
 
-def check_grad(got, dz, parts, by, e, old=None):
-    """got against dz @ by (dz and its parts transposed for the weight's)."""
+def check_grad(got, dz, parts, by, e, old=None, dz_bits=8):
+    """got against dz @ by (dz and its parts transposed for the weight's), dz rounded by 2^-dz_bits."""
     half = torch.finfo(got.dtype).eps / 2
     exact, by = dz @ by.double(), by.double().abs()
     want = exact if old is None else exact + old.double()
     slack = (2 * e + 2.0 ** -18) * (parts @ by)
-    lim = (2.0 ** -8 + dz.shape[1] * 2.0 ** -23) * (dz.abs() @ by) + slack + half * want.abs() + 1e-30
+    lim = (2.0 ** -dz_bits + dz.shape[1] * 2.0 ** -23) * (dz.abs() @ by) + slack + half * want.abs() + 1e-30
     err = (got.double() - want).abs()
     assert bool((err <= lim * (1 + half)).all()), float((err - lim).max())
     if exact.numel() >= 4096 and old is None:
@@ -262,6 +262,24 @@ def test_adding_over_many_tiles(cs, dtype, T, V, d):
         gh, got, dz, clean, parts = check_backward(cs, h, w, t, sup, seed=seed, out=(None, gw), accumulate=True)
         assert got is gw
         check_grad(gw, dz.T, parts.T, clean, e, old)
+
+
+@pytest.mark.parametrize("T,V,d,scored", [(1, 300, 64, 1.0), (7, 5000, 136, 1.0), (64, 3001, 256, 0.5), (65, 1000, 520, 1.0),
+                                          (128, 40000, 72, 0.9)])
+def test_few_rows_keep_what_bf16_cuts_off(cs, T, V, d, scored):
+    """dz in two parts: 2^-16 of an element is lost, so a gradient in 32 bits is that exact, and one in bf16 is off by its
+    own rounding (2^-8 / sqrt 3 in the root mean square, 0.6 of 2^-8 asked for)."""
+    h, w, t, sup = inputs(T, V, d, 90 + T, scored, 1)
+    wide = torch.empty((V, d), device="cuda")
+    gh, gw, dz, clean, parts = check_backward(cs, h, w, t, sup, out=(None, wide))
+    e = float(logit_error(h, w, (t >= 0) & (t < V), 1024).max())
+    check_grad(wide, dz.T, parts.T, clean, e, dz_bits=16)
+    check_grad(gh, dz, parts, w, e, dz_bits=16)
+    narrow = check_backward(cs, h, w, t, sup)[1]
+    want = dz.T @ clean
+    slack = (2 * e + 2.0 ** -18) * (parts.T @ clean.abs())
+    if want.numel() >= 4096:
+        assert float((narrow.double() - want).norm()) <= 0.6 * 2.0 ** -8 * float(want.norm()) + float(slack.norm())
 
 
 def test_strided_inputs_and_batches(cs):
