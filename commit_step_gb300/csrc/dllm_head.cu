@@ -28,7 +28,7 @@
 //
 // What bounds it: the weight's stream while there are few rows (32 x 126464 x 4096 in
 // 169 us, 6.1 TB/s), from some 300 rows on the tensor cores, and in a run of such
-// calls the card's power: 4096 x 152064 x 3584 in 2.5 to 2.6 ms (1.71 to 1.79 PFLOP/s),
+// calls the card's power: 4096 x 152064 x 3584 in 2.48 to 2.54 ms (1.76 to 1.80 PFLOP/s),
 // 4506 x 126464 x 4096 backward in 8.4 to 8.6 ms (1.63 to 1.67; a cuBLAS product of
 // 8192^3 run for seconds: 1.69).
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
@@ -73,11 +73,12 @@ enum HeadOp { kHdScore, kHdDz, kHdBack };         // the last: dH and dW, tiles 
 // The tensor core adds in fp32 and cuts off what does not fit: summed in one
 // accumulator, the logits of d = 4096 were off by 4e-6 of themselves, always toward
 // zero, and a confident row's log probability by 2e-5.  So an accumulator takes some
-// slabs of K, and these parts are added in registers, rounded.  Errors of the scores
-// of 8 rows of d = 4096 and 4096 x 152064 x 3584 rows' time in one part, in parts of
-// 16, 8 and 4 slabs: 5e-6, 1.3e-6, 6e-7, 2e-7 and 2506, 2507, 2605, 2750 us.  dz, which
-// is rounded to bf16, only has to agree with a log-sum-exp so formed.
-__host__ __device__ constexpr int hd_part(int op) { return op == kHdScore ? 8 : 16; }
+// slabs of K, and these parts are added in registers, rounded.  Entropies of 32 rows of
+// d = 4096 and the time of 4096 x 152064 x 3584 in parts of 8, 9, 10, 11 and 12 slabs: off
+// by 5.7e-7, 7.1e-7, 7.3e-7, 8.1e-7 and 8.9e-7 of themselves; 2575, 2530, 2478, 2521 and
+// 2462 us (16: 2463; 4: some 2760).  dz, which is rounded to bf16, only has to agree with
+// a log-sum-exp so formed.
+__host__ __device__ constexpr int hd_part(int op) { return op == kHdScore ? 10 : 16; }
 
 // A scored row's constants of the backward pass.
 struct HeadRow {
@@ -111,7 +112,7 @@ struct HeadParams {
   uint16_t* dz;                  // dz: (rows, dz_stride) bf16
   int32_t two;                   // at most 128 rows: dz in two parts, the second in the rows from 128 on
   int64_t dz_stride;
-  float* acc;                    // dh: (splits, row tiles x 128, acc_stride) fp32
+  float* acc;                    // dh: (splits, row tiles x 256, acc_stride) fp32
   int64_t acc_stride;
   int32_t add;                   // dh: the piece is not the first
   void* grad_w;                  // dw

@@ -2,9 +2,9 @@
 against 64-bit formulas.
 
 Tolerances (derived).  A logit is a sum of d products, added in parts of at most
-512 (1024 backward) one by one in 32 bits, truncated, and the parts rounded: off by
-at most (512 + d / 512) 2^-23 sum |h w|, called e below (its largest over the ids).  lse and log probabilities move by at most 2 e, the
-entropy by at most e sum p |log p + H| <= 2 e (H + 1) <= 2 e (ln V + 1), beside
+640 (1024 backward) one by one in 32 bits, truncated, and the parts rounded: off by
+at most (640 + d / 640) 2^-23 sum |h w|, called e below (its largest over the ids).
+lse and log probabilities move by at most 2 e, the entropy by at most e sum p |log p + H| <= 2 e (H + 1) <= 2 e (ln V + 1), beside
 2^-15 + 2^-21 |value| (2^-12 for the entropy) of the sums of exponentials.
 
 The gradient's dz is rounded to bf16 (2^-8 of itself at most) after the errors of z
@@ -42,7 +42,7 @@ def inputs(T, V, d, seed, scored=1.0, n_sup=0, spread=2.5):
     return h.to(BF16), w, t, sup
 
 
-def logit_error(h, w, scored, part=512):
+def logit_error(h, w, scored, part=640):
     """e, per row."""
     d = h.shape[1]
     terms = min(d, part) + d // part
