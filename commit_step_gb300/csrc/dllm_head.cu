@@ -40,7 +40,6 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <vector>
 
 #include "../../include/dllmcommit.h"
 #include "dllm_device.cuh"
@@ -1334,22 +1333,27 @@ HdPlan hd_plan(int64_t T, int64_t V, int64_t d, int64_t sms, bool backward) {
 
 constexpr int64_t kHdMaxT = int64_t{1} << 24, kHdMaxD = int64_t{1} << 20;
 
-// What forward and backward check alike; `sup` takes the suppressed ids.
+struct HdSup {
+  int32_t n = 0;
+  int32_t id[DLLM_MAX_SUPPRESS];
+};
+
+// What forward and backward check alike; `sup` takes the suppressed ids, each once.
 dllm_status hd_check(const void* hidden, int64_t T, int64_t d, int64_t hidden_stride, const void* weight, int64_t V,
                      int64_t weight_stride, const int32_t* targets, const int32_t* suppress_ids, int32_t n_suppress,
-                     std::vector<int32_t>& sup) {
+                     HdSup& sup) {
   if (T < 0 || V < 1 || V > INT32_MAX || d < 1) return DLLM_ERR_INVALID_ARGUMENT;
   if (hidden_stride < d || weight_stride < d) return DLLM_ERR_INVALID_ARGUMENT;
   if (mul_or_neg(mul_or_neg(T, hidden_stride), 2) < 0 || mul_or_neg(mul_or_neg(V, weight_stride), 4) < 0)
     return DLLM_ERR_INVALID_ARGUMENT;
   if (n_suppress < 0 || (n_suppress > 0 && !suppress_ids)) return DLLM_ERR_INVALID_ARGUMENT;
   if (n_suppress > DLLM_MAX_SUPPRESS) return DLLM_ERR_UNSUPPORTED;
-  sup.assign(suppress_ids, suppress_ids + n_suppress);
-  for (int32_t id : sup)
-    if (id < 0 || id >= V) return DLLM_ERR_INVALID_ARGUMENT;
-  std::sort(sup.begin(), sup.end());
-  sup.erase(std::unique(sup.begin(), sup.end()), sup.end());
-  if (static_cast<int64_t>(sup.size()) >= V) return DLLM_ERR_INVALID_ARGUMENT;
+  for (int32_t i = 0; i < n_suppress; ++i)
+    if (suppress_ids[i] < 0 || suppress_ids[i] >= V) return DLLM_ERR_INVALID_ARGUMENT;
+  std::copy(suppress_ids, suppress_ids + n_suppress, sup.id);
+  std::sort(sup.id, sup.id + n_suppress);
+  sup.n = static_cast<int32_t>(std::unique(sup.id, sup.id + n_suppress) - sup.id);
+  if (sup.n >= V) return DLLM_ERR_INVALID_ARGUMENT;
   if (T == 0) return DLLM_OK;
   if (!hidden || !weight || !targets || !aligned4(targets)) return DLLM_ERR_INVALID_ARGUMENT;
   if (d % 8 != 0 || !aligned16(hidden) || !aligned16(weight) || hidden_stride % 8 != 0 || weight_stride % 8 != 0)
@@ -1407,7 +1411,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
                                   int64_t V, int64_t weight_stride, const int32_t* targets, const int32_t* suppress_ids,
                                   int32_t n_suppress, float* logprob, float* entropy, float* lse, void* workspace,
                                   size_t workspace_bytes, dllm_stream_t stream) {
-  std::vector<int32_t> sup;
+  HdSup sup;
   dllm_status st = hd_check(hidden, T, d, hidden_stride, weight, V, weight_stride, targets, suppress_ids, n_suppress, sup);
   if (st != DLLM_OK || T == 0) return st;
   if (!logprob || !entropy || !lse || !aligned4(logprob) || !aligned4(entropy) || !aligned4(lse)) return DLLM_ERR_INVALID_ARGUMENT;
@@ -1451,8 +1455,8 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   p.idesc = hd_idesc(false, false, h.bn_v);
   hd_ring(p, kHdScore, static_cast<int32_t>(a_rows), dev->sms / 2);
   p.target = l.target;
-  p.n_sup = static_cast<int32_t>(sup.size());
-  std::copy(sup.begin(), sup.end(), p.sup);
+  p.n_sup = sup.n;
+  std::copy(sup.id, sup.id + sup.n, p.sup);
   // One row tile costs the same however many of its rows are scored: they are taken as
   // they are, without the kernel that numbers them (61 x 50257 x 768: 26 and 22 us).
   const bool direct = T <= kHdBM;
@@ -1477,8 +1481,8 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   f.pairs = dev->sms / 2;
   f.z_target = p.z_target;
   f.n_sup = p.n_sup;
-  std::copy(sup.begin(), sup.end(), f.sup);
-  f.ln_ids = static_cast<float>(std::log(static_cast<double>(V - static_cast<int64_t>(sup.size()))));
+  std::copy(sup.id, sup.id + sup.n, f.sup);
+  f.ln_ids = static_cast<float>(std::log(static_cast<double>(V - sup.n)));
   f.logprob = logprob;
   f.entropy = entropy;
   f.lse = lse;
@@ -1503,7 +1507,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
                                            void* grad_hidden, int64_t grad_hidden_stride, void* grad_weight,
                                            dllm_dtype grad_weight_dt, int64_t grad_weight_stride, int32_t accumulate,
                                            void* workspace, size_t workspace_bytes, dllm_stream_t stream) {
-  std::vector<int32_t> sup;
+  HdSup sup;
   dllm_status st = hd_check(hidden, T, d, hidden_stride, weight, V, weight_stride, targets, suppress_ids, n_suppress, sup);
   if (st != DLLM_OK) return st;
   if (grad_weight_dt != DLLM_F32 && grad_weight_dt != DLLM_BF16) return DLLM_ERR_INVALID_ARGUMENT;
@@ -1548,8 +1552,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   l.entropy = entropy;
   l.g = grad_logprob;
   l.gh = grad_entropy;
-  l.n_sup = static_cast<int32_t>(sup.size());
-  std::copy(sup.begin(), sup.end(), l.sup);
+  l.n_sup = sup.n;
+  std::copy(sup.id, sup.id + sup.n, l.sup);
   l.n_rows = n_rows;
   l.rows = reinterpret_cast<int32_t*>(ws + h.rows);
   l.place = reinterpret_cast<int32_t*>(ws + h.place);
@@ -1564,7 +1568,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   p.d = d;
   p.target = l.target;
   p.n_sup = l.n_sup;
-  std::copy(sup.begin(), sup.end(), p.sup);
+  std::copy(sup.id, sup.id + sup.n, p.sup);
   p.row = l.row;
   p.dz = reinterpret_cast<uint16_t*>(ws + h.dz);
   // Few rows leave half of every tile of dh empty: what bf16 cuts off dz takes it.
