@@ -8,7 +8,7 @@ import torch
 
 from . import DLLM_BF16, DLLM_F32, _check, _lib, _need_cuda
 from .cache import _raw_stream
-from .head import _size, _workspace
+from .head import _may_capture, _size, _stamp, _workspace
 
 
 _DTYPES = {torch.bfloat16: DLLM_BF16, torch.float32: DLLM_F32}
@@ -133,6 +133,7 @@ class _EmbedCanvas(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         tokens, = ctx.saved_tensors
+        _may_capture(ctx)
         g = g.contiguous()
         if torch.is_grad_enabled():                                              # (under create_graph)
             return None, _EmbedGrad.apply(tokens, g, ctx.V, ctx.scale), None
@@ -141,5 +142,7 @@ class _EmbedCanvas(torch.autograd.Function):
 
 def embed_canvas(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0):
     """embed_tokens for training: differentiable once with respect to ``weight``
-    through autograd."""
-    return _EmbedCanvas.apply(tokens, weight, float(scale))
+    through autograd, and captured as score_hidden is."""
+    out = _EmbedCanvas.apply(tokens, weight, float(scale))
+    _stamp(out)
+    return out

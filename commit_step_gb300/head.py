@@ -172,6 +172,30 @@ def lm_head_logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, target
     return gh, gw
 
 
+_STREAM = "commit_step_gb300.stream"
+
+
+def _leaves(node):
+    """The accumulators of the leaves that a step of a graph was made from.  One lives
+    as long as any graph that holds it, and runs on the stream of the first."""
+    return [f for f, _ in node.next_functions if f is not None and f.name().endswith("AccumulateGrad")]
+
+
+def _stamp(result):
+    """Writes the current stream down where the leaves' accumulators are new."""
+    if result.requires_grad:
+        for f in _leaves(result.grad_fn):
+            f.metadata.setdefault(_STREAM, torch._C._cuda_getCurrentRawStream(result.get_device()))
+
+
+def _may_capture(node):
+    """Refuses a captured gradient of a leaf whose accumulator a graph made on the
+    default stream keeps: it would run there, which a capture may not touch."""
+    if torch.cuda.is_current_stream_capturing() and any(f.metadata.get(_STREAM) == 0 for f in _leaves(node)):
+        raise RuntimeError("this gradient is captured while a result computed from the same leaf on the default stream "
+                           "lives: drop that result first, or compute it on another stream")
+
+
 def _head_grad(hidden, weight, targets, lse, ent, suppress_ids, g_lp, g_ent, want):
     # (gradients that reach here expanded from a scalar are not contiguous)
     g_lp, g_ent = [None if g is None else g.float().contiguous() for g in (g_lp, g_ent)]
@@ -205,6 +229,7 @@ class _ScoreHidden(torch.autograd.Function):
     def backward(ctx, g_lp, g_ent):
         hidden, weight, targets, lse, ent = ctx.saved_tensors
         want = ctx.needs_input_grad[:2]
+        _may_capture(ctx)
         grad = _HeadGrad.apply if torch.is_grad_enabled() else _head_grad        # (enabled under create_graph)
         gh, gw = grad(hidden, weight, targets, lse, ent, ctx.suppress_ids, g_lp, g_ent, want)
         return gh, gw, None, None
@@ -212,5 +237,9 @@ class _ScoreHidden(torch.autograd.Function):
 
 def score_hidden(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, suppress_ids: Sequence[int] = ()):
     """lm_head_logprobs for training: (logprob, entropy), differentiable once with
-    respect to ``hidden`` and ``weight`` through autograd."""
-    return _ScoreHidden.apply(hidden, weight, targets, tuple(suppress_ids))
+    respect to ``hidden`` and ``weight`` through autograd.  A backward pass that is
+    captured into a CUDA graph is refused while a result lives that was computed from
+    the same leaves on the default stream (warm up on another)."""
+    logprob, entropy = _ScoreHidden.apply(hidden, weight, targets, tuple(suppress_ids))
+    _stamp(logprob)
+    return logprob, entropy

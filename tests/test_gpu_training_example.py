@@ -79,5 +79,26 @@ def test_a_captured_step(cs):
             assert float((a.double() - b.double()).norm()) <= 2.0 ** -7 * float(b.double().norm())
 
 
+def test_a_captured_step_beside_a_living_result(cs):
+    """The leaves' accumulators of a result made on the default stream run there: a captured gradient is refused while
+    it lives, and made when it is gone."""
+    w = torch.randn((50, 16), device="cuda").to(torch.bfloat16).requires_grad_()
+    t = torch.randint(0, 50, (2, 9), dtype=torch.int32, device="cuda")
+    x = torch.randn((2, 9, 16), device="cuda").to(torch.bfloat16)
+    for value in (lambda: cs.score_hidden(x, w, t)[0].sum(), lambda: cs.embed_canvas(t, w).float().square().sum()):
+        want, = torch.autograd.grad(value(), w)
+        kept = value()
+        with pytest.raises(RuntimeError, match="default stream"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                torch.autograd.grad(value(), w)
+        del kept
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got, = torch.autograd.grad(value(), w)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_it_runs(cs):
     example().main()

@@ -141,3 +141,46 @@ def test_reference_embedding_gradient():
     out = embedding_grad(t, g, 5, 2.0)
     assert torch.equal(out[2], 2 * (g[0, 0] + g[0, 2]).double()) and torch.equal(out[4], 2 * g[1, 1].double())
     assert not bool(out[1].any() or out[3].any()) and torch.equal(out[0], 2 * g[0, 1].double())
+
+
+def test_a_captured_gradient_beside_a_living_graph_of_the_default_stream(monkeypatch):
+    """On the CPU, with the two questions about streams answered by the test."""
+    from commit_step_gb300 import head
+
+    class Twice(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, y, n):
+            return x * y.sum()
+
+        @staticmethod
+        def backward(ctx, g):
+            head._may_capture(ctx)
+            return g, None, None
+
+    stream, capturing = [0], [False]
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: stream[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+
+    def graph(x, y, on):
+        stream[0] = on
+        out = Twice.apply(x, y, 3)
+        head._stamp(out)
+        return out.sum()
+
+    w, v = torch.ones(4, requires_grad=True), torch.ones(2)
+    head._stamp(Twice.apply(v, v, 3))                        # nothing to differentiate
+    kept = graph(w, v, 0)
+    kept.backward()
+    capturing[0] = True
+    captured = graph(w, v, 7)
+    with pytest.raises(RuntimeError, match="default stream"):
+        captured.backward()
+    graph(w * 2, v, 7).backward()                            # not made from the leaf itself
+    del kept, captured
+    graph(w, v, 7).backward()
+    capturing[0] = False
+    warm = graph(w, v, 5)                                    # first made on a stream that may join a capture
+    kept = graph(w, v, 0)
+    capturing[0] = True
+    graph(w, v, 7).backward()
+    assert float(w.grad[0]) > 0 and warm is not None and kept is not None
