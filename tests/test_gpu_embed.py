@@ -110,6 +110,32 @@ def test_orders_of_tokens(cs, kind):
     assert torch.equal(got, cs.embed_tokens_backward(t, grad, V))
 
 
+def test_offsets_past_32_bits(cs):
+    """Rows of a weight and of its gradient, then tokens of a canvas, whose elements lie past 2^31."""
+    V, d, step = 1000, 64, 1 << 22
+    t = canvas(2, 700, V, 60, 0.1, 0.1)
+    t[0, :2] = torch.tensor([V - 1, V - 2], device="cuda")
+    w = torch.empty((V * step,), dtype=BF16, device="cuda").as_strided((V, d), (step, 1)).copy_(torch.randn((V, d)))
+    ok = (t >= 0) & (t < V)
+    want = torch.where(ok[..., None], w[torch.where(ok, t, torch.zeros_like(t)).long()], torch.zeros((), dtype=BF16, device="cuda"))
+    assert torch.equal(cs.embed_tokens(t, w), want)
+    g = torch.randn((2, 700, d), device="cuda").to(BF16)
+    check(cs.embed_tokens_backward(t, g, V, out=w), t, g, V, 1.0)
+    del w
+    B, L, V, d = 2, 270000, 50, 4096                       # 2.2e9 elements
+    t = torch.randint(0, V, (B, L), dtype=torch.int32, device="cuda")
+    w = torch.randn((V, d), device="cuda").to(BF16)
+    x = cs.embed_tokens(t, w)
+    for b in range(B):
+        for l in range(0, L, 45000):
+            assert torch.equal(x[b, l:l + 45000], w[t[b, l:l + 45000].long()])
+    value = torch.arange(B * L, device="cuda") % 7         # (whole numbers: every order gives the same sum)
+    x.copy_(value.view(B, L, 1))
+    out = cs.embed_tokens_backward(t, x, V, out=torch.empty((V, d), device="cuda"))
+    want = torch.bincount(t.view(-1).long(), weights=value.double(), minlength=V)
+    assert torch.equal(out.double(), want[:, None].expand(V, d))
+
+
 def test_no_tokens(cs):
     t, g = torch.empty((3, 0), dtype=torch.int32, device="cuda"), torch.empty((3, 0, 16), dtype=BF16, device="cuda")
     assert cs.embed_tokens(t, torch.randn((5, 16), device="cuda").to(BF16)).shape == (3, 0, 16)

@@ -296,6 +296,21 @@ def test_strided_inputs_and_batches(cs):
     assert torch.equal(c[0], e[0]) and torch.equal(c[1], e[1])
 
 
+def far(x, step):
+    """x in rows of `step` elements."""
+    wide = torch.empty((x.shape[0] * step,), dtype=x.dtype, device=x.device).as_strided(x.shape, (step, 1))
+    return wide.copy_(x)
+
+
+@pytest.mark.parametrize("T", [300, 200])
+def test_offsets_past_32_bits(cs, T):
+    h, w, t, sup = inputs(T, 1000, 64, 60 + T, 0.8, 2)
+    h, w = far(h, 1 << 24), far(w, 1 << 22)
+    check_scores(cs, h, w, t, sup)
+    check_backward(cs, h, w, t, sup, out=(far(h, 1 << 24), far(w.float(), 1 << 22)))
+    check_backward(cs, h, w, t, sup, out=(far(h, 1 << 24), far(w, 1 << 22)))
+
+
 def test_results_repeat_and_do_not_depend_on_the_workspace(cs):
     h, w, t, sup = inputs(900, 30000, 256, 14, 0.5, 1)
     g = torch.randn(900, device="cuda")
