@@ -28,7 +28,7 @@
 //
 // What bounds it: the weight's stream while there are few rows (32 x 126464 x 4096 in
 // 169 us, 6.1 TB/s), from some 300 rows on the tensor cores, and in a run of such
-// calls the card's power: 4096 x 152064 x 3584 in 2.48 to 2.54 ms (1.76 to 1.80 PFLOP/s),
+// calls the card's power: 4096 x 152064 x 3584 in 2.43 to 2.54 ms (1.76 to 1.84 PFLOP/s),
 // 4506 x 126464 x 4096 backward in 8.4 to 8.6 ms (1.63 to 1.67; a cuBLAS product of
 // 8192^3 run for seconds: 1.69).
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
