@@ -1328,8 +1328,14 @@ HdPlan hd_plan(int64_t T, int64_t V, int64_t d, int64_t sms, bool backward) {
     h.z_target = take(4 * T);
     h.part = take(static_cast<int64_t>(sizeof(float4)) * 2 * h.n_v * h.t_pad);
   }
-  h.bytes = at;
+  h.bytes = at + 240;                            // (hd_base leaves out as many at most)
   return h;
+}
+
+// Where the offsets of a plan begin: a workspace is 16-byte aligned, and dz is written
+// in stores of 32 bytes.  The fault word stays the workspace's own first word.
+uint8_t* hd_base(void* workspace) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
 }
 
 constexpr int64_t kHdMaxT = int64_t{1} << 24, kHdMaxD = int64_t{1} << 20;
@@ -1426,7 +1432,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   const HdDevice* dev = hd_device();
   if (!dev) return DLLM_ERR_CUDA;
   const HdPlan h = hd_plan(T, V, d, dev->sms, false);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = hd_base(workspace);
   int32_t* n_rows = reinterpret_cast<int32_t*>(ws + 128);
 
   HeadListParams l{};
@@ -1468,7 +1474,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   p.part = reinterpret_cast<float4*>(ws + h.part);
   p.part_rows = h.t_pad;
   p.z_target = reinterpret_cast<float*>(ws + h.z_target);
-  p.fault = reinterpret_cast<int32_t*>(ws);
+  p.fault = static_cast<int32_t*>(workspace);
 
   HeadFinishParams f{};
   f.n_rows = p.n_rows;
@@ -1541,7 +1547,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   const HdDevice* dev = hd_device();
   if (!dev) return DLLM_ERR_CUDA;
   const HdPlan h = hd_plan(T, V, d, dev->sms, true);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = hd_base(workspace);
   int32_t* n_rows = reinterpret_cast<int32_t*>(ws + 128);
 
   HeadListParams l{};
@@ -1581,7 +1587,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   p.grad_w_stride = grad_weight_stride;
   p.grad_w_f32 = grad_weight_dt == DLLM_F32 ? 1 : 0;
   p.accumulate = accumulate != 0 ? 1 : 0;
-  p.fault = reinterpret_cast<int32_t*>(ws);
+  p.fault = static_cast<int32_t*>(workspace);
   HeadParams pz = p, pb = p;
   const int64_t packed_rows = round_up(T, kHdBK);
   if (!make_map(&pz.tm_a, hidden, T, d, hidden_stride, a_rows) ||

@@ -327,6 +327,25 @@ def test_results_repeat_and_do_not_depend_on_the_workspace(cs):
     assert all(torch.equal(a, b) for a, b in zip(*runs))
 
 
+@pytest.mark.parametrize("T,V,d,scored", [(61, 1000, 72, 1.0), (300, 3000, 64, 0.5)])
+def test_workspaces_at_any_16_bytes(cs, T, V, d, scored):
+    """A workspace of just the size asked for, wherever it begins: the same results, and nothing behind it is touched."""
+    h, w, t, sup = inputs(T, V, d, 70 + T, scored, 1)
+    g = torch.randn(T, device="cuda")
+    want = [*cs.lm_head_logprobs(h, w, t, suppress_ids=sup)]
+    want += cs.lm_head_logprobs_backward(h, w, t, want[2], want[1], g, g, suppress_ids=sup)
+    sizes = [int(getattr(cs.lib_handle(), f"dllm_lm_head_logprobs_{x}workspace_size")(T, V, d)) for x in ("", "backward_")]
+    for shift in (16, 32, 48, 128, 240, 256):
+        pools = [torch.zeros(shift + need + 64, dtype=torch.uint8, device="cuda") for need in sizes]
+        ws = [pool[shift:shift + need] for pool, need in zip(pools, sizes)]
+        assert all(x.data_ptr() % 256 == shift % 256 for x in ws)
+        got = [*cs.lm_head_logprobs(h, w, t, suppress_ids=sup, ws=ws[0])]
+        got += cs.lm_head_logprobs_backward(h, w, t, got[2], got[1], g, g, suppress_ids=sup, ws=ws[1])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(cs.workspace_fault(x) == 0 for x in ws)
+        assert not any(bool(pool[:shift].any() or pool[shift + need:].any()) for pool, need in zip(pools, sizes))
+
+
 def test_autograd(cs):
     h, w, t, sup = inputs(77, 900, 128, 15, 0.6, 1)
     ha, wa = h.view(7, 11, 128).clone().requires_grad_(), w.clone().requires_grad_()
