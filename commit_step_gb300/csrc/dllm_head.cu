@@ -762,7 +762,8 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
           } else {
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-              const float y = fmaxf(z[q], -kHdCap) - info.lse;
+              // (a probability that small is 0; times gh the difference itself may pass fp32, and 0 inf is NaN)
+              const float y = fmaxf(z[q] - info.lse, -1000.0f);
               const float e = ex2_approx(y * kLog2e);
               z[q] = -e * fmaf(info.gh, y + info.entropy, info.g);
             }

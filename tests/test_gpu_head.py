@@ -212,6 +212,25 @@ def test_rows_without_mass_and_with_infinite_logits(cs):
     assert float(lse[0]) == math.inf and abs(float(lp[0]) + math.log(2)) < 1e-5 and abs(float(ent[0]) - math.log(2)) < 1e-5
 
 
+@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("far", [-2.0 ** 62, -2.0 ** 66, -2.0 ** 67, math.nan])
+def test_an_id_without_mass_under_a_large_entropy_gradient(cs, T, far):
+    """An id whose logit is far below the others' (-2^122 .. -2^127, or NaN) has no gradient, however large the entropy's:
+    bit for bit what suppressing it gives."""
+    h, w, t, _ = inputs(T, 300, 64, 80 + T)
+    h[:, 0], w[:, 0] = 2.0 ** 60, 0.0
+    w[17, 0] = far
+    t[t == 17] = 3
+    _, ent, lse = cs.lm_head_logprobs(h, w, t)
+    assert bool((lse.abs() < 100).all())
+    gl, ge = torch.randn(T, device="cuda"), torch.randn(T, device="cuda") * 1e4
+    finite = not math.isnan(far)                         # (times 0 a NaN would reach grad_hidden)
+    got = cs.lm_head_logprobs_backward(h, w, t, lse, ent, gl, ge, hidden_grad=finite)
+    want = cs.lm_head_logprobs_backward(h, w, t, lse, ent, gl, ge, suppress_ids=[17], hidden_grad=finite)
+    assert bool(torch.isfinite(got[1]).all()) and torch.equal(got[1], want[1])
+    assert not finite or (bool(torch.isfinite(got[0]).all()) and torch.equal(got[0], want[0]))
+
+
 def test_suppressed_target(cs):
     h, w, t, _ = inputs(9, 333, 64, 10)
     t[4] = 11
