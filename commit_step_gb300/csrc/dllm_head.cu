@@ -10,7 +10,7 @@
 // kernel joins a row's partials.
 //
 // Backward, over pieces of the vocabulary so that only a piece of dz is ever
-// held (bf16, as the product's operands have to be; up to 128 rows in two parts, whose
+// held (bf16, as the product's operands have to be; of up to 128 scored rows in two parts, whose
 // second takes the half of dH's tiles that is empty then): dz = the product again,
 // with p = exp(z - lse) and dz = -p (g + gH (z - lse + H)) + g [v = target] in its
 // epilogue; dH += dz W over the piece (K: the piece's ids); dW = dz^T H (K: the
@@ -109,7 +109,6 @@ struct HeadParams {
   float* z_target;               // score: per scored row
   const HeadRow* row;            // dz
   uint16_t* dz;                  // dz: (rows, dz_stride) bf16
-  int32_t two;                   // at most 128 rows: dz in two parts, the second in the rows from 128 on
   int64_t dz_stride;
   float* acc;                    // dh: (splits, row tiles x 256, acc_stride) fp32
   int64_t acc_stride;
@@ -288,6 +287,9 @@ struct HeadTile {
   bool dw;
 };
 
+// Up to kHdRows scored rows, however many are given, leave half of every tile of dh
+// empty: what bf16 cuts off dz takes it, as the rows from kHdRows on.
+
 // The tiles in the order in which this pair of CTAs takes them: tile i goes to pair i
 // mod pairs, dh's before dw's; the pairs that a last round of dh leaves out take as
 // many tiles of dw as fit its time first.
@@ -297,11 +299,12 @@ struct HeadWork {
   int32_t n_n;
   int32_t n_m, slabs, splits;            // of scores, dz or dh
   int64_t total;
+  bool two;                              // dz in two parts
   int32_t slabs_w, rest;                 // dw; dh's tiles in a last round
   int64_t total_w, extra;
 
   __device__ __forceinline__ HeadWork(const HeadParams& p, int64_t n)
-      : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), n_n(p.n_n), splits(1), slabs_w(0), rest(0), total_w(0), extra(0) {
+      : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), n_n(p.n_n), splits(1), two(n <= kHdRows), slabs_w(0), rest(0), total_w(0), extra(0) {
     n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
     if (OP != kHdBack) {
       slabs = static_cast<int32_t>((p.d + kHdBK - 1) / kHdBK);
@@ -311,7 +314,7 @@ struct HeadWork {
     slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
     splits = p.n_rows[1];
     total = p.want_h ? static_cast<int64_t>(n_m) * n_n * splits : 0;
-    slabs_w = static_cast<int32_t>((n + kHdBK - 1) / kHdBK) * (p.two ? 2 : 1);
+    slabs_w = static_cast<int32_t>((n + kHdBK - 1) / kHdBK) * (two ? 2 : 1);
     total_w = p.want_w && n > 0 ? (p.cols + kHdBM - 1) / kHdBM * n_n : 0;
     rest = static_cast<int32_t>(total % pairs);
     if (rest > 0) extra = min(static_cast<int64_t>(slabs / splits / hd_dw_cost(slabs_w)), total_w / (pairs - rest));
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       const int m0 = t.m * kHdBM + static_cast<int>(rank) * kHdRows, n0 = t.n * p.bn + static_cast<int>(rank) * half;
       // The second CTA's rows may all be past the end: then its A is not loaded.
       // (Of dz in two parts they are the second part.)
-      const bool second = (OP == kHdBack && !dw && p.two) || static_cast<int64_t>(t.m) * kHdBM + kHdRows < (dw ? p.cols : n);
+      const bool second = (OP == kHdBack && !dw && work.two) || static_cast<int64_t>(t.m) * kHdBM + kHdRows < (dw ? p.cols : n);
       const uint32_t tx = (second ? 2u : 1u) * (dw ? kHdABytes : p.a_bytes) + static_cast<uint32_t>(p.bn) * kHdBK * 2;
       const uint32_t lead_a = rank == 0 || second ? lead : 0u;
       for (int k = t.k0; k < t.k1; ++k) {
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         hd_expect(lead0, smem_addr(&full_bar[s]), tx);
         if (dw) {
           // (dz's second part meets the same hidden states)
-          const bool low = p.two && 2 * k >= t.k1;
+          const bool low = work.two && 2 * k >= t.k1;
           const int y = (low ? k - t.k1 / 2 : k) * kHdBK, yz = low ? y + kHdRows : y;
           hd_load(lead_a, a, &p.tm_aw, m0, yz, bar);
           hd_load(lead_a, a + 8192, &p.tm_aw, m0 + 64, yz, bar);
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
       const int in_tile = static_cast<int>(min(static_cast<int64_t>(p.bn), width - col0));
       // Rows a warp has to visit: those that exist; of dz also the rows up to the
       // end of the third product's last slab, which read as zero.
-      const int64_t visit = dw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : (p.two ? rank * kHdRows + n : n));
+      const int64_t visit = dw ? p.cols : (OP == kHdDz ? (n + kHdBK - 1) / kHdBK * kHdBK : (work.two ? rank * kHdRows + n : n));
       const bool warp_rows = row - lane < visit;
       if constexpr (OP != kHdBack) {
         HeadRow info{};
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
             // (up to the tile's end and the row's; what is there past the piece reads as zero)
             const int room = static_cast<int>(min(static_cast<int64_t>(p.bn - c), p.dz_stride - col0 - c));
             if (row < visit) hd_store_dz(p.dz + row * p.dz_stride + col0 + c, z, room);
-            if (row < visit && p.two) {
+            if (row < visit && work.two) {
 #pragma unroll
               for (int q = 0; q < 32; ++q) z[q] -= __bfloat162float(__float2bfloat16_rn(z[q]));
               hd_store_dz(p.dz + (row + kHdRows) * p.dz_stride + col0 + c, z, room);
@@ -1160,12 +1163,13 @@ __device__ __forceinline__ void hd_put8(uint16_t* at, const float (&y)[8]) {
 }
 
 __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, const int32_t* place, const float* acc,
-                                                      int64_t acc_stride, int32_t two, int32_t width, int64_t d, uint16_t* out,
+                                                      int64_t acc_stride, int32_t width, int64_t d, uint16_t* out,
                                                       int64_t out_stride) {
   __shared__ float part[8][8][33];
   pdl_wait();
   pdl_launch_dependents();
   const int64_t n = n_rows[0], t = blockIdx.x, c0 = blockIdx.y * static_cast<int64_t>(width);
+  const bool two = n <= kHdRows;
   const int splits = n_rows[1], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = (n + kHdBM - 1) / kHdBM * kHdBM * acc_stride;
   const int32_t row = place[t];
@@ -1579,8 +1583,6 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   std::copy(sup.id, sup.id + sup.n, p.sup);
   p.row = l.row;
   p.dz = reinterpret_cast<uint16_t*>(ws + h.dz);
-  // Few rows leave half of every tile of dh empty: what bf16 cuts off dz takes it.
-  p.two = T <= kHdRows ? 1 : 0;
   p.dz_stride = h.piece;
   p.acc = reinterpret_cast<float*>(ws + h.accs);
   p.acc_stride = static_cast<int64_t>(h.n_d) * h.bn_d;
@@ -1641,9 +1643,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   uint16_t* out = static_cast<uint16_t*>(grad_hidden);
   const int32_t* place = l.place;
   int64_t stride = p.acc_stride;
-  int32_t two = p.two;
   int32_t width = T <= kHdRows ? 256 : 2048;
-  void* args[] = {&n_rows, &place, &acc, &stride, &two, &width, &d, &out, &grad_hidden_stride};
+  void* args[] = {&n_rows, &place, &acc, &stride, &width, &d, &out, &grad_hidden_stride};
   return launch_pdl(reinterpret_cast<const void*>(&head_dh_kernel), dim3(static_cast<unsigned>(T), static_cast<unsigned>((d + width - 1) / width)),
                     dim3(256), 0, stream, args);
 }

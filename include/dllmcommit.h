@@ -680,8 +680,8 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
  * read into any result.  Suppressed ids get 0.
  * dz is formed piece by piece of the vocabulary (at most 2^28 elements, or 4096
  * ids, at a time) and held in bf16, as the products' operands have to be: each
- * element is rounded by at most 2^-8 of itself, with T up to 128 (held in two parts)
- * by 2^-16; sums are fp32.
+ * element is rounded by at most 2^-8 of itself, where up to 128 rows take part (held
+ * in two parts) by 2^-16; sums are fp32.
  *   grad_hidden  device bf16 (T, d), rows grad_hidden_stride elements apart, or
  *                NULL (not wanted)
  *   grad_weight  device (V, d) fp32 or bf16 (grad_weight_dt), rows

@@ -301,6 +301,20 @@ def test_few_rows_keep_what_bf16_cuts_off(cs, T, V, d, scored):
         assert float((narrow.double() - want).norm()) <= 0.6 * 2.0 ** -8 * float(want.norm()) + float(slack.norm())
 
 
+@pytest.mark.parametrize("T,V,d,scored", [(129, 300, 64, 0.02), (300, 3001, 256, 0.03), (8192, 5000, 136, 0.002),
+                                          (200, 1000, 520, 0.55), (20000, 9000, 64, 0.005)])
+def test_few_scored_rows_of_many_keep_what_bf16_cuts_off(cs, T, V, d, scored):
+    """The parts of dz go by the rows that take part, not by the rows given."""
+    h, w, t, sup = inputs(T, V, d, 95 + T, scored, 1)
+    n = int(((t >= 0) & (t < V)).sum())
+    assert 0 < n <= 128
+    wide = torch.empty((V, d), device="cuda")
+    gh, gw, dz, clean, parts = check_backward(cs, h, w, t, sup, out=(None, wide))
+    e = float(logit_error(h, w, (t >= 0) & (t < V), 1024).max())
+    check_grad(wide, dz.T, parts.T, clean, e, dz_bits=16)
+    check_grad(gh, dz, parts, w, e, dz_bits=16)
+
+
 def test_strided_inputs_and_batches(cs):
     h, w, t, sup = inputs(150, 700, 96, 13, 0.7, 1)
     hw = torch.full((150, 200), math.nan, dtype=BF16, device="cuda")
