@@ -256,9 +256,17 @@ __device__ __forceinline__ uint32_t hd_bf16x2(float lo, float hi) {
 }
 
 // A tile of dw costs its slabs and, for its output's 128 KB, those of 4 more (512 x
-// 126464 x 4096: 1148, 1129 and 1107 us with 0, 2 and 4 more); one of a slab or two
-// costs 4 (61 x 50257 x 768: 72, 64, 62, 63, 66 and 70 us with 2, 3, 4, 5, 6 and 8).
-__host__ __device__ constexpr int hd_dw_cost(int slabs) { return slabs > 2 ? slabs + 4 : 4; }
+// 126464 x 4096: 1146, 1120 and 1107 us with 2, 3 and 4 more); one of up to 4 slabs 2
+// more (61 x 50257 x 768, 2 slabs: 76, 68, 66, 67, 70 and 73 us with 0, 1, 2, 3, 4 and 6
+// more; 100 x 126464 x 4096, 4 slabs: 669, 635, 615, 616, 637 and 665).
+__host__ __device__ constexpr int hd_dw_cost(int slabs) { return slabs > 4 ? slabs + 4 : slabs + 2; }
+
+// dz in two parts: up to kHdRows scored rows, however many are given, leave half of every
+// tile of dh empty, and what bf16 cuts off dz takes it, as the rows from kHdRows on.
+__device__ __forceinline__ bool hd_two(int64_t n) { return n <= kHdRows; }
+
+// The slabs of a tile of dw.
+__device__ __forceinline__ int hd_dw_slabs(int64_t n) { return static_cast<int>((n + kHdBK - 1) / kHdBK) * (hd_two(n) ? 2 : 1); }
 
 // How many ways the second product's K is split: the least of the pairs' time, which
 // is their share of all tiles, or the rounds that dh's take where these are more (the
@@ -270,7 +278,7 @@ __device__ __forceinline__ int hd_splits(int64_t n, int n_n, int bn, int pairs, 
   const int tiles = static_cast<int>((n + kHdBM - 1) / kHdBM) * n_n;
   const float size = static_cast<float>(tiles) * static_cast<float>(kHdBM * bn);
   const float share = (static_cast<float>(tiles) * slabs +
-                       static_cast<float>(dw_tiles) * hd_dw_cost(static_cast<int>((n + kHdBK - 1) / kHdBK))) / static_cast<float>(pairs);
+                       static_cast<float>(dw_tiles) * hd_dw_cost(hd_dw_slabs(n))) / static_cast<float>(pairs);
   const float rounds = ceilf(static_cast<float>(tiles) * s / static_cast<float>(pairs)) * ceilf(static_cast<float>(slabs) / s);
   float cost = fmaxf(share, rounds) * (bn / 256.0f) + s * size * (8.0f / 1.5e6f);
   if (s > 1 && (s > slabs || static_cast<int64_t>(s) * tiles * kHdBM * bn > room)) cost = 3.0e38f;
@@ -287,9 +295,6 @@ struct HeadTile {
   bool dw;
 };
 
-// Up to kHdRows scored rows, however many are given, leave half of every tile of dh
-// empty: what bf16 cuts off dz takes it, as the rows from kHdRows on.
-
 // The tiles in the order in which this pair of CTAs takes them: tile i goes to pair i
 // mod pairs, dh's before dw's; the pairs that a last round of dh leaves out take as
 // many tiles of dw as fit its time first.
@@ -304,7 +309,7 @@ struct HeadWork {
   int64_t total_w, extra;
 
   __device__ __forceinline__ HeadWork(const HeadParams& p, int64_t n)
-      : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), n_n(p.n_n), splits(1), two(n <= kHdRows), slabs_w(0), rest(0), total_w(0), extra(0) {
+      : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), n_n(p.n_n), splits(1), two(hd_two(n)), slabs_w(0), rest(0), total_w(0), extra(0) {
     n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
     if (OP != kHdBack) {
       slabs = static_cast<int32_t>((p.d + kHdBK - 1) / kHdBK);
@@ -314,7 +319,7 @@ struct HeadWork {
     slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
     splits = p.n_rows[1];
     total = p.want_h ? static_cast<int64_t>(n_m) * n_n * splits : 0;
-    slabs_w = static_cast<int32_t>((n + kHdBK - 1) / kHdBK) * (two ? 2 : 1);
+    slabs_w = hd_dw_slabs(n);
     total_w = p.want_w && n > 0 ? (p.cols + kHdBM - 1) / kHdBM * n_n : 0;
     rest = static_cast<int32_t>(total % pairs);
     if (rest > 0) extra = min(static_cast<int64_t>(slabs / splits / hd_dw_cost(slabs_w)), total_w / (pairs - rest));
@@ -1169,7 +1174,7 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, con
   pdl_wait();
   pdl_launch_dependents();
   const int64_t n = n_rows[0], t = blockIdx.x, c0 = blockIdx.y * static_cast<int64_t>(width);
-  const bool two = n <= kHdRows;
+  const bool two = hd_two(n);
   const int splits = n_rows[1], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = (n + kHdBM - 1) / kHdBM * kHdBM * acc_stride;
   const int32_t row = place[t];
