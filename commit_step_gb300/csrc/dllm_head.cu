@@ -68,6 +68,7 @@ constexpr float kHdCap = 0x1p+125f;              // logits are read within +-2^1
 constexpr float kHdAbsent = -0x1p+126f;          // suppressed ids and columns past the vocabulary
 
 enum HeadOp { kHdScore, kHdDz, kHdBack };         // the last: dH and dW, tiles of both in one launch
+enum HeadOut { kHdBf16, kHdBf16Add, kHdF32 };
 
 // The tensor core adds in fp32 and cuts off what does not fit: summed in one
 // accumulator, the logits of d = 4096 were off by 4e-6 of themselves, always toward
@@ -77,7 +78,19 @@ enum HeadOp { kHdScore, kHdDz, kHdBack };         // the last: dH and dW, tiles 
 // by 5.7e-7, 7.1e-7, 7.3e-7, 8.1e-7 and 8.9e-7 of themselves; 2575, 2530, 2478, 2521 and
 // 2462 us (16: 2463; 4: some 2760).  dz, which is rounded to bf16, only has to agree with
 // a log-sum-exp so formed.
-__host__ __device__ constexpr int hd_part(int op) { return op == kHdScore ? 10 : 16; }
+//
+// A sum of dW is as long as the rows scored: of 2^21 terms of one sign it was off by
+// 1.4 %.  It takes parts of at most 128 slabs, of about one length (backward of 4506 x
+// 126464 x 4096, 71 slabs: in one part 8.54 ms, in two 8.58, in three 8.69).  The registers
+// that hold them make the epilogue of short tiles slower (61 x 50257 x 768: 65 and 69
+// us), so the kernel with parts is another one, taken where there may be as many rows.
+// dH's sums are rounded to bf16 and split over the piece's ids already.
+__host__ __device__ constexpr int hd_part(int op) { return op == kHdScore ? 10 : (op == kHdDz ? 16 : 128); }
+
+__device__ __forceinline__ int hd_dw_part(int slabs) {
+  const int parts = (slabs + hd_part(kHdBack) - 1) / hd_part(kHdBack);
+  return (slabs + parts - 1) / parts;
+}
 
 // A scored row's constants of the backward pass.
 struct HeadRow {
@@ -206,26 +219,26 @@ __device__ __forceinline__ void hd_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void hd_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // 32 consecutive fp32 columns of this warp's 32 TMEM lanes, one lane a thread.
-__device__ __forceinline__ void hd_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void hd_ld32(uint32_t taddr, float (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr)
       : "memory");
 }
 
 // 16 columns.
-__device__ __forceinline__ void hd_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void hd_ld16(uint32_t taddr, float (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(taddr)
       : "memory");
 }
@@ -415,38 +428,34 @@ __device__ __forceinline__ void hd_store_dz(uint16_t* out, const float (&x)[32],
   }
 }
 
-// This warp's 32 rows of 64 accumulator columns at taddr, as bf16, to columns x and
-// rows y of the tensor: through shared memory in the 128-byte swizzle and out by
-// TMA, so that memory sees whole lines (stored from registers, a row a thread, the
-// weight's gradient of 512 x 126464 x 4096 took 504 us in a launch of its own, and 381
-// so).
-// `done` is called once the accumulator has been read.
-template <class Done>
-__device__ __forceinline__ void hd_store_tile(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane, Done done) {
-  uint32_t w[32];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t r[32];
-    hd_ld32(taddr + 32 * h, r);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[16 * h + j] = hd_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-  }
-  done();
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (the last one has left the buffer)
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((j ^ (lane & 7)) << 4)), "r"(w[4 * j]),
-                 "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
-                 : "memory");
+// This warp's 32 rows of 64 columns (a row a thread, 32 of them in each of x and y), as
+// bf16, to column col and row `row` of the tensor: through shared memory in the 128-byte
+// swizzle and out by TMA, so that memory sees whole lines (stored from registers, a row a
+// thread, the weight's gradient of 512 x 126464 x 4096 took 504 us in a launch of its own,
+// and 381 so).
+__device__ __forceinline__ void hd_tile_out(const CUtensorMap* map, int col, int row, uint32_t buf, int lane) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
   if (lane == 0) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(buf)
+                 "r"(col), "r"(row), "r"(buf)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
+}
+
+__device__ __forceinline__ void hd_store_tile(const float (&x)[32], const float (&y)[32], uint32_t buf, const CUtensorMap* map, int col,
+                                              int row, int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (the last one has left the buffer)
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float* v = (j < 4 ? x : y) + 8 * (j & 3);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((j ^ (lane & 7)) << 4)), "r"(hd_bf16x2(v[0], v[1])),
+                 "r"(hd_bf16x2(v[2], v[3])), "r"(hd_bf16x2(v[4], v[5])), "r"(hd_bf16x2(v[6], v[7]))
+                 : "memory");
+  }
+  hd_tile_out(map, col, row, buf, lane);
 }
 
 // The same, added to what is there, whose 32 x 64 the buffer holds (loaded by TMA while
@@ -460,55 +469,42 @@ __device__ __forceinline__ void hd_load_old(uint32_t buf, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void hd_add_tile(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane) {
+__device__ __forceinline__ void hd_add_tile(const float (&x)[32], const float (&y)[32], uint32_t buf, const CUtensorMap* map, int col,
+                                            int row, int lane) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t r[32];
-    hd_ld32(taddr + 32 * h, r);
+  for (int j = 0; j < 8; ++j) {
+    const float* v = (j < 4 ? x : y) + 8 * (j & 3);
+    const uint32_t at = buf + lane * 128 + ((j ^ (lane & 7)) << 4);
+    const uint4 o = lds128(at);
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t at = buf + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4);
-      const uint4 o = lds128(at);
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = hd_bf16x2(__uint_as_float(r[8 * j + 2 * e]) + bf16lo((&o.x)[e]), __uint_as_float(r[8 * j + 2 * e + 1]) + bf16hi((&o.x)[e]));
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-    }
+    for (int e = 0; e < 4; ++e) w[e] = hd_bf16x2(v[2 * e] + bf16lo((&o.x)[e]), v[2 * e + 1] + bf16hi((&o.x)[e]));
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncwarp();
-  if (lane == 0) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(buf)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  }
+  hd_tile_out(map, col, row, buf, lane);
 }
 
 // 32 columns in fp32, stored or added to what is there.
-__device__ __forceinline__ void hd_store_tile_f32(uint32_t taddr, uint32_t buf, const CUtensorMap* map, int x, int y, int lane, bool add) {
-  uint32_t r[32];
-  hd_ld32(taddr, r);
+__device__ __forceinline__ void hd_store_tile_f32(const float (&x)[32], uint32_t buf, const CUtensorMap* map, int col, int row, int lane,
+                                                  bool add) {
   if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((j ^ (lane & 7)) << 4)), "r"(r[4 * j]),
-                 "r"(r[4 * j + 1]), "r"(r[4 * j + 2]), "r"(r[4 * j + 3])
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((j ^ (lane & 7)) << 4)), "f"(x[4 * j]),
+                 "f"(x[4 * j + 1]), "f"(x[4 * j + 2]), "f"(x[4 * j + 3])
                  : "memory");
+  if (!add) {
+    hd_tile_out(map, col, row, buf, lane);
+    return;
+  }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
   if (lane == 0) {
-    if (add)
-      asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                       reinterpret_cast<uint64_t>(map)),
-                   "r"(x), "r"(y), "r"(buf)
-                   : "memory");
-    else
-      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                   "r"(x), "r"(y), "r"(buf)
-                   : "memory");
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(col), "r"(row), "r"(buf)
+                 : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 }
@@ -527,7 +523,8 @@ __device__ __forceinline__ void hd_store_f32(float* out, const float (&x)[32], i
   }
 }
 
-template <int OP>
+// Of kHdBack, OUT: how dW leaves; LONG: in parts.
+template <int OP, int OUT = kHdBf16, bool LONG = false>
 __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_constant__ HeadParams p) {
   extern __shared__ __align__(1024) uint8_t hd_smem[];
   __shared__ __align__(8) uint64_t full_bar[kHdMaxStages], empty_bar[kHdMaxStages], accf_bar[2], acce_bar[2];
@@ -660,7 +657,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         if (t.k0 == t.k1) continue;
         const bool dw = OP == kHdBack && t.dw;
         const uint32_t idesc = dw ? p.idesc_w : p.idesc, step_a = (dw ? 2048u : 32u) >> 4;
-        const int part = OP == kHdBack ? t.k1 - t.k0 : hd_part(OP);
+        const int part = OP != kHdBack ? hd_part(OP) : (LONG && dw ? hd_dw_part(t.k1) : t.k1 - t.k0);
         for (int k0 = t.k0; k0 < t.k1 && ok; k0 += part, ++j) {
           const int buf = j & 1;
           ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&acce_bar[buf]), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag));
@@ -695,7 +692,7 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
   } else if (warp < kHdEpiWarps) {
     const int ew = warp & 3, half = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(ew * 32) << 16);
-    const bool add16 = OP == kHdBack && p.accumulate && !p.grad_w_f32;
+    constexpr bool add16 = OP == kHdBack && OUT == kHdBf16Add;
     const uint32_t store_buf = ring + kHdRing - (kHdEpiWarps - warp) * (add16 ? 2 : 1) * kHdStoreBytes;   // (back: behind the last stage)
     uint32_t old_phase[2] = {0, 0}, old_asked = 0;
     HeadSoft soft{-kHdCap, 0.0f, 0.0f};
@@ -800,11 +797,8 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
           if (!await()) break;
 #pragma unroll 1
           for (int c = 32 * half; c < end; c += 64) {
-            uint32_t r[32];
             float z[32];
-            hd_ld32(lanes + static_cast<uint32_t>((j & 1) * kHdBN + c), r);
-#pragma unroll
-            for (int q = 0; q < 32; ++q) z[q] = __uint_as_float(r[q]);
+            hd_ld32(lanes + static_cast<uint32_t>((j & 1) * kHdBN + c), z);
             chunk(z, c);
           }
           release();
@@ -824,10 +818,10 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
               if (warp_rows && c < in_tile) {
 #pragma unroll
                 for (int h = 0; h < 32; h += 16) {
-                  uint32_t r[16];
+                  float r[16];
                   hd_ld16(lanes + static_cast<uint32_t>((j & 1) * kHdBN + c + h), r);
 #pragma unroll
-                  for (int q = 0; q < 16; ++q) z[i][h + q] += __uint_as_float(r[q]);
+                  for (int q = 0; q < 16; ++q) z[i][h + q] += r[q];
                 }
               }
             }
@@ -851,54 +845,79 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
                           static_cast<int>(p.v0 + row), smem_addr(&old_bar[warp][b]));
           old_asked = 3;
         }
-        if (!await()) break;
-        const uint32_t from = lanes + static_cast<uint32_t>((j & 1) * kHdBN);
-        bool released = false;
-        if (dw && add16) {
-          bool ok = true;
-          if (warp_rows)
+        // This warp's columns: 64 at 64 half, and 64 more 128 further on.
+        auto col = [&](int b) { return 64 * half + 128 * b; };
+        const int out_row = static_cast<int>(p.v0 + row) - lane;
+        bool ok = true;
+        // What becomes of 64 columns of this thread's row, 32 of them in x and in y.
+        auto put = [&](const float (&x)[32], const float (&y)[32], int b) {
+          const int c = col(b), at = static_cast<int>(col0) + c;
+          if (dw && add16) {
+            ok = ok && __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&old_bar[warp][b]), old_phase[b], abort_flag));
+            if (!ok) return;
+            old_phase[b] ^= 1u;
+            hd_add_tile(x, y, store_buf + b * kHdStoreBytes, &p.tm_out, at, out_row, lane);
+          } else if (dw && OUT == kHdBf16) {
+            hd_store_tile(x, y, store_buf, &p.tm_out, at, out_row, lane);
+          } else if (dw) {
+            hd_store_tile_f32(x, store_buf, &p.tm_out, at, out_row, lane, p.accumulate != 0);
+            if (c + 32 < in_tile) hd_store_tile_f32(y, store_buf, &p.tm_out, at + 32, out_row, lane, p.accumulate != 0);
+          } else if (row < visit) {
+            float* to = p.acc + (static_cast<int64_t>(t.split) * work.n_m * kHdBM + row) * p.acc_stride + col0 + c;
+            hd_store_f32(to, x, min(32, in_tile - c), p.add != 0);
+            hd_store_f32(to + 32, y, min(32, in_tile - c - 32), p.add != 0);
+          }
+        };
+        const int part = LONG && dw ? hd_dw_part(t.k1) : 0;
+        if (!LONG || !dw || part == t.k1) {
+          // One part: 64 columns at a time, the accumulator given back before the last are stored.
+          if (!await()) break;
+          bool released = false;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int c = 64 * half + 128 * b;
-              if (c >= in_tile || !ok) continue;
-              ok = __all_sync(0xFFFFFFFFu, hd_wait(smem_addr(&old_bar[warp][b]), old_phase[b], abort_flag));
-              if (!ok) continue;
-              old_phase[b] ^= 1u;
-              hd_add_tile(from + c, store_buf + b * kHdStoreBytes, &p.tm_out, static_cast<int>(col0) + c,
-                          static_cast<int>(p.v0 + row) - lane, lane);
+          for (int b = 0; b < 2; ++b) {
+            if (!warp_rows || col(b) >= in_tile) break;
+            float x[32], y[32];
+            const uint32_t from = lanes + static_cast<uint32_t>((j & 1) * kHdBN + col(b));
+            hd_ld32(from, x);
+            hd_ld32(from + 32, y);
+            if (b == 1 || col(1) >= in_tile) {
+              release();
+              released = true;
             }
-          if (!ok) {
-            if (lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
-            break;
+            put(x, y, b);
           }
-        } else if (dw && !p.grad_w_f32) {
-          if (warp_rows)
-            for (int c = half * 64; c < in_tile; c += 128)
-              hd_store_tile(from + c, store_buf, &p.tm_out, static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane, lane, [&] {
-                if (c + 128 >= in_tile) {
-                  release();
-                  released = true;
-                }
-              });
-        } else if (dw && p.grad_w_f32) {
-#pragma unroll 1
-          for (int c = half * 32; warp_rows && c < in_tile; c += 64)
-            hd_store_tile_f32(from + c, store_buf, &p.tm_out, static_cast<int>(col0) + c, static_cast<int>(p.v0 + row) - lane, lane,
-                              p.accumulate != 0);
+          if (!released) release();
         } else {
-#pragma unroll 1
-          for (int c = half * 32; warp_rows && c < in_tile; c += 64) {
-            uint32_t r[32];
-            hd_ld32(from + c, r);
-            const int lim = min(32, in_tile - c);
-            float x[32];
+          float z[4][32];
 #pragma unroll
-            for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(r[q]);
-            if (row >= visit) continue;
-            hd_store_f32(p.acc + (static_cast<int64_t>(t.split) * work.n_m * kHdBM + row) * p.acc_stride + col0 + c, x, lim, p.add != 0);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 32; ++q) z[i][q] = 0.0f;
+          for (int k = t.k0; k < t.k1; k += part) {
+            ok = await();
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (warp_rows && col(i >> 1) < in_tile) {
+#pragma unroll
+                for (int h = 0; h < 32; h += 16) {
+                  float r[16];
+                  hd_ld16(lanes + static_cast<uint32_t>((j & 1) * kHdBN + col(i >> 1) + 32 * (i & 1) + h), r);
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) z[i][h + q] += r[q];
+                }
+              }
+            release();
           }
+          if (!ok) break;
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            if (warp_rows && col(b) < in_tile) put(z[2 * b], z[2 * b + 1], b);
         }
-        if (!released) release();
+        if (!ok) {
+          if (lane == 0) hd_fail(p, abort_flag, kFaultFullWait);
+          break;
+        }
         old_asked = 0;
       }
     }
@@ -1251,6 +1270,15 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+const void* hd_back(int out, bool parts) {
+  static const void* const k[3][2] = {
+      {reinterpret_cast<const void*>(&head_kernel<kHdBack, kHdBf16, false>), reinterpret_cast<const void*>(&head_kernel<kHdBack, kHdBf16, true>)},
+      {reinterpret_cast<const void*>(&head_kernel<kHdBack, kHdBf16Add, false>),
+       reinterpret_cast<const void*>(&head_kernel<kHdBack, kHdBf16Add, true>)},
+      {reinterpret_cast<const void*>(&head_kernel<kHdBack, kHdF32, false>), reinterpret_cast<const void*>(&head_kernel<kHdBack, kHdF32, true>)}};
+  return k[out][parts ? 1 : 0];
+}
+
 struct HdDevice {
   int sms = 0;
   cudaError_t err = cudaSuccess;
@@ -1265,7 +1293,8 @@ const HdDevice* hd_device() {
     HdDevice& d = g_hd[dev];
     d.err = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     for (const void* k : {reinterpret_cast<const void*>(&head_kernel<kHdScore>), reinterpret_cast<const void*>(&head_kernel<kHdDz>),
-                          reinterpret_cast<const void*>(&head_kernel<kHdBack>)})
+                          hd_back(kHdBf16, false), hd_back(kHdBf16, true), hd_back(kHdBf16Add, false), hd_back(kHdBf16Add, true),
+                          hd_back(kHdF32, false), hd_back(kHdF32, true)})
       if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kHdSmem);
     if (d.err != cudaSuccess) (void)cudaGetLastError();  // report through the status, leave no sticky error
   });
@@ -1390,11 +1419,9 @@ void hd_ring(HeadParams& p, int op, int32_t a_rows, int64_t pairs) {
   p.clear_a = p.T <= kHdRows ? 1 : 0;
 }
 
-template <int OP>
-dllm_status hd_launch(HeadParams& p, int sms, dllm_stream_t stream) {
+dllm_status hd_launch(const void* kernel, HeadParams& p, int sms, dllm_stream_t stream) {
   void* args[] = {&p};
-  return launch_pdl(reinterpret_cast<const void*>(&head_kernel<OP>), dim3(static_cast<unsigned>(sms / 2 * 2)), dim3(kHdThreads), kHdSmem,
-                    stream, args, 2);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(sms / 2 * 2)), dim3(kHdThreads), kHdSmem, stream, args, 2);
 }
 
 dllm_status hd_list(HeadListParams& l, const HdPlan& h, uint8_t* ws, dllm_stream_t stream) {
@@ -1510,7 +1537,7 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   l.packed = reinterpret_cast<uint16_t*>(ws + h.hidden);
   if (!direct) st = hd_list(l, h, ws, stream);
   if (st != DLLM_OK) return st;
-  st = hd_launch<kHdScore>(p, dev->sms, stream);
+  st = hd_launch(reinterpret_cast<const void*>(&head_kernel<kHdScore>), p, dev->sms, stream);
   if (st != DLLM_OK) return st;
   void* fargs[] = {&f};
   return launch_pdl(reinterpret_cast<const void*>(&head_finish_kernel),
@@ -1630,6 +1657,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   l.room = h.acc;
   st = hd_list(l, h, ws, stream);
   if (st != DLLM_OK) return st;
+  const void* back = hd_back(p.grad_w_f32 ? kHdF32 : (p.accumulate ? kHdBf16Add : kHdBf16), grad_weight && T > hd_part(kHdBack) * kHdBK);
   for (int64_t v0 = 0; v0 < V; v0 += h.piece) {
     const int64_t cols = std::min(h.piece, V - v0);
     for (HeadParams* q : {&pz, &pb}) {
@@ -1639,8 +1667,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
     }
     // (to the end of the second product's last slab, where dz reads as zero)
     pz.n_n = static_cast<int32_t>((round_up(cols, kHdBK) + h.bn_v - 1) / h.bn_v);
-    st = hd_launch<kHdDz>(pz, dev->sms, stream);
-    if (st == DLLM_OK) st = hd_launch<kHdBack>(pb, dev->sms, stream);
+    st = hd_launch(reinterpret_cast<const void*>(&head_kernel<kHdDz>), pz, dev->sms, stream);
+    if (st == DLLM_OK) st = hd_launch(back, pb, dev->sms, stream);
     if (st != DLLM_OK) return st;
   }
   if (!grad_hidden) return DLLM_OK;

@@ -315,6 +315,31 @@ def test_few_scored_rows_of_many_keep_what_bf16_cuts_off(cs, T, V, d, scored):
     check_grad(gh, dz, parts, w, e, dz_bits=16)
 
 
+@pytest.mark.parametrize("T", [1 << 15, 1 << 21])
+def test_long_sums_of_one_sign_do_not_drift(cs, T):
+    """A weight's gradient of many rows, every term of a sum of one sign.  The tensor core cuts off what 32 bits do not hold,
+    product by product at worst, so a part of 8192 products is off by 8192 2^-23 of itself at most; the parts are added
+    rounded (T / 8192 2^-24).  An element of dz is rounded by 2^-8 of itself at most, and where all terms are nearly one
+    value (1 - p near 1, whose bf16 neighbours are 2^-8 apart) all of them the same way, so that the sum is off by as much."""
+    V, d = 64, 64
+    g = torch.Generator(device="cuda").manual_seed(T)
+    h = (torch.rand((T, d), device="cuda", generator=g) + 0.5).to(BF16)
+    w = (torch.randn((V, d), device="cuda", generator=g) * 0.1).to(BF16)
+    t = torch.zeros(T, dtype=torch.int32, device="cuda")
+    one = torch.ones(T, device="cuda")
+    _, ent, lse = cs.lm_head_logprobs(h, w, t)
+    got = torch.empty((V, d), device="cuda")
+    cs.lm_head_logprobs_backward(h, w, t, lse, ent, one, hidden_grad=False, out=(None, got))
+    dz, clean = grads(h, w, t, lse, ent, one, None)
+    assert bool((dz[:, 0] >= 0).all()) and bool((dz[:, 1:] <= 0).all())
+    want = dz.T @ clean
+    e = float(logit_error(h, w, torch.ones_like(t, dtype=torch.bool), 1024).max())
+    lim = 8192 * 2.0 ** -23 + T / 8192 * 2.0 ** -24 + 2.0 ** -8
+    part = grad_parts(h, w, t, lse, ent, one, None, [])
+    slack = (2 * e + 2.0 ** -18) * (part.T @ clean)
+    assert bool(((got.double() - want).abs() <= lim * want.abs() + slack).all()), float(((got - want) / want).abs().max())
+
+
 def test_strided_inputs_and_batches(cs):
     h, w, t, sup = inputs(150, 700, 96, 13, 0.7, 1)
     hw = torch.full((150, 200), math.nan, dtype=BF16, device="cuda")
