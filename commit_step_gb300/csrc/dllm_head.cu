@@ -122,6 +122,7 @@ struct HeadParams {
   float* z_target;               // score: per scored row
   const HeadRow* row;            // dz
   uint16_t* dz;                  // dz: (rows, dz_stride) bf16
+  int32_t low;                   // a dw of 32 bits and more than kHdRows rows: dz's second part begins at this row
   int64_t dz_stride;
   float* acc;                    // dh: (splits, row tiles x 256, acc_stride) fp32
   int64_t acc_stride;
@@ -275,23 +276,29 @@ __device__ __forceinline__ uint32_t hd_bf16x2(float lo, float hi) {
 __host__ __device__ constexpr int hd_dw_cost(int slabs) { return slabs > 4 ? slabs + 4 : slabs + 2; }
 
 // dz in two parts: up to kHdRows scored rows, however many are given, leave half of every
-// tile of dh empty, and what bf16 cuts off dz takes it, as the rows from kHdRows on.
+// tile of dh empty, and what bf16 cuts off dz takes it, as the rows from kHdRows on.  For
+// a dw of 32 bits dz has its second part whatever the rows (`low`, where it begins, is
+// not 0), which meets the same hidden states in as many slabs more: of one part such
+// a gradient would be no more exact than one of 16 bits.  (512 x 126464 x 4096 into fp32:
+// 1.20 and 1.50 ms, 4506 rows 8.6 and 11.6.)
 __device__ __forceinline__ bool hd_two(int64_t n) { return n <= kHdRows; }
 
 // The slabs of a tile of dw.
-__device__ __forceinline__ int hd_dw_slabs(int64_t n) { return static_cast<int>((n + kHdBK - 1) / kHdBK) * (hd_two(n) ? 2 : 1); }
+__device__ __forceinline__ int hd_dw_slabs(int64_t n, int32_t low) {
+  return static_cast<int>((n + kHdBK - 1) / kHdBK) * (hd_two(n) || low > 0 ? 2 : 1);
+}
 
 // How many ways the second product's K is split: the least of the pairs' time, which
 // is their share of all tiles, or the rounds that dh's take where these are more (the
 // third product's tiles fill what a last round of dh leaves), and 8 bytes a split of
 // every element written and read again (1.5 MB in the time of a slab of 256 x 256 x
 // 64).  Called by a whole warp, a lane a number of splits.
-__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int bn, int pairs, int slabs, int64_t dw_tiles, int64_t room) {
+__device__ __forceinline__ int hd_splits(int64_t n, int n_n, int bn, int pairs, int slabs, int64_t dw_tiles, int32_t low, int64_t room) {
   const int s = (threadIdx.x & 31) + 1;
   const int tiles = static_cast<int>((n + kHdBM - 1) / kHdBM) * n_n;
   const float size = static_cast<float>(tiles) * static_cast<float>(kHdBM * bn);
   const float share = (static_cast<float>(tiles) * slabs +
-                       static_cast<float>(dw_tiles) * hd_dw_cost(hd_dw_slabs(n))) / static_cast<float>(pairs);
+                       static_cast<float>(dw_tiles) * hd_dw_cost(hd_dw_slabs(n, low))) / static_cast<float>(pairs);
   const float rounds = ceilf(static_cast<float>(tiles) * s / static_cast<float>(pairs)) * ceilf(static_cast<float>(slabs) / s);
   float cost = fmaxf(share, rounds) * (bn / 256.0f) + s * size * (8.0f / 1.5e6f);
   if (s > 1 && (s > slabs || static_cast<int64_t>(s) * tiles * kHdBM * bn > room)) cost = 3.0e38f;
@@ -317,12 +324,13 @@ struct HeadWork {
   int32_t n_n;
   int32_t n_m, slabs, splits;            // of scores, dz or dh
   int64_t total;
-  bool two;                              // dz in two parts
+  bool two;                              // dz in two parts, for dh and dw
+  int32_t low;                           // the second part's first row (0: there is none)
   int32_t slabs_w, rest;                 // dw; dh's tiles in a last round
   int64_t total_w, extra;
 
   __device__ __forceinline__ HeadWork(const HeadParams& p, int64_t n)
-      : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), n_n(p.n_n), splits(1), two(hd_two(n)), slabs_w(0), rest(0), total_w(0), extra(0) {
+      : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), n_n(p.n_n), splits(1), two(hd_two(n)), low(two ? kHdRows : p.low), slabs_w(0), rest(0), total_w(0), extra(0) {
     n_m = static_cast<int32_t>((n + kHdBM - 1) / kHdBM);
     if (OP != kHdBack) {
       slabs = static_cast<int32_t>((p.d + kHdBK - 1) / kHdBK);
@@ -332,7 +340,7 @@ struct HeadWork {
     slabs = static_cast<int32_t>((p.cols + kHdBK - 1) / kHdBK);
     splits = p.n_rows[1];
     total = p.want_h ? static_cast<int64_t>(n_m) * n_n * splits : 0;
-    slabs_w = hd_dw_slabs(n);
+    slabs_w = hd_dw_slabs(n, low);
     total_w = p.want_w && n > 0 ? (p.cols + kHdBM - 1) / kHdBM * n_n : 0;
     rest = static_cast<int32_t>(total % pairs);
     if (rest > 0) extra = min(static_cast<int64_t>(slabs / splits / hd_dw_cost(slabs_w)), total_w / (pairs - rest));
@@ -618,8 +626,8 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
         hd_expect(lead0, smem_addr(&full_bar[s]), tx);
         if (dw) {
           // (dz's second part meets the same hidden states)
-          const bool low = work.two && 2 * k >= t.k1;
-          const int y = (low ? k - t.k1 / 2 : k) * kHdBK, yz = low ? y + kHdRows : y;
+          const bool low = work.low > 0 && 2 * k >= t.k1;
+          const int y = (low ? k - t.k1 / 2 : k) * kHdBK, yz = low ? y + work.low : y;
           hd_load(lead_a, a, &p.tm_aw, m0, yz, bar);
           hd_load(lead_a, a + 8192, &p.tm_aw, m0 + 64, yz, bar);
           hd_load(lead, b, mw, n0, y, bar);
@@ -785,10 +793,10 @@ __global__ void __launch_bounds__(kHdThreads, 1) head_kernel(const __grid_consta
             // (up to the tile's end and the row's; what is there past the piece reads as zero)
             const int room = static_cast<int>(min(static_cast<int64_t>(p.bn - c), p.dz_stride - col0 - c));
             if (row < visit) hd_store_dz(p.dz + row * p.dz_stride + col0 + c, z, room);
-            if (row < visit && work.two) {
+            if (row < visit && work.low > 0) {
 #pragma unroll
               for (int q = 0; q < 32; ++q) z[q] -= __bfloat162float(__float2bfloat16_rn(z[q]));
-              hd_store_dz(p.dz + (row + kHdRows) * p.dz_stride + col0 + c, z, room);
+              hd_store_dz(p.dz + (row + work.low) * p.dz_stride + col0 + c, z, room);
             }
           }
         };
@@ -970,6 +978,7 @@ struct HeadListParams {
   uint16_t* packed;
   int32_t n_d, bn_d, pairs, slabs;         // backward: what decides the splits
   int64_t dw_tiles;
+  int32_t low;
   int64_t room;
   int32_t* counts;                         // more than kHdListMost rows: the scored rows of each block
 };
@@ -1070,7 +1079,7 @@ __global__ void __launch_bounds__(kHdListThreads) head_rows_kernel(const __grid_
     p.o_lse[t] = 0.0f;
   }
   if (blockIdx.x == 0 && warp == 0) {
-    const int splits = p.backward ? hd_splits(n, p.n_d, p.bn_d, p.pairs, p.slabs, p.dw_tiles, p.room) : 1;
+    const int splits = p.backward ? hd_splits(n, p.n_d, p.bn_d, p.pairs, p.slabs, p.dw_tiles, p.low, p.room) : 1;
     if (lane == 0) {
       p.n_rows[0] = static_cast<int32_t>(n);
       p.n_rows[1] = splits;
@@ -1316,15 +1325,18 @@ struct HdPlan {
 
 constexpr int64_t kPieceElements = int64_t{1} << 28;  // of dz: 512 MB
 
-HdPlan hd_plan(int64_t T, int64_t V, int64_t d, int64_t sms, bool backward) {
+// The ids of a piece of dz held in `parts` parts: equal pieces of at most 2^28 elements.
+int64_t hd_piece(int64_t t_pad, int64_t V, int64_t parts) {
+  const int64_t most = std::max<int64_t>(4096 / parts, kPieceElements / (parts * t_pad) / kHdBN * kHdBN);
+  const int64_t pieces = (V + most - 1) / most;
+  return round_up((V + pieces - 1) / pieces, kHdBN);
+}
+
+// `low`: dz has a second part for every row (the workspace has room for it either way).
+HdPlan hd_plan(int64_t T, int64_t V, int64_t d, int64_t sms, bool backward, bool low = false) {
   HdPlan h{};
   h.t_pad = round_up(T, kHdBM);
-  int64_t piece = round_up(V, kHdBN);
-  if (backward) {
-    const int64_t most = std::max<int64_t>(4096, kPieceElements / h.t_pad / kHdBN * kHdBN);
-    const int64_t pieces = (V + most - 1) / most;
-    piece = round_up((V + pieces - 1) / pieces, kHdBN);
-  }
+  const int64_t piece = !backward ? round_up(V, kHdBN) : hd_piece(h.t_pad, V, low ? 2 : 1);
   h.piece = piece;
   // One row tile: the width in [128, 256] with which the busiest pair has the fewest
   // ids (the weight's bytes are what such a call costs); else whole tiles.
@@ -1361,7 +1373,8 @@ HdPlan hd_plan(int64_t T, int64_t V, int64_t d, int64_t sms, bool backward) {
   if (backward) {
     h.place = take(4 * T);
     h.row = take(static_cast<int64_t>(sizeof(HeadRow)) * T);
-    h.dz = take(2 * h.t_pad * h.piece);
+    const int64_t one_part = h.t_pad * hd_piece(h.t_pad, V, 1), two_parts = T > kHdRows ? 2 * h.t_pad * hd_piece(h.t_pad, V, 2) : 0;
+    h.dz = take(2 * std::max(one_part, two_parts));
     h.accs = take(4 * h.acc);
   } else {
     h.z_target = take(4 * T);
@@ -1583,7 +1596,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
     return DLLM_ERR_INVALID_ARGUMENT;
   const HdDevice* dev = hd_device();
   if (!dev) return DLLM_ERR_CUDA;
-  const HdPlan h = hd_plan(T, V, d, dev->sms, true);
+  const bool low = grad_weight && grad_weight_dt == DLLM_F32 && T > kHdRows;
+  const HdPlan h = hd_plan(T, V, d, dev->sms, true, low);
   uint8_t* ws = hd_base(workspace);
   int32_t* n_rows = reinterpret_cast<int32_t*>(ws + 128);
 
@@ -1615,6 +1629,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   std::copy(sup.id, sup.id + sup.n, p.sup);
   p.row = l.row;
   p.dz = reinterpret_cast<uint16_t*>(ws + h.dz);
+  p.low = low ? static_cast<int32_t>(h.t_pad) : 0;
   p.dz_stride = h.piece;
   p.acc = reinterpret_cast<float*>(ws + h.accs);
   p.acc_stride = static_cast<int64_t>(h.n_d) * h.bn_d;
@@ -1629,7 +1644,7 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
       !make_map(&pz.tm_packed, ws + h.hidden, packed_rows, d, d, a_rows) ||
       !make_map(&pz.tm_b, weight, V, d, weight_stride, static_cast<uint32_t>(h.bn_v / 2)) ||
       !make_map(&pb.tm_a, p.dz, h.t_pad, h.piece, h.piece, a_rows) || !make_map(&pb.tm_b, weight, V, d, weight_stride, 64) ||
-      !make_map(&pb.tm_aw, p.dz, h.t_pad, h.piece, h.piece, 64) || !make_map(&pb.tm_bw, hidden, T, d, hidden_stride, 64) ||
+      !make_map(&pb.tm_aw, p.dz, h.t_pad + p.low, h.piece, h.piece, 64) || !make_map(&pb.tm_bw, hidden, T, d, hidden_stride, 64) ||
       !make_map(&pb.tm_packed, ws + h.hidden, packed_rows, d, d, 64) ||
       (grad_weight && !make_map(&pb.tm_out, grad_weight, V, d, grad_weight_stride, 32, grad_weight_dt == DLLM_F32)))
     return DLLM_ERR_CUDA;
@@ -1654,10 +1669,11 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   l.pairs = dev->sms / 2;
   l.slabs = static_cast<int32_t>((std::min(h.piece, V) + kHdBK - 1) / kHdBK);
   l.dw_tiles = grad_weight ? (std::min(h.piece, V) + kHdBM - 1) / kHdBM * h.n_d : 0;
+  l.low = p.low;
   l.room = h.acc;
   st = hd_list(l, h, ws, stream);
   if (st != DLLM_OK) return st;
-  const void* back = hd_back(p.grad_w_f32 ? kHdF32 : (p.accumulate ? kHdBf16Add : kHdBf16), grad_weight && T > hd_part(kHdBack) * kHdBK);
+  const void* back = hd_back(p.grad_w_f32 ? kHdF32 : (p.accumulate ? kHdBf16Add : kHdBf16), grad_weight && (low ? 2 : 1) * T > hd_part(kHdBack) * kHdBK);
   for (int64_t v0 = 0; v0 < V; v0 += h.piece) {
     const int64_t cols = std::min(h.piece, V - v0);
     for (HeadParams* q : {&pz, &pb}) {

@@ -680,10 +680,11 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
  * read into any result.  Suppressed ids get 0.
  * dz is formed piece by piece of the vocabulary (at most 2^28 elements, or 4096
  * ids, at a time) and held in bf16, as the products' operands have to be: each
- * element is rounded by at most 2^-8 of itself, where up to 128 rows take part (held
- * in two parts) by 2^-16.  Sums are the tensor core's, fp32 and cut off, in parts added
- * in fp32: grad_weight's of at most 8192 products, grad_hidden's of a share of a piece's
- * ids.
+ * element is rounded by at most 2^-8 of itself.  Where up to 128 rows take part, and
+ * for a grad_weight in fp32, it is held in two parts, within 2^-16 (grad_hidden of
+ * more rows is always made of the first).  Sums are the tensor core's, fp32 and cut
+ * off, in parts added in fp32: grad_weight's of at most 8192 products, grad_hidden's
+ * of a share of a piece's ids.
  *   grad_hidden  device bf16 (T, d), rows grad_hidden_stride elements apart, or
  *                NULL (not wanted)
  *   grad_weight  device (V, d) fp32 or bf16 (grad_weight_dt), rows

@@ -315,12 +315,39 @@ def test_few_scored_rows_of_many_keep_what_bf16_cuts_off(cs, T, V, d, scored):
     check_grad(gh, dz, parts, w, e, dz_bits=16)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("T,V,d,scored", [(129, 200, 64, 1.0), (257, 513, 72, 1.0), (300, 3000, 520, 0.6), (1025, 2049, 264, 1.0),
+                                          (700, 30011, 136, 0.9), (9000, 33000, 64, 0.9), (8192, 700, 128, 0.7)])
+def test_a_weight_gradient_in_32_bits_keeps_what_bf16_cuts_off(cs, T, V, d, scored, accumulate):
+    """dz in two parts for it, however many rows take part."""
+    h, w, t, sup = inputs(T, V, d, 97 + T, scored, 1)
+    wide = torch.randn((V, d), device="cuda") * 0.1
+    old = wide.clone() if accumulate else None
+    gh, gw, dz, clean, parts = check_backward(cs, h, w, t, sup, out=(None, wide), **({"accumulate": True} if accumulate else {}))
+    assert int((dz != 0).any(1).sum()) > 128
+    e = float(logit_error(h, w, (t >= 0) & (t < V), 1024).max())
+    check_grad(wide, dz.T, parts.T, clean, e, old, dz_bits=16)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,V,d", [(8200, 300, 72), (17000, 600, 136)])
+def test_weight_gradients_in_several_parts(cs, T, V, d, dtype, accumulate):
+    """More rows than one accumulator takes, stored and added to in either type."""
+    h, w, t, sup = inputs(T, V, d, 99 + T, 1.0, 1)
+    gw = (torch.randn((V, d), device="cuda") * 0.1).to(dtype)
+    old = gw.clone() if accumulate else None
+    _, _, dz, clean, parts = check_backward(cs, h, w, t, sup, out=(None, gw), **({"accumulate": True} if accumulate else {}))
+    e = float(logit_error(h, w, (t >= 0) & (t < V), 1024).max())
+    check_grad(gw, dz.T, parts.T, clean, e, old, dz_bits=8 if dtype is BF16 else 16)
+
+
 @pytest.mark.parametrize("T", [1 << 15, 1 << 21])
 def test_long_sums_of_one_sign_do_not_drift(cs, T):
     """A weight's gradient of many rows, every term of a sum of one sign.  The tensor core cuts off what 32 bits do not hold,
-    product by product at worst, so a part of 8192 products is off by 8192 2^-23 of itself at most; the parts are added
-    rounded (T / 8192 2^-24).  An element of dz is rounded by 2^-8 of itself at most, and where all terms are nearly one
-    value (1 - p near 1, whose bf16 neighbours are 2^-8 apart) all of them the same way, so that the sum is off by as much."""
+    product by product at worst, so a part of 8192 products is off by 8192 2^-23 of itself at most; the parts of dz's two
+    are added rounded (2 T / 8192 2^-24).  In 32 bits an element of dz is off by 2^-16 of itself at most (rounded to bf16 it
+    would be by 2^-8, and where all terms are nearly one value, 1 - p near 1, all of them the same way)."""
     V, d = 64, 64
     g = torch.Generator(device="cuda").manual_seed(T)
     h = (torch.rand((T, d), device="cuda", generator=g) + 0.5).to(BF16)
@@ -334,7 +361,7 @@ def test_long_sums_of_one_sign_do_not_drift(cs, T):
     assert bool((dz[:, 0] >= 0).all()) and bool((dz[:, 1:] <= 0).all())
     want = dz.T @ clean
     e = float(logit_error(h, w, torch.ones_like(t, dtype=torch.bool), 1024).max())
-    lim = 8192 * 2.0 ** -23 + T / 8192 * 2.0 ** -24 + 2.0 ** -8
+    lim = 8192 * 2.0 ** -23 + T / 4096 * 2.0 ** -24 + 2.0 ** -16
     part = grad_parts(h, w, t, lse, ent, one, None, [])
     slack = (2 * e + 2.0 ** -18) * (part.T @ clean)
     assert bool(((got.double() - want).abs() <= lim * want.abs() + slack).all()), float(((got - want) / want).abs().max())
