@@ -41,7 +41,7 @@ EXPORTS = (
     "dllm_cache_evict", "dllm_token_logprobs", "dllm_token_logprobs_backward",
     "dllm_lm_head_logprobs_workspace_size", "dllm_lm_head_logprobs", "dllm_lm_head_logprobs_backward_workspace_size",
     "dllm_lm_head_logprobs_backward", "dllm_embed_tokens", "dllm_embed_tokens_backward_workspace_size",
-    "dllm_embed_tokens_backward",
+    "dllm_embed_tokens_backward", "dllm_fault_word",
 )
 
 
@@ -93,6 +93,7 @@ def _load() -> C.CDLL:
     lib.dllm_transfer_schedule.argtypes = [P, i64, i32, P, P]
     lib.dllm_block_ranges.argtypes = [i64, i64, i64, C.c_int, P, i64, P]
     lib.dllm_workspace_fault.argtypes = [P, P, C.POINTER(C.c_int32)]
+    lib.dllm_fault_word.argtypes = [C.POINTER(P)]
     lib.dllm_token_stats_noalloc.argtypes = stats_args + [P]
     lib.dllm_noalloc_fault.argtypes = [P, C.POINTER(C.c_int32)]
     lib.dllm_token_stats_ex.argtypes = stats_args[:10] + [C.POINTER(StatsEx)] + stats_args[10:] + [P, sz, P]
@@ -630,6 +631,18 @@ def workspace_fault(ws: torch.Tensor, stream=None) -> int:
     if f.value != 0:
         with torch.cuda.stream(torch.cuda.current_stream(ws.device) if stream is None else stream):
             ws.zero_()
+    return f.value
+
+
+def kernel_fault(stream=None) -> int:
+    """The fault code that a head or embedding call (``lm_head_logprobs`` and its
+    backward pass, ``embed_tokens_backward``, ``score_hidden``, ``embed_canvas``,
+    replays of captured ones) left on the current device since this was last read
+    (0: none): a wait ran out and that call's results are undefined.  Synchronises
+    the stream, so read it after a step, say, or where a loss looks wrong."""
+    word, f = C.c_void_p(), C.c_int32(0)
+    _check(_lib.dllm_fault_word(C.byref(word)), "dllm_fault_word")
+    _check(_lib.dllm_workspace_fault(word, _stream(stream), C.byref(f)), "dllm_workspace_fault")
     return f.value
 
 

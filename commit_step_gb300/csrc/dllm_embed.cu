@@ -292,7 +292,7 @@ struct ZeroParams {
   int64_t row_bytes;
   EmDiv vecs;                   // 16-byte vectors of a row
   int32_t rows;                 // rows of a group: a power of two
-  int32_t* fault;
+  int32_t *fault, *seen;        // the workspace's word and the device's
 };
 
 __global__ void __launch_bounds__(kZeroThreads, 3) embed_zero_kernel(const __grid_constant__ ZeroParams p) {
@@ -360,7 +360,10 @@ __global__ void __launch_bounds__(kZeroThreads, 3) embed_zero_kernel(const __gri
         reinterpret_cast<uint4*>(p.out + (r0 + r) * p.row_bytes)[j - r * p.vecs.d] = make_uint4(0u, 0u, 0u, 0u);
     }
     if (!mbar_wait_bounded(bar, phase)) {
-      if (threadIdx.x == 0) atomicExch(p.fault, kFaultFullWait);
+      if (threadIdx.x == 0) {
+        atomicExch(p.fault, kFaultFullWait);
+        atomicExch(p.seen, kFaultFullWait);
+      }
       break;
     }
     uint32_t more;
@@ -811,6 +814,8 @@ dllm_status dllm_embed_tokens_backward(const int32_t* tokens, int64_t B, int64_t
   z.tok = k.tok;
   z.out = static_cast<uint8_t*>(grad_weight);
   z.fault = reinterpret_cast<int32_t*>(ws);
+  z.seen = fault_word();
+  if (!z.seen) return DLLM_ERR_CUDA;
   z.row_bytes = grad_weight_stride * size;
   z.vecs = em_div(static_cast<uint32_t>(d * size / 16));
   z.rows = 1;

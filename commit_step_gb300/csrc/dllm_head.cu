@@ -130,7 +130,7 @@ struct HeadParams {
   void* grad_w;                  // dw
   int64_t grad_w_stride;
   int32_t grad_w_f32, accumulate;
-  int32_t* fault;
+  int32_t *fault, *seen;         // the workspace's word and the device's
 };
 
 // Instruction descriptor of tcgen05.mma.kind::f16: fp32 accumulator (bits 4-5 =
@@ -258,6 +258,7 @@ __device__ __forceinline__ bool hd_wait(uint32_t bar, uint32_t parity, volatile 
 __device__ __forceinline__ void hd_fail(const HeadParams& p, volatile int32_t* abort_flag, int32_t code) {
   if (!*abort_flag) {
     atomicExch(p.fault, code);
+    atomicExch(p.seen, code);
     *abort_flag = 1;
   }
 }
@@ -1242,6 +1243,22 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const int32_t* n_rows, con
   }
 }
 
+// Which wait of any call on this device ran out last.
+static __device__ int32_t g_fault_word;
+
+int32_t* fault_word() {
+  static int32_t* word[64];
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  std::call_once(once[dev], [dev]() {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_fault_word) == cudaSuccess) word[dev] = static_cast<int32_t*>(p);
+    else (void)cudaGetLastError();  // report through the result, leave no sticky error
+  });
+  return word[dev];
+}
+
 }  // namespace dllm
 
 namespace {
@@ -1452,6 +1469,12 @@ dllm_status hd_list(HeadListParams& l, const HdPlan& h, uint8_t* ws, dllm_stream
 
 extern "C" {
 
+dllm_status dllm_fault_word(void** word) {
+  if (!word) return DLLM_ERR_INVALID_ARGUMENT;
+  *word = fault_word();
+  return *word ? DLLM_OK : DLLM_ERR_CUDA;
+}
+
 size_t dllm_lm_head_logprobs_workspace_size(int64_t T, int64_t V, int64_t d) {
   if (T <= 0 || V <= 0 || d <= 0 || T > kHdMaxT || V > INT32_MAX || d > kHdMaxD) return 256;
   const HdDevice* dev = hd_device();
@@ -1525,6 +1548,8 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   p.part_rows = h.t_pad;
   p.z_target = reinterpret_cast<float*>(ws + h.z_target);
   p.fault = static_cast<int32_t*>(workspace);
+  p.seen = fault_word();
+  if (!p.seen) return DLLM_ERR_CUDA;
 
   HeadFinishParams f{};
   f.n_rows = p.n_rows;
@@ -1638,6 +1663,8 @@ dllm_status dllm_lm_head_logprobs_backward(const void* hidden, int64_t T, int64_
   p.grad_w_f32 = grad_weight_dt == DLLM_F32 ? 1 : 0;
   p.accumulate = accumulate != 0 ? 1 : 0;
   p.fault = static_cast<int32_t*>(workspace);
+  p.seen = fault_word();
+  if (!p.seen) return DLLM_ERR_CUDA;
   HeadParams pz = p, pb = p;
   const int64_t packed_rows = round_up(T, kHdBK);
   if (!make_map(&pz.tm_a, hidden, T, d, hidden_stride, a_rows) ||

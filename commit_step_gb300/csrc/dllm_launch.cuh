@@ -43,6 +43,9 @@ inline int64_t mul_or_neg(int64_t a, int64_t b) {
   return a > lim / b ? -1 : a * b;
 }
 
+// The current device's fault word (dllm_fault_word), or null.
+int32_t* fault_word();
+
 // The bytes of rows x cols elements of `size` bytes, rows `stride` elements apart.
 struct Extent {
   const void* at;

@@ -142,7 +142,7 @@ class _EmbedCanvas(torch.autograd.Function):
 
 def embed_canvas(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0):
     """embed_tokens for training: differentiable once with respect to ``weight``
-    through autograd, and captured as score_hidden is."""
+    through autograd, captured and watched (``kernel_fault``) as score_hidden is."""
     out = _EmbedCanvas.apply(tokens, weight, float(scale))
     _stamp(out)
     return out

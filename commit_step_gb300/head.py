@@ -97,7 +97,7 @@ def lm_head_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
     gets 0 for all three, costs nothing, and its hidden state may hold anything.
     ``out``: the same three, preallocated.  ``ws``: a workspace of the caller's,
     not in use by another call; zeroed, it tells ``workspace_fault`` afterwards
-    whether a wait ran out."""
+    whether a wait ran out (``kernel_fault`` tells it of any call)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return lm_head_logprobs(hidden, weight, targets, suppress_ids, out, ws)
@@ -239,7 +239,8 @@ def score_hidden(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tens
     """lm_head_logprobs for training: (logprob, entropy), differentiable once with
     respect to ``hidden`` and ``weight`` through autograd.  A backward pass that is
     captured into a CUDA graph is refused while a result lives that was computed from
-    the same leaves on the default stream (warm up on another)."""
+    the same leaves on the default stream (warm up on another).  Workspaces are the
+    binding's own: ``kernel_fault`` tells whether a wait of a call ran out."""
     logprob, entropy = _ScoreHidden.apply(hidden, weight, targets, tuple(suppress_ids))
     _stamp(logprob)
     return logprob, entropy

@@ -755,6 +755,14 @@ dllm_status dllm_embed_tokens_backward(const int32_t* tokens, int64_t B, int64_t
  * fails. */
 dllm_status dllm_workspace_fault(void* workspace, dllm_stream_t stream, int32_t* fault);
 
+/* Stores the address, in device memory, of the current device's fault word (4 bytes,
+ * 0 at first; DLLM_ERR_CUDA without a usable device) in *word.  A call of dllm_lm_head_logprobs, its
+ * backward pass or dllm_embed_tokens_backward on that device whose wait ran out
+ * leaves its code here as well as in its workspace, whoever holds that (a binding
+ * that keeps workspaces, a captured graph).  Read and cleared by
+ * dllm_workspace_fault(word, stream, &fault). */
+dllm_status dllm_fault_word(void** word);
+
 #ifdef __cplusplus
 }
 #endif

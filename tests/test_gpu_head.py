@@ -19,6 +19,7 @@ held too: two roundings of at most 2^-8, spread evenly, have a root mean square 
 asked for beside the second term's norm; of few rows a handful of elements decides,
 which may all be off by the most: twice that.
 """
+import ctypes
 import math
 
 import pytest
@@ -429,6 +430,24 @@ def test_workspaces_at_any_16_bytes(cs, T, V, d, scored):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(cs.workspace_fault(x) == 0 for x in ws)
         assert not any(bool(pool[:shift].any() or pool[shift + need:].any()) for pool, need in zip(pools, sizes))
+
+
+def test_the_devices_fault_word(cs):
+    """It is read and cleared, and calls whose waits end leave it alone.  (The code that a kernel would leave is written by
+    the test.)"""
+    lib, code, word = cs.lib_handle(), ctypes.c_int32(2), ctypes.c_void_p()
+    assert lib.dllm_fault_word(ctypes.byref(word)) == 0
+    assert cs.kernel_fault() == 0
+    lib.cudaMemcpy.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int]     # (its runtime's)
+    assert lib.cudaMemcpy(word, ctypes.byref(code), 4, 1) == 0
+    h, w, t, sup = inputs(300, 3000, 64, 18, 0.5, 1)
+    ha, wa = h.clone().requires_grad_(), w.clone().requires_grad_()
+    cs.score_hidden(ha, wa, t)[0].sum().backward()
+    cs.embed_tokens_backward(t, h, 3000)
+    assert cs.kernel_fault() == 2 and cs.kernel_fault() == 0
+    cs.score_hidden(ha, wa, t)[0].sum().backward()
+    cs.embed_tokens_backward(t, h, 3000, stream=torch.cuda.Stream())
+    assert cs.kernel_fault() == 0
 
 
 def test_autograd(cs):

@@ -48,6 +48,13 @@ def test_head_refusals():
     assert grad(gh=None, gw=None) == 0 and grad(T=0, gw=None) == 0 and grad(T=0, acc=1) == 0
 
 
+def test_the_fault_word_needs_a_device():
+    assert cs.lib_handle().dllm_fault_word(None) == INVALID
+    if not torch.cuda.is_available():
+        with pytest.raises(cs.DllmError):
+            cs.kernel_fault()
+
+
 def embed(t=FAKE, B=2, L=8, ts=8, w=FAKE, dt=1, V=100, d=64, wst=64, scale=1.0, out=FAKE):
     return cs.lib_handle().dllm_embed_tokens(t, B, L, ts, w, dt, V, d, wst, scale, out, None)
 
