@@ -216,10 +216,27 @@ class _HeadGrad(torch.autograd.Function):
         raise RuntimeError("the gradient of score_hidden cannot be differentiated again")
 
 
+def _spaced(t):
+    """Hidden states whose rows are evenly spaced and whole vectors: t, or a copy of it."""
+    if t.dim() not in (2, 3) or t.numel() == 0:
+        return t
+    try:
+        _, _, stride = _rows(t, "hidden")
+    except ValueError:
+        return t.contiguous()
+    # (an expanded row, or one that begins between vectors)
+    even = stride >= t.shape[-1] and (t.shape[-1] % 8 != 0 or (stride % 8 == 0 and t.data_ptr() % 16 == 0))
+    return t if even else t.clone(memory_format=torch.contiguous_format)
+
+
 class _ScoreHidden(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, targets, suppress_ids):
         ctx.set_materialize_grads(False)
+        if torch.is_tensor(hidden) and hidden.is_cuda:
+            hidden = _spaced(hidden)
+        if torch.is_tensor(targets) and not targets.is_contiguous():
+            targets = targets.contiguous()
         lp, ent, lse = lm_head_logprobs(hidden, weight, targets, suppress_ids=suppress_ids)
         ctx.suppress_ids = suppress_ids
         ctx.save_for_backward(hidden, weight, targets, lse, ent)
@@ -237,7 +254,9 @@ class _ScoreHidden(torch.autograd.Function):
 
 def score_hidden(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, suppress_ids: Sequence[int] = ()):
     """lm_head_logprobs for training: (logprob, entropy), differentiable once with
-    respect to ``hidden`` and ``weight`` through autograd.  A backward pass that is
+    respect to ``hidden`` and ``weight`` through autograd.  Hidden states and targets
+    of any strides (``hidden[:, :-1]``, ``tokens[:, 1:]``): what a call cannot read as it
+    lies is copied.  A backward pass that is
     captured into a CUDA graph is refused while a result lives that was computed from
     the same leaves on the default stream (warm up on another).  Workspaces are the
     binding's own: ``kernel_fault`` tells whether a wait of a call ran out."""

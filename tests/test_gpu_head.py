@@ -469,6 +469,32 @@ def test_autograd(cs):
         g.float().sum().backward()
 
 
+@pytest.mark.parametrize("B,L", [(3, 21), (5, 1), (1, 40), (2, 300)])
+def test_autograd_of_windows(cs, B, L):
+    """Shifted scoring: hidden states without their last position, targets without their first; and other strides."""
+    h, w, t, sup = inputs(B * (L + 1), 700, 64, 90 + L, 0.8, 1)
+    h, t = h.view(B, L + 1, 64), t.view(B, L + 1)
+    wide = torch.zeros((B, L + 1, 68), dtype=BF16, device="cuda")
+    wide[..., 4:] = h
+    want = None
+    for x, y in ((h[:, :-1].contiguous(), t[:, 1:].contiguous()), (h[:, :-1], t[:, 1:]), (wide[:, :-1, 4:], t[:, 1:]),
+                 (h[:, :-1].transpose(0, 1).contiguous().transpose(0, 1), t[:, 1:].T.contiguous().T),
+                 (h[:, :-1].transpose(1, 2).contiguous().transpose(1, 2), t[:, 1:])):
+        x, v = x.detach().requires_grad_(), w.clone().requires_grad_()
+        lp, ent = cs.score_hidden(x, v, y, suppress_ids=sup)
+        (torch.nan_to_num(lp, neginf=0.0).sum() + 0.1 * ent.sum()).backward()
+        got = lp, ent, x.grad, v.grad
+        assert lp.shape == y.shape and x.grad.shape == x.shape
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    row = h[:1, :1].clone().requires_grad_()
+    lp, _ = cs.score_hidden(row.expand(B, L, 64), w, t[:, 1:])
+    lp.sum().backward()
+    each = h[:1, :1].expand(B, L, 64).contiguous().requires_grad_()
+    cs.score_hidden(each, w, t[:, 1:])[0].sum().backward()
+    assert torch.equal(row.grad, each.grad.sum((0, 1), keepdim=True))
+
+
 def test_matches_the_scores_of_stored_logits(cs):
     """The same model through logits in memory: one softmax, one loss."""
     h, w, t, sup = inputs(64, 4000, 256, 16, 1.0, 1)
