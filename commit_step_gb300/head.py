@@ -3,6 +3,7 @@ gradient with respect to hidden states and weight, without the logits in memory
 (``dllm_lm_head_logprobs``, ``dllm_lm_head_logprobs_backward``)."""
 from __future__ import annotations
 
+import functools
 import threading
 from typing import Optional, Sequence
 
@@ -181,11 +182,22 @@ def _leaves(node):
     return [f for f, _ in node.next_functions if f is not None and f.name().endswith("AccumulateGrad")]
 
 
+def _mark(marks, index, *_):
+    marks[_STREAM] = torch._C._cuda_getCurrentRawStream(index)
+
+
 def _stamp(result):
-    """Writes the current stream down where the leaves' accumulators are new."""
+    """Writes the leaves' accumulators' streams down: the current one where they seem
+    new, and the one they run on once they have run (something else, a data-parallel
+    wrapper say, may have made them and keep them)."""
     if result.requires_grad:
         for f in _leaves(result.grad_fn):
-            f.metadata.setdefault(_STREAM, torch._C._cuda_getCurrentRawStream(result.get_device()))
+            marks = f.metadata
+            if _STREAM not in marks:
+                # (the hook holds the marks and not f, which would hold itself)
+                mark = functools.partial(_mark, marks, result.get_device())
+                mark()
+                f.register_prehook(mark)
 
 
 def _may_capture(node):
@@ -258,7 +270,8 @@ def score_hidden(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tens
     of any strides (``hidden[:, :-1]``, ``tokens[:, 1:]``): what a call cannot read as it
     lies is copied.  A backward pass that is
     captured into a CUDA graph is refused while a result lives that was computed from
-    the same leaves on the default stream (warm up on another).  Workspaces are the
+    the same leaves on the default stream (warm up on another, backward pass included: a
+    leaf's accumulator that something else made is known once it has run).  Workspaces are the
     binding's own: ``kernel_fault`` tells whether a wait of a call ran out."""
     logprob, entropy = _ScoreHidden.apply(hidden, weight, targets, tuple(suppress_ids))
     _stamp(logprob)

@@ -100,5 +100,40 @@ def test_a_captured_step_beside_a_living_result(cs):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("made_on_side", [True, False])
+def test_a_captured_step_of_leaves_whose_accumulators_something_else_keeps(cs, made_on_side):
+    """As a data-parallel wrapper keeps them.  Made on a side stream, a step on the default stream before the capture does no
+    harm; made on the default stream, a warm-up on a side stream does not hide it."""
+    w = torch.randn((50, 16), device="cuda").to(torch.bfloat16).requires_grad_()
+    t = torch.randint(0, 50, (2, 9), dtype=torch.int32, device="cuda")
+    x = torch.randn((2, 9, 16), device="cuda").to(torch.bfloat16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    default = torch.cuda.current_stream()
+
+    def step():
+        w.grad = None
+        cs.score_hidden(x, w, t)[0].sum().backward()
+        return w.grad
+
+    with torch.cuda.stream(side if made_on_side else default):
+        keeps = w.expand_as(w)
+    with torch.cuda.stream(default if made_on_side else side):
+        want = step().clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    if not made_on_side:
+        with pytest.raises(RuntimeError, match="default stream"):
+            with torch.cuda.graph(graph):
+                step()
+        return
+    with torch.cuda.graph(graph):
+        got = step()
+    got.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and keeps is not None
+
+
 def test_it_runs(cs):
     example().main()

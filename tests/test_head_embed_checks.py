@@ -191,3 +191,51 @@ def test_a_captured_gradient_beside_a_living_graph_of_the_default_stream(monkeyp
     capturing[0] = True
     graph(w, v, 7).backward()
     assert float(w.grad[0]) > 0 and warm is not None and kept is not None
+
+
+def test_accumulators_that_something_else_made(monkeypatch):
+    """Where an accumulator runs is known once it has run, whatever stream it was first scored on.  As above."""
+    import gc
+    import weakref
+
+    from commit_step_gb300 import head
+
+    class Twice(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return x * 2
+
+        @staticmethod
+        def backward(ctx, g):
+            head._may_capture(ctx)
+            return g * 2
+
+    stream, capturing = [0], [False]
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: stream[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+
+    def step(w, on, accumulates_on):
+        stream[0] = on
+        out = Twice.apply(w)
+        head._stamp(out)
+        stream[0] = accumulates_on                           # (what the engine would make current)
+        out.sum().backward()
+
+    for made_on, scored_on in ((7, 0), (0, 7)):
+        w = torch.ones(4, requires_grad=True)
+        keeps = w.expand_as(w)                               # the accumulator, made elsewhere and kept
+        capturing[0] = False
+        step(w, scored_on, made_on)
+        capturing[0] = True
+        if made_on == 0:
+            with pytest.raises(RuntimeError, match="default stream"):
+                step(w, 9, made_on)
+        else:
+            step(w, 9, made_on)
+        marks = keeps.grad_fn.next_functions[0][0].metadata
+        assert marks[head._STREAM] == made_on
+        gone = weakref.ref(w)
+        del w, keeps, marks
+        gc.collect()
+        assert gone() is None                                # nothing holds the accumulator
+
