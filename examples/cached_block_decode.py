@@ -39,7 +39,7 @@ class TinyBlockModel:
     def project(self, tokens):
         """Queries, keys and values of (B, L) tokens: slices of one product."""
         B, L = tokens.shape
-        x = self.embed[tokens.long()]
+        x = cs.embed_tokens(tokens, self.embed)
         y = (x @ self.qkv.T).view(B, L, -1, self.head_dim)
         H, K = self.heads, self.kv_heads
         return x, y[:, :, :H], y[:, :, H:H + K], y[:, :, H + K:]

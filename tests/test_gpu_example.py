@@ -40,6 +40,16 @@ def torch_attention(q, cache, table, lens, weights=None, decay=1.0):
     return (p @ v).transpose(1, 2).to(torch.bfloat16), torch.logsumexp(x, -1).transpose(1, 2).float()
 
 
+def test_the_models_embedding(cs):
+    """The canvas is embedded by ``embed_tokens``: the rows of the table, an id outside it zeros."""
+    model = example().TinyBlockModel(seed=2)
+    tokens = torch.randint(0, model.vocab, (3, 16), dtype=torch.int32).cuda()
+    x, q, k, v = model.project(tokens)
+    assert torch.equal(x, model.embed[tokens.long()])
+    tokens[1, 5] = -1
+    assert not bool(model.project(tokens)[0][1, 5].any())
+
+
 def test_example_runs_and_matches_a_plain_attention(cs):
     m = example()
     torch.manual_seed(1)
