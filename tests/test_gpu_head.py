@@ -155,6 +155,20 @@ def test_no_row_is_scored(cs):
     assert same is old and torch.equal(old, kept)
 
 
+@pytest.mark.parametrize("T", [70, 300, 9000])
+@pytest.mark.parametrize("dtype", [BF16, torch.float32], ids=["bf16", "f32"])
+def test_no_row_takes_part(cs, T, dtype):
+    """Every row scored and none with a gradient: the weight's is zero in either type, and adding leaves what is there."""
+    h, w, t, _ = inputs(T, 500, 64, 77)
+    _, ent, lse = cs.lm_head_logprobs(h, w, t)
+    none = torch.zeros(T, device="cuda")
+    wide = torch.full((500, 72), 7.0, dtype=dtype, device="cuda")
+    gh, gw = cs.lm_head_logprobs_backward(h, w, t, lse, ent, none, none, out=(None, wide[:, :64]), accumulate=True)
+    assert not bool(gh.any()) and bool((wide == 7).all())
+    cs.lm_head_logprobs_backward(h, w, t, lse, ent, none, out=(None, wide[:, :64]))
+    assert not bool(wide[:, :64].any()) and bool((wide[:, 64:] == 7).all())
+
+
 def test_no_rows(cs):
     h, w, _, _ = inputs(4, 100, 64, 8)
     h, t, f = h[:0], torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, device="cuda")
