@@ -126,6 +126,10 @@ class _EmbedGrad(torch.autograd.Function):
 class _EmbedCanvas(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale):
+        if torch.is_tensor(tokens) and tokens.dim() in (1, 2) and tokens.numel() > 0:
+            L, (*rows, unit) = tokens.shape[-1], tokens.stride()
+            if (L > 1 and unit != 1) or (rows and tokens.shape[0] > 1 and rows[0] < L):
+                tokens = tokens.contiguous()
         ctx.V, ctx.scale = weight.shape[0], scale
         ctx.save_for_backward(tokens)
         return embed_tokens(tokens, weight, scale)
@@ -141,8 +145,8 @@ class _EmbedCanvas(torch.autograd.Function):
 
 
 def embed_canvas(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0):
-    """embed_tokens for training: differentiable once with respect to ``weight``
-    through autograd, captured and watched (``kernel_fault``) as score_hidden is."""
+    """embed_tokens for training, of tokens of any strides: differentiable once with
+    respect to ``weight`` through autograd, captured and watched (``kernel_fault``) as score_hidden is."""
     out = _EmbedCanvas.apply(tokens, weight, float(scale))
     _stamp(out)
     return out

@@ -152,6 +152,18 @@ def test_nan_reaches_its_own_row_only(cs):
     assert torch.isnan(got[3, 1]) and int(torch.isnan(got).sum()) == 1 and float(got[3, 0]) == 2.0
 
 
+def test_autograd_of_canvases_of_any_strides(cs):
+    w = torch.randn((50, 16), device="cuda").to(torch.bfloat16).requires_grad_()
+    t = torch.randint(-1, 51, (6, 9), dtype=torch.int32, device="cuda")
+    for view in (t.T, t[:, ::2], t[:1].expand(5, 9), t[:, :1].expand(6, 4), t[2:, 3:], t.T[4], t[0, :1], t[:0]):
+        got = cs.embed_canvas(view, w)
+        want = cs.embed_tokens(view.contiguous(), w.detach())
+        assert torch.equal(got, want)
+        g = torch.randn_like(got)
+        grad, = torch.autograd.grad(got, w, g)
+        assert torch.equal(grad, cs.embed_tokens_backward(view.contiguous(), g, 50))
+
+
 def test_autograd_and_tied_weight(cs):
     """Embedding and head share a weight: one gradient, the embedding's added to the head's."""
     V, d, B, L = 500, 128, 2, 40
