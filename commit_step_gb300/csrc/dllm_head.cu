@@ -27,10 +27,10 @@
 // of 64 m or n.
 //
 // What bounds it: the weight's stream while there are few rows (32 x 126464 x 4096 in
-// 169 us, 6.1 TB/s), from some 300 rows on the tensor cores, and in a run of such
-// calls the card's power: 4096 x 152064 x 3584 in 2.43 to 2.54 ms (1.76 to 1.84 PFLOP/s),
-// 4506 x 126464 x 4096 backward in 8.4 to 8.6 ms (1.63 to 1.67; a cuBLAS product of
-// 8192^3 run for seconds: 1.69).
+// 161 to 166 us, 6.2 to 6.5 TB/s), from some 300 rows on the tensor cores, and in a run of
+// such calls the card's power: 4096 x 152064 x 3584 in 2.43 to 2.54 ms (1.76 to 1.84
+// PFLOP/s), 4506 x 126464 x 4096 backward in 8.4 to 8.7 ms (1.61 to 1.67; a cuBLAS product
+// of 8192^3 run for seconds: 1.69).
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes from the driver at run time)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -157,7 +157,7 @@ __device__ __forceinline__ uint32_t hd_elect() {
 // What follows is issued by the one thread of the warp whose `lead` is set; the whole
 // warp executes the code around it, so that addresses and descriptors stay in uniform
 // registers (formed by a single thread, a product and a load held a slab up by some
-// 170 and 190 cycles each: 32 x 126464 x 4096 took 187 us and takes 169 so, 4506 x 126464 x 4096
+// 170 and 190 cycles each: 32 x 126464 x 4096 took 187 us, and 169 so, 4506 x 126464 x 4096
 // backward 9.0 and 8.4 ms).
 
 // A load of this CTA's shared memory that counts on the leader's barrier.
@@ -1538,7 +1538,8 @@ dllm_status dllm_lm_head_logprobs(const void* hidden, int64_t T, int64_t d, int6
   p.n_sup = sup.n;
   std::copy(sup.id, sup.id + sup.n, p.sup);
   // One row tile costs the same however many of its rows are scored: they are taken as
-  // they are, without the kernel that numbers them (61 x 50257 x 768: 26 and 22 us).
+  // they are, without the kernel that numbers them (61 x 50257 x 768: 26 and 22 us; 22.5 to
+  // 24.5 from box to box).
   const bool direct = T <= kHdBM;
   if (direct) {
     p.n_rows = nullptr;

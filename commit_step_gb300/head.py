@@ -95,7 +95,10 @@ def lm_head_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
 
     hidden (T, d) or (B, L, d) and weight (V, d) bf16; ``targets`` int32, hidden's
     shape without d.  A row whose target lies outside [0, V) is not scored: it
-    gets 0 for all three, costs nothing, and its hidden state may hold anything.
+    gets 0 for all three, and its hidden state may hold anything.  (Of more than 256
+    rows it costs nothing; as many are one tile, which reads the weight whatever is
+    scored.)  A hidden state with a NaN scores like logits of -inf: lse is -inf,
+    logprob -ln of the number of ids.
     ``out``: the same three, preallocated.  ``ws``: a workspace of the caller's,
     not in use by another call; zeroed, it tells ``workspace_fault`` afterwards
     whether a wait ran out (``kernel_fault`` tells it of any call)."""
@@ -131,8 +134,9 @@ def lm_head_logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, target
     grad_weight bf16 like weight), from the saved ``lse`` and ``entropy`` and the
     gradients of logprob and entropy (None: zero).  One that is not wanted
     (``hidden_grad``, ``weight_grad`` false) is None.  ``out``: the two,
-    preallocated (grad_weight bf16 or float32, either None to be made here);
-    ``accumulate`` adds to out's grad_weight.  ``ws`` as in lm_head_logprobs."""
+    preallocated (grad_weight bf16 or float32, either None to be made here; a float32
+    one is also made of a gradient of the logits held in more bits, for a product
+    more); ``accumulate`` adds to out's grad_weight.  ``ws`` as in lm_head_logprobs."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return lm_head_logprobs_backward(hidden, weight, targets, lse, entropy, grad_logprob, grad_entropy, suppress_ids,
@@ -268,7 +272,9 @@ def score_hidden(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tens
     """lm_head_logprobs for training: (logprob, entropy), differentiable once with
     respect to ``hidden`` and ``weight`` through autograd.  Hidden states and targets
     of any strides (``hidden[:, :-1]``, ``tokens[:, 1:]``): what a call cannot read as it
-    lies is copied.  A backward pass that is
+    lies is copied.  A hidden state with a NaN keeps a loss finite (a logprob of -ln of
+    the number of ids) and has no gradient: to see a run that diverges, look at the
+    hidden states, or at lm_head_logprobs' lse (-inf there).  A backward pass that is
     captured into a CUDA graph is refused while a result lives that was computed from
     the same leaves on the default stream (warm up on another, backward pass included: a
     leaf's accumulator that something else made is known once it has run).  Workspaces are the

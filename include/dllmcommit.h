@@ -658,7 +658,8 @@ dllm_status dllm_token_logprobs_backward(const void* logits, dllm_dtype dt, int6
  *            then undefined): zero it to read it later with dllm_workspace_fault.
  * d a multiple of 8, bases 16-byte aligned and row strides multiples of 8, T up
  * to 2^24, d up to 2^20 (else DLLM_ERR_UNSUPPORTED).  The work is that of the
- * scored rows.  Logits are summed in parts of 640 products, each in the tensor
+ * scored rows (up to 256 rows are one tile and are read as they are: the weight's
+ * stream, however many are scored).  Logits are summed in parts of 640 products, each in the tensor
  * core's fp32, the parts in fp32; the softmax's sums are fp32.  Results repeat bit
  * for bit.  Outputs must not overlap each other or an input.
  * ------------------------------------------------------------------------ */
