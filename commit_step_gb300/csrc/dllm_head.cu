@@ -10,8 +10,8 @@
 // kernel joins a row's partials.
 //
 // Backward, over pieces of the vocabulary so that only a piece of dz is ever
-// held (bf16, as the product's operands have to be; of up to 128 scored rows in two parts, whose
-// second takes the half of dH's tiles that is empty then): dz = the product again,
+// held (bf16, as the product's operands have to be; of up to 128 scored rows in two parts,
+// whose second takes the half of dH's tiles that is empty then, and for a dW of 32 bits): dz = the product again,
 // with p = exp(z - lse) and dz = -p (g + gH (z - lse + H)) + g [v = target] in its
 // epilogue; dH += dz W over the piece (K: the piece's ids); dW = dz^T H (K: the
 // scored rows).
@@ -437,11 +437,7 @@ __device__ __forceinline__ void hd_store_dz(uint16_t* out, const float (&x)[32],
   }
 }
 
-// This warp's 32 rows of 64 columns (a row a thread, 32 of them in each of x and y), as
-// bf16, to column col and row `row` of the tensor: through shared memory in the 128-byte
-// swizzle and out by TMA, so that memory sees whole lines (stored from registers, a row a
-// thread, the weight's gradient of 512 x 126464 x 4096 took 504 us in a launch of its own,
-// and 381 so).
+// What this warp wrote to its buffer, to column col and row `row` of the tensor.
 __device__ __forceinline__ void hd_tile_out(const CUtensorMap* map, int col, int row, uint32_t buf, int lane) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
@@ -453,6 +449,11 @@ __device__ __forceinline__ void hd_tile_out(const CUtensorMap* map, int col, int
   }
 }
 
+// This warp's 32 rows of 64 columns (a row a thread, 32 of them in each of x and y), as
+// bf16, to column col and row `row` of the tensor: through shared memory in the 128-byte
+// swizzle and out by TMA, so that memory sees whole lines (stored from registers, a row a
+// thread, the weight's gradient of 512 x 126464 x 4096 took 504 us in a launch of its own,
+// and 381 so).
 __device__ __forceinline__ void hd_store_tile(const float (&x)[32], const float (&y)[32], uint32_t buf, const CUtensorMap* map, int col,
                                               int row, int lane) {
   if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (the last one has left the buffer)
